@@ -1,8 +1,9 @@
 """ctypes binding of libkda.so (argument marshalling only).
 
 Names follow the C ABI in include/kda.h: kda_fwd, kda_fwd_ws, kda_fwd_noalloc,
-kda_fwd_intra, kda_fwd_scan, kda_fwd_trace, kda_fwd_cp, kda_decode, kda_bwd and
-their size queries, kda_status_string, kda_dv_slices.  Tensors are passed as
+kda_fwd_intra, kda_fwd_scan, kda_fwd_trace, kda_fwd_cp, kda_decode, kda_bwd,
+kda_gdr_fwd, kda_gdr_bwd, kda_gdr_decode, kda_qk_norm, kda_qk_norm_bwd and their
+size queries, kda_status_string, kda_dv_slices.  Tensors are passed as
 kda_tensor_t descriptors built from torch tensors (data pointer, dtype, shape,
 strides); the stream is torch's current HIP stream unless one is given.  Where
 an entry point takes a workspace, it is a uint8 device tensor the caller passes
@@ -10,6 +11,7 @@ or one taken here from torch's caching allocator.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -24,7 +26,8 @@ STATUS_NAMES = ["KDA_OK", "KDA_ERR_NULL", "KDA_ERR_DTYPE", "KDA_ERR_SHAPE", "KDA
 EXPORTED = ["kda_fwd", "kda_fwd_fused", "kda_fwd_ws", "kda_fwd_qg", "kda_fwd_noalloc", "kda_fwd_noalloc_max_bytes", "kda_fwd_intra",
             "kda_fwd_scan", "kda_fwd_trace", "kda_fwd_cp", "kda_decode", "kda_bwd", "kda_fwd_workspace_size",
             "kda_fwd_cp_workspace_size", "kda_fwd_cp_packed_workspace_size", "kda_fwd_cp_plan", "kda_bwd_workspace_size", "kda_status_string",
-            "kda_dv_slices"]
+            "kda_dv_slices", "kda_gdr_fwd", "kda_gdr_fwd_workspace_size", "kda_gdr_bwd", "kda_gdr_bwd_workspace_size",
+            "kda_gdr_decode", "kda_qk_norm", "kda_qk_norm_bwd", "kda_qk_norm_bwd_workspace_size"]
 
 
 class KdaTensor(ctypes.Structure):
@@ -95,6 +98,19 @@ def load_library(path=None):
     lib.kda_bwd.restype = ctypes.c_int
     lib.kda_bwd_workspace_size.argtypes = [ctypes.c_int64] * 4
     lib.kda_bwd_workspace_size.restype = ctypes.c_int64
+    vp, i64 = ctypes.c_void_p, ctypes.c_int64
+    lib.kda_gdr_fwd.argtypes = [vp] * 5 + [ctypes.c_float] + [vp] * 5 + [i64, vp]
+    lib.kda_gdr_bwd.argtypes = [vp] * 5 + [ctypes.c_float] + [vp] * 11 + [i64, vp]
+    lib.kda_gdr_decode.argtypes = [vp] * 5 + [ctypes.c_float] + [vp] * 5
+    lib.kda_qk_norm.argtypes = [vp] * 4 + [ctypes.c_int32, ctypes.c_float] + [vp] * 3 + [ctypes.c_int32] + [vp] * 3
+    lib.kda_qk_norm_bwd.argtypes = [vp] * 6 + [ctypes.c_int32, ctypes.c_float] + [vp] * 3 + [ctypes.c_int32] + \
+        [vp] * 5 + [i64, vp]
+    for name in ("kda_gdr_fwd", "kda_gdr_bwd", "kda_gdr_decode", "kda_qk_norm", "kda_qk_norm_bwd"):
+        getattr(lib, name).restype = ctypes.c_int
+    lib.kda_gdr_fwd_workspace_size.argtypes = lib.kda_gdr_bwd_workspace_size.argtypes = [i64] * 3
+    lib.kda_gdr_fwd_workspace_size.restype = lib.kda_gdr_bwd_workspace_size.restype = i64
+    lib.kda_qk_norm_bwd_workspace_size.argtypes = []
+    lib.kda_qk_norm_bwd_workspace_size.restype = i64
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_dv_slices.argtypes = [ctypes.c_int64, ctypes.c_int64]
@@ -428,3 +444,182 @@ def kda_bwd(q, k, v, g, beta, scale, d_out, initial_state=None, d_final_state=No
     _check(lib, lib.kda_bwd(_ref(descs[0]), _ref(descs[1]), _ref(descs[2]), _ref(descs[3]), _ref(descs[4]),
                             float(scale), *[_ref(d) for d in descs[5:]], ws, ws_size, s))
     return out
+
+
+# ---- gated delta rule with one decay per head, per-head q/k norm ----
+# These entry points are called once per layer and token while serving, where the host's
+# share of a call counts: all descriptors of a call are packed into one buffer.
+_DESC = struct.Struct("Pii8q")
+_ENTRY_DTYPES = {torch.bfloat16: KDA_BF16, torch.float16: KDA_F16, torch.float32: KDA_F32, torch.int32: KDA_I32}
+
+
+def _launch(entry, tensors, before, after, stream, workspace=()):
+    """Calls `entry` with descriptors of `tensors` (None: NULL) spliced into the scalar
+    arguments: before[i] scalars precede tensor i.  Tensors must be on one GPU, which is
+    made current for the call."""
+    dev = None
+    buf = ctypes.create_string_buffer(_DESC.size * len(tensors))
+    base = ctypes.addressof(buf)
+    args = []
+    for i, t in enumerate(tensors):
+        if i in before:
+            args += before[i]
+        if t is None:
+            args.append(None)
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{entry} needs every tensor on the GPU")
+        d = t.device
+        if dev is None:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{entry} needs every tensor on one GPU (got {dev} and {d})")
+        n = t.dim()
+        if n > 4:
+            raise ValueError("kda tensors have at most 4 dimensions")
+        pad = (0,) * (4 - n)
+        _DESC.pack_into(buf, i * _DESC.size, t.data_ptr() if t.numel() else 0, _ENTRY_DTYPES.get(t.dtype, 99), n,
+                        *t.shape, *pad, *t.stride(), *pad)
+        args.append(base + i * _DESC.size)
+    args += after
+    if workspace:
+        ws = workspace[0]
+        args += [None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size()]
+    lib = load_library()
+    if dev is None:
+        raise ValueError(f"{entry} needs its tensors on the GPU")
+    if dev.index == torch.cuda.current_device():
+        s = torch.cuda.current_stream(dev) if stream is None else stream
+        status = getattr(lib, entry)(*args, s.cuda_stream if hasattr(s, "cuda_stream") else int(s))
+    else:
+        with torch.cuda.device(dev):
+            s = torch.cuda.current_stream(dev) if stream is None else stream
+            status = getattr(lib, entry)(*args, s.cuda_stream if hasattr(s, "cuda_stream") else int(s))
+    if status:
+        _check(lib, status)
+
+
+def _scratch(size, like, stream):
+    """A workspace of torch's caching allocator, kept from reuse until `stream` is done with it."""
+    ws = torch.empty(max(size, 0), dtype=torch.uint8, device=like.device)
+    if stream is not None and isinstance(stream, torch.cuda.Stream):
+        ws.record_stream(stream)
+    return ws if size > 0 else None
+
+
+def _sequences(q, cu_seqlens):
+    return q.shape[0] if cu_seqlens is None else max(cu_seqlens.shape[0] - 1, 0)
+
+
+def kda_gdr_fwd_workspace_size(total_tokens, num_sequences, num_value_heads):
+    return int(load_library().kda_gdr_fwd_workspace_size(total_tokens, num_sequences, num_value_heads))
+
+
+def kda_gdr_bwd_workspace_size(total_tokens, num_sequences, num_value_heads):
+    return int(load_library().kda_gdr_bwd_workspace_size(total_tokens, num_sequences, num_value_heads))
+
+
+def kda_gdr_fwd(q, k, v, g, beta, scale, cu_seqlens=None, initial_state=None, out=None, final_state=None,
+                stream=None, workspace=None):
+    """Chunked forward of the gated delta rule with one decay per head: g [B, T, Hv]
+    (see include/kda.h).  q, k and v may be strided views.  Returns (out, final_state);
+    out and final_state=True are allocated here when not given.  `workspace`: a uint8
+    device tensor of kda_gdr_fwd_workspace_size() bytes, or None (taken here from
+    torch's caching allocator)."""
+    if out is None:
+        out = torch.empty(v.shape, dtype=torch.bfloat16, device=v.device)
+    ranks = q.dim() == 4 and v.dim() == 4   # the C library rejects other ranks
+    if final_state is True:
+        final_state = torch.empty((_sequences(q, cu_seqlens), v.shape[-2], 128, 128), dtype=torch.float32,
+                                  device=v.device)
+    if workspace is None and ranks:
+        workspace = _scratch(kda_gdr_fwd_workspace_size(q.shape[0] * q.shape[1], _sequences(q, cu_seqlens), v.shape[2]),
+                             v, stream)
+    _launch("kda_gdr_fwd", (q, k, v, g, beta, cu_seqlens, initial_state, out, final_state), {5: [scale]}, [], stream,
+            (workspace,))
+    return out, final_state
+
+
+def kda_gdr_bwd(q, k, v, g, beta, scale, d_out, initial_state=None, d_final_state=None, grads=None,
+                d_initial_state=False, stream=None, workspace=None, cu_seqlens=None):
+    """Gradients of kda_gdr_fwd: a dict with dq, dk, dv (bf16), dg, dbeta (fp32) and dh0
+    (fp32 [N, Hv, 128, 128] when d_initial_state is True or a tensor, else None).
+    `grads` may hold preallocated outputs under those names; `workspace` a uint8 device
+    tensor of kda_gdr_bwd_workspace_size() bytes (None: taken here)."""
+    res = dict(grads or {})
+    for name, like, dtype in (("dq", q, torch.bfloat16), ("dk", k, torch.bfloat16), ("dv", v, torch.bfloat16),
+                              ("dg", g, torch.float32), ("dbeta", beta, torch.float32)):
+        if res.get(name) is None:
+            res[name] = torch.empty(like.shape, dtype=dtype, device=v.device)
+    if isinstance(d_initial_state, torch.Tensor):
+        res["dh0"] = d_initial_state
+    elif d_initial_state:
+        res["dh0"] = torch.empty((_sequences(q, cu_seqlens), v.shape[-2], 128, 128), dtype=torch.float32,
+                                 device=v.device)
+    else:
+        res["dh0"] = None
+    if workspace is None and q.dim() == 4 and v.dim() == 4:
+        workspace = _scratch(kda_gdr_bwd_workspace_size(q.shape[0] * q.shape[1], _sequences(q, cu_seqlens), v.shape[2]),
+                             v, stream)
+    _launch("kda_gdr_bwd", (q, k, v, g, beta, cu_seqlens, initial_state, d_out, d_final_state, res["dq"], res["dk"],
+                            res["dv"], res["dg"], res["dbeta"], res["dh0"]), {5: [scale]}, [], stream, (workspace,))
+    return res
+
+
+def kda_gdr_decode(q, k, v, g, beta, scale, state, state_indices=None, out=None, new_state=None, stream=None):
+    """One token per row: q, k [N, Hq, 128], v [N, Hv, 128], g and beta [N, Hv].  `state`
+    [N, Hv, 128, 128] fp32 (None: zero), or with `state_indices` (int32 [N]) a pool
+    [slots, Hv, 128, 128]: rows with a slot outside it (-1) are skipped, rows that share
+    one are taken in order.  The new states go to `new_state`, by default `state` itself.
+    Returns (out, new_state); rows of `out` that are skipped are not written."""
+    if out is None:
+        out = torch.empty(v.shape, dtype=torch.bfloat16, device=v.device)
+    if new_state is None:
+        if state is None and state_indices is not None:
+            raise ValueError("kda_gdr_decode needs a pool where state_indices name its slots")
+        new_state = state if state is not None else torch.empty((v.shape[0], v.shape[1], 128, 128),
+                                                                dtype=torch.float32, device=v.device)
+    _launch("kda_gdr_decode", (q, k, v, g, beta, state, new_state, state_indices, out), {5: [scale]}, [], stream)
+    return out, new_state
+
+
+_NORM_MODES = {"l2": 0, "rms": 1}
+
+
+def kda_qk_norm(q, k, q_weight=None, k_weight=None, mode="l2", eps=1e-6, cos=None, sin=None, positions=None,
+                interleaved=False, out=None, stream=None):
+    """Per-head norm of q [B, T, Hq, 128] and k [B, T, Hk, 128] (bf16, fp16 or fp32, may be
+    strided) with an optional weight and position rotation (see include/kda.h); mode "l2"
+    or "rms".  Returns (q_out, k_out) in bf16; `out` a pair of outputs, allocated here
+    when not given."""
+    if mode not in _NORM_MODES:
+        raise ValueError(f"kda_qk_norm: mode {mode!r} is neither 'l2' nor 'rms'")
+    qo, ko = out if out is not None else (torch.empty(q.shape, dtype=torch.bfloat16, device=q.device),
+                                          torch.empty(k.shape, dtype=torch.bfloat16, device=k.device))
+    _launch("kda_qk_norm", (q, k, q_weight, k_weight, cos, sin, positions, qo, ko),
+            {4: [_NORM_MODES[mode], eps], 7: [int(bool(interleaved))]}, [], stream)
+    return qo, ko
+
+
+def kda_qk_norm_bwd(q, k, d_q_out, d_k_out, q_weight=None, k_weight=None, mode="l2", eps=1e-6, cos=None, sin=None,
+                    positions=None, interleaved=False, grads=None, stream=None, workspace=None):
+    """Gradients of kda_qk_norm: a dict with dq, dk (q's dtype) and dq_weight, dk_weight
+    (fp32 [128], or None for a weight that is None).  `grads` may hold preallocated
+    outputs under those names."""
+    if mode not in _NORM_MODES:
+        raise ValueError(f"kda_qk_norm_bwd: mode {mode!r} is neither 'l2' nor 'rms'")
+    res = dict(grads or {})
+    for name, x in (("dq", q), ("dk", k)):
+        if res.get(name) is None:
+            res[name] = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    for name, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
+        if w is None:
+            res[name] = None
+        elif res.get(name) is None:
+            res[name] = torch.empty(w.shape, dtype=torch.float32, device=w.device)
+    if workspace is None and (q_weight is not None or k_weight is not None):
+        workspace = _scratch(int(load_library().kda_qk_norm_bwd_workspace_size()), q, stream)
+    _launch("kda_qk_norm_bwd", (q, k, d_q_out, d_k_out, q_weight, k_weight, cos, sin, positions, res["dq"], res["dk"],
+                                res["dq_weight"], res["dk_weight"]),
+            {6: [_NORM_MODES[mode], eps], 9: [int(bool(interleaved))]}, [], stream, (workspace,))
+    return res

@@ -16,12 +16,13 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libkda.so")
 SOURCES = [os.path.join(HERE, "csrc", f)
            for f in ("kda_fused.hip", "kda_intra.hip", "kda_scan.hip", "kda_compose.hip", "kda_decode.hip", "kda_bwd.hip", "kda_scratch.hip",
-              "kda_api.cpp")]
+              "kda_gdr_prep.hip", "kda_gdr_scan.hip", "kda_gdr_grads.hip", "kda_gdr_decode.hip", "kda_qk_norm.hip",
+              "kda_api.cpp", "kda_gdr_api.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 
 def build(verbose: bool = False) -> str:
-    cmd = [HIPCC, "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    cmd = [HIPCC, "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared", "-parallel-jobs=8",
            "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-mllvm", "-amdgpu-mfma-vgpr-form",
            "-I", os.path.join(ROOT, "include"), "-o", LIB + ".tmp"] + SOURCES
     if verbose:

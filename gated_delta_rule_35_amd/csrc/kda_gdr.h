@@ -1,0 +1,97 @@
+// Internal interface of the gated delta rule with one decay per token and value
+// head (kda_gdr_fwd, kda_gdr_bwd, kda_gdr_decode) and of the per-head q/k norm.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace kda {
+
+// A bf16 tensor [B, T, H, 128] whose last dimension is contiguous: strides in elements.
+struct Rows {
+    const uint16_t* p;
+    int64_t sb, st, sh;
+};
+
+struct GdrParams {
+    Rows q, k, v, dO;      // dO: gradient of the output (backward only)
+    const float* g;        // [B, T, Hv] log-decay
+    const void* beta;      // [B, T, Hv] bf16 bits or fp32
+    const int32_t* cu;     // [N + 1] offsets of packed sequences (B = 1), or nullptr
+    const float* h0;       // [N, Hv, 128, 128] or nullptr
+    uint16_t* o;           // [B, T, Hv, 128] bf16 bits
+    float* hT;             // [N, Hv, 128, 128] or nullptr
+    char* rec;             // [nslots][Hv] chunk records of the prep kernel
+    int64_t T;             // tokens per row
+    int64_t nslots;        // chunk slots: N * nc, or with cu ceil(T / 64) + N
+    int32_t N, Hq, Hv, nc; // nc = ceil(T / 64)
+    int32_t beta_f32;
+    float scale;
+    // backward
+    const float* dhT;      // [N, Hv, 128, 128] or nullptr
+    float* dh0;            // [N, Hv, 128, 128] or nullptr
+    uint16_t *dq, *dk, *dv;// [B, T, H, 128] bf16 bits
+    float *dg, *dbeta;     // [B, T, Hv]
+    float* S;              // [nslots][Hv][128][128] state entering each chunk
+    float* dS;             // [nslots][Hv][128][128] gradient of the state leaving each chunk
+    float* u;              // [nslots][Hv][64][128] corrected values of each chunk
+    float* dx;             // [nslots][Hv][64][128] gradient of the right-hand side beta (v - e^G K S)
+};
+
+// Chunk record of the prep kernel (see kda_gdr_prep.hip): the triangular operands as
+// lists of six 1 KB fragments per bf16 part, and four rows of per-token numbers.
+constexpr int GDR_FRAG = 1024;
+constexpr int GDR_TRI = 6 * GDR_FRAG;              // one part of a triangular operand
+constexpr int GDR_T = 0;                           // T, three parts
+constexpr int GDR_SC = GDR_T + 3 * GDR_TRI;        // e^G, e^{G_last - G}, beta, e^{G_last} ([64] fp32 each)
+constexpr int GDR_A = GDR_SC + 1024;               // A (scale included): two parts forward, three backward
+constexpr int gdr_rec_bytes(int na) { return GDR_A + na * GDR_TRI; }
+constexpr int GDR_NA_FWD = 2, GDR_NA_BWD = 3;
+
+// Fills the records with na parts of A.
+hipError_t launch_gdr_prep(const GdrParams& p, int na, hipStream_t stream);
+hipError_t launch_gdr_grads(const GdrParams& p, hipStream_t stream);
+hipError_t launch_gdr_fwd(const GdrParams& p, hipStream_t stream);
+hipError_t launch_gdr_bwd(const GdrParams& p, hipStream_t stream);
+
+struct GdrDecodeParams {
+    Rows q, k, v;          // [N, H, 128]: sb is the stride of N, st is unused
+    const float* g;        // [N, Hv]
+    const void* beta;      // [N, Hv]
+    const int32_t* idx;    // [N] state slots, or nullptr (slot n)
+    const float* s_in;     // [slots, Hv, 128, 128] or nullptr (zero)
+    float* s_out;          // [slots, Hv, 128, 128]; may equal s_in
+    uint16_t* o;           // [N, Hv, 128]
+    int32_t N, Hq, Hv, slots;
+    int32_t beta_f32;
+    float scale;
+};
+hipError_t launch_gdr_decode(const GdrDecodeParams& p, int cus, hipStream_t stream);
+
+// One tensor of the per-head norm: rows [B, T, H, 128].
+struct NormSide {
+    const void* x;         // input, dtype NormParams::xt
+    int64_t sb, st, sh;    // its strides in elements
+    const void* dy;        // backward: gradient of the output, contiguous, dtype NormParams::dt
+    void* y;               // forward: output bf16; backward: gradient of x, x's dtype; contiguous
+    const float* w;        // [128] or nullptr
+    float* dw;             // [128] or nullptr
+    int32_t H;
+    int64_t rows;          // B * T * H
+};
+struct NormParams {
+    NormSide s[2];         // queries, keys
+    const float *cos, *sin;// [P, half] or nullptr
+    const int32_t* pos;    // [B, T] or nullptr (the token's index in its row)
+    float* part;           // backward with weights: [blocks][128] partial sums
+    int64_t T, P;
+    int32_t half, interleaved, rms;
+    int32_t xt, dt;        // 0 bf16, 1 fp16, 2 fp32
+    float eps;
+    int32_t blocks[2];     // work-groups of each side
+};
+hipError_t launch_qk_norm(const NormParams& p, hipStream_t stream);
+hipError_t launch_qk_norm_bwd(const NormParams& p, hipStream_t stream);
+constexpr int NORM_ROWS = 16;            // rows that a work-group takes at a time
+constexpr int NORM_DW_BLOCKS = 512;      // most work-groups of a side when weights have gradients
+
+}  // namespace kda

@@ -1,0 +1,210 @@
+// Device helpers of the gated delta rule with one decay per head.
+//
+// Every matrix product runs on v_mfma_f32_16x16x32_bf16.  q, k, v and the output's
+// gradient are bf16 and enter as they are; an fp32 operand enters as the sum of
+// bf16 parts (each the rounding of what the parts before it leave), so that
+// products keep fp32's accuracy at a third to a sixth of the bf16 rate, which is
+// still several times the rate of the fp32 matrix instructions: three parts hold
+// all 24 bits, two hold 16.
+#pragma once
+#include "kda_device.h"
+#include "kda_gdr.h"
+
+namespace kda {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ f32x4 mfma_bf(bf16x8 a, bf16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// Eight fp32 values as NS bf16 parts, packed as MFMA operands.
+template <int NS>
+struct Split {
+    bf16x8 s[NS];
+};
+template <int NS>
+__device__ __forceinline__ Split<NS> split8(const float (&x)[8]) {
+    u32x4 w[NS];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a = x[2 * i], b = x[2 * i + 1];
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+            const uint32_t h = pack_bf2(a, b);
+            w[n][i] = h;
+            if (n + 1 < NS) {
+                a -= bf_lo(h);
+                b -= bf_hi(h);
+            }
+        }
+    }
+    Split<NS> r;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) r.s[n] = __builtin_bit_cast(bf16x8, w[n]);
+    return r;
+}
+// Two accumulator tiles (rows 4 g + r of each, r < 4) as the B operand of a 32-wide
+// k step whose index runs over tile 0's four rows of lane group g, then tile 1's.
+template <int NS>
+__device__ __forceinline__ Split<NS> split_acc(f32x4 a, f32x4 b) {
+    const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    return split8<NS>(x);
+}
+
+// c += A B with A given in NA parts and B in NB; products of parts whose weights
+// are below 2^-8 LIM of the leading product's are left out (LIM = 3: what 24 bits
+// hold, LIM = 2: what 16 bits hold).  The small products come first.
+template <int LIM, int NA, int NB>
+__device__ __forceinline__ f32x4 mfma_split(const bf16x8 (&a)[NA], const Split<NB>& b, f32x4 c) {
+#pragma unroll
+    for (int d = LIM - 1; d >= 0; --d) {
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            if (d - i >= 0 && d - i < NB) c = mfma_bf(a[i], b.s[d - i], c);
+        }
+    }
+    return c;
+}
+
+// ---- swizzled [64][128] bf16 tiles in LDS: rows of 256 bytes, whose sixteen 16-byte
+// pieces are permuted by tsw(row), so that both an operand read (sixteen consecutive
+// rows at one piece) and a transposing read (four consecutive rows at four
+// consecutive pieces) touch every bank once.
+__device__ __forceinline__ int tsw(int row) { return ((row & 3) << 2) | ((row >> 2) & 3); }
+__device__ __forceinline__ int tile_off(int row, int piece) { return row * 256 + ((piece ^ tsw(row)) << 4); }
+
+__device__ __forceinline__ bf16x8 lds_bf8(const char* p) { return *reinterpret_cast<const bf16x8*>(p); }
+
+// Transposing read: in each group of 16 lanes, lane 4 a + b receives element b of the
+// 8-byte pieces addressed by lanes a, a + 4, a + 8, a + 12 of the group.
+__device__ __forceinline__ u32x2 lds_tr(const char* p) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                         (__attribute__((address_space(3))) v4i16*)(p)));
+}
+
+// Two transposing reads as one operand.
+__device__ __forceinline__ bf16x8 join(u32x2 a, u32x2 b) {
+    return __builtin_bit_cast(bf16x8, u32x4{a[0], a[1], b[0], b[1]});
+}
+
+// One 1 KB piece by DMA: lane l's 16 bytes at `voff` of the buffer to byte 16 l of
+// the LDS address.  Nothing waits for it here; offsets past the buffer's range
+// arrive as zeros.
+__device__ __forceinline__ void dma_piece(__amdgpu_buffer_rsrc_t r, uint32_t lds, int voff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(r)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t lds_addr(const char* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
+}
+
+// Rows of a chunk (64 rows, `rows` of them real) of a bf16 tensor: base of its first
+// row and the bytes that the real rows span.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rsrc(const uint16_t* base, int64_t st, int rows, int cols) {
+    return make_rsrc(base, rows > 0 ? ((int64_t)(rows - 1) * st + cols) * 2 : 0);
+}
+// The swizzled tile of a chunk's rows by DMA: the sixteen pieces split over `nw` waves.
+__device__ __forceinline__ void dma_tile(__amdgpu_buffer_rsrc_t r, uint32_t lds, int64_t st, int wave, int nw, int lane) {
+    for (int u = wave; u < 16; u += nw) {
+        const int row = 4 * u + (lane >> 4);
+        dma_piece(r, __builtin_amdgcn_readfirstlane(lds + u * 1024),
+                  (int)(row * st * 2) + (((lane & 15) ^ tsw(row)) << 4));
+    }
+}
+
+// ---- chunks ----
+// First token (in its row), length and row of sequence n, clamped to the row.
+__device__ __forceinline__ void gdr_seq(const GdrParams& p, int n, int64_t& bos, int64_t& len, int64_t& row,
+                                        int64_t& slot0) {
+    if (p.cu) {
+        int64_t a = p.cu[n], e = p.cu[n + 1];
+        a = a < 0 ? 0 : (a > p.T ? p.T : a);
+        e = e < a ? a : (e > p.T ? p.T : e);
+        bos = a;
+        len = e - a;
+        row = 0;
+        slot0 = a / CH + n;
+    } else {
+        bos = 0;
+        len = p.T;
+        row = n;
+        slot0 = (int64_t)n * p.nc;
+    }
+}
+// The chunk in slot s: its sequence, first token and real rows (0: the slot is empty).
+// Packed sequence n's slots start at cu[n] / 64 + n, which grows with n.
+__device__ __forceinline__ int gdr_chunk(const GdrParams& p, int64_t s, int64_t& tok, int64_t& row) {
+    int n;
+    if (p.cu) {
+        int lo = 0, hi = p.N - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            int64_t a = p.cu[mid];
+            a = a < 0 ? 0 : (a > p.T ? p.T : a);
+            if (a / CH + mid <= s) lo = mid;
+            else hi = mid - 1;
+        }
+        n = lo;
+    } else {
+        n = (int)(s / p.nc);
+    }
+    int64_t bos, len, slot0;
+    gdr_seq(p, n, bos, len, row, slot0);
+    const int64_t c = s - slot0;
+    tok = bos + c * CH;
+    const int64_t r = len - c * CH;
+    return c < 0 || r <= 0 ? 0 : (r >= CH ? CH : (int)r);
+}
+
+__device__ __forceinline__ float gdr_beta(const GdrParams& p, int64_t i) {
+    return p.beta_f32 ? reinterpret_cast<const float*>(p.beta)[i] : bf2f(reinterpret_cast<const uint16_t*>(p.beta)[i]);
+}
+
+// Running sum of a chunk's log-decays in units of log 2, lane i holding token i's:
+// summed in 64 bits and kept as an fp32 value and its remainder, so that differences
+// of far sums keep fp32's relative accuracy.  Log-decays below -200 (minus infinity
+// too) count as -200: their factor is 0 in fp32 either way, and sums stay finite.
+struct GSum {
+    float hi, lo;
+};
+__device__ __forceinline__ GSum gate_sum(float g, int lane) {
+    double x = (double)(g < -200.f ? -200.f : g) * 1.4426950408889634074;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const double y = __shfl_up(x, d);
+        if (lane >= d) x += y;
+    }
+    const float hi = (float)x;
+    return {hi, (float)(x - (double)hi)};
+}
+// 2^(a - b)
+__device__ __forceinline__ float gate_ratio(GSum a, GSum b) {
+    const float d = a.hi - b.hi;
+    return fexp2(d) * fmaf(a.lo - b.lo, LN2, 1.f);
+}
+__device__ __forceinline__ float gate_exp(GSum a) { return fexp2(a.hi) * fmaf(a.lo, LN2, 1.f); }
+
+// Sum over the 16 lanes of a group (lane & 15), in every lane.
+__device__ __forceinline__ float sum16(float x) {
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1) x += __shfl_xor(x, m);
+    return x;
+}
+
+// (sequence, value head) pair and dv slice of a work-group: work-groups are dealt to
+// the 8 XCDs round robin; each XCD takes a contiguous run of pairs with both slices,
+// so that the slices of a head and the value heads of a q/k head meet in one L2.
+__device__ __forceinline__ void pair_of_block(int b, int npairs, int& pair, int& sl) {
+    if ((npairs & 7) == 0) {
+        pair = (b & 7) * (npairs >> 3) + (b >> 4);
+        sl = (b >> 3) & 1;
+    } else {
+        pair = b >> 1;
+        sl = b & 1;
+    }
+}
+
+}  // namespace kda

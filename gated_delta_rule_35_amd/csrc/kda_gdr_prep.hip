@@ -1,0 +1,190 @@
+// Chunk-parallel preparation of the gated delta rule with one decay per head, on
+// gfx950 (MI355X).
+//
+// For a chunk of 64 tokens with G the running sum of g and Gam_ij = e^{G_i - G_j}:
+//   A = scale (Q K^T) Gam, j <= i;   M = beta_i (K K^T) Gam, j < i;   T = (I + M)^{-1}
+// The decay is one number per token, so Q K^T and K K^T are formed once per q/k head
+// from the bf16 operands as they are, and every value head of the group only scales
+// them: Gam_ij <= 1 is formed from the differences themselves, so no operand needs an
+// anchor and no decay is out of range.
+//
+// One 256-thread work-group per (chunk slot, q/k head) walks the group's value heads.
+// Wave w holds rows 16 w .. + 15: tiles (w, J <= w) of both products (at most 32
+// MFMAs).  T in fp32: wave w inverts the diagonal block w by forward substitution,
+// then forms block column w downwards on v_mfma_f32_16x16x4f32,
+//   T_IJ = -T_II sum_{K=J}^{I-1} M_IK T_KJ,
+// with the T_KJ of its column in registers (an accumulator tile is the next product's
+// B operand).  The results leave as operand fragments in bf16 parts, T in three and
+// A in NA (two for the forward's bf16 output, three for the backward).
+// Fragment (m, kk) holds in lane l rows 16 m + l % 16, columns 32 kk + 16 (s / 4) +
+// 4 (l / 16) + s % 4, s < 8: the order in which accumulator tiles list a 32-wide k
+// step.  The lists hold (0,0) (1,0) (2,0) (2,1) (3,0) (3,1), zeros above the diagonal.
+#include "kda_gdr_device.h"
+
+namespace kda {
+
+namespace {
+constexpr int SP = 68;   // row stride of the fp32 64x64 matrices (64 + 4: 16-byte aligned rows, spread banks)
+}
+
+template <int NA>
+__global__ void __launch_bounds__(256) kda_gdr_prep_kernel(const GdrParams p) {
+    __shared__ __attribute__((aligned(16))) float sM[64 * SP];
+    __shared__ __attribute__((aligned(16))) float sT[64 * SP];
+    __shared__ __attribute__((aligned(16))) float sA[64 * SP];
+    __shared__ GSum sG[64];
+    __shared__ float sBeta[64];
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, jj = lane & 15;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t slot = blockIdx.x / p.Hq;
+    const int hq = blockIdx.x % p.Hq, R = p.Hv / p.Hq;
+    int64_t tok, row;
+    const int rows = gdr_chunk(p, slot, tok, row);
+    if (rows == 0) return;
+
+    // raw products, tiles (w, J), J <= w: lane holds rows 16 w + 4 g + r of column 16 J + jj
+    f32x4 qk[4], kk[4];
+    {
+        const __amdgpu_buffer_rsrc_t rq =
+            chunk_rsrc(p.q.p + row * p.q.sb + tok * p.q.st + hq * p.q.sh, p.q.st, rows, DK);
+        const __amdgpu_buffer_rsrc_t rk =
+            chunk_rsrc(p.k.p + row * p.k.sb + tok * p.k.st + hq * p.k.sh, p.k.st, rows, DK);
+        const int qst = (int)p.q.st * 2, kst = (int)p.k.st * 2;
+        bf16x8 aq[4], ak[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            aq[c] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rq, (16 * w + jj) * qst + 64 * c + 16 * g, 0, 0));
+            ak[c] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rk, (16 * w + jj) * kst + 64 * c + 16 * g, 0, 0));
+        }
+#pragma unroll
+        for (int J = 0; J < 4; ++J) {
+            qk[J] = kk[J] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (J <= w) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const bf16x8 b = __builtin_bit_cast(
+                        bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rk, (16 * J + jj) * kst + 64 * c + 16 * g, 0, 0));
+                    qk[J] = mfma_bf(aq[c], b, qk[J]);
+                    kk[J] = mfma_bf(ak[c], b, kk[J]);
+                }
+            }
+        }
+    }
+    // tiles above the diagonal that fragments cover
+    for (int e = tid; e < 512; e += 256) {
+        const int t = e >> 8, x = e & 255, at = (32 * t + (x >> 4)) * SP + 32 * t + 16 + (x & 15);
+        sT[at] = 0.f;
+        sA[at] = 0.f;
+    }
+
+    for (int r = 0; r < R; ++r) {
+        const int hv = hq * R + r;
+        const int64_t gi = (row * p.T + tok) * p.Hv + hv;
+        if (w == 0) {
+            const bool in = lane < rows;   // tokens past the end change nothing: g = 0, beta = 0
+            sG[lane] = gate_sum(in ? p.g[gi + (int64_t)lane * p.Hv] : 0.f, lane);
+            sBeta[lane] = in ? gdr_beta(p, gi + (int64_t)lane * p.Hv) : 0.f;
+        }
+        __syncthreads();
+        char* rec = p.rec + (slot * p.Hv + hv) * gdr_rec_bytes(NA);
+        if (w == 0) {
+            float* sc = reinterpret_cast<float*>(rec + GDR_SC);
+            const GSum G = sG[lane], GL = sG[63];
+            sc[lane] = gate_exp(G);
+            sc[64 + lane] = gate_ratio(GL, G);
+            sc[128 + lane] = sBeta[lane];
+            sc[192 + lane] = gate_exp(GL);
+        }
+#pragma unroll
+        for (int J = 0; J < 4; ++J) {
+            if (J <= w) {
+                const int j = 16 * J + jj;
+                const GSum Gj = sG[j];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 16 * w + 4 * g + e;
+                    const float gam = j <= i ? gate_ratio(sG[i], Gj) : 0.f;
+                    sA[i * SP + j] = j <= i ? p.scale * (qk[J][e] * gam) : 0.f;
+                    sM[i * SP + j] = j < i ? sBeta[i] * (kk[J][e] * gam) : 0.f;
+                }
+            }
+        }
+        __syncthreads();
+        {   // diagonal block w: lane column jj (lane groups repeat each other)
+            const float* m = sM + 16 * w * SP + 16 * w;
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                x[i] = i == jj ? 1.f : 0.f;
+#pragma unroll
+                for (int k4 = 0; k4 < i; k4 += 4) {
+                    const f32x4 a = *reinterpret_cast<const f32x4*>(m + i * SP + k4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (k4 + e < i) x[i] = fmaf(-a[e], x[k4 + e], x[i]);
+                }
+            }
+            if (lane < 16) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sT[(16 * w + i) * SP + 16 * w + jj] = x[i];
+            }
+        }
+        __syncthreads();
+        {   // block column w downwards
+            f32x4 t[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[0][e] = sT[(16 * w + 4 * g + e) * SP + 16 * w + jj];
+#pragma unroll
+            for (int s = 1; s < 4; ++s) {   // row block I = w + s; t[n] is T_{w + n, w}
+                const int I = w + s;
+                if (I < 4) {
+                    f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = x;
+#pragma unroll
+                    for (int n = 0; n < s; ++n) {
+                        const f32x4 a =
+                            *reinterpret_cast<const f32x4*>(sM + (16 * I + jj) * SP + 16 * (w + n) + 4 * g);
+                        x = __builtin_amdgcn_mfma_f32_16x16x4f32(a[0], t[n][0], x, 0, 0, 0);
+                        y = __builtin_amdgcn_mfma_f32_16x16x4f32(a[1], t[n][1], y, 0, 0, 0);
+                        x = __builtin_amdgcn_mfma_f32_16x16x4f32(a[2], t[n][2], x, 0, 0, 0);
+                        y = __builtin_amdgcn_mfma_f32_16x16x4f32(a[3], t[n][3], y, 0, 0, 0);
+                    }
+                    x += y;
+                    const f32x4 a = *reinterpret_cast<const f32x4*>(sT + (16 * I + jj) * SP + 16 * I + 4 * g);
+                    f32x4 z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z = __builtin_amdgcn_mfma_f32_16x16x4f32(-a[e], x[e], z, 0, 0, 0);
+                    t[s] = z;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sT[(16 * I + 4 * g + e) * SP + 16 * w + jj] = z[e];
+                }
+            }
+        }
+        __syncthreads();
+        // fragments: six of T's and six of A's, three to a wave
+#pragma unroll
+        for (int f3 = 0; f3 < 3; ++f3) {
+            const int f = 4 * f3 + w, which = f >= 6, x = which ? f - 6 : f;
+            const int m = x < 2 ? x : 2 + ((x - 2) >> 1), c = x < 2 ? 0 : x & 1;   // (m, kk)
+            const float* a = (which ? sA : sT) + (16 * m + jj) * SP + 32 * c + 4 * g;
+            const f32x4 u0 = *reinterpret_cast<const f32x4*>(a), u1 = *reinterpret_cast<const f32x4*>(a + 16);
+            const Split<3> parts = split_acc<3>(u0, u1);
+            char* dst = rec + (which ? GDR_A : GDR_T) + x * GDR_FRAG + lane * 16;
+#pragma unroll
+            for (int n = 0; n < 3; ++n)
+                if (n < NA || !which) *reinterpret_cast<bf16x8*>(dst + n * GDR_TRI) = parts.s[n];
+        }
+        __syncthreads();   // the matrices' reads before the next value head's writes
+    }
+}
+
+hipError_t launch_gdr_prep(const GdrParams& p, int na, hipStream_t stream) {
+    const int64_t blocks = p.nslots * p.Hq;
+    if (blocks == 0) return hipSuccess;
+    if (na == GDR_NA_FWD)
+        hipLaunchKernelGGL(kda_gdr_prep_kernel<GDR_NA_FWD>, dim3((unsigned)blocks), dim3(256), 0, stream, p);
+    else
+        hipLaunchKernelGGL(kda_gdr_prep_kernel<GDR_NA_BWD>, dim3((unsigned)blocks), dim3(256), 0, stream, p);
+    return hipGetLastError();
+}
+
+}  // namespace kda

@@ -426,6 +426,138 @@ kda_status_t kda_bwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda_ten
                      const kda_tensor_t* dbeta, const kda_tensor_t* d_initial_state, void* workspace,
                      int64_t workspace_size, void* stream);
 
+/*
+ * The gated delta rule with one decay per token and value head, beside the
+ * per-channel decay of the entry points above: for every sequence and value head
+ *
+ *     S_t = e^{g_t} (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T,   o_t = scale * S_t^T q_t
+ *
+ * with g and beta one number per token and value head.  Everything below follows
+ * kda_fwd's conventions (stream order, host-side checks before any HIP call,
+ * bitwise reproducible results, no pointer kept) except where stated.
+ *
+ * Shapes (N = B, or cu_seqlens' sequences with B = 1, as for kda_fwd):
+ *   q, k           [B, T, Hq, 128]       bf16
+ *   v              [B, T, Hv, 128]       bf16
+ *   g              [B, T, Hv]            fp32 log-decay (<= 0; minus infinity forgets the state)
+ *   beta           [B, T, Hv]            bf16 or fp32
+ *   states         [N, Hv, 128, 128]     fp32 (key channel, value channel)
+ * Strided inputs: q, k, v (and d_out) may be views whose 128 channels are
+ * contiguous, with 16-byte aligned data and strides that are non-negative
+ * multiples of 8 elements, tokens 128 to 2^23 elements apart (for instance slices
+ * of one projection's rows); KDA_ERR_LAYOUT otherwise.  Every other tensor is
+ * contiguous, and so are all outputs.  An output that shares memory with an input
+ * or with another output returns KDA_ERR_LAYOUT (final_state may be initial_state).
+ * Log-decays below -200 count as -200 (their factor is 0 in fp32 either way).
+ * cu_seqlens' precondition and clamping are kda_fwd's; rows of tokens in no
+ * sequence are not written.  More than 2^22 (chunk slot, value head) units, 2^31 - 1
+ * tokens or 2^21 (sequence, value head) pairs return KDA_ERR_UNSUPPORTED.
+ * Precision: products run on bf16 matrix instructions with fp32 operands given in
+ * two or three bf16 parts, so that states, dg and dbeta have fp32's accuracy (about
+ * 1e-6 relative), whatever the range of the values; o, dq, dk and dv are rounded to
+ * bf16 once.
+ */
+
+/*
+ * kda_gdr_fwd -- the chunked forward (chunks of 64 tokens).  A prep kernel forms
+ * every chunk's triangular operands at once, a scan kernel walks the chunks.
+ * out [B, T, Hv, 128] bf16; initial_state and final_state may be NULL.
+ * workspace: at least kda_gdr_fwd_workspace_size(B * T, N, Hv) bytes of device
+ * memory, 16-byte aligned, owned by the caller and not used by anything else until
+ * the call's work on `stream` has finished; NULL makes the library allocate it with
+ * hipMallocAsync on `stream` and release it with hipFreeAsync.  With a workspace the
+ * call only launches kernels and can be captured into a HIP graph.
+ */
+int64_t kda_gdr_fwd_workspace_size(int64_t total_tokens, int64_t num_sequences, int64_t num_value_heads);
+kda_status_t kda_gdr_fwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda_tensor_t* v, const kda_tensor_t* g,
+                         const kda_tensor_t* beta, float scale, const kda_tensor_t* cu_seqlens,
+                         const kda_tensor_t* initial_state, const kda_tensor_t* out, const kda_tensor_t* final_state,
+                         void* workspace, int64_t workspace_size, void* stream);
+
+/*
+ * kda_gdr_bwd -- gradients of kda_gdr_fwd, given the gradients of the output (d_out
+ * [B, T, Hv, 128] bf16, may be strided) and of the final state (d_final_state, NULL
+ * for zero).
+ *   dq, dk   [B, T, Hq, 128] bf16 (summed over the value heads of a group)
+ *   dv       [B, T, Hv, 128] bf16
+ *   dg, dbeta [B, T, Hv]     fp32
+ *   d_initial_state [N, Hv, 128, 128] fp32, or NULL (not computed)
+ * An empty sequence passes d_final_state through to its d_initial_state.
+ * workspace: as for kda_gdr_fwd, of kda_gdr_bwd_workspace_size(B * T, N, Hv) bytes,
+ * 256-byte aligned.  Per (chunk slot, value head): 37,888 bytes of operands, the
+ * states entering and the state gradients leaving (64 KB each), and two fp32 token
+ * blocks (32 KB each).
+ */
+int64_t kda_gdr_bwd_workspace_size(int64_t total_tokens, int64_t num_sequences, int64_t num_value_heads);
+kda_status_t kda_gdr_bwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda_tensor_t* v, const kda_tensor_t* g,
+                         const kda_tensor_t* beta, float scale, const kda_tensor_t* cu_seqlens,
+                         const kda_tensor_t* initial_state, const kda_tensor_t* d_out,
+                         const kda_tensor_t* d_final_state, const kda_tensor_t* dq, const kda_tensor_t* dk,
+                         const kda_tensor_t* dv, const kda_tensor_t* dg, const kda_tensor_t* dbeta,
+                         const kda_tensor_t* d_initial_state, void* workspace, int64_t workspace_size, void* stream);
+
+/*
+ * kda_gdr_decode -- the recurrent form: one token for each of N rows.  Shapes: q, k
+ * [N, Hq, 128], v [N, Hv, 128] bf16 (may be strided as above, any row stride); g, beta
+ * [N, Hv]; out [N, Hv, 128] bf16.
+ * state_indices NULL: state_in (NULL for zero) and state_out are [N, Hv, 128, 128] and
+ * row n uses state n.  state_indices [N] int32: the states are pools [slots, Hv, 128,
+ * 128] and row n uses slot state_indices[n].  A row whose slot lies outside the pool
+ * (-1, say) is skipped: its row of out is not written.  Rows that name the same slot
+ * are tokens of one sequence, taken in the order of the batch.  Slots that no row
+ * names are not read, and not written.
+ * state_out may be state_in (updated in place) or a separate buffer; a partial overlap
+ * returns KDA_ERR_LAYOUT.  All arithmetic is fp32; o is rounded to bf16 once.  N * Hv
+ * above 2^20 returns KDA_ERR_UNSUPPORTED.  The call allocates nothing.
+ */
+kda_status_t kda_gdr_decode(const kda_tensor_t* q, const kda_tensor_t* k, const kda_tensor_t* v, const kda_tensor_t* g,
+                            const kda_tensor_t* beta, float scale, const kda_tensor_t* state_in,
+                            const kda_tensor_t* state_out, const kda_tensor_t* state_indices, const kda_tensor_t* out,
+                            void* stream);
+
+/*
+ * kda_qk_norm -- the norm of every query and key head before the delta rule (kda_fwd
+ * and kda_gdr_fwd want L2-normalised q and k), with an optional position rotation in
+ * the same pass.  For a row x of 128 channels:
+ *
+ *     z = x * r * w,  r = (sum x^2 + eps)^{-1/2} (mode 0, L2) or (sum x^2 / 128 + eps)^{-1/2} (mode 1, RMS)
+ *     y = z with the pairs (a, b) of its first 2 * half channels turned by the token's
+ *         position: (a cos - b sin, b cos + a sin); pairs (i, i + half), or (2i, 2i + 1)
+ *         when `interleaved` is not zero
+ *
+ *   q [B, T, Hq, 128], k [B, T, Hk, 128]  bf16, fp16 or fp32 (both the same), strided as above
+ *   q_weight, k_weight  [128] fp32, or NULL (ones)
+ *   cos, sin            [P, half] fp32 tables, half a multiple of 8 up to 64; both NULL: no rotation
+ *   positions           [B, T] int32 row of the tables of each token, or NULL (the token's
+ *                       index in its row); values outside [0, P) take the nearest row
+ *   q_out, k_out        bf16, contiguous; q_out may be q itself where q is contiguous bf16,
+ *                       and likewise k; any other overlap returns KDA_ERR_LAYOUT
+ * eps must be finite and positive, mode 0 or 1 (KDA_ERR_VALUE).  Arithmetic is fp32,
+ * each output is rounded once.
+ */
+kda_status_t kda_qk_norm(const kda_tensor_t* q, const kda_tensor_t* k, const kda_tensor_t* q_weight,
+                         const kda_tensor_t* k_weight, int32_t mode, float eps, const kda_tensor_t* cos,
+                         const kda_tensor_t* sin, const kda_tensor_t* positions, int32_t interleaved,
+                         const kda_tensor_t* q_out, const kda_tensor_t* k_out, void* stream);
+
+/*
+ * kda_qk_norm_bwd -- gradients of kda_qk_norm with respect to q, k and the weights.
+ *   d_q_out, d_k_out  contiguous bf16 or fp32 (both the same), of q's and k's shapes
+ *   dq, dk            contiguous, q's and k's dtype
+ *   d_q_weight, d_k_weight  [128] fp32, or NULL (not computed); without the weight
+ *                     itself KDA_ERR_NULL
+ * workspace: kda_qk_norm_bwd_workspace_size() bytes, 16-byte aligned, needed only with
+ * weight gradients; NULL then allocates it in stream order.  The weight gradients are
+ * summed in a fixed order.  Outputs must not overlap inputs or each other.
+ */
+int64_t kda_qk_norm_bwd_workspace_size(void);
+kda_status_t kda_qk_norm_bwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda_tensor_t* d_q_out,
+                             const kda_tensor_t* d_k_out, const kda_tensor_t* q_weight, const kda_tensor_t* k_weight,
+                             int32_t mode, float eps, const kda_tensor_t* cos, const kda_tensor_t* sin,
+                             const kda_tensor_t* positions, int32_t interleaved, const kda_tensor_t* dq,
+                             const kda_tensor_t* dk, const kda_tensor_t* d_q_weight, const kda_tensor_t* d_k_weight,
+                             void* workspace, int64_t workspace_size, void* stream);
+
 /* Human-readable name of a status code (static storage; never NULL). */
 const char* kda_status_string(kda_status_t status);
 

@@ -9,9 +9,9 @@ strides); the stream is torch's current HIP stream unless one is given.  Where
 an entry point takes a workspace, it is a uint8 device tensor the caller passes
 or one taken here from torch's caching allocator.
 """
+import array
 import ctypes
 import os
-import struct
 
 import torch
 
@@ -33,6 +33,9 @@ EXPORTED = ["kda_fwd", "kda_fwd_fused", "kda_fwd_ws", "kda_fwd_qg", "kda_fwd_noa
 class KdaTensor(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int), ("ndim", ctypes.c_int32),
                 ("shape", ctypes.c_int64 * 4), ("stride", ctypes.c_int64 * 4)]
+
+
+_DESC_BYTES = ctypes.sizeof(KdaTensor)
 
 
 class KdaTrace(ctypes.Structure):
@@ -447,64 +450,78 @@ def kda_bwd(q, k, v, g, beta, scale, d_out, initial_state=None, d_final_state=No
 
 
 # ---- gated delta rule with one decay per head, per-head q/k norm ----
-# These entry points are called once per layer and token while serving, where the host's
-# share of a call counts: all descriptors of a call are packed into one buffer.
-_DESC = struct.Struct("Pii8q")
-_ENTRY_DTYPES = {torch.bfloat16: KDA_BF16, torch.float16: KDA_F16, torch.float32: KDA_F32, torch.int32: KDA_I32}
+# These entry points are called for every layer and token while serving, where the
+# host's share of a call counts: all descriptors of a call lie in one array.
+_PAD = {n: (0,) * (4 - n) for n in range(5)}
 
 
-def _launch(entry, tensors, before, after, stream, workspace=()):
-    """Calls `entry` with descriptors of `tensors` (None: NULL) spliced into the scalar
-    arguments: before[i] scalars precede tensor i.  Tensors must be on one GPU, which is
-    made current for the call."""
-    dev = None
-    buf = ctypes.create_string_buffer(_DESC.size * len(tensors))
-    base = ctypes.addressof(buf)
-    args = []
-    for i, t in enumerate(tensors):
-        if i in before:
-            args += before[i]
-        if t is None:
-            args.append(None)
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{entry} needs every tensor on the GPU")
-        d = t.device
-        if dev is None:
+def _launch(entry, groups, stream, workspace=()):
+    """Calls `entry` with `groups`, alternating tuples of tensors (None: NULL) and of
+    scalars, then a workspace's address and size, then the stream.  The tensors must be on
+    one GPU, which is made current for the call."""
+    vals, dev = [], None
+    for t in [t for g in groups[::2] for t in g if t is not None]:
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
+                raise ValueError(f"{entry} needs every tensor on the GPU")
+            if dev is not None:
+                raise ValueError(f"{entry} needs every tensor on one GPU (got {dev} and {d})")
             dev = d
-        elif d != dev:
-            raise ValueError(f"{entry} needs every tensor on one GPU (got {dev} and {d})")
         n = t.dim()
-        if n > 4:
+        if n == 4:
+            vals += (t.data_ptr(), _DTYPES.get(t.dtype, 99) | 4 << 32, *t.shape, *t.stride())
+        elif n < 4:
+            pad = _PAD[n]
+            vals += (t.data_ptr(), _DTYPES.get(t.dtype, 99) | n << 32, *t.shape, *pad, *t.stride(), *pad)
+        else:
             raise ValueError("kda tensors have at most 4 dimensions")
-        pad = (0,) * (4 - n)
-        _DESC.pack_into(buf, i * _DESC.size, t.data_ptr() if t.numel() else 0, _ENTRY_DTYPES.get(t.dtype, 99), n,
-                        *t.shape, *pad, *t.stride(), *pad)
-        args.append(base + i * _DESC.size)
-    args += after
-    if workspace:
-        ws = workspace[0]
-        args += [None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size()]
-    lib = load_library()
     if dev is None:
         raise ValueError(f"{entry} needs its tensors on the GPU")
-    if dev.index == torch.cuda.current_device():
-        s = torch.cuda.current_stream(dev) if stream is None else stream
-        status = getattr(lib, entry)(*args, s.cuda_stream if hasattr(s, "cuda_stream") else int(s))
+    descs = array.array("q", vals)   # kda_tensor_t is ten 64-bit words (dtype and rank share one)
+    at = descs.buffer_info()[0]
+    args = []
+    for i, g in enumerate(groups):
+        if i & 1:
+            args += g
+            continue
+        for t in g:
+            if t is None:
+                args.append(None)
+            else:
+                args.append(at)
+                at += _DESC_BYTES
+    for ws in workspace:
+        args += (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+    lib = load_library()
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if dev == torch.cuda.current_device():
+        status = getattr(lib, entry)(*args, s)
     else:
         with torch.cuda.device(dev):
-            s = torch.cuda.current_stream(dev) if stream is None else stream
-            status = getattr(lib, entry)(*args, s.cuda_stream if hasattr(s, "cuda_stream") else int(s))
+            status = getattr(lib, entry)(*args, s)
     if status:
         _check(lib, status)
 
 
+def _new(like, dtype, shape=None):
+    """An uninitialised contiguous tensor beside `like`."""
+    if shape is None:
+        return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
+    return like.new_empty(shape, dtype=dtype)
+
+
 def _scratch(size, like, stream):
     """A workspace of torch's caching allocator, kept from reuse until `stream` is done with it."""
-    ws = torch.empty(max(size, 0), dtype=torch.uint8, device=like.device)
+    if size <= 0:
+        return None
+    ws = like.new_empty(size, dtype=torch.uint8)
     if stream is not None and isinstance(stream, torch.cuda.Stream):
         ws.record_stream(stream)
-    return ws if size > 0 else None
+    return ws
 
 
 def _sequences(q, cu_seqlens):
@@ -527,15 +544,13 @@ def kda_gdr_fwd(q, k, v, g, beta, scale, cu_seqlens=None, initial_state=None, ou
     device tensor of kda_gdr_fwd_workspace_size() bytes, or None (taken here from
     torch's caching allocator)."""
     if out is None:
-        out = torch.empty(v.shape, dtype=torch.bfloat16, device=v.device)
-    ranks = q.dim() == 4 and v.dim() == 4   # the C library rejects other ranks
+        out = _new(v, torch.bfloat16)
     if final_state is True:
-        final_state = torch.empty((_sequences(q, cu_seqlens), v.shape[-2], 128, 128), dtype=torch.float32,
-                                  device=v.device)
-    if workspace is None and ranks:
+        final_state = _new(v, torch.float32, (_sequences(q, cu_seqlens), v.shape[-2], 128, 128))
+    if workspace is None and q.dim() == 4 and v.dim() == 4:   # the C library rejects other ranks
         workspace = _scratch(kda_gdr_fwd_workspace_size(q.shape[0] * q.shape[1], _sequences(q, cu_seqlens), v.shape[2]),
                              v, stream)
-    _launch("kda_gdr_fwd", (q, k, v, g, beta, cu_seqlens, initial_state, out, final_state), {5: [scale]}, [], stream,
+    _launch("kda_gdr_fwd", ((q, k, v, g, beta), (scale,), (cu_seqlens, initial_state, out, final_state)), stream,
             (workspace,))
     return out, final_state
 
@@ -550,19 +565,19 @@ def kda_gdr_bwd(q, k, v, g, beta, scale, d_out, initial_state=None, d_final_stat
     for name, like, dtype in (("dq", q, torch.bfloat16), ("dk", k, torch.bfloat16), ("dv", v, torch.bfloat16),
                               ("dg", g, torch.float32), ("dbeta", beta, torch.float32)):
         if res.get(name) is None:
-            res[name] = torch.empty(like.shape, dtype=dtype, device=v.device)
+            res[name] = _new(like, dtype)
     if isinstance(d_initial_state, torch.Tensor):
         res["dh0"] = d_initial_state
     elif d_initial_state:
-        res["dh0"] = torch.empty((_sequences(q, cu_seqlens), v.shape[-2], 128, 128), dtype=torch.float32,
-                                 device=v.device)
+        res["dh0"] = _new(v, torch.float32, (_sequences(q, cu_seqlens), v.shape[-2], 128, 128))
     else:
         res["dh0"] = None
     if workspace is None and q.dim() == 4 and v.dim() == 4:
         workspace = _scratch(kda_gdr_bwd_workspace_size(q.shape[0] * q.shape[1], _sequences(q, cu_seqlens), v.shape[2]),
                              v, stream)
-    _launch("kda_gdr_bwd", (q, k, v, g, beta, cu_seqlens, initial_state, d_out, d_final_state, res["dq"], res["dk"],
-                            res["dv"], res["dg"], res["dbeta"], res["dh0"]), {5: [scale]}, [], stream, (workspace,))
+    _launch("kda_gdr_bwd", ((q, k, v, g, beta), (scale,),
+                            (cu_seqlens, initial_state, d_out, d_final_state, res["dq"], res["dk"], res["dv"],
+                             res["dg"], res["dbeta"], res["dh0"])), stream, (workspace,))
     return res
 
 
@@ -573,13 +588,12 @@ def kda_gdr_decode(q, k, v, g, beta, scale, state, state_indices=None, out=None,
     one are taken in order.  The new states go to `new_state`, by default `state` itself.
     Returns (out, new_state); rows of `out` that are skipped are not written."""
     if out is None:
-        out = torch.empty(v.shape, dtype=torch.bfloat16, device=v.device)
+        out = _new(v, torch.bfloat16)
     if new_state is None:
         if state is None and state_indices is not None:
             raise ValueError("kda_gdr_decode needs a pool where state_indices name its slots")
-        new_state = state if state is not None else torch.empty((v.shape[0], v.shape[1], 128, 128),
-                                                                dtype=torch.float32, device=v.device)
-    _launch("kda_gdr_decode", (q, k, v, g, beta, state, new_state, state_indices, out), {5: [scale]}, [], stream)
+        new_state = state if state is not None else _new(v, torch.float32, (v.shape[0], v.shape[1], 128, 128))
+    _launch("kda_gdr_decode", ((q, k, v, g, beta), (scale,), (state, new_state, state_indices, out)), stream)
     return out, new_state
 
 
@@ -594,10 +608,9 @@ def kda_qk_norm(q, k, q_weight=None, k_weight=None, mode="l2", eps=1e-6, cos=Non
     when not given."""
     if mode not in _NORM_MODES:
         raise ValueError(f"kda_qk_norm: mode {mode!r} is neither 'l2' nor 'rms'")
-    qo, ko = out if out is not None else (torch.empty(q.shape, dtype=torch.bfloat16, device=q.device),
-                                          torch.empty(k.shape, dtype=torch.bfloat16, device=k.device))
-    _launch("kda_qk_norm", (q, k, q_weight, k_weight, cos, sin, positions, qo, ko),
-            {4: [_NORM_MODES[mode], eps], 7: [int(bool(interleaved))]}, [], stream)
+    qo, ko = out if out is not None else (_new(q, torch.bfloat16), _new(k, torch.bfloat16))
+    _launch("kda_qk_norm", ((q, k, q_weight, k_weight), (_NORM_MODES[mode], eps), (cos, sin, positions),
+                            (int(bool(interleaved)),), (qo, ko)), stream)
     return qo, ko
 
 
@@ -611,15 +624,15 @@ def kda_qk_norm_bwd(q, k, d_q_out, d_k_out, q_weight=None, k_weight=None, mode="
     res = dict(grads or {})
     for name, x in (("dq", q), ("dk", k)):
         if res.get(name) is None:
-            res[name] = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            res[name] = _new(x, x.dtype)
     for name, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
         if w is None:
             res[name] = None
         elif res.get(name) is None:
-            res[name] = torch.empty(w.shape, dtype=torch.float32, device=w.device)
+            res[name] = _new(w, torch.float32)
     if workspace is None and (q_weight is not None or k_weight is not None):
         workspace = _scratch(int(load_library().kda_qk_norm_bwd_workspace_size()), q, stream)
-    _launch("kda_qk_norm_bwd", (q, k, d_q_out, d_k_out, q_weight, k_weight, cos, sin, positions, res["dq"], res["dk"],
-                                res["dq_weight"], res["dk_weight"]),
-            {6: [_NORM_MODES[mode], eps], 9: [int(bool(interleaved))]}, [], stream, (workspace,))
+    _launch("kda_qk_norm_bwd", ((q, k, d_q_out, d_k_out, q_weight, k_weight), (_NORM_MODES[mode], eps),
+                                (cos, sin, positions), (int(bool(interleaved)),),
+                                (res["dq"], res["dk"], res["dq_weight"], res["dk_weight"])), stream, (workspace,))
     return res

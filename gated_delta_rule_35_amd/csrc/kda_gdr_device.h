@@ -20,6 +20,16 @@ __device__ __forceinline__ f32x4 mfma_bf(bf16x8 a, bf16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+// The bf16 pair (-1, 0), or (0, -1) with HI, in a scalar register.  Written as a constant
+// operand, the first becomes the inline -1.0, which v_dot2c reads as a 32-bit float.
+template <bool HI>
+__device__ __forceinline__ bf16x2v minus_one() {
+    uint32_t x;
+    if (HI) asm("s_mov_b32 %0, 0xbf800000" : "=s"(x));
+    else asm("s_mov_b32 %0, 0xbf80" : "=s"(x));
+    return __builtin_bit_cast(bf16x2v, x);
+}
+
 // Eight fp32 values as NS bf16 parts, packed as MFMA operands.
 template <int NS>
 struct Split {
@@ -33,11 +43,11 @@ __device__ __forceinline__ Split<NS> split8(const float (&x)[8]) {
         float a = x[2 * i], b = x[2 * i + 1];
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-            const uint32_t h = pack_bf2(a, b);
-            w[n][i] = h;
-            if (n + 1 < NS) {
-                a -= bf_lo(h);
-                b -= bf_hi(h);
+            const bf16x2v h = __builtin_convertvector(f32x2{a, b}, bf16x2v);
+            w[n][i] = __builtin_bit_cast(uint32_t, h);
+            if (n + 1 < NS) {   // a - h[0], b - h[1]: one instruction each, and exact
+                a = __builtin_amdgcn_fdot2_f32_bf16(h, minus_one<false>(), a, false);
+                b = __builtin_amdgcn_fdot2_f32_bf16(h, minus_one<true>(), b, false);
             }
         }
     }

@@ -27,7 +27,7 @@ namespace kda {
 
 namespace {
 
-constexpr int SCAN_THREADS = 256;
+constexpr int SCAN_THREADS = 384;   // four waves that compute, two that load
 // One LDS buffer: K, Q tiles (swizzled), the slice of v (or of do) [64][64] bf16, the record.
 template <int NA>
 struct ScanL {
@@ -61,30 +61,43 @@ __device__ __forceinline__ bf16x8 tri_col_frag(const char* part, int m, int kk, 
                 lds_tr(part + tri_frag(2 * kk + 1, m >> 1) * GDR_FRAG + at));
 }
 
-// The four waves' DMA of one chunk into a buffer.
-template <int NA>
-__device__ __forceinline__ void load_chunk(const GdrParams& p, const Rows& vsrc, char* buf, int64_t row, int64_t tok,
-                                           int rows, int hq, int hv, int sl, int64_t slot, int nrec, bool with_q, int w,
-                                           int lane) {
+// One loading wave's (ld = 0, 1) half of a chunk's DMA into a buffer: 32 pieces of
+// tiles and slices, and nrec of the record.
+template <int NA, int NREC, bool WITH_Q>
+__device__ __forceinline__ void load_chunk(const GdrParams& p, const Rows& vsrc, uint32_t lds, int64_t row, int64_t tok,
+                                           int rows, int hq, int hv, int sl, int64_t slot, int ld, int lane) {
     typedef ScanL<NA> L;
-    const uint32_t lds = lds_addr(buf);
-    dma_tile(chunk_rsrc(p.k.p + row * p.k.sb + tok * p.k.st + hq * p.k.sh, p.k.st, rows, DK), lds + L::K, p.k.st, w, 4,
-             lane);
-    if (with_q)
-        dma_tile(chunk_rsrc(p.q.p + row * p.q.sb + tok * p.q.st + hq * p.q.sh, p.q.st, rows, DK), lds + L::Q, p.q.st,
-                 w, 4, lane);
+    const __amdgpu_buffer_rsrc_t rk =
+        chunk_rsrc(p.k.p + row * p.k.sb + tok * p.k.st + hq * p.k.sh, p.k.st, rows, DK);
+    const int l4 = lane >> 4, l16 = lane & 15;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        const int r = 4 * (8 * ld + u) + l4;
+        dma_piece(rk, lds + L::K + (8 * ld + u) * 1024, (int)(r * p.k.st * 2) + ((l16 ^ tsw(4 * u + l4)) << 4));
+    }
+    if (WITH_Q) {
+        const __amdgpu_buffer_rsrc_t rq =
+            chunk_rsrc(p.q.p + row * p.q.sb + tok * p.q.st + hq * p.q.sh, p.q.st, rows, DK);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int r = 4 * (8 * ld + u) + l4;
+            dma_piece(rq, lds + L::Q + (8 * ld + u) * 1024, (int)(r * p.q.st * 2) + ((l16 ^ tsw(4 * u + l4)) << 4));
+        }
+    }
     const __amdgpu_buffer_rsrc_t rv =
         chunk_rsrc(vsrc.p + row * vsrc.sb + tok * vsrc.st + hv * vsrc.sh + 64 * sl, vsrc.st, rows, 64);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int x = 4 * u + w;   // eight rows a piece
-        dma_piece(rv, __builtin_amdgcn_readfirstlane(lds + L::V + x * 1024),
-                  (int)((8 * x + (lane >> 3)) * vsrc.st * 2) + ((lane & 7) << 4));
+    for (int u = 0; u < 4; ++u) {   // eight rows a piece
+        const int x = 4 * ld + u;
+        dma_piece(rv, lds + L::V + x * 1024, (int)((8 * x + (lane >> 3)) * vsrc.st * 2) + ((lane & 7) << 4));
     }
     const __amdgpu_buffer_rsrc_t rr =
         make_rsrc(p.rec + (slot * p.Hv + hv) * gdr_rec_bytes(NA), gdr_rec_bytes(NA));
-    for (int x = w; x < nrec; x += 4)
-        dma_piece(rr, __builtin_amdgcn_readfirstlane(lds + L::REC + x * 1024), x * 1024 + lane * 16);
+#pragma unroll
+    for (int u = 0; u < (NREC + 1) / 2; ++u) {
+        const int x = 2 * u + ld;
+        if (x < NREC) dma_piece(rr, lds + L::REC + x * 1024, x * 1024 + lane * 16);
+    }
 }
 
 }  // namespace
@@ -105,7 +118,25 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_scan_kernel(const GdrPar
     gdr_seq(p, n, bos, len, row, slot0);
     const int nch = (int)((len + CH - 1) / CH);
     const int col = 64 * sl + 16 * w + jj;   // the lane's value channel
-    constexpr int NREC = KEEP ? 19 : 19 + 6 * NA;   // pieces of the record that are read
+    auto rows_of = [&](int c) -> int {
+        const int64_t r = len - (int64_t)c * CH;
+        return r <= 0 ? 0 : (r >= CH ? CH : (int)r);
+    };
+    if (w >= 4) {   // loading waves: chunk c + 1 while the others are at chunk c
+        constexpr int NREC = KEEP ? 19 : 19 + 6 * NA;   // pieces of the record that are read
+        const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+        auto load = [&](int c) {
+            load_chunk<NA, NREC, !KEEP>(p, p.v, lds + (c & 1) * L::BYTES, row, bos + (int64_t)c * CH, rows_of(c), hq, hv,
+                                        sl, slot0 + c, w - 4, lane);
+        };
+        if (nch > 0) load(0);
+        for (int c = 0; c < nch; ++c) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's pieces of chunk c
+            lds_barrier();
+            if (c + 1 < nch) load(c + 1);
+        }
+        return;
+    }
 
     f32x4 S[8];
     const int64_t so = ((int64_t)n * p.Hv + hv) * DK * DK + col;
@@ -114,19 +145,8 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_scan_kernel(const GdrPar
 #pragma unroll
         for (int r = 0; r < 4; ++r) S[t][r] = p.h0 ? p.h0[so + state_row(t, g, r) * DK] : 0.f;
     }
-    auto rows_of = [&](int c) -> int {
-        const int64_t r = len - (int64_t)c * CH;
-        return r <= 0 ? 0 : (r >= CH ? CH : (int)r);
-    };
-    auto load = [&](int c) {
-        load_chunk<NA>(p, p.v, smem + (c & 1) * L::BYTES, row, bos + (int64_t)c * CH, rows_of(c), hq, hv, sl, slot0 + c,
-                       NREC, !KEEP, w, lane);
-    };
-    if (nch > 0) load(0);
     for (int c = 0; c < nch; ++c) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's pieces of chunk c
-        lds_barrier();                                     // everyone's; and the other buffer's reads are done
-        if (c + 1 < nch) load(c + 1);
+        lds_barrier();   // chunk c is in LDS, and the other buffer's reads are done
         char* buf = smem + (c & 1) * L::BYTES;
         const char *sK = buf + L::K, *sQ = buf + L::Q, *rec = buf + L::REC;
         const float* sc = reinterpret_cast<const float*>(rec + GDR_SC);
@@ -264,7 +284,24 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_rscan_kernel(const GdrPa
     gdr_seq(p, n, bos, len, row, slot0);
     const int nch = (int)((len + CH - 1) / CH);
     const int col = 64 * sl + 16 * w + jj;
-    constexpr int NREC = 19 + 6 * NA;
+    auto rows_of = [&](int c) -> int {
+        const int64_t r = len - (int64_t)c * CH;
+        return r <= 0 ? 0 : (r >= CH ? CH : (int)r);
+    };
+    if (w >= 4) {
+        const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+        auto load = [&](int c) {
+            load_chunk<NA, 19 + 6 * NA, true>(p, p.dO, lds + (c & 1) * L::BYTES, row, bos + (int64_t)c * CH, rows_of(c),
+                                              hq, hv, sl, slot0 + c, w - 4, lane);
+        };
+        if (nch > 0) load(nch - 1);
+        for (int c = nch - 1; c >= 0; --c) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            lds_barrier();
+            if (c > 0) load(c - 1);
+        }
+        return;
+    }
 
     f32x4 S[8];   // dS
     const int64_t so = ((int64_t)n * p.Hv + hv) * DK * DK + col;
@@ -273,19 +310,8 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_rscan_kernel(const GdrPa
 #pragma unroll
         for (int r = 0; r < 4; ++r) S[t][r] = p.dhT ? p.dhT[so + state_row(t, g, r) * DK] : 0.f;
     }
-    auto rows_of = [&](int c) -> int {
-        const int64_t r = len - (int64_t)c * CH;
-        return r <= 0 ? 0 : (r >= CH ? CH : (int)r);
-    };
-    auto load = [&](int c) {
-        load_chunk<NA>(p, p.dO, smem + (c & 1) * L::BYTES, row, bos + (int64_t)c * CH, rows_of(c), hq, hv, sl,
-                       slot0 + c, NREC, true, w, lane);
-    };
-    if (nch > 0) load(nch - 1);
     for (int c = nch - 1; c >= 0; --c) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         lds_barrier();
-        if (c > 0) load(c - 1);
         char* buf = smem + (c & 1) * L::BYTES;
         const char *sK = buf + L::K, *sQ = buf + L::Q, *rec = buf + L::REC;
         const float* sc = reinterpret_cast<const float*>(rec + GDR_SC);

@@ -247,6 +247,28 @@ def test_binding_refuses_host_tensors_and_modes():
         binding.kda_qk_norm(x, x, mode="max")
 
 
+class _On:
+    """A tensor's host-side view that says it lies on a GPU."""
+
+    def __init__(self, index):
+        self.index, self.x = index, torch.zeros(1, 4, 1, 128, dtype=torch.bfloat16)
+
+    def get_device(self):
+        return self.index
+
+    def __getattr__(self, name):
+        return getattr(self.x, name)
+
+
+@pytest.mark.parametrize("places", [(-1, 0), (0, -1), (0, 1), (1, 1, 0), (-1, -1), (0, 0, -1, 0)])
+def test_binding_refuses_mixed_places(places):
+    """Nothing is launched unless every tensor is on one GPU, in whatever order they come."""
+    with pytest.raises(ValueError):
+        binding._launch("kda_gdr_fwd", (tuple(_On(i) for i in places),), 0)
+    with pytest.raises(ValueError):
+        binding._launch("kda_gdr_fwd", (tuple(_On(i) for i in places[:1]), (1.0,), (None,) + tuple(_On(i) for i in places[1:])), 0)
+
+
 def test_reference_gradients_match_differences():
     """The tests' own 64-bit forms, by finite differences."""
     gen = torch.Generator().manual_seed(0)

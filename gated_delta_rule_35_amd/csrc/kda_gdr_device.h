@@ -169,8 +169,39 @@ __device__ __forceinline__ int gdr_chunk(const GdrParams& p, int64_t s, int64_t&
     return c < 0 || r <= 0 ? 0 : (r >= CH ? CH : (int)r);
 }
 
+// beta of element i.  The backward (BWD) takes no beta nearer to zero than 2^-40: its
+// dbeta is u's product with a gradient divided by beta, and an update of 2^-40 is far
+// below what the state's 24 bits hold.
+template <bool BWD>
 __device__ __forceinline__ float gdr_beta(const GdrParams& p, int64_t i) {
-    return p.beta_f32 ? reinterpret_cast<const float*>(p.beta)[i] : bf2f(reinterpret_cast<const uint16_t*>(p.beta)[i]);
+    const float b =
+        p.beta_f32 ? reinterpret_cast<const float*>(p.beta)[i] : bf2f(reinterpret_cast<const uint16_t*>(p.beta)[i]);
+    return BWD && fabsf(b) < 0x1p-40f ? 0x1p-40f : b;
+}
+
+// x of the lane that a DPP control names, 0 where it names none (or the row is masked out).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_f64(double x) {
+    const u32x2 w = __builtin_bit_cast(u32x2, x);
+    return __builtin_bit_cast(double, u32x2{(uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[0], CTRL, ROWS, 0xf, true),
+                                            (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[1], CTRL, ROWS, 0xf, true)});
+}
+// Sum of x over this lane and those before it in the wave: within rows of 16 lanes by
+// shifts, then each row's total on to the rows after it.
+__device__ __forceinline__ double prefix64(double x) {
+    x += dpp_f64<0x111, 0xf>(x);   // row_shr 1, 2, 4, 8
+    x += dpp_f64<0x112, 0xf>(x);
+    x += dpp_f64<0x114, 0xf>(x);
+    x += dpp_f64<0x118, 0xf>(x);
+    x += dpp_f64<0x142, 0xa>(x);   // row_bcast 15 into rows 1 and 3
+    x += dpp_f64<0x143, 0xc>(x);   // row_bcast 31 into rows 2 and 3
+    return x;
+}
+// x of one lane, in every lane (to be called where all lanes are active).
+__device__ __forceinline__ double lane_f64(double x, int lane) {
+    const u32x2 w = __builtin_bit_cast(u32x2, x);
+    return __builtin_bit_cast(double, u32x2{(uint32_t)__builtin_amdgcn_readlane((int)w[0], lane),
+                                            (uint32_t)__builtin_amdgcn_readlane((int)w[1], lane)});
 }
 
 // Running sum of a chunk's log-decays in units of log 2, lane i holding token i's:
@@ -180,13 +211,8 @@ __device__ __forceinline__ float gdr_beta(const GdrParams& p, int64_t i) {
 struct GSum {
     float hi, lo;
 };
-__device__ __forceinline__ GSum gate_sum(float g, int lane) {
-    double x = (double)(g < -200.f ? -200.f : g) * 1.4426950408889634074;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const double y = __shfl_up(x, d);
-        if (lane >= d) x += y;
-    }
+__device__ __forceinline__ GSum gate_sum(float g) {
+    const double x = prefix64((double)(g < -200.f ? -200.f : g) * 1.4426950408889634074);
     const float hi = (float)x;
     return {hi, (float)(x - (double)hi)};
 }
@@ -197,11 +223,23 @@ __device__ __forceinline__ float gate_ratio(GSum a, GSum b) {
 }
 __device__ __forceinline__ float gate_exp(GSum a) { return fexp2(a.hi) * fmaf(a.lo, LN2, 1.f); }
 
-// Sum over the 16 lanes of a group (lane & 15), in every lane.
+// x of the lane N places on in its group of 16 lanes (row_ror: no LDS access).
+template <int N>
+__device__ __forceinline__ float ror16(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x120 + N, 0xf, 0xf, true));
+}
+// Sum over the 16 lanes of a group (lane & 15), the same bits in every lane.
 __device__ __forceinline__ float sum16(float x) {
-#pragma unroll
-    for (int m = 1; m < 16; m <<= 1) x += __shfl_xor(x, m);
-    return x;
+    x += ror16<8>(x);
+    x += ror16<4>(x);
+    x += ror16<2>(x);
+    return x + ror16<1>(x);
+}
+// Sum over the wave.
+__device__ __forceinline__ float sum64(float x) {
+    x = sum16(x);
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
 }
 
 // (sequence, value head) pair and dv slice of a work-group: work-groups are dealt to

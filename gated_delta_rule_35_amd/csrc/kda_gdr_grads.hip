@@ -7,18 +7,21 @@
 // E = -beta_i Gam (dx u^T) (j < i), R1 = do S^T, R2 = u dS^T, R3 = dx S^T:
 //   dq = scale e^G R1 + P K
 //   dk = gam R2 - beta e^G R3 + P^T Q + (E + E^T) K
-//   dbeta_i = dx_i . v_i - e^{G_i} k_i . R3_i - sum_j Gam_ij (dx_i . u_j) (k_i . k_j)
-//   dG_i = scale e^{G_i} q_i . R1_i - beta_i e^{G_i} k_i . R3_i - t_i + (row i - column i
-//          of P (QK^T) + E (KK^T)),   t_i = gam_i k_i . R2_i,
-//   dG_last += sum t + e^{G_last} <S, dS>,   dg_t = sum_{i >= t} dG_i within the chunk.
+//   dbeta_i = dx_i . u_i / beta_i           (u = beta times what it multiplies)
+//   dG_i = scale e^{G_i} q_i . R1_i - beta_i e^{G_i} k_i . R3_i - gam_i k_i . R2_i
+//          + (row i - column i of P (QK^T) + E (KK^T) below the diagonal)
+//   dG_last += sum_i gam_i k_i . R2_i + e^{G_last} <S, dS>
+//   dg_t = sum_{i >= t} dG_i within the chunk
+// (dG sums to do . o - dv . v per token, but every term above carries the decay it
+// passes through, so that dg keeps its accuracy where the state is soon forgotten.)
 //
 // One 512-thread work-group per (chunk slot, q/k head) walks the group's value heads
 // and sums their dq and dk in registers (so the sum's order is fixed).  It holds the
 // chunk's do, u and dx (bf16 parts) and k, q in LDS; wave w owns channels 16 w .. + 15
 // of R1, R2, R3, dq and dk, so S and dS are read once and split once; the ten lower
-// 16x16 tiles of the token-by-token products are dealt to the eight waves.  All inputs
-// that gradients of g and beta depend on enter in three bf16 parts (fp32's accuracy);
-// P and E enter dq and dk, which are rounded to bf16, in two.
+// 16x16 tiles of P and of E are dealt to the eight waves.  What dg depends on enters in
+// three bf16 parts (fp32's accuracy); P and E enter dq and dk, which are rounded to
+// bf16, in two.
 //   The kernel is bound by its reads: 64 KB each of S and dS and 32 KB each of u and dx
 // per chunk and value head.
 #include "kda_gdr_device.h"
@@ -29,7 +32,7 @@ namespace {
 constexpr int GT = 512;
 constexpr int PS = 144;   // bytes per row of 64 bf16 (+16)
 struct GL {
-    static constexpr int K = 0, Q = 16384, DO = 32768, U = 49152, X = U + 3 * 16384;
+    static constexpr int K = 0, Q = 16384, DO = 32768, U = 49152, X = U + 3 * 16384;   // U, X in three parts
     static constexpr int PL = 64 * PS;                  // one part of P or E, over U
     static constexpr int OUT = U, OS = 272;             // dq, dk on the way out: rows of 128 bf16 (+16)
     static constexpr int END = X + 3 * 16384;
@@ -37,10 +40,10 @@ struct GL {
 };
 struct GShared {
     GSum G[64];
-    float eg[64], ga[64], be[64], vdot[64];
-    float z[8][64], t[8][64], b[8][64];   // row dots by wave (channel sixteenths)
-    float rowv[10][16], colv[10][16], rowb[10][16];   // row and column sums by tile
-    float sdot[8];
+    float eg[64], ga[64], be[64], xu[64];   // xu: dx . u
+    float z[8][64];        // the row dots of dG by wave (channel sixteenths)
+    float row[20][16], col[20][16];   // row and column sums by tile: P (QK^T), then E (KK^T)
+    float sd[8], ts[8];    // <S, dS> and sum gam k . R2 by wave
 };
 
 // The lane's 16 x 16 tile piece: tokens 16 m + 4 g + r of channel 16 w + jj.
@@ -88,207 +91,210 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p) {
         const int64_t gi = (row * p.T + tok) * p.Hv + hv;
         dma_tile(chunk_rsrc(p.dO.p + row * p.dO.sb + tok * p.dO.st + hv * p.dO.sh, p.dO.st, rows, DK), lds + GL::DO,
                  p.dO.st, w, 8, lane);
-        // u and dx in three parts, and dx . v
+        f32x4 s[8], ds[8];
+        float gate = 0.f, be = 0.f;
+        if (w == 7 && lane < rows) {
+            gate = p.g[gi + (int64_t)lane * p.Hv];
+            be = gdr_beta<true>(p, gi + (int64_t)lane * p.Hv);
+        }
         {
-            const __amdgpu_buffer_rsrc_t rv =
-                chunk_rsrc(p.v.p + row * p.v.sb + tok * p.v.st + hv * p.v.sh, p.v.st, rows, DK);
+            const int pc = tid & 15;
+            f32x4 u[4], x[4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int i = 32 * h + (tid >> 4), pc = tid & 15;
-                const float* us = p.u + unit * CH * DK + i * DK + 8 * pc;
-                const float* xs = p.dx + unit * CH * DK + i * DK + 8 * pc;
-                const f32x4 u0 = *reinterpret_cast<const f32x4*>(us), u1 = *reinterpret_cast<const f32x4*>(us + 4);
-                const f32x4 x0 = *reinterpret_cast<const f32x4*>(xs), x1 = *reinterpret_cast<const f32x4*>(xs + 4);
-                const i32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rv, (int)(i * p.v.st * 2) + 16 * pc, 0, 0);
-                const Split<3> us3 = split_acc<3>(u0, u1), xs3 = split_acc<3>(x0, x1);
-                const int at = tile_off(i, pc);
+                const int i = 32 * h + (tid >> 4);
+                const float* up = p.u + unit * CH * DK + i * DK + 8 * pc;
+                const float* xp = p.dx + unit * CH * DK + i * DK + 8 * pc;
+                u[2 * h] = *reinterpret_cast<const f32x4*>(up);
+                u[2 * h + 1] = *reinterpret_cast<const f32x4*>(up + 4);
+                x[2 * h] = *reinterpret_cast<const f32x4*>(xp);
+                x[2 * h + 1] = *reinterpret_cast<const f32x4*>(xp + 4);
+            }
+            asm volatile("" ::: "memory");   // S and dS are in flight while u and dx are split
+            const float* sp = p.S + unit * DK * DK + (16 * w + jj) * DK + 8 * g;
+            const float* dp = p.dS + unit * DK * DK + (16 * w + jj) * DK + 8 * g;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                s[n] = *reinterpret_cast<const f32x4*>(sp + 32 * (n >> 1) + 4 * (n & 1));
+                ds[n] = *reinterpret_cast<const f32x4*>(dp + 32 * (n >> 1) + 4 * (n & 1));
+            }
+            if (w == 7) {
+                const GSum G = gate_sum(gate);
+                const GSum last = {__shfl(G.hi, 63), __shfl(G.lo, 63)};
+                sh.G[lane] = G;
+                sh.eg[lane] = gate_exp(G);
+                sh.ga[lane] = gate_ratio(last, G);
+                sh.be[lane] = be;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int i = 32 * h + (tid >> 4), at = tile_off(i, pc);
+                const Split<3> u3 = split_acc<3>(u[2 * h], u[2 * h + 1]);
+                const Split<3> x3 = split_acc<3>(x[2 * h], x[2 * h + 1]);
 #pragma unroll
                 for (int n = 0; n < 3; ++n) {
-                    *reinterpret_cast<bf16x8*>(smem + GL::U + n * 16384 + at) = us3.s[n];
-                    *reinterpret_cast<bf16x8*>(smem + GL::X + n * 16384 + at) = xs3.s[n];
+                    *reinterpret_cast<bf16x8*>(smem + GL::U + n * 16384 + at) = u3.s[n];
+                    *reinterpret_cast<bf16x8*>(smem + GL::X + n * 16384 + at) = x3.s[n];
                 }
-                float d = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t vv = (uint32_t)v[e];
-                    const float xa = e < 2 ? x0[2 * e] : x1[2 * e - 4], xb = e < 2 ? x0[2 * e + 1] : x1[2 * e - 3];
-                    d = fmaf(xa, bf_lo(vv), d);
-                    d = fmaf(xb, bf_hi(vv), d);
-                }
-                d = sum16(d);
-                if (pc == 0) sh.vdot[i] = d;
+                const f32x4 a = x[2 * h] * u[2 * h] + x[2 * h + 1] * u[2 * h + 1];
+                const float xu = sum16((a[0] + a[1]) + (a[2] + a[3]));
+                if (pc == 0) sh.xu[i] = xu;
             }
         }
-        if (w == 0) {
-            const bool in = lane < rows;
-            const GSum G = gate_sum(in ? p.g[gi + (int64_t)lane * p.Hv] : 0.f, lane);
-            const GSum last = {__shfl(G.hi, 63), __shfl(G.lo, 63)};
-            sh.G[lane] = G;
-            sh.eg[lane] = gate_exp(G);
-            sh.ga[lane] = gate_ratio(last, G);
-            sh.be[lane] = in ? gdr_beta(p, gi + (int64_t)lane * p.Hv) : 0.f;
-        }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
+        asm volatile("s_waitcnt vmcnt(16)" ::: "memory");   // the DMA; S and dS, issued last, may still be on their way
+        lds_barrier();
 
-        // R1, R2, R3 for channels 16 w + jj
+        // R1, R3, then R2, for channels 16 w + jj
         {
-            Split<3> sb[4], db[4];
-            float sd = 0.f;
-            const float* ss = p.S + unit * DK * DK + (16 * w + jj) * DK + 8 * g;
-            const float* ds = p.dS + unit * DK * DK + (16 * w + jj) * DK + 8 * g;
+            Split<3> sb[4];
+            {
+                f32x4 d4 = z4;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                const f32x4 a0 = *reinterpret_cast<const f32x4*>(ss + 32 * kk);
-                const f32x4 a1 = *reinterpret_cast<const f32x4*>(ss + 32 * kk + 4);
-                const f32x4 b0 = *reinterpret_cast<const f32x4*>(ds + 32 * kk);
-                const f32x4 b1 = *reinterpret_cast<const f32x4*>(ds + 32 * kk + 4);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sd = fmaf(a0[e], b0[e], fmaf(a1[e], b1[e], sd));
-                sb[kk] = split_acc<3>(a0, a1);
-                db[kk] = split_acc<3>(b0, b1);
+                for (int n = 0; n < 8; ++n) d4 += s[n] * ds[n];
+                const float sd = sum64((d4[0] + d4[1]) + (d4[2] + d4[3]));
+                if (lane == 0) sh.sd[w] = sd;
             }
-            sd = sum16(sd);
-            sd += __shfl_xor(sd, 16);
-            sd += __shfl_xor(sd, 32);
-            if (lane == 0) sh.sdot[w] = sd;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) sb[kk] = split_acc<3>(s[2 * kk], s[2 * kk + 1]);
+            f32x4 z[4];   // the lane's part of the row dots
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                f32x4 r1 = z4, r2 = z4, r3 = z4;
+                f32x4 r1 = z4, r3 = z4;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                     const int at = tile_off(16 * m + jj, 4 * kk + g);
                     const bf16x8 fo[1] = {lds_bf8(smem + GL::DO + at)};
-                    bf16x8 fu[3], fx[3];
+                    bf16x8 fx[3];
 #pragma unroll
-                    for (int n = 0; n < 3; ++n) {
-                        fu[n] = lds_bf8(smem + GL::U + n * 16384 + at);
-                        fx[n] = lds_bf8(smem + GL::X + n * 16384 + at);
-                    }
+                    for (int n = 0; n < 3; ++n) fx[n] = lds_bf8(smem + GL::X + n * 16384 + at);
                     r1 = mfma_split<3>(fo, sb[kk], r1);
-                    r2 = mfma_split<3>(fu, db[kk], r2);
                     r3 = mfma_split<3>(fx, sb[kk], r3);
                 }
                 const f32x4 eg = *reinterpret_cast<const f32x4*>(sh.eg + 16 * m + 4 * g);
-                const f32x4 ga = *reinterpret_cast<const f32x4*>(sh.ga + 16 * m + 4 * g);
                 const f32x4 be = *reinterpret_cast<const f32x4*>(sh.be + 16 * m + 4 * g);
-                const f32x4 kv = widen(chan_frag(smem + GL::K, m, w, g, jj));
-                const f32x4 qv = widen(chan_frag(smem + GL::Q, m, w, g, jj));
                 r1 = (p.scale * eg) * r1;
-                r2 = ga * r2;
-                r3 = eg * r3;
+                r3 = (be * eg) * r3;
                 dq[m] += r1;
-                dk[m] += r2 - be * r3;
+                dk[m] -= r3;
+                z[m] = widen(chan_frag(smem + GL::Q, m, w, g, jj)) * r1 -
+                       widen(chan_frag(smem + GL::K, m, w, g, jj)) * r3;
+            }
+#pragma unroll
+            for (int n = 0; n < 8; ++n) asm volatile("" : "+v"(ds[n]));   // dS's parts are formed after S's are done with
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) sb[kk] = split_acc<3>(ds[2 * kk], ds[2 * kk + 1]);
+            f32x4 ts = z4;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                f32x4 r2 = z4;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const int at = tile_off(16 * m + jj, 4 * kk + g);
+                    bf16x8 fu[3];
+#pragma unroll
+                    for (int n = 0; n < 3; ++n) fu[n] = lds_bf8(smem + GL::U + n * 16384 + at);
+                    r2 = mfma_split<3>(fu, sb[kk], r2);
+                }
+                r2 *= *reinterpret_cast<const f32x4*>(sh.ga + 16 * m + 4 * g);
+                dk[m] += r2;
+                r2 *= widen(chan_frag(smem + GL::K, m, w, g, jj));
+                ts += r2;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float t = sum16(kv[e] * r2[e]), b = sum16(kv[e] * r3[e]), a = sum16(qv[e] * r1[e]);
-                    if (jj == 0) {
-                        const int i = 16 * m + 4 * g + e;
-                        sh.t[w][i] = t;
-                        sh.b[w][i] = b;
-                        sh.z[w][i] = a - be[e] * b - t;
-                    }
+                    const float x = sum16(z[m][e] - r2[e]);
+                    if (jj == 0) sh.z[w][16 * m + 4 * g + e] = x;
                 }
             }
+            const float t = sum64((ts[0] + ts[1]) + (ts[2] + ts[3]));
+            if (lane == 0) sh.ts[w] = t;
         }
-        // token-by-token tiles w and w + 8 of the ten lower ones
+        // lower tiles of P and E: wave w has tile w of both; tiles 8 and 9 of P go to
+        // waves 0 and 1, of E to waves 2 and 3
         f32x4 P[2], E[2];
         int ti[2], tj[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int id = w + 8 * x;
+            const int id = x == 0 ? w : 8 + (w & 1);
+            const bool hasP = x == 0 || w < 2, hasE = x == 0 || (w >> 1) == 1;
             ti[x] = id >= 6 ? 3 : id >= 3 ? 2 : id >= 1 ? 1 : 0;
             tj[x] = id - ti[x] * (ti[x] + 1) / 2;
             P[x] = E[x] = z4;
-            if (id >= 10) continue;
-            f32x4 a = z4, mm = z4, qk = z4, kk2 = z4;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                const int ai = tile_off(16 * ti[x] + jj, 4 * kk + g), aj = tile_off(16 * tj[x] + jj, 4 * kk + g);
-                Split<3> ub;
-                bf16x8 fx[3];
-#pragma unroll
-                for (int n = 0; n < 3; ++n) {
-                    ub.s[n] = lds_bf8(smem + GL::U + n * 16384 + aj);
-                    fx[n] = lds_bf8(smem + GL::X + n * 16384 + ai);
-                }
-                const bf16x8 fo[1] = {lds_bf8(smem + GL::DO + ai)};
-                a = mfma_split<3>(fo, ub, a);
-                mm = mfma_split<3>(fx, ub, mm);
-                const bf16x8 kb = lds_bf8(smem + GL::K + aj);
-                qk = mfma_bf(lds_bf8(smem + GL::Q + ai), kb, qk);
-                kk2 = mfma_bf(lds_bf8(smem + GL::K + ai), kb, kk2);
-            }
             const int j = 16 * tj[x] + jj;
+            // row and column sums of a tile's entries below the diagonal
+            auto tile_sums = [&](f32x4 v, int id, int base) {
+                float cs = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float y = j < 16 * ti[x] + 4 * g + e ? v[e] : 0.f, rs = sum16(y);
+                    cs += y;
+                    if (jj == 0) sh.row[base + id][4 * g + e] = rs;
+                }
+                cs += __shfl_xor(cs, 16);
+                cs += __shfl_xor(cs, 32);
+                if (g == 0) sh.col[base + id][jj] = cs;
+            };
             const GSum Gj = sh.G[j];
-            float cs = 0.f;
+            f32x4 gam;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = 16 * ti[x] + 4 * g + e;
-                const float gam = j <= i ? gate_ratio(sh.G[i], Gj) : 0.f;
-                const float pe = j <= i ? p.scale * (gam * a[e]) : 0.f;
-                const float ge = j < i ? -(gam * mm[e]) : 0.f;   // Gam times dM
-                const float ee = sh.be[i] * ge;
-                P[x][e] = pe;
-                E[x][e] = ee;
-                const float val = pe * qk[e] + ee * kk2[e];
-                cs += val;
-                const float rs = sum16(val), rb = sum16(ge * kk2[e]);
-                if (jj == 0) {
-                    sh.rowv[id][4 * g + e] = rs;
-                    sh.rowb[id][4 * g + e] = rb;
+                gam[e] = j <= i ? gate_ratio(sh.G[i], Gj) : 0.f;
+            }
+            if (hasP) {
+                f32x4 a = z4, qk = z4;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const int ai = tile_off(16 * ti[x] + jj, 4 * kk + g), aj = tile_off(16 * tj[x] + jj, 4 * kk + g);
+                    const Split<3> ub = {{lds_bf8(smem + GL::U + aj), lds_bf8(smem + GL::U + 16384 + aj),
+                                          lds_bf8(smem + GL::U + 32768 + aj)}};
+                    const bf16x8 fo[1] = {lds_bf8(smem + GL::DO + ai)};
+                    a = mfma_split<3>(fo, ub, a);
+                    qk = mfma_bf(lds_bf8(smem + GL::Q + ai), lds_bf8(smem + GL::K + aj), qk);
                 }
-            }
-            cs += __shfl_xor(cs, 16);
-            cs += __shfl_xor(cs, 32);
-            if (g == 0) sh.colv[id][jj] = cs;
-        }
-        __syncthreads();   // u's parts read; the sums complete
-        if (w == 7) {      // the wave with the fewest tiles
-            const int i = lane, I = i >> 4;
-            double dG = 0.0;
-            float db = sh.vdot[i], ts = 0.f, sd = 0.f;
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                dG += (double)sh.z[n][i];
-                db -= sh.b[n][i];
-                ts += sh.t[n][i];
-                sd += sh.sdot[n];
+                for (int e = 0; e < 4; ++e) P[x][e] = j <= 16 * ti[x] + 4 * g + e ? p.scale * (gam[e] * a[e]) : 0.f;
+                tile_sums(P[x] * qk, id, 0);
             }
-            for (int n = 0; n < 4; ++n) {
-                if (n <= I) {
-                    dG += (double)sh.rowv[I * (I + 1) / 2 + n][i & 15];
-                    db += sh.rowb[I * (I + 1) / 2 + n][i & 15];
+            if (hasE) {
+                f32x4 a = z4, kk2 = z4;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const int ai = tile_off(16 * ti[x] + jj, 4 * kk + g), aj = tile_off(16 * tj[x] + jj, 4 * kk + g);
+                    Split<3> ub;
+                    bf16x8 fx[3];
+#pragma unroll
+                    for (int n = 0; n < 3; ++n) {
+                        ub.s[n] = lds_bf8(smem + GL::U + n * 16384 + aj);
+                        fx[n] = lds_bf8(smem + GL::X + n * 16384 + ai);
+                    }
+                    a = mfma_split<3>(fx, ub, a);
+                    kk2 = mfma_bf(lds_bf8(smem + GL::K + ai), lds_bf8(smem + GL::K + aj), kk2);
                 }
-                if (n >= I) dG -= (double)sh.colv[n * (n + 1) / 2 + I][i & 15];
-            }
-            double tsum = (double)ts;
+                const f32x4 be = *reinterpret_cast<const f32x4*>(sh.be + 16 * ti[x] + 4 * g);
 #pragma unroll
-            for (int m = 1; m < 64; m <<= 1) tsum += __shfl_xor(tsum, m);
-            if (i == 63) dG += tsum + (double)(sh.eg[63] * sd);
-#pragma unroll
-            for (int m = 1; m < 64; m <<= 1) {   // suffix sums
-                const double y = __shfl_down(dG, m);
-                if (i + m < 64) dG += y;
-            }
-            if (i < rows) {
-                p.dg[gi + (int64_t)i * p.Hv] = (float)dG;
-                p.dbeta[gi + (int64_t)i * p.Hv] = db;
+                for (int e = 0; e < 4; ++e)
+                    E[x][e] = j < 16 * ti[x] + 4 * g + e ? -(be[e] * (gam[e] * a[e])) : 0.f;
+                tile_sums(E[x] * kk2, id, 10);
             }
         }
+        lds_barrier();   // u's parts read; the sums complete
         // P and E as row-major planes of two bf16 parts
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            if (w + 8 * x >= 10) continue;
+            const bool hasP = x == 0 || w < 2, hasE = x == 0 || (w >> 1) == 1;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int at = (16 * ti[x] + 4 * g + e) * PS + 2 * (16 * tj[x] + jj);
                 const uint32_t h = pack_bf2(P[x][e], E[x][e]);
                 const uint32_t l = pack_bf2(P[x][e] - bf_lo(h), E[x][e] - bf_hi(h));
-                *reinterpret_cast<uint16_t*>(smem + GL::U + at) = (uint16_t)h;
-                *reinterpret_cast<uint16_t*>(smem + GL::U + GL::PL + at) = (uint16_t)l;
-                *reinterpret_cast<uint16_t*>(smem + GL::U + 2 * GL::PL + at) = (uint16_t)(h >> 16);
-                *reinterpret_cast<uint16_t*>(smem + GL::U + 3 * GL::PL + at) = (uint16_t)(l >> 16);
+                if (hasP) {
+                    *reinterpret_cast<uint16_t*>(smem + GL::U + at) = (uint16_t)h;
+                    *reinterpret_cast<uint16_t*>(smem + GL::U + GL::PL + at) = (uint16_t)l;
+                }
+                if (hasE) {
+                    *reinterpret_cast<uint16_t*>(smem + GL::U + 2 * GL::PL + at) = (uint16_t)(h >> 16);
+                    *reinterpret_cast<uint16_t*>(smem + GL::U + 3 * GL::PL + at) = (uint16_t)(l >> 16);
+                }
             }
         }
         for (int e = tid; e < 2048; e += GT) {   // the tiles above the diagonal that operands cover
@@ -296,7 +302,30 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p) {
             *reinterpret_cast<uint16_t*>(smem + GL::U + (e >> 9) * GL::PL + (32 * t + (x >> 4)) * PS +
                                          2 * (32 * t + 16 + (x & 15))) = 0;
         }
-        __syncthreads();
+        if (w == 7) {
+            const int i = lane, I = i >> 4;
+            double dG = 0.0, last = 0.0;
+            float sd = 0.f;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                dG += (double)sh.z[n][i];
+                last += (double)sh.ts[n];
+                sd += sh.sd[n];
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const int ra = I * (I + 1) / 2 + n, ca = n * (n + 1) / 2 + I;
+                if (n <= I) dG += (double)sh.row[ra][i & 15] + (double)sh.row[10 + ra][i & 15];
+                if (n >= I) dG -= (double)sh.col[ca][i & 15] + (double)sh.col[10 + ca][i & 15];
+            }
+            last += (double)(sh.eg[63] * sd);
+            const double sum = prefix64(dG), rest = lane_f64(sum, 63) - sum + dG;
+            if (i < rows) {
+                p.dg[gi + (int64_t)i * p.Hv] = (float)(rest + last);
+                p.dbeta[gi + (int64_t)i * p.Hv] = sh.xu[i] / sh.be[i];
+            }
+        }
+        lds_barrier();
         {
             bf16x8 kb[2], qb[2];
 #pragma unroll
@@ -324,7 +353,7 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p) {
                 }
             }
         }
-        __syncthreads();   // the planes' reads before the next value head's parts
+        lds_barrier();   // the planes' reads before the next value head's parts
     }
     // dq and dk, rounded once
 #pragma unroll

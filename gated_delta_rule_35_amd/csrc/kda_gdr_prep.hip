@@ -82,8 +82,8 @@ __global__ void __launch_bounds__(256) kda_gdr_prep_kernel(const GdrParams p) {
         const int64_t gi = (row * p.T + tok) * p.Hv + hv;
         if (w == 0) {
             const bool in = lane < rows;   // tokens past the end change nothing: g = 0, beta = 0
-            sG[lane] = gate_sum(in ? p.g[gi + (int64_t)lane * p.Hv] : 0.f, lane);
-            sBeta[lane] = in ? gdr_beta(p, gi + (int64_t)lane * p.Hv) : 0.f;
+            sG[lane] = gate_sum(in ? p.g[gi + (int64_t)lane * p.Hv] : 0.f);
+            sBeta[lane] = in ? gdr_beta<NA == GDR_NA_BWD>(p, gi + (int64_t)lane * p.Hv) : 0.f;
         }
         __syncthreads();
         char* rec = p.rec + (slot * p.Hv + hv) * gdr_rec_bytes(NA);

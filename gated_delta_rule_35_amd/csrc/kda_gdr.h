@@ -49,9 +49,10 @@ constexpr int GDR_NA_FWD = 2, GDR_NA_BWD = 3;
 
 // Fills the records with na parts of A.
 hipError_t launch_gdr_prep(const GdrParams& p, int na, hipStream_t stream);
-hipError_t launch_gdr_grads(const GdrParams& p, hipStream_t stream);
+hipError_t launch_gdr_grads(const GdrParams& p, int cus, hipStream_t stream);
 hipError_t launch_gdr_fwd(const GdrParams& p, hipStream_t stream);
-hipError_t launch_gdr_bwd(const GdrParams& p, hipStream_t stream);
+// cus: compute units of the current device.
+hipError_t launch_gdr_bwd(const GdrParams& p, int cus, hipStream_t stream);
 
 struct GdrDecodeParams {
     Rows q, k, v;          // [N, H, 128]: sb is the stride of N, st is unused

@@ -254,7 +254,7 @@ kda_status_t kda_gdr_bwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda
         p.u = reinterpret_cast<float*>(base + L.u);
         p.dx = reinterpret_cast<float*>(base + L.dx);
     }
-    hipError_t e = kda::launch_gdr_bwd(p, hs);
+    hipError_t e = kda::launch_gdr_bwd(p, std::max(device_cus(), 1), hs);
     if (!workspace && ws && hipFreeAsync(ws, hs) != hipSuccess && e == hipSuccess) e = hipErrorUnknown;
     return finish(e, hs);
 }

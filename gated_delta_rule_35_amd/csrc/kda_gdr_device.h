@@ -125,6 +125,13 @@ __device__ __forceinline__ void dma_tile(__amdgpu_buffer_rsrc_t r, uint32_t lds,
     }
 }
 
+// A copy of x that the compiler cannot see through: per-lane addresses derived from it
+// are formed where they are used instead of being kept across a loop.
+__device__ __forceinline__ int opaque(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // ---- chunks ----
 // First token (in its row), length and row of sequence n, clamped to the row.
 __device__ __forceinline__ void gdr_seq(const GdrParams& p, int n, int64_t& bos, int64_t& len, int64_t& row,

@@ -15,8 +15,10 @@
 // (dG sums to do . o - dv . v per token, but every term above carries the decay it
 // passes through, so that dg keeps its accuracy where the state is soon forgotten.)
 //
-// One 512-thread work-group per (chunk slot, q/k head) walks the group's value heads
-// and sums their dq and dk in registers (so the sum's order is fixed).  It holds the
+// One 512-thread work-group per compute unit takes items (chunk slot, q/k head), walks
+// the group's value heads and sums their dq and dk in registers (so the sum's order is
+// fixed); the next unit's S, dS, u and dx are loaded into registers, its do into LDS,
+// while the last products of this one run.  It holds the
 // chunk's do, u and dx (bf16 parts) and k, q in LDS; wave w owns channels 16 w .. + 15
 // of R1, R2, R3, dq and dk, so S and dS are read once and split once; the ten lower
 // 16x16 tiles of P and of E are dealt to the eight waves.  What dg depends on enters in
@@ -34,9 +36,9 @@ constexpr int PS = 144;   // bytes per row of 64 bf16 (+16)
 struct GL {
     static constexpr int K = 0, Q = 16384, DO = 32768, U = 49152, X = U + 3 * 16384;   // U, X in three parts
     static constexpr int PL = 64 * PS;                  // one part of P or E, over U
-    static constexpr int OUT = U, OS = 272;             // dq, dk on the way out: rows of 128 bf16 (+16)
+    static constexpr int OUT = X, OS = 272;             // dq, dk on the way out, over X: rows of 128 bf16 (+16)
     static constexpr int END = X + 3 * 16384;
-    static_assert(4 * PL <= 3 * 16384 && 2 * 64 * OS <= 6 * 16384, "overlays");
+    static_assert(4 * PL <= 3 * 16384 && 2 * 64 * OS <= 3 * 16384, "overlays");
 };
 struct GShared {
     GSum G[64];
@@ -65,87 +67,103 @@ __device__ __forceinline__ bf16x8 plane_col(const char* pl, int m, int kk, int g
 }
 }  // namespace
 
-__global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p) {
+__global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, const int items) {
     __shared__ __attribute__((aligned(1024))) char smem[GL::END];
     __shared__ GShared sh;
-    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, jj = lane & 15;
+    const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t slot = blockIdx.x / p.Hq;
-    const int hq = blockIdx.x % p.Hq, R = p.Hv / p.Hq;
-    int64_t tok, row;
-    const int rows = gdr_chunk(p, slot, tok, row);
-    if (rows == 0) return;
-    const uint32_t lds = lds_addr(smem);
-    dma_tile(chunk_rsrc(p.k.p + row * p.k.sb + tok * p.k.st + hq * p.k.sh, p.k.st, rows, DK), lds + GL::K, p.k.st, w, 8,
-             lane);
-    dma_tile(chunk_rsrc(p.q.p + row * p.q.sb + tok * p.q.st + hq * p.q.sh, p.q.st, rows, DK), lds + GL::Q, p.q.st, w, 8,
-             lane);
+    const int R = p.Hv / p.Hq;
+    const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(smem));
     const f32x4 z4 = {0.f, 0.f, 0.f, 0.f};
+
+    // The unit at hand, one value head r of an item (chunk slot, q/k head); item >= items: none.
+    int item = blockIdx.x, r = 0, rows = 0, hq = 0;
+    int64_t slot = 0, tok = 0, row = 0;
+    auto find = [&]() {   // the first item from `item` on whose slot holds a chunk
+        for (; item < items; item += gridDim.x) {
+            slot = item / p.Hq;
+            hq = item % p.Hq;
+            rows = gdr_chunk(p, slot, tok, row);
+            if (rows) break;
+        }
+    };
+    f32x4 u[4], x[4], s[8], ds[8];
+    float gate = 0.f, beta = 0.f;
+    auto fetch = [&]() {   // the unit's fp32 inputs into registers
+        const int t = opaque(tid), ln = t & 63, g = ln >> 4, jj = ln & 15;
+        const int64_t unit = slot * p.Hv + hq * R + r;
+        if (w == 7) {
+            const int64_t gi = (row * p.T + tok + lane) * p.Hv + hq * R + r;
+            gate = lane < rows ? p.g[gi] : 0.f;
+            beta = lane < rows ? gdr_beta<true>(p, gi) : 0.f;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t at = unit * CH * DK + (32 * h + (t >> 4)) * DK + 8 * (t & 15);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                u[2 * h + n] = *reinterpret_cast<const f32x4*>(p.u + at + 4 * n);
+                x[2 * h + n] = *reinterpret_cast<const f32x4*>(p.dx + at + 4 * n);
+            }
+        }
+        const int64_t at = unit * DK * DK + (16 * w + jj) * DK + 8 * g;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            s[n] = *reinterpret_cast<const f32x4*>(p.S + at + 32 * (n >> 1) + 4 * (n & 1));
+            ds[n] = *reinterpret_cast<const f32x4*>(p.dS + at + 32 * (n >> 1) + 4 * (n & 1));
+        }
+    };
+    auto dma_do = [&]() {
+        dma_tile(chunk_rsrc(p.dO.p + row * p.dO.sb + tok * p.dO.st + (hq * R + r) * p.dO.sh, p.dO.st, rows, DK),
+                 lds + GL::DO, p.dO.st, w, 8, opaque(lane));
+    };
+    auto dma_kq = [&]() {
+        const int lane = opaque(tid & 63);
+        dma_tile(chunk_rsrc(p.k.p + row * p.k.sb + tok * p.k.st + hq * p.k.sh, p.k.st, rows, DK), lds + GL::K, p.k.st, w,
+                 8, lane);
+        dma_tile(chunk_rsrc(p.q.p + row * p.q.sb + tok * p.q.st + hq * p.q.sh, p.q.st, rows, DK), lds + GL::Q, p.q.st, w,
+                 8, lane);
+    };
+    find();
+    if (item >= items) return;
+    fetch();
+    dma_do();
+    dma_kq();
     f32x4 dq[4], dk[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) dq[m] = dk[m] = z4;
 
-    for (int r = 0; r < R; ++r) {
-        const int hv = hq * R + r;
-        const int64_t unit = slot * p.Hv + hv;
-        const int64_t gi = (row * p.T + tok) * p.Hv + hv;
-        dma_tile(chunk_rsrc(p.dO.p + row * p.dO.sb + tok * p.dO.st + hv * p.dO.sh, p.dO.st, rows, DK), lds + GL::DO,
-                 p.dO.st, w, 8, lane);
-        f32x4 s[8], ds[8];
-        float gate = 0.f, be = 0.f;
-        if (w == 7 && lane < rows) {
-            gate = p.g[gi + (int64_t)lane * p.Hv];
-            be = gdr_beta<true>(p, gi + (int64_t)lane * p.Hv);
+    while (item < items) {
+        // u and dx in three parts, and dx . u
+        const int t = opaque(tid);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int pc = t & 15, i = 32 * h + (t >> 4), at = tile_off(i, pc);
+            const Split<3> u3 = split_acc<3>(u[2 * h], u[2 * h + 1]);
+            const Split<3> x3 = split_acc<3>(x[2 * h], x[2 * h + 1]);
+#pragma unroll
+            for (int n = 0; n < 3; ++n) {
+                *reinterpret_cast<bf16x8*>(smem + GL::U + n * 16384 + at) = u3.s[n];
+                *reinterpret_cast<bf16x8*>(smem + GL::X + n * 16384 + at) = x3.s[n];
+            }
+            const f32x4 a = x[2 * h] * u[2 * h] + x[2 * h + 1] * u[2 * h + 1];
+            const float xu = sum16((a[0] + a[1]) + (a[2] + a[3]));
+            if (pc == 0) sh.xu[i] = xu;
         }
-        {
-            const int pc = tid & 15;
-            f32x4 u[4], x[4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int i = 32 * h + (tid >> 4);
-                const float* up = p.u + unit * CH * DK + i * DK + 8 * pc;
-                const float* xp = p.dx + unit * CH * DK + i * DK + 8 * pc;
-                u[2 * h] = *reinterpret_cast<const f32x4*>(up);
-                u[2 * h + 1] = *reinterpret_cast<const f32x4*>(up + 4);
-                x[2 * h] = *reinterpret_cast<const f32x4*>(xp);
-                x[2 * h + 1] = *reinterpret_cast<const f32x4*>(xp + 4);
-            }
-            asm volatile("" ::: "memory");   // S and dS are in flight while u and dx are split
-            const float* sp = p.S + unit * DK * DK + (16 * w + jj) * DK + 8 * g;
-            const float* dp = p.dS + unit * DK * DK + (16 * w + jj) * DK + 8 * g;
-#pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                s[n] = *reinterpret_cast<const f32x4*>(sp + 32 * (n >> 1) + 4 * (n & 1));
-                ds[n] = *reinterpret_cast<const f32x4*>(dp + 32 * (n >> 1) + 4 * (n & 1));
-            }
-            if (w == 7) {
-                const GSum G = gate_sum(gate);
-                const GSum last = {__shfl(G.hi, 63), __shfl(G.lo, 63)};
-                sh.G[lane] = G;
-                sh.eg[lane] = gate_exp(G);
-                sh.ga[lane] = gate_ratio(last, G);
-                sh.be[lane] = be;
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int i = 32 * h + (tid >> 4), at = tile_off(i, pc);
-                const Split<3> u3 = split_acc<3>(u[2 * h], u[2 * h + 1]);
-                const Split<3> x3 = split_acc<3>(x[2 * h], x[2 * h + 1]);
-#pragma unroll
-                for (int n = 0; n < 3; ++n) {
-                    *reinterpret_cast<bf16x8*>(smem + GL::U + n * 16384 + at) = u3.s[n];
-                    *reinterpret_cast<bf16x8*>(smem + GL::X + n * 16384 + at) = x3.s[n];
-                }
-                const f32x4 a = x[2 * h] * u[2 * h] + x[2 * h + 1] * u[2 * h + 1];
-                const float xu = sum16((a[0] + a[1]) + (a[2] + a[3]));
-                if (pc == 0) sh.xu[i] = xu;
-            }
+        if (w == 7) {
+            const GSum G = gate_sum(gate);
+            const GSum last = {__shfl(G.hi, 63), __shfl(G.lo, 63)};
+            sh.G[lane] = G;
+            sh.eg[lane] = gate_exp(G);
+            sh.ga[lane] = gate_ratio(last, G);
+            sh.be[lane] = beta;
         }
-        asm volatile("s_waitcnt vmcnt(16)" ::: "memory");   // the DMA; S and dS, issued last, may still be on their way
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's pieces of do, k and q
         lds_barrier();
 
         // R1, R3, then R2, for channels 16 w + jj
         {
+            const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
             Split<3> sb[4];
             {
                 f32x4 d4 = z4;
@@ -186,6 +204,7 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p) {
             f32x4 ts = z4;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
+                const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
                 f32x4 r2 = z4;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
@@ -214,6 +233,7 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p) {
         int ti[2], tj[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
+            const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
             const int id = x == 0 ? w : 8 + (w & 1);
             const bool hasP = x == 0 || w < 2, hasE = x == 0 || (w >> 1) == 1;
             ti[x] = id >= 6 ? 3 : id >= 3 ? 2 : id >= 1 ? 1 : 0;
@@ -282,6 +302,7 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const bool hasP = x == 0 || w < 2, hasE = x == 0 || (w >> 1) == 1;
+            const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int at = (16 * ti[x] + 4 * g + e) * PS + 2 * (16 * tj[x] + jj);
@@ -302,8 +323,9 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p) {
             *reinterpret_cast<uint16_t*>(smem + GL::U + (e >> 9) * GL::PL + (32 * t + (x >> 4)) * PS +
                                          2 * (32 * t + 16 + (x & 15))) = 0;
         }
-        if (w == 7) {
+        if (w == 7) {   // dg and dbeta
             const int i = lane, I = i >> 4;
+            const int64_t gi = (row * p.T + tok + i) * p.Hv + hq * R + r;
             double dG = 0.0, last = 0.0;
             float sd = 0.f;
 #pragma unroll
@@ -321,12 +343,28 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p) {
             last += (double)(sh.eg[63] * sd);
             const double sum = prefix64(dG), rest = lane_f64(sum, 63) - sum + dG;
             if (i < rows) {
-                p.dg[gi + (int64_t)i * p.Hv] = (float)(rest + last);
-                p.dbeta[gi + (int64_t)i * p.Hv] = sh.xu[i] / sh.be[i];
+                p.dg[gi] = (float)(rest + last);
+                p.dbeta[gi] = sh.xu[i] / sh.be[i];
             }
+        }
+        // the next unit's inputs, in flight from here on
+        const int rows0 = rows, hq0 = hq;
+        const int64_t tok0 = tok, row0 = row;
+        const bool done = r == R - 1;   // the item's last value head
+        if (done) {
+            r = 0;
+            item += gridDim.x;
+            find();
+        } else {
+            ++r;
+        }
+        if (item < items) {
+            fetch();
+            dma_do();
         }
         lds_barrier();
         {
+            const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
             bf16x8 kb[2], qb[2];
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
@@ -353,35 +391,43 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p) {
                 }
             }
         }
-        lds_barrier();   // the planes' reads before the next value head's parts
-    }
-    // dq and dk, rounded once
+        if (done) {   // dq and dk, rounded once
+            const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
+            for (int m = 0; m < 4; ++m) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t h = pack_bf2(dq[m][e], dk[m][e]);
-            const int at = (16 * m + 4 * g + e) * GL::OS + 2 * (16 * w + jj);
-            *reinterpret_cast<uint16_t*>(smem + GL::OUT + at) = (uint16_t)h;
-            *reinterpret_cast<uint16_t*>(smem + GL::OUT + 64 * GL::OS + at) = (uint16_t)(h >> 16);
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t h = pack_bf2(dq[m][e], dk[m][e]);
+                    const int at = (16 * m + 4 * g + e) * GL::OS + 2 * (16 * w + jj);
+                    *reinterpret_cast<uint16_t*>(smem + GL::OUT + at) = (uint16_t)h;
+                    *reinterpret_cast<uint16_t*>(smem + GL::OUT + 64 * GL::OS + at) = (uint16_t)(h >> 16);
+                }
+                dq[m] = dk[m] = z4;
+            }
         }
-    }
-    __syncthreads();
+        lds_barrier();   // k, q and the planes are read, dq and dk complete
+        if (done) {
+            if (item < items) dma_kq();
+            const int t = opaque(tid);
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-        const int i = 32 * (h & 1) + (tid >> 4), pc = tid & 15;
-        if (i < rows) {
-            uint16_t* dst = (h < 2 ? p.dq : p.dk) + ((row * p.T + tok + i) * p.Hq + hq) * DK + 8 * pc;
-            *reinterpret_cast<u32x4*>(dst) =
-                *reinterpret_cast<const u32x4*>(smem + GL::OUT + (h < 2 ? 0 : 64 * GL::OS) + i * GL::OS + 16 * pc);
+            for (int h = 0; h < 4; ++h) {
+                const int i = 32 * (h & 1) + (t >> 4), pc = t & 15;
+                if (i < rows0) {
+                    uint16_t* dst = (h < 2 ? p.dq : p.dk) + ((row0 * p.T + tok0 + i) * p.Hq + hq0) * DK + 8 * pc;
+                    *reinterpret_cast<u32x4*>(dst) = *reinterpret_cast<const u32x4*>(
+                        smem + GL::OUT + (h < 2 ? 0 : 64 * GL::OS) + i * GL::OS + 16 * pc);
+                }
+            }
+            lds_barrier();   // read before the next unit's parts are written there
         }
     }
 }
 
-hipError_t launch_gdr_grads(const GdrParams& p, hipStream_t stream) {
-    const int64_t blocks = p.nslots * p.Hq;
-    if (blocks == 0) return hipSuccess;
-    hipLaunchKernelGGL(kda_gdr_grads_kernel, dim3((unsigned)blocks), dim3(GT), 0, stream, p);
+hipError_t launch_gdr_grads(const GdrParams& p, int cus, hipStream_t stream) {
+    const int64_t items = p.nslots * p.Hq;
+    if (items == 0) return hipSuccess;
+    const int64_t blocks = items < cus ? items : cus;
+    hipLaunchKernelGGL(kda_gdr_grads_kernel, dim3((unsigned)blocks), dim3(GT), 0, stream, p, (int)items);
     return hipGetLastError();
 }
 

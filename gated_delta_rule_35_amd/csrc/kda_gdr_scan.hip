@@ -440,7 +440,7 @@ hipError_t launch_gdr_fwd(const GdrParams& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t launch_gdr_bwd(const GdrParams& p, hipStream_t stream) {
+hipError_t launch_gdr_bwd(const GdrParams& p, int cus, hipStream_t stream) {
     const unsigned blocks = (unsigned)((int64_t)p.N * p.Hv * 2);
     hipError_t e = launch_gdr_prep(p, GDR_NA_BWD, stream);
     if (e != hipSuccess) return e;
@@ -450,7 +450,7 @@ hipError_t launch_gdr_bwd(const GdrParams& p, hipStream_t stream) {
     }
     hipLaunchKernelGGL(kda_gdr_rscan_kernel, dim3(blocks), dim3(SCAN_THREADS), 0, stream, p);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    return launch_gdr_grads(p, stream);
+    return launch_gdr_grads(p, cus, stream);
 }
 
 }  // namespace kda

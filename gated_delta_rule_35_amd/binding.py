@@ -2,14 +2,14 @@
 
 Names follow the C ABI in include/kda.h: kda_fwd, kda_fwd_ws, kda_fwd_noalloc,
 kda_fwd_intra, kda_fwd_scan, kda_fwd_trace, kda_fwd_cp, kda_decode, kda_bwd,
-kda_gdr_fwd, kda_gdr_bwd, kda_gdr_decode, kda_qk_norm, kda_qk_norm_bwd and their
-size queries, kda_status_string, kda_dv_slices.  Tensors are passed as
+kda_gdr_fwd, kda_gdr_bwd, kda_gdr_decode, kda_qk_norm, kda_qk_norm_bwd (called
+through the extension _kda_py) and their size queries, kda_status_string,
+kda_dv_slices.  Tensors are passed as
 kda_tensor_t descriptors built from torch tensors (data pointer, dtype, shape,
 strides); the stream is torch's current HIP stream unless one is given.  Where
 an entry point takes a workspace, it is a uint8 device tensor the caller passes
 or one taken here from torch's caching allocator.
 """
-import array
 import ctypes
 import os
 
@@ -33,9 +33,6 @@ EXPORTED = ["kda_fwd", "kda_fwd_fused", "kda_fwd_ws", "kda_fwd_qg", "kda_fwd_noa
 class KdaTensor(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int), ("ndim", ctypes.c_int32),
                 ("shape", ctypes.c_int64 * 4), ("stride", ctypes.c_int64 * 4)]
-
-
-_DESC_BYTES = ctypes.sizeof(KdaTensor)
 
 
 class KdaTrace(ctypes.Structure):
@@ -451,60 +448,40 @@ def kda_bwd(q, k, v, g, beta, scale, d_out, initial_state=None, d_final_state=No
 
 # ---- gated delta rule with one decay per head, per-head q/k norm ----
 # These entry points are called for every layer and token while serving, where the
-# host's share of a call counts: all descriptors of a call lie in one array.
-_PAD = {n: (0,) * (4 - n) for n in range(5)}
+# host's share of a call counts: descriptors are made by the extension _kda_py (csrc/kda_py.c).
+_ENTRIES = ("kda_gdr_fwd", "kda_gdr_bwd", "kda_gdr_decode", "kda_qk_norm", "kda_qk_norm_bwd")
+_GDR_FWD, _GDR_BWD, _GDR_DECODE, _QK_NORM, _QK_NORM_BWD = range(5)
+_call_entry = None
 
 
-def _launch(entry, groups, stream, workspace=()):
-    """Calls `entry` with `groups`, alternating tuples of tensors (None: NULL) and of
-    scalars, then a workspace's address and size, then the stream.  The tensors must be on
-    one GPU, which is made current for the call."""
-    vals, dev = [], None
-    for t in [t for g in groups[::2] for t in g if t is not None]:
-        d = t.get_device()
-        if d != dev:
-            if d < 0:
-                raise ValueError(f"{entry} needs every tensor on the GPU")
-            if dev is not None:
-                raise ValueError(f"{entry} needs every tensor on one GPU (got {dev} and {d})")
-            dev = d
-        n = t.dim()
-        if n == 4:
-            vals += (t.data_ptr(), _DTYPES.get(t.dtype, 99) | 4 << 32, *t.shape, *t.stride())
-        elif n < 4:
-            pad = _PAD[n]
-            vals += (t.data_ptr(), _DTYPES.get(t.dtype, 99) | n << 32, *t.shape, *pad, *t.stride(), *pad)
-        else:
-            raise ValueError("kda tensors have at most 4 dimensions")
-    if dev is None:
-        raise ValueError(f"{entry} needs its tensors on the GPU")
-    descs = array.array("q", vals)   # kda_tensor_t is ten 64-bit words (dtype and rank share one)
-    at = descs.buffer_info()[0]
-    args = []
-    for i, g in enumerate(groups):
-        if i & 1:
-            args += g
-            continue
-        for t in g:
-            if t is None:
-                args.append(None)
-            else:
-                args.append(at)
-                at += _DESC_BYTES
-    for ws in workspace:
-        args += (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+def _load_caller():
+    """The extension's call(), bound to the loaded library."""
+    global _call_entry
     lib = load_library()
+    from . import _kda_py
+    _kda_py.bind(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _ENTRIES),
+                 (torch.bfloat16, torch.float16, torch.float32, torch.int32))
+    _call_entry = _kda_py.call
+    return _call_entry
+
+
+def _launch(entry, dev, scalars, tensors, stream, workspace=None):
+    """Calls entry point number `entry` with `tensors` (None: NULL), all of which must lie
+    on GPU `dev`, which is made current for the call."""
+    call = _call_entry or _load_caller()
+    if dev < 0:
+        raise ValueError(f"{_ENTRIES[entry]} needs every tensor on the GPU")
     if stream is None:
         s = torch._C._cuda_getCurrentRawStream(dev)
     else:
         s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if dev == torch.cuda.current_device():
-        status = getattr(lib, entry)(*args, s)
+    if dev == torch._C._cuda_getDevice():
+        status = call(entry, dev, s, workspace, scalars, tensors)
     else:
         with torch.cuda.device(dev):
-            status = getattr(lib, entry)(*args, s)
+            status = call(entry, dev, s, workspace, scalars, tensors)
     if status:
-        _check(lib, status)
+        _check(_lib, status)
 
 
 def _new(like, dtype, shape=None):
@@ -547,11 +524,11 @@ def kda_gdr_fwd(q, k, v, g, beta, scale, cu_seqlens=None, initial_state=None, ou
         out = _new(v, torch.bfloat16)
     if final_state is True:
         final_state = _new(v, torch.float32, (_sequences(q, cu_seqlens), v.shape[-2], 128, 128))
-    if workspace is None and q.dim() == 4 and v.dim() == 4:   # the C library rejects other ranks
+    if workspace is None and q.dim() == 4 and v.dim() == 4 and v.is_cuda:   # the C library rejects other ranks
         workspace = _scratch(kda_gdr_fwd_workspace_size(q.shape[0] * q.shape[1], _sequences(q, cu_seqlens), v.shape[2]),
                              v, stream)
-    _launch("kda_gdr_fwd", ((q, k, v, g, beta), (scale,), (cu_seqlens, initial_state, out, final_state)), stream,
-            (workspace,))
+    _launch(_GDR_FWD, v.get_device(), (scale,), (q, k, v, g, beta, cu_seqlens, initial_state, out, final_state), stream,
+            workspace)
     return out, final_state
 
 
@@ -575,9 +552,9 @@ def kda_gdr_bwd(q, k, v, g, beta, scale, d_out, initial_state=None, d_final_stat
     if workspace is None and q.dim() == 4 and v.dim() == 4:
         workspace = _scratch(kda_gdr_bwd_workspace_size(q.shape[0] * q.shape[1], _sequences(q, cu_seqlens), v.shape[2]),
                              v, stream)
-    _launch("kda_gdr_bwd", ((q, k, v, g, beta), (scale,),
-                            (cu_seqlens, initial_state, d_out, d_final_state, res["dq"], res["dk"], res["dv"],
-                             res["dg"], res["dbeta"], res["dh0"])), stream, (workspace,))
+    _launch(_GDR_BWD, v.get_device(), (scale,),
+            (q, k, v, g, beta, cu_seqlens, initial_state, d_out, d_final_state, res["dq"], res["dk"], res["dv"],
+             res["dg"], res["dbeta"], res["dh0"]), stream, workspace)
     return res
 
 
@@ -593,7 +570,7 @@ def kda_gdr_decode(q, k, v, g, beta, scale, state, state_indices=None, out=None,
         if state is None and state_indices is not None:
             raise ValueError("kda_gdr_decode needs a pool where state_indices name its slots")
         new_state = state if state is not None else _new(v, torch.float32, (v.shape[0], v.shape[1], 128, 128))
-    _launch("kda_gdr_decode", ((q, k, v, g, beta), (scale,), (state, new_state, state_indices, out)), stream)
+    _launch(_GDR_DECODE, v.get_device(), (scale,), (q, k, v, g, beta, state, new_state, state_indices, out), stream)
     return out, new_state
 
 
@@ -609,8 +586,8 @@ def kda_qk_norm(q, k, q_weight=None, k_weight=None, mode="l2", eps=1e-6, cos=Non
     if mode not in _NORM_MODES:
         raise ValueError(f"kda_qk_norm: mode {mode!r} is neither 'l2' nor 'rms'")
     qo, ko = out if out is not None else (_new(q, torch.bfloat16), _new(k, torch.bfloat16))
-    _launch("kda_qk_norm", ((q, k, q_weight, k_weight), (_NORM_MODES[mode], eps), (cos, sin, positions),
-                            (int(bool(interleaved)),), (qo, ko)), stream)
+    _launch(_QK_NORM, q.get_device(), (_NORM_MODES[mode], eps, bool(interleaved)),
+            (q, k, q_weight, k_weight, cos, sin, positions, qo, ko), stream)
     return qo, ko
 
 
@@ -632,7 +609,7 @@ def kda_qk_norm_bwd(q, k, d_q_out, d_k_out, q_weight=None, k_weight=None, mode="
             res[name] = _new(w, torch.float32)
     if workspace is None and (q_weight is not None or k_weight is not None):
         workspace = _scratch(int(load_library().kda_qk_norm_bwd_workspace_size()), q, stream)
-    _launch("kda_qk_norm_bwd", ((q, k, d_q_out, d_k_out, q_weight, k_weight), (_NORM_MODES[mode], eps),
-                                (cos, sin, positions), (int(bool(interleaved)),),
-                                (res["dq"], res["dk"], res["dq_weight"], res["dk_weight"])), stream, (workspace,))
+    _launch(_QK_NORM_BWD, q.get_device(), (_NORM_MODES[mode], eps, bool(interleaved)),
+            (q, k, d_q_out, d_k_out, q_weight, k_weight, cos, sin, positions, res["dq"], res["dk"], res["dq_weight"],
+             res["dk_weight"]), stream, workspace)
     return res

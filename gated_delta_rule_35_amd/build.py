@@ -1,4 +1,5 @@
-"""Builds libkda.so, the HIP library behind the C ABI in include/kda.h, for gfx950.
+"""Builds libkda.so, the HIP library behind the C ABI in include/kda.h, for gfx950, and
+_kda_py.so, the small Python extension that calls part of it.
 
 hipcc compiles the kernels and the C-ABI front end into one shared object next to
 this file.  -packed-fp32-ops is turned off for the device code: the compiler then
@@ -10,6 +11,7 @@ read accumulation registers, so the other form costs a register move per element
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,6 +21,19 @@ SOURCES = [os.path.join(HERE, "csrc", f)
               "kda_gdr_prep.hip", "kda_gdr_scan.hip", "kda_gdr_grads.hip", "kda_gdr_decode.hip", "kda_qk_norm.hip",
               "kda_api.cpp", "kda_gdr_api.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+
+
+CALLER = os.path.join(HERE, "_kda_py.so")   # the Python extension that makes the descriptors
+
+
+def build_caller(verbose: bool = False) -> str:
+    cmd = ["gcc", "-O2", "-std=c11", "-fPIC", "-shared", "-Wall", "-I", sysconfig.get_paths()["include"],
+           "-o", CALLER + ".tmp", os.path.join(HERE, "csrc", "kda_py.c")]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(CALLER + ".tmp", CALLER)
+    return CALLER
 
 
 def build(verbose: bool = False) -> str:
@@ -34,6 +49,7 @@ def build(verbose: bool = False) -> str:
     if verbose and out.strip():
         print(out)
     os.replace(LIB + ".tmp", LIB)
+    build_caller(verbose)
     return LIB
 
 

@@ -260,13 +260,37 @@ class _On:
         return getattr(self.x, name)
 
 
-@pytest.mark.parametrize("places", [(-1, 0), (0, -1), (0, 1), (1, 1, 0), (-1, -1), (0, 0, -1, 0)])
-def test_binding_refuses_mixed_places(places):
-    """Nothing is launched unless every tensor is on one GPU, in whatever order they come."""
+@pytest.mark.parametrize("other", [-1, 1])
+@pytest.mark.parametrize("place", range(9))
+def test_binding_refuses_mixed_places(place, other):
+    """Nothing is launched unless every tensor is on the GPU of the call."""
+    call = binding._load_caller()
+    tensors = tuple(_On(other if i == place else 0) for i in range(9))
     with pytest.raises(ValueError):
-        binding._launch("kda_gdr_fwd", (tuple(_On(i) for i in places),), 0)
+        call(binding._GDR_DECODE, 0, 0, None, (1.0,), tensors)
     with pytest.raises(ValueError):
-        binding._launch("kda_gdr_fwd", (tuple(_On(i) for i in places[:1]), (1.0,), (None,) + tuple(_On(i) for i in places[1:])), 0)
+        call(binding._GDR_FWD, 0, 0, _On(other), (1.0,), (_On(0),) * 9)
+    with pytest.raises(ValueError):
+        call(binding._GDR_FWD, -1, 0, None, (1.0,), (_On(-1),) * 9)
+
+
+def test_caller_checks_its_own_arguments():
+    call = binding._load_caller()
+    ok = (_On(0),) * 9
+    for args in ((9, 0, 0, None, (1.0,), ok), (binding._GDR_FWD, 0, 0, None, (1.0,), ok[:8]),
+                 (binding._GDR_FWD, 0, 0, None, (), ok), (binding._GDR_FWD, 0, 0, None, ("x",), ok),
+                 (binding._GDR_FWD, 0, 0, None, (1.0,), ok[:8] + (3,)), (binding._GDR_FWD, 0, 0, None, (1.0,))):
+        with pytest.raises((TypeError, RuntimeError, AttributeError)):
+            call(*args)
+    deep = _On(0)
+    deep.x = torch.zeros(1, 1, 1, 1, 128)
+    with pytest.raises(ValueError):
+        call(binding._GDR_FWD, 0, 0, None, (1.0,), (deep,) * 9)
+    # what it hands over is what the library checks: an fp32 q is refused by its dtype
+    wrong = _On(0)
+    wrong.x = torch.zeros(1, 4, 1, 128)
+    st = call(binding._GDR_FWD, 0, 0, None, (1.0,), (wrong,) + (_On(0),) * 8)
+    assert binding.STATUS_NAMES[st] == "KDA_ERR_DTYPE"
 
 
 def test_reference_gradients_match_differences():

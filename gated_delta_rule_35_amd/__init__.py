@@ -11,12 +11,12 @@ from .binding import (KdaError, kda_bwd, kda_bwd_workspace_size, kda_decode, kda
                       kda_fwd_cp_packed_workspace_size, kda_fwd_cp_plan, kda_fwd_cp_workspace_size, kda_fwd_intra, kda_fwd_noalloc,
                       kda_fwd_noalloc_max_bytes, kda_fwd_qg, kda_fwd_scan, kda_fwd_trace, kda_fwd_workspace_size, kda_fwd_ws,
                       kda_gdr_bwd, kda_gdr_bwd_workspace_size, kda_gdr_decode, kda_gdr_fwd, kda_gdr_fwd_workspace_size,
-                      kda_qk_norm, kda_qk_norm_bwd,
+                      kda_qk_norm, kda_qk_norm_bwd, kda_qk_norm_bwd_workspace_size,
                       library_path, load_library)
 
 __all__ = ["KdaError", "kda_bwd", "kda_bwd_workspace_size", "kda_decode", "kda_dv_slices", "kda_fwd", "kda_fwd_cp", "kda_fwd_cp_plan", "kda_fwd_fused",
            "kda_fwd_cp_packed_workspace_size", "kda_fwd_cp_workspace_size", "kda_fwd_intra", "kda_fwd_noalloc", "kda_fwd_noalloc_max_bytes", "kda_fwd_qg", "kda_fwd_scan",
            "kda_fwd_ws", "kda_fwd_trace", "kda_fwd_workspace_size",
            "kda_gdr_bwd", "kda_gdr_bwd_workspace_size", "kda_gdr_decode", "kda_gdr_fwd", "kda_gdr_fwd_workspace_size",
-           "kda_qk_norm", "kda_qk_norm_bwd",
+           "kda_qk_norm", "kda_qk_norm_bwd", "kda_qk_norm_bwd_workspace_size",
            "library_path", "load_library"]

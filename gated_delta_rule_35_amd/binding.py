@@ -574,6 +574,11 @@ def kda_gdr_decode(q, k, v, g, beta, scale, state, state_indices=None, out=None,
     return out, new_state
 
 
+def kda_qk_norm_bwd_workspace_size():
+    """Bytes of device workspace kda_qk_norm_bwd needs for weight gradients."""
+    return int(load_library().kda_qk_norm_bwd_workspace_size())
+
+
 _NORM_MODES = {"l2": 0, "rms": 1}
 
 
@@ -608,7 +613,7 @@ def kda_qk_norm_bwd(q, k, d_q_out, d_k_out, q_weight=None, k_weight=None, mode="
         elif res.get(name) is None:
             res[name] = _new(w, torch.float32)
     if workspace is None and (q_weight is not None or k_weight is not None):
-        workspace = _scratch(int(load_library().kda_qk_norm_bwd_workspace_size()), q, stream)
+        workspace = _scratch(kda_qk_norm_bwd_workspace_size(), q, stream)
     _launch(_QK_NORM_BWD, q.get_device(), (_NORM_MODES[mode], eps, bool(interleaved)),
             (q, k, d_q_out, d_k_out, q_weight, k_weight, cos, sin, positions, res["dq"], res["dk"], res["dq_weight"],
              res["dk_weight"]), stream, workspace)

@@ -93,6 +93,6 @@ struct NormParams {
 hipError_t launch_qk_norm(const NormParams& p, hipStream_t stream);
 hipError_t launch_qk_norm_bwd(const NormParams& p, hipStream_t stream);
 constexpr int NORM_ROWS = 16;            // rows that a work-group takes at a time
-constexpr int NORM_DW_BLOCKS = 512;      // most work-groups of a side when weights have gradients
+constexpr int NORM_DW_BLOCKS = 1536;     // most work-groups when weights have gradients, about
 
 }  // namespace kda

@@ -328,7 +328,8 @@ kda_status_t prepare_norm(const kda_tensor_t* const (&x)[2], const kda_tensor_t*
         if (x[i]->dtype != x[0]->dtype) return KDA_ERR_DTYPE;
         if (x[i]->shape[0] != x[0]->shape[0] || x[i]->shape[1] != x[0]->shape[1] || x[i]->shape[2] <= 0)
             return KDA_ERR_SHAPE;
-        if (x[i]->shape[2] > (int64_t(1) << 16)) return KDA_ERR_UNSUPPORTED;
+        if (x[i]->shape[2] > (int64_t(1) << 16) || x[i]->shape[0] * x[i]->shape[1] > kMaxTokens)
+            return KDA_ERR_UNSUPPORTED;
         if (w[i]) {
             if ((st = check_tensor(w[i], 1, KDA_F32, KDA_F32, 4)) != KDA_OK) return st;
             if (w[i]->shape[0] != kHeadDim) return KDA_ERR_SHAPE;
@@ -347,8 +348,8 @@ kda_status_t prepare_norm(const kda_tensor_t* const (&x)[2], const kda_tensor_t*
     const int64_t B = x[0]->shape[0], T = x[0]->shape[1];
     if (B * T > kMaxTokens) return KDA_ERR_UNSUPPORTED;
     if (cos) {
-        if ((st = check_tensor(cos, 2, KDA_F32, KDA_F32, 4)) != KDA_OK) return st;
-        if ((st = check_tensor(sin, 2, KDA_F32, KDA_F32, 4)) != KDA_OK) return st;
+        if ((st = check_tensor(cos, 2, KDA_F32, KDA_F32, 16)) != KDA_OK) return st;
+        if ((st = check_tensor(sin, 2, KDA_F32, KDA_F32, 16)) != KDA_OK) return st;
         if (!same_shape(sin, cos->shape, 2) || cos->shape[0] < 1) return KDA_ERR_SHAPE;
         if (cos->shape[1] < 8 || cos->shape[1] > kHeadDim / 2 || cos->shape[1] % 8 != 0) return KDA_ERR_UNSUPPORTED;
         p.cos = static_cast<const float*>(cos->data);
@@ -369,17 +370,18 @@ kda_status_t prepare_norm(const kda_tensor_t* const (&x)[2], const kda_tensor_t*
     return KDA_OK;
 }
 
-// Work-groups of a side: one per 16 rows, at most `most` where they loop.
-kda_status_t norm_blocks(kda::NormParams& p, int64_t most) {
-    int64_t all = 0;
+// Work-groups of both sides: one per 16 rows; with weight gradients at most
+// NORM_DW_BLOCKS in proportion to the sides' rows (rounded up), which then loop.
+kda_status_t norm_blocks(kda::NormParams& p, bool weights) {
+    const int64_t total = p.s[0].rows + p.s[1].rows;
+    if (total > kMaxTokens) return KDA_ERR_UNSUPPORTED;
     for (int i = 0; i < 2; ++i) {
         int64_t b = (p.s[i].rows + kda::NORM_ROWS - 1) / kda::NORM_ROWS;
-        if (p.s[i].dw) b = std::min(b, most);
-        if (b > 2 * kMaxBlocks) return KDA_ERR_UNSUPPORTED;
+        if (weights && total > 0) b = std::min(b, (kda::NORM_DW_BLOCKS * p.s[i].rows + total - 1) / total);
+        if (b > kMaxBlocks) return KDA_ERR_UNSUPPORTED;
         p.blocks[i] = static_cast<int32_t>(b);
-        all += b;
     }
-    return all > 2 * kMaxBlocks ? KDA_ERR_UNSUPPORTED : KDA_OK;
+    return KDA_OK;
 }
 
 }  // namespace
@@ -405,12 +407,12 @@ kda_status_t kda_qk_norm(const kda_tensor_t* q, const kda_tensor_t* k, const kda
         p.s[i].y = y[i]->data;
     }
     if (overlaps(q_out, k_out)) return KDA_ERR_LAYOUT;
-    if ((st = norm_blocks(p, 0)) != KDA_OK) return st;
+    if ((st = norm_blocks(p, false)) != KDA_OK) return st;
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     return finish(kda::launch_qk_norm(p, hs), hs);
 }
 
-int64_t kda_qk_norm_bwd_workspace_size(void) { return 2 * (int64_t)kda::NORM_DW_BLOCKS * kHeadDim * 4; }
+int64_t kda_qk_norm_bwd_workspace_size(void) { return ((int64_t)kda::NORM_DW_BLOCKS + 2) * kHeadDim * 4; }
 
 kda_status_t kda_qk_norm_bwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda_tensor_t* d_q_out,
                              const kda_tensor_t* d_k_out, const kda_tensor_t* q_weight, const kda_tensor_t* k_weight,
@@ -441,8 +443,8 @@ kda_status_t kda_qk_norm_bwd(const kda_tensor_t* q, const kda_tensor_t* k, const
     const kda_tensor_t* ins[] = {q, k, d_q_out, d_k_out, q_weight, k_weight, cos, sin, positions};
     const kda_tensor_t* outs[] = {dq, dk, d_q_weight, d_k_weight};
     if (any_overlap(outs, 4, ins, 9)) return KDA_ERR_LAYOUT;
-    if ((st = norm_blocks(p, kda::NORM_DW_BLOCKS)) != KDA_OK) return st;
     const bool weights = d_q_weight || d_k_weight;
+    if ((st = norm_blocks(p, weights)) != KDA_OK) return st;
     const int64_t need = weights ? kda_qk_norm_bwd_workspace_size() : 0;
     if (weights && workspace && (workspace_size < need || reinterpret_cast<uintptr_t>(workspace) % 16 != 0))
         return KDA_ERR_WORKSPACE;

@@ -27,8 +27,11 @@ struct NormType;
 template <>
 struct NormType<0> {   // bf16
     typedef uint16_t T;
-    static __device__ __forceinline__ void load(const void* p, int64_t at, float (&x)[8]) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(static_cast<const T*>(p) + at);
+    typedef u32x4 Raw;   // eight channels as they lie in memory
+    static __device__ __forceinline__ Raw load(const void* p, int64_t at) {
+        return *reinterpret_cast<const Raw*>(static_cast<const T*>(p) + at);
+    }
+    static __device__ __forceinline__ void widen(const Raw& v, float (&x)[8]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             x[2 * i] = bf_lo(v[i]);
@@ -43,8 +46,11 @@ struct NormType<0> {   // bf16
 template <>
 struct NormType<1> {   // fp16
     typedef uint16_t T;
-    static __device__ __forceinline__ void load(const void* p, int64_t at, float (&x)[8]) {
-        const half8 v = *reinterpret_cast<const half8*>(static_cast<const T*>(p) + at);
+    typedef half8 Raw;
+    static __device__ __forceinline__ Raw load(const void* p, int64_t at) {
+        return *reinterpret_cast<const Raw*>(static_cast<const T*>(p) + at);
+    }
+    static __device__ __forceinline__ void widen(const Raw& v, float (&x)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = (float)v[i];
     }
@@ -56,13 +62,18 @@ struct NormType<1> {   // fp16
 template <>
 struct NormType<2> {   // fp32
     typedef float T;
-    static __device__ __forceinline__ void load(const void* p, int64_t at, float (&x)[8]) {
+    struct Raw {
+        f32x4 a, b;
+    };
+    static __device__ __forceinline__ Raw load(const void* p, int64_t at) {
         const f32x4* s = reinterpret_cast<const f32x4*>(static_cast<const T*>(p) + at);
-        const f32x4 a = s[0], b = s[1];
+        return {s[0], s[1]};
+    }
+    static __device__ __forceinline__ void widen(const Raw& v, float (&x)[8]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            x[i] = a[i];
-            x[4 + i] = b[i];
+            x[i] = v.a[i];
+            x[4 + i] = v.b[i];
         }
     }
     static __device__ __forceinline__ void store(void* p, int64_t at, const float (&x)[8]) {
@@ -72,43 +83,60 @@ struct NormType<2> {   // fp32
     }
 };
 
-// Row `i` of a side: its offset in x, its token, and its offset in a contiguous tensor.
+// Row `i` of a side: its offset in x and its token (a side has fewer than 2^31 rows).
 struct RowAt {
-    int64_t x, token, flat;
+    int64_t x;
+    uint32_t token;
 };
-__device__ __forceinline__ RowAt row_at(const NormParams& p, const NormSide& s, int64_t i) {
-    const int64_t token = i / s.H, h = i - token * s.H, b = token / p.T, t = token - b * p.T;
-    return {b * s.sb + t * s.st + h * s.sh, token, i * DK};
+__device__ __forceinline__ RowAt row_at(const NormParams& p, const NormSide& s, uint32_t i) {
+    const uint32_t token = i / (uint32_t)s.H, h = i - token * (uint32_t)s.H, T = (uint32_t)p.T, b = token / T, t = token - b * T;
+    return {b * s.sb + t * s.st + h * s.sh, token};
 }
 
-// The rotation of the lane's eight channels 8 l .. + 7 by the token's position (DIR 1),
-// or back (DIR -1).  Positions outside the tables take their nearest row.
-template <int DIR>
-__device__ __forceinline__ void rotate(const NormParams& p, int64_t token, int l, int lane, float (&x)[8]) {
-    if (!p.cos) return;
-    int64_t pos = p.pos ? (int64_t)p.pos[token] : token % p.T;
+// The lane's cos and sin of a rotation: of its eight channels' angles (half pairs), or
+// of its four pairs' (adjacent pairs).  Positions outside the tables take their nearest row.
+struct Angles {
+    f32x4 c[2], s[2];
+};
+__device__ __forceinline__ Angles angles(const NormParams& p, uint32_t token, int l) {
+    Angles a;
+    if (!p.cos) return a;
+    int64_t pos = p.pos ? (int64_t)p.pos[token] : (int64_t)(token % (uint32_t)p.T);
     pos = pos < 0 ? 0 : (pos >= p.P ? p.P - 1 : pos);
+    const int hl = p.half / 8, step = p.interleaved ? 4 : 8;
+    // lanes past the rotated channels read the first angles and do not use them
+    const int at = 8 * l >= 2 * p.half ? 0 : step * (p.interleaved || l < hl ? l : l - hl);
+    const f32x4* c = reinterpret_cast<const f32x4*>(p.cos + pos * p.half + at);
+    const f32x4* s = reinterpret_cast<const f32x4*>(p.sin + pos * p.half + at);
+    a.c[0] = c[0];
+    a.s[0] = s[0];
+    if (!p.interleaved) {
+        a.c[1] = c[1];
+        a.s[1] = s[1];
+    }
+    return a;
+}
+
+// The rotation of the lane's eight channels 8 l .. + 7 (DIR 1), or back (DIR -1).
+template <int DIR>
+__device__ __forceinline__ void rotate(const NormParams& p, const Angles& a, int l, int lane, float (&x)[8]) {
+    if (!p.cos) return;
     const bool in = 8 * l < 2 * p.half;
     if (p.interleaved) {
         if (!in) return;
-        const float* c = p.cos + pos * p.half + 4 * l;
-        const float* s = p.sin + pos * p.half + 4 * l;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float cc = c[i], ss = DIR * s[i], a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = a * cc - b * ss;
-            x[2 * i + 1] = b * cc + a * ss;
+            const float cc = a.c[0][i], ss = DIR * a.s[0][i], u = x[2 * i], v = x[2 * i + 1];
+            x[2 * i] = u * cc - v * ss;
+            x[2 * i + 1] = v * cc + u * ss;
         }
     } else {
         const int hl = p.half / 8;                      // lanes of the first members
-        const int to = lane - l + (l < hl ? l + hl : l - hl);
-        const int at = l < hl ? 8 * l : 8 * (l - hl);
-        const float* c = p.cos + pos * p.half + (in ? at : 0);
-        const float* s = p.sin + pos * p.half + (in ? at : 0);
+        const int to = in ? lane - l + (l < hl ? l + hl : l - hl) : lane;
+        const float sign = l < hl ? -DIR : DIR;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float y = __shfl(x[i], in ? to : lane);
-            const float cc = c[i], ss = (l < hl ? -DIR : DIR) * s[i];
+            const float y = __shfl(x[i], to), cc = a.c[i >> 2][i & 3], ss = sign * a.s[i >> 2][i & 3];
             x[i] = in ? x[i] * cc + y * ss : x[i];
         }
     }
@@ -129,18 +157,19 @@ __global__ void __launch_bounds__(NT) kda_qk_norm_kernel(const NormParams p) {
     float w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = s.w ? s.w[8 * l + i] : 1.f;
-    const int64_t row = (int64_t)block * NORM_ROWS + (threadIdx.x >> 4);
-    const RowAt at = row_at(p, s, row < s.rows ? row : s.rows - 1);   // lanes past the end repeat the last row
+    const uint32_t row = (uint32_t)block * NORM_ROWS + (threadIdx.x >> 4), rows = (uint32_t)s.rows;
+    const RowAt at = row_at(p, s, row < rows ? row : rows - 1);   // lanes past the end repeat the last row
     float x[8];
-    NormType<XT>::load(s.x, at.x + 8 * l, x);
+    NormType<XT>::widen(NormType<XT>::load(s.x, at.x + 8 * l), x);
+    const Angles an = angles(p, at.token, l);
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
     const float r = inverse_norm(p, sum16(ss));
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] *= r * w[i];
-    rotate<1>(p, at.token, l, lane, x);
-    if (row < s.rows) NormType<0>::store(s.y, at.flat + 8 * l, x);
+    rotate<1>(p, an, l, lane, x);
+    if (row < rows) NormType<0>::store(s.y, (int64_t)row * DK + 8 * l, x);
 }
 
 template <int XT, int DT>
@@ -156,14 +185,19 @@ __global__ void __launch_bounds__(NT) kda_qk_norm_bwd_kernel(const NormParams p)
         w[i] = s.w ? s.w[8 * l + i] : 1.f;
         dw[i] = 0.f;
     }
-    for (int64_t base = (int64_t)block * NORM_ROWS; base < s.rows; base += (int64_t)p.blocks[side] * NORM_ROWS) {
-        const int64_t row = base + (threadIdx.x >> 4);
-        const bool in = row < s.rows;
-        const RowAt at = row_at(p, s, in ? row : s.rows - 1);
+    const uint32_t rows = (uint32_t)s.rows, stride = (uint32_t)p.blocks[side] * NORM_ROWS;
+    // a work-group's rows are `stride` apart; every lane of a group takes the same number
+    for (uint64_t base = (uint64_t)block * NORM_ROWS; base < rows; base += stride) {
+        const uint64_t row = base + (threadIdx.x >> 4);
+        const uint32_t i0 = row < rows ? (uint32_t)row : rows - 1;
+        const RowAt at = row_at(p, s, i0);
+        const auto rx = NormType<XT>::load(s.x, at.x + 8 * l);
+        const auto rd = NormType<DT>::load(s.dy, (int64_t)i0 * DK + 8 * l);
+        const Angles an = angles(p, at.token, l);
         float x[8], d[8];
-        NormType<XT>::load(s.x, at.x + 8 * l, x);
-        NormType<DT>::load(s.dy, at.flat + 8 * l, d);
-        rotate<-1>(p, at.token, l, lane, d);
+        NormType<XT>::widen(rx, x);
+        NormType<DT>::widen(rd, d);
+        rotate<-1>(p, an, l, lane, d);
         float ss = 0.f, xd = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -172,13 +206,13 @@ __global__ void __launch_bounds__(NT) kda_qk_norm_bwd_kernel(const NormParams p)
         }
         const float r = inverse_norm(p, sum16(ss));
         const float m = sum16(xd) * r * r * (p.rms ? 1.f / DK : 1.f);
-        if (in) {
+        if (row < rows) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 dw[i] = fmaf(d[i] * r, x[i], dw[i]);
                 d[i] = r * (w[i] * d[i] - x[i] * m);
             }
-            NormType<XT>::store(s.y, at.flat + 8 * l, d);
+            NormType<XT>::store(s.y, (int64_t)row * DK + 8 * l, d);
         }
     }
     if (!s.dw) return;
@@ -193,21 +227,23 @@ __global__ void __launch_bounds__(NT) kda_qk_norm_bwd_kernel(const NormParams p)
     }
 }
 
-// dw of side blockIdx.x: the work-groups' sums, in order.
-__global__ void __launch_bounds__(1024) kda_qk_norm_dw_kernel(const NormParams p) {
-    __shared__ float part[8][DK];
-    const int side = blockIdx.x, c = threadIdx.x & (DK - 1), g = threadIdx.x >> 7;
+// dw of side blockIdx.x / 8, channels 16 (blockIdx.x % 8) .. + 15: the work-groups'
+// sums, 64 of them side by side, then in order.
+__global__ void __launch_bounds__(NT) kda_qk_norm_dw_kernel(const NormParams p) {
+    __shared__ __attribute__((aligned(16))) float part[64][16];
+    const int side = blockIdx.x >> 3, c = 4 * (threadIdx.x & 3), g = threadIdx.x >> 2, c0 = 16 * (blockIdx.x & 7);
     if (!p.s[side].dw) return;
-    const float* src = p.part + (side ? (int64_t)p.blocks[0] * DK : 0);
-    float t = 0.f;
-    for (int b = g; b < p.blocks[side]; b += 8) t += src[(int64_t)b * DK + c];
-    part[g][c] = t;
+    const float* src = p.part + (side ? (int64_t)p.blocks[0] * DK : 0) + c0 + c;
+    f32x4 t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int b = g; b < p.blocks[side]; b += 64) t += *reinterpret_cast<const f32x4*>(src + (int64_t)b * DK);
+    *reinterpret_cast<f32x4*>(&part[g][c]) = t;
     __syncthreads();
-    if (g == 0) {
-        t = 0.f;
+    if (threadIdx.x < 16) {
+        float y = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t += part[i][c];
-        p.s[side].dw[c] = t;
+        for (int i = 0; i < 64; ++i) y += part[i][threadIdx.x];
+        p.s[side].dw[c0 + threadIdx.x] = y;
     }
 }
 
@@ -231,7 +267,7 @@ hipError_t launch_qk_norm_bwd(const NormParams& p, hipStream_t stream) {
         if (e != hipSuccess) return e;
     }
     if (p.s[0].dw || p.s[1].dw) {
-        hipLaunchKernelGGL(kda_qk_norm_dw_kernel, dim3(2), dim3(1024), 0, stream, p);
+        hipLaunchKernelGGL(kda_qk_norm_dw_kernel, dim3(16), dim3(NT), 0, stream, p);
         return hipGetLastError();
     }
     return hipSuccess;

@@ -527,12 +527,14 @@ kda_status_t kda_gdr_decode(const kda_tensor_t* q, const kda_tensor_t* k, const 
  *
  *   q [B, T, Hq, 128], k [B, T, Hk, 128]  bf16, fp16 or fp32 (both the same), strided as above
  *   q_weight, k_weight  [128] fp32, or NULL (ones)
- *   cos, sin            [P, half] fp32 tables, half a multiple of 8 up to 64; both NULL: no rotation
+ *   cos, sin            [P, half] fp32 tables, 16-byte aligned, half a multiple of 8 up to 64;
+ *                       both NULL: no rotation
  *   positions           [B, T] int32 row of the tables of each token, or NULL (the token's
  *                       index in its row); values outside [0, P) take the nearest row
  *   q_out, k_out        bf16, contiguous; q_out may be q itself where q is contiguous bf16,
  *                       and likewise k; any other overlap returns KDA_ERR_LAYOUT
- * eps must be finite and positive, mode 0 or 1 (KDA_ERR_VALUE).  Arithmetic is fp32,
+ * eps must be finite and positive, mode 0 or 1 (KDA_ERR_VALUE).  More than 2^26 rows of
+ * one tensor, or 2^31 - 1 of both, return KDA_ERR_UNSUPPORTED.  Arithmetic is fp32,
  * each output is rounded once.
  */
 kda_status_t kda_qk_norm(const kda_tensor_t* q, const kda_tensor_t* k, const kda_tensor_t* q_weight,

@@ -11,7 +11,7 @@ from tests import gdr_ref as ref
 from tests.test_boundary import FAKE, T
 
 F32, BF16, F16, I32 = binding.KDA_F32, binding.KDA_BF16, binding.KDA_F16, binding.KDA_I32
-STEP = 1 << 32   # distinct, far apart addresses
+STEP = 1 << 42   # distinct, far apart addresses
 
 
 @pytest.fixture(scope="module")
@@ -201,6 +201,10 @@ def norm(lib, backward=False, mode=0, eps=1e-6, ws=FAKE, size=1 << 30, **change)
     ("UNSUPPORTED", dict(cos=at(5, [9, 20], F32), sin=at(6, [9, 20], F32))),
     ("UNSUPPORTED", dict(cos=at(5, [9, 72], F32), sin=at(6, [9, 72], F32))),
     ("LAYOUT", dict(q=at(1, [2, 5, 4, 128], strides=[4096, 516, 128, 1]))),
+    ("LAYOUT", dict(sin=T([9, 32], F32, data=FAKE + 6 * STEP + 4))),
+    ("UNSUPPORTED", dict(q=at(1, [2, 1 << 29, 4, 128]), k=at(2, [2, 1 << 29, 2, 128]), pos=None,
+                         qo=at(8, [2, 1 << 29, 4, 128]), ko=at(9, [2, 1 << 29, 2, 128]),
+                         dq=at(10, [2, 1 << 29, 4, 128]), dk=at(11, [2, 1 << 29, 2, 128]))),
     ("VALUE", dict(mode=2)), ("VALUE", dict(eps=0.0)), ("VALUE", dict(eps=float("nan"))),
 ])
 def test_norm(lib, name, change):

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from gated_delta_rule_35_amd import kda_fwd, kda_gdr_bwd, kda_gdr_fwd, kda_qk_norm, kda_qk_norm_bwd, load_library
+from gated_delta_rule_35_amd import kda_qk_norm_bwd_workspace_size
 from tests import gdr_ref as ref
 
 pytestmark = pytest.mark.gpu
@@ -154,7 +155,7 @@ def test_graph():
     kw = kwargs(c, "rms", True)
     q, k = c["q"].cuda(), c["k"].cuda()
     dy = [torch.randn_like(q), torch.randn_like(k)]
-    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(kda_qk_norm_bwd_workspace_size(), dtype=torch.uint8, device="cuda")
 
     def both():
         y = kda_qk_norm(q, k, **kw)

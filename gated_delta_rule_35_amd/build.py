@@ -18,7 +18,7 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libkda.so")
 SOURCES = [os.path.join(HERE, "csrc", f)
            for f in ("kda_fused.hip", "kda_intra.hip", "kda_scan.hip", "kda_compose.hip", "kda_decode.hip", "kda_bwd.hip", "kda_scratch.hip",
-              "kda_gdr_prep.hip", "kda_gdr_scan.hip", "kda_gdr_grads.hip", "kda_gdr_decode.hip", "kda_qk_norm.hip",
+              "kda_gdr_prep.hip", "kda_gdr_fwd.hip", "kda_gdr_bwd.hip", "kda_gdr_grads.hip", "kda_gdr_decode.hip", "kda_qk_norm.hip",
               "kda_api.cpp", "kda_gdr_api.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

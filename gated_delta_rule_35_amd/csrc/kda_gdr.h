@@ -37,18 +37,16 @@ struct GdrParams {
     float* dx;             // [nslots][Hv][64][128] gradient of the right-hand side beta (v - e^G K S)
 };
 
-// Chunk record of the prep kernel (see kda_gdr_prep.hip): the triangular operands as
-// lists of six 1 KB fragments per bf16 part, and four rows of per-token numbers.
+// Chunk records of the prep kernel (see kda_gdr_prep.hip): triangular operands as lists
+// of six 1 KB fragments per part, and rows of 64 per-token numbers (fp32).
 constexpr int GDR_FRAG = 1024;
 constexpr int GDR_TRI = 6 * GDR_FRAG;              // one part of a triangular operand
-constexpr int GDR_T = 0;                           // T, three parts
-constexpr int GDR_SC = GDR_T + 3 * GDR_TRI;        // e^G, e^{G_last - G}, beta, e^{G_last} ([64] fp32 each)
-constexpr int GDR_A = GDR_SC + 1024;               // A (scale included): two parts forward, three backward
-constexpr int gdr_rec_bytes(int na) { return GDR_A + na * GDR_TRI; }
-constexpr int GDR_NA_FWD = 2, GDR_NA_BWD = 3;
+// Forward, fp16: T in two parts, A in one, the per-token rows.
+constexpr int FWD_T = 0, FWD_A = 2 * GDR_TRI, FWD_SC = 3 * GDR_TRI, FWD_ROWS = 8, FWD_REC = FWD_SC + FWD_ROWS * 256;
+// Backward, bf16: T in three parts, the per-token rows, A (scale included) in three parts.
+constexpr int GDR_T = 0, GDR_SC = 3 * GDR_TRI, GDR_A = GDR_SC + 1024, GDR_REC = GDR_A + 3 * GDR_TRI;
 
-// Fills the records with na parts of A.
-hipError_t launch_gdr_prep(const GdrParams& p, int na, hipStream_t stream);
+hipError_t launch_gdr_prep(const GdrParams& p, bool bwd, hipStream_t stream);
 hipError_t launch_gdr_grads(const GdrParams& p, int cus, hipStream_t stream);
 hipError_t launch_gdr_fwd(const GdrParams& p, hipStream_t stream);
 // cus: compute units of the current device.

@@ -144,13 +144,13 @@ int64_t up256(int64_t x) { return (x + 255) & ~int64_t(255); }
 
 // Workspace of a call in units of one (chunk slot, value head): the records, then, for
 // the backward, S, dS, u and dx.
-int64_t fwd_bytes(int64_t units) { return units * kda::gdr_rec_bytes(kda::GDR_NA_FWD); }
+int64_t fwd_bytes(int64_t units) { return units * kda::FWD_REC; }
 struct BwdLayout {
     int64_t S, dS, u, dx, total;
 };
 BwdLayout bwd_layout(int64_t units) {
     BwdLayout L{};
-    L.S = up256(units * kda::gdr_rec_bytes(kda::GDR_NA_BWD));
+    L.S = up256(units * kda::GDR_REC);
     L.dS = L.S + units * kHeadDim * kHeadDim * 4;
     L.u = L.dS + units * kHeadDim * kHeadDim * 4;
     L.dx = L.u + units * 64 * kHeadDim * 4;

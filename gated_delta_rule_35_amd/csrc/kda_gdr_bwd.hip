@@ -1,12 +1,10 @@
-// The sequential walks of the gated delta rule with one decay per head, on gfx950
-// (MI355X): the forward's (state, output) and the backward's (state gradient).
-//
-// Forward, per chunk with the prep kernel's T and A (G, e^{..} as there):
-//   e = v - e^G (K S),  u = T (beta e),  o = scale e^G (Q S) + A u,
-//   S <- e^{G_last} S + K^T (e^{G_last - G} u)
-// Backward, chunks in reverse, dS the gradient of the state that leaves the chunk:
+// The sequential walks of the backward of the gated delta rule with one decay per head,
+// on gfx950 (MI355X), with the prep kernel's T and A:
+// forwards once more, for the state that enters each chunk and the corrected values,
+//   e = v - e^G (K S),  u = T (beta e),  S <- e^{G_last} S + K^T (e^{G_last - G} u),
+// then chunks in reverse, dS the gradient of the state that leaves the chunk,
 //   du = A^T do + e^{G_last - G} (K dS),  dx = T^T du,  dv = beta dx,
-//   dS <- e^{G_last} dS + Q^T (scale e^G do) - K^T (beta e^G dx)
+//   dS <- e^{G_last} dS + Q^T (scale e^G do) - K^T (beta e^G dx).
 //
 // Every product's right-hand side is a set of columns of S (value channels), and no
 // product mixes columns: a wave owns 16 of them for the whole sequence and needs
@@ -19,8 +17,7 @@
 //   Tile t = 2 kk + h of the state holds key channel 32 kk + 8 g + 4 h + r in row
 // 4 g + r (g = lane / 16), so that the two tiles of a 32-channel step list the lane's
 // eight channels as they lie in K's rows.
-//   fp32 operands go in as three bf16 parts (two where the result is the bf16 output),
-// see kda_gdr_device.h.
+//   fp32 operands go in as three bf16 parts, see kda_gdr_device.h.
 #include "kda_gdr_device.h"
 
 namespace kda {
@@ -29,9 +26,8 @@ namespace {
 
 constexpr int SCAN_THREADS = 384;   // four waves that compute, two that load
 // One LDS buffer: K, Q tiles (swizzled), the slice of v (or of do) [64][64] bf16, the record.
-template <int NA>
 struct ScanL {
-    static constexpr int K = 0, Q = 16384, V = 32768, REC = 40960, BYTES = REC + gdr_rec_bytes(NA);
+    static constexpr int K = 0, Q = 16384, V = 32768, REC = 40960, BYTES = REC + GDR_REC;
 };
 
 // The lane's eight (key channel, tile) rows: channel of row 4 g + r of tile t.
@@ -63,10 +59,10 @@ __device__ __forceinline__ bf16x8 tri_col_frag(const char* part, int m, int kk, 
 
 // One loading wave's (ld = 0, 1) half of a chunk's DMA into a buffer: 32 pieces of
 // tiles and slices, and nrec of the record.
-template <int NA, int NREC, bool WITH_Q>
+template <int NREC, bool WITH_Q>
 __device__ __forceinline__ void load_chunk(const GdrParams& p, const Rows& vsrc, uint32_t lds, int64_t row, int64_t tok,
                                            int rows, int hq, int hv, int sl, int64_t slot, int ld, int lane) {
-    typedef ScanL<NA> L;
+    typedef ScanL L;
     const __amdgpu_buffer_rsrc_t rk =
         chunk_rsrc(p.k.p + row * p.k.sb + tok * p.k.st + hq * p.k.sh, p.k.st, rows, DK);
     const int l4 = lane >> 4, l16 = lane & 15;
@@ -92,7 +88,7 @@ __device__ __forceinline__ void load_chunk(const GdrParams& p, const Rows& vsrc,
         dma_piece(rv, lds + L::V + x * 1024, (int)((8 * x + (lane >> 3)) * vsrc.st * 2) + ((lane & 7) << 4));
     }
     const __amdgpu_buffer_rsrc_t rr =
-        make_rsrc(p.rec + (slot * p.Hv + hv) * gdr_rec_bytes(NA), gdr_rec_bytes(NA));
+        make_rsrc(p.rec + (slot * p.Hv + hv) * GDR_REC, GDR_REC);
 #pragma unroll
     for (int u = 0; u < (NREC + 1) / 2; ++u) {
         const int x = 2 * u + ld;
@@ -102,12 +98,8 @@ __device__ __forceinline__ void load_chunk(const GdrParams& p, const Rows& vsrc,
 
 }  // namespace
 
-// KEEP: the backward's walk forwards: writes each chunk's entering state and u instead
-// of the output.
-template <bool KEEP>
-__global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_scan_kernel(const GdrParams p) {
-    constexpr int NA = KEEP ? GDR_NA_BWD : GDR_NA_FWD;
-    typedef ScanL<NA> L;
+__global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_keep_kernel(const GdrParams p) {
+    typedef ScanL L;
     __shared__ __attribute__((aligned(1024))) char smem[2 * L::BYTES];
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, jj = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -123,10 +115,10 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_scan_kernel(const GdrPar
         return r <= 0 ? 0 : (r >= CH ? CH : (int)r);
     };
     if (w >= 4) {   // loading waves: chunk c + 1 while the others are at chunk c
-        constexpr int NREC = KEEP ? 19 : 19 + 6 * NA;   // pieces of the record that are read
+        constexpr int NREC = 19;   // pieces of the record that are read: T and the numbers
         const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(smem));
         auto load = [&](int c) {
-            load_chunk<NA, NREC, !KEEP>(p, p.v, lds + (c & 1) * L::BYTES, row, bos + (int64_t)c * CH, rows_of(c), hq, hv,
+            load_chunk<NREC, false>(p, p.v, lds + (c & 1) * L::BYTES, row, bos + (int64_t)c * CH, rows_of(c), hq, hv,
                                         sl, slot0 + c, w - 4, lane);
         };
         if (nch > 0) load(0);
@@ -150,7 +142,7 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_scan_kernel(const GdrPar
         char* buf = smem + (c & 1) * L::BYTES;
         const char *sK = buf + L::K, *sQ = buf + L::Q, *rec = buf + L::REC;
         const float* sc = reinterpret_cast<const float*>(rec + GDR_SC);
-        if (KEEP) {
+        {
             float* dst = p.S + ((slot0 + c) * p.Hv + hv) * DK * DK + col;
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
@@ -162,7 +154,7 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_scan_kernel(const GdrPar
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) sb[kk] = split_acc<3>(S[2 * kk], S[2 * kk + 1]);
         // x = beta (v - e^G K S)
-        f32x4 x[4], o[4];
+        f32x4 x[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             f32x4 a = {0.f, 0.f, 0.f, 0.f};
@@ -171,20 +163,10 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_scan_kernel(const GdrPar
                 const bf16x8 f[1] = {row_frag(sK, m, kk, g, jj)};
                 a = mfma_split<3>(f, sb[kk], a);
             }
-            const f32x4 eg = *reinterpret_cast<const f32x4*>(sc + 16 * m + 4 * g);
-            const f32x4 be = *reinterpret_cast<const f32x4*>(sc + 128 + 16 * m + 4 * g);
+            const f32x4 eg = *reinterpret_cast<const f32x4*>(sc + SC_EG + 16 * m + 4 * g);
+            const f32x4 be = *reinterpret_cast<const f32x4*>(sc + SC_BE + 16 * m + 4 * g);
             const f32x4 v = widen(slice_frag(buf + L::V, m, w, g, jj));
             x[m] = be * (v - eg * a);
-            if (!KEEP) {
-                f32x4 b = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    const bf16x8 f = row_frag(sQ, m, kk, g, jj);
-                    b = mfma_bf(f, sb[kk].s[1], b);
-                    b = mfma_bf(f, sb[kk].s[0], b);
-                }
-                o[m] = (p.scale * eg) * b;
-            }
         }
         // u = T x
         f32x4 u[4];
@@ -204,53 +186,23 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_scan_kernel(const GdrPar
                 u[m] = a;
             }
         }
-        const int rows = rows_of(c);
-        if (KEEP) {
+        {
             float* dst = p.u + ((slot0 + c) * p.Hv + hv) * CH * DK + col;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) dst[(16 * m + 4 * g + r) * DK] = u[m][r];
             }
-        } else {
-            // o += A u, rounded once, through this wave's columns of the v slice
-            Split<2> ub[2];
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) ub[kk] = split_acc<2>(u[2 * kk], u[2 * kk + 1]);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-#pragma unroll
-                for (int kk = 0; kk <= m / 2; ++kk) {
-                    const char* f = rec + GDR_A + tri_frag(m, kk) * GDR_FRAG + lane * 16;
-                    const bf16x8 ap[2] = {lds_bf8(f), lds_bf8(f + GDR_TRI)};
-                    o[m] = mfma_split<2>(ap, ub[kk], o[m]);
-                }
-                const uint32_t p0 = pack_bf2(o[m][0], o[m][1]), p1 = pack_bf2(o[m][2], o[m][3]);
-                char* dst = buf + L::V + (16 * m + 4 * g) * 128 + 2 * (16 * w + jj);
-                *reinterpret_cast<uint16_t*>(dst) = (uint16_t)p0;
-                *reinterpret_cast<uint16_t*>(dst + 128) = (uint16_t)(p0 >> 16);
-                *reinterpret_cast<uint16_t*>(dst + 256) = (uint16_t)p1;
-                *reinterpret_cast<uint16_t*>(dst + 384) = (uint16_t)(p1 >> 16);
-            }
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int i = 32 * q + (lane >> 1);
-                const u32x4 y = *reinterpret_cast<const u32x4*>(buf + L::V + i * 128 + 32 * w + 16 * (lane & 1));
-                if (i < rows)
-                    *reinterpret_cast<u32x4*>(p.o + ((row * p.T + bos + (int64_t)c * CH + i) * p.Hv + hv) * DK +
-                                              64 * sl + 16 * w + 8 * (lane & 1)) = y;
-            }
         }
         // S <- e^{G_last} S + K^T (e^{G_last - G} u)
         Split<3> wb[2];
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
-            const f32x4 g0 = *reinterpret_cast<const f32x4*>(sc + 64 + 32 * kk + 4 * g);
-            const f32x4 g1 = *reinterpret_cast<const f32x4*>(sc + 64 + 32 * kk + 16 + 4 * g);
+            const f32x4 g0 = *reinterpret_cast<const f32x4*>(sc + SC_GA + 32 * kk + 4 * g);
+            const f32x4 g1 = *reinterpret_cast<const f32x4*>(sc + SC_GA + 32 * kk + 16 + 4 * g);
             wb[kk] = split_acc<3>(g0 * u[2 * kk], g1 * u[2 * kk + 1]);
         }
-        const float el = sc[192];
+        const float el = sc[SC_EL];
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
             f32x4 a = S[t] * el;
@@ -262,18 +214,12 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_scan_kernel(const GdrPar
             S[t] = a;
         }
     }
-    if (p.hT && !KEEP) {
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) p.hT[so + state_row(t, g, r) * DK] = S[t][r];
-        }
-    }
 }
 
 __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_rscan_kernel(const GdrParams p) {
-    constexpr int NA = GDR_NA_BWD;
-    typedef ScanL<NA> L;
+    constexpr int NREC = 37;   // pieces of the record
+    static_assert(NREC * 1024 == GDR_REC, "record");
+    typedef ScanL L;
     __shared__ __attribute__((aligned(1024))) char smem[2 * L::BYTES];
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, jj = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -291,7 +237,7 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_rscan_kernel(const GdrPa
     if (w >= 4) {
         const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(smem));
         auto load = [&](int c) {
-            load_chunk<NA, 19 + 6 * NA, true>(p, p.dO, lds + (c & 1) * L::BYTES, row, bos + (int64_t)c * CH, rows_of(c),
+            load_chunk<NREC, true>(p, p.dO, lds + (c & 1) * L::BYTES, row, bos + (int64_t)c * CH, rows_of(c),
                                               hq, hv, sl, slot0 + c, w - 4, lane);
         };
         if (nch > 0) load(nch - 1);
@@ -340,7 +286,7 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_rscan_kernel(const GdrPa
                     const bf16x8 f[1] = {row_frag(sK, m, kk, g, jj)};
                     a = mfma_split<3>(f, sb[kk], a);
                 }
-                a *= *reinterpret_cast<const f32x4*>(sc + 64 + 16 * m + 4 * g);
+                a *= *reinterpret_cast<const f32x4*>(sc + SC_GA + 16 * m + 4 * g);
 #pragma unroll
                 for (int kk = m / 2; kk < 2; ++kk) {
                     const bf16x8 db = join(d[2 * kk], d[2 * kk + 1]);
@@ -382,7 +328,7 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_rscan_kernel(const GdrPa
         // dv = beta dx, rounded once, through this wave's columns of the do slice
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            const f32x4 y = dx[m] * *reinterpret_cast<const f32x4*>(sc + 128 + 16 * m + 4 * g);
+            const f32x4 y = dx[m] * *reinterpret_cast<const f32x4*>(sc + SC_BE + 16 * m + 4 * g);
             const uint32_t p0 = pack_bf2(y[0], y[1]), p1 = pack_bf2(y[2], y[3]);
             char* dst = buf + L::V + (16 * m + 4 * g) * 128 + 2 * (16 * w + jj);
             *reinterpret_cast<uint16_t*>(dst) = (uint16_t)p0;
@@ -404,12 +350,12 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_rscan_kernel(const GdrPa
         Split<3> qb[2], kb[2];
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
-            const f32x4 e0 = *reinterpret_cast<const f32x4*>(sc + 32 * kk + 4 * g);
-            const f32x4 e1 = *reinterpret_cast<const f32x4*>(sc + 32 * kk + 16 + 4 * g);
+            const f32x4 e0 = *reinterpret_cast<const f32x4*>(sc + SC_EG + 32 * kk + 4 * g);
+            const f32x4 e1 = *reinterpret_cast<const f32x4*>(sc + SC_EG + 32 * kk + 16 + 4 * g);
             qb[kk] = split_acc<3>((p.scale * e0) * widen(d[2 * kk]), (p.scale * e1) * widen(d[2 * kk + 1]));
             kb[kk] = split_acc<3>(-(e0 * dx[2 * kk]), -(e1 * dx[2 * kk + 1]));
         }
-        const float el = sc[192];
+        const float el = sc[SC_EL];
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
             f32x4 a = S[t] * el;
@@ -431,21 +377,12 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_rscan_kernel(const GdrPa
     }
 }
 
-hipError_t launch_gdr_fwd(const GdrParams& p, hipStream_t stream) {
-    hipError_t e = launch_gdr_prep(p, GDR_NA_FWD, stream);
-    if (e != hipSuccess) return e;
-    const int64_t blocks = (int64_t)p.N * p.Hv * 2;
-    hipLaunchKernelGGL(kda_gdr_scan_kernel<false>, dim3((unsigned)blocks), dim3(SCAN_THREADS),
-                       0, stream, p);
-    return hipGetLastError();
-}
-
 hipError_t launch_gdr_bwd(const GdrParams& p, int cus, hipStream_t stream) {
     const unsigned blocks = (unsigned)((int64_t)p.N * p.Hv * 2);
-    hipError_t e = launch_gdr_prep(p, GDR_NA_BWD, stream);
+    hipError_t e = launch_gdr_prep(p, true, stream);
     if (e != hipSuccess) return e;
     if (p.nslots > 0) {
-        hipLaunchKernelGGL(kda_gdr_scan_kernel<true>, dim3(blocks), dim3(SCAN_THREADS), 0, stream, p);
+        hipLaunchKernelGGL(kda_gdr_keep_kernel, dim3(blocks), dim3(SCAN_THREADS), 0, stream, p);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     hipLaunchKernelGGL(kda_gdr_rscan_kernel, dim3(blocks), dim3(SCAN_THREADS), 0, stream, p);

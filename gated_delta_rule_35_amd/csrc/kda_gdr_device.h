@@ -79,6 +79,55 @@ __device__ __forceinline__ f32x4 mfma_split(const bf16x8 (&a)[NA], const Split<N
     return c;
 }
 
+// ---- fp16 operands ----
+__device__ __forceinline__ f32x4 mfma_h(half8 a, half8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+// Two accumulator tiles as B operand in fp16, and with PARTS = 2 what that leaves.
+template <int PARTS>
+struct HSplit {
+    half8 s[PARTS];
+};
+template <int PARTS>
+__device__ __forceinline__ HSplit<PARTS> hsplit(f32x4 a, f32x4 b) {
+    HSplit<PARTS> r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float x = i < 2 ? a[2 * i] : b[2 * i - 4], y = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
+        const half2v h = __builtin_convertvector(f32x2{x, y}, half2v);
+        r.s[0][2 * i] = h[0];
+        r.s[0][2 * i + 1] = h[1];
+        if (PARTS == 2) {
+            const half2v l = __builtin_convertvector(f32x2{fmaf((float)h[0], -1.f, x), fmaf((float)h[1], -1.f, y)}, half2v);
+            r.s[1][2 * i] = l[0];
+            r.s[1][2 * i + 1] = l[1];
+        }
+    }
+    return r;
+}
+// The power of two that divides a bf16 row's largest entry into [1, 2): the row lies in
+// lanes l, l + 16, l + 32, l + 48, 32 entries each.  0 where there is nothing to divide
+// (a row of zeros) or the largest is not finite.
+__device__ __forceinline__ float row_power(const bf16x8 (&x)[4]) {
+    typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+    u16x8 m = __builtin_bit_cast(u16x8, x[0]) & (uint16_t)0x7fff;
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+        m = __builtin_elementwise_max(m, (u16x8)(__builtin_bit_cast(u16x8, x[i]) & (uint16_t)0x7fff));
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t = max(t, (uint32_t)m[i]);
+    t = max(t, (uint32_t)__shfl_xor((int)t, 16));
+    t = max(t, (uint32_t)__shfl_xor((int)t, 32));
+    const uint32_t e = t >> 7;   // biased exponent
+    return e == 0 || e == 255 ? 0.f : __uint_as_float(min(e, 253u) << 23);
+}
+
+// Per-token rows of a record's numbers, in elements: e^G, e^{G_last - G}, beta,
+// e^{G_last}; forward also e^G 2^ek, 2^ek, scale 2^eq (2^ek, 2^eq: what the scan divides
+// the token's k and q by) and 2^ek again with 0 for a row of zeros.
+enum { SC_EG = 0, SC_GA = 64, SC_BE = 128, SC_EL = 192, SC_EGK = 256, SC_KS = 320, SC_QS = 384, SC_KP = 448 };
+
 // ---- swizzled [64][128] bf16 tiles in LDS: rows of 256 bytes, whose sixteen 16-byte
 // pieces are permuted by tsw(row), so that both an operand read (sixteen consecutive
 // rows at one piece) and a transposing read (four consecutive rows at four

@@ -1,0 +1,319 @@
+// The forward's walk over the chunks of the gated delta rule with one decay per head, on
+// gfx950 (MI355X).  With the prep kernel's T, A (fp16 fragments) and per-token numbers:
+//   x = beta (v - e^G K S),  u = T x,  o = scale (e^G Q S + A u)
+//   S <- e^{G_last} S + K^T (e^{G_last - G} u)
+//
+// Every product's right-hand side is a set of columns of S (value channels), and no
+// product mixes columns: a wave owns 16 of them for the whole sequence and needs nothing
+// from the others.  Its state is eight 16x16 accumulator tiles (32 registers a lane), and
+// since an accumulator tile holds what a lane needs as B operand, the whole chain of a
+// chunk stays in registers.  A work-group is four such waves (64 value channels) and four
+// that stage the next chunk's left-hand operands in LDS: k and q rows as fp16, v, T and A
+// by DMA; one barrier a chunk.  Tile t = 2 kk + h of the state holds key channel
+// 32 kk + 8 g + 4 h + r in row 4 g + r (g = lane / 16), so that the two tiles of a
+// 32-channel step list the lane's eight channels as they lie in K's rows.
+//
+// Precision.  All products run on v_mfma_f32_16x16x32_f16.  k and q rows enter divided by
+// a power of two that brings their largest entry into [1, 2): exact for entries down to
+// 2^-14 of that, and off by 2^-25 of it below.  S, x, u and T enter as two fp16 parts, 22
+// bits, so that the state keeps fp32's accuracy with two thirds of the matrix work of
+// three bf16 parts and a fifth of fp32 instructions'; what only reaches the bf16 output
+// (S in Q S, A, u in A u) enters as one part, eight times finer than o's own rounding.
+// fp16's range is met by two powers of two: `kap` for the (sequence, head), the size of
+// its first chunk's keys, by which S is divided, and one for each value channel (each
+// lane's column), which keeps its largest |S| / kap and |v| within [2^-2, 2^10]; it
+// changes rarely, when a chunk starts.
+#include "kda_gdr_device.h"
+
+namespace kda {
+
+namespace {
+
+constexpr int FT = 512;
+// One slot: K, Q tiles (fp16, swizzled), v's slice [64][64] bf16 (o's on the way out), T
+// and A fragments, per-token numbers.
+struct FL {
+    static constexpr int K = 0, Q = 16384, V = 32768, T = 40960, A = T + 2 * GDR_TRI, SC = A + GDR_TRI,
+                         BYTES = SC + FWD_ROWS * 256;
+};
+
+// Channel of row 4 g + r of state tile t.
+__device__ __forceinline__ int state_row(int t, int g, int r) { return 32 * (t >> 1) + 8 * g + 4 * (t & 1) + r; }
+// A operand (m, kk) of a tile: rows 16 m + jj, channels 32 kk + 8 g ..
+__device__ __forceinline__ half8 row_frag(const char* tile, int m, int kk, int g, int jj) {
+    return *reinterpret_cast<const half8*>(tile + tile_off(16 * m + jj, 4 * kk + g));
+}
+// A operand of the transposed tile: state tile t's channels, tokens of k step kk.
+__device__ __forceinline__ half8 col_frag(const char* tile, int t, int kk, int g, int jj) {
+    const int row = 32 * kk + 4 * g + (jj >> 2), piece = 4 * (t >> 1) + (jj & 3), b = 8 * (t & 1);
+    return __builtin_bit_cast(half8, join(lds_tr(tile + tile_off(row, piece) + b), lds_tr(tile + tile_off(row + 16, piece) + b)));
+}
+__device__ __forceinline__ constexpr int tri_frag(int m, int kk) { return m < 2 ? m : 2 * m - 2 + kk; }
+__device__ __forceinline__ f32x4 sc4(const float* sc, int row, int m, int g) {
+    return *reinterpret_cast<const f32x4*>(sc + row + 16 * m + 4 * g);
+}
+__device__ __forceinline__ float max_abs(float m, f32x4 x) {
+    return fmaxf(fmaxf(m, fmaxf(fabsf(x[0]), fabsf(x[1]))), fmaxf(fabsf(x[2]), fabsf(x[3])));
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
+    __shared__ __attribute__((aligned(1024))) char smem[2 * FL::BYTES];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int pair, sl;
+    pair_of_block((int)blockIdx.x, p.N * p.Hv, pair, sl);
+    const int n = pair / p.Hv, hv = pair % p.Hv, hq = hv / (p.Hv / p.Hq);
+    int64_t bos, len, row, slot0;
+    gdr_seq(p, n, bos, len, row, slot0);
+    const int nch = (int)((len + CH - 1) / CH);
+    auto rows_of = [&](int c) -> int {
+        const int64_t r = len - (int64_t)c * CH;
+        return r <= 0 ? 0 : (r >= CH ? CH : (int)r);
+    };
+    auto record = [&](int c) -> const char* { return p.rec + ((slot0 + c) * p.Hv + hv) * FWD_REC; };
+    // the largest power of two that the first chunk's keys are divided by
+    float kap = nch > 0 ? reinterpret_cast<const float*>(record(0) + FWD_SC)[SC_KP + lane] : 0.f;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) kap = fmaxf(kap, __shfl_xor(kap, m));
+    kap = kap > 0.f ? kap : 1.f;
+
+    if (wave >= 4) {
+        // ================= staging waves =================
+        const int w = wave - 4;
+        const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+        i32x4 kr[4], qr[4];   // rows 4 w + l / 16 (mod 16) of the next chunk: one 16-byte piece a lane
+        float kp, qp, sc[2];
+        // Rows 16 w + 4 x + lane / 16, piece lane % 16 of the next chunk's k and q, and (lane
+        // for token) what they are divided by; two of the eight rows of numbers.
+        auto fetch = [&](int c) {
+            const int ln = opaque(lane), rows = rows_of(c);
+            const int64_t tok = bos + (int64_t)c * CH;
+            const __amdgpu_buffer_rsrc_t rk =
+                chunk_rsrc(p.k.p + row * p.k.sb + tok * p.k.st + hq * p.k.sh, p.k.st, rows, DK);
+            const __amdgpu_buffer_rsrc_t rq =
+                chunk_rsrc(p.q.p + row * p.q.sb + tok * p.q.st + hq * p.q.sh, p.q.st, rows, DK);
+            const int r = 16 * w + (ln >> 4), b = 16 * (ln & 15);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                kr[x] = __builtin_amdgcn_raw_buffer_load_b128(rk, (int)((r + 4 * x) * p.k.st * 2) + b, 0, 0);
+                qr[x] = __builtin_amdgcn_raw_buffer_load_b128(rq, (int)((r + 4 * x) * p.q.st * 2) + b, 0, 0);
+            }
+            const float* s = reinterpret_cast<const float*>(record(c) + FWD_SC);
+            kp = s[SC_KS + ln];
+            qp = s[SC_QS + ln];
+            sc[0] = s[128 * w + ln];
+            sc[1] = s[128 * w + 64 + ln];
+        };
+        auto dma = [&](int c) {   // v, T and A
+            const int ln = opaque(lane);
+            const uint32_t to = lds + (c & 1) * FL::BYTES;
+            const __amdgpu_buffer_rsrc_t rv = chunk_rsrc(
+                p.v.p + row * p.v.sb + (bos + (int64_t)c * CH) * p.v.st + hv * p.v.sh + 64 * sl, p.v.st, rows_of(c), 64);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                dma_piece(rv, to + FL::V + (2 * w + u) * 1024,
+                          (int)((8 * (2 * w + u) + (ln >> 3)) * p.v.st * 2) + ((ln & 7) << 4));
+            const __amdgpu_buffer_rsrc_t rr = make_rsrc(record(c), FWD_SC);
+#pragma unroll
+            for (int u = 0; u < 5; ++u) {   // eighteen pieces
+                const int x = 4 * u + w;
+                if (x < 18) dma_piece(rr, to + FL::T + x * 1024, x * 1024 + ln * 16);
+            }
+        };
+        // 16 bytes of bf16 times `by` as fp16
+        auto to_half = [&](const i32x4& raw, float by) -> u32x4 {
+            u32x4 h;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t v = (uint32_t)raw[i];
+                h[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{bf_lo(v) * by, bf_hi(v) * by}, half2v));
+            }
+            return h;
+        };
+        auto stage = [&](int c) {
+            const int ln = opaque(lane), r = 16 * w + (ln >> 4);
+            char* to = smem + (c & 1) * FL::BYTES;
+            float* out = reinterpret_cast<float*>(to + FL::SC);
+            const float kinv = 1.f / kp, qinv = p.scale / qp;   // powers of two (qp holds scale 2^eq)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int at = tile_off(r + 4 * x, ln & 15);
+                *reinterpret_cast<u32x4*>(to + FL::K + at) = to_half(kr[x], __shfl(kinv, r + 4 * x));
+                *reinterpret_cast<u32x4*>(to + FL::Q + at) = to_half(qr[x], __shfl(qinv, r + 4 * x));
+            }
+            // e^G 2^ek kap and 2^ek / kap (rows 4 and 5: wave 2)
+            out[128 * w + ln] = sc[0] * (w == 2 ? kap : 1.f);
+            out[128 * w + 64 + ln] = sc[1] * (w == 2 ? 1.f / kap : 1.f);
+        };
+        if (nch > 0) {
+            dma(0);
+            fetch(0);
+            stage(0);
+            if (nch > 1) fetch(1);
+        }
+        for (int c = 0; c < nch; ++c) {
+            // v, T and A of chunk c have landed; the twelve loads for chunk c + 1, issued later, may be on their way
+            if (c + 1 < nch) asm volatile("s_waitcnt vmcnt(12)" ::: "memory");
+            else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            lds_barrier();
+            if (c + 1 < nch) {
+                stage(c + 1);   // before the DMA: what it reads is the only thing it waits for
+                dma(c + 1);
+                if (c + 2 < nch) fetch(c + 2);
+            }
+        }
+        return;
+    }
+
+    // ================= scan waves =================
+    const int w = wave;
+    const int64_t so = ((int64_t)n * p.Hv + hv) * DK * DK + 64 * sl + 16 * w + (lane & 15);
+    f32x4 S[8];                     // the state times down / kap
+    float down = 1.f, up = 1.f;     // the lane's column: a power of two and its inverse
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[t][r] = p.h0 ? p.h0[so + state_row(t, lane >> 4, r) * DK] * (1.f / kap) : 0.f;
+    }
+    for (int c = 0; c < nch; ++c) {
+        lds_barrier();   // chunk c is in LDS, and the other slot's reads are done
+        const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
+        char* slot = smem + (c & 1) * FL::BYTES;
+        const char *tk = slot + FL::K, *tq = slot + FL::Q;
+        char* tv = slot + FL::V;
+        const float* sc = reinterpret_cast<const float*>(slot + FL::SC);
+        f32x4 v[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const u32x2 b = lds_tr(tv + (16 * m + 4 * g + (jj >> 2)) * 128 + 32 * w + 8 * (jj & 3));
+            v[m] = f32x4{bf_lo(b[0]), bf_hi(b[0]), bf_lo(b[1]), bf_hi(b[1])} * down;
+        }
+        float top = 0.f;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) top = max_abs(top, S[t]);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) top = max_abs(top, v[m]);
+        if (__any(top > 1024.f || (top < 0.25f && top > 0.f))) {
+            // columns whose largest value left [2^-2, 2^10] go back to [1, 2)
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            if (top > 1024.f || (top < 0.25f && top > 0.f)) {
+                int e = (int)(__float_as_uint(top) >> 23) - 127;   // its exponent
+                const int was = 127 - (int)(__float_as_uint(down) >> 23);
+                e = max(-120 - was, min(120 - was, e));            // keep the power of two itself in range
+                const float by = __uint_as_float((uint32_t)(127 - max(-126, min(126, e))) << 23);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) S[t] *= by;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) v[m] *= by;
+                down *= by;
+                up = 1.f / down;
+            }
+        }
+        // x = beta (v - e^G K S) and e^G Q S
+        f32x4 x[4], o[4];
+        {
+            HSplit<2> sb[4];
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) sb[kk] = hsplit<2>(S[2 * kk], S[2 * kk + 1]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const half8 f = row_frag(tk, m, kk, g, jj);
+                    a = mfma_h(f, sb[kk].s[1], a);
+                    b = mfma_h(row_frag(tq, m, kk, g, jj), sb[kk].s[0], b);
+                    a = mfma_h(f, sb[kk].s[0], a);
+                }
+                x[m] = sc4(sc, SC_BE, m, g) * (v[m] - sc4(sc, SC_EGK, m, g) * a);
+                o[m] = sc4(sc, SC_EG, m, g) * b;
+            }
+        }
+        // u = T x, times 2^ek / kap
+        f32x4 u[4];
+        {
+            HSplit<2> xb[2];
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) xb[kk] = hsplit<2>(x[2 * kk], x[2 * kk + 1]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                f32x4 a = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int kk = 0; kk <= m / 2; ++kk) {
+                    const char* f = slot + FL::T + tri_frag(m, kk) * GDR_FRAG + ln * 16;
+                    const half8 th = *reinterpret_cast<const half8*>(f), tl = *reinterpret_cast<const half8*>(f + GDR_TRI);
+                    a = mfma_h(tl, xb[kk].s[0], a);
+                    a = mfma_h(th, xb[kk].s[1], a);
+                    a = mfma_h(th, xb[kk].s[0], a);
+                }
+                u[m] = a * sc4(sc, SC_KS, m, g);
+            }
+        }
+        // S <- e^{G_last} S + K^T (e^{G_last - G} u)
+        {
+            HSplit<2> wb[2];
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+                wb[kk] = hsplit<2>(sc4(sc, SC_GA, 2 * kk, g) * u[2 * kk], sc4(sc, SC_GA, 2 * kk + 1, g) * u[2 * kk + 1]);
+            const float el = sc[SC_EL];
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                f32x4 a = S[t] * el;
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    const half8 f = col_frag(tk, t, kk, g, jj);
+                    a = mfma_h(f, wb[kk].s[1], a);
+                    a = mfma_h(f, wb[kk].s[0], a);
+                }
+                S[t] = a;
+            }
+        }
+        // o, rounded once, through this wave's columns of v's slice
+        HSplit<1> ub[2];
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) ub[kk] = hsplit<1>(u[2 * kk], u[2 * kk + 1]);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+#pragma unroll
+            for (int kk = 0; kk <= m / 2; ++kk)
+                o[m] = mfma_h(*reinterpret_cast<const half8*>(slot + FL::A + tri_frag(m, kk) * GDR_FRAG + ln * 16),
+                              ub[kk].s[0], o[m]);
+            o[m] *= sc4(sc, SC_QS, m, g) * (up * kap);
+            const uint32_t p0 = pack_bf2(o[m][0], o[m][1]), p1 = pack_bf2(o[m][2], o[m][3]);
+            char* dst = tv + (16 * m + 4 * g) * 128 + 2 * (16 * w + jj);
+            *reinterpret_cast<uint16_t*>(dst) = (uint16_t)p0;
+            *reinterpret_cast<uint16_t*>(dst + 128) = (uint16_t)(p0 >> 16);
+            *reinterpret_cast<uint16_t*>(dst + 256) = (uint16_t)p1;
+            *reinterpret_cast<uint16_t*>(dst + 384) = (uint16_t)(p1 >> 16);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // this wave's columns of the slice
+        const int rows = rows_of(c);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int i = 32 * q + (ln >> 1);
+            const u32x4 y = *reinterpret_cast<const u32x4*>(tv + i * 128 + 32 * w + 16 * (ln & 1));
+            if (i < rows)
+                *reinterpret_cast<u32x4*>(p.o + ((row * p.T + bos + (int64_t)c * CH + i) * p.Hv + hv) * DK + 64 * sl +
+                                          16 * w + 8 * (ln & 1)) = y;
+        }
+    }
+    if (p.hT) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) p.hT[so + state_row(t, lane >> 4, r) * DK] = S[t][r] * (up * kap);
+        }
+    }
+}
+
+hipError_t launch_gdr_fwd(const GdrParams& p, hipStream_t stream) {
+    hipError_t e = launch_gdr_prep(p, false, stream);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kda_gdr_scan_kernel, dim3((unsigned)((int64_t)p.N * p.Hv * 2)), dim3(FT), 0, stream, p);
+    return hipGetLastError();
+}
+
+}  // namespace kda

@@ -14,8 +14,9 @@
 // then forms block column w downwards on v_mfma_f32_16x16x4f32,
 //   T_IJ = -T_II sum_{K=J}^{I-1} M_IK T_KJ,
 // with the T_KJ of its column in registers (an accumulator tile is the next product's
-// B operand).  The results leave as operand fragments in bf16 parts, T in three and
-// A in NA (two for the forward's bf16 output, three for the backward).
+// B operand).  T and A leave as operand fragments: for the backward in three bf16 parts
+// each; for the forward T in two fp16 parts and A in one, without the scale and divided
+// by the powers of two that the scan divides q's and k's rows by.
 // Fragment (m, kk) holds in lane l rows 16 m + l % 16, columns 32 kk + 16 (s / 4) +
 // 4 (l / 16) + s % 4, s < 8: the order in which accumulator tiles list a 32-wide k
 // step.  The lists hold (0,0) (1,0) (2,0) (2,1) (3,0) (3,1), zeros above the diagonal.
@@ -27,13 +28,14 @@ namespace {
 constexpr int SP = 68;   // row stride of the fp32 64x64 matrices (64 + 4: 16-byte aligned rows, spread banks)
 }
 
-template <int NA>
+template <bool BWD>
 __global__ void __launch_bounds__(256) kda_gdr_prep_kernel(const GdrParams p) {
     __shared__ __attribute__((aligned(16))) float sM[64 * SP];
     __shared__ __attribute__((aligned(16))) float sT[64 * SP];
     __shared__ __attribute__((aligned(16))) float sA[64 * SP];
     __shared__ GSum sG[64];
     __shared__ float sBeta[64];
+    __shared__ float sKp[64], sQp[64];
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, jj = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t slot = blockIdx.x / p.Hq;
@@ -44,6 +46,7 @@ __global__ void __launch_bounds__(256) kda_gdr_prep_kernel(const GdrParams p) {
 
     // raw products, tiles (w, J), J <= w: lane holds rows 16 w + 4 g + r of column 16 J + jj
     f32x4 qk[4], kk[4];
+    float kp = 0.f, qp = 0.f;   // forward: what the scan divides row 16 w + jj of k and q by (kp 0: a row of zeros)
     {
         const __amdgpu_buffer_rsrc_t rq =
             chunk_rsrc(p.q.p + row * p.q.sb + tok * p.q.st + hq * p.q.sh, p.q.st, rows, DK);
@@ -55,6 +58,10 @@ __global__ void __launch_bounds__(256) kda_gdr_prep_kernel(const GdrParams p) {
         for (int c = 0; c < 4; ++c) {
             aq[c] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rq, (16 * w + jj) * qst + 64 * c + 16 * g, 0, 0));
             ak[c] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rk, (16 * w + jj) * kst + 64 * c + 16 * g, 0, 0));
+        }
+        if (!BWD) {
+            kp = row_power(ak);
+            qp = row_power(aq);
         }
 #pragma unroll
         for (int J = 0; J < 4; ++J) {
@@ -70,6 +77,10 @@ __global__ void __launch_bounds__(256) kda_gdr_prep_kernel(const GdrParams p) {
             }
         }
     }
+    if (!BWD && g == 0) {
+        sKp[16 * w + jj] = kp;
+        sQp[16 * w + jj] = qp > 0.f ? qp : 1.f;
+    }
     // tiles above the diagonal that fragments cover
     for (int e = tid; e < 512; e += 256) {
         const int t = e >> 8, x = e & 255, at = (32 * t + (x >> 4)) * SP + 32 * t + 16 + (x & 15);
@@ -83,28 +94,38 @@ __global__ void __launch_bounds__(256) kda_gdr_prep_kernel(const GdrParams p) {
         if (w == 0) {
             const bool in = lane < rows;   // tokens past the end change nothing: g = 0, beta = 0
             sG[lane] = gate_sum(in ? p.g[gi + (int64_t)lane * p.Hv] : 0.f);
-            sBeta[lane] = in ? gdr_beta<NA == GDR_NA_BWD>(p, gi + (int64_t)lane * p.Hv) : 0.f;
+            sBeta[lane] = in ? gdr_beta<BWD>(p, gi + (int64_t)lane * p.Hv) : 0.f;
         }
         __syncthreads();
-        char* rec = p.rec + (slot * p.Hv + hv) * gdr_rec_bytes(NA);
+        char* rec = p.rec + (slot * p.Hv + hv) * (BWD ? GDR_REC : FWD_REC);
         if (w == 0) {
-            float* sc = reinterpret_cast<float*>(rec + GDR_SC);
+            float* sc = reinterpret_cast<float*>(rec + (BWD ? GDR_SC : FWD_SC)) + lane;
             const GSum G = sG[lane], GL = sG[63];
-            sc[lane] = gate_exp(G);
-            sc[64 + lane] = gate_ratio(GL, G);
-            sc[128 + lane] = sBeta[lane];
-            sc[192 + lane] = gate_exp(GL);
+            const float eg = gate_exp(G);
+            sc[SC_EG] = eg;
+            sc[SC_GA] = gate_ratio(GL, G);
+            sc[SC_BE] = sBeta[lane];
+            sc[SC_EL] = gate_exp(GL);
+            if (!BWD) {
+                const float ks = sKp[lane] > 0.f ? sKp[lane] : 1.f;
+                sc[SC_EGK] = eg * ks;
+                sc[SC_KS] = ks;
+                sc[SC_QS] = p.scale * sQp[lane];
+                sc[SC_KP] = sKp[lane];
+            }
         }
 #pragma unroll
         for (int J = 0; J < 4; ++J) {
             if (J <= w) {
                 const int j = 16 * J + jj;
                 const GSum Gj = sG[j];
+                const float kinv = BWD ? 1.f : 1.f / (sKp[j] > 0.f ? sKp[j] : 1.f);   // exact: powers of two
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int i = 16 * w + 4 * g + e;
                     const float gam = j <= i ? gate_ratio(sG[i], Gj) : 0.f;
-                    sA[i * SP + j] = j <= i ? p.scale * (qk[J][e] * gam) : 0.f;
+                    const float by = BWD ? p.scale : kinv * (1.f / sQp[i]);
+                    sA[i * SP + j] = j <= i ? by * (qk[J][e] * gam) : 0.f;
                     sM[i * SP + j] = j < i ? sBeta[i] * (kk[J][e] * gam) : 0.f;
                 }
             }
@@ -114,14 +135,18 @@ __global__ void __launch_bounds__(256) kda_gdr_prep_kernel(const GdrParams p) {
             const float* m = sM + 16 * w * SP + 16 * w;
             float x[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                x[i] = i == jj ? 1.f : 0.f;
+            for (int i = 0; i < 16; ++i) x[i] = i == jj ? 1.f : 0.f;
 #pragma unroll
-                for (int k4 = 0; k4 < i; k4 += 4) {
-                    const f32x4 a = *reinterpret_cast<const f32x4*>(m + i * SP + k4);
+            for (int kb = 0; kb < 4; ++kb) {   // four columns eliminated from the rows below them
+                f32x4 r4[16];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (k4 + e < i) x[i] = fmaf(-a[e], x[k4 + e], x[i]);
+                for (int i = 1; i < 16; ++i)
+                    if (i > 4 * kb) r4[i] = *reinterpret_cast<const f32x4*>(m + i * SP + 4 * kb);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                    for (int i = 1; i < 16; ++i)
+                        if (i > 4 * kb + e) x[i] = fmaf(-r4[i][e], x[4 * kb + e], x[i]);
                 }
             }
             if (lane < 16) {
@@ -167,23 +192,26 @@ __global__ void __launch_bounds__(256) kda_gdr_prep_kernel(const GdrParams p) {
             const int m = x < 2 ? x : 2 + ((x - 2) >> 1), c = x < 2 ? 0 : x & 1;   // (m, kk)
             const float* a = (which ? sA : sT) + (16 * m + jj) * SP + 32 * c + 4 * g;
             const f32x4 u0 = *reinterpret_cast<const f32x4*>(a), u1 = *reinterpret_cast<const f32x4*>(a + 16);
-            const Split<3> parts = split_acc<3>(u0, u1);
-            char* dst = rec + (which ? GDR_A : GDR_T) + x * GDR_FRAG + lane * 16;
+            char* dst = rec + (which ? (BWD ? GDR_A : FWD_A) : (BWD ? GDR_T : FWD_T)) + x * GDR_FRAG + lane * 16;
+            if (BWD) {
+                const Split<3> parts = split_acc<3>(u0, u1);
 #pragma unroll
-            for (int n = 0; n < 3; ++n)
-                if (n < NA || !which) *reinterpret_cast<bf16x8*>(dst + n * GDR_TRI) = parts.s[n];
+                for (int n = 0; n < 3; ++n) *reinterpret_cast<bf16x8*>(dst + n * GDR_TRI) = parts.s[n];
+            } else {
+                const HSplit<2> parts = hsplit<2>(u0, u1);
+                *reinterpret_cast<half8*>(dst) = parts.s[0];
+                if (!which) *reinterpret_cast<half8*>(dst + GDR_TRI) = parts.s[1];
+            }
         }
         __syncthreads();   // the matrices' reads before the next value head's writes
     }
 }
 
-hipError_t launch_gdr_prep(const GdrParams& p, int na, hipStream_t stream) {
+hipError_t launch_gdr_prep(const GdrParams& p, bool bwd, hipStream_t stream) {
     const int64_t blocks = p.nslots * p.Hq;
     if (blocks == 0) return hipSuccess;
-    if (na == GDR_NA_FWD)
-        hipLaunchKernelGGL(kda_gdr_prep_kernel<GDR_NA_FWD>, dim3((unsigned)blocks), dim3(256), 0, stream, p);
-    else
-        hipLaunchKernelGGL(kda_gdr_prep_kernel<GDR_NA_BWD>, dim3((unsigned)blocks), dim3(256), 0, stream, p);
+    if (bwd) hipLaunchKernelGGL(kda_gdr_prep_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL(kda_gdr_prep_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 

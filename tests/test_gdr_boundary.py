@@ -123,7 +123,7 @@ def test_overlaps(lib):
 
 def test_workspaces(lib):
     need = lib.kda_gdr_fwd_workspace_size(100, 1, 4)
-    assert need == (2 + 1) * 4 * 31744
+    assert need == (2 + 1) * 4 * 20480
     assert fwd(lib, good(), size=need - 1) == "KDA_ERR_WORKSPACE"
     assert fwd(lib, good(), ws=FAKE + 8) == "KDA_ERR_WORKSPACE"
     need = lib.kda_gdr_bwd_workspace_size(100, 1, 4)

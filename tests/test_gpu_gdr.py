@@ -39,7 +39,7 @@ def check_forward(x, cu=None):
     torch.cuda.synchronize()
     o_ref, h_ref = ref.forward(x, SCALE, cu)
     assert torch.equal(torch.isnan(out.cpu()), torch.isnan(o_ref))   # rows in no sequence stay as they were
-    ref.assert_rows(out, o_ref, "o")
+    ref.assert_rows(out, o_ref, "o", half=ref.forward_magnitude(x, SCALE, cu))
     ref.assert_states(hT, h_ref, "final state")
     return out, hT
 
@@ -116,7 +116,8 @@ def test_backward_packed(lens, tail):
     check_backward(x, cu)
 
 
-@pytest.mark.parametrize("kind", ["keeps", "forgets", "resets", "no update", "wide values", "small values", "long keys"])
+@pytest.mark.parametrize("kind", ["keeps", "forgets", "resets", "no update", "wide values", "small values", "long keys",
+                                  "tiny keys", "tiny queries", "growing keys"])
 def test_gates_and_ranges(kind):
     """Log-decays of zero, strong ones, minus infinity between tokens, beta of zero, and
     values far from one."""
@@ -134,10 +135,39 @@ def test_gates_and_ranges(kind):
         x["v"] = (x["v"].float() * 3e6).bfloat16()
     elif kind == "small values":
         x["v"], x["h0"] = (x["v"].float() * 1e-9).bfloat16(), x["h0"] * 1e-9
-    else:
+    elif kind == "long keys":
         x["k"] = (x["k"].float() * 1.2).bfloat16()
+    elif kind == "tiny keys":
+        x["k"], x["h0"] = (x["k"].float() * 1e-7).bfloat16(), x["h0"] * 1e-7
+    elif kind == "tiny queries":
+        x["q"] = (x["q"].float() * 1e-20).bfloat16()
+    else:   # each token's key longer than the one before, 2^-8 to 1
+        x["k"] = (x["k"].float() * 2.0 ** torch.linspace(-8, 0, 150)[None, :, None, None]).bfloat16()
     check_forward(x)
     check_backward(x, with_state=kind != "wide values")
+
+
+def test_value_channels_are_independent():
+    """Value channels of sizes from 2^-60 to 2^60, changing from token to token block: every
+    channel keeps the accuracy that it has alone (all products are linear in it)."""
+    say("gdr_fwd with channels of all sizes")
+    x = ref.make(1, 333, 1, 2, h0=True, seed=23)
+    size = 2.0 ** torch.linspace(-60, 60, 128).round()[torch.randperm(128, generator=torch.Generator().manual_seed(5))]
+    y = dict(x, v=(x["v"].float() * size).bfloat16(), h0=x["h0"] * size)
+    d, e = ref.cuda(x), ref.cuda(y)
+    o, h = kda_gdr_fwd(*args(d), initial_state=d["h0"], final_state=True)
+    o2, h2 = kda_gdr_fwd(*args(e), initial_state=e["h0"], final_state=True)
+    torch.cuda.synchronize()
+    o_ref, h_ref = ref.forward(x, SCALE)
+    ref.assert_rows(o2.cpu().double() / size.double(), o_ref, "o", half=ref.forward_magnitude(x, SCALE))
+    ref.assert_states(h2.cpu().double() / size.double(), h_ref, "state")
+    # blocks of tokens that are large, then small, then large again
+    steps = 2.0 ** torch.tensor([0, 30, -30, 12, -20, 0]).repeat_interleave(64)[:333].double()
+    z = dict(x, v=(x["v"].double() * steps[None, :, None, None]).bfloat16(), g=x["g"] * 20)
+    check_forward(z)
+    for c in range(0, 333, 64):   # block by block, each against its own size
+        w = {n: (t[:, c:c + 64].contiguous() if n != "h0" else None) for n, t in z.items()}
+        check_forward(w)
 
 
 def test_correlated_keys():
@@ -399,7 +429,7 @@ def test_decode_continues_the_forward():
         outs.append(kda_gdr_decode(*args(one), S)[0][:, None])
     torch.cuda.synchronize()
     o_ref, h_ref = ref.forward(x, SCALE)
-    ref.assert_rows(torch.cat(outs, 1), o_ref, "o")
+    ref.assert_rows(torch.cat(outs, 1), o_ref, "o", half=ref.forward_magnitude(x, SCALE))
     ref.assert_states(S, h_ref, "state")
 
 

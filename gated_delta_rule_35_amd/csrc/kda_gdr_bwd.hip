@@ -103,9 +103,8 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_keep_kernel(const GdrPar
     __shared__ __attribute__((aligned(1024))) char smem[2 * L::BYTES];
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, jj = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int pair, sl;
-    pair_of_block((int)blockIdx.x, p.N * p.Hv, pair, sl);
-    const int n = pair / p.Hv, hv = pair % p.Hv, hq = hv / (p.Hv / p.Hq);
+    const Walk walk = walk_of_block(p, (int)blockIdx.x, reinterpret_cast<int*>(smem));
+    const int n = walk.n, hv = walk.hv, sl = walk.sl, hq = hv / (p.Hv / p.Hq);
     int64_t bos, len, row, slot0;
     gdr_seq(p, n, bos, len, row, slot0);
     const int nch = (int)((len + CH - 1) / CH);
@@ -223,9 +222,8 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_rscan_kernel(const GdrPa
     __shared__ __attribute__((aligned(1024))) char smem[2 * L::BYTES];
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, jj = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int pair, sl;
-    pair_of_block((int)blockIdx.x, p.N * p.Hv, pair, sl);
-    const int n = pair / p.Hv, hv = pair % p.Hv, hq = hv / (p.Hv / p.Hq);
+    const Walk walk = walk_of_block(p, (int)blockIdx.x, reinterpret_cast<int*>(smem));
+    const int n = walk.n, hv = walk.hv, sl = walk.sl, hq = hv / (p.Hv / p.Hq);
     int64_t bos, len, row, slot0;
     gdr_seq(p, n, bos, len, row, slot0);
     const int nch = (int)((len + CH - 1) / CH);

@@ -298,17 +298,47 @@ __device__ __forceinline__ float sum64(float x) {
     return x + __shfl_xor(x, 32);
 }
 
-// (sequence, value head) pair and dv slice of a work-group: work-groups are dealt to
-// the 8 XCDs round robin; each XCD takes a contiguous run of pairs with both slices,
-// so that the slices of a head and the value heads of a q/k head meet in one L2.
-__device__ __forceinline__ void pair_of_block(int b, int npairs, int& pair, int& sl) {
-    if ((npairs & 7) == 0) {
-        pair = (b & 7) * (npairs >> 3) + (b >> 4);
-        sl = (b >> 3) & 1;
+// The (sequence, value head, 64-wide slice of value channels) of a walk's work-group.
+// Work-groups start in order and are dealt to the 8 XCDs round robin.  An XCD takes an
+// eighth of the heads of every sequence, both slices of a head and a group's heads
+// together, so that they share k, q and the records in one L2.  Packed sequences are
+// taken longest first (ties in order), so that the last work-groups to start are short:
+// `sh` holds N + 1 words for that.  With more sequences than threads they keep their order.
+struct Walk {
+    int n, hv, sl;
+};
+__device__ __forceinline__ Walk walk_of_block(const GdrParams& p, int b, int* sh) {
+    Walk k;
+    if ((p.Hv & 7) == 0) {
+        const int per = p.Hv >> 3, rest = b >> 4;
+        k.sl = (b >> 3) & 1;
+        k.n = rest / per;
+        k.hv = (b & 7) * per + rest % per;
     } else {
-        pair = b >> 1;
-        sl = b & 1;
+        k.sl = b & 1;
+        k.n = (b >> 1) / p.Hv;
+        k.hv = (b >> 1) % p.Hv;
     }
+    if (p.cu && p.N > 1 && p.N <= (int)blockDim.x) {
+        const int t = threadIdx.x;
+        if (t < p.N) {
+            int64_t a = p.cu[t], e = p.cu[t + 1];
+            a = a < 0 ? 0 : (a > p.T ? p.T : a);
+            e = e < a ? a : (e > p.T ? p.T : e);
+            sh[1 + t] = (int)(e - a);
+        }
+        __syncthreads();
+        if (t < p.N) {
+            const int mine = sh[1 + t];
+            int rank = 0;
+            for (int m = 0; m < p.N; ++m) rank += sh[1 + m] > mine || (sh[1 + m] == mine && m < t);
+            if (rank == k.n) sh[0] = t;
+        }
+        __syncthreads();
+        k.n = __builtin_amdgcn_readfirstlane(sh[0]);
+        __syncthreads();   // read before the words are used for something else
+    }
+    return k;
 }
 
 }  // namespace kda

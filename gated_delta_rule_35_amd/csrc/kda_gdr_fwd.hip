@@ -52,8 +52,11 @@ __device__ __forceinline__ constexpr int tri_frag(int m, int kk) { return m < 2 
 __device__ __forceinline__ f32x4 sc4(const float* sc, int row, int m, int g) {
     return *reinterpret_cast<const f32x4*>(sc + row + 16 * m + 4 * g);
 }
+// max(m, |x|): the instructions themselves, since fmaxf first quiets every operand.
 __device__ __forceinline__ float max_abs(float m, f32x4 x) {
-    return fmaxf(fmaxf(m, fmaxf(fabsf(x[0]), fabsf(x[1]))), fmaxf(fabsf(x[2]), fabsf(x[3])));
+    asm("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(m) : "v"(x[0]), "v"(x[1]));
+    asm("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(m) : "v"(x[2]), "v"(x[3]));
+    return m;
 }
 
 }  // namespace
@@ -62,9 +65,8 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
     __shared__ __attribute__((aligned(1024))) char smem[2 * FL::BYTES];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int pair, sl;
-    pair_of_block((int)blockIdx.x, p.N * p.Hv, pair, sl);
-    const int n = pair / p.Hv, hv = pair % p.Hv, hq = hv / (p.Hv / p.Hq);
+    const Walk walk = walk_of_block(p, (int)blockIdx.x, reinterpret_cast<int*>(smem));
+    const int n = walk.n, hv = walk.hv, sl = walk.sl, hq = hv / (p.Hv / p.Hq);
     int64_t bos, len, row, slot0;
     gdr_seq(p, n, bos, len, row, slot0);
     const int nch = (int)((len + CH - 1) / CH);
@@ -153,17 +155,36 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
             stage(0);
             if (nch > 1) fetch(1);
         }
+        // o of chunk c (64 rows of 64 channels where v was): the rows whose place this wave's DMA takes next
+        auto store_o = [&](int c) {
+            const int ln = opaque(lane), rows = rows_of(c);
+            const char* tv = smem + (c & 1) * FL::BYTES + FL::V;
+            u32x4 y[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) y[u] = *reinterpret_cast<const u32x4*>(tv + (2 * w + u) * 1024 + ln * 16);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int i = 8 * (2 * w + u) + (ln >> 3);
+                if (i < rows)
+                    *reinterpret_cast<u32x4*>(p.o + ((row * p.T + bos + (int64_t)c * CH + i) * p.Hv + hv) * DK + 64 * sl +
+                                              8 * (ln & 7)) = y[u];
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        };
         for (int c = 0; c < nch; ++c) {
             // v, T and A of chunk c have landed; the twelve loads for chunk c + 1, issued later, may be on their way
             if (c + 1 < nch) asm volatile("s_waitcnt vmcnt(12)" ::: "memory");
             else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             lds_barrier();
+            if (c > 0) store_o(c - 1);
             if (c + 1 < nch) {
                 stage(c + 1);   // before the DMA: what it reads is the only thing it waits for
                 dma(c + 1);
                 if (c + 2 < nch) fetch(c + 2);
             }
         }
+        lds_barrier();
+        if (nch > 0) store_o(nch - 1);
         return;
     }
 
@@ -271,7 +292,7 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
                 S[t] = a;
             }
         }
-        // o, rounded once, through this wave's columns of v's slice
+        // o, rounded once, into this wave's columns of v's slice: the staging waves store it
         HSplit<1> ub[2];
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) ub[kk] = hsplit<1>(u[2 * kk], u[2 * kk + 1]);
@@ -289,17 +310,8 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
             *reinterpret_cast<uint16_t*>(dst + 256) = (uint16_t)p1;
             *reinterpret_cast<uint16_t*>(dst + 384) = (uint16_t)(p1 >> 16);
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // this wave's columns of the slice
-        const int rows = rows_of(c);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int i = 32 * q + (ln >> 1);
-            const u32x4 y = *reinterpret_cast<const u32x4*>(tv + i * 128 + 32 * w + 16 * (ln & 1));
-            if (i < rows)
-                *reinterpret_cast<u32x4*>(p.o + ((row * p.T + bos + (int64_t)c * CH + i) * p.Hv + hv) * DK + 64 * sl +
-                                          16 * w + 8 * (ln & 1)) = y;
-        }
     }
+    lds_barrier();   // the last chunk's o is complete
     if (p.hT) {
 #pragma unroll
         for (int t = 0; t < 8; ++t) {

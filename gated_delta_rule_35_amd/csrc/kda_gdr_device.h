@@ -215,7 +215,7 @@ __device__ __forceinline__ int gdr_chunk(const GdrParams& p, int64_t s, int64_t&
         }
         n = lo;
     } else {
-        n = (int)(s / p.nc);
+        n = (int)s / p.nc;
     }
     int64_t bos, len, slot0;
     gdr_seq(p, n, bos, len, row, slot0);

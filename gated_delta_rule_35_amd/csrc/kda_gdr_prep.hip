@@ -29,20 +29,26 @@ constexpr int SP = 68;   // row stride of the fp32 64x64 matrices (64 + 4: 16-by
 }
 
 template <bool BWD>
-__global__ void __launch_bounds__(256) kda_gdr_prep_kernel(const GdrParams p) {
-    __shared__ __attribute__((aligned(16))) float sM[64 * SP];
-    __shared__ __attribute__((aligned(16))) float sT[64 * SP];
+__global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p) {
+    __shared__ __attribute__((aligned(16))) float sM[64 * SP];   // M, then T in its place
     __shared__ __attribute__((aligned(16))) float sA[64 * SP];
     __shared__ GSum sG[64];
     __shared__ float sBeta[64];
     __shared__ float sKp[64], sQp[64];
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, jj = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t slot = blockIdx.x / p.Hq;
-    const int hq = blockIdx.x % p.Hq, R = p.Hv / p.Hq;
+    const int slot = (int)blockIdx.x / p.Hq, hq = (int)blockIdx.x % p.Hq, R = p.Hv / p.Hq;
     int64_t tok, row;
     const int rows = gdr_chunk(p, slot, tok, row);
     if (rows == 0) return;
+    // g and beta of the value head at hand, token = lane (wave 0); tokens past the end
+    // change nothing: g = 0, beta = 0
+    const int64_t gi = (row * p.T + tok + lane) * p.Hv + hq * R;
+    float gate = 0.f, beta = 0.f;
+    if (w == 0 && lane < rows) {
+        gate = p.g[gi];
+        beta = gdr_beta<BWD>(p, gi);
+    }
 
     // raw products, tiles (w, J), J <= w: lane holds rows 16 w + 4 g + r of column 16 J + jj
     f32x4 qk[4], kk[4];
@@ -84,20 +90,22 @@ __global__ void __launch_bounds__(256) kda_gdr_prep_kernel(const GdrParams p) {
     // tiles above the diagonal that fragments cover
     for (int e = tid; e < 512; e += 256) {
         const int t = e >> 8, x = e & 255, at = (32 * t + (x >> 4)) * SP + 32 * t + 16 + (x & 15);
-        sT[at] = 0.f;
+        sM[at] = 0.f;
         sA[at] = 0.f;
     }
 
     for (int r = 0; r < R; ++r) {
         const int hv = hq * R + r;
-        const int64_t gi = (row * p.T + tok) * p.Hv + hv;
         if (w == 0) {
-            const bool in = lane < rows;   // tokens past the end change nothing: g = 0, beta = 0
-            sG[lane] = gate_sum(in ? p.g[gi + (int64_t)lane * p.Hv] : 0.f);
-            sBeta[lane] = in ? gdr_beta<BWD>(p, gi + (int64_t)lane * p.Hv) : 0.f;
+            sG[lane] = gate_sum(gate);
+            sBeta[lane] = beta;
+            if (r + 1 < R && lane < rows) {
+                gate = p.g[gi + r + 1];
+                beta = gdr_beta<BWD>(p, gi + r + 1);
+            }
         }
         __syncthreads();
-        char* rec = p.rec + (slot * p.Hv + hv) * (BWD ? GDR_REC : FWD_REC);
+        char* rec = p.rec + ((int64_t)slot * p.Hv + hv) * (BWD ? GDR_REC : FWD_REC);
         if (w == 0) {
             float* sc = reinterpret_cast<float*>(rec + (BWD ? GDR_SC : FWD_SC)) + lane;
             const GSum G = sG[lane], GL = sG[63];
@@ -114,6 +122,8 @@ __global__ void __launch_bounds__(256) kda_gdr_prep_kernel(const GdrParams p) {
                 sc[SC_KP] = sKp[lane];
             }
         }
+        {
+            const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;   // formed anew: kept through the loop, addresses would spill
 #pragma unroll
         for (int J = 0; J < 4; ++J) {
             if (J <= w) {
@@ -130,14 +140,17 @@ __global__ void __launch_bounds__(256) kda_gdr_prep_kernel(const GdrParams p) {
                 }
             }
         }
-        __syncthreads();
-        {   // diagonal block w: lane column jj (lane groups repeat each other)
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // this wave's block row of M
+        {   // diagonal block w, in its place: lane column jj (lane groups repeat each other)
+            const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
             const float* m = sM + 16 * w * SP + 16 * w;
             float x[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] = i == jj ? 1.f : 0.f;
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb) {   // four columns eliminated from the rows below them
+                asm volatile("" : "+v"(x[15])::"memory");   // no earlier: all columns' loads at once would spill
                 f32x4 r4[16];
 #pragma unroll
                 for (int i = 1; i < 16; ++i)
@@ -149,16 +162,18 @@ __global__ void __launch_bounds__(256) kda_gdr_prep_kernel(const GdrParams p) {
                         if (i > 4 * kb + e) x[i] = fmaf(-r4[i][e], x[4 * kb + e], x[i]);
                 }
             }
-            if (lane < 16) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the block is read before it is overwritten
+            if (g == 0) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sT[(16 * w + i) * SP + 16 * w + jj] = x[i];
+                for (int i = 0; i < 16; ++i) sM[(16 * w + i) * SP + 16 * w + jj] = x[i];
             }
         }
         __syncthreads();
+        f32x4 t[4];
         {   // block column w downwards
-            f32x4 t[4];
+            const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) t[0][e] = sT[(16 * w + 4 * g + e) * SP + 16 * w + jj];
+            for (int e = 0; e < 4; ++e) t[0][e] = sM[(16 * w + 4 * g + e) * SP + 16 * w + jj];
 #pragma unroll
             for (int s = 1; s < 4; ++s) {   // row block I = w + s; t[n] is T_{w + n, w}
                 const int I = w + s;
@@ -174,25 +189,34 @@ __global__ void __launch_bounds__(256) kda_gdr_prep_kernel(const GdrParams p) {
                         y = __builtin_amdgcn_mfma_f32_16x16x4f32(a[3], t[n][3], y, 0, 0, 0);
                     }
                     x += y;
-                    const f32x4 a = *reinterpret_cast<const f32x4*>(sT + (16 * I + jj) * SP + 16 * I + 4 * g);
+                    const f32x4 a = *reinterpret_cast<const f32x4*>(sM + (16 * I + jj) * SP + 16 * I + 4 * g);
                     f32x4 z = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) z = __builtin_amdgcn_mfma_f32_16x16x4f32(-a[e], x[e], z, 0, 0, 0);
                     t[s] = z;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sT[(16 * I + 4 * g + e) * SP + 16 * w + jj] = z[e];
                 }
+            }
+        }
+        __syncthreads();   // M is read
+#pragma unroll
+        for (int s = 1; s < 4; ++s) {
+            const int I = w + s;
+            if (I < 4) {
+                const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sM[(16 * I + 4 * g + e) * SP + 16 * w + jj] = t[s][e];
             }
         }
         __syncthreads();
         // fragments: six of T's and six of A's, three to a wave
 #pragma unroll
         for (int f3 = 0; f3 < 3; ++f3) {
+            const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
             const int f = 4 * f3 + w, which = f >= 6, x = which ? f - 6 : f;
             const int m = x < 2 ? x : 2 + ((x - 2) >> 1), c = x < 2 ? 0 : x & 1;   // (m, kk)
-            const float* a = (which ? sA : sT) + (16 * m + jj) * SP + 32 * c + 4 * g;
+            const float* a = (which ? sA : sM) + (16 * m + jj) * SP + 32 * c + 4 * g;
             const f32x4 u0 = *reinterpret_cast<const f32x4*>(a), u1 = *reinterpret_cast<const f32x4*>(a + 16);
-            char* dst = rec + (which ? (BWD ? GDR_A : FWD_A) : (BWD ? GDR_T : FWD_T)) + x * GDR_FRAG + lane * 16;
+            char* dst = rec + (which ? (BWD ? GDR_A : FWD_A) : (BWD ? GDR_T : FWD_T)) + x * GDR_FRAG + ln * 16;
             if (BWD) {
                 const Split<3> parts = split_acc<3>(u0, u1);
 #pragma unroll

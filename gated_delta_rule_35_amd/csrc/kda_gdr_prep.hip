@@ -9,9 +9,9 @@
 // anchor and no decay is out of range.
 //
 // One 256-thread work-group per (chunk slot, q/k head) walks the group's value heads.
-// Wave w holds rows 16 w .. + 15: tiles (w, J <= w) of both products (at most 32
-// MFMAs).  T in fp32: wave w inverts the diagonal block w by forward substitution,
-// then forms block column w downwards on v_mfma_f32_16x16x4f32,
+// k and q come into LDS by DMA, where M and A go once the products are formed.  Wave w
+// takes the diagonal tile (w, w) of both and one or two of the six below.  T in fp32:
+// wave w inverts the diagonal block w by forward substitution, then forms block column w downwards on v_mfma_f32_16x16x4f32,
 //   T_IJ = -T_II sum_{K=J}^{I-1} M_IK T_KJ,
 // with the T_KJ of its column in registers (an accumulator tile is the next product's
 // B operand).  T and A leave as operand fragments: for the backward in three bf16 parts
@@ -30,12 +30,13 @@ constexpr int SP = 68;   // row stride of the fp32 64x64 matrices (64 + 4: 16-by
 
 template <bool BWD>
 __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p) {
-    __shared__ __attribute__((aligned(16))) float sM[64 * SP];   // M, then T in its place
-    __shared__ __attribute__((aligned(16))) float sA[64 * SP];
+    __shared__ __attribute__((aligned(1024))) float mats[2 * 64 * SP];
+    float *const sM = mats, *const sA = mats + 64 * SP;   // M, then T in its place; A
+    char *const tk = reinterpret_cast<char*>(mats), *const tq = tk + 16384;   // before them k and q
+    static_assert(2 * 64 * SP * 4 >= 2 * 16384, "k and q fit where M and A go");
     __shared__ GSum sG[64];
-    __shared__ float sBeta[64];
-    __shared__ float sKp[64], sQp[64];
-    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, jj = lane & 15;
+    __shared__ __attribute__((aligned(16))) float sBeta[64], sKp[64], sQp[64];
+    const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int slot = (int)blockIdx.x / p.Hq, hq = (int)blockIdx.x % p.Hq, R = p.Hv / p.Hq;
     int64_t tok, row;
@@ -50,43 +51,50 @@ __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p)
         beta = gdr_beta<BWD>(p, gi);
     }
 
-    // raw products, tiles (w, J), J <= w: lane holds rows 16 w + 4 g + r of column 16 J + jj
-    f32x4 qk[4], kk[4];
-    float kp = 0.f, qp = 0.f;   // forward: what the scan divides row 16 w + jj of k and q by (kp 0: a row of zeros)
     {
-        const __amdgpu_buffer_rsrc_t rq =
-            chunk_rsrc(p.q.p + row * p.q.sb + tok * p.q.st + hq * p.q.sh, p.q.st, rows, DK);
-        const __amdgpu_buffer_rsrc_t rk =
-            chunk_rsrc(p.k.p + row * p.k.sb + tok * p.k.st + hq * p.k.sh, p.k.st, rows, DK);
-        const int qst = (int)p.q.st * 2, kst = (int)p.k.st * 2;
-        bf16x8 aq[4], ak[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            aq[c] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rq, (16 * w + jj) * qst + 64 * c + 16 * g, 0, 0));
-            ak[c] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rk, (16 * w + jj) * kst + 64 * c + 16 * g, 0, 0));
+        const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(tk));
+        dma_tile(chunk_rsrc(p.k.p + row * p.k.sb + tok * p.k.st + hq * p.k.sh, p.k.st, rows, DK), lds, p.k.st, w, 4, lane);
+        dma_tile(chunk_rsrc(p.q.p + row * p.q.sb + tok * p.q.st + hq * p.q.sh, p.q.st, rows, DK), lds + 16384, p.q.st, w,
+                 4, lane);
+        if (w == 0) {
+            sG[lane] = gate_sum(gate);
+            sBeta[lane] = beta;
         }
-        if (!BWD) {
-            kp = row_power(ak);
-            qp = row_power(aq);
-        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+    }
+    // The wave's tiles (I, J): the diagonal one, then (1,0) (3,0) | (2,0) (3,1) | (2,1) | (3,2).
+    const int ti[3] = {w, w == 0 ? 1 : w == 3 ? 3 : 2, 3}, tj[3] = {w, w == 2 ? 1 : w == 3 ? 2 : 0, w};
+    const int nt = w < 2 ? 3 : 2;
+    f32x4 qk[3], kk[3];   // raw products: lane holds rows 16 I + 4 g + r of column 16 J + jj
+    {
+        const int g = lane >> 4, jj = lane & 15;
 #pragma unroll
-        for (int J = 0; J < 4; ++J) {
-            qk[J] = kk[J] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (J <= w) {
+        for (int x = 0; x < 3; ++x) {
+            qk[x] = kk[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (x >= nt) continue;
+            bf16x8 aq[4], ak[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const bf16x8 b = __builtin_bit_cast(
-                        bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rk, (16 * J + jj) * kst + 64 * c + 16 * g, 0, 0));
-                    qk[J] = mfma_bf(aq[c], b, qk[J]);
-                    kk[J] = mfma_bf(ak[c], b, kk[J]);
+            for (int c = 0; c < 4; ++c) {
+                aq[c] = lds_bf8(tq + tile_off(16 * ti[x] + jj, 4 * c + g));
+                ak[c] = lds_bf8(tk + tile_off(16 * ti[x] + jj, 4 * c + g));
+            }
+            if (!BWD && x == 0) {   // what the scan divides row 16 w + jj of k and q by (sKp 0: a row of zeros)
+                const float kp = row_power(ak), qp = row_power(aq);
+                if (g == 0) {
+                    sKp[16 * w + jj] = kp;
+                    sQp[16 * w + jj] = qp > 0.f ? qp : 1.f;
                 }
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const bf16x8 b = x == 0 ? ak[c] : lds_bf8(tk + tile_off(16 * tj[x] + jj, 4 * c + g));
+                qk[x] = mfma_bf(aq[c], b, qk[x]);
+                kk[x] = mfma_bf(ak[c], b, kk[x]);
             }
         }
     }
-    if (!BWD && g == 0) {
-        sKp[16 * w + jj] = kp;
-        sQp[16 * w + jj] = qp > 0.f ? qp : 1.f;
-    }
+    __syncthreads();   // k and q are read
     // tiles above the diagonal that fragments cover
     for (int e = tid; e < 512; e += 256) {
         const int t = e >> 8, x = e & 255, at = (32 * t + (x >> 4)) * SP + 32 * t + 16 + (x & 15);
@@ -97,14 +105,16 @@ __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p)
     for (int r = 0; r < R; ++r) {
         const int hv = hq * R + r;
         if (w == 0) {
-            sG[lane] = gate_sum(gate);
-            sBeta[lane] = beta;
+            if (r > 0) {
+                sG[lane] = gate_sum(gate);
+                sBeta[lane] = beta;
+            }
             if (r + 1 < R && lane < rows) {
                 gate = p.g[gi + r + 1];
                 beta = gdr_beta<BWD>(p, gi + r + 1);
             }
         }
-        __syncthreads();
+        if (r > 0) __syncthreads();
         char* rec = p.rec + ((int64_t)slot * p.Hv + hv) * (BWD ? GDR_REC : FWD_REC);
         if (w == 0) {
             float* sc = reinterpret_cast<float*>(rec + (BWD ? GDR_SC : FWD_SC)) + lane;
@@ -125,23 +135,27 @@ __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p)
         {
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;   // formed anew: kept through the loop, addresses would spill
 #pragma unroll
-        for (int J = 0; J < 4; ++J) {
-            if (J <= w) {
-                const int j = 16 * J + jj;
+        for (int x = 0; x < 3; ++x) {
+            if (x < nt) {
+                const int j = 16 * tj[x] + jj, i0 = 16 * ti[x] + 4 * g;
                 const GSum Gj = sG[j];
-                const float kinv = BWD ? 1.f : 1.f / (sKp[j] > 0.f ? sKp[j] : 1.f);   // exact: powers of two
+                const f32x4 be = *reinterpret_cast<const f32x4*>(sBeta + i0);
+                f32x4 by = f32x4{p.scale, p.scale, p.scale, p.scale};
+                if (!BWD) {   // exact: powers of two
+                    by = 1.f / *reinterpret_cast<const f32x4*>(sQp + i0);
+                    by *= 1.f / (sKp[j] > 0.f ? sKp[j] : 1.f);
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int i = 16 * w + 4 * g + e;
+                    const int i = i0 + e;
                     const float gam = j <= i ? gate_ratio(sG[i], Gj) : 0.f;
-                    const float by = BWD ? p.scale : kinv * (1.f / sQp[i]);
-                    sA[i * SP + j] = j <= i ? by * (qk[J][e] * gam) : 0.f;
-                    sM[i * SP + j] = j < i ? sBeta[i] * (kk[J][e] * gam) : 0.f;
+                    sA[i * SP + j] = j <= i ? by[e] * (qk[x][e] * gam) : 0.f;
+                    sM[i * SP + j] = j < i ? be[e] * (kk[x][e] * gam) : 0.f;
                 }
             }
         }
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // this wave's block row of M
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // this wave's tiles of M
         {   // diagonal block w, in its place: lane column jj (lane groups repeat each other)
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
             const float* m = sM + 16 * w * SP + 16 * w;

@@ -21,7 +21,10 @@
 // while the last products of this one run.  It holds the
 // chunk's do, u and dx (bf16 parts) and k, q in LDS; wave w owns channels 16 w .. + 15
 // of R1, R2, R3, dq and dk, so S and dS are read once and split once; the ten lower
-// 16x16 tiles of P and of E are dealt to the eight waves.  What dg depends on enters in
+// 16x16 tiles of P and of E are dealt to the eight waves.  Every product is formed
+// transposed (channels or the earlier token down, tokens across), so that a lane holds
+// one token and four channels: a dot over channels is four products in the lane and two
+// exchanges, per-token factors are one number, and results leave four at a time.  What dg depends on enters in
 // three bf16 parts (fp32's accuracy); P and E enter dq and dk, which are rounded to
 // bf16, in two.
 //   The kernel is bound by its reads: 64 KB each of S and dS and 32 KB each of u and dx
@@ -41,22 +44,40 @@ struct GL {
     static_assert(4 * PL <= 3 * 16384 && 2 * 64 * OS <= 3 * 16384, "overlays");
 };
 struct GShared {
-    GSum G[64];
+    float hi[64], lo[64];  // G
     float eg[64], ga[64], be[64], xu[64];   // xu: dx . u
     float z[8][64];        // the row dots of dG by wave (channel sixteenths)
     float row[20][16], col[20][16];   // row and column sums by tile: P (QK^T), then E (KK^T)
     float sd[8], ts[8];    // <S, dS> and sum gam k . R2 by wave
 };
 
-// The lane's 16 x 16 tile piece: tokens 16 m + 4 g + r of channel 16 w + jj.
+// Operand of channels 16 w + jj: tokens 16 m + 4 g + r, r < 4.
 __device__ __forceinline__ u32x2 chan_frag(const char* tile, int m, int w, int g, int jj) {
     return lds_tr(tile + tile_off(16 * m + 4 * g + (jj >> 2), 2 * w + ((jj & 3) >> 1)) + 8 * (jj & 1));
 }
-__device__ __forceinline__ bf16x8 row_frag(const char* tile, int m, int kk, int g, int jj) {
-    return lds_bf8(tile + tile_off(16 * m + jj, 4 * kk + g));
+// Channels 16 w + 4 g + e, e < 4, of token 16 m + jj.
+__device__ __forceinline__ f32x4 chan4(const char* tile, int m, int w, int g, int jj) {
+    const u32x2 x = *reinterpret_cast<const u32x2*>(tile + tile_off(16 * m + jj, 2 * w + (g >> 1)) + 8 * (g & 1));
+    return f32x4{bf_lo(x[0]), bf_hi(x[0]), bf_lo(x[1]), bf_hi(x[1])};
 }
-__device__ __forceinline__ f32x4 widen(u32x2 x) { return f32x4{bf_lo(x[0]), bf_hi(x[0]), bf_lo(x[1]), bf_hi(x[1])}; }
-// A operand (m, kk) of a 64x64 plane, and of its transpose.
+// c += A B, both in parts, without the products below 2^-24 of the leading one; small ones first.
+template <int NB>
+__device__ __forceinline__ f32x4 mfma_parts(const Split<3>& a, const bf16x8 (&b)[NB], f32x4 c) {
+#pragma unroll
+    for (int d = 2; d >= 0; --d) {
+#pragma unroll
+        for (int i = 0; i <= d; ++i)
+            if (d - i < NB) c = mfma_bf(a.s[i], b[d - i], c);
+    }
+    return c;
+}
+__device__ __forceinline__ float dot4(f32x4 a, f32x4 b) { return fmaf(a[0], b[0], fmaf(a[1], b[1], fmaf(a[2], b[2], a[3] * b[3]))); }
+// Sum over the four lane groups, in every one.
+__device__ __forceinline__ float sum_groups(float x) {
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
+}
+// Operand (m, kk) of a 64x64 plane: rows 16 m + jj, columns of k step kk; and of its transpose.
 __device__ __forceinline__ bf16x8 plane_row(const char* pl, int m, int kk, int g, int jj) {
     const char* a = pl + (16 * m + jj) * PS + 64 * kk + 8 * g;
     return join(*reinterpret_cast<const u32x2*>(a), *reinterpret_cast<const u32x2*>(a + 32));
@@ -153,7 +174,8 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
         if (w == 7) {
             const GSum G = gate_sum(gate);
             const GSum last = {__shfl(G.hi, 63), __shfl(G.lo, 63)};
-            sh.G[lane] = G;
+            sh.hi[lane] = G.hi;
+            sh.lo[lane] = G.lo;
             sh.eg[lane] = gate_exp(G);
             sh.ga[lane] = gate_ratio(last, G);
             sh.be[lane] = beta;
@@ -174,7 +196,7 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             }
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) sb[kk] = split_acc<3>(s[2 * kk], s[2 * kk + 1]);
-            f32x4 z[4];   // the lane's part of the row dots
+            float z[4];   // the lane's part of its tokens' row dots
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 f32x4 r1 = z4, r3 = z4;
@@ -185,26 +207,23 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
                     bf16x8 fx[3];
 #pragma unroll
                     for (int n = 0; n < 3; ++n) fx[n] = lds_bf8(smem + GL::X + n * 16384 + at);
-                    r1 = mfma_split<3>(fo, sb[kk], r1);
-                    r3 = mfma_split<3>(fx, sb[kk], r3);
+                    r1 = mfma_parts(sb[kk], fo, r1);
+                    r3 = mfma_parts(sb[kk], fx, r3);
                 }
-                const f32x4 eg = *reinterpret_cast<const f32x4*>(sh.eg + 16 * m + 4 * g);
-                const f32x4 be = *reinterpret_cast<const f32x4*>(sh.be + 16 * m + 4 * g);
-                r1 = (p.scale * eg) * r1;
-                r3 = (be * eg) * r3;
+                const float eg = sh.eg[16 * m + jj];
+                r1 *= p.scale * eg;
+                r3 *= sh.be[16 * m + jj] * eg;
                 dq[m] += r1;
                 dk[m] -= r3;
-                z[m] = widen(chan_frag(smem + GL::Q, m, w, g, jj)) * r1 -
-                       widen(chan_frag(smem + GL::K, m, w, g, jj)) * r3;
+                z[m] = dot4(chan4(smem + GL::Q, m, w, g, jj), r1) - dot4(chan4(smem + GL::K, m, w, g, jj), r3);
             }
 #pragma unroll
             for (int n = 0; n < 8; ++n) asm volatile("" : "+v"(ds[n]));   // dS's parts are formed after S's are done with
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) sb[kk] = split_acc<3>(ds[2 * kk], ds[2 * kk + 1]);
-            f32x4 ts = z4;
+            float ts = 0.f;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
                 f32x4 r2 = z4;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
@@ -212,23 +231,20 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
                     bf16x8 fu[3];
 #pragma unroll
                     for (int n = 0; n < 3; ++n) fu[n] = lds_bf8(smem + GL::U + n * 16384 + at);
-                    r2 = mfma_split<3>(fu, sb[kk], r2);
+                    r2 = mfma_parts(sb[kk], fu, r2);
                 }
-                r2 *= *reinterpret_cast<const f32x4*>(sh.ga + 16 * m + 4 * g);
+                r2 *= sh.ga[16 * m + jj];
                 dk[m] += r2;
-                r2 *= widen(chan_frag(smem + GL::K, m, w, g, jj));
-                ts += r2;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = sum16(z[m][e] - r2[e]);
-                    if (jj == 0) sh.z[w][16 * m + 4 * g + e] = x;
-                }
+                const float t = dot4(chan4(smem + GL::K, m, w, g, jj), r2);
+                ts += t;
+                z[m] = sum_groups(z[m] - t);
             }
-            const float t = sum64((ts[0] + ts[1]) + (ts[2] + ts[3]));
-            if (lane == 0) sh.ts[w] = t;
+            sh.z[w][lane] = g == 0 ? z[0] : g == 1 ? z[1] : g == 2 ? z[2] : z[3];   // group m writes tokens 16 m ..
+            ts = sum64(ts);
+            if (lane == 0) sh.ts[w] = ts;
         }
-        // lower tiles of P and E: wave w has tile w of both; tiles 8 and 9 of P go to
-        // waves 0 and 1, of E to waves 2 and 3
+        // lower tiles of P and E, transposed (lane: token i = 16 I + jj, j = 16 J + 4 g + e): wave w
+        // has tile w of both; tiles 8 and 9 of P go to waves 0 and 1, of E to waves 2 and 3
         f32x4 P[2], E[2];
         int ti[2], tj[2];
 #pragma unroll
@@ -239,89 +255,86 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             ti[x] = id >= 6 ? 3 : id >= 3 ? 2 : id >= 1 ? 1 : 0;
             tj[x] = id - ti[x] * (ti[x] + 1) / 2;
             P[x] = E[x] = z4;
-            const int j = 16 * tj[x] + jj;
+            const int i = 16 * ti[x] + jj, j0 = 16 * tj[x] + 4 * g;
             // row and column sums of a tile's entries below the diagonal
-            auto tile_sums = [&](f32x4 v, int id, int base) {
-                float cs = 0.f;
+            auto tile_sums = [&](f32x4 v, int id) {
+                f32x4 cs;
+                float rs = 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float y = j < 16 * ti[x] + 4 * g + e ? v[e] : 0.f, rs = sum16(y);
-                    cs += y;
-                    if (jj == 0) sh.row[base + id][4 * g + e] = rs;
+                    const float y = j0 + e < i ? v[e] : 0.f;
+                    rs += y;
+                    cs[e] = sum16(y);
                 }
-                cs += __shfl_xor(cs, 16);
-                cs += __shfl_xor(cs, 32);
-                if (g == 0) sh.col[base + id][jj] = cs;
+                rs = sum_groups(rs);
+                if (g == 0) sh.row[id][jj] = rs;
+                if (jj == 0) *reinterpret_cast<f32x4*>(&sh.col[id][4 * g]) = cs;
             };
-            const GSum Gj = sh.G[j];
             f32x4 gam;
+            if (hasP || hasE) {
+                const GSum Gi = {sh.hi[i], sh.lo[i]};
+                const f32x4 hj = *reinterpret_cast<const f32x4*>(sh.hi + j0), lj = *reinterpret_cast<const f32x4*>(sh.lo + j0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = 16 * ti[x] + 4 * g + e;
-                gam[e] = j <= i ? gate_ratio(sh.G[i], Gj) : 0.f;
+                for (int e = 0; e < 4; ++e) gam[e] = j0 + e <= i ? gate_ratio(Gi, GSum{hj[e], lj[e]}) : 0.f;
             }
             if (hasP) {
                 f32x4 a = z4, qk = z4;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                     const int ai = tile_off(16 * ti[x] + jj, 4 * kk + g), aj = tile_off(16 * tj[x] + jj, 4 * kk + g);
-                    const Split<3> ub = {{lds_bf8(smem + GL::U + aj), lds_bf8(smem + GL::U + 16384 + aj),
+                    const Split<3> ua = {{lds_bf8(smem + GL::U + aj), lds_bf8(smem + GL::U + 16384 + aj),
                                           lds_bf8(smem + GL::U + 32768 + aj)}};
                     const bf16x8 fo[1] = {lds_bf8(smem + GL::DO + ai)};
-                    a = mfma_split<3>(fo, ub, a);
-                    qk = mfma_bf(lds_bf8(smem + GL::Q + ai), lds_bf8(smem + GL::K + aj), qk);
+                    a = mfma_parts(ua, fo, a);
+                    qk = mfma_bf(lds_bf8(smem + GL::K + aj), lds_bf8(smem + GL::Q + ai), qk);
                 }
+                // what lies above the diagonal stays out, NaN and infinity too
 #pragma unroll
-                for (int e = 0; e < 4; ++e) P[x][e] = j <= 16 * ti[x] + 4 * g + e ? p.scale * (gam[e] * a[e]) : 0.f;
-                tile_sums(P[x] * qk, id, 0);
+                for (int e = 0; e < 4; ++e) P[x][e] = j0 + e <= i ? p.scale * (gam[e] * a[e]) : 0.f;
+                tile_sums(P[x] * qk, id);
             }
             if (hasE) {
                 f32x4 a = z4, kk2 = z4;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                     const int ai = tile_off(16 * ti[x] + jj, 4 * kk + g), aj = tile_off(16 * tj[x] + jj, 4 * kk + g);
-                    Split<3> ub;
+                    Split<3> ua;
                     bf16x8 fx[3];
 #pragma unroll
                     for (int n = 0; n < 3; ++n) {
-                        ub.s[n] = lds_bf8(smem + GL::U + n * 16384 + aj);
+                        ua.s[n] = lds_bf8(smem + GL::U + n * 16384 + aj);
                         fx[n] = lds_bf8(smem + GL::X + n * 16384 + ai);
                     }
-                    a = mfma_split<3>(fx, ub, a);
-                    kk2 = mfma_bf(lds_bf8(smem + GL::K + ai), lds_bf8(smem + GL::K + aj), kk2);
+                    a = mfma_parts(ua, fx, a);
+                    kk2 = mfma_bf(lds_bf8(smem + GL::K + aj), lds_bf8(smem + GL::K + ai), kk2);
                 }
-                const f32x4 be = *reinterpret_cast<const f32x4*>(sh.be + 16 * ti[x] + 4 * g);
+                const float be = sh.be[i];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    E[x][e] = j < 16 * ti[x] + 4 * g + e ? -(be[e] * (gam[e] * a[e])) : 0.f;
-                tile_sums(E[x] * kk2, id, 10);
+                for (int e = 0; e < 4; ++e) E[x][e] = j0 + e < i ? -(be * (gam[e] * a[e])) : 0.f;
+                tile_sums(E[x] * kk2, 10 + id);
             }
         }
         lds_barrier();   // u's parts read; the sums complete
         // P and E as row-major planes of two bf16 parts
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const bool hasP = x == 0 || w < 2, hasE = x == 0 || (w >> 1) == 1;
+        {
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int at = (16 * ti[x] + 4 * g + e) * PS + 2 * (16 * tj[x] + jj);
-                const uint32_t h = pack_bf2(P[x][e], E[x][e]);
-                const uint32_t l = pack_bf2(P[x][e] - bf_lo(h), E[x][e] - bf_hi(h));
-                if (hasP) {
-                    *reinterpret_cast<uint16_t*>(smem + GL::U + at) = (uint16_t)h;
-                    *reinterpret_cast<uint16_t*>(smem + GL::U + GL::PL + at) = (uint16_t)l;
-                }
-                if (hasE) {
-                    *reinterpret_cast<uint16_t*>(smem + GL::U + 2 * GL::PL + at) = (uint16_t)(h >> 16);
-                    *reinterpret_cast<uint16_t*>(smem + GL::U + 3 * GL::PL + at) = (uint16_t)(l >> 16);
-                }
+            for (int x = 0; x < 2; ++x) {
+                const bool hasP = x == 0 || w < 2, hasE = x == 0 || (w >> 1) == 1;
+                char* to = smem + GL::U + (16 * ti[x] + jj) * PS + 2 * (16 * tj[x] + 4 * g);
+                auto put = [&](f32x4 v, char* to) {
+                    const uint32_t h0 = pack_bf2(v[0], v[1]), h1 = pack_bf2(v[2], v[3]);
+                    *reinterpret_cast<u32x2*>(to) = u32x2{h0, h1};
+                    *reinterpret_cast<u32x2*>(to + GL::PL) =
+                        u32x2{pack_bf2(v[0] - bf_lo(h0), v[1] - bf_hi(h0)), pack_bf2(v[2] - bf_lo(h1), v[3] - bf_hi(h1))};
+                };
+                if (hasP) put(P[x], to);
+                if (hasE) put(E[x], to + 2 * GL::PL);
             }
-        }
-        for (int e = tid; e < 2048; e += GT) {   // the tiles above the diagonal that operands cover
-            const int x = e & 255, t = (e >> 8) & 1;
-            *reinterpret_cast<uint16_t*>(smem + GL::U + (e >> 9) * GL::PL + (32 * t + (x >> 4)) * PS +
-                                         2 * (32 * t + 16 + (x & 15))) = 0;
+            // the tiles above the diagonal that operands cover: 8 bytes a thread
+            const int e = opaque(tid), t = (e >> 6) & 1;
+            *reinterpret_cast<u32x2*>(smem + GL::U + (e >> 7) * GL::PL + (32 * t + ((e >> 2) & 15)) * PS +
+                                      2 * (32 * t + 16 + 4 * (e & 3))) = u32x2{0, 0};
         }
         if (w == 7) {   // dg and dbeta
             const int i = lane, I = i >> 4;
@@ -380,12 +393,12 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
 #pragma unroll
                     for (int kk = 0; kk < 2; ++kk) {
                         if (kk <= m / 2) {
-                            dq[m] = mfma_bf(plane_row(pp, m, kk, g, jj), kb[kk], dq[m]);
-                            dk[m] = mfma_bf(plane_row(pe, m, kk, g, jj), kb[kk], dk[m]);
+                            dq[m] = mfma_bf(kb[kk], plane_row(pp, m, kk, g, jj), dq[m]);
+                            dk[m] = mfma_bf(kb[kk], plane_row(pe, m, kk, g, jj), dk[m]);
                         }
                         if (kk >= m / 2) {
-                            dk[m] = mfma_bf(plane_col(pp, m, kk, g, jj), qb[kk], dk[m]);
-                            dk[m] = mfma_bf(plane_col(pe, m, kk, g, jj), kb[kk], dk[m]);
+                            dk[m] = mfma_bf(qb[kk], plane_col(pp, m, kk, g, jj), dk[m]);
+                            dk[m] = mfma_bf(kb[kk], plane_col(pe, m, kk, g, jj), dk[m]);
                         }
                     }
                 }
@@ -395,13 +408,9 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t h = pack_bf2(dq[m][e], dk[m][e]);
-                    const int at = (16 * m + 4 * g + e) * GL::OS + 2 * (16 * w + jj);
-                    *reinterpret_cast<uint16_t*>(smem + GL::OUT + at) = (uint16_t)h;
-                    *reinterpret_cast<uint16_t*>(smem + GL::OUT + 64 * GL::OS + at) = (uint16_t)(h >> 16);
-                }
+                char* to = smem + GL::OUT + (16 * m + jj) * GL::OS + 2 * (16 * w + 4 * g);
+                *reinterpret_cast<u32x2*>(to) = u32x2{pack_bf2(dq[m][0], dq[m][1]), pack_bf2(dq[m][2], dq[m][3])};
+                *reinterpret_cast<u32x2*>(to + 64 * GL::OS) = u32x2{pack_bf2(dk[m][0], dk[m][1]), pack_bf2(dk[m][2], dk[m][3])};
                 dq[m] = dk[m] = z4;
             }
         }

@@ -17,8 +17,8 @@
 //
 // One 512-thread work-group per compute unit takes items (chunk slot, q/k head), walks
 // the group's value heads and sums their dq and dk in registers (so the sum's order is
-// fixed); the next unit's S, dS, u and dx are loaded into registers, its do into LDS,
-// while the last products of this one run.  It holds the
+// fixed); the next unit's S, u and dx are loaded into registers, its do into LDS, while
+// the last products of this one run, and dS while S's do.  It holds the
 // chunk's do, u and dx (bf16 parts) and k, q in LDS; wave w owns channels 16 w .. + 15
 // of R1, R2, R3, dq and dk, so S and dS are read once and split once; the ten lower
 // 16x16 tiles of P and of E are dealt to the eight waves.  Every product is formed
@@ -29,6 +29,8 @@
 // bf16, in two.
 //   The kernel is bound by its reads: 64 KB each of S and dS and 32 KB each of u and dx
 // per chunk and value head.
+#include <type_traits>
+
 #include "kda_gdr_device.h"
 
 namespace kda {
@@ -108,10 +110,17 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             if (rows) break;
         }
     };
-    f32x4 u[4], x[4], s[8], ds[8];
+    f32x4 u[4], x[4], s[8];
     float gate = 0.f, beta = 0.f;
-    auto fetch = [&]() {   // the unit's fp32 inputs into registers
-        const int t = opaque(tid), ln = t & 63, g = ln >> 4, jj = ln & 15;
+    // the unit's fp32 inputs into registers
+    auto fetch_state = [&](const float* from, f32x4 (&to)[8]) {
+        const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
+        const float* at = from + (slot * p.Hv + hq * R + r) * DK * DK + (16 * w + jj) * DK + 8 * g;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) to[n] = *reinterpret_cast<const f32x4*>(at + 32 * (n >> 1) + 4 * (n & 1));
+    };
+    auto fetch_tokens = [&]() {
+        const int t = opaque(tid), lane = t & 63;
         const int64_t unit = slot * p.Hv + hq * R + r;
         if (w == 7) {
             const int64_t gi = (row * p.T + tok + lane) * p.Hv + hq * R + r;
@@ -127,12 +136,6 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
                 x[2 * h + n] = *reinterpret_cast<const f32x4*>(p.dx + at + 4 * n);
             }
         }
-        const int64_t at = unit * DK * DK + (16 * w + jj) * DK + 8 * g;
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            s[n] = *reinterpret_cast<const f32x4*>(p.S + at + 32 * (n >> 1) + 4 * (n & 1));
-            ds[n] = *reinterpret_cast<const f32x4*>(p.dS + at + 32 * (n >> 1) + 4 * (n & 1));
-        }
     };
     auto dma_do = [&]() {
         dma_tile(chunk_rsrc(p.dO.p + row * p.dO.sb + tok * p.dO.st + (hq * R + r) * p.dO.sh, p.dO.st, rows, DK),
@@ -147,14 +150,17 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
     };
     find();
     if (item >= items) return;
-    fetch();
+    fetch_tokens();
     dma_do();
     dma_kq();
+    fetch_state(p.S, s);
     f32x4 dq[4], dk[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) dq[m] = dk[m] = z4;
 
     while (item < items) {
+        f32x4 ds[8];   // needed after S's products: in flight until then
+        fetch_state(p.dS, ds);
         // u and dx in three parts, and dx . u
         const int t = opaque(tid);
 #pragma unroll
@@ -180,20 +186,13 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             sh.ga[lane] = gate_ratio(last, G);
             sh.be[lane] = beta;
         }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's pieces of do, k and q
+        asm volatile("s_waitcnt vmcnt(8)" ::: "memory");   // this wave's pieces of do, k and q; dS may be on its way
         lds_barrier();
 
         // R1, R3, then R2, for channels 16 w + jj
         {
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
             Split<3> sb[4];
-            {
-                f32x4 d4 = z4;
-#pragma unroll
-                for (int n = 0; n < 8; ++n) d4 += s[n] * ds[n];
-                const float sd = sum64((d4[0] + d4[1]) + (d4[2] + d4[3]));
-                if (lane == 0) sh.sd[w] = sd;
-            }
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) sb[kk] = split_acc<3>(s[2 * kk], s[2 * kk + 1]);
             float z[4];   // the lane's part of its tokens' row dots
@@ -216,6 +215,13 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
                 dq[m] += r1;
                 dk[m] -= r3;
                 z[m] = dot4(chan4(smem + GL::Q, m, w, g, jj), r1) - dot4(chan4(smem + GL::K, m, w, g, jj), r3);
+            }
+            {
+                f32x4 d4 = z4;
+#pragma unroll
+                for (int n = 0; n < 8; ++n) d4 += s[n] * ds[n];
+                const float sd = sum64((d4[0] + d4[1]) + (d4[2] + d4[3]));
+                if (lane == 0) sh.sd[w] = sd;
             }
 #pragma unroll
             for (int n = 0; n < 8; ++n) asm volatile("" : "+v"(ds[n]));   // dS's parts are formed after S's are done with
@@ -243,94 +249,90 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             ts = sum64(ts);
             if (lane == 0) sh.ts[w] = ts;
         }
+        // the next unit, whose inputs are asked for bit by bit from here on: S now
+        const int rows0 = rows, hq0 = hq;
+        const int64_t tok0 = tok, row0 = row, gi0 = (row * p.T + tok) * p.Hv + hq * R + r;
+        const bool done = r == R - 1;   // the item's last value head
+        if (done) {
+            r = 0;
+            item += gridDim.x;
+            find();
+        } else {
+            ++r;
+        }
+        if (item < items) fetch_state(p.S, s);
         // lower tiles of P and E, transposed (lane: token i = 16 I + jj, j = 16 J + 4 g + e): wave w
         // has tile w of both; tiles 8 and 9 of P go to waves 0 and 1, of E to waves 2 and 3
-        f32x4 P[2], E[2];
-        int ti[2], tj[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        auto tile_rc = [&](int id, int& I, int& J) {
+            I = id >= 6 ? 3 : id >= 3 ? 2 : id >= 1 ? 1 : 0;
+            J = id - I * (I + 1) / 2;
+        };
+        // tile `id` of P, or of E, and the row and column sums of its entries below the diagonal
+        // times QK^T or KK^T
+        auto tile = [&](auto of_p, int id) -> f32x4 {
+            constexpr bool OF_P = decltype(of_p)::value;
+            int I, J;
+            tile_rc(id, I, J);
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
-            const int id = x == 0 ? w : 8 + (w & 1);
-            const bool hasP = x == 0 || w < 2, hasE = x == 0 || (w >> 1) == 1;
-            ti[x] = id >= 6 ? 3 : id >= 3 ? 2 : id >= 1 ? 1 : 0;
-            tj[x] = id - ti[x] * (ti[x] + 1) / 2;
-            P[x] = E[x] = z4;
-            const int i = 16 * ti[x] + jj, j0 = 16 * tj[x] + 4 * g;
-            // row and column sums of a tile's entries below the diagonal
-            auto tile_sums = [&](f32x4 v, int id) {
-                f32x4 cs;
-                float rs = 0.f;
+            const int i = 16 * I + jj, j0 = 16 * J + 4 * g;
+            f32x4 a = z4, raw = z4;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float y = j0 + e < i ? v[e] : 0.f;
-                    rs += y;
-                    cs[e] = sum16(y);
-                }
-                rs = sum_groups(rs);
-                if (g == 0) sh.row[id][jj] = rs;
-                if (jj == 0) *reinterpret_cast<f32x4*>(&sh.col[id][4 * g]) = cs;
-            };
-            f32x4 gam;
-            if (hasP || hasE) {
-                const GSum Gi = {sh.hi[i], sh.lo[i]};
-                const f32x4 hj = *reinterpret_cast<const f32x4*>(sh.hi + j0), lj = *reinterpret_cast<const f32x4*>(sh.lo + j0);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) gam[e] = j0 + e <= i ? gate_ratio(Gi, GSum{hj[e], lj[e]}) : 0.f;
-            }
-            if (hasP) {
-                f32x4 a = z4, qk = z4;
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    const int ai = tile_off(16 * ti[x] + jj, 4 * kk + g), aj = tile_off(16 * tj[x] + jj, 4 * kk + g);
-                    const Split<3> ua = {{lds_bf8(smem + GL::U + aj), lds_bf8(smem + GL::U + 16384 + aj),
-                                          lds_bf8(smem + GL::U + 32768 + aj)}};
+            for (int kk = 0; kk < 4; ++kk) {
+                if (kk == 2) asm volatile("" ::: "memory");   // two steps' operands at a time: more would spill
+                const int ai = tile_off(16 * I + jj, 4 * kk + g), aj = tile_off(16 * J + jj, 4 * kk + g);
+                const Split<3> ua = {{lds_bf8(smem + GL::U + aj), lds_bf8(smem + GL::U + 16384 + aj),
+                                      lds_bf8(smem + GL::U + 32768 + aj)}};
+                const bf16x8 kj = lds_bf8(smem + GL::K + aj);
+                if (OF_P) {
                     const bf16x8 fo[1] = {lds_bf8(smem + GL::DO + ai)};
                     a = mfma_parts(ua, fo, a);
-                    qk = mfma_bf(lds_bf8(smem + GL::K + aj), lds_bf8(smem + GL::Q + ai), qk);
-                }
-                // what lies above the diagonal stays out, NaN and infinity too
-#pragma unroll
-                for (int e = 0; e < 4; ++e) P[x][e] = j0 + e <= i ? p.scale * (gam[e] * a[e]) : 0.f;
-                tile_sums(P[x] * qk, id);
-            }
-            if (hasE) {
-                f32x4 a = z4, kk2 = z4;
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    const int ai = tile_off(16 * ti[x] + jj, 4 * kk + g), aj = tile_off(16 * tj[x] + jj, 4 * kk + g);
-                    Split<3> ua;
-                    bf16x8 fx[3];
-#pragma unroll
-                    for (int n = 0; n < 3; ++n) {
-                        ua.s[n] = lds_bf8(smem + GL::U + n * 16384 + aj);
-                        fx[n] = lds_bf8(smem + GL::X + n * 16384 + ai);
-                    }
+                    raw = mfma_bf(kj, lds_bf8(smem + GL::Q + ai), raw);
+                } else {
+                    const bf16x8 fx[3] = {lds_bf8(smem + GL::X + ai), lds_bf8(smem + GL::X + 16384 + ai),
+                                          lds_bf8(smem + GL::X + 32768 + ai)};
                     a = mfma_parts(ua, fx, a);
-                    kk2 = mfma_bf(lds_bf8(smem + GL::K + aj), lds_bf8(smem + GL::K + ai), kk2);
+                    raw = mfma_bf(kj, lds_bf8(smem + GL::K + ai), raw);
                 }
-                const float be = sh.be[i];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) E[x][e] = j0 + e < i ? -(be * (gam[e] * a[e])) : 0.f;
-                tile_sums(E[x] * kk2, 10 + id);
             }
-        }
+            const GSum Gi = {sh.hi[i], sh.lo[i]};
+            const f32x4 hj = *reinterpret_cast<const f32x4*>(sh.hi + j0), lj = *reinterpret_cast<const f32x4*>(sh.lo + j0);
+            const float by = OF_P ? p.scale : -sh.be[i];
+            f32x4 v, cs;
+            float rs = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {   // what lies above the diagonal stays out, NaN and infinity too
+                v[e] = j0 + e < i + OF_P ? by * (gate_ratio(Gi, GSum{hj[e], lj[e]}) * a[e]) : 0.f;
+                const float y = j0 + e < i ? v[e] * raw[e] : 0.f;
+                rs += y;
+                cs[e] = sum16(y);
+            }
+            rs = sum_groups(rs);
+            const int at = OF_P ? id : 10 + id;
+            if (g == 0) sh.row[at][jj] = rs;
+            if (jj == 0) *reinterpret_cast<f32x4*>(&sh.col[at][4 * g]) = cs;
+            return v;
+        };
+        const f32x4 P = tile(std::true_type{}, w), E = tile(std::false_type{}, w);
+        f32x4 Z = z4;
+        if (w < 2) Z = tile(std::true_type{}, 8 + w);
+        else if (w < 4) Z = tile(std::false_type{}, 6 + w);
         lds_barrier();   // u's parts read; the sums complete
         // P and E as row-major planes of two bf16 parts
         {
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const bool hasP = x == 0 || w < 2, hasE = x == 0 || (w >> 1) == 1;
-                char* to = smem + GL::U + (16 * ti[x] + jj) * PS + 2 * (16 * tj[x] + 4 * g);
-                auto put = [&](f32x4 v, char* to) {
-                    const uint32_t h0 = pack_bf2(v[0], v[1]), h1 = pack_bf2(v[2], v[3]);
-                    *reinterpret_cast<u32x2*>(to) = u32x2{h0, h1};
-                    *reinterpret_cast<u32x2*>(to + GL::PL) =
-                        u32x2{pack_bf2(v[0] - bf_lo(h0), v[1] - bf_hi(h0)), pack_bf2(v[2] - bf_lo(h1), v[3] - bf_hi(h1))};
-                };
-                if (hasP) put(P[x], to);
-                if (hasE) put(E[x], to + 2 * GL::PL);
-            }
+            auto put = [&](f32x4 v, int id, int part) {
+                int I, J;
+                tile_rc(id, I, J);
+                char* to = smem + GL::U + part * GL::PL + (16 * I + jj) * PS + 2 * (16 * J + 4 * g);
+                const uint32_t h0 = pack_bf2(v[0], v[1]), h1 = pack_bf2(v[2], v[3]);
+                *reinterpret_cast<u32x2*>(to) = u32x2{h0, h1};
+                *reinterpret_cast<u32x2*>(to + GL::PL) =
+                    u32x2{pack_bf2(v[0] - bf_lo(h0), v[1] - bf_hi(h0)), pack_bf2(v[2] - bf_lo(h1), v[3] - bf_hi(h1))};
+            };
+            put(P, w, 0);
+            put(E, w, 2);
+            if (w < 2) put(Z, 8 + w, 0);
+            else if (w < 4) put(Z, 6 + w, 2);
             // the tiles above the diagonal that operands cover: 8 bytes a thread
             const int e = opaque(tid), t = (e >> 6) & 1;
             *reinterpret_cast<u32x2*>(smem + GL::U + (e >> 7) * GL::PL + (32 * t + ((e >> 2) & 15)) * PS +
@@ -338,7 +340,7 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
         }
         if (w == 7) {   // dg and dbeta
             const int i = lane, I = i >> 4;
-            const int64_t gi = (row * p.T + tok + i) * p.Hv + hq * R + r;
+            const int64_t gi = gi0 + (int64_t)i * p.Hv;
             double dG = 0.0, last = 0.0;
             float sd = 0.f;
 #pragma unroll
@@ -355,24 +357,13 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             }
             last += (double)(sh.eg[63] * sd);
             const double sum = prefix64(dG), rest = lane_f64(sum, 63) - sum + dG;
-            if (i < rows) {
+            if (i < rows0) {
                 p.dg[gi] = (float)(rest + last);
                 p.dbeta[gi] = sh.xu[i] / sh.be[i];
             }
         }
-        // the next unit's inputs, in flight from here on
-        const int rows0 = rows, hq0 = hq;
-        const int64_t tok0 = tok, row0 = row;
-        const bool done = r == R - 1;   // the item's last value head
-        if (done) {
-            r = 0;
-            item += gridDim.x;
-            find();
-        } else {
-            ++r;
-        }
         if (item < items) {
-            fetch();
+            fetch_tokens();
             dma_do();
         }
         lds_barrier();

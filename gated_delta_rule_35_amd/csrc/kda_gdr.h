@@ -40,6 +40,9 @@ struct GdrParams {
 // Chunk records of the prep kernel (see kda_gdr_prep.hip): triangular operands as lists
 // of six 1 KB fragments per part, and rows of 64 per-token numbers (fp32).
 constexpr int GDR_FRAG = 1024;
+// Place of lane l's 16 bytes in a fragment that is also read transposed: the sixteen lanes of
+// a group four apart from the group's before, else such a read meets each bank four times.
+__host__ __device__ constexpr int frag_piece(int l) { return 16 * (l ^ ((l >> 4) << 2)); }
 constexpr int GDR_TRI = 6 * GDR_FRAG;              // one part of a triangular operand
 // Forward, fp16: T in two parts, A in one, the per-token rows.
 constexpr int FWD_T = 0, FWD_A = 2 * GDR_TRI, FWD_SC = 3 * GDR_TRI, FWD_ROWS = 8, FWD_REC = FWD_SC + FWD_ROWS * 256;

@@ -52,23 +52,127 @@ __device__ __forceinline__ f32x4 widen(u32x2 x) { return f32x4{bf_lo(x[0]), bf_h
 __device__ __forceinline__ constexpr int tri_frag(int m, int kk) { return m < 2 ? m : 2 * m - 2 + kk; }
 // Fragment (m, kk) of the transposed matrix (rows 16 m + jj, k step kk), kk >= m / 2.
 __device__ __forceinline__ bf16x8 tri_col_frag(const char* part, int m, int kk, int g, int jj) {
-    const int at = (jj & 3) * 256 + (4 * g + (jj >> 2)) * 16 + 8 * (m & 1);
+    const int at = frag_piece(16 * (jj & 3) + 4 * g + (jj >> 2)) + 8 * (m & 1);
     return join(lds_tr(part + tri_frag(2 * kk, m >> 1) * GDR_FRAG + at),
                 lds_tr(part + tri_frag(2 * kk + 1, m >> 1) * GDR_FRAG + at));
 }
 
+// The order of a stretch of code that ends here: after each of N matrix instructions up to
+// VALU vector instructions, DS reads of LDS and VM stores.  Left to itself the compiler
+// forms one tile after the other, each a chain of dependent matrix instructions that waits
+// for its operands in between.
+template <int N, int VALU, int DS, int VM>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (VALU) __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+        if (DS) __builtin_amdgcn_sched_group_barrier(0x100, DS, 0);
+        if (VM) __builtin_amdgcn_sched_group_barrier(0x040, VM, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// a[m] = rows 16 m .. of the tile times S, four tiles side by side, while the next step's
+// operands are read and split; S is stored first, by all waves at once (two waves make up a
+// 128-byte line): spread over the products, the stores cost the keeping walk at B=2 H=64
+// T=8192 580 us for 460 to 500 and the reverse walk 735 for 680.
+__device__ __forceinline__ void tile_times_state(const char* tile, const f32x4 (&S)[8], f32x4 (&a)[4], float* dst, int g,
+                                                 int jj) {
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) dst[state_row(t, g, r) * DK] = S[t][r];
+    }
+    bf16x8 f[2][4];
+    u32x4 sb[2][3];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        a[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+        f[0][m] = row_frag(tile, m, 0, g, jj);
+    }
+    auto split = [&](int kk, int i) { split_pair<3>(sb[kk & 1], i, S[2 * kk + (i >> 1)][2 * (i & 1)], S[2 * kk + (i >> 1)][2 * (i & 1) + 1]); };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split(0, i);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+        for (int n = 2; n >= 0; --n) {
+            if (kk < 3) {
+                if (n == 2) {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) f[(kk + 1) & 1][m] = row_frag(tile, m, kk + 1, g, jj);
+                    split(kk + 1, 0);
+                } else {
+                    split(kk + 1, 3 - n);
+                }
+                if (n == 0) split(kk + 1, 1);
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) a[m] = mfma_bf(f[kk & 1][m], __builtin_bit_cast(bf16x8, sb[kk & 1][n]), a[m]);
+            interleave<4, 5, 1, 1>();
+        }
+    }
+}
+
+// y = a triangular matrix in three parts times x, fragment(part, m, kk) its operands: the
+// parts' products of 2^-16 and more of the leading one's, the small parts first, six tiles
+// side by side.  work(n), n = 2, 1, 0, is done meanwhile.
+template <bool UPPER, typename F, typename W>
+__device__ __forceinline__ void tri_times(F fragment, const f32x4 (&x)[4], f32x4 (&y)[4], W work) {
+    // the six (m, kk) of the triangle: lower kk <= m / 2, upper kk >= m / 2
+    constexpr int M[6] = {0, 1, 2, 3, UPPER ? 0 : 2, UPPER ? 1 : 3};
+    constexpr int KK[6] = {0, 0, UPPER ? 1 : 0, UPPER ? 1 : 0, 1, 1};
+    bf16x8 f[2][6];
+    f32x4 a[6];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+        f[0][i] = fragment(2, M[i], KK[i]);
+        a[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    const Split<3> xb[2] = {split_acc<3>(x[0], x[1]), split_acc<3>(x[2], x[3])};
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 2; n >= 0; --n) {
+        if (n) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) f[(n + 1) & 1][i] = fragment(n - 1, M[i], KK[i]);
+        }
+        work(n);
+#pragma unroll
+        for (int d = 2 - n; d >= 0; --d) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) a[i] = mfma_bf(f[n & 1][i], xb[KK[i]].s[d], a[i]);
+            if (d == 2 - n) interleave<6, 2, 2, 0>();
+            else interleave<6, 2, 0, 0>();
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) y[m] = (M[4] == m) ? a[m] + a[4] : (M[5] == m) ? a[m] + a[5] : a[m];
+}
+
+template <bool X>
+struct Bool {
+    static constexpr bool value = X;
+};
+
 // One loading wave's (ld = 0, 1) half of a chunk's DMA into a buffer: 32 pieces of
 // tiles and slices, and nrec of the record.
-template <int NREC, bool WITH_Q>
+template <int NREC, bool WITH_Q, bool PACED>
 __device__ __forceinline__ void load_chunk(const GdrParams& p, const Rows& vsrc, uint32_t lds, int64_t row, int64_t tok,
                                            int rows, int hq, int hv, int sl, int64_t slot, int ld, int lane) {
     typedef ScanL L;
+    auto pause = [] {
+        if (PACED) __builtin_amdgcn_s_sleep(1);
+    };
     const __amdgpu_buffer_rsrc_t rk =
         chunk_rsrc(p.k.p + row * p.k.sb + tok * p.k.st + hq * p.k.sh, p.k.st, rows, DK);
     const int l4 = lane >> 4, l16 = lane & 15;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
         const int r = 4 * (8 * ld + u) + l4;
+        pause();
         dma_piece(rk, lds + L::K + (8 * ld + u) * 1024, (int)(r * p.k.st * 2) + ((l16 ^ tsw(4 * u + l4)) << 4));
     }
     if (WITH_Q) {
@@ -77,6 +181,7 @@ __device__ __forceinline__ void load_chunk(const GdrParams& p, const Rows& vsrc,
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             const int r = 4 * (8 * ld + u) + l4;
+            pause();
             dma_piece(rq, lds + L::Q + (8 * ld + u) * 1024, (int)(r * p.q.st * 2) + ((l16 ^ tsw(4 * u + l4)) << 4));
         }
     }
@@ -85,6 +190,7 @@ __device__ __forceinline__ void load_chunk(const GdrParams& p, const Rows& vsrc,
 #pragma unroll
     for (int u = 0; u < 4; ++u) {   // eight rows a piece
         const int x = 4 * ld + u;
+        pause();
         dma_piece(rv, lds + L::V + x * 1024, (int)((8 * x + (lane >> 3)) * vsrc.st * 2) + ((lane & 7) << 4));
     }
     const __amdgpu_buffer_rsrc_t rr =
@@ -92,6 +198,7 @@ __device__ __forceinline__ void load_chunk(const GdrParams& p, const Rows& vsrc,
 #pragma unroll
     for (int u = 0; u < (NREC + 1) / 2; ++u) {
         const int x = 2 * u + ld;
+        pause();
         if (x < NREC) dma_piece(rr, lds + L::REC + x * 1024, x * 1024 + lane * 16);
     }
 }
@@ -116,15 +223,15 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_keep_kernel(const GdrPar
     if (w >= 4) {   // loading waves: chunk c + 1 while the others are at chunk c
         constexpr int NREC = 19;   // pieces of the record that are read: T and the numbers
         const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(smem));
-        auto load = [&](int c) {
-            load_chunk<NREC, false>(p, p.v, lds + (c & 1) * L::BYTES, row, bos + (int64_t)c * CH, rows_of(c), hq, hv,
+        auto load = [&](int c, auto paced) {
+            load_chunk<NREC, false, paced.value>(p, p.v, lds + (c & 1) * L::BYTES, row, bos + (int64_t)c * CH, rows_of(c), hq, hv,
                                         sl, slot0 + c, w - 4, lane);
         };
-        if (nch > 0) load(0);
+        if (nch > 0) load(0, Bool<false>());
         for (int c = 0; c < nch; ++c) {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's pieces of chunk c
             lds_barrier();
-            if (c + 1 < nch) load(c + 1);
+            if (c + 1 < nch) load(c + 1, Bool<true>());
         }
         return;
     }
@@ -141,58 +248,28 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_keep_kernel(const GdrPar
         char* buf = smem + (c & 1) * L::BYTES;
         const char *sK = buf + L::K, *sQ = buf + L::Q, *rec = buf + L::REC;
         const float* sc = reinterpret_cast<const float*>(rec + GDR_SC);
-        {
-            float* dst = p.S + ((slot0 + c) * p.Hv + hv) * DK * DK + col;
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) dst[state_row(t, g, r) * DK] = S[t][r];
-            }
-        }
-        Split<3> sb[4];
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) sb[kk] = split_acc<3>(S[2 * kk], S[2 * kk + 1]);
         // x = beta (v - e^G K S)
         f32x4 x[4];
+        tile_times_state(sK, S, x, p.S + ((slot0 + c) * p.Hv + hv) * DK * DK + col, g, jj);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            f32x4 a = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                const bf16x8 f[1] = {row_frag(sK, m, kk, g, jj)};
-                a = mfma_split<3>(f, sb[kk], a);
-            }
             const f32x4 eg = *reinterpret_cast<const f32x4*>(sc + SC_EG + 16 * m + 4 * g);
             const f32x4 be = *reinterpret_cast<const f32x4*>(sc + SC_BE + 16 * m + 4 * g);
             const f32x4 v = widen(slice_frag(buf + L::V, m, w, g, jj));
-            x[m] = be * (v - eg * a);
+            x[m] = be * (v - eg * x[m]);
         }
         // u = T x
+        const float el = sc[SC_EL];
         f32x4 u[4];
-        {
-            Split<3> xb[2];
+        tri_times<false>(
+            [&](int n3, int m, int kk) {
+                return lds_bf8(rec + GDR_T + n3 * GDR_TRI + tri_frag(m, kk) * GDR_FRAG + frag_piece(lane));
+            },
+            x, u, [&](int n3) {
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) xb[kk] = split_acc<3>(x[2 * kk], x[2 * kk + 1]);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                f32x4 a = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int kk = 0; kk <= m / 2; ++kk) {
-                    const char* f = rec + GDR_T + tri_frag(m, kk) * GDR_FRAG + lane * 16;
-                    const bf16x8 tp[3] = {lds_bf8(f), lds_bf8(f + GDR_TRI), lds_bf8(f + 2 * GDR_TRI)};
-                    a = mfma_split<3>(tp, xb[kk], a);
-                }
-                u[m] = a;
-            }
-        }
-        {
-            float* dst = p.u + ((slot0 + c) * p.Hv + hv) * CH * DK + col;
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) dst[(16 * m + 4 * g + r) * DK] = u[m][r];
-            }
-        }
+                for (int t = 0; t < 8; ++t)
+                    if (t % 3 == n3) S[t] *= el;
+            });
         // S <- e^{G_last} S + K^T (e^{G_last - G} u)
         Split<3> wb[2];
 #pragma unroll
@@ -201,16 +278,27 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_keep_kernel(const GdrPar
             const f32x4 g1 = *reinterpret_cast<const f32x4*>(sc + SC_GA + 32 * kk + 16 + 4 * g);
             wb[kk] = split_acc<3>(g0 * u[2 * kk], g1 * u[2 * kk + 1]);
         }
-        const float el = sc[SC_EL];
+        float* dst = p.u + ((slot0 + c) * p.Hv + hv) * CH * DK + col;
+        bf16x8 f[2][4];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            f32x4 a = S[t] * el;
+        for (int t = 0; t < 4; ++t) f[0][t] = col_frag(sK, t, 0, g, jj);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                const bf16x8 f[1] = {col_frag(sK, t, kk, g, jj)};
-                a = mfma_split<3>(f, wb[kk], a);
+        for (int i = 0; i < 4; ++i) {   // tiles 4 (i / 2) .., k step i & 1; u is stored meanwhile
+            const int t0 = 4 * (i >> 1), kk = i & 1;
+            if (i < 3) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) f[kk ^ 1][t] = col_frag(sK, 4 * ((i + 1) >> 1) + t, kk ^ 1, g, jj);
             }
-            S[t] = a;
+#pragma unroll
+            for (int n3 = 2; n3 >= 0; --n3) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (r % 3 == n3) dst[(16 * i + 4 * g + r) * DK] = u[i][r];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) S[t0 + t] = mfma_bf(f[kk][t], wb[kk].s[n3], S[t0 + t]);
+                interleave<4, 2, 2, 1>();
+            }
         }
     }
 }
@@ -234,15 +322,15 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_rscan_kernel(const GdrPa
     };
     if (w >= 4) {
         const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(smem));
-        auto load = [&](int c) {
-            load_chunk<NREC, true>(p, p.dO, lds + (c & 1) * L::BYTES, row, bos + (int64_t)c * CH, rows_of(c),
+        auto load = [&](int c, auto paced) {
+            load_chunk<NREC, true, paced.value>(p, p.dO, lds + (c & 1) * L::BYTES, row, bos + (int64_t)c * CH, rows_of(c),
                                               hq, hv, sl, slot0 + c, w - 4, lane);
         };
-        if (nch > 0) load(nch - 1);
+        if (nch > 0) load(nch - 1, Bool<false>());
         for (int c = nch - 1; c >= 0; --c) {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             lds_barrier();
-            if (c > 0) load(c - 1);
+            if (c > 0) load(c - 1, Bool<true>());
         }
         return;
     }
@@ -259,111 +347,100 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_rscan_kernel(const GdrPa
         char* buf = smem + (c & 1) * L::BYTES;
         const char *sK = buf + L::K, *sQ = buf + L::Q, *rec = buf + L::REC;
         const float* sc = reinterpret_cast<const float*>(rec + GDR_SC);
-        {
-            float* dst = p.dS + ((slot0 + c) * p.Hv + hv) * DK * DK + col;
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) dst[state_row(t, g, r) * DK] = S[t][r];
-            }
-        }
         u32x2 d[4];   // do, as it is: accumulator order and, in pairs, B operand
 #pragma unroll
         for (int m = 0; m < 4; ++m) d[m] = slice_frag(buf + L::V, m, w, g, jj);
-        // du = e^{G_last - G} (K dS) + A^T do
-        f32x4 du[4];
+        // du = e^{G_last - G} (K dS) + A^T do, scale e^G do split meanwhile
+        f32x4 du[4], eg[4], be[4];
+        u32x4 qb[2][3], kb[2][3];
+        tile_times_state(sK, S, du, p.dS + ((slot0 + c) * p.Hv + hv) * DK * DK + col, g, jj);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            du[m] *= *reinterpret_cast<const f32x4*>(sc + SC_GA + 16 * m + 4 * g);
+            eg[m] = *reinterpret_cast<const f32x4*>(sc + SC_EG + 16 * m + 4 * g);
+            be[m] = *reinterpret_cast<const f32x4*>(sc + SC_BE + 16 * m + 4 * g);
+        }
+        const float el = sc[SC_EL];
         {
-            Split<3> sb[4];
+            const bf16x8 db[2] = {join(d[0], d[1]), join(d[2], d[3])};
+            bf16x8 f[2][6];
+            constexpr int M[6] = {0, 1, 2, 3, 0, 1}, KK[6] = {0, 0, 1, 1, 1, 1};
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) sb[kk] = split_acc<3>(S[2 * kk], S[2 * kk + 1]);
+            for (int i = 0; i < 6; ++i) f[0][i] = tri_col_frag(rec + GDR_A + 2 * GDR_TRI, M[i], KK[i], g, jj);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                f32x4 a = {0.f, 0.f, 0.f, 0.f};
+            for (int n3 = 2; n3 >= 0; --n3) {
+                if (n3) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    const bf16x8 f[1] = {row_frag(sK, m, kk, g, jj)};
-                    a = mfma_split<3>(f, sb[kk], a);
+                    for (int i = 0; i < 6; ++i)
+                        f[(n3 + 1) & 1][i] = tri_col_frag(rec + GDR_A + (n3 - 1) * GDR_TRI, M[i], KK[i], g, jj);
                 }
-                a *= *reinterpret_cast<const f32x4*>(sc + SC_GA + 16 * m + 4 * g);
 #pragma unroll
-                for (int kk = m / 2; kk < 2; ++kk) {
-                    const bf16x8 db = join(d[2 * kk], d[2 * kk + 1]);
-#pragma unroll
-                    for (int n3 = 2; n3 >= 0; --n3)
-                        a = mfma_bf(tri_col_frag(rec + GDR_A + n3 * GDR_TRI, m, kk, g, jj), db, a);
+                for (int i = 0; i < 8; ++i) {
+                    if (i % 3 != n3) continue;
+                    const int m = i >> 1, e = 2 * (i & 1);
+                    const f32x4 o = widen(d[m]);
+                    split_pair<3>(qb[m >> 1], i & 3, (p.scale * eg[m][e]) * o[e], (p.scale * eg[m][e + 1]) * o[e + 1]);
                 }
-                du[m] = a;
+#pragma unroll
+                for (int i = 0; i < 6; ++i) du[M[i]] = mfma_bf(f[n3 & 1][i], db[KK[i]], du[M[i]]);
+                interleave<6, 7, 2, 0>();
             }
         }
         // dx = T^T du
         f32x4 dx[4];
-        {
-            Split<3> db[2];
+        tri_times<true>([&](int n3, int m, int kk) { return tri_col_frag(rec + GDR_T + n3 * GDR_TRI, m, kk, g, jj); }, du,
+                        dx, [&](int n3) {
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) db[kk] = split_acc<3>(du[2 * kk], du[2 * kk + 1]);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                f32x4 a = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int kk = m / 2; kk < 2; ++kk) {
-                    const bf16x8 tp[3] = {tri_col_frag(rec + GDR_T, m, kk, g, jj),
-                                          tri_col_frag(rec + GDR_T + GDR_TRI, m, kk, g, jj),
-                                          tri_col_frag(rec + GDR_T + 2 * GDR_TRI, m, kk, g, jj)};
-                    a = mfma_split<3>(tp, db[kk], a);
-                }
-                dx[m] = a;
-            }
-        }
+                            for (int t = 0; t < 8; ++t)
+                                if (t % 3 == n3) S[t] *= el;
+                        });
         const int rows = rows_of(c);
-        {
-            float* dst = p.dx + ((slot0 + c) * p.Hv + hv) * CH * DK + col;
+        float* dst = p.dx + ((slot0 + c) * p.Hv + hv) * CH * DK + col;
+        // dS <- e^{G_last} dS + Q^T (scale e^G do) - K^T (beta e^G dx), Q's part first;
+        // dv = beta dx meanwhile, rounded once, through this wave's columns of the do slice
+        bf16x8 f[2][4];
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
+        for (int t = 0; t < 4; ++t) f[0][t] = col_frag(sQ, t, 0, g, jj);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) dst[(16 * m + 4 * g + r) * DK] = dx[m][r];
+        for (int i = 0; i < 8; ++i) {   // Q's products, then K's; tiles 4 (i / 2 mod 2) .., k step i & 1
+            const int t0 = 4 * ((i >> 1) & 1), kk = i & 1;
+            if (i < 7) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    f[kk ^ 1][t] = col_frag(i + 1 < 4 ? sQ : sK, 4 * (((i + 1) >> 1) & 1) + t, kk ^ 1, g, jj);
             }
-        }
-        // dv = beta dx, rounded once, through this wave's columns of the do slice
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const f32x4 y = dx[m] * *reinterpret_cast<const f32x4*>(sc + SC_BE + 16 * m + 4 * g);
-            const uint32_t p0 = pack_bf2(y[0], y[1]), p1 = pack_bf2(y[2], y[3]);
-            char* dst = buf + L::V + (16 * m + 4 * g) * 128 + 2 * (16 * w + jj);
-            *reinterpret_cast<uint16_t*>(dst) = (uint16_t)p0;
-            *reinterpret_cast<uint16_t*>(dst + 128) = (uint16_t)(p0 >> 16);
-            *reinterpret_cast<uint16_t*>(dst + 256) = (uint16_t)p1;
-            *reinterpret_cast<uint16_t*>(dst + 384) = (uint16_t)(p1 >> 16);
-            dx[m] = y;
-        }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            for (int n3 = 2; n3 >= 0; --n3) {
+                if (i < 4 && n3 == 2) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int i = 32 * q + (lane >> 1);
-            const u32x4 y = *reinterpret_cast<const u32x4*>(buf + L::V + i * 128 + 32 * w + 16 * (lane & 1));
-            if (i < rows)
-                *reinterpret_cast<u32x4*>(p.dv + ((row * p.T + bos + (int64_t)c * CH + i) * p.Hv + hv) * DK + 64 * sl +
-                                          16 * w + 8 * (lane & 1)) = y;
-        }
-        // dS <- e^{G_last} dS + Q^T (scale e^G do) - K^T (e^G dv)
-        Split<3> qb[2], kb[2];
+                    for (int r = 0; r < 4; ++r) dst[(16 * i + 4 * g + r) * DK] = dx[i][r];
+                    dx[i] *= be[i];
+                } else if (i < 4 && n3 == 1) {
+                    const uint32_t p0 = pack_bf2(dx[i][0], dx[i][1]), p1 = pack_bf2(dx[i][2], dx[i][3]);
+                    char* at = buf + L::V + (16 * i + 4 * g) * 128 + 2 * (16 * w + jj);
+                    *reinterpret_cast<uint16_t*>(at) = (uint16_t)p0;
+                    *reinterpret_cast<uint16_t*>(at + 128) = (uint16_t)(p0 >> 16);
+                    *reinterpret_cast<uint16_t*>(at + 256) = (uint16_t)p1;
+                    *reinterpret_cast<uint16_t*>(at + 384) = (uint16_t)(p1 >> 16);
+                    split_pair<3>(kb[i >> 1], 2 * (i & 1), -(eg[i][0] * dx[i][0]), -(eg[i][1] * dx[i][1]));
+                } else if (i < 4) {
+                    split_pair<3>(kb[i >> 1], 2 * (i & 1) + 1, -(eg[i][2] * dx[i][2]), -(eg[i][3] * dx[i][3]));
+                }
+                if (i >= 4 && i < 6 && n3 == 2) {
+                    asm volatile("" ::: "memory");   // the pieces written above, which LDS takes in order
+                    const int j = 32 * (i - 4) + (lane >> 1);
+                    const u32x4 y = *reinterpret_cast<const u32x4*>(buf + L::V + j * 128 + 32 * w + 16 * (lane & 1));
+                    if (j < rows)
+                        *reinterpret_cast<u32x4*>(p.dv + ((row * p.T + bos + (int64_t)c * CH + j) * p.Hv + hv) * DK +
+                                                  64 * sl + 16 * w + 8 * (lane & 1)) = y;
+                }
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            const f32x4 e0 = *reinterpret_cast<const f32x4*>(sc + SC_EG + 32 * kk + 4 * g);
-            const f32x4 e1 = *reinterpret_cast<const f32x4*>(sc + SC_EG + 32 * kk + 16 + 4 * g);
-            qb[kk] = split_acc<3>((p.scale * e0) * widen(d[2 * kk]), (p.scale * e1) * widen(d[2 * kk + 1]));
-            kb[kk] = split_acc<3>(-(e0 * dx[2 * kk]), -(e1 * dx[2 * kk + 1]));
-        }
-        const float el = sc[SC_EL];
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            f32x4 a = S[t] * el;
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                const bf16x8 fq[1] = {col_frag(sQ, t, kk, g, jj)}, fk[1] = {col_frag(sK, t, kk, g, jj)};
-                a = mfma_split<3>(fq, qb[kk], a);
-                a = mfma_split<3>(fk, kb[kk], a);
+                for (int t = 0; t < 4; ++t)
+                    S[t0 + t] = mfma_bf(f[kk][t], __builtin_bit_cast(bf16x8, (i < 4 ? qb : kb)[kk][n3]), S[t0 + t]);
+                interleave<4, 4, 2, 1>();
             }
-            S[t] = a;
         }
     }
     if (p.dh0) {

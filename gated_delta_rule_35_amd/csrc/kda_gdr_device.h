@@ -20,37 +20,30 @@ __device__ __forceinline__ f32x4 mfma_bf(bf16x8 a, bf16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// The bf16 pair (-1, 0), or (0, -1) with HI, in a scalar register.  Written as a constant
-// operand, the first becomes the inline -1.0, which v_dot2c reads as a 32-bit float.
-template <bool HI>
-__device__ __forceinline__ bf16x2v minus_one() {
-    uint32_t x;
-    if (HI) asm("s_mov_b32 %0, 0xbf800000" : "=s"(x));
-    else asm("s_mov_b32 %0, 0xbf80" : "=s"(x));
-    return __builtin_bit_cast(bf16x2v, x);
-}
-
 // Eight fp32 values as NS bf16 parts, packed as MFMA operands.
 template <int NS>
 struct Split {
     bf16x8 s[NS];
 };
+// Values 2 i and 2 i + 1 into word i of the parts.  What a part leaves is formed by plain
+// subtractions (exact): v_dot2c would take one instruction for two, but it occupies the
+// matrix unit, and these run beside it.
+template <int NS>
+__device__ __forceinline__ void split_pair(u32x4 (&w)[NS], int i, float a, float b) {
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+        w[n][i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2v));
+        if (n + 1 < NS) {
+            a -= bf_lo(w[n][i]);
+            b -= bf_hi(w[n][i]);
+        }
+    }
+}
 template <int NS>
 __device__ __forceinline__ Split<NS> split8(const float (&x)[8]) {
     u32x4 w[NS];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float a = x[2 * i], b = x[2 * i + 1];
-#pragma unroll
-        for (int n = 0; n < NS; ++n) {
-            const bf16x2v h = __builtin_convertvector(f32x2{a, b}, bf16x2v);
-            w[n][i] = __builtin_bit_cast(uint32_t, h);
-            if (n + 1 < NS) {   // a - h[0], b - h[1]: one instruction each, and exact
-                a = __builtin_amdgcn_fdot2_f32_bf16(h, minus_one<false>(), a, false);
-                b = __builtin_amdgcn_fdot2_f32_bf16(h, minus_one<true>(), b, false);
-            }
-        }
-    }
+    for (int i = 0; i < 4; ++i) split_pair<NS>(w, i, x[2 * i], x[2 * i + 1]);
     Split<NS> r;
 #pragma unroll
     for (int n = 0; n < NS; ++n) r.s[n] = __builtin_bit_cast(bf16x8, w[n]);
@@ -83,6 +76,13 @@ __device__ __forceinline__ f32x4 mfma_split(const bf16x8 (&a)[NA], const Split<N
 __device__ __forceinline__ f32x4 mfma_h(half8 a, half8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
+// x - h[0] and y - h[1], one instruction each (exact: what an fp16 rounding leaves fits fp32).
+__device__ __forceinline__ f32x2 minus_half(half2v h, float x, float y) {
+    f32x2 r;
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(r[0]) : "v"(h), "v"(x));
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r[1]) : "v"(h), "v"(y));
+    return r;
+}
 // Two accumulator tiles as B operand in fp16, and with PARTS = 2 what that leaves.
 template <int PARTS>
 struct HSplit {
@@ -98,7 +98,7 @@ __device__ __forceinline__ HSplit<PARTS> hsplit(f32x4 a, f32x4 b) {
         r.s[0][2 * i] = h[0];
         r.s[0][2 * i + 1] = h[1];
         if (PARTS == 2) {
-            const half2v l = __builtin_convertvector(f32x2{fmaf((float)h[0], -1.f, x), fmaf((float)h[1], -1.f, y)}, half2v);
+            const half2v l = __builtin_convertvector(minus_half(h, x, y), half2v);
             r.s[1][2 * i] = l[0];
             r.s[1][2 * i + 1] = l[1];
         }

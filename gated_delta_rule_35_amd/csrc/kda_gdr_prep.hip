@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p)
             const int m = x < 2 ? x : 2 + ((x - 2) >> 1), c = x < 2 ? 0 : x & 1;   // (m, kk)
             const float* a = (which ? sA : sM) + (16 * m + jj) * SP + 32 * c + 4 * g;
             const f32x4 u0 = *reinterpret_cast<const f32x4*>(a), u1 = *reinterpret_cast<const f32x4*>(a + 16);
-            char* dst = rec + (which ? (BWD ? GDR_A : FWD_A) : (BWD ? GDR_T : FWD_T)) + x * GDR_FRAG + ln * 16;
+            char* dst = rec + (which ? (BWD ? GDR_A : FWD_A) : (BWD ? GDR_T : FWD_T)) + x * GDR_FRAG + (BWD ? frag_piece(ln) : ln * 16);
             if (BWD) {
                 const Split<3> parts = split_acc<3>(u0, u1);
 #pragma unroll

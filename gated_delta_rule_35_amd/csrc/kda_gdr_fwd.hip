@@ -19,10 +19,14 @@
 // bits, so that the state keeps fp32's accuracy with two thirds of the matrix work of
 // three bf16 parts and a fifth of fp32 instructions'; what only reaches the bf16 output
 // (S in Q S, A, u in A u) enters as one part, eight times finer than o's own rounding.
-// fp16's range is met by two powers of two: `kap` for the (sequence, head), the size of
-// its first chunk's keys, by which S is divided, and one for each value channel (each
-// lane's column), which keeps its largest |S| / kap and |v| within [2^-2, 2^10]; it
-// changes rarely, when a chunk starts.
+// fp16's range is met by two powers of two: `kap`, the size of the chunk's keys, by which
+// S is divided, and one for each value channel (each lane's column), which keeps the
+// largest |S| / kap and |beta v| within [2^2, 2^10] when a chunk starts, and again the
+// largest of what its end keeps of them, before S is formed anew; all change rarely.
+// With beta |k|^2 <= 2, where the update does not expand the state, x, u and u 2^ek / kap
+// are then a few times those at most, and |T| <= 2.  An entry keeps its 22 bits down to
+// 2^-4 to 2^-12 of the largest, and is off by 2^-25 in these units below that, 2^-27 to
+// 2^-35 of the largest.
 #include "kda_gdr_device.h"
 
 namespace kda {
@@ -75,18 +79,14 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
         return r <= 0 ? 0 : (r >= CH ? CH : (int)r);
     };
     auto record = [&](int c) -> const char* { return p.rec + ((slot0 + c) * p.Hv + hv) * FWD_REC; };
-    // the largest power of two that the first chunk's keys are divided by
-    float kap = nch > 0 ? reinterpret_cast<const float*>(record(0) + FWD_SC)[SC_KP + lane] : 0.f;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) kap = fmaxf(kap, __shfl_xor(kap, m));
-    kap = kap > 0.f ? kap : 1.f;
+    float kap = 1.f;   // of the chunk at hand; a chunk of zero keys keeps the one before
 
     if (wave >= 4) {
         // ================= staging waves =================
         const int w = wave - 4;
         const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(smem));
         i32x4 kr[4], qr[4];   // rows 4 w + l / 16 (mod 16) of the next chunk: one 16-byte piece a lane
-        float kp, qp, sc[2];
+        float kp, qp, km, sc[2];
         // Rows 16 w + 4 x + lane / 16, piece lane % 16 of the next chunk's k and q, and (lane
         // for token) what they are divided by; two of the eight rows of numbers.
         auto fetch = [&](int c) {
@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
             const float* s = reinterpret_cast<const float*>(record(c) + FWD_SC);
             kp = s[SC_KS + ln];
             qp = s[SC_QS + ln];
+            km = s[SC_KP + ln];   // a vector load like the others: they are counted
             sc[0] = s[128 * w + ln];
             sc[1] = s[128 * w + 64 + ln];
         };
@@ -138,14 +139,15 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
             const int ln = opaque(lane), r = 16 * w + (ln >> 4);
             char* to = smem + (c & 1) * FL::BYTES;
             float* out = reinterpret_cast<float*>(to + FL::SC);
-            const float kinv = 1.f / kp, qinv = p.scale / qp;   // powers of two (qp holds scale 2^eq)
+            const float kinv = kp > 0.f ? 1.f / kp : 1.f, qinv = 1.f / qp;   // powers of two
+            if (km > 0.f) kap = km;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int at = tile_off(r + 4 * x, ln & 15);
                 *reinterpret_cast<u32x4*>(to + FL::K + at) = to_half(kr[x], __shfl(kinv, r + 4 * x));
                 *reinterpret_cast<u32x4*>(to + FL::Q + at) = to_half(qr[x], __shfl(qinv, r + 4 * x));
             }
-            // e^G 2^ek kap and 2^ek / kap (rows 4 and 5: wave 2)
+            // beta e^G 2^ek kap and 2^ek / kap (rows 4 and 5: wave 2)
             out[128 * w + ln] = sc[0] * (w == 2 ? kap : 1.f);
             out[128 * w + 64 + ln] = sc[1] * (w == 2 ? 1.f / kap : 1.f);
         };
@@ -172,8 +174,8 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         };
         for (int c = 0; c < nch; ++c) {
-            // v, T and A of chunk c have landed; the twelve loads for chunk c + 1, issued later, may be on their way
-            if (c + 1 < nch) asm volatile("s_waitcnt vmcnt(12)" ::: "memory");
+            // v, T and A of chunk c have landed; the thirteen loads for chunk c + 1, issued later, may be on their way
+            if (c + 1 < nch) asm volatile("s_waitcnt vmcnt(13)" ::: "memory");
             else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             lds_barrier();
             if (c > 0) store_o(c - 1);
@@ -196,8 +198,26 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S[t][r] = p.h0 ? p.h0[so + state_row(t, lane >> 4, r) * DK] * (1.f / kap) : 0.f;
+        for (int r = 0; r < 4; ++r) S[t][r] = p.h0 ? p.h0[so + state_row(t, lane >> 4, r) * DK] : 0.f;
     }
+    // Columns whose largest value left [2^2, 2^10] go back to [2^7, 2^8); top: the lane's part
+    // of it, x: what is scaled with the state.
+    auto rescale = [&](float top, f32x4 (&x)[4]) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        if (top > 1024.f || (top < 4.f && top > 0.f)) {
+            int e = (int)(__float_as_uint(top) >> 23) - 127 - 7;   // what its exponent has too many
+            const int was = 127 - (int)(__float_as_uint(down) >> 23);
+            e = max(-120 - was, min(120 - was, e));                // keep the power of two itself in range
+            const float by = __uint_as_float((uint32_t)(127 - max(-126, min(126, e))) << 23);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) S[t] *= by;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) x[m] *= by;
+            down *= by;
+            up = 1.f / down;
+        }
+    };
     for (int c = 0; c < nch; ++c) {
         lds_barrier();   // chunk c is in LDS, and the other slot's reads are done
         const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
@@ -205,35 +225,26 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
         const char *tk = slot + FL::K, *tq = slot + FL::Q;
         char* tv = slot + FL::V;
         const float* sc = reinterpret_cast<const float*>(slot + FL::SC);
-        f32x4 v[4];
+        const float km = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(sc[SC_KP])));
+        if (km > 0.f && km != kap) {   // powers of two: exact
+#pragma unroll
+            for (int t = 0; t < 8; ++t) S[t] *= kap / km;
+            kap = km;
+        }
+        f32x4 v[4];   // beta v
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const u32x2 b = lds_tr(tv + (16 * m + 4 * g + (jj >> 2)) * 128 + 32 * w + 8 * (jj & 3));
-            v[m] = f32x4{bf_lo(b[0]), bf_hi(b[0]), bf_lo(b[1]), bf_hi(b[1])} * down;
+            v[m] = f32x4{bf_lo(b[0]), bf_hi(b[0]), bf_lo(b[1]), bf_hi(b[1])} * down * sc4(sc, SC_BE, m, g);
         }
         float top = 0.f;
 #pragma unroll
         for (int t = 0; t < 8; ++t) top = max_abs(top, S[t]);
 #pragma unroll
         for (int m = 0; m < 4; ++m) top = max_abs(top, v[m]);
-        if (__any(top > 1024.f || (top < 0.25f && top > 0.f))) {
-            // columns whose largest value left [2^-2, 2^10] go back to [1, 2)
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            if (top > 1024.f || (top < 0.25f && top > 0.f)) {
-                int e = (int)(__float_as_uint(top) >> 23) - 127;   // its exponent
-                const int was = 127 - (int)(__float_as_uint(down) >> 23);
-                e = max(-120 - was, min(120 - was, e));            // keep the power of two itself in range
-                const float by = __uint_as_float((uint32_t)(127 - max(-126, min(126, e))) << 23);
-#pragma unroll
-                for (int t = 0; t < 8; ++t) S[t] *= by;
-#pragma unroll
-                for (int m = 0; m < 4; ++m) v[m] *= by;
-                down *= by;
-                up = 1.f / down;
-            }
-        }
-        // x = beta (v - e^G K S) and e^G Q S
+        if (__any(top > 1024.f || (top < 4.f && top > 0.f))) rescale(top, v);
+        const float whole = up * kap * p.scale;   // what o's sums are multiplied by
+        // x = beta v - beta e^G K S and e^G Q S
         f32x4 x[4], o[4];
         {
             HSplit<2> sb[4];
@@ -249,7 +260,7 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
                     b = mfma_h(row_frag(tq, m, kk, g, jj), sb[kk].s[0], b);
                     a = mfma_h(f, sb[kk].s[0], a);
                 }
-                x[m] = sc4(sc, SC_BE, m, g) * (v[m] - sc4(sc, SC_EGK, m, g) * a);
+                x[m] = v[m] - sc4(sc, SC_EGK, m, g) * a;
                 o[m] = sc4(sc, SC_EG, m, g) * b;
             }
         }
@@ -275,14 +286,24 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
         }
         // S <- e^{G_last} S + K^T (e^{G_last - G} u)
         {
-            HSplit<2> wb[2];
+            f32x4 wu[4];
+            float tw = 0.f;
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-                wb[kk] = hsplit<2>(sc4(sc, SC_GA, 2 * kk, g) * u[2 * kk], sc4(sc, SC_GA, 2 * kk + 1, g) * u[2 * kk + 1]);
+            for (int m = 0; m < 4; ++m) tw = max_abs(tw, wu[m] = sc4(sc, SC_GA, m, g) * u[m]);
             const float el = sc[SC_EL];
 #pragma unroll
+            for (int t = 0; t < 8; ++t) S[t] *= el;
+            if (__any(tw < 4.f && tw > 0.f)) {   // what is left of the chunk may be far less than what it started with
+#pragma unroll
+                for (int t = 0; t < 8; ++t) tw = max_abs(tw, S[t]);
+                rescale(tw, wu);
+            }
+            HSplit<2> wb[2];
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) wb[kk] = hsplit<2>(wu[2 * kk], wu[2 * kk + 1]);
+#pragma unroll
             for (int t = 0; t < 8; ++t) {
-                f32x4 a = S[t] * el;
+                f32x4 a = S[t];
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
                     const half8 f = col_frag(tk, t, kk, g, jj);
@@ -302,7 +323,7 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
             for (int kk = 0; kk <= m / 2; ++kk)
                 o[m] = mfma_h(*reinterpret_cast<const half8*>(slot + FL::A + tri_frag(m, kk) * GDR_FRAG + ln * 16),
                               ub[kk].s[0], o[m]);
-            o[m] *= sc4(sc, SC_QS, m, g) * (up * kap);
+            o[m] *= sc4(sc, SC_QS, m, g) * whole;
             const uint32_t p0 = pack_bf2(o[m][0], o[m][1]), p1 = pack_bf2(o[m][2], o[m][3]);
             char* dst = tv + (16 * m + 4 * g) * 128 + 2 * (16 * w + jj);
             *reinterpret_cast<uint16_t*>(dst) = (uint16_t)p0;
@@ -316,7 +337,7 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) p.hT[so + state_row(t, lane >> 4, r) * DK] = S[t][r] * (up * kap);
+            for (int r = 0; r < 4; ++r) p.hT[so + state_row(t, lane >> 4, r) * DK] = S[t][r] * up * kap;
         }
     }
 }

@@ -95,6 +95,13 @@ __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p)
         }
     }
     __syncthreads();   // k and q are read
+    float kmax = 0.f;   // wave 0: the largest of the chunk's key divisors
+    if (!BWD && w == 0) {
+        kmax = sKp[lane];
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) kmax = fmaxf(kmax, __shfl_xor(kmax, m));
+        if (kmax > 0.f) kmax = fminf(fmaxf(kmax, 0x1p-60f), 0x1p60f);
+    }
     // tiles above the diagonal that fragments cover
     for (int e = tid; e < 512; e += 256) {
         const int t = e >> 8, x = e & 255, at = (32 * t + (x >> 4)) * SP + 32 * t + 16 + (x & 15);
@@ -126,10 +133,10 @@ __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p)
             sc[SC_EL] = gate_exp(GL);
             if (!BWD) {
                 const float ks = sKp[lane] > 0.f ? sKp[lane] : 1.f;
-                sc[SC_EGK] = eg * ks;
-                sc[SC_KS] = ks;
-                sc[SC_QS] = p.scale * sQp[lane];
-                sc[SC_KP] = sKp[lane];
+                sc[SC_EGK] = sBeta[lane] * eg * ks;
+                sc[SC_KS] = sKp[lane];
+                sc[SC_QS] = sQp[lane];
+                sc[SC_KP] = kmax;
             }
         }
         {

@@ -147,6 +147,70 @@ def test_gates_and_ranges(kind):
     check_backward(x, with_state=kind != "wide values")
 
 
+@pytest.mark.parametrize("kind", ["keys grow", "keys shrink", "keys start at zero", "no update of a small state",
+                                  "values grow", "small state, large values later"])
+def test_sizes_that_change_between_chunks(kind):
+    """Keys, values and states whose sizes change by many powers of two from one chunk to the
+    next, in both directions."""
+    say(f"gdr fwd and bwd, {kind}")
+    x = ref.make(1, 270, 1, 2, h0=True, seed=31)
+    step = torch.ones(270)
+    if kind == "keys grow":
+        step[:70] = 2.0 ** -20
+        x["k"], x["h0"] = (x["k"].float() * step[None, :, None, None]).bfloat16(), None
+    elif kind == "keys shrink":   # and the state built from the large ones is forgotten
+        step[100:] = 2.0 ** -20
+        x["k"] = (x["k"].float() * step[None, :, None, None]).bfloat16()
+        x["g"][0, 128] = -90
+    elif kind == "keys start at zero":
+        x["k"][0, :70] = 0
+        x["k"][0, 140:210] = 0
+    elif kind == "no update of a small state":
+        x["beta"][0, :130] = 0
+        x["h0"] = x["h0"] * 2.0 ** -24
+        x["g"] = x["g"] * 0.01
+    elif kind == "values grow":
+        step = 2.0 ** torch.linspace(-30, 30, 270)
+        x["v"] = (x["v"].float() * step[None, :, None, None]).bfloat16()
+    else:
+        step[:200] = 2.0 ** -24
+        x["v"], x["h0"] = (x["v"].float() * step[None, :, None, None]).bfloat16(), x["h0"] * 2.0 ** -24
+    check_forward(x)
+    for a, b in ((0, 64), (64, 128), (128, 192)):   # chunk by chunk, each against its own size
+        if x["h0"] is None or a:
+            check_forward({n: (t[:, a:b].contiguous() if n != "h0" else None) for n, t in x.items()})
+    out, _ = check_forward(x)
+    want, _ = ref.forward(x, SCALE)
+    half = ref.forward_magnitude(x, SCALE)
+    for a in range(0, 270, 64):
+        ref.assert_rows(out[:, a:a + 64], want[:, a:a + 64], (kind, a), half=half[:, a:a + 64])
+    check_backward(x, with_state=x["h0"] is not None)
+
+
+def test_far_scales():
+    """A scale and queries whose product lies below fp32's normal numbers, on large values."""
+    say("gdr_fwd, scale 2^-40, queries 2^-100, values 2^60")
+    x = ref.make(1, 100, 1, 1, seed=33)
+    x["q"], x["v"] = (x["q"].double() * 2.0 ** -100).bfloat16(), (x["v"].double() * 2.0 ** 60).bfloat16()
+    d = ref.cuda(x)
+    o, _ = kda_gdr_fwd(*args(d)[:5], 2.0 ** -40)
+    torch.cuda.synchronize()
+    ref.assert_rows(o, ref.forward(x, 2.0 ** -40)[0], "o", half=ref.forward_magnitude(x, 2.0 ** -40))
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_packed_heads_of_eight_and_many_sequences(many):
+    """Value heads in a multiple of eight (each XCD an eighth of them), and more sequences than
+    a work-group has threads."""
+    lens = [1, 2, 0, 3] * 150 if many else [70, 3, 0, 129, 64]
+    Hq, Hv = (1, 1) if many else (2, 8)
+    say(f"gdr fwd and bwd, {len(lens)} sequences, Hv={Hv}")
+    x = ref.make(1, sum(lens), Hq, Hv, h0=True, N=len(lens), seed=35)
+    cu = torch.tensor([0] + list(torch.tensor(lens).cumsum(0)), dtype=torch.int32)
+    check_forward(x, cu)
+    check_backward(x, cu)
+
+
 def test_value_channels_are_independent():
     """Value channels of sizes from 2^-60 to 2^60, changing from token to token block: every
     channel keeps the accuracy that it has alone (all products are linear in it)."""

@@ -5,8 +5,11 @@
 //
 // Bound by the state's 64 KB read and 64 KB written per row and value head.  Columns of
 // S never mix, so a work-group takes CW of a head's 128 columns: all of them where rows
-// and heads alone give every compute unit several work-groups, 32 where they do not
-// (more work-groups in flight and a quarter of the work in each).  256 threads, each a
+// and heads alone give every compute unit a work-group, 32 where they do not (four times
+// the work-groups, a quarter of the work in each).  With 256 compute units, 128 and 32
+// columns: 4.4 and 3.6 us at 16 rows and heads, 4.8 and 4.1 at 64, 6.6 and 6.9 at 256,
+// 20.2 and 22.3 at 1024, 83 and 83 at 4096 (537 MB, 6.5 TB/s with part of the states in
+// the last-level cache; 5.1 TB/s at 16,384, what a large copy reaches).  256 threads, each a
 // quad of columns and every 256 / (CW / 4)-th row, so that loads and stores are 16 bytes
 // a lane and CW columns of a row one run; S stays in registers.  The sums over rows go
 // by lane exchange, then through LDS in wave order: runs are bitwise equal.
@@ -114,7 +117,7 @@ __global__ void __launch_bounds__(DT) kda_gdr_decode_kernel(const GdrDecodeParam
 hipError_t launch_gdr_decode(const GdrDecodeParams& p, int cus, hipStream_t stream) {
     const int64_t heads = (int64_t)p.N * p.Hv;
     if (heads == 0) return hipSuccess;
-    if (heads >= 8 * (int64_t)cus)
+    if (heads >= cus)
         hipLaunchKernelGGL(kda_gdr_decode_kernel<128>, dim3((unsigned)heads), dim3(DT), 0, stream, p);
     else
         hipLaunchKernelGGL(kda_gdr_decode_kernel<32>, dim3((unsigned)(4 * heads)), dim3(DT), 0, stream, p);

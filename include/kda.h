@@ -439,7 +439,7 @@ kda_status_t kda_bwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda_ten
  * Shapes (N = B, or cu_seqlens' sequences with B = 1, as for kda_fwd):
  *   q, k           [B, T, Hq, 128]       bf16
  *   v              [B, T, Hv, 128]       bf16
- *   g              [B, T, Hv]            fp32 log-decay (<= 0; minus infinity forgets the state)
+ *   g              [B, T, Hv]            fp32 log-decay (<= 0; minus infinity forgets a finite state)
  *   beta           [B, T, Hv]            bf16 or fp32
  *   states         [N, Hv, 128, 128]     fp32 (key channel, value channel)
  * Strided inputs: q, k, v (and d_out) may be views whose 128 channels are
@@ -452,10 +452,19 @@ kda_status_t kda_bwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda_ten
  * cu_seqlens' precondition and clamping are kda_fwd's; rows of tokens in no
  * sequence are not written.  More than 2^22 (chunk slot, value head) units, 2^31 - 1
  * tokens or 2^21 (sequence, value head) pairs return KDA_ERR_UNSUPPORTED.
- * Precision: products run on bf16 matrix instructions with fp32 operands given in
- * two or three bf16 parts, so that states, dg and dbeta have fp32's accuracy (about
- * 1e-6 relative), whatever the range of the values; o, dq, dk and dv are rounded to
- * bf16 once.
+ * Precision: every sum is fp32.  The forward's products run on fp16 matrix
+ * instructions: states, corrections and T in two parts (22 bits), what only reaches o
+ * in one; each key and query row, and each value channel, is scaled by powers of two
+ * that follow the sizes met, so that values of any size keep states to about 1e-6 of
+ * their largest entries.  An entry below 2^-12 of the largest |S| or |beta v| of its
+ * value channel in the chunk is off by up to 2^-27 of that.  The update must not expand
+ * the state, beta |k|^2 <= 2 (L2-normalised keys and 0 <= beta <= 2 do not): where
+ * (I - beta k k^T) grows it past fp16's range within a chunk, results are infinite or
+ * NaN.  The backward's products run on bf16 matrix instructions with fp32 operands in
+ * three parts, at fp32's accuracy and range (about 1e-6 relative for dg and dbeta).  o,
+ * dq, dk and dv are rounded to bf16 once.  A token that holds NaN or infinity may reach
+ * every token of its 64-token chunk and later ones of its sequence and head, no other
+ * sequence, and through v no other value channel of o and the states.
  */
 
 /*
@@ -482,7 +491,9 @@ kda_status_t kda_gdr_fwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda
  *   dv       [B, T, Hv, 128] bf16
  *   dg, dbeta [B, T, Hv]     fp32
  *   d_initial_state [N, Hv, 128, 128] fp32, or NULL (not computed)
- * An empty sequence passes d_final_state through to its d_initial_state.
+ * An empty sequence passes d_final_state through to its d_initial_state.  A |beta| below
+ * 2^-40 counts as 2^-40: dbeta_t is formed as u_t . dx_t / beta_t, u_t = beta_t times
+ * what it multiplies.
  * workspace: as for kda_gdr_fwd, of kda_gdr_bwd_workspace_size(B * T, N, Hv) bytes,
  * 256-byte aligned.  Per (chunk slot, value head): 37,888 bytes of operands, the
  * states entering and the state gradients leaving (64 KB each), and two fp32 token

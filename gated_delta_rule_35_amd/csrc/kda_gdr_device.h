@@ -229,9 +229,8 @@ __device__ __forceinline__ int gdr_chunk(const GdrParams& p, int64_t s, int64_t&
 // dbeta is u's product with a gradient divided by beta, and an update of 2^-40 is far
 // below what the state's 24 bits hold.
 template <bool BWD>
-__device__ __forceinline__ float gdr_beta(const GdrParams& p, int64_t i) {
-    const float b =
-        p.beta_f32 ? reinterpret_cast<const float*>(p.beta)[i] : bf2f(reinterpret_cast<const uint16_t*>(p.beta)[i]);
+__device__ __forceinline__ float gdr_beta(const void* beta, int f32, int64_t i) {
+    const float b = f32 ? reinterpret_cast<const float*>(beta)[i] : bf2f(reinterpret_cast<const uint16_t*>(beta)[i]);
     return BWD && fabsf(b) < 0x1p-40f ? 0x1p-40f : b;
 }
 

@@ -88,6 +88,14 @@ __device__ __forceinline__ bf16x8 plane_col(const char* pl, int m, int kk, int g
     const char* a = pl + (32 * kk + 4 * g + (jj >> 2)) * PS + 32 * m + 8 * (jj & 3);
     return join(lds_tr(a), lds_tr(a + 16 * PS));
 }
+// The kernel's arguments, read anew at each use (a scalar load): kept in registers through
+// the loop they would not fit the scalar ones.
+typedef const __attribute__((address_space(4))) GdrParams Args;
+__device__ __forceinline__ Args& args_again() {
+    Args* a = (Args*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(a));
+    return *a;
+}
 }  // namespace
 
 __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, const int items) {
@@ -120,12 +128,13 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
         for (int n = 0; n < 8; ++n) to[n] = *reinterpret_cast<const f32x4*>(at + 32 * (n >> 1) + 4 * (n & 1));
     };
     auto fetch_tokens = [&]() {
+        Args& p = args_again();
         const int t = opaque(tid), lane = t & 63;
         const int64_t unit = slot * p.Hv + hq * R + r;
         if (w == 7) {
             const int64_t gi = (row * p.T + tok + lane) * p.Hv + hq * R + r;
             gate = lane < rows ? p.g[gi] : 0.f;
-            beta = lane < rows ? gdr_beta<true>(p, gi) : 0.f;
+            beta = lane < rows ? gdr_beta<true>(p.beta, p.beta_f32, gi) : 0.f;
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -138,10 +147,12 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
         }
     };
     auto dma_do = [&]() {
+        Args& p = args_again();
         dma_tile(chunk_rsrc(p.dO.p + row * p.dO.sb + tok * p.dO.st + (hq * R + r) * p.dO.sh, p.dO.st, rows, DK),
                  lds + GL::DO, p.dO.st, w, 8, opaque(lane));
     };
     auto dma_kq = [&]() {
+        Args& p = args_again();
         const int lane = opaque(tid & 63);
         dma_tile(chunk_rsrc(p.k.p + row * p.k.sb + tok * p.k.st + hq * p.k.sh, p.k.st, rows, DK), lds + GL::K, p.k.st, w,
                  8, lane);
@@ -153,14 +164,14 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
     fetch_tokens();
     dma_do();
     dma_kq();
-    fetch_state(p.S, s);
+    fetch_state(args_again().S, s);
     f32x4 dq[4], dk[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) dq[m] = dk[m] = z4;
 
     while (item < items) {
         f32x4 ds[8];   // needed after S's products: in flight until then
-        fetch_state(p.dS, ds);
+        fetch_state(args_again().dS, ds);
         // u and dx in three parts, and dx . u
         const int t = opaque(tid);
 #pragma unroll
@@ -260,7 +271,7 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
         } else {
             ++r;
         }
-        if (item < items) fetch_state(p.S, s);
+        if (item < items) fetch_state(args_again().S, s);
         // lower tiles of P and E, transposed (lane: token i = 16 I + jj, j = 16 J + 4 g + e): wave w
         // has tile w of both; tiles 8 and 9 of P go to waves 0 and 1, of E to waves 2 and 3
         auto tile_rc = [&](int id, int& I, int& J) {
@@ -358,6 +369,7 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             last += (double)(sh.eg[63] * sd);
             const double sum = prefix64(dG), rest = lane_f64(sum, 63) - sum + dG;
             if (i < rows0) {
+                Args& p = args_again();
                 p.dg[gi] = (float)(rest + last);
                 p.dbeta[gi] = sh.xu[i] / sh.be[i];
             }
@@ -408,6 +420,7 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
         lds_barrier();   // k, q and the planes are read, dq and dk complete
         if (done) {
             if (item < items) dma_kq();
+            Args& p = args_again();
             const int t = opaque(tid);
 #pragma unroll
             for (int h = 0; h < 4; ++h) {

@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p)
     float gate = 0.f, beta = 0.f;
     if (w == 0 && lane < rows) {
         gate = p.g[gi];
-        beta = gdr_beta<BWD>(p, gi);
+        beta = gdr_beta<BWD>(p.beta, p.beta_f32, gi);
     }
 
     {
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p)
             }
             if (r + 1 < R && lane < rows) {
                 gate = p.g[gi + r + 1];
-                beta = gdr_beta<BWD>(p, gi + r + 1);
+                beta = gdr_beta<BWD>(p.beta, p.beta_f32, gi + r + 1);
             }
         }
         if (r > 0) __syncthreads();

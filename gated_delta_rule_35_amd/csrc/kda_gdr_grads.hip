@@ -203,29 +203,33 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
         // R1, R3, then R2, for channels 16 w + jj
         {
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
-            Split<3> sb[4];
+            // k steps outermost: eight (then four) chains of products side by side, one step's parts at a time
+            f32x4 r1[4], r3[4];
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) sb[kk] = split_acc<3>(s[2 * kk], s[2 * kk + 1]);
-            float z[4];   // the lane's part of its tokens' row dots
+            for (int m = 0; m < 4; ++m) r1[m] = r3[m] = z4;
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                f32x4 r1 = z4, r3 = z4;
+            for (int kk = 0; kk < 4; ++kk) {
+                const Split<3> sb = split_acc<3>(s[2 * kk], s[2 * kk + 1]);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
+                for (int m = 0; m < 4; ++m) {
                     const int at = tile_off(16 * m + jj, 4 * kk + g);
                     const bf16x8 fo[1] = {lds_bf8(smem + GL::DO + at)};
                     bf16x8 fx[3];
 #pragma unroll
                     for (int n = 0; n < 3; ++n) fx[n] = lds_bf8(smem + GL::X + n * 16384 + at);
-                    r1 = mfma_parts(sb[kk], fo, r1);
-                    r3 = mfma_parts(sb[kk], fx, r3);
+                    r1[m] = mfma_parts(sb, fo, r1[m]);
+                    r3[m] = mfma_parts(sb, fx, r3[m]);
                 }
+            }
+            float z[4];   // the lane's part of its tokens' row dots
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
                 const float eg = sh.eg[16 * m + jj];
-                r1 *= p.scale * eg;
-                r3 *= sh.be[16 * m + jj] * eg;
-                dq[m] += r1;
-                dk[m] -= r3;
-                z[m] = dot4(chan4(smem + GL::Q, m, w, g, jj), r1) - dot4(chan4(smem + GL::K, m, w, g, jj), r3);
+                r1[m] *= p.scale * eg;
+                r3[m] *= sh.be[16 * m + jj] * eg;
+                dq[m] += r1[m];
+                dk[m] -= r3[m];
+                z[m] = dot4(chan4(smem + GL::Q, m, w, g, jj), r1[m]) - dot4(chan4(smem + GL::K, m, w, g, jj), r3[m]);
             }
             {
                 f32x4 d4 = z4;
@@ -236,23 +240,27 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             }
 #pragma unroll
             for (int n = 0; n < 8; ++n) asm volatile("" : "+v"(ds[n]));   // dS's parts are formed after S's are done with
+            f32x4 r2[4];
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) sb[kk] = split_acc<3>(ds[2 * kk], ds[2 * kk + 1]);
-            float ts = 0.f;
+            for (int m = 0; m < 4; ++m) r2[m] = z4;
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                f32x4 r2 = z4;
+            for (int kk = 0; kk < 4; ++kk) {
+                const Split<3> sb = split_acc<3>(ds[2 * kk], ds[2 * kk + 1]);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
+                for (int m = 0; m < 4; ++m) {
                     const int at = tile_off(16 * m + jj, 4 * kk + g);
                     bf16x8 fu[3];
 #pragma unroll
                     for (int n = 0; n < 3; ++n) fu[n] = lds_bf8(smem + GL::U + n * 16384 + at);
-                    r2 = mfma_parts(sb[kk], fu, r2);
+                    r2[m] = mfma_parts(sb, fu, r2[m]);
                 }
-                r2 *= sh.ga[16 * m + jj];
-                dk[m] += r2;
-                const float t = dot4(chan4(smem + GL::K, m, w, g, jj), r2);
+            }
+            float ts = 0.f;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                r2[m] *= sh.ga[16 * m + jj];
+                dk[m] += r2[m];
+                const float t = dot4(chan4(smem + GL::K, m, w, g, jj), r2[m]);
                 ts += t;
                 z[m] = sum_groups(z[m] - t);
             }
@@ -388,22 +396,20 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
                 qb[kk] = join(chan_frag(smem + GL::Q, 2 * kk, w, g, jj), chan_frag(smem + GL::Q, 2 * kk + 1, w, g, jj));
             }
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
+            for (int n = 1; n >= 0; --n) {
+                const char* pp = smem + GL::U + n * GL::PL;
+                const char* pe = smem + GL::U + (2 + n) * GL::PL;
 #pragma unroll
-                for (int n = 1; n >= 0; --n) {
-                    const char* pp = smem + GL::U + n * GL::PL;
-                    const char* pe = smem + GL::U + (2 + n) * GL::PL;
+                for (int kk = 0; kk < 2; ++kk) {   // four tiles of dq and of dk side by side
 #pragma unroll
-                    for (int kk = 0; kk < 2; ++kk) {
-                        if (kk <= m / 2) {
-                            dq[m] = mfma_bf(kb[kk], plane_row(pp, m, kk, g, jj), dq[m]);
-                            dk[m] = mfma_bf(kb[kk], plane_row(pe, m, kk, g, jj), dk[m]);
-                        }
-                        if (kk >= m / 2) {
-                            dk[m] = mfma_bf(qb[kk], plane_col(pp, m, kk, g, jj), dk[m]);
-                            dk[m] = mfma_bf(kb[kk], plane_col(pe, m, kk, g, jj), dk[m]);
-                        }
+                    for (int m = 2 * kk; m < 4; ++m) {
+                        dq[m] = mfma_bf(kb[kk], plane_row(pp, m, kk, g, jj), dq[m]);
+                        dk[m] = mfma_bf(kb[kk], plane_row(pe, m, kk, g, jj), dk[m]);
                     }
+#pragma unroll
+                    for (int m = 0; m < 2 * kk + 2; ++m) dk[m] = mfma_bf(qb[kk], plane_col(pp, m, kk, g, jj), dk[m]);
+#pragma unroll
+                    for (int m = 0; m < 2 * kk + 2; ++m) dk[m] = mfma_bf(kb[kk], plane_col(pe, m, kk, g, jj), dk[m]);
                 }
             }
         }

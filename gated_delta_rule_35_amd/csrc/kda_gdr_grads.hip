@@ -286,15 +286,15 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             I = id >= 6 ? 3 : id >= 3 ? 2 : id >= 1 ? 1 : 0;
             J = id - I * (I + 1) / 2;
         };
-        // tile `id` of P, or of E, and the row and column sums of its entries below the diagonal
-        // times QK^T or KK^T
-        auto tile = [&](auto of_p, int id) -> f32x4 {
-            constexpr bool OF_P = decltype(of_p)::value;
+        // tile `id` of P, of E, or of both (u's and k's operands serve both), and the row and column
+        // sums of their entries below the diagonal times QK^T and KK^T
+        auto tile = [&](auto of_p, auto of_e, int id, f32x4& P, f32x4& E) {
+            constexpr bool OF_P = decltype(of_p)::value, OF_E = decltype(of_e)::value;
             int I, J;
             tile_rc(id, I, J);
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
             const int i = 16 * I + jj, j0 = 16 * J + 4 * g;
-            f32x4 a = z4, raw = z4;
+            f32x4 a = z4, ra = z4, b = z4, rb = z4;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
                 if (kk == 2) asm volatile("" ::: "memory");   // two steps' operands at a time: more would spill
@@ -305,36 +305,45 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
                 if (OF_P) {
                     const bf16x8 fo[1] = {lds_bf8(smem + GL::DO + ai)};
                     a = mfma_parts(ua, fo, a);
-                    raw = mfma_bf(kj, lds_bf8(smem + GL::Q + ai), raw);
-                } else {
+                    ra = mfma_bf(kj, lds_bf8(smem + GL::Q + ai), ra);
+                }
+                if (OF_E) {
                     const bf16x8 fx[3] = {lds_bf8(smem + GL::X + ai), lds_bf8(smem + GL::X + 16384 + ai),
                                           lds_bf8(smem + GL::X + 32768 + ai)};
-                    a = mfma_parts(ua, fx, a);
-                    raw = mfma_bf(kj, lds_bf8(smem + GL::K + ai), raw);
+                    b = mfma_parts(ua, fx, b);
+                    rb = mfma_bf(kj, lds_bf8(smem + GL::K + ai), rb);
                 }
             }
             const GSum Gi = {sh.hi[i], sh.lo[i]};
             const f32x4 hj = *reinterpret_cast<const f32x4*>(sh.hi + j0), lj = *reinterpret_cast<const f32x4*>(sh.lo + j0);
-            const float by = OF_P ? p.scale : -sh.be[i];
-            f32x4 v, cs;
-            float rs = 0.f;
+            f32x4 gam;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {   // what lies above the diagonal stays out, NaN and infinity too
-                v[e] = j0 + e < i + OF_P ? by * (gate_ratio(Gi, GSum{hj[e], lj[e]}) * a[e]) : 0.f;
-                const float y = j0 + e < i ? v[e] * raw[e] : 0.f;
-                rs += y;
-                cs[e] = sum16(y);
-            }
-            rs = sum_groups(rs);
-            const int at = OF_P ? id : 10 + id;
-            if (g == 0) sh.row[at][jj] = rs;
-            if (jj == 0) *reinterpret_cast<f32x4*>(&sh.col[at][4 * g]) = cs;
-            return v;
+            for (int e = 0; e < 4; ++e) gam[e] = j0 + e <= i ? gate_ratio(Gi, GSum{hj[e], lj[e]}) : 0.f;
+            auto finish = [&](auto is_p, const f32x4& a, const f32x4& raw) -> f32x4 {
+                constexpr bool IS_P = decltype(is_p)::value;
+                const float by = IS_P ? p.scale : -sh.be[i];
+                f32x4 v, cs;
+                float rs = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {   // what lies above the diagonal stays out, NaN and infinity too
+                    v[e] = j0 + e < i + IS_P ? by * (gam[e] * a[e]) : 0.f;
+                    const float y = j0 + e < i ? v[e] * raw[e] : 0.f;
+                    rs += y;
+                    cs[e] = sum16(y);
+                }
+                rs = sum_groups(rs);
+                const int at = IS_P ? id : 10 + id;
+                if (g == 0) sh.row[at][jj] = rs;
+                if (jj == 0) *reinterpret_cast<f32x4*>(&sh.col[at][4 * g]) = cs;
+                return v;
+            };
+            if (OF_P) P = finish(std::true_type{}, a, ra);
+            if (OF_E) E = finish(std::false_type{}, b, rb);
         };
-        const f32x4 P = tile(std::true_type{}, w), E = tile(std::false_type{}, w);
-        f32x4 Z = z4;
-        if (w < 2) Z = tile(std::true_type{}, 8 + w);
-        else if (w < 4) Z = tile(std::false_type{}, 6 + w);
+        f32x4 P, E, Z = z4;
+        tile(std::true_type{}, std::true_type{}, w, P, E);
+        if (w < 2) tile(std::true_type{}, std::false_type{}, 8 + w, Z, Z);
+        else if (w < 4) tile(std::false_type{}, std::true_type{}, 6 + w, Z, Z);
         lds_barrier();   // u's parts read; the sums complete
         // P and E as row-major planes of two bf16 parts
         {

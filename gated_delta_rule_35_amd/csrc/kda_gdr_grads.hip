@@ -41,9 +41,8 @@ constexpr int PS = 144;   // bytes per row of 64 bf16 (+16)
 struct GL {
     static constexpr int K = 0, Q = 16384, DO = 32768, U = 49152, X = U + 3 * 16384;   // U, X in three parts
     static constexpr int PL = 64 * PS;                  // one part of P or E, over U
-    static constexpr int OUT = X, OS = 272;             // dq, dk on the way out, over X: rows of 128 bf16 (+16)
     static constexpr int END = X + 3 * 16384;
-    static_assert(4 * PL <= 3 * 16384 && 2 * 64 * OS <= 3 * 16384, "overlays");
+    static_assert(4 * PL <= 3 * 16384, "overlay");
 };
 struct GShared {
     float hi[64], lo[64];  // G
@@ -131,7 +130,7 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
         Args& p = args_again();
         const int t = opaque(tid), lane = t & 63;
         const int64_t unit = slot * p.Hv + hq * R + r;
-        if (w == 7) {
+        if (w == 6) {
             const int64_t gi = (row * p.T + tok + lane) * p.Hv + hq * R + r;
             gate = lane < rows ? p.g[gi] : 0.f;
             beta = lane < rows ? gdr_beta<true>(p.beta, p.beta_f32, gi) : 0.f;
@@ -188,7 +187,7 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             const float xu = sum16((a[0] + a[1]) + (a[2] + a[3]));
             if (pc == 0) sh.xu[i] = xu;
         }
-        if (w == 7) {
+        if (w == 6) {
             const GSum G = gate_sum(gate);
             const GSum last = {__shfl(G.hi, 63), __shfl(G.lo, 63)};
             sh.hi[lane] = G.hi;
@@ -366,7 +365,8 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             *reinterpret_cast<u32x2*>(smem + GL::U + (e >> 7) * GL::PL + (32 * t + ((e >> 2) & 15)) * PS +
                                       2 * (32 * t + 16 + 4 * (e & 3))) = u32x2{0, 0};
         }
-        if (w == 7) {   // dg and dbeta
+        if (w == 5 && lane < rows0) args_again().dbeta[gi0 + (int64_t)lane * args_again().Hv] = sh.xu[lane] / sh.be[lane];
+        if (w == 7) {   // dg
             const int i = lane, I = i >> 4;
             const int64_t gi = gi0 + (int64_t)i * p.Hv;
             double dG = 0.0, last = 0.0;
@@ -388,7 +388,6 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             if (i < rows0) {
                 Args& p = args_again();
                 p.dg[gi] = (float)(rest + last);
-                p.dbeta[gi] = sh.xu[i] / sh.be[i];
             }
         }
         if (item < items) {
@@ -422,32 +421,22 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
                 }
             }
         }
-        if (done) {   // dq and dk, rounded once
+        if (done) {   // dq and dk, rounded once: eight bytes a lane, the waves' make up whole rows in L2
+            Args& p = args_again();
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
+            const int64_t at = ((row0 * p.T + tok0 + jj) * p.Hq + hq0) * DK + 16 * w + 4 * g;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                char* to = smem + GL::OUT + (16 * m + jj) * GL::OS + 2 * (16 * w + 4 * g);
-                *reinterpret_cast<u32x2*>(to) = u32x2{pack_bf2(dq[m][0], dq[m][1]), pack_bf2(dq[m][2], dq[m][3])};
-                *reinterpret_cast<u32x2*>(to + 64 * GL::OS) = u32x2{pack_bf2(dk[m][0], dk[m][1]), pack_bf2(dk[m][2], dk[m][3])};
+                if (16 * m + jj < rows0) {
+                    const int64_t to = at + (int64_t)16 * m * p.Hq * DK;
+                    *reinterpret_cast<u32x2*>(p.dq + to) = u32x2{pack_bf2(dq[m][0], dq[m][1]), pack_bf2(dq[m][2], dq[m][3])};
+                    *reinterpret_cast<u32x2*>(p.dk + to) = u32x2{pack_bf2(dk[m][0], dk[m][1]), pack_bf2(dk[m][2], dk[m][3])};
+                }
                 dq[m] = dk[m] = z4;
             }
         }
-        lds_barrier();   // k, q and the planes are read, dq and dk complete
-        if (done) {
-            if (item < items) dma_kq();
-            Args& p = args_again();
-            const int t = opaque(tid);
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const int i = 32 * (h & 1) + (t >> 4), pc = t & 15;
-                if (i < rows0) {
-                    uint16_t* dst = (h < 2 ? p.dq : p.dk) + ((row0 * p.T + tok0 + i) * p.Hq + hq0) * DK + 8 * pc;
-                    *reinterpret_cast<u32x4*>(dst) = *reinterpret_cast<const u32x4*>(
-                        smem + GL::OUT + (h < 2 ? 0 : 64 * GL::OS) + i * GL::OS + 16 * pc);
-                }
-            }
-            lds_barrier();   // read before the next unit's parts are written there
-        }
+        lds_barrier();   // k, q and the planes are read
+        if (done && item < items) dma_kq();
     }
 }
 

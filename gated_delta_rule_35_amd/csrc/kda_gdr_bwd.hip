@@ -18,6 +18,14 @@
 // 4 g + r (g = lane / 16), so that the two tiles of a 32-channel step list the lane's
 // eight channels as they lie in K's rows.
 //   fp32 operands go in as three bf16 parts, see kda_gdr_device.h.
+//
+// At B=2 H=64 T=8192 both walks are bound by HBM: forwards 495 us, 2.45 GB at 4.9 TB/s, of
+// which 1.6 GB are S and u; reverse 685 us, 3.3 GB at 4.8 TB/s.  With few sequences and heads
+// they are bound by the chain of a chunk: at T=1000 on 8 heads 45 and 62 us, 2.8 and 3.9 us
+// a chunk.  There the order of the matrix instructions counts: four to six tiles side by
+// side with the next operands read and split meanwhile took the reverse walk from 70 to 62
+// us; T and A placed so that their transposed reads meet each bank twice instead of four
+// times are part of it.
 #include "kda_gdr_device.h"
 
 namespace kda {
@@ -159,6 +167,8 @@ struct Bool {
 
 // One loading wave's (ld = 0, 1) half of a chunk's DMA into a buffer: 32 pieces of
 // tiles and slices, and nrec of the record.
+// PACED: with a pause of 64 clocks before each piece, so that the walking waves' stores need
+// not wait for all of them (backward at T=1000 on 8 heads 157 -> 154 us; no change on full batches).
 template <int NREC, bool WITH_Q, bool PACED>
 __device__ __forceinline__ void load_chunk(const GdrParams& p, const Rows& vsrc, uint32_t lds, int64_t row, int64_t tok,
                                            int rows, int hq, int hv, int sl, int64_t slot, int ld, int lane) {

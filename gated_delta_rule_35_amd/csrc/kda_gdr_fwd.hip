@@ -27,6 +27,12 @@
 // are then a few times those at most, and |T| <= 2.  An entry keeps its 22 bits down to
 // 2^-4 to 2^-12 of the largest, and is off by 2^-25 in these units below that, 2^-27 to
 // 2^-35 of the largest.
+//
+// At B=2 H=64 T=8192 the walk takes 385 us, 1.43 GB at 3.7 TB/s: a chunk is 5,700 clocks,
+// in which a SIMD issues the vector instructions of one walking and one staging wave, about
+// 1,000, and 104 matrix instructions.  Tried without gain: the next step's operands read
+// ahead and the products of four tiles side by side (each wave waits less, the SIMD issues
+// the same), v, T and A by DMA two chunks ahead, k and q fetched two chunks ahead.
 #include "kda_gdr_device.h"
 
 namespace kda {

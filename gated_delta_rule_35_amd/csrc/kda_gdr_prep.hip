@@ -10,13 +10,21 @@
 //
 // One 256-thread work-group per (chunk slot, q/k head) walks the group's value heads.
 // k and q come into LDS by DMA, where M and A go once the products are formed.  Wave w
-// takes the diagonal tile (w, w) of both and one or two of the six below.  T in fp32:
-// wave w inverts the diagonal block w by forward substitution, then forms block column w downwards on v_mfma_f32_16x16x4f32,
+// takes the diagonal tile (w, w) of both and one or two of the six below.  T in fp32: wave
+// w inverts the diagonal block w by forward substitution, then forms block column w
+// downwards on v_mfma_f32_16x16x4f32,
 //   T_IJ = -T_II sum_{K=J}^{I-1} M_IK T_KJ,
 // with the T_KJ of its column in registers (an accumulator tile is the next product's
 // B operand).  T and A leave as operand fragments: for the backward in three bf16 parts
 // each; for the forward T in two fp16 parts and A in one, without the scale and divided
 // by the powers of two that the scan divides q's and k's rows by.
+//
+// At B=2 H=64 T=8192 (16,384 chunks of a head): forward 203 us, 0.94 GB at 4.6 TB/s; with the
+// backward's records 207 us, 1.22 GB at 5.9 TB/s (part of what it writes stays in the
+// last-level cache).  What brought it there from 332 us: four work-groups a compute unit, k
+// and q by DMA, and the tiles dealt evenly; a form that kept M and A beside k and q in LDS
+// (two work-groups a unit) took 292 us.  Forming the operands inside the walk instead, a
+// work-group for both, took 848 us and more for 680 us of the two kernels then.
 // Fragment (m, kk) holds in lane l rows 16 m + l % 16, columns 32 kk + 16 (s / 4) +
 // 4 (l / 16) + s % 4, s < 8: the order in which accumulator tiles list a 32-wide k
 // step.  The lists hold (0,0) (1,0) (2,0) (2,1) (3,0) (3,1), zeros above the diagonal.

@@ -11,6 +11,9 @@
 // rows, and a work-group takes 16 rows at a time.  The sum over a row is four lane
 // exchanges; a rotation's partner channel is in the same lane (adjacent pairs) or in the
 // lane half / 8 away (half pairs).  Sums and products are fp32, rounded once at the end.
+// At 16,384 tokens of 64 + 64 heads 175 us (1.07 GB, 6.1 TB/s, of which the last-level cache
+// holds a part); gradients with weights and rotation at 8192 tokens of 64 + 16 heads 109 us
+// (0.51 GB, 4.7 TB/s).  Small calls take 3 to 4 us on the device and are bound by their launch.
 // Weight gradients: each lane sums its eight channels over the rows of its work-group's
 // stride, work-groups leave 128 sums each, and a second launch adds those in a fixed
 // order (no atomics).

@@ -272,6 +272,72 @@ def test_strided_inputs_match_contiguous_ones():
     assert torch.equal(a, b) and torch.equal(sa, sb)
 
 
+def test_broadcast_heads_and_batches():
+    """q, k and v that are one head or one row of the batch, seen as many (strides of 0)."""
+    say("gdr fwd and bwd on expanded views")
+    x = ref.cuda(ref.make(1, 90, 1, 1, h0=False, seed=41))
+    g, beta = -torch.rand(2, 90, 4, device="cuda"), torch.rand(2, 90, 4, device="cuda")
+    q, k = (x[n].expand(2, 90, 2, 128) for n in "qk")
+    v = x["v"].expand(2, 90, 4, 128)
+    do = torch.randn(1, 90, 1, 128, device="cuda").bfloat16().expand(2, 90, 4, 128)
+    a = kda_gdr_fwd(q, k, v, g, beta, SCALE, final_state=True)
+    b = kda_gdr_fwd(*(t.contiguous() for t in (q, k, v)), g, beta, SCALE, final_state=True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    a = kda_gdr_bwd(q, k, v, g, beta, SCALE, do)
+    b = kda_gdr_bwd(*(t.contiguous() for t in (q, k, v)), g, beta, SCALE, do.contiguous())
+    assert all(torch.equal(a[n], b[n]) for n in ("dq", "dk", "dv", "dg", "dbeta"))
+
+
+def test_nothing_to_do():
+    """No tokens, no sequences, only empty sequences, no rows: states pass through, nothing
+    else is written."""
+    say("gdr fwd, bwd and decode without tokens or sequences")
+    h0 = torch.randn(2, 4, 128, 128, device="cuda")
+    e = lambda *s, t=torch.bfloat16: torch.empty(*s, dtype=t, device="cuda")  # noqa: E731
+    x = (e(2, 0, 2, 128), e(2, 0, 2, 128), e(2, 0, 4, 128), e(2, 0, 4, t=torch.float32), e(2, 0, 4, t=torch.float32), SCALE)
+    o, hT = kda_gdr_fwd(*x, initial_state=h0, final_state=True)
+    assert o.shape == (2, 0, 4, 128) and torch.equal(hT, h0)
+    assert torch.equal(kda_gdr_fwd(*x, final_state=True)[1], torch.zeros_like(h0))
+    assert torch.equal(kda_gdr_bwd(*x, x[2], d_final_state=h0, d_initial_state=True)["dh0"], h0)
+    for cu in ([0], [0, 0, 0]):   # no sequence; two empty ones
+        y = ref.cuda(ref.make(1, 70, 2, 4, seed=43))
+        cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        n = len(cu) - 1
+        out, do = torch.full_like(y["v"], NAN), torch.zeros_like(y["v"])
+        _, hT = kda_gdr_fwd(*args(y), cu_seqlens=cu, initial_state=h0[:n], out=out, final_state=True)
+        assert torch.isnan(out).all() and torch.equal(hT, h0[:n])
+        grads = {m: torch.full_like(y[s], NAN) for m, s in (("dq", "q"), ("dk", "k"), ("dv", "v"), ("dg", "g"),
+                                                            ("dbeta", "beta"))}
+        got = kda_gdr_bwd(*args(y), do, d_final_state=h0[:n], d_initial_state=True, grads=grads, cu_seqlens=cu)
+        assert all(torch.isnan(got[m]).all() for m in grads) and torch.equal(got["dh0"], h0[:n])
+    o, s = kda_gdr_decode(e(0, 2, 128), e(0, 2, 128), e(0, 4, 128), e(0, 4, t=torch.float32), e(0, 4, t=torch.float32),
+                          SCALE, h0.clone(), state_indices=e(0, t=torch.int32))
+    assert o.shape == (0, 4, 128) and torch.equal(s, h0)
+
+
+def test_rows_in_no_sequence_are_not_read():
+    """NaN in every input of rows behind the last sequence reaches nothing."""
+    say("gdr fwd and bwd, NaN behind the last sequence")
+    x = ref.make(1, 150, 1, 2, h0=True, N=2, seed=45)
+    cu = torch.tensor([0, 70, 141], dtype=torch.int32)
+    for n in ("q", "k", "v", "g", "beta"):
+        x[n][0, 141:] = NAN
+    d = ref.cuda(x)
+    out, hT = kda_gdr_fwd(*args(d), cu_seqlens=cu.cuda(), initial_state=d["h0"], out=torch.full_like(d["v"], 7.0),
+                          final_state=True)
+    do = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(3)).bfloat16()
+    do[0, 141:] = NAN
+    got = kda_gdr_bwd(*args(d), do.cuda(), initial_state=d["h0"], d_initial_state=True, cu_seqlens=cu.cuda())
+    torch.cuda.synchronize()
+    assert (out[0, 141:] == 7).all() and torch.isfinite(hT).all()
+    want, _ = ref.forward(x, SCALE, cu)
+    ref.assert_rows(out[:, :141], want[:, :141], "o", half=ref.forward_magnitude(x, SCALE, cu)[:, :141])
+    grads = ref.gradients(x, SCALE, do, None, cu)
+    for n, m in (("dq", "q"), ("dk", "k"), ("dv", "v")):
+        ref.assert_rows(got[n][:, :141], grads[m][:, :141], n)
+    assert torch.isfinite(got["dh0"]).all()
+
+
 def test_repeats_aliases_and_streams():
     """Runs are bitwise equal: again, with the final state over the initial one, with a
     caller's workspace, on another stream; two workspaces on two streams at once."""

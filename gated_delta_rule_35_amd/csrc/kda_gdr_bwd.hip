@@ -99,7 +99,10 @@ __device__ __forceinline__ void tile_times_state(const char* tile, const f32x4 (
         a[m] = f32x4{0.f, 0.f, 0.f, 0.f};
         f[0][m] = row_frag(tile, m, 0, g, jj);
     }
-    auto split = [&](int kk, int i) { split_pair<3>(sb[kk & 1], i, S[2 * kk + (i >> 1)][2 * (i & 1)], S[2 * kk + (i >> 1)][2 * (i & 1) + 1]); };
+    auto split = [&](int kk, int i) {
+        const f32x4& s = S[2 * kk + (i >> 1)];
+        split_pair<3>(sb[kk & 1], i, s[2 * (i & 1)], s[2 * (i & 1) + 1]);
+    };
 #pragma unroll
     for (int i = 0; i < 4; ++i) split(0, i);
     __builtin_amdgcn_sched_barrier(0);
@@ -160,6 +163,7 @@ __device__ __forceinline__ void tri_times(F fragment, const f32x4 (&x)[4], f32x4
     for (int m = 0; m < 4; ++m) y[m] = (M[4] == m) ? a[m] + a[4] : (M[5] == m) ? a[m] + a[5] : a[m];
 }
 
+// A choice made when compiling, as an argument.
 template <bool X>
 struct Bool {
     static constexpr bool value = X;
@@ -234,8 +238,8 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_keep_kernel(const GdrPar
         constexpr int NREC = 19;   // pieces of the record that are read: T and the numbers
         const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(smem));
         auto load = [&](int c, auto paced) {
-            load_chunk<NREC, false, paced.value>(p, p.v, lds + (c & 1) * L::BYTES, row, bos + (int64_t)c * CH, rows_of(c), hq, hv,
-                                        sl, slot0 + c, w - 4, lane);
+            load_chunk<NREC, false, paced.value>(p, p.v, lds + (c & 1) * L::BYTES, row, bos + (int64_t)c * CH,
+                                                 rows_of(c), hq, hv, sl, slot0 + c, w - 4, lane);
         };
         if (nch > 0) load(0, Bool<false>());
         for (int c = 0; c < nch; ++c) {
@@ -256,7 +260,7 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_keep_kernel(const GdrPar
     for (int c = 0; c < nch; ++c) {
         lds_barrier();   // chunk c is in LDS, and the other buffer's reads are done
         char* buf = smem + (c & 1) * L::BYTES;
-        const char *sK = buf + L::K, *sQ = buf + L::Q, *rec = buf + L::REC;
+        const char *sK = buf + L::K, *rec = buf + L::REC;
         const float* sc = reinterpret_cast<const float*>(rec + GDR_SC);
         // x = beta (v - e^G K S)
         f32x4 x[4];
@@ -333,8 +337,8 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_rscan_kernel(const GdrPa
     if (w >= 4) {
         const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(smem));
         auto load = [&](int c, auto paced) {
-            load_chunk<NREC, true, paced.value>(p, p.dO, lds + (c & 1) * L::BYTES, row, bos + (int64_t)c * CH, rows_of(c),
-                                              hq, hv, sl, slot0 + c, w - 4, lane);
+            load_chunk<NREC, true, paced.value>(p, p.dO, lds + (c & 1) * L::BYTES, row, bos + (int64_t)c * CH,
+                                                 rows_of(c), hq, hv, sl, slot0 + c, w - 4, lane);
         };
         if (nch > 0) load(nch - 1, Bool<false>());
         for (int c = nch - 1; c >= 0; --c) {

@@ -1,11 +1,12 @@
 // Device helpers of the gated delta rule with one decay per head.
 //
-// Every matrix product runs on v_mfma_f32_16x16x32_bf16.  q, k, v and the output's
-// gradient are bf16 and enter as they are; an fp32 operand enters as the sum of
-// bf16 parts (each the rounding of what the parts before it leave), so that
-// products keep fp32's accuracy at a third to a sixth of the bf16 rate, which is
-// still several times the rate of the fp32 matrix instructions: three parts hold
-// all 24 bits, two hold 16.
+// Matrix products run on the 16x16x32 instructions for 16-bit operands.  q, k, v and the
+// output's gradient are bf16; an fp32 operand enters as the sum of parts, each the rounding
+// of what the parts before it leave, so that products keep fp32's accuracy at a third to a
+// sixth of the 16-bit rate, several times that of the fp32 matrix instructions.  The prep
+// kernel and the backward use bf16 parts, three of which hold all 24 bits at any size; the
+// forward's walk uses fp16 parts, two of which hold 22 bits of what powers of two keep in
+// range, with q and k turned into fp16 rows divided by powers of two.
 #pragma once
 #include "kda_device.h"
 #include "kda_gdr.h"
@@ -55,21 +56,6 @@ template <int NS>
 __device__ __forceinline__ Split<NS> split_acc(f32x4 a, f32x4 b) {
     const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
     return split8<NS>(x);
-}
-
-// c += A B with A given in NA parts and B in NB; products of parts whose weights
-// are below 2^-8 LIM of the leading product's are left out (LIM = 3: what 24 bits
-// hold, LIM = 2: what 16 bits hold).  The small products come first.
-template <int LIM, int NA, int NB>
-__device__ __forceinline__ f32x4 mfma_split(const bf16x8 (&a)[NA], const Split<NB>& b, f32x4 c) {
-#pragma unroll
-    for (int d = LIM - 1; d >= 0; --d) {
-#pragma unroll
-        for (int i = 0; i < NA; ++i) {
-            if (d - i >= 0 && d - i < NB) c = mfma_bf(a[i], b.s[d - i], c);
-        }
-    }
-    return c;
 }
 
 // ---- fp16 operands ----
@@ -125,7 +111,8 @@ __device__ __forceinline__ float row_power(const bf16x8 (&x)[4]) {
 
 // Per-token rows of a record's numbers, in elements: e^G, e^{G_last - G}, beta,
 // e^{G_last}; forward also beta e^G 2^ek, 2^ek, 2^eq (what the scan divides the token's k
-// and q by; 2^ek is 0 for a key of zeros, whose u takes no part) and the chunk's largest 2^ek, within 2^-60 and 2^60 (0: all its keys are zero).
+// and q by; 2^ek is 0 for a key of zeros, whose u takes no part) and the chunk's largest
+// 2^ek, within 2^-60 and 2^60 (0: all its keys are zero).
 enum { SC_EG = 0, SC_GA = 64, SC_BE = 128, SC_EL = 192, SC_EGK = 256, SC_KS = 320, SC_QS = 384, SC_KP = 448 };
 
 // ---- swizzled [64][128] bf16 tiles in LDS: rows of 256 bytes, whose sixteen 16-byte

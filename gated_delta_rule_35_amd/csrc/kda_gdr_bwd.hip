@@ -65,22 +65,6 @@ __device__ __forceinline__ bf16x8 tri_col_frag(const char* part, int m, int kk, 
                 lds_tr(part + tri_frag(2 * kk + 1, m >> 1) * GDR_FRAG + at));
 }
 
-// The order of a stretch of code that ends here: after each of N matrix instructions up to
-// VALU vector instructions, DS reads of LDS and VM stores.  Left to itself the compiler
-// forms one tile after the other, each a chain of dependent matrix instructions that waits
-// for its operands in between.
-template <int N, int VALU, int DS, int VM>
-__device__ __forceinline__ void interleave() {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        if (VALU) __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
-        if (DS) __builtin_amdgcn_sched_group_barrier(0x100, DS, 0);
-        if (VM) __builtin_amdgcn_sched_group_barrier(0x040, VM, 0);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-}
-
 // a[m] = rows 16 m .. of the tile times S, four tiles side by side, while the next step's
 // operands are read and split; S is stored first, by all waves at once (two waves make up a
 // 128-byte line): spread over the products, the stores cost the keeping walk at B=2 H=64

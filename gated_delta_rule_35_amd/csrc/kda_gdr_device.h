@@ -59,6 +59,8 @@ __device__ __forceinline__ Split<NS> split_acc(f32x4 a, f32x4 b) {
 }
 
 // ---- fp16 operands ----
+// 1 / x of a power of two within 2^-126 and 2^126.
+__device__ __forceinline__ float inverse2(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
 __device__ __forceinline__ f32x4 mfma_h(half8 a, half8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
@@ -166,6 +168,22 @@ __device__ __forceinline__ void dma_tile(__amdgpu_buffer_rsrc_t r, uint32_t lds,
 __device__ __forceinline__ int opaque(int x) {
     asm volatile("" : "+v"(x));
     return x;
+}
+
+// The order of a stretch of code that ends here: after each of N matrix instructions up to
+// VALU vector instructions, DS reads of LDS and VM stores.  Left to itself the compiler
+// forms one tile after the other, each a chain of dependent matrix instructions that waits
+// for its operands in between.
+template <int N, int VALU, int DS, int VM>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (VALU) __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+        if (DS) __builtin_amdgcn_sched_group_barrier(0x100, DS, 0);
+        if (VM) __builtin_amdgcn_sched_group_barrier(0x040, VM, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 // ---- chunks ----

@@ -28,11 +28,11 @@
 // 2^-4 to 2^-12 of the largest, and is off by 2^-25 in these units below that, 2^-27 to
 // 2^-35 of the largest.
 //
-// At B=2 H=64 T=8192 the walk takes 385 us, 1.43 GB at 3.7 TB/s: a chunk is 5,700 clocks,
+// At B=2 H=64 T=8192 the walk takes 375 us, 1.43 GB at 3.8 TB/s: a chunk is 5,500 clocks,
 // in which a SIMD issues the vector instructions of one walking and one staging wave, about
-// 1,000, and 104 matrix instructions.  Tried without gain: the next step's operands read
-// ahead and the products of four tiles side by side (each wave waits less, the SIMD issues
-// the same), v, T and A by DMA two chunks ahead, k and q fetched two chunks ahead.
+// 850 of four clocks, and 104 matrix instructions; the walking wave goes first (s_setprio).
+// Products of four tiles side by side, v, T and A by DMA two chunks ahead, the priority and
+// inverses of powers of two by integer subtraction brought 586 us of the whole call to 571.
 #include "kda_gdr_device.h"
 
 namespace kda {
@@ -40,11 +40,13 @@ namespace kda {
 namespace {
 
 constexpr int FT = 512;
-// One slot: K, Q tiles (fp16, swizzled), v's slice [64][64] bf16 (o's on the way out), T
-// and A fragments, per-token numbers.
+// Two slots of what passes through the staging waves' registers: K, Q tiles (fp16, swizzled)
+// and per-token numbers; three of what comes by DMA, a chunk further ahead: v's slice
+// [64][64] bf16 (o's on the way out), T and A fragments.
 struct FL {
-    static constexpr int K = 0, Q = 16384, V = 32768, T = 40960, A = T + 2 * GDR_TRI, SC = A + GDR_TRI,
-                         BYTES = SC + FWD_ROWS * 256;
+    static constexpr int K = 0, Q = 16384, SC = 32768, STAGED = SC + FWD_ROWS * 256;
+    static constexpr int V = 0, T = 8192, A = T + 2 * GDR_TRI, DMA = A + GDR_TRI;
+    static constexpr int BYTES = 2 * STAGED + 3 * DMA;
 };
 
 // Channel of row 4 g + r of state tile t.
@@ -72,7 +74,7 @@ __device__ __forceinline__ float max_abs(float m, f32x4 x) {
 }  // namespace
 
 __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
-    __shared__ __attribute__((aligned(1024))) char smem[2 * FL::BYTES];
+    __shared__ __attribute__((aligned(1024))) char smem[FL::BYTES];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const Walk walk = walk_of_block(p, (int)blockIdx.x, reinterpret_cast<int*>(smem));
@@ -115,9 +117,9 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
             sc[0] = s[128 * w + ln];
             sc[1] = s[128 * w + 64 + ln];
         };
-        auto dma = [&](int c) {   // v, T and A
+        auto dma = [&](int c, int slot) {   // v, T and A
             const int ln = opaque(lane);
-            const uint32_t to = lds + (c & 1) * FL::BYTES;
+            const uint32_t to = lds + 2 * FL::STAGED + slot * FL::DMA;
             const __amdgpu_buffer_rsrc_t rv = chunk_rsrc(
                 p.v.p + row * p.v.sb + (bos + (int64_t)c * CH) * p.v.st + hv * p.v.sh + 64 * sl, p.v.st, rows_of(c), 64);
 #pragma unroll
@@ -143,9 +145,9 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
         };
         auto stage = [&](int c) {
             const int ln = opaque(lane), r = 16 * w + (ln >> 4);
-            char* to = smem + (c & 1) * FL::BYTES;
+            char* to = smem + (c & 1) * FL::STAGED;
             float* out = reinterpret_cast<float*>(to + FL::SC);
-            const float kinv = kp > 0.f ? 1.f / kp : 1.f, qinv = 1.f / qp;   // powers of two
+            const float kinv = kp > 0.f ? inverse2(kp) : 1.f, qinv = inverse2(qp);
             if (km > 0.f) kap = km;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -155,18 +157,21 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
             }
             // beta e^G 2^ek kap and 2^ek / kap (rows 4 and 5: wave 2)
             out[128 * w + ln] = sc[0] * (w == 2 ? kap : 1.f);
-            out[128 * w + 64 + ln] = sc[1] * (w == 2 ? 1.f / kap : 1.f);
+            out[128 * w + 64 + ln] = sc[1] * (w == 2 ? inverse2(kap) : 1.f);
         };
         if (nch > 0) {
-            dma(0);
+            dma(0, 0);
             fetch(0);
             stage(0);
-            if (nch > 1) fetch(1);
+            if (nch > 1) {
+                dma(1, 1);
+                fetch(1);
+            }
         }
         // o of chunk c (64 rows of 64 channels where v was): the rows whose place this wave's DMA takes next
-        auto store_o = [&](int c) {
+        auto store_o = [&](int c, int slot) {
             const int ln = opaque(lane), rows = rows_of(c);
-            const char* tv = smem + (c & 1) * FL::BYTES + FL::V;
+            const char* tv = smem + 2 * FL::STAGED + slot * FL::DMA + FL::V;
             u32x4 y[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) y[u] = *reinterpret_cast<const u32x4*>(tv + (2 * w + u) * 1024 + ln * 16);
@@ -179,24 +184,30 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
             }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         };
+        int slot = 2;   // of chunk c + 2, and of c - 1
         for (int c = 0; c < nch; ++c) {
-            // v, T and A of chunk c have landed; the thirteen loads for chunk c + 1, issued later, may be on their way
-            if (c + 1 < nch) asm volatile("s_waitcnt vmcnt(13)" ::: "memory");
+            // v, T and A of chunk c have landed; six or seven pieces and thirteen loads for chunk
+            // c + 1, issued later, may be on their way
+            if (c + 1 < nch) asm volatile("s_waitcnt vmcnt(19)" ::: "memory");
             else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             lds_barrier();
-            if (c > 0) store_o(c - 1);
+            if (c > 0) store_o(c - 1, slot);
             if (c + 1 < nch) {
                 stage(c + 1);   // before the DMA: what it reads is the only thing it waits for
-                dma(c + 1);
-                if (c + 2 < nch) fetch(c + 2);
+                if (c + 2 < nch) {
+                    dma(c + 2, slot);
+                    fetch(c + 2);
+                }
             }
+            slot = slot == 2 ? 0 : slot + 1;
         }
         lds_barrier();
-        if (nch > 0) store_o(nch - 1);
+        if (nch > 0) store_o(nch - 1, slot);
         return;
     }
 
     // ================= scan waves =================
+    __builtin_amdgcn_s_setprio(3);
     const int w = wave;
     const int64_t so = ((int64_t)n * p.Hv + hv) * DK * DK + 64 * sl + 16 * w + (lane & 15);
     f32x4 S[8];                     // the state times down / kap
@@ -221,20 +232,22 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
 #pragma unroll
             for (int m = 0; m < 4; ++m) x[m] *= by;
             down *= by;
-            up = 1.f / down;
+            up = inverse2(down);
         }
     };
+    int third = 0;   // chunk c's slot of three
     for (int c = 0; c < nch; ++c) {
-        lds_barrier();   // chunk c is in LDS, and the other slot's reads are done
+        lds_barrier();   // chunk c is in LDS, and the other slots' reads are done
         const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
-        char* slot = smem + (c & 1) * FL::BYTES;
-        const char *tk = slot + FL::K, *tq = slot + FL::Q;
+        char* slot = smem + 2 * FL::STAGED + third * FL::DMA;
+        third = third == 2 ? 0 : third + 1;
+        const char *tk = smem + (c & 1) * FL::STAGED + FL::K, *tq = tk + FL::Q;
         char* tv = slot + FL::V;
-        const float* sc = reinterpret_cast<const float*>(slot + FL::SC);
+        const float* sc = reinterpret_cast<const float*>(tk + FL::SC);
         const float km = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(sc[SC_KP])));
         if (km > 0.f && km != kap) {   // powers of two: exact
 #pragma unroll
-            for (int t = 0; t < 8; ++t) S[t] *= kap / km;
+            for (int t = 0; t < 8; ++t) S[t] *= kap * inverse2(km);
             kap = km;
         }
         f32x4 v[4];   // beta v
@@ -250,47 +263,72 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
         for (int m = 0; m < 4; ++m) top = max_abs(top, v[m]);
         if (__any(top > 1024.f || (top < 4.f && top > 0.f))) rescale(top, v);
         const float whole = up * kap * p.scale;   // what o's sums are multiplied by
-        // x = beta v - beta e^G K S and e^G Q S
+        // x = beta v - beta e^G K S and e^G Q S, eight tiles side by side; the next step's
+        // operands are read and split meanwhile
         f32x4 x[4], o[4];
         {
-            HSplit<2> sb[4];
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) sb[kk] = hsplit<2>(S[2 * kk], S[2 * kk + 1]);
+            half8 fk[2][4], fq[2][4];
+            HSplit<2> sb[2];
+            sb[0] = hsplit<2>(S[0], S[1]);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
+                fk[0][m] = row_frag(tk, m, 0, g, jj);
+                fq[0][m] = row_frag(tq, m, 0, g, jj);
+                x[m] = o[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    const half8 f = row_frag(tk, m, kk, g, jj);
-                    a = mfma_h(f, sb[kk].s[1], a);
-                    b = mfma_h(row_frag(tq, m, kk, g, jj), sb[kk].s[0], b);
-                    a = mfma_h(f, sb[kk].s[0], a);
+            for (int kk = 0; kk < 4; ++kk) {
+                const int now = kk & 1, next = now ^ 1;
+                if (kk < 3) {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        fk[next][m] = row_frag(tk, m, kk + 1, g, jj);
+                        fq[next][m] = row_frag(tq, m, kk + 1, g, jj);
+                    }
+                    sb[next] = hsplit<2>(S[2 * kk + 2], S[2 * kk + 3]);
                 }
-                x[m] = v[m] - sc4(sc, SC_EGK, m, g) * a;
-                o[m] = sc4(sc, SC_EG, m, g) * b;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) x[m] = mfma_h(fk[now][m], sb[now].s[1], x[m]);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) o[m] = mfma_h(fq[now][m], sb[now].s[0], o[m]);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) x[m] = mfma_h(fk[now][m], sb[now].s[0], x[m]);
+                interleave<12, 2, 1, 0>();
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                x[m] = v[m] - sc4(sc, SC_EGK, m, g) * x[m];
+                o[m] *= sc4(sc, SC_EG, m, g);
             }
         }
-        // u = T x, times 2^ek / kap
+        // u = T x, times 2^ek / kap: six tiles side by side
         f32x4 u[4];
+        constexpr int TM[6] = {0, 1, 2, 3, 2, 3}, TK[6] = {0, 0, 0, 0, 1, 1};   // fragments (m, kk)
         {
-            HSplit<2> xb[2];
+            half8 th[6], tl[6];
+            f32x4 a[6];
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) xb[kk] = hsplit<2>(x[2 * kk], x[2 * kk + 1]);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                f32x4 a = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int kk = 0; kk <= m / 2; ++kk) {
-                    const char* f = slot + FL::T + tri_frag(m, kk) * GDR_FRAG + ln * 16;
-                    const half8 th = *reinterpret_cast<const half8*>(f), tl = *reinterpret_cast<const half8*>(f + GDR_TRI);
-                    a = mfma_h(tl, xb[kk].s[0], a);
-                    a = mfma_h(th, xb[kk].s[1], a);
-                    a = mfma_h(th, xb[kk].s[0], a);
-                }
-                u[m] = a * sc4(sc, SC_KS, m, g);
+            for (int i = 0; i < 6; ++i) {
+                const char* f = slot + FL::T + tri_frag(TM[i], TK[i]) * GDR_FRAG + ln * 16;
+                th[i] = *reinterpret_cast<const half8*>(f);
+                tl[i] = *reinterpret_cast<const half8*>(f + GDR_TRI);
+                a[i] = f32x4{0.f, 0.f, 0.f, 0.f};
             }
+            const HSplit<2> xb[2] = {hsplit<2>(x[0], x[1]), hsplit<2>(x[2], x[3])};
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < 6; ++i) a[i] = mfma_h(tl[i], xb[TK[i]].s[0], a[i]);
+#pragma unroll
+            for (int i = 0; i < 6; ++i) a[i] = mfma_h(th[i], xb[TK[i]].s[1], a[i]);
+#pragma unroll
+            for (int i = 0; i < 6; ++i) a[i] = mfma_h(th[i], xb[TK[i]].s[0], a[i]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) u[m] = (m < 2 ? a[m] : a[m] + a[m + 2]) * sc4(sc, SC_KS, m, g);
         }
-        // S <- e^{G_last} S + K^T (e^{G_last - G} u)
+        // S <- e^{G_last} S + K^T (e^{G_last - G} u), four tiles side by side; between them
+        // o's second part, rounded once, into this wave's columns of v's slice: the staging
+        // waves store it
         {
             f32x4 wu[4];
             float tw = 0.f;
@@ -304,38 +342,47 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
                 for (int t = 0; t < 8; ++t) tw = max_abs(tw, S[t]);
                 rescale(tw, wu);
             }
-            HSplit<2> wb[2];
+            const HSplit<2> wb[2] = {hsplit<2>(wu[0], wu[1]), hsplit<2>(wu[2], wu[3])};
+            const HSplit<1> ub[2] = {hsplit<1>(u[0], u[1]), hsplit<1>(u[2], u[3])};
+            half8 f[2][4], fa[6];
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) wb[kk] = hsplit<2>(wu[2 * kk], wu[2 * kk + 1]);
+            for (int t = 0; t < 4; ++t) f[0][t] = col_frag(tk, t, 0, g, jj);
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                f32x4 a = S[t];
+            for (int i = 0; i < 6; ++i)
+                fa[i] = *reinterpret_cast<const half8*>(slot + FL::A + tri_frag(TM[i], TK[i]) * GDR_FRAG + ln * 16);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                    const half8 f = col_frag(tk, t, kk, g, jj);
-                    a = mfma_h(f, wb[kk].s[1], a);
-                    a = mfma_h(f, wb[kk].s[0], a);
+            for (int i = 0; i < 4; ++i) {   // tiles 4 (i / 2) .., k step i & 1
+                const int t0 = 4 * (i >> 1), kk = i & 1;
+                if (i < 3) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) f[kk ^ 1][t] = col_frag(tk, 4 * ((i + 1) >> 1) + t, kk ^ 1, g, jj);
                 }
-                S[t] = a;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) S[t0 + t] = mfma_h(f[kk][t], wb[kk].s[1], S[t0 + t]);
+                if (i == 0) {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) o[m] = mfma_h(fa[m], ub[0].s[0], o[m]);
+                } else if (i == 1) {
+#pragma unroll
+                    for (int m = 2; m < 4; ++m) o[m] = mfma_h(fa[m + 2], ub[1].s[0], o[m]);
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) S[t0 + t] = mfma_h(f[kk][t], wb[kk].s[0], S[t0 + t]);
+                if (i >= 2) {
+#pragma unroll
+                    for (int m = 2 * i - 4; m < 2 * i - 2; ++m) {
+                        o[m] *= sc4(sc, SC_QS, m, g) * whole;
+                        const uint32_t p0 = pack_bf2(o[m][0], o[m][1]), p1 = pack_bf2(o[m][2], o[m][3]);
+                        char* dst = tv + (16 * m + 4 * g) * 128 + 2 * (16 * w + jj);
+                        *reinterpret_cast<uint16_t*>(dst) = (uint16_t)p0;
+                        *reinterpret_cast<uint16_t*>(dst + 128) = (uint16_t)(p0 >> 16);
+                        *reinterpret_cast<uint16_t*>(dst + 256) = (uint16_t)p1;
+                        *reinterpret_cast<uint16_t*>(dst + 384) = (uint16_t)(p1 >> 16);
+                    }
+                }
+                interleave<8, 3, 1, 0>();
             }
-        }
-        // o, rounded once, into this wave's columns of v's slice: the staging waves store it
-        HSplit<1> ub[2];
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) ub[kk] = hsplit<1>(u[2 * kk], u[2 * kk + 1]);
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-#pragma unroll
-            for (int kk = 0; kk <= m / 2; ++kk)
-                o[m] = mfma_h(*reinterpret_cast<const half8*>(slot + FL::A + tri_frag(m, kk) * GDR_FRAG + ln * 16),
-                              ub[kk].s[0], o[m]);
-            o[m] *= sc4(sc, SC_QS, m, g) * whole;
-            const uint32_t p0 = pack_bf2(o[m][0], o[m][1]), p1 = pack_bf2(o[m][2], o[m][3]);
-            char* dst = tv + (16 * m + 4 * g) * 128 + 2 * (16 * w + jj);
-            *reinterpret_cast<uint16_t*>(dst) = (uint16_t)p0;
-            *reinterpret_cast<uint16_t*>(dst + 128) = (uint16_t)(p0 >> 16);
-            *reinterpret_cast<uint16_t*>(dst + 256) = (uint16_t)p1;
-            *reinterpret_cast<uint16_t*>(dst + 384) = (uint16_t)(p1 >> 16);
         }
     }
     lds_barrier();   // the last chunk's o is complete

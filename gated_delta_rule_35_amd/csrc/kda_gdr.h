@@ -51,8 +51,8 @@ constexpr int GDR_T = 0, GDR_SC = 3 * GDR_TRI, GDR_A = GDR_SC + 1024, GDR_REC = 
 
 hipError_t launch_gdr_prep(const GdrParams& p, bool bwd, hipStream_t stream);
 hipError_t launch_gdr_grads(const GdrParams& p, int cus, hipStream_t stream);
-hipError_t launch_gdr_fwd(const GdrParams& p, hipStream_t stream);
 // cus: compute units of the current device.
+hipError_t launch_gdr_fwd(const GdrParams& p, int cus, hipStream_t stream);
 hipError_t launch_gdr_bwd(const GdrParams& p, int cus, hipStream_t stream);
 
 struct GdrDecodeParams {

@@ -201,7 +201,7 @@ kda_status_t kda_gdr_fwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda
     void* ws = workspace;
     if (!ws && need > 0 && hipMallocAsync(&ws, (size_t)need, hs) != hipSuccess) return KDA_ERR_HIP;
     p.rec = static_cast<char*>(ws);
-    hipError_t e = kda::launch_gdr_fwd(p, hs);
+    hipError_t e = kda::launch_gdr_fwd(p, std::max(device_cus(), 1), hs);
     if (!workspace && ws && hipFreeAsync(ws, hs) != hipSuccess && e == hipSuccess) e = hipErrorUnknown;
     return finish(e, hs);
 }

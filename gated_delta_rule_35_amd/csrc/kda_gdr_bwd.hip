@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_keep_kernel(const GdrPar
     __shared__ __attribute__((aligned(1024))) char smem[2 * L::BYTES];
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, jj = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const Walk walk = walk_of_block(p, (int)blockIdx.x, reinterpret_cast<int*>(smem));
+    const Walk walk = walk_of_block<2>(p, (int)blockIdx.x, reinterpret_cast<int*>(smem));
     const int n = walk.n, hv = walk.hv, sl = walk.sl, hq = hv / (p.Hv / p.Hq);
     int64_t bos, len, row, slot0;
     gdr_seq(p, n, bos, len, row, slot0);
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_rscan_kernel(const GdrPa
     __shared__ __attribute__((aligned(1024))) char smem[2 * L::BYTES];
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, jj = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const Walk walk = walk_of_block(p, (int)blockIdx.x, reinterpret_cast<int*>(smem));
+    const Walk walk = walk_of_block<2>(p, (int)blockIdx.x, reinterpret_cast<int*>(smem));
     const int n = walk.n, hv = walk.hv, sl = walk.sl, hq = hv / (p.Hv / p.Hq);
     int64_t bos, len, row, slot0;
     gdr_seq(p, n, bos, len, row, slot0);

@@ -314,17 +314,18 @@ __device__ __forceinline__ float sum64(float x) {
 struct Walk {
     int n, hv, sl;
 };
+template <int SLICES>   // 2, or 1: whole heads
 __device__ __forceinline__ Walk walk_of_block(const GdrParams& p, int b, int* sh) {
     Walk k;
     if ((p.Hv & 7) == 0) {
-        const int per = p.Hv >> 3, rest = b >> 4;
-        k.sl = (b >> 3) & 1;
+        const int per = p.Hv >> 3, rest = b / (8 * SLICES);
+        k.sl = (b >> 3) % SLICES;
         k.n = rest / per;
         k.hv = (b & 7) * per + rest % per;
     } else {
-        k.sl = b & 1;
-        k.n = (b >> 1) / p.Hv;
-        k.hv = (b >> 1) % p.Hv;
+        k.sl = b % SLICES;
+        k.n = b / SLICES / p.Hv;
+        k.hv = b / SLICES % p.Hv;
     }
     if (p.cu && p.N > 1 && p.N <= (int)blockDim.x) {
         const int t = threadIdx.x;

@@ -7,9 +7,9 @@
 // product mixes columns: a wave owns 16 of them for the whole sequence and needs nothing
 // from the others.  Its state is eight 16x16 accumulator tiles (32 registers a lane), and
 // since an accumulator tile holds what a lane needs as B operand, the whole chain of a
-// chunk stays in registers.  A work-group is four such waves (64 value channels) and four
-// that stage the next chunk's left-hand operands in LDS: k and q rows as fp16, v, T and A
-// by DMA; one barrier a chunk.  Tile t = 2 kk + h of the state holds key channel
+// chunk stays in registers.  A work-group is four such waves (half a head, 64 value
+// channels) or eight, and four that stage the next chunk's left-hand operands in LDS: k and
+// q rows as fp16, v, T and A by DMA; one barrier a chunk.  Tile t = 2 kk + h of the state holds key channel
 // 32 kk + 8 g + 4 h + r in row 4 g + r (g = lane / 16), so that the two tiles of a
 // 32-channel step list the lane's eight channels as they lie in K's rows.
 //
@@ -39,14 +39,16 @@ namespace kda {
 
 namespace {
 
-constexpr int FT = 512;
 // Two slots of what passes through the staging waves' registers: K, Q tiles (fp16, swizzled)
-// and per-token numbers; three of what comes by DMA, a chunk further ahead: v's slice
-// [64][64] bf16 (o's on the way out), T and A fragments.
+// and per-token numbers; of what comes by DMA three, a chunk further ahead, or two where
+// there is no room for more: T and A fragments, and v's slices [64][64] bf16 (o's on the way
+// out), one for each half of a head that the work-group walks.
+template <int HALVES>
 struct FL {
     static constexpr int K = 0, Q = 16384, SC = 32768, STAGED = SC + FWD_ROWS * 256;
-    static constexpr int V = 0, T = 8192, A = T + 2 * GDR_TRI, DMA = A + GDR_TRI;
-    static constexpr int BYTES = 2 * STAGED + 3 * DMA;
+    static constexpr int T = 0, A = T + 2 * GDR_TRI, V = A + GDR_TRI, DMA = V + HALVES * 8192;
+    static constexpr int SLOTS = HALVES == 1 ? 3 : 2, BYTES = 2 * STAGED + SLOTS * DMA;
+    static constexpr int THREADS = 256 * HALVES + 256;
 };
 
 // Channel of row 4 g + r of state tile t.
@@ -73,11 +75,13 @@ __device__ __forceinline__ float max_abs(float m, f32x4 x) {
 
 }  // namespace
 
-__global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
-    __shared__ __attribute__((aligned(1024))) char smem[FL::BYTES];
+template <int HALVES>
+__global__ void __launch_bounds__(FL<HALVES>::THREADS) kda_gdr_scan_kernel(const GdrParams p) {
+    typedef FL<HALVES> L;
+    __shared__ __attribute__((aligned(1024))) char smem[L::BYTES];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const Walk walk = walk_of_block(p, (int)blockIdx.x, reinterpret_cast<int*>(smem));
+    const Walk walk = walk_of_block<2 / HALVES>(p, (int)blockIdx.x, reinterpret_cast<int*>(smem));
     const int n = walk.n, hv = walk.hv, sl = walk.sl, hq = hv / (p.Hv / p.Hq);
     int64_t bos, len, row, slot0;
     gdr_seq(p, n, bos, len, row, slot0);
@@ -89,9 +93,9 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
     auto record = [&](int c) -> const char* { return p.rec + ((slot0 + c) * p.Hv + hv) * FWD_REC; };
     float kap = 1.f;   // of the chunk at hand; a chunk of zero keys keeps the one before
 
-    if (wave >= 4) {
+    if (wave >= 4 * HALVES) {
         // ================= staging waves =================
-        const int w = wave - 4;
+        const int w = wave - 4 * HALVES;
         const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(smem));
         i32x4 kr[4], qr[4];   // rows 4 w + l / 16 (mod 16) of the next chunk: one 16-byte piece a lane
         float kp, qp, km, sc[2];
@@ -119,18 +123,19 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
         };
         auto dma = [&](int c, int slot) {   // v, T and A
             const int ln = opaque(lane);
-            const uint32_t to = lds + 2 * FL::STAGED + slot * FL::DMA;
-            const __amdgpu_buffer_rsrc_t rv = chunk_rsrc(
-                p.v.p + row * p.v.sb + (bos + (int64_t)c * CH) * p.v.st + hv * p.v.sh + 64 * sl, p.v.st, rows_of(c), 64);
+            const uint32_t to = lds + 2 * L::STAGED + slot * L::DMA;
+            const __amdgpu_buffer_rsrc_t rv =
+                chunk_rsrc(p.v.p + row * p.v.sb + (bos + (int64_t)c * CH) * p.v.st + hv * p.v.sh + 64 * sl, p.v.st,
+                           rows_of(c), 64 * HALVES);
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-                dma_piece(rv, to + FL::V + (2 * w + u) * 1024,
-                          (int)((8 * (2 * w + u) + (ln >> 3)) * p.v.st * 2) + ((ln & 7) << 4));
+            for (int u = 0; u < 2 * HALVES; ++u)
+                dma_piece(rv, to + L::V + (u >> 1) * 8192 + (2 * w + (u & 1)) * 1024,
+                          (int)((8 * (2 * w + (u & 1)) + (ln >> 3)) * p.v.st * 2) + 128 * (u >> 1) + ((ln & 7) << 4));
             const __amdgpu_buffer_rsrc_t rr = make_rsrc(record(c), FWD_SC);
 #pragma unroll
             for (int u = 0; u < 5; ++u) {   // eighteen pieces
                 const int x = 4 * u + w;
-                if (x < 18) dma_piece(rr, to + FL::T + x * 1024, x * 1024 + ln * 16);
+                if (x < 18) dma_piece(rr, to + L::T + x * 1024, x * 1024 + ln * 16);
             }
         };
         // 16 bytes of bf16 times `by` as fp16
@@ -145,15 +150,15 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
         };
         auto stage = [&](int c) {
             const int ln = opaque(lane), r = 16 * w + (ln >> 4);
-            char* to = smem + (c & 1) * FL::STAGED;
-            float* out = reinterpret_cast<float*>(to + FL::SC);
+            char* to = smem + (c & 1) * L::STAGED;
+            float* out = reinterpret_cast<float*>(to + L::SC);
             const float kinv = kp > 0.f ? inverse2(kp) : 1.f, qinv = inverse2(qp);
             if (km > 0.f) kap = km;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int at = tile_off(r + 4 * x, ln & 15);
-                *reinterpret_cast<u32x4*>(to + FL::K + at) = to_half(kr[x], __shfl(kinv, r + 4 * x));
-                *reinterpret_cast<u32x4*>(to + FL::Q + at) = to_half(qr[x], __shfl(qinv, r + 4 * x));
+                *reinterpret_cast<u32x4*>(to + L::K + at) = to_half(kr[x], __shfl(kinv, r + 4 * x));
+                *reinterpret_cast<u32x4*>(to + L::Q + at) = to_half(qr[x], __shfl(qinv, r + 4 * x));
             }
             // beta e^G 2^ek kap and 2^ek / kap (rows 4 and 5: wave 2)
             out[128 * w + ln] = sc[0] * (w == 2 ? kap : 1.f);
@@ -164,42 +169,43 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
             fetch(0);
             stage(0);
             if (nch > 1) {
-                dma(1, 1);
+                if (L::SLOTS == 3) dma(1, 1);
                 fetch(1);
             }
         }
         // o of chunk c (64 rows of 64 channels where v was): the rows whose place this wave's DMA takes next
         auto store_o = [&](int c, int slot) {
             const int ln = opaque(lane), rows = rows_of(c);
-            const char* tv = smem + 2 * FL::STAGED + slot * FL::DMA + FL::V;
-            u32x4 y[2];
+            const char* tv = smem + 2 * L::STAGED + slot * L::DMA + L::V;
+            u32x4 y[2 * HALVES];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) y[u] = *reinterpret_cast<const u32x4*>(tv + (2 * w + u) * 1024 + ln * 16);
+            for (int u = 0; u < 2 * HALVES; ++u)
+                y[u] = *reinterpret_cast<const u32x4*>(tv + (u >> 1) * 8192 + (2 * w + (u & 1)) * 1024 + ln * 16);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int i = 8 * (2 * w + u) + (ln >> 3);
+            for (int u = 0; u < 2 * HALVES; ++u) {
+                const int i = 8 * (2 * w + (u & 1)) + (ln >> 3);
                 if (i < rows)
                     *reinterpret_cast<u32x4*>(p.o + ((row * p.T + bos + (int64_t)c * CH + i) * p.Hv + hv) * DK + 64 * sl +
-                                              8 * (ln & 7)) = y[u];
+                                              64 * (u >> 1) + 8 * (ln & 7)) = y[u];
             }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         };
-        int slot = 2;   // of chunk c + 2, and of c - 1
+        constexpr int AHEAD = L::SLOTS - 1;
+        int slot = AHEAD;   // of chunk c + AHEAD, and of c - 1
         for (int c = 0; c < nch; ++c) {
-            // v, T and A of chunk c have landed; six or seven pieces and thirteen loads for chunk
-            // c + 1, issued later, may be on their way
-            if (c + 1 < nch) asm volatile("s_waitcnt vmcnt(19)" ::: "memory");
-            else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            // v, T and A of chunk c have landed; what was issued later may be on its way: thirteen loads
+            // for chunk c + 1, before them with three slots six pieces or more of its v, T and A
+            if (c + 1 == nch) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            else if (AHEAD == 2) asm volatile("s_waitcnt vmcnt(19)" ::: "memory");
+            else asm volatile("s_waitcnt vmcnt(13)" ::: "memory");
             lds_barrier();
             if (c > 0) store_o(c - 1, slot);
             if (c + 1 < nch) {
                 stage(c + 1);   // before the DMA: what it reads is the only thing it waits for
-                if (c + 2 < nch) {
-                    dma(c + 2, slot);
-                    fetch(c + 2);
-                }
+                if (c + AHEAD < nch) dma(c + AHEAD, slot);
+                if (c + 2 < nch) fetch(c + 2);
             }
-            slot = slot == 2 ? 0 : slot + 1;
+            slot = slot == AHEAD ? 0 : slot + 1;
         }
         lds_barrier();
         if (nch > 0) store_o(nch - 1, slot);
@@ -208,8 +214,8 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
 
     // ================= scan waves =================
     __builtin_amdgcn_s_setprio(3);
-    const int w = wave;
-    const int64_t so = ((int64_t)n * p.Hv + hv) * DK * DK + 64 * sl + 16 * w + (lane & 15);
+    const int w = wave & 3;   // sixteen columns of half wave / 4 of those that the work-group walks
+    const int64_t so = ((int64_t)n * p.Hv + hv) * DK * DK + 64 * sl + 16 * wave + (lane & 15);
     f32x4 S[8];                     // the state times down / kap
     float down = 1.f, up = 1.f;     // the lane's column: a power of two and its inverse
 #pragma unroll
@@ -235,15 +241,15 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
             up = inverse2(down);
         }
     };
-    int third = 0;   // chunk c's slot of three
+    int at = 0;   // chunk c's slot of what comes by DMA
     for (int c = 0; c < nch; ++c) {
         lds_barrier();   // chunk c is in LDS, and the other slots' reads are done
         const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
-        char* slot = smem + 2 * FL::STAGED + third * FL::DMA;
-        third = third == 2 ? 0 : third + 1;
-        const char *tk = smem + (c & 1) * FL::STAGED + FL::K, *tq = tk + FL::Q;
-        char* tv = slot + FL::V;
-        const float* sc = reinterpret_cast<const float*>(tk + FL::SC);
+        char* slot = smem + 2 * L::STAGED + at * L::DMA;
+        at = at + 1 == L::SLOTS ? 0 : at + 1;
+        const char *tk = smem + (c & 1) * L::STAGED + L::K, *tq = tk + L::Q;
+        char* tv = slot + L::V + (wave >> 2) * 8192;
+        const float* sc = reinterpret_cast<const float*>(tk + L::SC);
         const float km = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(sc[SC_KP])));
         if (km > 0.f && km != kap) {   // powers of two: exact
 #pragma unroll
@@ -310,7 +316,7 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
             f32x4 a[6];
 #pragma unroll
             for (int i = 0; i < 6; ++i) {
-                const char* f = slot + FL::T + tri_frag(TM[i], TK[i]) * GDR_FRAG + ln * 16;
+                const char* f = slot + L::T + tri_frag(TM[i], TK[i]) * GDR_FRAG + ln * 16;
                 th[i] = *reinterpret_cast<const half8*>(f);
                 tl[i] = *reinterpret_cast<const half8*>(f + GDR_TRI);
                 a[i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -349,7 +355,7 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
             for (int t = 0; t < 4; ++t) f[0][t] = col_frag(tk, t, 0, g, jj);
 #pragma unroll
             for (int i = 0; i < 6; ++i)
-                fa[i] = *reinterpret_cast<const half8*>(slot + FL::A + tri_frag(TM[i], TK[i]) * GDR_FRAG + ln * 16);
+                fa[i] = *reinterpret_cast<const half8*>(slot + L::A + tri_frag(TM[i], TK[i]) * GDR_FRAG + ln * 16);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {   // tiles 4 (i / 2) .., k step i & 1
@@ -395,10 +401,20 @@ __global__ void __launch_bounds__(FT) kda_gdr_scan_kernel(const GdrParams p) {
     }
 }
 
-hipError_t launch_gdr_fwd(const GdrParams& p, hipStream_t stream) {
+hipError_t launch_gdr_fwd(const GdrParams& p, int cus, hipStream_t stream) {
     hipError_t e = launch_gdr_prep(p, false, stream);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kda_gdr_scan_kernel, dim3((unsigned)((int64_t)p.N * p.Hv * 2)), dim3(FT), 0, stream, p);
+    // Whole heads share the staging of k, q, T and A, and take 1.75 times a half's time: worth it
+    // where heads alone fill the compute units and no sequence is much longer than the others,
+    // for packed ones taken to be so with four times as many.  Halves and whole heads: 560 and
+    // 502 us at B=4 H=64 T=4096, 152 and 130 at B=32 H=16 T=512, 656 and 484 at 64 packed
+    // sequences of 256 tokens and 64 heads; but 519 and 581 at 11 of 16,384 tokens together, the
+    // longest half of them.
+    const int64_t heads = (int64_t)p.N * p.Hv;
+    if (heads >= (p.cu ? 4 * (int64_t)cus : cus))
+        hipLaunchKernelGGL(kda_gdr_scan_kernel<2>, dim3((unsigned)heads), dim3(FL<2>::THREADS), 0, stream, p);
+    else
+        hipLaunchKernelGGL(kda_gdr_scan_kernel<1>, dim3((unsigned)(2 * heads)), dim3(FL<1>::THREADS), 0, stream, p);
     return hipGetLastError();
 }
 

@@ -95,6 +95,25 @@ def test_forward_packed(lens, tail):
     check_forward(x, cu)
 
 
+@pytest.mark.parametrize("packed", [False, True])
+def test_forward_more_heads_than_compute_units(packed):
+    """Batches whose (sequence, value head) pairs alone fill the GPU, packed ones four times: a
+    work-group then walks both halves of a head."""
+    lens = [0, 1, 200, 64, 65, 3, 130, 128] * 8 if packed else None
+    say(f"gdr_fwd {'packed' if packed else 'B=20'}, Hv=16")
+    x = ref.make(1, sum(lens) + 9, 4, 16, h0=True, N=64, seed=51) if packed else ref.make(20, 150, 4, 16, h0=True, seed=52)
+    cu = torch.tensor([0] + list(torch.tensor(lens).cumsum(0)), dtype=torch.int32) if packed else None
+    pairs = 64 * 16 // 4 if packed else 20 * 16
+    assert pairs >= torch.cuda.get_device_properties(0).multi_processor_count
+    check_forward(x, cu)
+    if not packed:   # the same rows a few at a time, where a work-group walks half a head
+        d = ref.cuda(x)
+        o, h = kda_gdr_fwd(*args(d), initial_state=d["h0"], final_state=True)
+        o1, h1 = kda_gdr_fwd(*(t[3:6] for t in args(d)[:5]), SCALE, initial_state=d["h0"][3:6].contiguous(),
+                             final_state=True)
+        assert torch.equal(o[3:6], o1) and torch.equal(h[3:6], h1)
+
+
 @pytest.mark.parametrize("T", [1, 3, 16, 17, 63, 64, 65, 129, 200])
 def test_backward_lengths(T):
     say(f"gdr_bwd B=2 T={T} Hq=1 Hv=2")

@@ -203,6 +203,9 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
         asm volatile("s_waitcnt vmcnt(8)" ::: "memory");   // this wave's pieces of do, k and q; dS may be on its way
         lds_barrier();
 
+        const int rows0 = rows, hq0 = hq;
+        const int64_t tok0 = tok, row0 = row, gi0 = (row * p.T + tok) * p.Hv + hq * R + r;
+        const bool done = r == R - 1;   // the item's last value head
         // R1, R3, then R2, for channels 16 w + jj
         {
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
@@ -243,6 +246,16 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             }
 #pragma unroll
             for (int n = 0; n < 8; ++n) asm volatile("" : "+v"(ds[n]));   // dS's parts are formed after S's are done with
+            // the next unit, whose inputs are asked for as soon as there are registers or LDS to put
+            // them in: S now
+            if (done) {
+                r = 0;
+                item += gridDim.x;
+                find();
+            } else {
+                ++r;
+            }
+            if (item < items) fetch_state(args_again().S, s);
             f32x4 r2[4];
 #pragma unroll
             for (int m = 0; m < 4; ++m) r2[m] = z4;
@@ -271,18 +284,7 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             ts = sum64(ts);
             if (lane == 0) sh.ts[w] = ts;
         }
-        // the next unit, whose inputs are asked for bit by bit from here on: S now
-        const int rows0 = rows, hq0 = hq;
-        const int64_t tok0 = tok, row0 = row, gi0 = (row * p.T + tok) * p.Hv + hq * R + r;
-        const bool done = r == R - 1;   // the item's last value head
-        if (done) {
-            r = 0;
-            item += gridDim.x;
-            find();
-        } else {
-            ++r;
-        }
-        if (item < items) fetch_state(args_again().S, s);
+        if (item < items) fetch_tokens();   // and u and dx now
         // lower tiles of P and E, transposed (lane: token i = 16 I + jj, j = 16 J + 4 g + e): wave w
         // has tile w of both; tiles 8 and 9 of P go to waves 0 and 1, of E to waves 2 and 3
         auto tile_rc = [&](int id, int& I, int& J) {
@@ -394,10 +396,7 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
                 p.dg[gi] = (float)(rest + last);
             }
         }
-        if (item < items) {
-            fetch_tokens();
-            dma_do();
-        }
+        if (item < items) dma_do();
         lds_barrier();
         {
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;

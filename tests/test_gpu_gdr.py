@@ -582,6 +582,50 @@ def test_decode_continues_the_forward():
     ref.assert_states(S, h_ref, "state")
 
 
+def test_far_offsets():
+    """Tensors, workspaces and pools of more than 2^31 elements: the last sequence, and the last
+    slot, get the bits that they get alone."""
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GB of free device memory")
+    last, T, Hv = 100, 270000, 64
+    say(f"gdr_fwd and gdr_bwd, T={T} Hv={Hv}")
+    gen = torch.Generator(device="cuda").manual_seed(61)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    q, k = (torch.nn.functional.normalize(rnd(1, T, 1, 128), dim=-1) for _ in range(2))
+    v = rnd(1, T, Hv, 128)
+    g, beta = -torch.rand(1, T, Hv, device="cuda", generator=gen), torch.rand(1, T, Hv, device="cuda", generator=gen)
+    assert v.numel() > 1 << 31
+    cu = torch.tensor([0, T - last, T], dtype=torch.int32, device="cuda")
+    one = torch.tensor([0, last], dtype=torch.int32, device="cuda")
+    tail = [t[:, T - last:].contiguous() for t in (q, k, v, g, beta)]
+    o, hT = kda_gdr_fwd(q, k, v, g, beta, SCALE, cu_seqlens=cu, final_state=True)
+    o1, h1 = kda_gdr_fwd(*tail, SCALE, cu_seqlens=one, final_state=True)
+    assert torch.equal(o[:, T - last:], o1) and torch.equal(hT[1], h1[0]) and torch.isfinite(hT).all()
+    del o, hT
+    first = 150000   # 2344 chunks of 64 heads: 2^31 elements of kept states are passed
+    b = [t[:, T - last - first:].contiguous() for t in (q, k, v, g, beta)]
+    do = rnd(1, first + last, Hv, 128)
+    del q, k, v, g, beta
+    cu = torch.tensor([0, first, first + last], dtype=torch.int32, device="cuda")
+    got = kda_gdr_bwd(*b, SCALE, do, cu_seqlens=cu, d_initial_state=True)
+    want = kda_gdr_bwd(*tail, SCALE, do[:, first:].contiguous(), cu_seqlens=one, d_initial_state=True)
+    assert all(torch.equal(got[n][:, first:], want[n]) for n in ("dq", "dk", "dv", "dg", "dbeta"))
+    assert torch.equal(got["dh0"][1], want["dh0"][0])
+    assert all(torch.isfinite(got[n]).all() for n in ("dq", "dk", "dg", "dbeta"))
+    del got, b, do
+    slots = 140000
+    say(f"gdr_decode, a pool of {slots} slots")
+    pool = torch.empty(slots, 1, 128, 128, device="cuda")
+    S = torch.randn(1, 1, 128, 128, device="cuda", generator=gen)
+    pool[-1], pool[0] = S[0], 0
+    row = [t[:, 0, :1].contiguous() for t in tail]
+    a, new = kda_gdr_decode(*row, SCALE, S.clone())
+    b, _ = kda_gdr_decode(*row, SCALE, pool, state_indices=torch.tensor([slots - 1], dtype=torch.int32, device="cuda"))
+    assert torch.equal(a, b) and torch.equal(pool[-1], new[0]) and not pool[0].any()
+    del pool
+    torch.cuda.empty_cache()
+
+
 def test_refusal_on_device_tensors():
     x = ref.cuda(ref.make(1, 10, 1, 2, seed=91))
     with pytest.raises(KdaError) as e:

@@ -3,7 +3,7 @@ norm, the gated delta rule and both backwards used together."""
 import pytest
 import torch
 
-from gated_delta_rule_35_amd import kda_fwd, kda_gdr_bwd, kda_gdr_fwd, kda_qk_norm, kda_qk_norm_bwd, load_library
+from gated_delta_rule_35_amd import KdaError, kda_fwd, kda_gdr_bwd, kda_gdr_fwd, kda_qk_norm, kda_qk_norm_bwd, load_library
 from gated_delta_rule_35_amd import kda_qk_norm_bwd_workspace_size
 from tests import gdr_ref as ref
 
@@ -175,6 +175,49 @@ def test_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(held, want))
+
+
+def test_two_streams_at_once():
+    """Calls with weight gradients on two streams, each with its own scratch, and repeats:
+    the same bits."""
+    say("norm and its gradients on two streams")
+    c = {n: (t.cuda() if t is not None else None) for n, t in case(2, 500, 4, 2, weight=True, rot=64, seed=21).items()}
+    kw = kwargs(c, "rms", False)
+    dq, dk = torch.randn_like(c["q"]), torch.randn_like(c["k"])
+    want = kda_qk_norm_bwd(c["q"], c["k"], dq, dk, **kw)
+    y = kda_qk_norm(c["q"], c["k"], **kw)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for i in range(6):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append((kda_qk_norm_bwd(c["q"], c["k"], dq, dk, **kw), kda_qk_norm(c["q"], c["k"], **kw)))
+    torch.cuda.synchronize()
+    for g, z in got:
+        assert all(torch.equal(g[n], want[n]) for n in want) and all(torch.equal(a, b) for a, b in zip(z, y))
+
+
+def test_far_offsets():
+    """As many rows as a tensor may have, 2^26 of 2^33 elements: the last tokens get the bits
+    that they get alone."""
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GB of free device memory")
+    T, last = 1 << 20, 40
+    say(f"norm and its gradients, T={T}, 64 + 1 heads")
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    q, k = (torch.randn(1, T, h, 128, generator=gen, device="cuda", dtype=torch.bfloat16) for h in (64, 1))
+    q1, k1 = q[:, T - last:].contiguous(), k[:, T - last:].contiguous()
+    a, b = kda_qk_norm(q, k), kda_qk_norm(q1, k1)
+    assert all(torch.equal(x[:, T - last:], y) for x, y in zip(a, b))
+    del a
+    dq = torch.randn(1, T, 64, 128, generator=gen, device="cuda", dtype=torch.bfloat16)
+    a = kda_qk_norm_bwd(q, k, dq, k)
+    b = kda_qk_norm_bwd(q1, k1, dq[:, T - last:].contiguous(), k1)
+    assert all(torch.equal(a[n][:, T - last:], b[n]) for n in ("dq", "dk"))
+    more = [torch.empty(1, T + 1, h, 128, device="cuda", dtype=torch.bfloat16) for h in (64, 1)]
+    with pytest.raises(KdaError, match="UNSUPPORTED"):   # more rows than a tensor may have
+        kda_qk_norm(*more)
+    del a, q, dq, more
+    torch.cuda.empty_cache()
 
 
 def test_norm_feeds_the_per_channel_rule():

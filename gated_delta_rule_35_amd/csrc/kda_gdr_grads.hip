@@ -28,11 +28,12 @@
 // depends on enters in three bf16 parts (fp32's accuracy); P and E enter dq and dk, which
 // are rounded to bf16, in two.
 //   The kernel reads 64 KB each of S and dS and 32 KB each of u and dx per chunk and value
-// head.  At B=2 H=64 T=8192 it takes 1350 us, 4.7 GB at 3.5 TB/s, with LDS busy half of the
-// time, vector and matrix units a third each; a unit is 40,000 clocks with four barriers.
+// head.  At B=2 H=64 T=8192 it takes 1320 us, 4.7 GB at 3.6 TB/s, with LDS busy half of the
+// time, vector and matrix units a third each; a unit is 39,000 clocks with three barriers.
 // What brought it there from 2080 us: results formed transposed, inputs asked for in steps,
-// arguments read anew instead of kept in spilled scalar registers (1600 -> 1440 us), and the
-// chains of four tiles side by side (1440 -> 1350 us).
+// arguments read anew instead of kept in spilled scalar registers (1600 -> 1440 us), the
+// chains of four tiles side by side (1440 -> 1350 us), and inputs asked for as soon as the
+// registers of the last ones are free (1350 -> 1320 us).
 #include <type_traits>
 
 #include "kda_gdr_device.h"

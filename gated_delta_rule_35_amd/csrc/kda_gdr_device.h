@@ -93,6 +93,12 @@ __device__ __forceinline__ HSplit<PARTS> hsplit(f32x4 a, f32x4 b) {
     }
     return r;
 }
+// max(m, |x|): the instructions themselves, since fmaxf first quiets every operand.
+__device__ __forceinline__ float max_abs(float m, f32x4 x) {
+    asm("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(m) : "v"(x[0]), "v"(x[1]));
+    asm("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(m) : "v"(x[2]), "v"(x[3]));
+    return m;
+}
 // The power of two that divides a bf16 row's largest entry into [1, 2): the row lies in
 // lanes l, l + 16, l + 32, l + 48, 32 entries each.  0 where there is nothing to divide
 // (a row of zeros) or the largest is not finite.
@@ -294,6 +300,13 @@ __device__ __forceinline__ float sum16(float x) {
     x += ror16<4>(x);
     x += ror16<2>(x);
     return x + ror16<1>(x);
+}
+// Largest over the 16 lanes of a group.
+__device__ __forceinline__ float max16(float x) {
+    x = fmaxf(x, ror16<8>(x));
+    x = fmaxf(x, ror16<4>(x));
+    x = fmaxf(x, ror16<2>(x));
+    return fmaxf(x, ror16<1>(x));
 }
 // Sum over the wave.
 __device__ __forceinline__ float sum64(float x) {

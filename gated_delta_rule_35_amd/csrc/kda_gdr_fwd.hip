@@ -66,13 +66,6 @@ __device__ __forceinline__ constexpr int tri_frag(int m, int kk) { return m < 2 
 __device__ __forceinline__ f32x4 sc4(const float* sc, int row, int m, int g) {
     return *reinterpret_cast<const f32x4*>(sc + row + 16 * m + 4 * g);
 }
-// max(m, |x|): the instructions themselves, since fmaxf first quiets every operand.
-__device__ __forceinline__ float max_abs(float m, f32x4 x) {
-    asm("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(m) : "v"(x[0]), "v"(x[1]));
-    asm("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(m) : "v"(x[2]), "v"(x[3]));
-    return m;
-}
-
 }  // namespace
 
 template <int HALVES>

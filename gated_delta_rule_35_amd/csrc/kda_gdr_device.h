@@ -3,10 +3,10 @@
 // Matrix products run on the 16x16x32 instructions for 16-bit operands.  q, k, v and the
 // output's gradient are bf16; an fp32 operand enters as the sum of parts, each the rounding
 // of what the parts before it leave, so that products keep fp32's accuracy at a third to a
-// sixth of the 16-bit rate, several times that of the fp32 matrix instructions.  The prep
-// kernel and the backward use bf16 parts, three of which hold all 24 bits at any size; the
-// forward's walk uses fp16 parts, two of which hold 22 bits of what powers of two keep in
-// range, with q and k turned into fp16 rows divided by powers of two.
+// sixth of the 16-bit rate, several times that of the fp32 matrix instructions.  The
+// backward's walks use bf16 parts, three of which hold all 24 bits at any size; the
+// forward's walk and the token gradients use fp16 parts, two of which hold 22 bits of what
+// powers of two keep in range (the forward's q and k too are fp16 rows divided by such).
 #pragma once
 #include "kda_device.h"
 #include "kda_gdr.h"

@@ -17,23 +17,27 @@
 //
 // One 512-thread work-group per compute unit takes items (chunk slot, q/k head), walks
 // the group's value heads and sums their dq and dk in registers (so the sum's order is
-// fixed); the next unit's S, u and dx are loaded into registers, its do into LDS, while
-// the last products of this one run, and dS while S's do.  It holds the
-// chunk's do, u and dx (bf16 parts) and k, q in LDS; wave w owns channels 16 w .. + 15
-// of R1, R2, R3, dq and dk, so S and dS are read once and split once; the ten lower
-// 16x16 tiles of P and of E are dealt to the eight waves.  Every product is formed
-// transposed (channels or the earlier token down, tokens across), so that a lane holds
-// one token and four channels: a dot over channels is four products in the lane and two
-// exchanges, per-token factors are one number, and results leave four at a time.  What dg
-// depends on enters in three bf16 parts (fp32's accuracy); P and E enter dq and dk, which
-// are rounded to bf16, in two.
+// fixed); the next unit's S, u, dx and do are loaded into registers as soon as those of
+// this one's are free, and dS while S's products run.  It holds the chunk's do, u and dx
+// (fp16 parts) and k, q in LDS; wave w owns channels 16 w .. + 15 of R1, R2, R3, dq and
+// dk, so S and dS are read once and split once; the ten lower 16x16 tiles of P and of E
+// are dealt to the eight waves.  Every product is formed transposed (channels or the
+// earlier token down, tokens across), so that a lane holds one token and four channels: a
+// dot over channels is four products in the lane and two exchanges, per-token factors are
+// one number, and results leave four at a time.
+//   Precision: each row of S, dS, u, dx and do is brought to [2^10, 2^11) by a power of two
+// and enters in fp16, do in one part (its eight bits are exact down to 2^-24 of the row's
+// largest), the others in two (22 bits down to 2^-13 of it), which dg needs; P and E enter
+// dq and dk, which are rounded to bf16, in two bf16 parts.
 //   The kernel reads 64 KB each of S and dS and 32 KB each of u and dx per chunk and value
-// head.  At B=2 H=64 T=8192 it takes 1320 us, 4.7 GB at 3.6 TB/s, with LDS busy half of the
-// time, vector and matrix units a third each; a unit is 39,000 clocks with three barriers.
+// head.  At B=2 H=64 T=8192 it takes 1244 us, 4.7 GB at 3.8 TB/s; LDS, vector and matrix
+// units are busy a quarter to a half of the time, with three barriers a unit.
 // What brought it there from 2080 us: results formed transposed, inputs asked for in steps,
 // arguments read anew instead of kept in spilled scalar registers (1600 -> 1440 us), the
-// chains of four tiles side by side (1440 -> 1350 us), and inputs asked for as soon as the
-// registers of the last ones are free (1350 -> 1320 us).
+// chains of four tiles side by side (1440 -> 1350 us), inputs asked for as soon as there are
+// registers (-> 1320 us), fp16 parts instead of three of bf16 (-> 1244 us).  Asking for all
+// inputs a whole unit ahead and turning the next unit's into fp16 beside the last products
+// took as long, and longer where a head's group is small.
 #include <type_traits>
 
 #include "kda_gdr_device.h"

@@ -94,7 +94,7 @@ def gradients(x, scale, do, dhT=None, cu=None):
         S0 = (h0[n].clone() if h0 is not None else torch.zeros(d["v"].shape[2], 128, 128, dtype=torch.float64))
         S0.requires_grad_()
         o, S = recurrence(*leaves, scale, S0)
-        loss = (o * do[b, a:e].detach().cpu().double()).sum() if e > a else 0.0
+        loss = (o * do[b, a:e].detach().cpu().double()).sum()
         if dhT is not None:
             loss = loss + (S * dhT[n].detach().cpu().double()).sum()
         got = torch.autograd.grad(loss, leaves + [S0], allow_unused=True)

@@ -23,6 +23,16 @@ namespace kda {
 
 namespace {
 constexpr int DT = 256;
+// Sum over the wave's lanes that are equal modulo N, in each of them.
+template <int N>
+__device__ __forceinline__ float sum_above(float x) {
+    static_assert(N == 8 || N == 32, "rows of quads");
+    if (N == 32) {
+        const Pair p = across<32>(x);
+        return p.a + p.b;
+    }
+    return sum_groups(x + ror16<8>(x));
+}
 }
 
 template <int CW>
@@ -71,14 +81,11 @@ __global__ void __launch_bounds__(DT) kda_gdr_decode_kernel(const GdrDecodeParam
             qk = fmaf(qq, kk[i], qk);
         }
 #pragma unroll
-        for (int m = NQ; m < 64; m <<= 1) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                u[e] += __shfl_xor(u[e], m);
-                o[e] += __shfl_xor(o[e], m);
-            }
-            qk += __shfl_xor(qk, m);
+        for (int e = 0; e < 4; ++e) {
+            u[e] = sum_above<NQ>(u[e]);
+            o[e] = sum_above<NQ>(o[e]);
         }
+        qk = sum_above<NQ>(qk);
         if (lane < NQ) {
             *reinterpret_cast<f32x4*>(&sU[wave][4 * lane]) = u;
             *reinterpret_cast<f32x4*>(&sQ[wave][4 * lane]) = o;

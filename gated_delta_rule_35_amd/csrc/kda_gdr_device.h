@@ -308,12 +308,30 @@ __device__ __forceinline__ float max16(float x) {
     x = fmaxf(x, ror16<2>(x));
     return fmaxf(x, ror16<1>(x));
 }
-// Sum over the wave.
-__device__ __forceinline__ float sum64(float x) {
-    x = sum16(x);
-    x += __shfl_xor(x, 16);
-    return x + __shfl_xor(x, 32);
+// x of this lane and of the lane 16, or 32, places away (lane ^ N), in either order: for sums
+// and largest values, the same bits in both lanes, without an LDS access.
+struct Pair {
+    float a, b;
+};
+template <int N>
+__device__ __forceinline__ Pair across(float x) {
+    const uint32_t v = __float_as_uint(x);
+    const auto r = N == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                           : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return {__uint_as_float(r[0]), __uint_as_float(r[1])};
 }
+// Sum over the four lane groups, in every one.
+__device__ __forceinline__ float sum_groups(float x) {
+    const Pair p = across<16>(x), q = across<32>(p.a + p.b);
+    return q.a + q.b;
+}
+// Largest over the four lane groups.
+__device__ __forceinline__ float max_groups(float x) {
+    const Pair p = across<16>(x), q = across<32>(fmaxf(p.a, p.b));
+    return fmaxf(q.a, q.b);
+}
+// Sum over the wave.
+__device__ __forceinline__ float sum64(float x) { return sum_groups(sum16(x)); }
 
 // The (sequence, value head, 64-wide slice of value channels) of a walk's work-group.
 // Work-groups start in order and are dealt to the 8 XCDs round robin.  An XCD takes an

@@ -219,8 +219,7 @@ __global__ void __launch_bounds__(FL<HALVES>::THREADS) kda_gdr_scan_kernel(const
     // Columns whose largest value left [2^2, 2^10] go back to [2^7, 2^8); top: the lane's part
     // of it, x: what is scaled with the state.
     auto rescale = [&](float top, f32x4 (&x)[4]) {
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
+        top = max_groups(top);
         if (top > 1024.f || (top < 4.f && top > 0.f)) {
             int e = (int)(__float_as_uint(top) >> 23) - 127 - 7;   // what its exponent has too many
             const int was = 127 - (int)(__float_as_uint(down) >> 23);

@@ -30,12 +30,13 @@
 // largest), the others in two (22 bits down to 2^-13 of it), which dg needs; P and E enter
 // dq and dk, which are rounded to bf16, in two bf16 parts.
 //   The kernel reads 64 KB each of S and dS and 32 KB each of u and dx per chunk and value
-// head.  At B=2 H=64 T=8192 it takes 1244 us, 4.7 GB at 3.8 TB/s; LDS, vector and matrix
+// head.  At B=2 H=64 T=8192 it takes 1207 us, 4.7 GB at 3.9 TB/s; LDS, vector and matrix
 // units are busy a quarter to a half of the time, with three barriers a unit.
 // What brought it there from 2080 us: results formed transposed, inputs asked for in steps,
 // arguments read anew instead of kept in spilled scalar registers (1600 -> 1440 us), the
 // chains of four tiles side by side (1440 -> 1350 us), inputs asked for as soon as there are
-// registers (-> 1320 us), fp16 parts instead of three of bf16 (-> 1244 us).  Asking for all
+// registers (-> 1320 us), fp16 parts instead of three of bf16 (-> 1244 us), sums across lane
+// groups by v_permlane swaps instead of through LDS (-> 1207 us).  Asking for all
 // inputs a whole unit ahead and turning the next unit's into fp16 beside the last products
 // took as long, and longer where a head's group is small.
 #include <type_traits>
@@ -86,11 +87,6 @@ __device__ __forceinline__ f32x4 mfma_22(const HSplit<2>& a, const half8 (&b)[2]
 }
 __device__ __forceinline__ half8 lds_h8(const char* p) { return *reinterpret_cast<const half8*>(p); }
 __device__ __forceinline__ float dot4(f32x4 a, f32x4 b) { return fmaf(a[0], b[0], fmaf(a[1], b[1], fmaf(a[2], b[2], a[3] * b[3]))); }
-// Sum over the four lane groups, in every one.
-__device__ __forceinline__ float sum_groups(float x) {
-    x += __shfl_xor(x, 16);
-    return x + __shfl_xor(x, 32);
-}
 // Operand (m, kk) of a 64x64 plane: rows 16 m + jj, columns of k step kk; and of its transpose.
 __device__ __forceinline__ bf16x8 plane_row(const char* pl, int m, int kk, int g, int jj) {
     const char* a = pl + (16 * m + jj) * PS + 64 * kk + 8 * g;
@@ -232,8 +228,7 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
                 float top = 0.f;
 #pragma unroll
                 for (int n = 0; n < 8; ++n) top = max_abs(top, a[n]);
-                top = fmaxf(top, __shfl_xor(top, 16));
-                return raise(fmaxf(top, __shfl_xor(top, 32)));
+                return raise(max_groups(top));
             };
             // k steps outermost: eight (then four) chains of products side by side, one step's parts at a time
             f32x4 r1[4], r3[4];

@@ -28,11 +28,13 @@
 // 2^-4 to 2^-12 of the largest, and is off by 2^-25 in these units below that, 2^-27 to
 // 2^-35 of the largest.
 //
-// At B=2 H=64 T=8192 the walk takes 375 us, 1.43 GB at 3.8 TB/s: a chunk is 5,500 clocks,
-// in which a SIMD issues the vector instructions of one walking and one staging wave, about
-// 850 of four clocks, and 104 matrix instructions; the walking wave goes first (s_setprio).
-// Products of four tiles side by side, v, T and A by DMA two chunks ahead, the priority and
-// inverses of powers of two by integer subtraction brought 586 us of the whole call to 571.
+// At B=2 H=64 T=8192 the walk takes 370 us, 1.43 GB at 3.9 TB/s: 5,300 clocks a chunk, the
+// chain of its products (gate and window 900, K S and Q S 1,700, T x 700, S and o 2,000),
+// where four waves' reads of the same operands keep LDS busy half of the time and splits and
+// matrix instructions share the issue.  A chunk takes nearly as long when only 16 work-groups
+// run, and 2% less without the staging waves' conversions.  Products of four tiles side by
+// side, v, T and A by DMA two chunks ahead, the walking waves' priority and inverses of
+// powers of two by integer subtraction brought 586 us of the whole call to 560.
 #include "kda_gdr_device.h"
 
 namespace kda {
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(FL<HALVES>::THREADS) kda_gdr_scan_kernel(const
                 for (int m = 0; m < 4; ++m) o[m] = mfma_h(fq[now][m], sb[now].s[0], o[m]);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) x[m] = mfma_h(fk[now][m], sb[now].s[0], x[m]);
-                interleave<12, 2, 1, 0>();
+                interleave<12, 3, 1, 0>();
             }
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(FL<HALVES>::THREADS) kda_gdr_scan_kernel(const
                         *reinterpret_cast<uint16_t*>(dst + 384) = (uint16_t)(p1 >> 16);
                     }
                 }
-                interleave<8, 3, 1, 0>();
+                interleave<8, 4, 1, 0>();
             }
         }
     }

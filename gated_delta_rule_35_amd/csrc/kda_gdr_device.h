@@ -117,10 +117,10 @@ __device__ __forceinline__ float row_power(const bf16x8 (&x)[4]) {
     return e == 0 || e == 255 ? 0.f : __uint_as_float(min(e, 253u) << 23);
 }
 
-// Per-token rows of a record's numbers, in elements: e^G, e^{G_last - G}, beta,
-// e^{G_last}; forward also beta e^G 2^ek, 2^ek, 2^eq (what the scan divides the token's k
-// and q by; 2^ek is 0 for a key of zeros, whose u takes no part) and the chunk's largest
-// 2^ek, within 2^-60 and 2^60 (0: all its keys are zero).
+// Per-token rows of a record's numbers, in elements: e^G, e^{G_last - G}, beta (forward:
+// beta 2^ek), e^{G_last}; forward also beta 2^{2 ek} e^G, 2^ek, 2^eq (what the scan divides
+// the token's k and q by; 2^ek is 0 for a key of zeros, whose u takes no part) and the
+// chunk's largest 2^ek, within 2^-60 and 2^60 (0: all its keys are zero).
 enum { SC_EG = 0, SC_GA = 64, SC_BE = 128, SC_EL = 192, SC_EGK = 256, SC_KS = 320, SC_QS = 384, SC_KP = 448 };
 
 // ---- swizzled [64][128] bf16 tiles in LDS: rows of 256 bytes, whose sixteen 16-byte

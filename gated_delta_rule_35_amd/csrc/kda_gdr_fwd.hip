@@ -19,14 +19,18 @@
 // bits, so that the state keeps fp32's accuracy with two thirds of the matrix work of
 // three bf16 parts and a fifth of fp32 instructions'; what only reaches the bf16 output
 // (S in Q S, A, u in A u) enters as one part, eight times finer than o's own rounding.
-// fp16's range is met by two powers of two: `kap`, the size of the chunk's keys, by which
-// S is divided, and one for each value channel (each lane's column), which keeps the
-// largest |S| / kap and |beta v| within [2^2, 2^10] when a chunk starts, and again the
-// largest of what its end keeps of them, before S is formed anew; all change rarely.
-// With beta |k|^2 <= 2, where the update does not expand the state, x, u and u 2^ek / kap
-// are then a few times those at most, and |T| <= 2.  An entry keeps its 22 bits down to
-// 2^-4 to 2^-12 of the largest, and is off by 2^-25 in these units below that, 2^-27 to
-// 2^-35 of the largest.
+// fp16's range is met by powers of two.  x and u are those of the rows times 2^ek / kap,
+// 2^ek the power that divides the row's key and `kap` the chunk's largest, by which S is
+// divided: what a key adds to S, and what it reads of it, then have S's units, and T's
+// entries stay below 46 (kda_gdr_prep.hip).  One more for each value channel (each lane's
+// column) keeps the largest |S| / kap and |beta v| 2^ek / kap within [2^2, 2^10] when a
+// chunk starts; with beta |k|^2 <= 2, where the update does not expand the state,
+// |x| <= 2^10 + beta 2^2ek |k^| |k^ . S| <= 2^10 + 2 128^{1/2} 2^10 < 2^15.  u can be 128 |k^|
+// times larger where keys repeat (beta 2 and values of alternating signs: the state grows
+// by 2 |v| a token): past 2^15 the column is scaled down, and what the chunk's end keeps is
+// scaled up where it is far less than what it started with, before S is formed anew; all
+// change rarely.  An entry keeps its 22 bits down to 2^-4 to 2^-12 of the largest, and is
+// off by 2^-25 in these units below that, 2^-27 to 2^-35 of the largest.
 //
 // At B=2 H=64 T=8192 the walk takes 370 us, 1.43 GB at 3.9 TB/s: 5,300 clocks a chunk, the
 // chain of its products (gate and window 900, K S and Q S 1,700, T x 700, S and o 2,000),
@@ -155,9 +159,8 @@ __global__ void __launch_bounds__(FL<HALVES>::THREADS) kda_gdr_scan_kernel(const
                 *reinterpret_cast<u32x4*>(to + L::K + at) = to_half(kr[x], __shfl(kinv, r + 4 * x));
                 *reinterpret_cast<u32x4*>(to + L::Q + at) = to_half(qr[x], __shfl(qinv, r + 4 * x));
             }
-            // beta e^G 2^ek kap and 2^ek / kap (rows 4 and 5: wave 2)
-            out[128 * w + ln] = sc[0] * (w == 2 ? kap : 1.f);
-            out[128 * w + 64 + ln] = sc[1] * (w == 2 ? inverse2(kap) : 1.f);
+            out[128 * w + ln] = sc[0] * (w == 1 ? inverse2(kap) : 1.f);   // row 2: beta 2^ek / kap
+            out[128 * w + 64 + ln] = sc[1];
         };
         if (nch > 0) {
             dma(0, 0);
@@ -218,22 +221,26 @@ __global__ void __launch_bounds__(FL<HALVES>::THREADS) kda_gdr_scan_kernel(const
 #pragma unroll
         for (int r = 0; r < 4; ++r) S[t][r] = p.h0 ? p.h0[so + state_row(t, lane >> 4, r) * DK] : 0.f;
     }
-    // Columns whose largest value left [2^2, 2^10] go back to [2^7, 2^8); top: the lane's part
-    // of it, x: what is scaled with the state.
-    auto rescale = [&](float top, f32x4 (&x)[4]) {
+    // Columns whose largest value lies below `least` or above `most` go back to [2^7, 2^8); top: the
+    // lane's part of it.  Returns what the state was multiplied by: what is at hand in its units is too.
+    auto rescale = [&](float top, float least, float most) -> float {
         top = max_groups(top);
-        if (top > 1024.f || (top < 4.f && top > 0.f)) {
+        if (top > most || (top < least && top > 0.f)) {
             int e = (int)(__float_as_uint(top) >> 23) - 127 - 7;   // what its exponent has too many
             const int was = 127 - (int)(__float_as_uint(down) >> 23);
             e = max(-120 - was, min(120 - was, e));                // keep the power of two itself in range
             const float by = __uint_as_float((uint32_t)(127 - max(-126, min(126, e))) << 23);
 #pragma unroll
             for (int t = 0; t < 8; ++t) S[t] *= by;
-#pragma unroll
-            for (int m = 0; m < 4; ++m) x[m] *= by;
             down *= by;
             up = inverse2(down);
+            return by;
         }
+        return 1.f;
+    };
+    auto times = [](f32x4 (&x)[4], float by) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) x[m] *= by;
     };
     int at = 0;   // chunk c's slot of what comes by DMA
     for (int c = 0; c < nch; ++c) {
@@ -250,7 +257,7 @@ __global__ void __launch_bounds__(FL<HALVES>::THREADS) kda_gdr_scan_kernel(const
             for (int t = 0; t < 8; ++t) S[t] *= kap * inverse2(km);
             kap = km;
         }
-        f32x4 v[4];   // beta v
+        f32x4 v[4];   // beta v 2^ek / kap
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const u32x2 b = lds_tr(tv + (16 * m + 4 * g + (jj >> 2)) * 128 + 32 * w + 8 * (jj & 3));
@@ -261,10 +268,9 @@ __global__ void __launch_bounds__(FL<HALVES>::THREADS) kda_gdr_scan_kernel(const
         for (int t = 0; t < 8; ++t) top = max_abs(top, S[t]);
 #pragma unroll
         for (int m = 0; m < 4; ++m) top = max_abs(top, v[m]);
-        if (__any(top > 1024.f || (top < 4.f && top > 0.f))) rescale(top, v);
-        const float whole = up * kap * p.scale;   // what o's sums are multiplied by
-        // x = beta v - beta e^G K S and e^G Q S, eight tiles side by side; the next step's
-        // operands are read and split meanwhile
+        if (__any(top > 1024.f || (top < 4.f && top > 0.f))) times(v, rescale(top, 4.f, 1024.f));
+        // x = (beta v - beta e^G K S) 2^ek / kap and e^G Q S, eight tiles side by side; the next
+        // step's operands are read and split meanwhile
         f32x4 x[4], o[4];
         {
             half8 fk[2][4], fq[2][4];
@@ -302,7 +308,7 @@ __global__ void __launch_bounds__(FL<HALVES>::THREADS) kda_gdr_scan_kernel(const
                 o[m] *= sc4(sc, SC_EG, m, g);
             }
         }
-        // u = T x, times 2^ek / kap: six tiles side by side
+        // u = T x (of the rows times 2^ek / kap, as x is): six tiles side by side
         f32x4 u[4];
         constexpr int TM[6] = {0, 1, 2, 3, 2, 3}, TK[6] = {0, 0, 0, 0, 1, 1};   // fragments (m, kk)
         {
@@ -324,8 +330,20 @@ __global__ void __launch_bounds__(FL<HALVES>::THREADS) kda_gdr_scan_kernel(const
 #pragma unroll
             for (int i = 0; i < 6; ++i) a[i] = mfma_h(th[i], xb[TK[i]].s[0], a[i]);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) u[m] = (m < 2 ? a[m] : a[m] + a[m + 2]) * sc4(sc, SC_KS, m, g);
+            for (int m = 0; m < 4; ++m) u[m] = m < 2 ? a[m] : a[m] + a[m + 2];
         }
+        // repeated keys can make u up to 128 |k^| times what the chunk started with
+        {
+            float tu = 0.f;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) tu = max_abs(tu, u[m]);
+            if (__any(tu > 32768.f)) {
+                const float by = rescale(tu, 0.f, 32768.f);
+                times(u, by);
+                times(o, by);
+            }
+        }
+        const float whole = up * kap * p.scale;   // what o's sums are multiplied by
         // S <- e^{G_last} S + K^T (e^{G_last - G} u), four tiles side by side; between them
         // o's second part, rounded once, into this wave's columns of v's slice: the staging
         // waves store it
@@ -340,7 +358,7 @@ __global__ void __launch_bounds__(FL<HALVES>::THREADS) kda_gdr_scan_kernel(const
             if (__any(tw < 4.f && tw > 0.f)) {   // what is left of the chunk may be far less than what it started with
 #pragma unroll
                 for (int t = 0; t < 8; ++t) tw = max_abs(tw, S[t]);
-                rescale(tw, wu);
+                times(wu, rescale(tw, 4.f, __builtin_inff()));
             }
             const HSplit<2> wb[2] = {hsplit<2>(wu[0], wu[1]), hsplit<2>(wu[2], wu[3])};
             const HSplit<1> ub[2] = {hsplit<1>(u[0], u[1]), hsplit<1>(u[2], u[3])};

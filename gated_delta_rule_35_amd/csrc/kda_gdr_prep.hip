@@ -17,7 +17,10 @@
 // with the T_KJ of its column in registers (an accumulator tile is the next product's
 // B operand).  T and A leave as operand fragments: for the backward in three bf16 parts
 // each; for the forward T in two fp16 parts and A in one, without the scale and divided
-// by the powers of two that the scan divides q's and k's rows by.
+// by the powers of two 2^eq and 2^ek that the scan divides q's and k's rows by.  The
+// forward's T is that of the rows times 2^ek, D T D^{-1} with D = diag(2^ek): its entries
+// are at most |beta_i k^_i| 2^{2 ek_i} |k^_j|, k^ = k / 2^ek, so that beta |k|^2 <= 2 keeps
+// them below 2 |k^_j| / |k^_i| <= 46 for keys of any sizes beside each other.
 //
 // At B=2 H=64 T=8192 (16,384 chunks of a head): forward 192 us, 0.94 GB at 4.9 TB/s; with the
 // backward's records 207 us, 1.22 GB at 5.9 TB/s (part of what it writes stays in the
@@ -137,11 +140,11 @@ __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p)
             const float eg = gate_exp(G);
             sc[SC_EG] = eg;
             sc[SC_GA] = gate_ratio(GL, G);
-            sc[SC_BE] = sBeta[lane];
+            sc[SC_BE] = BWD ? sBeta[lane] : sBeta[lane] * sKp[lane];
             sc[SC_EL] = gate_exp(GL);
             if (!BWD) {
                 const float ks = sKp[lane] > 0.f ? sKp[lane] : 1.f;
-                sc[SC_EGK] = sBeta[lane] * eg * ks;
+                sc[SC_EGK] = sBeta[lane] * ks * ks * eg;
                 sc[SC_KS] = sKp[lane];
                 sc[SC_QS] = sQp[lane];
                 sc[SC_KP] = kmax;
@@ -155,18 +158,22 @@ __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p)
                 const int j = 16 * tj[x] + jj, i0 = 16 * ti[x] + 4 * g;
                 const GSum Gj = sG[j];
                 const f32x4 be = *reinterpret_cast<const f32x4*>(sBeta + i0);
-                f32x4 by = f32x4{p.scale, p.scale, p.scale, p.scale};
+                f32x4 by = f32x4{p.scale, p.scale, p.scale, p.scale}, ks = f32x4{1.f, 1.f, 1.f, 1.f};
+                float kinv = 1.f;
                 if (!BWD) {   // exact: powers of two
                     const f32x4 qp = *reinterpret_cast<const f32x4*>(sQp + i0);
-                    const float kinv = sKp[j] > 0.f ? inverse2(sKp[j]) : 1.f;
+                    const f32x4 kp = *reinterpret_cast<const f32x4*>(sKp + i0);
+                    kinv = sKp[j] > 0.f ? inverse2(sKp[j]) : 1.f;
                     by = f32x4{inverse2(qp[0]), inverse2(qp[1]), inverse2(qp[2]), inverse2(qp[3])} * kinv;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) ks[e] = kp[e] > 0.f ? kp[e] : 1.f;
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int i = i0 + e;
                     const float gam = j <= i ? gate_ratio(sG[i], Gj) : 0.f;
                     sA[i * SP + j] = j <= i ? by[e] * (qk[x][e] * gam) : 0.f;
-                    sM[i * SP + j] = j < i ? be[e] * (kk[x][e] * gam) : 0.f;
+                    sM[i * SP + j] = j < i ? be[e] * (kk[x][e] * gam * kinv) * ks[e] : 0.f;
                 }
             }
         }

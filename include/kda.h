@@ -458,9 +458,9 @@ kda_status_t kda_bwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda_ten
  * that follow the sizes met, so that values of any size keep states to about 1e-6 of
  * their largest entries.  An entry below 2^-12 of the largest |S| or |beta v| of its
  * value channel in the chunk is off by up to 2^-27 of that.  The update must not expand
- * the state, beta |k|^2 <= 2 (L2-normalised keys and 0 <= beta <= 2 do not): where
- * (I - beta k k^T) grows it past fp16's range within a chunk, results are infinite or
- * NaN.  The backward's walks take fp32 operands in three bf16 parts, at fp32's accuracy
+ * the state, beta |k|^2 <= 2 (L2-normalised keys and 0 <= beta <= 2 do not, keys of any
+ * sizes beside each other): where (I - beta k k^T) grows it past fp16's range within a
+ * chunk, results are infinite or NaN.  The backward's walks take fp32 operands in three bf16 parts, at fp32's accuracy
  * and range; its token gradients take rows of them, brought to one size by powers of two,
  * in two fp16 parts (about 1e-6 relative for dg and dbeta; an entry below 2^-13 of its
  * row's largest is off by up to 2^-36 of that).  o, dq, dk and dv are rounded to bf16 once.  A token that holds NaN or infinity may reach

@@ -8,8 +8,12 @@ kda_dv_slices.  Tensors are passed as
 kda_tensor_t descriptors built from torch tensors (data pointer, dtype, shape,
 strides); the stream is torch's current HIP stream unless one is given.  Where
 an entry point takes a workspace, it is a uint8 device tensor the caller passes
-or one taken here from torch's caching allocator.
+or one taken here from torch's caching allocator.  What is allocated here for a
+call on a given stream (a torch stream of the tensors' device, or a handle) belongs
+to that stream, as under torch.cuda.stream(): whoever uses an output on another
+stream waits for the call's and records the use.
 """
+import contextlib
 import ctypes
 import os
 
@@ -484,6 +488,24 @@ def _launch(entry, dev, scalars, tensors, stream, workspace=None):
         _check(_lib, status)
 
 
+_CURRENT = contextlib.nullcontext()
+
+
+def _place(stream, dev):
+    """Where a call's outputs and scratch are allocated: under its stream, so that the
+    caching allocator takes and reuses their memory in that stream's order."""
+    if stream is None:
+        return _CURRENT
+    if dev < 0:
+        raise ValueError("a call on a stream needs its tensors on the GPU")
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != dev:
+            raise ValueError(f"the stream is on GPU {stream.device.index}, the tensors are on GPU {dev}")
+        return torch.cuda.stream(stream)
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev))
+
+
 def _new(like, dtype, shape=None):
     """An uninitialised contiguous tensor beside `like`."""
     if shape is None:
@@ -491,14 +513,9 @@ def _new(like, dtype, shape=None):
     return like.new_empty(shape, dtype=dtype)
 
 
-def _scratch(size, like, stream):
-    """A workspace of torch's caching allocator, kept from reuse until `stream` is done with it."""
-    if size <= 0:
-        return None
-    ws = like.new_empty(size, dtype=torch.uint8)
-    if stream is not None and isinstance(stream, torch.cuda.Stream):
-        ws.record_stream(stream)
-    return ws
+def _scratch(size, like):
+    """A workspace of torch's caching allocator."""
+    return like.new_empty(size, dtype=torch.uint8) if size > 0 else None
 
 
 def _sequences(q, cu_seqlens):
@@ -520,13 +537,14 @@ def kda_gdr_fwd(q, k, v, g, beta, scale, cu_seqlens=None, initial_state=None, ou
     out and final_state=True are allocated here when not given.  `workspace`: a uint8
     device tensor of kda_gdr_fwd_workspace_size() bytes, or None (taken here from
     torch's caching allocator)."""
-    if out is None:
-        out = _new(v, torch.bfloat16)
-    if final_state is True:
-        final_state = _new(v, torch.float32, (_sequences(q, cu_seqlens), v.shape[-2], 128, 128))
-    if workspace is None and q.dim() == 4 and v.dim() == 4 and v.is_cuda:   # the C library rejects other ranks
-        workspace = _scratch(kda_gdr_fwd_workspace_size(q.shape[0] * q.shape[1], _sequences(q, cu_seqlens), v.shape[2]),
-                             v, stream)
+    with _place(stream, v.get_device()):
+        if out is None:
+            out = _new(v, torch.bfloat16)
+        if final_state is True:
+            final_state = _new(v, torch.float32, (_sequences(q, cu_seqlens), v.shape[-2], 128, 128))
+        if workspace is None and q.dim() == 4 and v.dim() == 4 and v.is_cuda:   # the C library rejects other ranks
+            size = kda_gdr_fwd_workspace_size(q.shape[0] * q.shape[1], _sequences(q, cu_seqlens), v.shape[2])
+            workspace = _scratch(size, v)
     _launch(_GDR_FWD, v.get_device(), (scale,), (q, k, v, g, beta, cu_seqlens, initial_state, out, final_state), stream,
             workspace)
     return out, final_state
@@ -539,19 +557,20 @@ def kda_gdr_bwd(q, k, v, g, beta, scale, d_out, initial_state=None, d_final_stat
     `grads` may hold preallocated outputs under those names; `workspace` a uint8 device
     tensor of kda_gdr_bwd_workspace_size() bytes (None: taken here)."""
     res = dict(grads or {})
-    for name, like, dtype in (("dq", q, torch.bfloat16), ("dk", k, torch.bfloat16), ("dv", v, torch.bfloat16),
-                              ("dg", g, torch.float32), ("dbeta", beta, torch.float32)):
-        if res.get(name) is None:
-            res[name] = _new(like, dtype)
-    if isinstance(d_initial_state, torch.Tensor):
-        res["dh0"] = d_initial_state
-    elif d_initial_state:
-        res["dh0"] = _new(v, torch.float32, (_sequences(q, cu_seqlens), v.shape[-2], 128, 128))
-    else:
-        res["dh0"] = None
-    if workspace is None and q.dim() == 4 and v.dim() == 4:
-        workspace = _scratch(kda_gdr_bwd_workspace_size(q.shape[0] * q.shape[1], _sequences(q, cu_seqlens), v.shape[2]),
-                             v, stream)
+    with _place(stream, v.get_device()):
+        for name, like, dtype in (("dq", q, torch.bfloat16), ("dk", k, torch.bfloat16), ("dv", v, torch.bfloat16),
+                                  ("dg", g, torch.float32), ("dbeta", beta, torch.float32)):
+            if res.get(name) is None:
+                res[name] = _new(like, dtype)
+        if isinstance(d_initial_state, torch.Tensor):
+            res["dh0"] = d_initial_state
+        elif d_initial_state:
+            res["dh0"] = _new(v, torch.float32, (_sequences(q, cu_seqlens), v.shape[-2], 128, 128))
+        else:
+            res["dh0"] = None
+        if workspace is None and q.dim() == 4 and v.dim() == 4:
+            size = kda_gdr_bwd_workspace_size(q.shape[0] * q.shape[1], _sequences(q, cu_seqlens), v.shape[2])
+            workspace = _scratch(size, v)
     _launch(_GDR_BWD, v.get_device(), (scale,),
             (q, k, v, g, beta, cu_seqlens, initial_state, d_out, d_final_state, res["dq"], res["dk"], res["dv"],
              res["dg"], res["dbeta"], res["dh0"]), stream, workspace)
@@ -564,12 +583,13 @@ def kda_gdr_decode(q, k, v, g, beta, scale, state, state_indices=None, out=None,
     [slots, Hv, 128, 128]: rows with a slot outside it (-1) are skipped, rows that share
     one are taken in order.  The new states go to `new_state`, by default `state` itself.
     Returns (out, new_state); rows of `out` that are skipped are not written."""
-    if out is None:
-        out = _new(v, torch.bfloat16)
-    if new_state is None:
-        if state is None and state_indices is not None:
-            raise ValueError("kda_gdr_decode needs a pool where state_indices name its slots")
-        new_state = state if state is not None else _new(v, torch.float32, (v.shape[0], v.shape[1], 128, 128))
+    if new_state is None and state is None and state_indices is not None:
+        raise ValueError("kda_gdr_decode needs a pool where state_indices name its slots")
+    with _place(stream, v.get_device()):
+        if out is None:
+            out = _new(v, torch.bfloat16)
+        if new_state is None:
+            new_state = state if state is not None else _new(v, torch.float32, (v.shape[0], v.shape[1], 128, 128))
     _launch(_GDR_DECODE, v.get_device(), (scale,), (q, k, v, g, beta, state, new_state, state_indices, out), stream)
     return out, new_state
 
@@ -590,7 +610,8 @@ def kda_qk_norm(q, k, q_weight=None, k_weight=None, mode="l2", eps=1e-6, cos=Non
     when not given."""
     if mode not in _NORM_MODES:
         raise ValueError(f"kda_qk_norm: mode {mode!r} is neither 'l2' nor 'rms'")
-    qo, ko = out if out is not None else (_new(q, torch.bfloat16), _new(k, torch.bfloat16))
+    with _place(stream, q.get_device()):
+        qo, ko = out if out is not None else (_new(q, torch.bfloat16), _new(k, torch.bfloat16))
     _launch(_QK_NORM, q.get_device(), (_NORM_MODES[mode], eps, bool(interleaved)),
             (q, k, q_weight, k_weight, cos, sin, positions, qo, ko), stream)
     return qo, ko
@@ -604,16 +625,17 @@ def kda_qk_norm_bwd(q, k, d_q_out, d_k_out, q_weight=None, k_weight=None, mode="
     if mode not in _NORM_MODES:
         raise ValueError(f"kda_qk_norm_bwd: mode {mode!r} is neither 'l2' nor 'rms'")
     res = dict(grads or {})
-    for name, x in (("dq", q), ("dk", k)):
-        if res.get(name) is None:
-            res[name] = _new(x, x.dtype)
-    for name, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
-        if w is None:
-            res[name] = None
-        elif res.get(name) is None:
-            res[name] = _new(w, torch.float32)
-    if workspace is None and (q_weight is not None or k_weight is not None):
-        workspace = _scratch(kda_qk_norm_bwd_workspace_size(), q, stream)
+    with _place(stream, q.get_device()):
+        for name, x in (("dq", q), ("dk", k)):
+            if res.get(name) is None:
+                res[name] = _new(x, x.dtype)
+        for name, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
+            if w is None:
+                res[name] = None
+            elif res.get(name) is None:
+                res[name] = _new(w, torch.float32)
+        if workspace is None and (q_weight is not None or k_weight is not None):
+            workspace = _scratch(kda_qk_norm_bwd_workspace_size(), q)
     _launch(_QK_NORM_BWD, q.get_device(), (_NORM_MODES[mode], eps, bool(interleaved)),
             (q, k, d_q_out, d_k_out, q_weight, k_weight, cos, sin, positions, res["dq"], res["dk"], res["dq_weight"],
              res["dk_weight"]), stream, workspace)

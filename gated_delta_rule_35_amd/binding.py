@@ -156,6 +156,24 @@ def _stream_handle(stream, tensors):
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
 
+_CURRENT = contextlib.nullcontext()
+
+
+def _place(stream, dev):
+    """Where a call's outputs and scratch are allocated: under its stream, so that the
+    caching allocator takes and reuses their memory in that stream's order."""
+    if stream is None:
+        return _CURRENT
+    if dev < 0:
+        raise ValueError("a call on a stream needs its tensors on the GPU")
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != dev:
+            raise ValueError(f"the stream is on GPU {stream.device.index}, the tensors are on GPU {dev}")
+        return torch.cuda.stream(stream)
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev))
+
+
 def _check(lib, status):
     if status != 0:
         raise KdaError(status, lib.kda_status_string(status).decode())
@@ -171,10 +189,8 @@ def kda_fwd_workspace_size(total_tokens, num_sequences, num_value_heads):
 
 def _workspace(workspace, q, v, cu_seqlens, stream):
     """(tensor, pointer, size) of a workspace argument: the given uint8 tensor, or
-    a fresh one from torch's caching allocator of the size the library asks for.
-    A fresh tensor is marked as used on an explicitly given stream, so the
-    caching allocator does not hand it out again before that stream's work on it
-    is done."""
+    a fresh one from torch's caching allocator, of the call's stream, of the size the
+    library asks for."""
     if workspace is None:
         if q.dim() != 4 or v.dim() != 4:
             return None, None, 0   # the C library rejects the shapes
@@ -182,9 +198,8 @@ def _workspace(workspace, q, v, cu_seqlens, stream):
         size = kda_fwd_workspace_size(q.shape[0] * q.shape[1], max(n, 0), v.shape[2])
         if size <= 0:
             return None, None, 0
-        workspace = torch.empty(size, dtype=torch.uint8, device=v.device)
-        if stream is not None and isinstance(stream, torch.cuda.Stream):
-            workspace.record_stream(stream)
+        with _place(stream, v.get_device()):
+            workspace = torch.empty(size, dtype=torch.uint8, device=v.device)
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -214,12 +229,13 @@ def _call(q, k, v, g, beta, scale, cu_seqlens, initial_state, out, final_state, 
         _check(lib, lib.kda_fwd_trace(*args, ctypes.byref(tr), s))
 
 
-def _outputs(q, v, cu_seqlens, out, final_state):
-    if out is None:
-        out = torch.empty(v.shape, dtype=torch.bfloat16, device=v.device)
-    if final_state is True:
-        n = q.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
-        final_state = torch.empty((n, v.shape[2], q.shape[3], v.shape[3]), dtype=torch.float32, device=v.device)
+def _outputs(q, v, cu_seqlens, out, final_state, stream):
+    with _place(stream, v.get_device()):
+        if out is None:
+            out = torch.empty(v.shape, dtype=torch.bfloat16, device=v.device)
+        if final_state is True:
+            n = q.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
+            final_state = torch.empty((n, v.shape[2], q.shape[3], v.shape[3]), dtype=torch.float32, device=v.device)
     return out, final_state
 
 
@@ -231,7 +247,7 @@ def kda_fwd(q, k, v, g, beta, scale, cu_seqlens=None, initial_state=None, out=No
     fixed-length batches that fill the device, else the two-pass kernels); with a
     uint8 device tensor of at least kda_fwd_workspace_size() bytes it is
     kda_fwd_ws (the two-pass kernels) on that workspace."""
-    out, final_state = _outputs(q, v, cu_seqlens, out, final_state)
+    out, final_state = _outputs(q, v, cu_seqlens, out, final_state, stream)
     entry = "kda_fwd" if workspace is None else "kda_fwd_ws"
     _call(q, k, v, g, beta, scale, cu_seqlens, initial_state, out, final_state, stream, None, workspace, entry)
     return out, final_state
@@ -241,7 +257,7 @@ def kda_fwd_fused(q, k, v, g, beta, scale, cu_seqlens=None, initial_state=None, 
                   stream=None):
     """The single-pass forward (C kda_fwd_fused).  Returns (out, final_state); out
     and final_state=True are allocated here when not given."""
-    out, final_state = _outputs(q, v, cu_seqlens, out, final_state)
+    out, final_state = _outputs(q, v, cu_seqlens, out, final_state, stream)
     _call(q, k, v, g, beta, scale, cu_seqlens, initial_state, out, final_state, stream, None, None,
           "kda_fwd_fused")
     return out, final_state
@@ -251,7 +267,7 @@ def kda_fwd_ws(q, k, v, g, beta, scale, cu_seqlens=None, initial_state=None, out
                stream=None, workspace=None):
     """The two-pass forward with a caller workspace (C kda_fwd_ws); `workspace`
     None takes one from torch's caching allocator.  Returns (out, final_state)."""
-    out, final_state = _outputs(q, v, cu_seqlens, out, final_state)
+    out, final_state = _outputs(q, v, cu_seqlens, out, final_state, stream)
     _call(q, k, v, g, beta, scale, cu_seqlens, initial_state, out, final_state, stream, None, workspace,
           "kda_fwd_ws")
     return out, final_state
@@ -263,9 +279,10 @@ def kda_fwd_qg(q, k, v, g, beta, scale, cu_seqlens=None, initial_state=None, out
     inclusive cumsum of g, bf16 of v's shape.  Returns (out, final_state, qg); out,
     qg and final_state=True are allocated here when not given.  Without
     `workspace` the C call allocates its records in stream order."""
-    out, final_state = _outputs(q, v, cu_seqlens, out, final_state)
+    out, final_state = _outputs(q, v, cu_seqlens, out, final_state, stream)
     if qg is None:
-        qg = torch.empty(v.shape, dtype=torch.bfloat16, device=v.device)
+        with _place(stream, v.get_device()):
+            qg = torch.empty(v.shape, dtype=torch.bfloat16, device=v.device)
     lib = load_library()
     tensors = (q, k, v, g, beta, cu_seqlens, initial_state, out, final_state, qg)
     for t in tensors:
@@ -287,7 +304,7 @@ def kda_fwd_noalloc(q, k, v, g, beta, scale, cu_seqlens=None, initial_state=None
     """kda_fwd_ws on the library's static device scratch (C kda_fwd_noalloc):
     the C call allocates nothing.  Returns (out, final_state); out and
     final_state=True are allocated here when not given."""
-    out, final_state = _outputs(q, v, cu_seqlens, out, final_state)
+    out, final_state = _outputs(q, v, cu_seqlens, out, final_state, stream)
     _call(q, k, v, g, beta, scale, cu_seqlens, initial_state, out, final_state, stream, None, None,
           "kda_fwd_noalloc")
     return out, final_state
@@ -317,7 +334,7 @@ def kda_fwd_trace(q, k, v, g, beta, scale, trace, cu_seqlens=None, initial_state
                   final_state=None, stream=None, workspace=None):
     """kda_fwd that also fills the fp32 intermediate dumps in `trace`, a dict with
     any of the keys G, Aqk, Akk, T, W, U, v_new, h (see include/kda.h)."""
-    out, final_state = _outputs(q, v, cu_seqlens, out, final_state)
+    out, final_state = _outputs(q, v, cu_seqlens, out, final_state, stream)
     _call(q, k, v, g, beta, scale, cu_seqlens, initial_state, out, final_state, stream, trace, workspace,
           "kda_fwd_trace")
     return out, final_state
@@ -356,12 +373,8 @@ def kda_fwd_cp(q, k, v, g, beta, scale, segment_chunks, first_segment_chunks=0, 
     kda_fwd_cp_packed_workspace_size() bytes (packed), or None (allocated here
     from torch's caching allocator)."""
     lib = load_library()
-    if out is None:
-        out = torch.empty(v.shape, dtype=torch.bfloat16, device=v.device)
     n_seq = q.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    if final_state is True:
-        final_state = torch.empty((n_seq, v.shape[2], q.shape[3], v.shape[3]), dtype=torch.float32,
-                                  device=v.device)
+    out, final_state = _outputs(q, v, cu_seqlens, out, final_state, stream)
     tensors = (q, k, v, g, beta, cu_seqlens, initial_state, out, final_state)
     for t in tensors:
         if t is not None and not t.is_cuda:
@@ -374,9 +387,8 @@ def kda_fwd_cp(q, k, v, g, beta, scale, segment_chunks, first_segment_chunks=0, 
             size = kda_fwd_cp_workspace_size(q.shape[0], q.shape[1], v.shape[2], L, L0)
         else:
             size = kda_fwd_cp_packed_workspace_size(q.shape[0] * q.shape[1], max(n_seq, 0), v.shape[2], L, L0)
-        workspace = torch.empty(max(size, 0), dtype=torch.uint8, device=v.device)
-        if stream is not None and isinstance(stream, torch.cuda.Stream):
-            workspace.record_stream(stream)
+        with _place(stream, v.get_device()):
+            workspace = torch.empty(max(size, 0), dtype=torch.uint8, device=v.device)
     ws_ptr = workspace.data_ptr() if workspace is not None and workspace.numel() else None
     ws_size = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib, lib.kda_fwd_cp(_ref(descs[0]), _ref(descs[1]), _ref(descs[2]), _ref(descs[3]), _ref(descs[4]),
@@ -391,11 +403,12 @@ def kda_decode(q, k, v, g, beta, scale, state, out=None, new_state=None, stream=
     state); the new state goes to `new_state`, by default `state` itself (updated
     in place; allocated when state is None).  Returns (out, new_state)."""
     lib = load_library()
-    if out is None:
-        out = torch.empty(v.shape, dtype=torch.bfloat16, device=v.device)
-    if new_state is None:
-        new_state = state if state is not None else torch.empty(
-            (v.shape[0], v.shape[1], q.shape[2], v.shape[2]), dtype=torch.float32, device=v.device)
+    with _place(stream, v.get_device()):
+        if out is None:
+            out = torch.empty(v.shape, dtype=torch.bfloat16, device=v.device)
+        if new_state is None:
+            new_state = state if state is not None else torch.empty(
+                (v.shape[0], v.shape[1], q.shape[2], v.shape[2]), dtype=torch.float32, device=v.device)
     tensors = (q, k, v, g, beta, state, new_state, out)
     for t in tensors:
         if t is not None and not t.is_cuda:
@@ -428,15 +441,16 @@ def kda_bwd(q, k, v, g, beta, scale, d_out, initial_state=None, d_final_state=No
     dev = v.device
     out = dict(grads or {})
     f32 = torch.float32
-    for name, shape in (("dq", q.shape), ("dk", q.shape), ("dv", v.shape), ("dg", g.shape), ("dbeta", beta.shape)):
-        if out.get(name) is None:
-            out[name] = torch.empty(shape, dtype=f32, device=dev)
-    if isinstance(d_initial_state, torch.Tensor):
-        out["dh0"] = d_initial_state
-    elif d_initial_state:
-        out["dh0"] = torch.empty((N, Hv, q.shape[3], v.shape[3]), dtype=f32, device=dev)
-    else:
-        out["dh0"] = None
+    with _place(stream, v.get_device()):
+        for name, shape in (("dq", q.shape), ("dk", q.shape), ("dv", v.shape), ("dg", g.shape), ("dbeta", beta.shape)):
+            if out.get(name) is None:
+                out[name] = torch.empty(shape, dtype=f32, device=dev)
+        if isinstance(d_initial_state, torch.Tensor):
+            out["dh0"] = d_initial_state
+        elif d_initial_state:
+            out["dh0"] = torch.empty((N, Hv, q.shape[3], v.shape[3]), dtype=f32, device=dev)
+        else:
+            out["dh0"] = None
     tensors = (q, k, v, g, beta, cu_seqlens, initial_state, d_out, d_final_state, out["dq"], out["dk"], out["dv"],
                out["dg"], out["dbeta"], out["dh0"])
     for t in tensors:
@@ -486,24 +500,6 @@ def _launch(entry, dev, scalars, tensors, stream, workspace=None):
             status = call(entry, dev, s, workspace, scalars, tensors)
     if status:
         _check(_lib, status)
-
-
-_CURRENT = contextlib.nullcontext()
-
-
-def _place(stream, dev):
-    """Where a call's outputs and scratch are allocated: under its stream, so that the
-    caching allocator takes and reuses their memory in that stream's order."""
-    if stream is None:
-        return _CURRENT
-    if dev < 0:
-        raise ValueError("a call on a stream needs its tensors on the GPU")
-    if isinstance(stream, torch.cuda.Stream):
-        if stream.device.index != dev:
-            raise ValueError(f"the stream is on GPU {stream.device.index}, the tensors are on GPU {dev}")
-        return torch.cuda.stream(stream)
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    return torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev))
 
 
 def _new(like, dtype, shape=None):

@@ -64,7 +64,7 @@ def calls(monkeypatch):
         def __getattr__(self, name):
             if name.endswith("_size"):
                 return lambda *a: 4096
-            return lambda *a: seen.append(a[-1].value if hasattr(a[-1], "value") else a[-1]) or 0
+            return lambda *a: seen.append(a[-1].value or 0) or 0   # c_void_p(0).value is None
 
     def call(entry, dev, stream, workspace, scalars, tensors):
         seen.append(stream)
@@ -120,15 +120,19 @@ PER_HEAD = [gdr_fwd, gdr_bwd, gdr_decode, qk_norm, qk_norm_bwd]
 STREAMS = [77, 0, "stream", None]
 
 
-@pytest.mark.parametrize("call", PER_HEAD)
-@pytest.mark.parametrize("stream", STREAMS)
-def test_allocations_belong_to_the_stream_of_the_call(calls, call, stream):
+def check_allocations(calls, call, stream):
     s = FakeStream(55) if stream == "stream" else stream
     call(s)
     want = HERE if s is None else getattr(s, "cuda_stream", s)
     assert calls == [want]
     assert len(OnGpu.allocated) >= 2 and set(OnGpu.allocated) == {want}
     assert OnGpu.current == [HERE]
+
+
+@pytest.mark.parametrize("call", PER_HEAD)
+@pytest.mark.parametrize("stream", STREAMS)
+def test_allocations_belong_to_the_stream_of_the_call(calls, call, stream):
+    check_allocations(calls, call, stream)
 
 
 @pytest.mark.parametrize("call", PER_HEAD)
@@ -187,3 +191,43 @@ def test_unfinished_calls_on_two_streams_share_nothing(how, monkeypatch):
                 assert all(a >= f or e >= b for a, b in spans for e, f in others)
     for g, r in zip(got, want):
         assert all(torch.equal(a, b) for a, b in zip(g, r))
+
+
+def fwd(name, **kw):
+    def call(stream):
+        x, b, f = inputs(channels=True)
+        getattr(binding, name)(*x, 1.0, final_state=True, stream=stream, **kw)
+    call.__name__ = name
+    return call
+
+
+def fwd_trace(stream):
+    x, b, f = inputs(channels=True)
+    binding.kda_fwd_trace(*x, 1.0, {}, final_state=True, stream=stream)
+
+
+def bwd(stream):
+    x, b, f = inputs(channels=True)
+    binding.kda_bwd(*x, 1.0, b(1, 8, 2, 128), d_initial_state=True, stream=stream)
+
+
+def decode(stream):
+    x, b, f = inputs(channels=True)
+    binding.kda_decode(b(8, 1, 128), b(8, 1, 128), b(8, 2, 128), f(8, 2, 128), f(8, 2), 1.0, None, stream=stream)
+
+
+PER_CHANNEL = [fwd(n) for n in ("kda_fwd", "kda_fwd_fused", "kda_fwd_ws", "kda_fwd_qg", "kda_fwd_noalloc")] + \
+    [fwd("kda_fwd_cp", segment_chunks=2), fwd_trace, bwd, decode]
+
+
+@pytest.mark.parametrize("call", PER_CHANNEL)
+@pytest.mark.parametrize("stream", STREAMS)
+def test_allocations_of_the_per_channel_rule(calls, call, stream):
+    check_allocations(calls, call, stream)
+
+
+@pytest.mark.parametrize("call", PER_CHANNEL)
+def test_a_stream_of_another_device_is_refused_by_the_per_channel_rule(calls, call):
+    with pytest.raises(ValueError):
+        call(FakeStream(55, index=1))
+    assert calls == [] and OnGpu.allocated == []

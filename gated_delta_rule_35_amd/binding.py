@@ -483,12 +483,18 @@ def _load_caller():
     return _call_entry
 
 
+def _gpu_of(t, entry):
+    """The GPU that t lies on, asked before anything is allocated for the call."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{_ENTRIES[entry]} needs every tensor on the GPU")
+    return dev
+
+
 def _launch(entry, dev, scalars, tensors, stream, workspace=None):
     """Calls entry point number `entry` with `tensors` (None: NULL), all of which must lie
     on GPU `dev`, which is made current for the call."""
     call = _call_entry or _load_caller()
-    if dev < 0:
-        raise ValueError(f"{_ENTRIES[entry]} needs every tensor on the GPU")
     if stream is None:
         s = torch._C._cuda_getCurrentRawStream(dev)
     else:
@@ -533,15 +539,16 @@ def kda_gdr_fwd(q, k, v, g, beta, scale, cu_seqlens=None, initial_state=None, ou
     out and final_state=True are allocated here when not given.  `workspace`: a uint8
     device tensor of kda_gdr_fwd_workspace_size() bytes, or None (taken here from
     torch's caching allocator)."""
-    with _place(stream, v.get_device()):
+    dev = _gpu_of(v, _GDR_FWD)
+    with _place(stream, dev):
         if out is None:
             out = _new(v, torch.bfloat16)
         if final_state is True:
             final_state = _new(v, torch.float32, (_sequences(q, cu_seqlens), v.shape[-2], 128, 128))
-        if workspace is None and q.dim() == 4 and v.dim() == 4 and v.is_cuda:   # the C library rejects other ranks
+        if workspace is None and q.dim() == 4 and v.dim() == 4:   # the C library rejects other ranks
             size = kda_gdr_fwd_workspace_size(q.shape[0] * q.shape[1], _sequences(q, cu_seqlens), v.shape[2])
             workspace = _scratch(size, v)
-    _launch(_GDR_FWD, v.get_device(), (scale,), (q, k, v, g, beta, cu_seqlens, initial_state, out, final_state), stream,
+    _launch(_GDR_FWD, dev, (scale,), (q, k, v, g, beta, cu_seqlens, initial_state, out, final_state), stream,
             workspace)
     return out, final_state
 
@@ -552,8 +559,9 @@ def kda_gdr_bwd(q, k, v, g, beta, scale, d_out, initial_state=None, d_final_stat
     (fp32 [N, Hv, 128, 128] when d_initial_state is True or a tensor, else None).
     `grads` may hold preallocated outputs under those names; `workspace` a uint8 device
     tensor of kda_gdr_bwd_workspace_size() bytes (None: taken here)."""
+    dev = _gpu_of(v, _GDR_BWD)
     res = dict(grads or {})
-    with _place(stream, v.get_device()):
+    with _place(stream, dev):
         for name, like, dtype in (("dq", q, torch.bfloat16), ("dk", k, torch.bfloat16), ("dv", v, torch.bfloat16),
                                   ("dg", g, torch.float32), ("dbeta", beta, torch.float32)):
             if res.get(name) is None:
@@ -567,7 +575,7 @@ def kda_gdr_bwd(q, k, v, g, beta, scale, d_out, initial_state=None, d_final_stat
         if workspace is None and q.dim() == 4 and v.dim() == 4:
             size = kda_gdr_bwd_workspace_size(q.shape[0] * q.shape[1], _sequences(q, cu_seqlens), v.shape[2])
             workspace = _scratch(size, v)
-    _launch(_GDR_BWD, v.get_device(), (scale,),
+    _launch(_GDR_BWD, dev, (scale,),
             (q, k, v, g, beta, cu_seqlens, initial_state, d_out, d_final_state, res["dq"], res["dk"], res["dv"],
              res["dg"], res["dbeta"], res["dh0"]), stream, workspace)
     return res
@@ -581,12 +589,13 @@ def kda_gdr_decode(q, k, v, g, beta, scale, state, state_indices=None, out=None,
     Returns (out, new_state); rows of `out` that are skipped are not written."""
     if new_state is None and state is None and state_indices is not None:
         raise ValueError("kda_gdr_decode needs a pool where state_indices name its slots")
-    with _place(stream, v.get_device()):
+    dev = _gpu_of(v, _GDR_DECODE)
+    with _place(stream, dev):
         if out is None:
             out = _new(v, torch.bfloat16)
         if new_state is None:
             new_state = state if state is not None else _new(v, torch.float32, (v.shape[0], v.shape[1], 128, 128))
-    _launch(_GDR_DECODE, v.get_device(), (scale,), (q, k, v, g, beta, state, new_state, state_indices, out), stream)
+    _launch(_GDR_DECODE, dev, (scale,), (q, k, v, g, beta, state, new_state, state_indices, out), stream)
     return out, new_state
 
 
@@ -606,9 +615,10 @@ def kda_qk_norm(q, k, q_weight=None, k_weight=None, mode="l2", eps=1e-6, cos=Non
     when not given."""
     if mode not in _NORM_MODES:
         raise ValueError(f"kda_qk_norm: mode {mode!r} is neither 'l2' nor 'rms'")
-    with _place(stream, q.get_device()):
+    dev = _gpu_of(q, _QK_NORM)
+    with _place(stream, dev):
         qo, ko = out if out is not None else (_new(q, torch.bfloat16), _new(k, torch.bfloat16))
-    _launch(_QK_NORM, q.get_device(), (_NORM_MODES[mode], eps, bool(interleaved)),
+    _launch(_QK_NORM, dev, (_NORM_MODES[mode], eps, bool(interleaved)),
             (q, k, q_weight, k_weight, cos, sin, positions, qo, ko), stream)
     return qo, ko
 
@@ -620,8 +630,9 @@ def kda_qk_norm_bwd(q, k, d_q_out, d_k_out, q_weight=None, k_weight=None, mode="
     outputs under those names."""
     if mode not in _NORM_MODES:
         raise ValueError(f"kda_qk_norm_bwd: mode {mode!r} is neither 'l2' nor 'rms'")
+    dev = _gpu_of(q, _QK_NORM_BWD)
     res = dict(grads or {})
-    with _place(stream, q.get_device()):
+    with _place(stream, dev):
         for name, x in (("dq", q), ("dk", k)):
             if res.get(name) is None:
                 res[name] = _new(x, x.dtype)
@@ -632,7 +643,7 @@ def kda_qk_norm_bwd(q, k, d_q_out, d_k_out, q_weight=None, k_weight=None, mode="
                 res[name] = _new(w, torch.float32)
         if workspace is None and (q_weight is not None or k_weight is not None):
             workspace = _scratch(kda_qk_norm_bwd_workspace_size(), q)
-    _launch(_QK_NORM_BWD, q.get_device(), (_NORM_MODES[mode], eps, bool(interleaved)),
+    _launch(_QK_NORM_BWD, dev, (_NORM_MODES[mode], eps, bool(interleaved)),
             (q, k, d_q_out, d_k_out, q_weight, k_weight, cos, sin, positions, res["dq"], res["dk"], res["dq_weight"],
              res["dk_weight"]), stream, workspace)
     return res

@@ -476,7 +476,11 @@ def _load_caller():
     """The extension's call(), bound to the loaded library."""
     global _call_entry
     lib = load_library()
-    from . import _kda_py
+    try:
+        from . import _kda_py
+    except ImportError as e:
+        raise ImportError("the extension _kda_py is missing or built for another Python: build it with "
+                          "gated_delta_rule_35_amd/build.py (or __graft_entry__.build())") from e
     _kda_py.bind(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _ENTRIES),
                  (torch.bfloat16, torch.float16, torch.float32, torch.int32))
     _call_entry = _kda_py.call

@@ -1,5 +1,6 @@
 """Builds libkda.so, the HIP library behind the C ABI in include/kda.h, for gfx950, and
-_kda_py.so, the small Python extension that calls part of it.
+_kda_py, the small Python extension that calls part of it (its file name carries the
+interpreter's tag).
 
 hipcc compiles the kernels and the C-ABI front end into one shared object next to
 this file.  -packed-fp32-ops is turned off for the device code: the compiler then
@@ -21,19 +22,18 @@ SOURCES = [os.path.join(HERE, "csrc", f)
               "kda_gdr_prep.hip", "kda_gdr_fwd.hip", "kda_gdr_bwd.hip", "kda_gdr_grads.hip", "kda_gdr_decode.hip", "kda_qk_norm.hip",
               "kda_api.cpp", "kda_gdr_api.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+# the Python extension that makes the descriptors
+CALLER = os.path.join(HERE, "_kda_py" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 
-CALLER = os.path.join(HERE, "_kda_py.so")   # the Python extension that makes the descriptors
-
-
-def build_caller(verbose: bool = False) -> str:
+def _compile_caller(verbose: bool) -> str:
+    out = CALLER + ".tmp"
     cmd = ["gcc", "-O2", "-std=c11", "-fPIC", "-shared", "-Wall", "-I", sysconfig.get_paths()["include"],
-           "-o", CALLER + ".tmp", os.path.join(HERE, "csrc", "kda_py.c")]
+           "-o", out, os.path.join(HERE, "csrc", "kda_py.c")]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
-    os.replace(CALLER + ".tmp", CALLER)
-    return CALLER
+    return out
 
 
 def build(verbose: bool = False) -> str:
@@ -48,8 +48,9 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError("hipcc failed:\n" + out)
     if verbose and out.strip():
         print(out)
-    os.replace(LIB + ".tmp", LIB)
-    build_caller(verbose)
+    caller = _compile_caller(verbose)
+    os.replace(LIB + ".tmp", LIB)   # both, or neither
+    os.replace(caller, CALLER)
     return LIB
 
 

@@ -44,10 +44,9 @@ constexpr int GDR_FRAG = 1024;
 // a group four apart from the group's before, else such a read meets each bank four times.
 __host__ __device__ constexpr int frag_piece(int l) { return 16 * (l ^ ((l >> 4) << 2)); }
 constexpr int GDR_TRI = 6 * GDR_FRAG;              // one part of a triangular operand
-// Forward, fp16: T in two parts, A in one, the per-token rows.
-constexpr int FWD_T = 0, FWD_A = 2 * GDR_TRI, FWD_SC = 3 * GDR_TRI, FWD_ROWS = 8, FWD_REC = FWD_SC + FWD_ROWS * 256;
-// Backward, bf16: T in three parts, the per-token rows, A (scale included) in three parts.
-constexpr int GDR_T = 0, GDR_SC = 3 * GDR_TRI, GDR_A = GDR_SC + 1024, GDR_REC = GDR_A + 3 * GDR_TRI;
+// T in three bf16 parts and the per-token rows; the backward also A (scale included) in three parts.
+constexpr int GDR_T = 0, GDR_SC = 3 * GDR_TRI, FWD_REC = GDR_SC + 2048;
+constexpr int GDR_A = GDR_SC + 1024, GDR_REC = GDR_A + 3 * GDR_TRI;
 
 hipError_t launch_gdr_prep(const GdrParams& p, bool bwd, hipStream_t stream);
 hipError_t launch_gdr_grads(const GdrParams& p, int cus, hipStream_t stream);

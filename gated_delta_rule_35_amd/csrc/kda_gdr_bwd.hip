@@ -38,26 +38,6 @@ struct ScanL {
     static constexpr int K = 0, Q = 16384, V = 32768, REC = 40960, BYTES = REC + GDR_REC;
 };
 
-// The lane's eight (key channel, tile) rows: channel of row 4 g + r of tile t.
-__device__ __forceinline__ int state_row(int t, int g, int r) { return 32 * (t >> 1) + 8 * g + 4 * (t & 1) + r; }
-
-// A operand (m, kk) of a tile [64][128]: rows 16 m + jj, channels 32 kk + 8 g ..
-__device__ __forceinline__ bf16x8 row_frag(const char* tile, int m, int kk, int g, int jj) {
-    return lds_bf8(tile + tile_off(16 * m + jj, 4 * kk + g));
-}
-// A operand of the transposed tile: state tile t's channels, tokens of k step kk.
-__device__ __forceinline__ bf16x8 col_frag(const char* tile, int t, int kk, int g, int jj) {
-    const int row = 32 * kk + 4 * g + (jj >> 2), piece = 4 * (t >> 1) + (jj & 3), b = 8 * (t & 1);
-    return join(lds_tr(tile + tile_off(row, piece) + b), lds_tr(tile + tile_off(row + 16, piece) + b));
-}
-// Columns 16 w + jj of tokens 16 m + 4 g + r, r < 4, of the [64][64] slice, as packed bf16.
-__device__ __forceinline__ u32x2 slice_frag(const char* v, int m, int w, int g, int jj) {
-    return lds_tr(v + (16 * m + 4 * g + (jj >> 2)) * 128 + 32 * w + 8 * (jj & 3));
-}
-__device__ __forceinline__ f32x4 widen(u32x2 x) { return f32x4{bf_lo(x[0]), bf_hi(x[0]), bf_lo(x[1]), bf_hi(x[1])}; }
-
-// Index of fragment (m, kk) in a record's lower triangular list.
-__device__ __forceinline__ constexpr int tri_frag(int m, int kk) { return m < 2 ? m : 2 * m - 2 + kk; }
 // Fragment (m, kk) of the transposed matrix (rows 16 m + jj, k step kk), kk >= m / 2.
 __device__ __forceinline__ bf16x8 tri_col_frag(const char* part, int m, int kk, int g, int jj) {
     const int at = frag_piece(16 * (jj & 3) + 4 * g + (jj >> 2)) + 8 * (m & 1);
@@ -109,42 +89,6 @@ __device__ __forceinline__ void tile_times_state(const char* tile, const f32x4 (
             interleave<4, 5, 1, 1>();
         }
     }
-}
-
-// y = a triangular matrix in three parts times x, fragment(part, m, kk) its operands: the
-// parts' products of 2^-16 and more of the leading one's, the small parts first, six tiles
-// side by side.  work(n), n = 2, 1, 0, is done meanwhile.
-template <bool UPPER, typename F, typename W>
-__device__ __forceinline__ void tri_times(F fragment, const f32x4 (&x)[4], f32x4 (&y)[4], W work) {
-    // the six (m, kk) of the triangle: lower kk <= m / 2, upper kk >= m / 2
-    constexpr int M[6] = {0, 1, 2, 3, UPPER ? 0 : 2, UPPER ? 1 : 3};
-    constexpr int KK[6] = {0, 0, UPPER ? 1 : 0, UPPER ? 1 : 0, 1, 1};
-    bf16x8 f[2][6];
-    f32x4 a[6];
-#pragma unroll
-    for (int i = 0; i < 6; ++i) {
-        f[0][i] = fragment(2, M[i], KK[i]);
-        a[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-    const Split<3> xb[2] = {split_acc<3>(x[0], x[1]), split_acc<3>(x[2], x[3])};
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int n = 2; n >= 0; --n) {
-        if (n) {
-#pragma unroll
-            for (int i = 0; i < 6; ++i) f[(n + 1) & 1][i] = fragment(n - 1, M[i], KK[i]);
-        }
-        work(n);
-#pragma unroll
-        for (int d = 2 - n; d >= 0; --d) {
-#pragma unroll
-            for (int i = 0; i < 6; ++i) a[i] = mfma_bf(f[n & 1][i], xb[KK[i]].s[d], a[i]);
-            if (d == 2 - n) interleave<6, 2, 2, 0>();
-            else interleave<6, 2, 0, 0>();
-        }
-    }
-#pragma unroll
-    for (int m = 0; m < 4; ++m) y[m] = (M[4] == m) ? a[m] + a[4] : (M[5] == m) ? a[m] + a[5] : a[m];
 }
 
 // A choice made when compiling, as an argument.

@@ -3,10 +3,9 @@
 // Matrix products run on the 16x16x32 instructions for 16-bit operands.  q, k, v and the
 // output's gradient are bf16; an fp32 operand enters as the sum of parts, each the rounding
 // of what the parts before it leave, so that products keep fp32's accuracy at a third to a
-// sixth of the 16-bit rate, several times that of the fp32 matrix instructions.  The
-// backward's walks use bf16 parts, three of which hold all 24 bits at any size; the
-// forward's walk and the token gradients use fp16 parts, two of which hold 22 bits of what
-// powers of two keep in range (the forward's q and k too are fp16 rows divided by such).
+// sixth of the 16-bit rate, several times that of the fp32 matrix instructions.  The walks
+// use bf16 parts, three of which hold all 24 bits at any size; the token gradients use fp16
+// parts, two of which hold 22 bits of what powers of two keep in range.
 #pragma once
 #include "kda_device.h"
 #include "kda_gdr.h"
@@ -99,29 +98,9 @@ __device__ __forceinline__ float max_abs(float m, f32x4 x) {
     asm("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(m) : "v"(x[2]), "v"(x[3]));
     return m;
 }
-// The power of two that divides a bf16 row's largest entry into [1, 2): the row lies in
-// lanes l, l + 16, l + 32, l + 48, 32 entries each.  0 where there is nothing to divide
-// (a row of zeros) or the largest is not finite.
-__device__ __forceinline__ float row_power(const bf16x8 (&x)[4]) {
-    typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
-    u16x8 m = __builtin_bit_cast(u16x8, x[0]) & (uint16_t)0x7fff;
-#pragma unroll
-    for (int i = 1; i < 4; ++i)
-        m = __builtin_elementwise_max(m, (u16x8)(__builtin_bit_cast(u16x8, x[i]) & (uint16_t)0x7fff));
-    uint32_t t = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t = max(t, (uint32_t)m[i]);
-    t = max(t, (uint32_t)__shfl_xor((int)t, 16));
-    t = max(t, (uint32_t)__shfl_xor((int)t, 32));
-    const uint32_t e = t >> 7;   // biased exponent
-    return e == 0 || e == 255 ? 0.f : __uint_as_float(min(e, 253u) << 23);
-}
-
-// Per-token rows of a record's numbers, in elements: e^G, e^{G_last - G}, beta (forward:
-// beta 2^ek), e^{G_last}; forward also beta 2^{2 ek} e^G, 2^ek, 2^eq (what the scan divides
-// the token's k and q by; 2^ek is 0 for a key of zeros, whose u takes no part) and the
-// chunk's largest 2^ek, within 2^-60 and 2^60 (0: all its keys are zero).
-enum { SC_EG = 0, SC_GA = 64, SC_BE = 128, SC_EL = 192, SC_EGK = 256, SC_KS = 320, SC_QS = 384, SC_KP = 448 };
+// Per-token rows of a record's numbers, in elements: e^G, e^{G_last - G}, beta; backward also
+// e^{G_last}; forward also G as an fp32 value and its remainder.
+enum { SC_EG = 0, SC_GA = 64, SC_BE = 128, SC_EL = 192, SC_GH = 192, SC_GL = 256 };
 
 // ---- swizzled [64][128] bf16 tiles in LDS: rows of 256 bytes, whose sixteen 16-byte
 // pieces are permuted by tsw(row), so that both an operand read (sixteen consecutive
@@ -190,6 +169,63 @@ __device__ __forceinline__ void interleave() {
         if (VM) __builtin_amdgcn_sched_group_barrier(0x040, VM, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
+}
+
+// ---- walks over the chunks: a wave owns sixteen columns of the state in eight accumulator tiles ----
+// The lane's eight (key channel, tile) rows: channel of row 4 g + r of tile t.
+__device__ __forceinline__ int state_row(int t, int g, int r) { return 32 * (t >> 1) + 8 * g + 4 * (t & 1) + r; }
+
+// A operand (m, kk) of a tile [64][128]: rows 16 m + jj, channels 32 kk + 8 g ..
+__device__ __forceinline__ bf16x8 row_frag(const char* tile, int m, int kk, int g, int jj) {
+    return lds_bf8(tile + tile_off(16 * m + jj, 4 * kk + g));
+}
+// A operand of the transposed tile: state tile t's channels, tokens of k step kk.
+__device__ __forceinline__ bf16x8 col_frag(const char* tile, int t, int kk, int g, int jj) {
+    const int row = 32 * kk + 4 * g + (jj >> 2), piece = 4 * (t >> 1) + (jj & 3), b = 8 * (t & 1);
+    return join(lds_tr(tile + tile_off(row, piece) + b), lds_tr(tile + tile_off(row + 16, piece) + b));
+}
+// Columns 16 w + jj of tokens 16 m + 4 g + r, r < 4, of the [64][64] slice, as packed bf16.
+__device__ __forceinline__ u32x2 slice_frag(const char* v, int m, int w, int g, int jj) {
+    return lds_tr(v + (16 * m + 4 * g + (jj >> 2)) * 128 + 32 * w + 8 * (jj & 3));
+}
+__device__ __forceinline__ f32x4 widen(u32x2 x) { return f32x4{bf_lo(x[0]), bf_hi(x[0]), bf_lo(x[1]), bf_hi(x[1])}; }
+
+// Index of fragment (m, kk) in a record's lower triangular list.
+__device__ __forceinline__ constexpr int tri_frag(int m, int kk) { return m < 2 ? m : 2 * m - 2 + kk; }
+// y = a triangular matrix in three parts times x, fragment(part, m, kk) its operands: the
+// parts' products of 2^-16 and more of the leading one's, the small parts first, six tiles
+// side by side.  work(n), n = 2, 1, 0, is done meanwhile.
+template <bool UPPER, typename F, typename W>
+__device__ __forceinline__ void tri_times(F fragment, const f32x4 (&x)[4], f32x4 (&y)[4], W work) {
+    // the six (m, kk) of the triangle: lower kk <= m / 2, upper kk >= m / 2
+    constexpr int M[6] = {0, 1, 2, 3, UPPER ? 0 : 2, UPPER ? 1 : 3};
+    constexpr int KK[6] = {0, 0, UPPER ? 1 : 0, UPPER ? 1 : 0, 1, 1};
+    bf16x8 f[2][6];
+    f32x4 a[6];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+        f[0][i] = fragment(2, M[i], KK[i]);
+        a[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    const Split<3> xb[2] = {split_acc<3>(x[0], x[1]), split_acc<3>(x[2], x[3])};
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 2; n >= 0; --n) {
+        if (n) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) f[(n + 1) & 1][i] = fragment(n - 1, M[i], KK[i]);
+        }
+        work(n);
+#pragma unroll
+        for (int d = 2 - n; d >= 0; --d) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) a[i] = mfma_bf(f[n & 1][i], xb[KK[i]].s[d], a[i]);
+            if (d == 2 - n) interleave<6, 2, 2, 0>();
+            else interleave<6, 2, 0, 0>();
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) y[m] = (M[4] == m) ? a[m] + a[4] : (M[5] == m) ? a[m] + a[5] : a[m];
 }
 
 // ---- chunks ----

@@ -2,32 +2,29 @@
 // gfx950 (MI355X).
 //
 // For a chunk of 64 tokens with G the running sum of g and Gam_ij = e^{G_i - G_j}:
-//   A = scale (Q K^T) Gam, j <= i;   M = beta_i (K K^T) Gam, j < i;   T = (I + M)^{-1}
-// The decay is one number per token, so Q K^T and K K^T are formed once per q/k head
-// from the bf16 operands as they are, and every value head of the group only scales
+//   M = beta_i (K K^T) Gam, j < i;   T = (I + M)^{-1};   backward also A = scale (Q K^T) Gam, j <= i
+// The decay is one number per token, so the products are formed once per q/k head from
+// the bf16 operands as they are, and every value head of the group only scales
 // them: Gam_ij <= 1 is formed from the differences themselves, so no operand needs an
 // anchor and no decay is out of range.
 //
 // One 256-thread work-group per (chunk slot, q/k head) walks the group's value heads.
-// k and q come into LDS by DMA, where M and A go once the products are formed.  Wave w
+// k (and q) come into LDS by DMA, where M (and A) go once the products are formed.  Wave w
 // takes the diagonal tile (w, w) of both and one or two of the six below.  T in fp32: wave
 // w inverts the diagonal block w by forward substitution, then forms block column w
 // downwards on v_mfma_f32_16x16x4f32,
 //   T_IJ = -T_II sum_{K=J}^{I-1} M_IK T_KJ,
 // with the T_KJ of its column in registers (an accumulator tile is the next product's
-// B operand).  T and A leave as operand fragments: for the backward in three bf16 parts
-// each; for the forward T in two fp16 parts and A in one, without the scale and divided
-// by the powers of two 2^eq and 2^ek that the scan divides q's and k's rows by.  The
-// forward's T is that of the rows times 2^ek, D T D^{-1} with D = diag(2^ek): its entries
-// are at most |beta_i k^_i| 2^{2 ek_i} |k^_j|, k^ = k / 2^ek, so that beta |k|^2 <= 2 keeps
-// them below 2 |k^_j| / |k^_i| <= 46 for keys of any sizes beside each other.
+// B operand).  T and A leave as operand fragments in three bf16 parts each, the forward's T
+// with its columns times beta.  The forward's walk forms A itself, from the k and q that it
+// holds anyway, so that q is not read here and records stay at 20 KB.
 //
-// At B=2 H=64 T=8192 (16,384 chunks of a head): forward 192 us, 0.94 GB at 4.9 TB/s; with the
+// At B=2 H=64 T=8192 (16,384 chunks of a head): forward 135 us, 0.6 GB at 4.4 TB/s; with the
 // backward's records 207 us, 1.22 GB at 5.9 TB/s (part of what it writes stays in the
-// last-level cache).  What brought it there from 332 us: four work-groups a compute unit, k
+// last-level cache).  What brought the latter there: four work-groups a compute unit, k
 // and q by DMA, and the tiles dealt evenly; a form that kept M and A beside k and q in LDS
-// (two work-groups a unit) took 292 us.  Forming the operands inside the walk instead, a
-// work-group for both, took 848 us and more for 680 us of the two kernels then.
+// (two work-groups a unit) took 292 us of the forward's 200 then.  Forming T inside the walk
+// instead, a work-group for both, took 848 us and more for 680 us of the two kernels then.
 // Fragment (m, kk) holds in lane l rows 16 m + l % 16, columns 32 kk + 16 (s / 4) +
 // 4 (l / 16) + s % 4, s < 8: the order in which accumulator tiles list a 32-wide k
 // step.  The lists hold (0,0) (1,0) (2,0) (2,1) (3,0) (3,1), zeros above the diagonal.
@@ -46,7 +43,7 @@ __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p)
     char *const tk = reinterpret_cast<char*>(mats), *const tq = tk + 16384;   // before them k and q
     static_assert(2 * 64 * SP * 4 >= 2 * 16384, "k and q fit where M and A go");
     __shared__ GSum sG[64];
-    __shared__ __attribute__((aligned(16))) float sBeta[64], sKp[64], sQp[64];
+    __shared__ __attribute__((aligned(16))) float sBeta[64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int slot = (int)blockIdx.x / p.Hq, hq = (int)blockIdx.x % p.Hq, R = p.Hv / p.Hq;
@@ -65,8 +62,9 @@ __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p)
     {
         const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(tk));
         dma_tile(chunk_rsrc(p.k.p + row * p.k.sb + tok * p.k.st + hq * p.k.sh, p.k.st, rows, DK), lds, p.k.st, w, 4, lane);
-        dma_tile(chunk_rsrc(p.q.p + row * p.q.sb + tok * p.q.st + hq * p.q.sh, p.q.st, rows, DK), lds + 16384, p.q.st, w,
-                 4, lane);
+        if (BWD)
+            dma_tile(chunk_rsrc(p.q.p + row * p.q.sb + tok * p.q.st + hq * p.q.sh, p.q.st, rows, DK), lds + 16384, p.q.st,
+                     w, 4, lane);
         if (w == 0) {
             sG[lane] = gate_sum(gate);
             sBeta[lane] = beta;
@@ -87,37 +85,23 @@ __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p)
             bf16x8 aq[4], ak[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                aq[c] = lds_bf8(tq + tile_off(16 * ti[x] + jj, 4 * c + g));
+                if (BWD) aq[c] = lds_bf8(tq + tile_off(16 * ti[x] + jj, 4 * c + g));
                 ak[c] = lds_bf8(tk + tile_off(16 * ti[x] + jj, 4 * c + g));
-            }
-            if (!BWD && x == 0) {   // what the scan divides row 16 w + jj of k and q by (sKp 0: a row of zeros)
-                const float kp = row_power(ak), qp = row_power(aq);
-                if (g == 0) {
-                    sKp[16 * w + jj] = kp;
-                    sQp[16 * w + jj] = qp > 0.f ? qp : 1.f;
-                }
             }
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const bf16x8 b = x == 0 ? ak[c] : lds_bf8(tk + tile_off(16 * tj[x] + jj, 4 * c + g));
-                qk[x] = mfma_bf(aq[c], b, qk[x]);
+                if (BWD) qk[x] = mfma_bf(aq[c], b, qk[x]);
                 kk[x] = mfma_bf(ak[c], b, kk[x]);
             }
         }
     }
     __syncthreads();   // k and q are read
-    float kmax = 0.f;   // wave 0: the largest of the chunk's key divisors
-    if (!BWD && w == 0) {
-        kmax = sKp[lane];
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) kmax = fmaxf(kmax, __shfl_xor(kmax, m));
-        if (kmax > 0.f) kmax = fminf(fmaxf(kmax, 0x1p-60f), 0x1p60f);
-    }
     // tiles above the diagonal that fragments cover
     for (int e = tid; e < 512; e += 256) {
         const int t = e >> 8, x = e & 255, at = (32 * t + (x >> 4)) * SP + 32 * t + 16 + (x & 15);
         sM[at] = 0.f;
-        sA[at] = 0.f;
+        if (BWD) sA[at] = 0.f;
     }
 
     for (int r = 0; r < R; ++r) {
@@ -135,19 +119,16 @@ __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p)
         if (r > 0) __syncthreads();
         char* rec = p.rec + ((int64_t)slot * p.Hv + hv) * (BWD ? GDR_REC : FWD_REC);
         if (w == 0) {
-            float* sc = reinterpret_cast<float*>(rec + (BWD ? GDR_SC : FWD_SC)) + lane;
+            float* sc = reinterpret_cast<float*>(rec + GDR_SC) + lane;
             const GSum G = sG[lane], GL = sG[63];
-            const float eg = gate_exp(G);
-            sc[SC_EG] = eg;
+            sc[SC_EG] = gate_exp(G);
             sc[SC_GA] = gate_ratio(GL, G);
-            sc[SC_BE] = BWD ? sBeta[lane] : sBeta[lane] * sKp[lane];
-            sc[SC_EL] = gate_exp(GL);
-            if (!BWD) {
-                const float ks = sKp[lane] > 0.f ? sKp[lane] : 1.f;
-                sc[SC_EGK] = sBeta[lane] * ks * ks * eg;
-                sc[SC_KS] = sKp[lane];
-                sc[SC_QS] = sQp[lane];
-                sc[SC_KP] = kmax;
+            sc[SC_BE] = sBeta[lane];
+            if (BWD) {
+                sc[SC_EL] = gate_exp(GL);
+            } else {
+                sc[SC_GH] = G.hi;
+                sc[SC_GL] = G.lo;
             }
         }
         {
@@ -158,22 +139,12 @@ __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p)
                 const int j = 16 * tj[x] + jj, i0 = 16 * ti[x] + 4 * g;
                 const GSum Gj = sG[j];
                 const f32x4 be = *reinterpret_cast<const f32x4*>(sBeta + i0);
-                f32x4 by = f32x4{p.scale, p.scale, p.scale, p.scale}, ks = f32x4{1.f, 1.f, 1.f, 1.f};
-                float kinv = 1.f;
-                if (!BWD) {   // exact: powers of two
-                    const f32x4 qp = *reinterpret_cast<const f32x4*>(sQp + i0);
-                    const f32x4 kp = *reinterpret_cast<const f32x4*>(sKp + i0);
-                    kinv = sKp[j] > 0.f ? inverse2(sKp[j]) : 1.f;
-                    by = f32x4{inverse2(qp[0]), inverse2(qp[1]), inverse2(qp[2]), inverse2(qp[3])} * kinv;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) ks[e] = kp[e] > 0.f ? kp[e] : 1.f;
-                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int i = i0 + e;
                     const float gam = j <= i ? gate_ratio(sG[i], Gj) : 0.f;
-                    sA[i * SP + j] = j <= i ? by[e] * (qk[x][e] * gam) : 0.f;
-                    sM[i * SP + j] = j < i ? be[e] * (kk[x][e] * gam * kinv) * ks[e] : 0.f;
+                    if (BWD) sA[i * SP + j] = j <= i ? p.scale * (qk[x][e] * gam) : 0.f;
+                    sM[i * SP + j] = j < i ? be[e] * (kk[x][e] * gam) : 0.f;
                 }
             }
         }
@@ -245,24 +216,23 @@ __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p)
             }
         }
         __syncthreads();
-        // fragments: six of T's and six of A's, three to a wave
+        // fragments: six of T's and, for the backward, six of A's
 #pragma unroll
-        for (int f3 = 0; f3 < 3; ++f3) {
+        for (int f3 = 0; f3 < (BWD ? 3 : 2); ++f3) {
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
             const int f = 4 * f3 + w, which = f >= 6, x = which ? f - 6 : f;
+            if (!BWD && which) continue;
             const int m = x < 2 ? x : 2 + ((x - 2) >> 1), c = x < 2 ? 0 : x & 1;   // (m, kk)
             const float* a = (which ? sA : sM) + (16 * m + jj) * SP + 32 * c + 4 * g;
-            const f32x4 u0 = *reinterpret_cast<const f32x4*>(a), u1 = *reinterpret_cast<const f32x4*>(a + 16);
-            char* dst = rec + (which ? (BWD ? GDR_A : FWD_A) : (BWD ? GDR_T : FWD_T)) + x * GDR_FRAG + (BWD ? frag_piece(ln) : ln * 16);
-            if (BWD) {
-                const Split<3> parts = split_acc<3>(u0, u1);
-#pragma unroll
-                for (int n = 0; n < 3; ++n) *reinterpret_cast<bf16x8*>(dst + n * GDR_TRI) = parts.s[n];
-            } else {
-                const HSplit<2> parts = hsplit<2>(u0, u1);
-                *reinterpret_cast<half8*>(dst) = parts.s[0];
-                if (!which) *reinterpret_cast<half8*>(dst + GDR_TRI) = parts.s[1];
+            f32x4 u0 = *reinterpret_cast<const f32x4*>(a), u1 = *reinterpret_cast<const f32x4*>(a + 16);
+            if (!BWD) {   // T diag(beta)
+                u0 *= *reinterpret_cast<const f32x4*>(sBeta + 32 * c + 4 * g);
+                u1 *= *reinterpret_cast<const f32x4*>(sBeta + 32 * c + 16 + 4 * g);
             }
+            char* dst = rec + (which ? GDR_A : GDR_T) + x * GDR_FRAG + frag_piece(ln);
+            const Split<3> parts = split_acc<3>(u0, u1);
+#pragma unroll
+            for (int n = 0; n < 3; ++n) *reinterpret_cast<bf16x8*>(dst + n * GDR_TRI) = parts.s[n];
         }
         __syncthreads();   // the matrices' reads before the next value head's writes
     }

@@ -452,18 +452,15 @@ kda_status_t kda_bwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda_ten
  * cu_seqlens' precondition and clamping are kda_fwd's; rows of tokens in no
  * sequence are not written.  More than 2^22 (chunk slot, value head) units, 2^31 - 1
  * tokens or 2^21 (sequence, value head) pairs return KDA_ERR_UNSUPPORTED.
- * Precision: every sum is fp32.  The forward's products run on fp16 matrix
- * instructions: states, corrections and T in two parts (22 bits), what only reaches o
- * in one; each key and query row, and each value channel, is scaled by powers of two
- * that follow the sizes met, so that values of any size keep states to about 1e-6 of
- * their largest entries.  An entry below 2^-12 of the largest |S| or |beta v| of its
- * value channel in the chunk is off by up to 2^-27 of that.  The update must not expand
- * the state, beta |k|^2 <= 2 (L2-normalised keys and 0 <= beta <= 2 do not, keys of any
- * sizes beside each other): where (I - beta k k^T) grows it past fp16's range within a
- * chunk, results are infinite or NaN.  The backward's walks take fp32 operands in three bf16 parts, at fp32's accuracy
- * and range; its token gradients take rows of them, brought to one size by powers of two,
- * in two fp16 parts (about 1e-6 relative for dg and dbeta; an entry below 2^-13 of its
- * row's largest is off by up to 2^-36 of that).  o, dq, dk and dv are rounded to bf16 once.  A token that holds NaN or infinity may reach
+ * Precision: every sum is fp32, and operands of matrix products enter at fp32's accuracy
+ * and range, as three bf16 parts (S, T, the corrections, the walks' gradients); what only
+ * adds to o (S in q S, A and the corrections in A u) enters in two, 16 bits for o's eight.
+ * Nothing is scaled, so that values, keys and states may have any sizes beside each other,
+ * and an update may expand the state (beta |k|^2 > 2) until fp32 overflows.  The backward's
+ * token gradients take rows of S, dS, the corrections and their gradients, brought to one
+ * size by powers of two, in two fp16 parts (about 1e-6 relative for dg and dbeta; an entry
+ * below 2^-13 of its row's largest is off by up to 2^-36 of that).  o, dq, dk and dv are
+ * rounded to bf16 once.  A token that holds NaN or infinity may reach
  * every token of its 64-token chunk and later ones of its sequence and head, no other
  * sequence, and through v no other value channel of o and the states.
  */

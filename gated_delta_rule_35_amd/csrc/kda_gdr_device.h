@@ -1,11 +1,11 @@
 // Device helpers of the gated delta rule with one decay per head.
 //
-// Matrix products run on the 16x16x32 instructions for 16-bit operands.  q, k, v and the
-// output's gradient are bf16; an fp32 operand enters as the sum of parts, each the rounding
-// of what the parts before it leave, so that products keep fp32's accuracy at a third to a
-// sixth of the 16-bit rate, several times that of the fp32 matrix instructions.  The walks
-// use bf16 parts, three of which hold all 24 bits at any size; the token gradients use fp16
-// parts, two of which hold 22 bits of what powers of two keep in range.
+// Matrix products run on the 16x16x32 instructions for bf16 operands.  q, k, v and the
+// output's gradient are bf16; an fp32 operand enters as the sum of bf16 parts, each the
+// rounding of what the parts before it leave: three hold all 24 bits at any size, so that
+// products keep fp32's accuracy and range at a third to a sixth of the 16-bit rate, several
+// times that of the fp32 matrix instructions.  (Two fp16 parts hold 22 bits for less, of
+// what powers of two keep in range: entries far below their row's largest lose theirs.)
 #pragma once
 #include "kda_device.h"
 #include "kda_gdr.h"
@@ -57,47 +57,6 @@ __device__ __forceinline__ Split<NS> split_acc(f32x4 a, f32x4 b) {
     return split8<NS>(x);
 }
 
-// ---- fp16 operands ----
-// 1 / x of a power of two within 2^-126 and 2^126.
-__device__ __forceinline__ float inverse2(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
-__device__ __forceinline__ f32x4 mfma_h(half8 a, half8 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-}
-// x - h[0] and y - h[1], one instruction each (exact: what an fp16 rounding leaves fits fp32).
-__device__ __forceinline__ f32x2 minus_half(half2v h, float x, float y) {
-    f32x2 r;
-    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(r[0]) : "v"(h), "v"(x));
-    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r[1]) : "v"(h), "v"(y));
-    return r;
-}
-// Two accumulator tiles as B operand in fp16, and with PARTS = 2 what that leaves.
-template <int PARTS>
-struct HSplit {
-    half8 s[PARTS];
-};
-template <int PARTS>
-__device__ __forceinline__ HSplit<PARTS> hsplit(f32x4 a, f32x4 b) {
-    HSplit<PARTS> r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float x = i < 2 ? a[2 * i] : b[2 * i - 4], y = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
-        const half2v h = __builtin_convertvector(f32x2{x, y}, half2v);
-        r.s[0][2 * i] = h[0];
-        r.s[0][2 * i + 1] = h[1];
-        if (PARTS == 2) {
-            const half2v l = __builtin_convertvector(minus_half(h, x, y), half2v);
-            r.s[1][2 * i] = l[0];
-            r.s[1][2 * i + 1] = l[1];
-        }
-    }
-    return r;
-}
-// max(m, |x|): the instructions themselves, since fmaxf first quiets every operand.
-__device__ __forceinline__ float max_abs(float m, f32x4 x) {
-    asm("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(m) : "v"(x[0]), "v"(x[1]));
-    asm("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(m) : "v"(x[2]), "v"(x[3]));
-    return m;
-}
 // Per-token rows of a record's numbers, in elements: e^G, e^{G_last - G}, beta; backward also
 // e^{G_last}; forward also G as an fp32 value and its remainder.
 enum { SC_EG = 0, SC_GA = 64, SC_BE = 128, SC_EL = 192, SC_GH = 192, SC_GL = 256 };
@@ -337,15 +296,8 @@ __device__ __forceinline__ float sum16(float x) {
     x += ror16<2>(x);
     return x + ror16<1>(x);
 }
-// Largest over the 16 lanes of a group.
-__device__ __forceinline__ float max16(float x) {
-    x = fmaxf(x, ror16<8>(x));
-    x = fmaxf(x, ror16<4>(x));
-    x = fmaxf(x, ror16<2>(x));
-    return fmaxf(x, ror16<1>(x));
-}
-// x of this lane and of the lane 16, or 32, places away (lane ^ N), in either order: for sums
-// and largest values, the same bits in both lanes, without an LDS access.
+// x of this lane and of the lane 16, or 32, places away (lane ^ N), in either order: for sums,
+// the same bits in both lanes, without an LDS access.
 struct Pair {
     float a, b;
 };
@@ -360,11 +312,6 @@ __device__ __forceinline__ Pair across(float x) {
 __device__ __forceinline__ float sum_groups(float x) {
     const Pair p = across<16>(x), q = across<32>(p.a + p.b);
     return q.a + q.b;
-}
-// Largest over the four lane groups.
-__device__ __forceinline__ float max_groups(float x) {
-    const Pair p = across<16>(x), q = across<32>(fmaxf(p.a, p.b));
-    return fmaxf(q.a, q.b);
 }
 // Sum over the wave.
 __device__ __forceinline__ float sum64(float x) { return sum_groups(sum16(x)); }

@@ -19,26 +19,24 @@
 // the group's value heads and sums their dq and dk in registers (so the sum's order is
 // fixed); the next unit's S, u, dx and do are loaded into registers as soon as those of
 // this one's are free, and dS while S's products run.  It holds the chunk's do, u and dx
-// (fp16 parts) and k, q in LDS; wave w owns channels 16 w .. + 15 of R1, R2, R3, dq and
+// (u and dx in three bf16 parts) and k, q in LDS; wave w owns channels 16 w .. + 15 of R1, R2, R3, dq and
 // dk, so S and dS are read once and split once; the ten lower 16x16 tiles of P and of E
 // are dealt to the eight waves.  Every product is formed transposed (channels or the
 // earlier token down, tokens across), so that a lane holds one token and four channels: a
 // dot over channels is four products in the lane and two exchanges, per-token factors are
 // one number, and results leave four at a time.
-//   Precision: each row of S, dS, u, dx and do is brought to [2^10, 2^11) by a power of two
-// and enters in fp16, do in one part (its eight bits are exact down to 2^-24 of the row's
-// largest), the others in two (22 bits down to 2^-13 of it), which dg needs; P and E enter
-// dq and dk, which are rounded to bf16, in two bf16 parts.
+//   Precision: S, dS, u and dx enter in three bf16 parts each, which dg needs and which have
+// fp32's range: value channels and tokens of any sizes beside each other; P and E enter dq and
+// dk, which are rounded to bf16, in two.  (Rows of two fp16 parts, brought to one size by
+// powers of two, took 1080 us and lost every channel far below its
+// row's largest.)
 //   The kernel reads 64 KB each of S and dS and 32 KB each of u and dx per chunk and value
-// head.  At B=2 H=64 T=8192 it takes 1207 us, 4.7 GB at 3.9 TB/s; LDS, vector and matrix
-// units are busy a quarter to a half of the time, with three barriers a unit.
+// head.  At B=2 H=64 T=8192 it takes 1200 us, 4.7 GB at 3.9 TB/s; LDS, vector and matrix
+// units are busy a quarter to a half of the time, with four barriers a unit.
 // What brought it there from 2080 us: results formed transposed, inputs asked for in steps,
 // arguments read anew instead of kept in spilled scalar registers (1600 -> 1440 us), the
 // chains of four tiles side by side (1440 -> 1350 us), inputs asked for as soon as there are
-// registers (-> 1320 us), fp16 parts instead of three of bf16 (-> 1244 us), sums across lane
-// groups by v_permlane swaps instead of through LDS (-> 1207 us).  Asking for all
-// inputs a whole unit ahead and turning the next unit's into fp16 beside the last products
-// took as long, and longer where a head's group is small.
+// registers (-> 1320 us), sums across lane groups by v_permlane swaps instead of through LDS.
 #include <type_traits>
 
 #include "kda_gdr_device.h"
@@ -49,16 +47,14 @@ namespace {
 constexpr int GT = 512;
 constexpr int PS = 144;   // bytes per row of 64 bf16 (+16)
 struct GL {
-    // do in fp16, u and dx in two fp16 parts, the planes of P and E in two bf16 parts
-    static constexpr int K = 0, Q = 16384, DO = 32768, U = 49152, X = U + 2 * 16384, P = X + 2 * 16384;
-    static constexpr int PL = 64 * PS;                  // one part of P or E
-    static constexpr int END = P + 4 * PL;
+    static constexpr int K = 0, Q = 16384, DO = 32768, U = 49152, X = U + 3 * 16384;   // U, X in three parts
+    static constexpr int PL = 64 * PS;                  // one part of P or E, over U
+    static constexpr int END = X + 3 * 16384;
+    static_assert(4 * PL <= 3 * 16384, "overlay");
 };
 struct GShared {
     float hi[64], lo[64];  // G
     float eg[64], ga[64], be[64], xu[64];   // xu: dx . u
-    float iu[64], ix[64], io[64];           // what the tokens' u, dx and do in LDS are to be multiplied by
-    float is[8][16], ids[8][16];            // and the channels of S and dS in the waves' registers
     float z[8][64];        // the row dots of dG by wave (channel sixteenths)
     float row[20][16], col[20][16];   // row and column sums by tile: P (QK^T), then E (KK^T)
     float sd[8], ts[8];    // <S, dS> and sum gam k . R2 by wave
@@ -73,19 +69,17 @@ __device__ __forceinline__ f32x4 chan4(const char* tile, int m, int w, int g, in
     const u32x2 x = *reinterpret_cast<const u32x2*>(tile + tile_off(16 * m + jj, 2 * w + (g >> 1)) + 8 * (g & 1));
     return f32x4{bf_lo(x[0]), bf_hi(x[0]), bf_lo(x[1]), bf_hi(x[1])};
 }
-// The power of two that brings a row's largest magnitude into [2^10, 2^11): two fp16 parts
-// then hold 22 bits down to 2^-13 of it, and what is less to 2^-36 of it.
-__device__ __forceinline__ float raise(float top) {
-    return __uint_as_float((264u - max(__float_as_uint(top) >> 23, 11u)) << 23);
+// c += A B, both in parts, without the products below 2^-24 of the leading one; small ones first.
+template <int NB>
+__device__ __forceinline__ f32x4 mfma_parts(const Split<3>& a, const bf16x8 (&b)[NB], f32x4 c) {
+#pragma unroll
+    for (int d = 2; d >= 0; --d) {
+#pragma unroll
+        for (int i = 0; i <= d; ++i)
+            if (d - i < NB) c = mfma_bf(a.s[i], b[d - i], c);
+    }
+    return c;
 }
-// c += A B with A in two parts and B in one, or in two without the product of the small ones.
-__device__ __forceinline__ f32x4 mfma_21(const HSplit<2>& a, half8 b, f32x4 c) {
-    return mfma_h(a.s[0], b, mfma_h(a.s[1], b, c));
-}
-__device__ __forceinline__ f32x4 mfma_22(const HSplit<2>& a, const half8 (&b)[2], f32x4 c) {
-    return mfma_h(a.s[0], b[0], mfma_h(a.s[1], b[0], mfma_h(a.s[0], b[1], c)));
-}
-__device__ __forceinline__ half8 lds_h8(const char* p) { return *reinterpret_cast<const half8*>(p); }
 __device__ __forceinline__ float dot4(f32x4 a, f32x4 b) { return fmaf(a[0], b[0], fmaf(a[1], b[1], fmaf(a[2], b[2], a[3] * b[3]))); }
 // Operand (m, kk) of a 64x64 plane: rows 16 m + jj, columns of k step kk; and of its transpose.
 __device__ __forceinline__ bf16x8 plane_row(const char* pl, int m, int kk, int g, int jj) {
@@ -127,7 +121,6 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
         }
     };
     f32x4 u[4], x[4], s[8];
-    i32x4 o[2];
     float gate = 0.f, beta = 0.f;
     // the unit's fp32 inputs into registers
     auto fetch_state = [&](const float* from, f32x4 (&to)[8]) {
@@ -145,11 +138,8 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             gate = lane < rows ? p.g[gi] : 0.f;
             beta = lane < rows ? gdr_beta<true>(p.beta, p.beta_f32, gi) : 0.f;
         }
-        const __amdgpu_buffer_rsrc_t ro =
-            chunk_rsrc(p.dO.p + row * p.dO.sb + tok * p.dO.st + (hq * R + r) * p.dO.sh, p.dO.st, rows, DK);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            o[h] = __builtin_amdgcn_raw_buffer_load_b128(ro, (int)((32 * h + (t >> 4)) * p.dO.st * 2) + 16 * (t & 15), 0, 0);
             const int64_t at = unit * CH * DK + (32 * h + (t >> 4)) * DK + 8 * (t & 15);
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
@@ -157,6 +147,11 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
                 x[2 * h + n] = *reinterpret_cast<const f32x4*>(p.dx + at + 4 * n);
             }
         }
+    };
+    auto dma_do = [&]() {
+        Args& p = args_again();
+        dma_tile(chunk_rsrc(p.dO.p + row * p.dO.sb + tok * p.dO.st + (hq * R + r) * p.dO.sh, p.dO.st, rows, DK),
+                 lds + GL::DO, p.dO.st, w, 8, opaque(lane));
     };
     auto dma_kq = [&]() {
         Args& p = args_again();
@@ -169,6 +164,7 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
     find();
     if (item >= items) return;
     fetch_tokens();
+    dma_do();
     dma_kq();
     fetch_state(args_again().S, s);
     f32x4 dq[4], dk[4];
@@ -178,33 +174,21 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
     while (item < items) {
         f32x4 ds[8];   // needed after S's products: in flight until then
         fetch_state(args_again().dS, ds);
-        // u, dx and do, and dx . u
+        // u and dx in three parts, and dx . u
         const int t = opaque(tid);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int pc = t & 15, i = 32 * h + (t >> 4), at = tile_off(i, pc);
-            const float fu = raise(max16(max_abs(max_abs(0.f, u[2 * h]), u[2 * h + 1])));
-            const float fx = raise(max16(max_abs(max_abs(0.f, x[2 * h]), x[2 * h + 1])));
-            const HSplit<2> u2 = hsplit<2>(u[2 * h] * fu, u[2 * h + 1] * fu);
-            const HSplit<2> x2 = hsplit<2>(x[2 * h] * fx, x[2 * h + 1] * fx);
+            const Split<3> u3 = split_acc<3>(u[2 * h], u[2 * h + 1]);
+            const Split<3> x3 = split_acc<3>(x[2 * h], x[2 * h + 1]);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                *reinterpret_cast<half8*>(smem + GL::U + n * 16384 + at) = u2.s[n];
-                *reinterpret_cast<half8*>(smem + GL::X + n * 16384 + at) = x2.s[n];
+            for (int n = 0; n < 3; ++n) {
+                *reinterpret_cast<bf16x8*>(smem + GL::U + n * 16384 + at) = u3.s[n];
+                *reinterpret_cast<bf16x8*>(smem + GL::X + n * 16384 + at) = x3.s[n];
             }
-            const u32x4 ow = __builtin_bit_cast(u32x4, o[h]);
-            const f32x4 o0 = {bf_lo(ow[0]), bf_hi(ow[0]), bf_lo(ow[1]), bf_hi(ow[1])};
-            const f32x4 o1 = {bf_lo(ow[2]), bf_hi(ow[2]), bf_lo(ow[3]), bf_hi(ow[3])};
-            const float fo = raise(max16(max_abs(max_abs(0.f, o0), o1)));
-            *reinterpret_cast<half8*>(smem + GL::DO + at) = hsplit<1>(o0 * fo, o1 * fo).s[0];
             const f32x4 a = x[2 * h] * u[2 * h] + x[2 * h + 1] * u[2 * h + 1];
             const float xu = sum16((a[0] + a[1]) + (a[2] + a[3]));
-            if (pc == 0) {
-                sh.xu[i] = xu;
-                sh.iu[i] = inverse2(fu);
-                sh.ix[i] = inverse2(fx);
-                sh.io[i] = inverse2(fo);
-            }
+            if (pc == 0) sh.xu[i] = xu;
         }
         if (w == 6) {
             const GSum G = gate_sum(gate);
@@ -215,7 +199,7 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             sh.ga[lane] = gate_ratio(last, G);
             sh.be[lane] = beta;
         }
-        asm volatile("s_waitcnt vmcnt(8)" ::: "memory");   // this wave's pieces of k and q; dS may be on its way
+        asm volatile("s_waitcnt vmcnt(8)" ::: "memory");   // this wave's pieces of do, k and q; dS may be on its way
         lds_barrier();
 
         const int rows0 = rows, hq0 = hq;
@@ -224,36 +208,30 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
         // R1, R3, then R2, for channels 16 w + jj
         {
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
-            auto rows_top = [&](const f32x4 (&a)[8]) {   // of the lane's channel
-                float top = 0.f;
-#pragma unroll
-                for (int n = 0; n < 8; ++n) top = max_abs(top, a[n]);
-                return raise(max_groups(top));
-            };
             // k steps outermost: eight (then four) chains of products side by side, one step's parts at a time
             f32x4 r1[4], r3[4];
 #pragma unroll
             for (int m = 0; m < 4; ++m) r1[m] = r3[m] = z4;
-            const float fs = rows_top(s);
-            if (g == 0) sh.is[w][jj] = inverse2(fs);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-                const HSplit<2> sb = hsplit<2>(s[2 * kk] * fs, s[2 * kk + 1] * fs);
+                const Split<3> sb = split_acc<3>(s[2 * kk], s[2 * kk + 1]);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     const int at = tile_off(16 * m + jj, 4 * kk + g);
-                    const half8 fx[2] = {lds_h8(smem + GL::X + at), lds_h8(smem + GL::X + 16384 + at)};
-                    r1[m] = mfma_21(sb, lds_h8(smem + GL::DO + at), r1[m]);
-                    r3[m] = mfma_22(sb, fx, r3[m]);
+                    const bf16x8 fo[1] = {lds_bf8(smem + GL::DO + at)};
+                    bf16x8 fx[3];
+#pragma unroll
+                    for (int n = 0; n < 3; ++n) fx[n] = lds_bf8(smem + GL::X + n * 16384 + at);
+                    r1[m] = mfma_parts(sb, fo, r1[m]);
+                    r3[m] = mfma_parts(sb, fx, r3[m]);
                 }
             }
-            const f32x4 is = *reinterpret_cast<const f32x4*>(&sh.is[w][4 * g]);
             float z[4];   // the lane's part of its tokens' row dots
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 const float eg = sh.eg[16 * m + jj];
-                r1[m] = r1[m] * is * (p.scale * eg * sh.io[16 * m + jj]);
-                r3[m] = r3[m] * is * (sh.be[16 * m + jj] * eg * sh.ix[16 * m + jj]);
+                r1[m] *= p.scale * eg;
+                r3[m] *= sh.be[16 * m + jj] * eg;
                 dq[m] += r1[m];
                 dk[m] -= r3[m];
                 z[m] = dot4(chan4(smem + GL::Q, m, w, g, jj), r1[m]) - dot4(chan4(smem + GL::K, m, w, g, jj), r3[m]);
@@ -280,23 +258,22 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             f32x4 r2[4];
 #pragma unroll
             for (int m = 0; m < 4; ++m) r2[m] = z4;
-            const float fd = rows_top(ds);
-            if (g == 0) sh.ids[w][jj] = inverse2(fd);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-                const HSplit<2> sb = hsplit<2>(ds[2 * kk] * fd, ds[2 * kk + 1] * fd);
+                const Split<3> sb = split_acc<3>(ds[2 * kk], ds[2 * kk + 1]);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     const int at = tile_off(16 * m + jj, 4 * kk + g);
-                    const half8 fu[2] = {lds_h8(smem + GL::U + at), lds_h8(smem + GL::U + 16384 + at)};
-                    r2[m] = mfma_22(sb, fu, r2[m]);
+                    bf16x8 fu[3];
+#pragma unroll
+                    for (int n = 0; n < 3; ++n) fu[n] = lds_bf8(smem + GL::U + n * 16384 + at);
+                    r2[m] = mfma_parts(sb, fu, r2[m]);
                 }
             }
-            const f32x4 ids = *reinterpret_cast<const f32x4*>(&sh.ids[w][4 * g]);
             float ts = 0.f;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                r2[m] = r2[m] * ids * (sh.ga[16 * m + jj] * sh.iu[16 * m + jj]);
+                r2[m] *= sh.ga[16 * m + jj];
                 dk[m] += r2[m];
                 const float t = dot4(chan4(smem + GL::K, m, w, g, jj), r2[m]);
                 ts += t;
@@ -326,27 +303,29 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             for (int kk = 0; kk < 4; ++kk) {
                 if (kk == 2) asm volatile("" ::: "memory");   // two steps' operands at a time: more would spill
                 const int ai = tile_off(16 * I + jj, 4 * kk + g), aj = tile_off(16 * J + jj, 4 * kk + g);
-                const HSplit<2> ua = {{lds_h8(smem + GL::U + aj), lds_h8(smem + GL::U + 16384 + aj)}};
+                const Split<3> ua = {{lds_bf8(smem + GL::U + aj), lds_bf8(smem + GL::U + 16384 + aj),
+                                      lds_bf8(smem + GL::U + 32768 + aj)}};
                 const bf16x8 kj = lds_bf8(smem + GL::K + aj);
                 if (OF_P) {
-                    a = mfma_21(ua, lds_h8(smem + GL::DO + ai), a);
+                    const bf16x8 fo[1] = {lds_bf8(smem + GL::DO + ai)};
+                    a = mfma_parts(ua, fo, a);
                     ra = mfma_bf(kj, lds_bf8(smem + GL::Q + ai), ra);
                 }
                 if (OF_E) {
-                    const half8 fx[2] = {lds_h8(smem + GL::X + ai), lds_h8(smem + GL::X + 16384 + ai)};
-                    b = mfma_22(ua, fx, b);
+                    const bf16x8 fx[3] = {lds_bf8(smem + GL::X + ai), lds_bf8(smem + GL::X + 16384 + ai),
+                                          lds_bf8(smem + GL::X + 32768 + ai)};
+                    b = mfma_parts(ua, fx, b);
                     rb = mfma_bf(kj, lds_bf8(smem + GL::K + ai), rb);
                 }
             }
             const GSum Gi = {sh.hi[i], sh.lo[i]};
             const f32x4 hj = *reinterpret_cast<const f32x4*>(sh.hi + j0), lj = *reinterpret_cast<const f32x4*>(sh.lo + j0);
-            const f32x4 iu = *reinterpret_cast<const f32x4*>(sh.iu + j0);
             f32x4 gam;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) gam[e] = j0 + e <= i ? gate_ratio(Gi, GSum{hj[e], lj[e]}) * iu[e] : 0.f;
+            for (int e = 0; e < 4; ++e) gam[e] = j0 + e <= i ? gate_ratio(Gi, GSum{hj[e], lj[e]}) : 0.f;
             auto finish = [&](auto is_p, const f32x4& a, const f32x4& raw) -> f32x4 {
                 constexpr bool IS_P = decltype(is_p)::value;
-                const float by = IS_P ? p.scale * sh.io[i] : -sh.be[i] * sh.ix[i];
+                const float by = IS_P ? p.scale : -sh.be[i];
                 f32x4 v, cs;
                 float rs = 0.f;
 #pragma unroll
@@ -369,13 +348,14 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
         tile(std::true_type{}, std::true_type{}, w, P, E);
         if (w < 2) tile(std::true_type{}, std::false_type{}, 8 + w, Z, Z);
         else if (w < 4) tile(std::false_type{}, std::true_type{}, 6 + w, Z, Z);
+        lds_barrier();   // u's parts read; the sums complete
         // P and E as row-major planes of two bf16 parts
         {
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
             auto put = [&](f32x4 v, int id, int part) {
                 int I, J;
                 tile_rc(id, I, J);
-                char* to = smem + GL::P + part * GL::PL + (16 * I + jj) * PS + 2 * (16 * J + 4 * g);
+                char* to = smem + GL::U + part * GL::PL + (16 * I + jj) * PS + 2 * (16 * J + 4 * g);
                 const uint32_t h0 = pack_bf2(v[0], v[1]), h1 = pack_bf2(v[2], v[3]);
                 *reinterpret_cast<u32x2*>(to) = u32x2{h0, h1};
                 *reinterpret_cast<u32x2*>(to + GL::PL) =
@@ -387,10 +367,9 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             else if (w < 4) put(Z, 6 + w, 2);
             // the tiles above the diagonal that operands cover: 8 bytes a thread
             const int e = opaque(tid), t = (e >> 6) & 1;
-            *reinterpret_cast<u32x2*>(smem + GL::P + (e >> 7) * GL::PL + (32 * t + ((e >> 2) & 15)) * PS +
+            *reinterpret_cast<u32x2*>(smem + GL::U + (e >> 7) * GL::PL + (32 * t + ((e >> 2) & 15)) * PS +
                                       2 * (32 * t + 16 + 4 * (e & 3))) = u32x2{0, 0};
         }
-        lds_barrier();   // the planes and the sums are complete
         if (w == 5 && lane < rows0) args_again().dbeta[gi0 + (int64_t)lane * args_again().Hv] = sh.xu[lane] / sh.be[lane];
         if (w == 7) {   // dg
             const int i = lane, I = i >> 4;
@@ -416,6 +395,8 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
                 p.dg[gi] = (float)(rest + last);
             }
         }
+        if (item < items) dma_do();
+        lds_barrier();
         {
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
             bf16x8 kb[2], qb[2];
@@ -426,8 +407,8 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             }
 #pragma unroll
             for (int n = 1; n >= 0; --n) {
-                const char* pp = smem + GL::P + n * GL::PL;
-                const char* pe = smem + GL::P + (2 + n) * GL::PL;
+                const char* pp = smem + GL::U + n * GL::PL;
+                const char* pe = smem + GL::U + (2 + n) * GL::PL;
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {   // four tiles of dq and of dk side by side
 #pragma unroll

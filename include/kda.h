@@ -456,10 +456,8 @@ kda_status_t kda_bwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda_ten
  * and range, as three bf16 parts (S, T, the corrections, the walks' gradients); what only
  * adds to o (S in q S, A and the corrections in A u) enters in two, 16 bits for o's eight.
  * Nothing is scaled, so that values, keys and states may have any sizes beside each other,
- * and an update may expand the state (beta |k|^2 > 2) until fp32 overflows.  The backward's
- * token gradients take rows of S, dS, the corrections and their gradients, brought to one
- * size by powers of two, in two fp16 parts (about 1e-6 relative for dg and dbeta; an entry
- * below 2^-13 of its row's largest is off by up to 2^-36 of that).  o, dq, dk and dv are
+ * and an update may expand the state (beta |k|^2 > 2) until fp32 overflows; in the backward
+ * P and E, which only reach the bf16 dq and dk, enter in two.  o, dq, dk and dv are
  * rounded to bf16 once.  A token that holds NaN or infinity may reach
  * every token of its 64-token chunk and later ones of its sequence and head, no other
  * sequence, and through v no other value channel of o and the states.

@@ -8,12 +8,13 @@
 //   dq = scale e^G R1 + P K
 //   dk = gam R2 - beta e^G R3 + P^T Q + (E + E^T) K
 //   dbeta_i = dx_i . u_i / beta_i           (u = beta times what it multiplies)
-//   dG_i = scale e^{G_i} q_i . R1_i - beta_i e^{G_i} k_i . R3_i - gam_i k_i . R2_i
-//          + (row i - column i of P (QK^T) + E (KK^T) below the diagonal)
-//   dG_last += sum_i gam_i k_i . R2_i + e^{G_last} <S, dS>
-//   dg_t = sum_{i >= t} dG_i within the chunk
-// (dG sums to do . o - dv . v per token, but every term above carries the decay it
-// passes through, so that dg keeps its accuracy where the state is soon forgotten.)
+//   z_i = scale e^{G_i} q_i . R1_i - beta_i e^{G_i} k_i . R3_i
+//         + (row i - column i of P (QK^T) + E (KK^T) below the diagonal)
+//   dg_t = sum_{i >= t} z_i + sum_{i < t} gam_i k_i . R2_i + e^{G_last} <S, dS>, within the chunk
+// (z_i - gam_i k_i . R2_i sums to do . o - dv . v per token, but every term above carries the
+// decays that it passes, g_t's among them, but for the pairs behind t, whose rows and columns
+// cancel: dg keeps its accuracy where the state is soon forgotten.  Summed as all tokens' k . R2
+// less those from t on, what leaves the chunk without passing a decay left 2^-24 of itself.)
 //
 // One 512-thread work-group per compute unit takes items (chunk slot, q/k head), walks
 // the group's value heads and sums their dq and dk in registers (so the sum's order is
@@ -55,9 +56,9 @@ struct GL {
 struct GShared {
     float hi[64], lo[64];  // G
     float eg[64], ga[64], be[64], xu[64];   // xu: dx . u
-    float z[8][64];        // the row dots of dG by wave (channel sixteenths)
+    float z[8][64], k2[8][64];   // the row dots of z and k . R2 by wave (channel sixteenths)
     float row[20][16], col[20][16];   // row and column sums by tile: P (QK^T), then E (KK^T)
-    float sd[8], ts[8];    // <S, dS> and sum gam k . R2 by wave
+    float sd[8];           // <S, dS> by wave
 };
 
 // Operand of channels 16 w + jj: tokens 16 m + 4 g + r, r < 4.
@@ -270,18 +271,16 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
                     r2[m] = mfma_parts(sb, fu, r2[m]);
                 }
             }
-            float ts = 0.f;
+            float k2[4];
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 r2[m] *= sh.ga[16 * m + jj];
                 dk[m] += r2[m];
-                const float t = dot4(chan4(smem + GL::K, m, w, g, jj), r2[m]);
-                ts += t;
-                z[m] = sum_groups(z[m] - t);
+                k2[m] = sum_groups(dot4(chan4(smem + GL::K, m, w, g, jj), r2[m]));
+                z[m] = sum_groups(z[m]);
             }
             sh.z[w][lane] = g == 0 ? z[0] : g == 1 ? z[1] : g == 2 ? z[2] : z[3];   // group m writes tokens 16 m ..
-            ts = sum64(ts);
-            if (lane == 0) sh.ts[w] = ts;
+            sh.k2[w][lane] = g == 0 ? k2[0] : g == 1 ? k2[1] : g == 2 ? k2[2] : k2[3];
         }
         if (item < items) fetch_tokens();   // and u and dx now
         // lower tiles of P and E, transposed (lane: token i = 16 I + jj, j = 16 J + 4 g + e): wave w
@@ -374,25 +373,25 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
         if (w == 7) {   // dg
             const int i = lane, I = i >> 4;
             const int64_t gi = gi0 + (int64_t)i * p.Hv;
-            double dG = 0.0, last = 0.0;
+            double z = 0.0, k2 = 0.0;
             float sd = 0.f;
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
-                dG += (double)sh.z[n][i];
-                last += (double)sh.ts[n];
+                z += (double)sh.z[n][i];
+                k2 += (double)sh.k2[n][i];
                 sd += sh.sd[n];
             }
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 const int ra = I * (I + 1) / 2 + n, ca = n * (n + 1) / 2 + I;
-                if (n <= I) dG += (double)sh.row[ra][i & 15] + (double)sh.row[10 + ra][i & 15];
-                if (n >= I) dG -= (double)sh.col[ca][i & 15] + (double)sh.col[10 + ca][i & 15];
+                if (n <= I) z += (double)sh.row[ra][i & 15] + (double)sh.row[10 + ra][i & 15];
+                if (n >= I) z -= (double)sh.col[ca][i & 15] + (double)sh.col[10 + ca][i & 15];
             }
-            last += (double)(sh.eg[63] * sd);
-            const double sum = prefix64(dG), rest = lane_f64(sum, 63) - sum + dG;
+            const double sum = prefix64(z), rest = lane_f64(sum, 63) - sum + z;
+            const double upto = prefix64(k2), before = __shfl_up(upto, 1);
             if (i < rows0) {
                 Args& p = args_again();
-                p.dg[gi] = (float)(rest + last);
+                p.dg[gi] = (float)(rest + (i > 0 ? before : 0.0) + (double)(sh.eg[63] * sd));
             }
         }
         if (item < items) dma_do();

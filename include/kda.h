@@ -453,7 +453,7 @@ kda_status_t kda_bwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda_ten
  * sequence are not written.  More than 2^22 (chunk slot, value head) units, 2^31 - 1
  * tokens or 2^21 (sequence, value head) pairs return KDA_ERR_UNSUPPORTED.
  * Precision: every sum is fp32, and operands of matrix products enter at fp32's accuracy
- * and range, as three bf16 parts (S, T, the corrections, the walks' gradients); what only
+ * and range, as three bf16 parts (states, T, corrections, their gradients); what only
  * adds to o (S in q S, A and the corrections in A u) enters in two, 16 bits for o's eight.
  * Nothing is scaled, so that values, keys and states may have any sizes beside each other,
  * and an update may expand the state (beta |k|^2 > 2) until fp32 overflows; in the backward

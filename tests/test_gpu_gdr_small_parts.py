@@ -122,6 +122,15 @@ def test_reference_against_autograd():
         assert ref.rel(got[n], want[m]) <= 1e-12 and (most[n] >= got[n].abs() * (1 - 1e-9)).all()
 
 
+def test_heads_of_very_different_decay():
+    """Heads that keep everything beside heads that forget within a token: each decay a head's own."""
+    say("gdr_bwd, log-decays of 1e-4 to 50 by head")
+    x = ref.make(1, 200, 2, 8, h0=True, seed=3)
+    rate = torch.tensor([1e-4, 50.0, 0.1, 5.0, 1.0, 20.0, 1e-2, 0.5])
+    x["g"] = -rate * (0.5 + torch.rand(1, 200, 8, generator=torch.Generator().manual_seed(4)))
+    check(x, dhT=0.1 * torch.randn(1, 8, 128, 128, generator=torch.Generator().manual_seed(5)))
+
+
 @pytest.mark.parametrize("span", [10, 30])
 def test_heads_of_very_different_sizes(span):
     say(f"gdr_bwd, values and output gradients of 2^-{span} to 2^{span} by head")

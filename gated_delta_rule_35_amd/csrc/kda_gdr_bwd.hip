@@ -196,12 +196,12 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_keep_kernel(const GdrPar
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const f32x4 eg = *reinterpret_cast<const f32x4*>(sc + SC_EG + 16 * m + 4 * g);
-            const f32x4 be = *reinterpret_cast<const f32x4*>(sc + SC_BE + 16 * m + 4 * g);
+            const f32x4 be = *reinterpret_cast<const f32x4*>(sc + SC_BU + 16 * m + 4 * g);
             const f32x4 v = widen(slice_frag(buf + L::V, m, w, g, jj));
             x[m] = be * (v - eg * x[m]);
         }
         // u = T x
-        const float el = sc[SC_EL];
+        const float el = sc[SC_EG + 63];
         f32x4 u[4];
         tri_times<false>(
             [&](int n3, int m, int kk) {
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(SCAN_THREADS) kda_gdr_rscan_kernel(const GdrPa
             eg[m] = *reinterpret_cast<const f32x4*>(sc + SC_EG + 16 * m + 4 * g);
             be[m] = *reinterpret_cast<const f32x4*>(sc + SC_BE + 16 * m + 4 * g);
         }
-        const float el = sc[SC_EL];
+        const float el = sc[SC_EG + 63];
         {
             const bf16x8 db[2] = {join(d[0], d[1]), join(d[2], d[3])};
             bf16x8 f[2][6];

@@ -57,9 +57,10 @@ __device__ __forceinline__ Split<NS> split_acc(f32x4 a, f32x4 b) {
     return split8<NS>(x);
 }
 
-// Per-token rows of a record's numbers, in elements: e^G, e^{G_last - G}, beta; backward also
-// e^{G_last}; forward also G as an fp32 value and its remainder.
-enum { SC_EG = 0, SC_GA = 64, SC_BE = 128, SC_EL = 192, SC_GH = 192, SC_GL = 256 };
+// Per-token rows of a record's numbers, in elements: e^G (the last is e^{G_last}), e^{G_last - G},
+// beta; backward also the beta that u is formed with; forward also G as an fp32 value and its
+// remainder.
+enum { SC_EG = 0, SC_GA = 64, SC_BE = 128, SC_BU = 192, SC_GH = 192, SC_GL = 256 };
 
 // ---- swizzled [64][128] bf16 tiles in LDS: rows of 256 bytes, whose sixteen 16-byte
 // pieces are permuted by tsw(row), so that both an operand read (sixteen consecutive
@@ -231,14 +232,15 @@ __device__ __forceinline__ int gdr_chunk(const GdrParams& p, int64_t s, int64_t&
     return c < 0 || r <= 0 ? 0 : (r >= CH ? CH : (int)r);
 }
 
-// beta of element i.  The backward (BWD) takes no beta nearer to zero than 2^-40: its
-// dbeta is u's product with a gradient divided by beta, and an update of 2^-40 is far
-// below what the state's 24 bits hold.
-template <bool BWD>
+// beta of element i.
 __device__ __forceinline__ float gdr_beta(const void* beta, int f32, int64_t i) {
-    const float b = f32 ? reinterpret_cast<const float*>(beta)[i] : bf2f(reinterpret_cast<const uint16_t*>(beta)[i]);
-    return BWD && fabsf(b) < 0x1p-40f ? 0x1p-40f : b;
+    return f32 ? reinterpret_cast<const float*>(beta)[i] : bf2f(reinterpret_cast<const uint16_t*>(beta)[i]);
 }
+// The beta that the backward forms u with: none nearer to zero than 2^-40.  dbeta is u's product
+// with a gradient divided by it, and an update of 2^-40 is far below what the state's 24 bits
+// hold.  The other gradients take u times beta_share: beta over the one it is formed with.
+__device__ __forceinline__ float beta_of_u(float b) { return fabsf(b) < 0x1p-40f ? 0x1p-40f : b; }
+__device__ __forceinline__ float beta_share(float b) { return fabsf(b) < 0x1p-40f ? b * 0x1p40f : 1.f; }
 
 // x of the lane that a DPP control names, 0 where it names none (or the row is masked out).
 template <int CTRL, int ROWS>

@@ -55,7 +55,8 @@ struct GL {
 };
 struct GShared {
     float hi[64], lo[64];  // G
-    float eg[64], ga[64], be[64], xu[64];   // xu: dx . u
+    float eg[64], ga[64], be[64], xu[64];   // ga times beta's share of u; xu: dx . u
+    float su[64];          // beta's share of u
     float z[8][64], k2[8][64];   // the row dots of z and k . R2 by wave (channel sixteenths)
     float row[20][16], col[20][16];   // row and column sums by tile: P (QK^T), then E (KK^T)
     float sd[8];           // <S, dS> by wave
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
         if (w == 6) {
             const int64_t gi = (row * p.T + tok + lane) * p.Hv + hq * R + r;
             gate = lane < rows ? p.g[gi] : 0.f;
-            beta = lane < rows ? gdr_beta<true>(p.beta, p.beta_f32, gi) : 0.f;
+            beta = lane < rows ? gdr_beta(p.beta, p.beta_f32, gi) : 0.f;
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -197,7 +198,8 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             sh.hi[lane] = G.hi;
             sh.lo[lane] = G.lo;
             sh.eg[lane] = gate_exp(G);
-            sh.ga[lane] = gate_ratio(last, G);
+            sh.su[lane] = beta_share(beta);
+            sh.ga[lane] = gate_ratio(last, G) * beta_share(beta);
             sh.be[lane] = beta;
         }
         asm volatile("s_waitcnt vmcnt(8)" ::: "memory");   // this wave's pieces of do, k and q; dS may be on its way
@@ -319,9 +321,10 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             }
             const GSum Gi = {sh.hi[i], sh.lo[i]};
             const f32x4 hj = *reinterpret_cast<const f32x4*>(sh.hi + j0), lj = *reinterpret_cast<const f32x4*>(sh.lo + j0);
+            const f32x4 su = *reinterpret_cast<const f32x4*>(sh.su + j0);
             f32x4 gam;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) gam[e] = j0 + e <= i ? gate_ratio(Gi, GSum{hj[e], lj[e]}) : 0.f;
+            for (int e = 0; e < 4; ++e) gam[e] = j0 + e <= i ? gate_ratio(Gi, GSum{hj[e], lj[e]}) * su[e] : 0.f;
             auto finish = [&](auto is_p, const f32x4& a, const f32x4& raw) -> f32x4 {
                 constexpr bool IS_P = decltype(is_p)::value;
                 const float by = IS_P ? p.scale : -sh.be[i];
@@ -369,7 +372,7 @@ __global__ void __launch_bounds__(GT) kda_gdr_grads_kernel(const GdrParams p, co
             *reinterpret_cast<u32x2*>(smem + GL::U + (e >> 7) * GL::PL + (32 * t + ((e >> 2) & 15)) * PS +
                                       2 * (32 * t + 16 + 4 * (e & 3))) = u32x2{0, 0};
         }
-        if (w == 5 && lane < rows0) args_again().dbeta[gi0 + (int64_t)lane * args_again().Hv] = sh.xu[lane] / sh.be[lane];
+        if (w == 5 && lane < rows0) args_again().dbeta[gi0 + (int64_t)lane * args_again().Hv] = sh.xu[lane] / beta_of_u(sh.be[lane]);
         if (w == 7) {   // dg
             const int i = lane, I = i >> 4;
             const int64_t gi = gi0 + (int64_t)i * p.Hv;

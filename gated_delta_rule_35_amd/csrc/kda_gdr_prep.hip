@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p)
     float gate = 0.f, beta = 0.f;
     if (w == 0 && lane < rows) {
         gate = p.g[gi];
-        beta = gdr_beta<BWD>(p.beta, p.beta_f32, gi);
+        beta = gdr_beta(p.beta, p.beta_f32, gi);
     }
 
     {
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p)
                      w, 4, lane);
         if (w == 0) {
             sG[lane] = gate_sum(gate);
-            sBeta[lane] = beta;
+            sBeta[lane] = BWD ? beta_of_u(beta) : beta;
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
@@ -106,14 +106,16 @@ __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p)
 
     for (int r = 0; r < R; ++r) {
         const int hv = hq * R + r;
+        float own = 0.f;   // this value head's beta (wave 0)
         if (w == 0) {
             if (r > 0) {
                 sG[lane] = gate_sum(gate);
-                sBeta[lane] = beta;
+                sBeta[lane] = BWD ? beta_of_u(beta) : beta;
             }
+            own = beta;
             if (r + 1 < R && lane < rows) {
                 gate = p.g[gi + r + 1];
-                beta = gdr_beta<BWD>(p.beta, p.beta_f32, gi + r + 1);
+                beta = gdr_beta(p.beta, p.beta_f32, gi + r + 1);
             }
         }
         if (r > 0) __syncthreads();
@@ -123,9 +125,9 @@ __global__ void __launch_bounds__(256, 4) kda_gdr_prep_kernel(const GdrParams p)
             const GSum G = sG[lane], GL = sG[63];
             sc[SC_EG] = gate_exp(G);
             sc[SC_GA] = gate_ratio(GL, G);
-            sc[SC_BE] = sBeta[lane];
+            sc[SC_BE] = own;
             if (BWD) {
-                sc[SC_EL] = gate_exp(GL);
+                sc[SC_BU] = sBeta[lane];
             } else {
                 sc[SC_GH] = G.hi;
                 sc[SC_GL] = G.lo;

@@ -487,9 +487,9 @@ kda_status_t kda_gdr_fwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda
  *   dv       [B, T, Hv, 128] bf16
  *   dg, dbeta [B, T, Hv]     fp32
  *   d_initial_state [N, Hv, 128, 128] fp32, or NULL (not computed)
- * An empty sequence passes d_final_state through to its d_initial_state.  A |beta| below
- * 2^-40 counts as 2^-40: dbeta_t is formed as u_t . dx_t / beta_t, u_t = beta_t times
- * what it multiplies.
+ * An empty sequence passes d_final_state through to its d_initial_state.  dbeta_t is formed
+ * as u_t . dx_t / beta_t, u_t = beta_t times what it multiplies, for which a |beta| below
+ * 2^-40 counts as 2^-40; dk and dv of a token with beta 0 are 0.
  * workspace: as for kda_gdr_fwd, of kda_gdr_bwd_workspace_size(B * T, N, Hv) bytes,
  * 256-byte aligned.  Per (chunk slot, value head): 37,888 bytes of operands, the
  * states entering and the state gradients leaving (64 KB each), and two fp32 token

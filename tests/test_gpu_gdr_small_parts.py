@@ -202,3 +202,13 @@ def test_updates_up_to_two(hi):
     x["k"] = (k / k.norm(dim=-1, keepdim=True) * (1 - 2.0 ** -7)).bfloat16()
     x["beta"] = hi * (0.5 + 0.5 * torch.rand(1, 150, 4, generator=gen))
     check(x)
+
+
+def test_tokens_without_an_update():
+    """beta of zero, of 2^-60 and of -2^-60: dv is exactly beta times what it multiplies, zero for a
+    padded token, and nothing else sees an update that is not there."""
+    say("gdr_bwd, beta of zero and near it")
+    x = ref.make(1, 130, 1, 2, h0=True, seed=12)
+    x["beta"][0, 20:70] = 0
+    x["beta"][0, 100:110, 0], x["beta"][0, 100:110, 1] = 2.0 ** -60, -(2.0 ** -60)
+    check(x)

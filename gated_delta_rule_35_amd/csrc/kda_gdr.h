@@ -44,7 +44,8 @@ constexpr int GDR_FRAG = 1024;
 // a group four apart from the group's before, else such a read meets each bank four times.
 __host__ __device__ constexpr int frag_piece(int l) { return 16 * (l ^ ((l >> 4) << 2)); }
 constexpr int GDR_TRI = 6 * GDR_FRAG;              // one part of a triangular operand
-// T in three bf16 parts and the per-token rows; the backward also A (scale included) in three parts.
+// T in three bf16 parts (the forward's with its columns times beta) and the per-token rows; the
+// backward also A (scale included) in three parts.
 constexpr int GDR_T = 0, GDR_SC = 3 * GDR_TRI, FWD_REC = GDR_SC + 2048;
 constexpr int GDR_A = GDR_SC + 1024, GDR_REC = GDR_A + 3 * GDR_TRI;
 

@@ -19,9 +19,9 @@
 // eight channels as they lie in K's rows.
 //   fp32 operands go in as three bf16 parts, see kda_gdr_device.h.
 //
-// At B=2 H=64 T=8192 both walks are bound by HBM: forwards 495 us, 2.45 GB at 4.9 TB/s, of
-// which 1.6 GB are S and u; reverse 685 us, 3.3 GB at 4.8 TB/s.  With few sequences and heads
-// they are bound by the chain of a chunk: at T=1000 on 8 heads 45 and 62 us, 2.8 and 3.9 us
+// At B=2 H=64 T=8192 both walks are bound by HBM: forwards 487 us, 2.47 GB at 5.1 TB/s, of
+// which 1.6 GB are S and u; reverse 675 us, 3.3 GB at 4.9 TB/s.  With few sequences and heads
+// they are bound by the chain of a chunk: at T=1000 on 8 heads 44 and 61 us, 2.8 and 3.8 us
 // a chunk.  There the order of the matrix instructions counts: four to six tiles side by
 // side with the next operands read and split meanwhile took the reverse walk from 70 to 62
 // us; T and A placed so that their transposed reads meet each bank twice instead of four

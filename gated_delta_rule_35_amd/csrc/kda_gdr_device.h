@@ -324,9 +324,9 @@ __device__ __forceinline__ float sum64(float x) { return sum_groups(sum16(x)); }
 // together, so that they share k, q and the records in one L2.  Packed sequences are
 // taken longest first (ties in order), so that the last work-groups to start are short:
 // `sh` holds N + 1 words for that.  With more sequences than threads they keep their order.
-//   Forward of 11 sequences of 16,384 tokens on 64 heads, 16 of q and k: longest first 632 us,
-// in order 1583; its gradients on 7 of 4096 tokens and 32 heads 572 and 677.  Heads dealt to
-// the XCDs: forward at B=2 H=64 T=8192 680 us, in order 696.
+//   Forward of 11 sequences of 16,384 tokens on 64 heads, 16 of q and k: longest first 594 us,
+// in order 690; its gradients on 7 of 4096 tokens and 32 heads 371 and 405.  Heads dealt to
+// the XCDs: the same forward 594 us, in order 614; at B=2 H=64 T=8192 608 and 618.
 struct Walk {
     int n, hv, sl;
 };

@@ -1,6 +1,6 @@
 // The forward's walk over the chunks of the gated delta rule with one decay per head, on
-// gfx950 (MI355X).  With the prep kernel's T and per-token numbers:
-//   x = beta (v - e^G K S),  u = T x,  o = scale (e^G Q S + A u),  A = e^{G_i - G_j} Q K^T, j <= i
+// gfx950 (MI355X).  With the prep kernel's T (its columns times beta) and per-token numbers:
+//   x = v - e^G K S,  u = T x,  o = scale (e^G Q S + A u),  A = e^{G_i - G_j} Q K^T, j <= i
 //   S <- e^{G_last} S + K^T (e^{G_last - G} u)
 //
 // Every product's right-hand side is a set of columns of S (value channels), and no
@@ -23,12 +23,12 @@
 // two for each row, chunk and value channel, windows in which small entries lose bits, and
 // waves that turn k and q: with A in two parts those were busy 7,500 of a chunk's 8,460 clocks.
 //
-// At B=2 H=64 T=8192 the walk takes 470 us (a warm kernel trace's median), 1.4 GB at 3.0 TB/s:
-// 7,300 clocks a chunk at 2.0 GHz.  It is bound by what one wave a SIMD can issue: 984
-// instructions a chunk, 182 of them matrix (9.7 clocks each with vector ones between), 563
-// vector (4.4 each, whether they depend on each other or not), 110 LDS reads; 400 of the vector
-// ones split S, x and u.  With 64 work-groups on the chip, no DMA, no A or neither, a chunk
-// takes as long to within 5%.
+// At B=2 H=64 T=8192 the walk takes 490 us (a warm kernel trace's median), 1.43 GB at 2.9 TB/s:
+// 7,400 clocks a chunk at 1.95 GHz, matrix units busy 41%, LDS 50%.  It is bound by what one
+// wave a SIMD can issue: 984 instructions a chunk, 182 of them matrix (9.7 clocks each with
+// vector ones between), 563 vector (4.4 each, whether they depend on each other or not), 110
+// LDS reads; 400 of the vector ones split S, x and u.  With 64 work-groups on the chip, no
+// DMA, no A or neither, a chunk takes as long to within 5%.
 #include "kda_gdr_device.h"
 
 namespace kda {

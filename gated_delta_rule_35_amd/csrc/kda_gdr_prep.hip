@@ -19,8 +19,8 @@
 // with its columns times beta.  The forward's walk forms A itself, from the k and q that it
 // holds anyway, so that q is not read here and records stay at 20 KB.
 //
-// At B=2 H=64 T=8192 (16,384 chunks of a head): forward 135 us, 0.6 GB at 4.4 TB/s; with the
-// backward's records 207 us, 1.22 GB at 5.9 TB/s (part of what it writes stays in the
+// At B=2 H=64 T=8192 (16,384 chunks of a head): forward 140 us, 0.66 GB at 4.7 TB/s; with the
+// backward's records 203 us, 1.22 GB at 6.0 TB/s (part of what it writes stays in the
 // last-level cache).  What brought the latter there: four work-groups a compute unit, k
 // and q by DMA, and the tiles dealt evenly; a form that kept M and A beside k and q in LDS
 // (two work-groups a unit) took 292 us of the forward's 200 then.  Forming T inside the walk

@@ -1,4 +1,4 @@
-"""MI355X-native Kimi Delta Attention (KDA): chunked forward, decode step and backward.
+"""MI355X-native Kimi Delta Attention (KDA): chunked forward, decode step and backward, and what stands around it in a block.
 
 The compute lives in libkda.so (hand-written HIP for gfx950, C ABI in
 include/kda.h).  This package is a thin ctypes binding: it turns torch tensors
@@ -12,6 +12,8 @@ from .binding import (KdaError, kda_bwd, kda_bwd_workspace_size, kda_decode, kda
                       kda_fwd_noalloc_max_bytes, kda_fwd_qg, kda_fwd_scan, kda_fwd_trace, kda_fwd_workspace_size, kda_fwd_ws,
                       kda_gdr_bwd, kda_gdr_bwd_workspace_size, kda_gdr_decode, kda_gdr_fwd, kda_gdr_fwd_workspace_size,
                       kda_qk_norm, kda_qk_norm_bwd, kda_qk_norm_bwd_workspace_size,
+                      kda_add_norm, kda_add_norm_bwd, kda_conv, kda_conv_bwd, kda_conv_bwd_workspace_size, kda_conv_decode,
+                      kda_gated_norm, kda_gated_norm_bwd, kda_norm_bwd_workspace_size,
                       library_path, load_library)
 
 __all__ = ["KdaError", "kda_bwd", "kda_bwd_workspace_size", "kda_decode", "kda_dv_slices", "kda_fwd", "kda_fwd_cp", "kda_fwd_cp_plan", "kda_fwd_fused",
@@ -19,4 +21,6 @@ __all__ = ["KdaError", "kda_bwd", "kda_bwd_workspace_size", "kda_decode", "kda_d
            "kda_fwd_ws", "kda_fwd_trace", "kda_fwd_workspace_size",
            "kda_gdr_bwd", "kda_gdr_bwd_workspace_size", "kda_gdr_decode", "kda_gdr_fwd", "kda_gdr_fwd_workspace_size",
            "kda_qk_norm", "kda_qk_norm_bwd", "kda_qk_norm_bwd_workspace_size",
+           "kda_add_norm", "kda_add_norm_bwd", "kda_conv", "kda_conv_bwd", "kda_conv_bwd_workspace_size", "kda_conv_decode",
+           "kda_gated_norm", "kda_gated_norm_bwd", "kda_norm_bwd_workspace_size",
            "library_path", "load_library"]

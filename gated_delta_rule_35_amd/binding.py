@@ -2,9 +2,10 @@
 
 Names follow the C ABI in include/kda.h: kda_fwd, kda_fwd_ws, kda_fwd_noalloc,
 kda_fwd_intra, kda_fwd_scan, kda_fwd_trace, kda_fwd_cp, kda_decode, kda_bwd,
-kda_gdr_fwd, kda_gdr_bwd, kda_gdr_decode, kda_qk_norm, kda_qk_norm_bwd (called
-through the extension _kda_py) and their size queries, kda_status_string,
-kda_dv_slices.  Tensors are passed as
+kda_gdr_fwd, kda_gdr_bwd, kda_gdr_decode, kda_qk_norm, kda_qk_norm_bwd, kda_conv,
+kda_conv_bwd, kda_conv_decode, kda_gated_norm, kda_gated_norm_bwd, kda_add_norm,
+kda_add_norm_bwd (called through the extension _kda_py) and their size queries,
+kda_status_string, kda_dv_slices.  Tensors are passed as
 kda_tensor_t descriptors built from torch tensors (data pointer, dtype, shape,
 strides); the stream is torch's current HIP stream unless one is given.  Where
 an entry point takes a workspace, it is a uint8 device tensor the caller passes
@@ -31,7 +32,9 @@ EXPORTED = ["kda_fwd", "kda_fwd_fused", "kda_fwd_ws", "kda_fwd_qg", "kda_fwd_noa
             "kda_fwd_scan", "kda_fwd_trace", "kda_fwd_cp", "kda_decode", "kda_bwd", "kda_fwd_workspace_size",
             "kda_fwd_cp_workspace_size", "kda_fwd_cp_packed_workspace_size", "kda_fwd_cp_plan", "kda_bwd_workspace_size", "kda_status_string",
             "kda_dv_slices", "kda_gdr_fwd", "kda_gdr_fwd_workspace_size", "kda_gdr_bwd", "kda_gdr_bwd_workspace_size",
-            "kda_gdr_decode", "kda_qk_norm", "kda_qk_norm_bwd", "kda_qk_norm_bwd_workspace_size"]
+            "kda_gdr_decode", "kda_qk_norm", "kda_qk_norm_bwd", "kda_qk_norm_bwd_workspace_size", "kda_conv", "kda_conv_bwd",
+            "kda_conv_bwd_workspace_size", "kda_conv_decode", "kda_gated_norm", "kda_gated_norm_bwd",
+            "kda_norm_bwd_workspace_size", "kda_add_norm", "kda_add_norm_bwd"]
 
 
 class KdaTensor(ctypes.Structure):
@@ -109,8 +112,18 @@ def load_library(path=None):
     lib.kda_qk_norm.argtypes = [vp] * 4 + [ctypes.c_int32, ctypes.c_float] + [vp] * 3 + [ctypes.c_int32] + [vp] * 3
     lib.kda_qk_norm_bwd.argtypes = [vp] * 6 + [ctypes.c_int32, ctypes.c_float] + [vp] * 3 + [ctypes.c_int32] + \
         [vp] * 5 + [i64, vp]
-    for name in ("kda_gdr_fwd", "kda_gdr_bwd", "kda_gdr_decode", "kda_qk_norm", "kda_qk_norm_bwd"):
+    i32, f32 = ctypes.c_int32, ctypes.c_float
+    lib.kda_conv.argtypes = lib.kda_conv_decode.argtypes = [vp] * 3 + [i32] + [vp] * 5
+    lib.kda_conv_bwd.argtypes = [vp] * 3 + [i32] + [vp] * 9 + [i64, vp]
+    lib.kda_gated_norm.argtypes = [vp] * 3 + [i32, i32, f32] + [vp] * 2
+    lib.kda_gated_norm_bwd.argtypes = [vp] * 3 + [i32, i32, f32] + [vp] * 5 + [i64, vp]
+    lib.kda_add_norm.argtypes = [vp] * 3 + [f32, f32] + [vp] * 3
+    lib.kda_add_norm_bwd.argtypes = [vp] * 2 + [f32, f32] + [vp] * 6 + [i64, vp]
+    for name in _ENTRIES:
         getattr(lib, name).restype = ctypes.c_int
+    lib.kda_conv_bwd_workspace_size.argtypes = [i64] * 3
+    lib.kda_norm_bwd_workspace_size.argtypes = [i64] * 2
+    lib.kda_conv_bwd_workspace_size.restype = lib.kda_norm_bwd_workspace_size.restype = i64
     lib.kda_gdr_fwd_workspace_size.argtypes = lib.kda_gdr_bwd_workspace_size.argtypes = [i64] * 3
     lib.kda_gdr_fwd_workspace_size.restype = lib.kda_gdr_bwd_workspace_size.restype = i64
     lib.kda_qk_norm_bwd_workspace_size.argtypes = []
@@ -464,11 +477,13 @@ def kda_bwd(q, k, v, g, beta, scale, d_out, initial_state=None, d_final_state=No
     return out
 
 
-# ---- gated delta rule with one decay per head, per-head q/k norm ----
+# ---- gated delta rule with one decay per head, norms, short convolution ----
 # These entry points are called for every layer and token while serving, where the
 # host's share of a call counts: descriptors are made by the extension _kda_py (csrc/kda_py.c).
-_ENTRIES = ("kda_gdr_fwd", "kda_gdr_bwd", "kda_gdr_decode", "kda_qk_norm", "kda_qk_norm_bwd")
-_GDR_FWD, _GDR_BWD, _GDR_DECODE, _QK_NORM, _QK_NORM_BWD = range(5)
+_ENTRIES = ("kda_gdr_fwd", "kda_gdr_bwd", "kda_gdr_decode", "kda_qk_norm", "kda_qk_norm_bwd", "kda_conv", "kda_conv_bwd",
+            "kda_conv_decode", "kda_gated_norm", "kda_gated_norm_bwd", "kda_add_norm", "kda_add_norm_bwd")
+(_GDR_FWD, _GDR_BWD, _GDR_DECODE, _QK_NORM, _QK_NORM_BWD, _CONV, _CONV_BWD, _CONV_DECODE, _GATED_NORM, _GATED_NORM_BWD,
+ _ADD_NORM, _ADD_NORM_BWD) = range(len(_ENTRIES))
 _call_entry = None
 
 
@@ -650,4 +665,167 @@ def kda_qk_norm_bwd(q, k, d_q_out, d_k_out, q_weight=None, k_weight=None, mode="
     _launch(_QK_NORM_BWD, dev, (_NORM_MODES[mode], eps, bool(interleaved)),
             (q, k, d_q_out, d_k_out, q_weight, k_weight, cos, sin, positions, res["dq"], res["dk"], res["dq_weight"],
              res["dk_weight"]), stream, workspace)
+    return res
+
+
+_ACTIVATIONS = {None: 0, "silu": 1, "sigmoid": 2}
+
+
+def _activation(entry, activation, allowed):
+    if activation not in allowed:
+        raise ValueError(f"{entry}: activation {activation!r} is none of {', '.join(map(repr, allowed))}")
+    return _ACTIVATIONS[activation]
+
+
+def kda_conv_bwd_workspace_size(total_tokens, channels, width):
+    return int(load_library().kda_conv_bwd_workspace_size(total_tokens, channels, width))
+
+
+def kda_conv(x, weight, bias=None, activation="silu", cu_seqlens=None, initial_state=None, out=None, final_state=None,
+             stream=None):
+    """Short causal convolution of each channel of x [B, T, C] (bf16, fp16 or fp32, may be a view) with its
+    taps weight [C, W] (fp32, W 2 to 4); activation "silu" or None (see include/kda.h).  The states
+    [N, W - 1, C] hold the inputs before a sequence's first and its last ones.  Returns (out, final_state);
+    out and final_state=True are allocated here when not given."""
+    act = _activation("kda_conv", activation, (None, "silu"))
+    dev = _gpu_of(x, _CONV)
+    with _place(stream, dev):
+        if out is None:
+            out = _new(x, x.dtype)
+        if final_state is True:
+            final_state = _new(x, x.dtype, (_sequences(x, cu_seqlens), max(weight.shape[-1] - 1, 0), x.shape[-1]))
+    _launch(_CONV, dev, (act,), (x, weight, bias, cu_seqlens, initial_state, out, final_state), stream)
+    return out, final_state
+
+
+def kda_conv_bwd(x, weight, d_out, bias=None, activation="silu", cu_seqlens=None, initial_state=None, d_final_state=None,
+                 grads=None, d_initial_state=False, stream=None, workspace=None):
+    """Gradients of kda_conv: a dict with dx (x's dtype), dweight and dbias (fp32; dbias None without bias)
+    and dstate (x's dtype, [N, W - 1, C] when d_initial_state is True or a tensor, else None).  `grads` may
+    hold preallocated outputs under those names; `workspace` a uint8 device tensor of
+    kda_conv_bwd_workspace_size() bytes (None: taken here)."""
+    act = _activation("kda_conv_bwd", activation, (None, "silu"))
+    dev = _gpu_of(x, _CONV_BWD)
+    res = dict(grads or {})
+    with _place(stream, dev):
+        if res.get("dx") is None:
+            res["dx"] = _new(x, x.dtype)
+        if res.get("dweight") is None:
+            res["dweight"] = _new(weight, torch.float32)
+        if bias is None:
+            res["dbias"] = None
+        elif res.get("dbias") is None:
+            res["dbias"] = _new(bias, torch.float32)
+        if isinstance(d_initial_state, torch.Tensor):
+            res["dstate"] = d_initial_state
+        elif d_initial_state:
+            res["dstate"] = _new(x, x.dtype, (_sequences(x, cu_seqlens), max(weight.shape[-1] - 1, 0), x.shape[-1]))
+        else:
+            res["dstate"] = None
+        if workspace is None and x.dim() == 3 and weight.dim() == 2:   # the C library rejects other ranks
+            workspace = _scratch(kda_conv_bwd_workspace_size(x.shape[0] * x.shape[1], x.shape[2], weight.shape[1]), x)
+    _launch(_CONV_BWD, dev, (act,),
+            (x, weight, bias, cu_seqlens, initial_state, d_out, d_final_state, res["dx"], res["dweight"], res["dbias"],
+             res["dstate"]), stream, workspace)
+    return res
+
+
+def kda_conv_decode(x, weight, state, bias=None, activation="silu", state_indices=None, out=None, new_state=None,
+                    stream=None):
+    """One token per row of kda_conv: x [N, C].  `state` [N, W - 1, C] of x's dtype (None: zeros), or with
+    `state_indices` (int32 [N]) a pool [slots, W - 1, C], under kda_gdr_decode's rules.  The new states go to
+    `new_state`, by default `state` itself.  Returns (out, new_state); rows of `out` that are skipped are not
+    written."""
+    if new_state is None and state is None and state_indices is not None:
+        raise ValueError("kda_conv_decode needs a pool where state_indices name its slots")
+    act = _activation("kda_conv_decode", activation, (None, "silu"))
+    dev = _gpu_of(x, _CONV_DECODE)
+    with _place(stream, dev):
+        if out is None:
+            out = _new(x, x.dtype)
+        if new_state is None:
+            new_state = state if state is not None else _new(x, x.dtype, (x.shape[0], max(weight.shape[-1] - 1, 0), x.shape[-1]))
+    _launch(_CONV_DECODE, dev, (act,), (x, weight, bias, state, new_state, state_indices, out), stream)
+    return out, new_state
+
+
+def kda_norm_bwd_workspace_size(heads, channels):
+    """Bytes of device workspace kda_gated_norm_bwd and kda_add_norm_bwd need for weight gradients: `heads` H
+    for a weight per head, else 1."""
+    return int(load_library().kda_norm_bwd_workspace_size(heads, channels))
+
+
+def kda_gated_norm(x, gate, weight=None, activation="silu", gate_first=False, eps=1e-6, out=None, stream=None):
+    """Norm over the last dimension of x [B, T, H, D] (bf16, fp16 or fp32, may be a view) times weight ([D], or [H, D],
+    fp32) and the activation of the gate ("silu" or "sigmoid"), or with gate_first the norm of their product
+    (see include/kda.h).  Returns out, of x's dtype."""
+    act = _activation("kda_gated_norm", activation, ("silu", "sigmoid"))
+    dev = _gpu_of(x, _GATED_NORM)
+    if out is None:
+        with _place(stream, dev):
+            out = _new(x, x.dtype)
+    _launch(_GATED_NORM, dev, (act, bool(gate_first), eps), (x, gate, weight, out), stream)
+    return out
+
+
+def _norm_scratch(weight, x):
+    if weight is None or weight.dim() not in (1, 2):
+        return None
+    return _scratch(kda_norm_bwd_workspace_size(weight.shape[0] if weight.dim() == 2 else 1, weight.shape[-1]), x)
+
+
+def kda_gated_norm_bwd(x, gate, d_out, weight=None, activation="silu", gate_first=False, eps=1e-6, grads=None, stream=None,
+                       workspace=None):
+    """Gradients of kda_gated_norm: a dict with dx, dgate (x's dtype) and dweight (fp32, or None without weight).
+    `grads` may hold preallocated outputs under those names."""
+    act = _activation("kda_gated_norm_bwd", activation, ("silu", "sigmoid"))
+    dev = _gpu_of(x, _GATED_NORM_BWD)
+    res = dict(grads or {})
+    with _place(stream, dev):
+        for name, like in (("dx", x), ("dgate", gate)):
+            if res.get(name) is None:
+                res[name] = _new(like, x.dtype)
+        if weight is None:
+            res["dweight"] = None
+        elif res.get("dweight") is None:
+            res["dweight"] = _new(weight, torch.float32)
+        if workspace is None:
+            workspace = _norm_scratch(weight, x)
+    _launch(_GATED_NORM_BWD, dev, (act, bool(gate_first), eps),
+            (x, gate, weight, d_out, res["dx"], res["dgate"], res["dweight"]), stream, workspace)
+    return res
+
+
+def kda_add_norm(x, residual, weight=None, scale=1.0, eps=1e-6, out=None, new_residual=None, stream=None):
+    """sum = residual + scale x and its norm over the last dimension times weight [D] (fp32): x [B, T, D], the residual of
+    x's dtype or fp32 (both may be views).  Returns (out, sum), of x's and of the residual's dtype; `out` may be
+    x and `new_residual`, where the sum goes, the residual itself."""
+    dev = _gpu_of(x, _ADD_NORM)
+    with _place(stream, dev):
+        if out is None:
+            out = _new(x, x.dtype)
+        if new_residual is None:
+            new_residual = _new(residual, residual.dtype)
+    _launch(_ADD_NORM, dev, (scale, eps), (x, residual, weight, out, new_residual), stream)
+    return out, new_residual
+
+
+def kda_add_norm_bwd(sum, d_out, weight=None, scale=1.0, eps=1e-6, d_sum=None, grads=None, stream=None, workspace=None):
+    """Gradients of kda_add_norm from the sum that it returned: a dict with dx (d_out's dtype), dresidual (the
+    sum's dtype) and dweight (fp32, or None without weight).  `d_sum`: the gradient that reaches the sum from
+    elsewhere.  `grads` may hold preallocated outputs under those names."""
+    dev = _gpu_of(sum, _ADD_NORM_BWD)
+    res = dict(grads or {})
+    with _place(stream, dev):
+        for name, like in (("dx", d_out), ("dresidual", sum)):
+            if res.get(name) is None:
+                res[name] = _new(like, like.dtype)
+        if weight is None:
+            res["dweight"] = None
+        elif res.get("dweight") is None:
+            res["dweight"] = _new(weight, torch.float32)
+        if workspace is None:
+            workspace = _norm_scratch(weight, sum)
+    _launch(_ADD_NORM_BWD, dev, (scale, eps),
+            (sum, weight, d_out, d_sum, res["dx"], res["dresidual"], res["dweight"]), stream, workspace)
     return res

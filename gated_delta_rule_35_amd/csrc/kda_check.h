@@ -65,6 +65,45 @@ inline bool ranges_overlap(const void* a, int64_t abytes, const void* b, int64_t
     return x < y + bbytes && y < x + abytes;
 }
 
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 1;
+
+// A tensor's bytes in memory, from its first element to past its last.
+struct Span {
+    const void* p;
+    int64_t bytes;
+};
+inline Span span_of(const kda_tensor_t* t) {
+    if (!t) return {nullptr, 0};
+    int64_t last = 0;
+    for (int i = 0; i < t->ndim; ++i) {
+        if (t->shape[i] <= 0) return {nullptr, 0};
+        last += (t->shape[i] - 1) * t->stride[i];
+    }
+    return {t->data, (last + 1) * (int64_t)elem_size(t->dtype)};
+}
+inline bool overlaps(const kda_tensor_t* a, const kda_tensor_t* b) {
+    const Span x = span_of(a), y = span_of(b);
+    return ranges_overlap(x.p, x.bytes, y.p, y.bytes);
+}
+// Whether an output shares memory with an input or with another output.
+inline bool any_overlap(const kda_tensor_t* const* outs, int no, const kda_tensor_t* const* ins, int ni) {
+    for (int i = 0; i < no; ++i) {
+        for (int j = 0; j < ni; ++j)
+            if (overlaps(outs[i], ins[j])) return true;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(outs[i], outs[j])) return true;
+    }
+    return false;
+}
+
+inline bool sizes_ok(const kda_tensor_t* t) {
+    for (int i = 0; i < t->ndim; ++i)
+        if (t->shape[i] < 0 || t->shape[i] > kMaxTokens) return false;
+    return true;
+}
+
+inline int64_t up256(int64_t x) { return (x + 255) & ~int64_t(255); }
+
 inline bool same_shape(const kda_tensor_t* a, const int64_t* s, int nd) {
     for (int i = 0; i < nd; ++i)
         if (a->shape[i] != s[i]) return false;

@@ -1,0 +1,98 @@
+// Eight neighbouring elements of a row as a lane holds them: 16 bytes of bf16 or fp16, 32 of
+// fp32, widened to fp32 and rounded back once (to nearest, ties to even).
+#pragma once
+#include "kda_gdr_device.h"
+
+namespace kda {
+
+template <int XT>
+struct Elems;
+template <>
+struct Elems<0> {   // bf16
+    typedef uint16_t T;
+    typedef u32x4 Raw;   // eight channels as they lie in memory
+    static __device__ __forceinline__ Raw load(const void* p, int64_t at) {
+        return *reinterpret_cast<const Raw*>(static_cast<const T*>(p) + at);
+    }
+    static __device__ __forceinline__ void widen(const Raw& v, float (&x)[8]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = bf_lo(v[i]);
+            x[2 * i + 1] = bf_hi(v[i]);
+        }
+    }
+    static __device__ __forceinline__ void store(void* p, int64_t at, const float (&x)[8]) {
+        *reinterpret_cast<u32x4*>(static_cast<T*>(p) + at) =
+            u32x4{pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]), pack_bf2(x[6], x[7])};
+    }
+};
+template <>
+struct Elems<1> {   // fp16
+    typedef uint16_t T;
+    typedef half8 Raw;
+    static __device__ __forceinline__ Raw load(const void* p, int64_t at) {
+        return *reinterpret_cast<const Raw*>(static_cast<const T*>(p) + at);
+    }
+    static __device__ __forceinline__ void widen(const Raw& v, float (&x)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = (float)v[i];
+    }
+    static __device__ __forceinline__ void store(void* p, int64_t at, const float (&x)[8]) {
+        *reinterpret_cast<u32x4*>(static_cast<T*>(p) + at) =
+            u32x4{pack_h2(x[0], x[1]), pack_h2(x[2], x[3]), pack_h2(x[4], x[5]), pack_h2(x[6], x[7])};
+    }
+};
+template <>
+struct Elems<2> {   // fp32
+    typedef float T;
+    struct Raw {
+        f32x4 a, b;
+    };
+    static __device__ __forceinline__ Raw load(const void* p, int64_t at) {
+        const f32x4* s = reinterpret_cast<const f32x4*>(static_cast<const T*>(p) + at);
+        return {s[0], s[1]};
+    }
+    static __device__ __forceinline__ void widen(const Raw& v, float (&x)[8]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = v.a[i];
+            x[4 + i] = v.b[i];
+        }
+    }
+    static __device__ __forceinline__ void store(void* p, int64_t at, const float (&x)[8]) {
+        f32x4* d = reinterpret_cast<f32x4*>(static_cast<T*>(p) + at);
+        d[0] = f32x4{x[0], x[1], x[2], x[3]};
+        d[1] = f32x4{x[4], x[5], x[6], x[7]};
+    }
+};
+
+// e^x for finite and infinite x to about one unit in the last place: the product with log2 e is
+// kept with what its rounding leaves.  Below -200 the result is 0 either way; NaN stays.
+__device__ __forceinline__ float exp_of(float x) {
+    x = x < -200.f ? -200.f : (x > 200.f ? 200.f : x);
+    const float h = x * LOG2E, l = fmaf(x, LOG2E, -h) + x * 1.92596299e-8f;
+    return fexp2(h) * fmaf(l, LN2, 1.f);
+}
+// 1 / (1 + e^-z), and z times it.
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + exp_of(-z)); }
+
+enum { ACT_NONE = 0, ACT_SILU = 1, ACT_SIGMOID = 2 };
+// act(z), and its derivative where `slope` is wanted.
+__device__ __forceinline__ float activation(int act, float z) {
+    if (act == ACT_NONE) return z;
+    const float s = sigmoid(z);
+    return act == ACT_SILU ? z * s : s;
+}
+__device__ __forceinline__ void activation(int act, float z, float& y, float& slope) {
+    if (act == ACT_NONE) {
+        y = z;
+        slope = 1.f;
+        return;
+    }
+    const float e = exp_of(-z), s = __builtin_amdgcn_rcpf(1.f + e);
+    const float r = e >= 0x1p100f ? 1.f : e * s;   // 1 - s without its cancellation
+    y = act == ACT_SILU ? z * s : s;
+    slope = act == ACT_SILU ? s * fmaf(z, r, 1.f) : s * r;
+}
+
+}  // namespace kda

@@ -16,43 +16,7 @@ namespace {
 using namespace kda::check;
 using kda::Rows;
 
-constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxRowStride = int64_t(1) << 23;   // a chunk's byte offsets stay below 2^31
-
-// A tensor's bytes in memory, from its first element to past its last.
-struct Span {
-    const void* p;
-    int64_t bytes;
-};
-Span span_of(const kda_tensor_t* t) {
-    if (!t) return {nullptr, 0};
-    int64_t last = 0;
-    for (int i = 0; i < t->ndim; ++i) {
-        if (t->shape[i] <= 0) return {nullptr, 0};
-        last += (t->shape[i] - 1) * t->stride[i];
-    }
-    return {t->data, (last + 1) * (int64_t)elem_size(t->dtype)};
-}
-bool overlaps(const kda_tensor_t* a, const kda_tensor_t* b) {
-    const Span x = span_of(a), y = span_of(b);
-    return ranges_overlap(x.p, x.bytes, y.p, y.bytes);
-}
-// Whether an output shares memory with an input or with another output.
-bool any_overlap(const kda_tensor_t* const* outs, int no, const kda_tensor_t* const* ins, int ni) {
-    for (int i = 0; i < no; ++i) {
-        for (int j = 0; j < ni; ++j)
-            if (overlaps(outs[i], ins[j])) return true;
-        for (int j = 0; j < i; ++j)
-            if (overlaps(outs[i], outs[j])) return true;
-    }
-    return false;
-}
-
-bool sizes_ok(const kda_tensor_t* t) {
-    for (int i = 0; i < t->ndim; ++i)
-        if (t->shape[i] < 0 || t->shape[i] > kMaxTokens) return false;
-    return true;
-}
 
 // Rows of 128 channels [B, T, H, 128], or [N, H, 128] with ndim 3: the channels are
 // contiguous and rows start on multiples of 8 elements (16 bytes of bf16); tokens lie
@@ -139,8 +103,6 @@ kda_status_t check_out(const kda_tensor_t* t, const kda_tensor_t* like) {
     if (st != KDA_OK) return st;
     return same_shape(t, like->shape, like->ndim) ? KDA_OK : KDA_ERR_SHAPE;
 }
-
-int64_t up256(int64_t x) { return (x + 255) & ~int64_t(255); }
 
 // Workspace of a call in units of one (chunk slot, value head): the records, then, for
 // the backward, S, dS, u and dx.

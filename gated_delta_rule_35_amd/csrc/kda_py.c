@@ -1,6 +1,6 @@
 /*
- * The calling side of the per-head-decay delta rule and the q/k norm for Python
- * (module _kda_py): turns tensors into kda_tensor_t descriptors and calls the C entry
+ * The calling side of the per-head-decay delta rule, the q/k norm and what stands around
+ * them in a block for Python (module _kda_py): turns tensors into kda_tensor_t descriptors and calls the C entry
  * point, so that a one-token call's host share is a few microseconds.  Tensors are
  * read through their own methods (get_device, data_ptr, dim, shape, stride, dtype);
  * nothing of torch's headers or of the library is linked: bind() hands over the entry
@@ -11,14 +11,19 @@
 
 #include "../../include/kda.h"
 
-enum { GDR_FWD, GDR_BWD, GDR_DECODE, QK_NORM, QK_NORM_BWD, ENTRIES };
+enum {
+    GDR_FWD, GDR_BWD, GDR_DECODE, QK_NORM, QK_NORM_BWD, CONV, CONV_BWD, CONV_DECODE, GATED_NORM, GATED_NORM_BWD,
+    ADD_NORM, ADD_NORM_BWD, ENTRIES
+};
 #define MOST_TENSORS 16
 
 typedef const kda_tensor_t* T;
 static void* entry_point[ENTRIES];
 static const char* const entry_name[ENTRIES] = {"kda_gdr_fwd", "kda_gdr_bwd", "kda_gdr_decode", "kda_qk_norm",
-                                                "kda_qk_norm_bwd"};
-static const int entry_tensors[ENTRIES] = {9, 15, 9, 9, 13}, entry_scalars[ENTRIES] = {1, 1, 1, 3, 3};
+                                                "kda_qk_norm_bwd", "kda_conv", "kda_conv_bwd", "kda_conv_decode",
+                                                "kda_gated_norm", "kda_gated_norm_bwd", "kda_add_norm", "kda_add_norm_bwd"};
+static const int entry_tensors[ENTRIES] = {9, 15, 9, 9, 13, 7, 11, 7, 4, 7, 5, 7};
+static const int entry_scalars[ENTRIES] = {1, 1, 1, 3, 3, 1, 1, 1, 3, 3, 2, 2};
 static PyObject* dtypes[4];   /* by kda_dtype_t */
 static PyObject *s_get_device, *s_data_ptr, *s_dim, *s_shape, *s_stride, *s_dtype, *s_nbytes;
 
@@ -146,11 +151,39 @@ static PyObject* call(PyObject* self, PyObject* const* a, Py_ssize_t na) {
                 t[0], t[1], t[2], t[3], (int32_t)s[0], (float)s[1], t[4], t[5], t[6], (int32_t)s[2], t[7], t[8],
                 stream);
             break;
-        default:
+        case QK_NORM_BWD:
             st = ((kda_status_t(*)(T, T, T, T, T, T, int32_t, float, T, T, T, int32_t, T, T, T, T, void*, int64_t,
                                    void*))entry_point[e])(t[0], t[1], t[2], t[3], t[4], t[5], (int32_t)s[0],
                                                           (float)s[1], t[6], t[7], t[8], (int32_t)s[2], t[9], t[10],
                                                           t[11], t[12], ws, ws_bytes, stream);
+            break;
+        case CONV:
+            st = ((kda_status_t(*)(T, T, T, int32_t, T, T, T, T, void*))entry_point[e])(
+                t[0], t[1], t[2], (int32_t)s[0], t[3], t[4], t[5], t[6], stream);
+            break;
+        case CONV_BWD:
+            st = ((kda_status_t(*)(T, T, T, int32_t, T, T, T, T, T, T, T, T, void*, int64_t, void*))entry_point[e])(
+                t[0], t[1], t[2], (int32_t)s[0], t[3], t[4], t[5], t[6], t[7], t[8], t[9], t[10], ws, ws_bytes, stream);
+            break;
+        case CONV_DECODE:
+            st = ((kda_status_t(*)(T, T, T, int32_t, T, T, T, T, void*))entry_point[e])(
+                t[0], t[1], t[2], (int32_t)s[0], t[3], t[4], t[5], t[6], stream);
+            break;
+        case GATED_NORM:
+            st = ((kda_status_t(*)(T, T, T, int32_t, int32_t, float, T, void*))entry_point[e])(
+                t[0], t[1], t[2], (int32_t)s[0], (int32_t)s[1], (float)s[2], t[3], stream);
+            break;
+        case GATED_NORM_BWD:
+            st = ((kda_status_t(*)(T, T, T, int32_t, int32_t, float, T, T, T, T, void*, int64_t, void*))entry_point[e])(
+                t[0], t[1], t[2], (int32_t)s[0], (int32_t)s[1], (float)s[2], t[3], t[4], t[5], t[6], ws, ws_bytes, stream);
+            break;
+        case ADD_NORM:
+            st = ((kda_status_t(*)(T, T, T, float, float, T, T, void*))entry_point[e])(t[0], t[1], t[2], (float)s[0],
+                                                                                       (float)s[1], t[3], t[4], stream);
+            break;
+        case ADD_NORM_BWD:
+            st = ((kda_status_t(*)(T, T, float, float, T, T, T, T, T, void*, int64_t, void*))entry_point[e])(
+                t[0], t[1], (float)s[0], (float)s[1], t[2], t[3], t[4], t[5], t[6], ws, ws_bytes, stream);
             break;
     }
     Py_END_ALLOW_THREADS
@@ -163,7 +196,7 @@ static PyObject* bind(PyObject* self, PyObject* args) {
     PyObject *fns, *dts;
     if (!PyArg_ParseTuple(args, "O!O!", &PyTuple_Type, &fns, &PyTuple_Type, &dts)) return NULL;
     if (PyTuple_GET_SIZE(fns) != ENTRIES || PyTuple_GET_SIZE(dts) != 4) {
-        PyErr_SetString(PyExc_TypeError, "bind() takes five addresses and four dtypes");
+        PyErr_SetString(PyExc_TypeError, "bind() takes one address for each entry point and four dtypes");
         return NULL;
     }
     void* p[ENTRIES];

@@ -17,74 +17,13 @@
 // Weight gradients: each lane sums its eight channels over the rows of its work-group's
 // stride, work-groups leave 128 sums each, and a second launch adds those in a fixed
 // order (no atomics).
-#include "kda_gdr_device.h"
+#include "kda_elems.h"
 
 namespace kda {
 
 namespace {
 
 constexpr int NT = 256;
-
-template <int XT>
-struct NormType;
-template <>
-struct NormType<0> {   // bf16
-    typedef uint16_t T;
-    typedef u32x4 Raw;   // eight channels as they lie in memory
-    static __device__ __forceinline__ Raw load(const void* p, int64_t at) {
-        return *reinterpret_cast<const Raw*>(static_cast<const T*>(p) + at);
-    }
-    static __device__ __forceinline__ void widen(const Raw& v, float (&x)[8]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = bf_lo(v[i]);
-            x[2 * i + 1] = bf_hi(v[i]);
-        }
-    }
-    static __device__ __forceinline__ void store(void* p, int64_t at, const float (&x)[8]) {
-        *reinterpret_cast<u32x4*>(static_cast<T*>(p) + at) =
-            u32x4{pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]), pack_bf2(x[6], x[7])};
-    }
-};
-template <>
-struct NormType<1> {   // fp16
-    typedef uint16_t T;
-    typedef half8 Raw;
-    static __device__ __forceinline__ Raw load(const void* p, int64_t at) {
-        return *reinterpret_cast<const Raw*>(static_cast<const T*>(p) + at);
-    }
-    static __device__ __forceinline__ void widen(const Raw& v, float (&x)[8]) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = (float)v[i];
-    }
-    static __device__ __forceinline__ void store(void* p, int64_t at, const float (&x)[8]) {
-        *reinterpret_cast<u32x4*>(static_cast<T*>(p) + at) =
-            u32x4{pack_h2(x[0], x[1]), pack_h2(x[2], x[3]), pack_h2(x[4], x[5]), pack_h2(x[6], x[7])};
-    }
-};
-template <>
-struct NormType<2> {   // fp32
-    typedef float T;
-    struct Raw {
-        f32x4 a, b;
-    };
-    static __device__ __forceinline__ Raw load(const void* p, int64_t at) {
-        const f32x4* s = reinterpret_cast<const f32x4*>(static_cast<const T*>(p) + at);
-        return {s[0], s[1]};
-    }
-    static __device__ __forceinline__ void widen(const Raw& v, float (&x)[8]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[i] = v.a[i];
-            x[4 + i] = v.b[i];
-        }
-    }
-    static __device__ __forceinline__ void store(void* p, int64_t at, const float (&x)[8]) {
-        f32x4* d = reinterpret_cast<f32x4*>(static_cast<T*>(p) + at);
-        d[0] = f32x4{x[0], x[1], x[2], x[3]};
-        d[1] = f32x4{x[4], x[5], x[6], x[7]};
-    }
-};
 
 // Row `i` of a side: its offset in x and its token (a side has fewer than 2^31 rows).
 struct RowAt {
@@ -163,7 +102,7 @@ __global__ void __launch_bounds__(NT) kda_qk_norm_kernel(const NormParams p) {
     const uint32_t row = (uint32_t)block * NORM_ROWS + (threadIdx.x >> 4), rows = (uint32_t)s.rows;
     const RowAt at = row_at(p, s, row < rows ? row : rows - 1);   // lanes past the end repeat the last row
     float x[8];
-    NormType<XT>::widen(NormType<XT>::load(s.x, at.x + 8 * l), x);
+    Elems<XT>::widen(Elems<XT>::load(s.x, at.x + 8 * l), x);
     const Angles an = angles(p, at.token, l);
     float ss = 0.f;
 #pragma unroll
@@ -172,7 +111,7 @@ __global__ void __launch_bounds__(NT) kda_qk_norm_kernel(const NormParams p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] *= r * w[i];
     rotate<1>(p, an, l, lane, x);
-    if (row < rows) NormType<0>::store(s.y, (int64_t)row * DK + 8 * l, x);
+    if (row < rows) Elems<0>::store(s.y, (int64_t)row * DK + 8 * l, x);
 }
 
 template <int XT, int DT>
@@ -194,12 +133,12 @@ __global__ void __launch_bounds__(NT) kda_qk_norm_bwd_kernel(const NormParams p)
         const uint64_t row = base + (threadIdx.x >> 4);
         const uint32_t i0 = row < rows ? (uint32_t)row : rows - 1;
         const RowAt at = row_at(p, s, i0);
-        const auto rx = NormType<XT>::load(s.x, at.x + 8 * l);
-        const auto rd = NormType<DT>::load(s.dy, (int64_t)i0 * DK + 8 * l);
+        const auto rx = Elems<XT>::load(s.x, at.x + 8 * l);
+        const auto rd = Elems<DT>::load(s.dy, (int64_t)i0 * DK + 8 * l);
         const Angles an = angles(p, at.token, l);
         float x[8], d[8];
-        NormType<XT>::widen(rx, x);
-        NormType<DT>::widen(rd, d);
+        Elems<XT>::widen(rx, x);
+        Elems<DT>::widen(rd, d);
         rotate<-1>(p, an, l, lane, d);
         float ss = 0.f, xd = 0.f;
 #pragma unroll
@@ -215,7 +154,7 @@ __global__ void __launch_bounds__(NT) kda_qk_norm_bwd_kernel(const NormParams p)
                 dw[i] = fmaf(d[i] * r, x[i], dw[i]);
                 d[i] = r * (w[i] * d[i] - x[i] * m);
             }
-            NormType<XT>::store(s.y, (int64_t)row * DK + 8 * l, d);
+            Elems<XT>::store(s.y, (int64_t)row * DK + 8 * l, d);
         }
     }
     if (!s.dw) return;

@@ -567,6 +567,116 @@ kda_status_t kda_qk_norm_bwd(const kda_tensor_t* q, const kda_tensor_t* k, const
                              const kda_tensor_t* dk, const kda_tensor_t* d_q_weight, const kda_tensor_t* d_k_weight,
                              void* workspace, int64_t workspace_size, void* stream);
 
+/*
+ * What stands around the delta rule in a block.  Everything below follows kda_fwd's
+ * conventions (stream order, host-side checks before any HIP call, bitwise repeatable
+ * results, no pointer kept) except where stated.  "A view" is a tensor whose last dimension is
+ * contiguous, whose data is 16-byte aligned and whose other strides are non-negative
+ * multiples of 8 elements (slices of one projection's rows, for instance); every other tensor
+ * is contiguous.  Types: bf16, fp16 or fp32, the same for all of a call's tensors except where
+ * one is named.  Arithmetic and sums are fp32, each output is rounded once.  An output that
+ * shares memory with an input or another output returns KDA_ERR_LAYOUT except where it may
+ * replace one.
+ *
+ * kda_conv -- the short causal convolution before q, k and v (or x, B and C): one filter of
+ * W taps for each channel,
+ *
+ *     z_t = bias + sum_{i < W} weight[:, i] x_{t - W + 1 + i},  out_t = z_t (activation 0) or
+ *     z_t / (1 + e^{-z_t}) (activation 1)
+ *
+ * over each sequence by itself.  The W - 1 inputs before a sequence's first token are its
+ * initial state, its last W - 1 inputs (older ones of the initial state where it is shorter)
+ * the final state.
+ *   x               [B, T, C], a view; C a multiple of 8
+ *   weight, bias    [C, W] fp32 (16-byte aligned), W 2 to 4; [C] fp32, or NULL (zeros)
+ *   cu_seqlens      as for kda_fwd; rows of tokens in no sequence are not written
+ *   initial_state, final_state  [N, W - 1, C] of x's type, or NULL (zeros; not written)
+ *   out             [B, T, C] of x's type
+ * Other widths, channels and more than 2^20 channels, 2^31 - 1 tokens or 2^24 sequences return
+ * KDA_ERR_UNSUPPORTED.
+ */
+kda_status_t kda_conv(const kda_tensor_t* x, const kda_tensor_t* weight, const kda_tensor_t* bias, int32_t activation,
+                      const kda_tensor_t* cu_seqlens, const kda_tensor_t* initial_state, const kda_tensor_t* out,
+                      const kda_tensor_t* final_state, void* stream);
+
+/*
+ * kda_conv_bwd -- gradients of kda_conv, given those of the output (d_out [B, T, C]) and of
+ * the final state (d_final_state, NULL for zero).
+ *   dx               [B, T, C] of x's type
+ *   dweight, dbias   [C, W] and [C] fp32, summed over all tokens in a fixed order; dbias may be NULL
+ *                    and without bias has to be
+ *   d_initial_state  [N, W - 1, C] of x's type, or NULL (not computed)
+ * workspace: kda_conv_bwd_workspace_size(B * T, C, W) bytes, 16-byte aligned, as for
+ * kda_gdr_fwd; NULL allocates it in stream order.
+ */
+int64_t kda_conv_bwd_workspace_size(int64_t total_tokens, int64_t channels, int64_t width);
+kda_status_t kda_conv_bwd(const kda_tensor_t* x, const kda_tensor_t* weight, const kda_tensor_t* bias, int32_t activation,
+                          const kda_tensor_t* cu_seqlens, const kda_tensor_t* initial_state, const kda_tensor_t* d_out,
+                          const kda_tensor_t* d_final_state, const kda_tensor_t* dx, const kda_tensor_t* dweight,
+                          const kda_tensor_t* dbias, const kda_tensor_t* d_initial_state, void* workspace,
+                          int64_t workspace_size, void* stream);
+
+/*
+ * kda_conv_decode -- one token for each of N rows: x [N, C] (a view, any row stride), out
+ * [N, C].  The states are [N, W - 1, C], or with state_indices ([N] int32) pools [slots, W - 1,
+ * C], under kda_gdr_decode's rules: slots outside the pool skip their row, rows that name one
+ * slot are tokens of one sequence in the order of the batch, state_in may be NULL (zeros),
+ * state_out may be state_in, a partial overlap returns KDA_ERR_LAYOUT.
+ */
+kda_status_t kda_conv_decode(const kda_tensor_t* x, const kda_tensor_t* weight, const kda_tensor_t* bias,
+                             int32_t activation, const kda_tensor_t* state_in, const kda_tensor_t* state_out,
+                             const kda_tensor_t* state_indices, const kda_tensor_t* out, void* stream);
+
+/*
+ * kda_gated_norm -- the norm after a block with the block's gate.  With r(v) = (mean v^2 +
+ * eps)^{-1/2} over the D channels of a row and act(z) = z / (1 + e^{-z}) (activation 1) or
+ * 1 / (1 + e^{-z}) (activation 2):
+ *
+ *     out = x r(x) weight act(gate),  or with gate_first  out = v r(v) weight,  v = x act(gate)
+ *
+ *   x, gate   [B, T, H, D], views; D a multiple of 8 up to 8192
+ *   weight    [D], or [H, D] (one per head), fp32, 16-byte aligned; or NULL (ones)
+ *   out       [B, T, H, D] of x's type; may be x itself where x is contiguous
+ * More than 2^31 - 1 rows or 2^16 heads return KDA_ERR_UNSUPPORTED.
+ */
+kda_status_t kda_gated_norm(const kda_tensor_t* x, const kda_tensor_t* gate, const kda_tensor_t* weight,
+                            int32_t activation, int32_t gate_first, float eps, const kda_tensor_t* out, void* stream);
+
+/*
+ * kda_gated_norm_bwd -- gradients of kda_gated_norm: d_out, dx, dgate [B, T, H, D] of x's
+ * type; dweight fp32 of weight's shape, or NULL, summed in a fixed order.  workspace:
+ * kda_norm_bwd_workspace_size(H for a weight per head, else 1, D) bytes, 16-byte aligned,
+ * needed only with dweight; NULL then allocates it in stream order.
+ */
+int64_t kda_norm_bwd_workspace_size(int64_t heads, int64_t channels);
+kda_status_t kda_gated_norm_bwd(const kda_tensor_t* x, const kda_tensor_t* gate, const kda_tensor_t* weight,
+                                int32_t activation, int32_t gate_first, float eps, const kda_tensor_t* d_out,
+                                const kda_tensor_t* dx, const kda_tensor_t* dgate, const kda_tensor_t* dweight,
+                                void* workspace, int64_t workspace_size, void* stream);
+
+/*
+ * kda_add_norm -- a block's output added to the residual, and the norm before the next block:
+ *
+ *     sum = residual + scale x,  out = sum r(sum) weight     (out from the unrounded sum)
+ *
+ *   x [B, T, D] and residual [B, T, D], views, the residual of x's type or fp32; weight [D] fp32 or
+ *   NULL; out [B, T, D] of x's type, may be x itself where x is contiguous; sum [B, T, D] of the
+ *   residual's type, may be the residual itself where it is contiguous.  scale must be finite.
+ */
+kda_status_t kda_add_norm(const kda_tensor_t* x, const kda_tensor_t* residual, const kda_tensor_t* weight, float scale,
+                          float eps, const kda_tensor_t* out, const kda_tensor_t* sum, void* stream);
+
+/*
+ * kda_add_norm_bwd -- gradients of kda_add_norm from the sum as it was returned (a view):
+ * d_out [B, T, D] of x's type; d_sum the gradient that reaches the sum from elsewhere (of the
+ * sum's type), or NULL; dx of d_out's type, dresidual of the sum's, dweight fp32 or NULL.
+ * workspace: kda_norm_bwd_workspace_size(1, D) bytes, as for kda_gated_norm_bwd.
+ */
+kda_status_t kda_add_norm_bwd(const kda_tensor_t* sum, const kda_tensor_t* weight, float scale, float eps,
+                              const kda_tensor_t* d_out, const kda_tensor_t* d_sum, const kda_tensor_t* dx,
+                              const kda_tensor_t* dresidual, const kda_tensor_t* dweight, void* workspace,
+                              int64_t workspace_size, void* stream);
+
 /* Human-readable name of a status code (static storage; never NULL). */
 const char* kda_status_string(kda_status_t status);
 

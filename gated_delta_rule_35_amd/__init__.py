@@ -13,7 +13,8 @@ from .binding import (KdaError, kda_bwd, kda_bwd_workspace_size, kda_decode, kda
                       kda_gdr_bwd, kda_gdr_bwd_workspace_size, kda_gdr_decode, kda_gdr_fwd, kda_gdr_fwd_workspace_size,
                       kda_qk_norm, kda_qk_norm_bwd, kda_qk_norm_bwd_workspace_size,
                       kda_add_norm, kda_add_norm_bwd, kda_conv, kda_conv_bwd, kda_conv_bwd_workspace_size, kda_conv_decode,
-                      kda_gated_norm, kda_gated_norm_bwd, kda_norm_bwd_workspace_size,
+                      kda_gated_norm, kda_gated_norm_bwd, kda_norm_bwd_workspace_size, kda_ssm_bwd, kda_ssm_bwd_workspace_size,
+                      kda_ssm_decode, kda_ssm_fwd, kda_ssm_fwd_workspace_size,
                       library_path, load_library)
 
 __all__ = ["KdaError", "kda_bwd", "kda_bwd_workspace_size", "kda_decode", "kda_dv_slices", "kda_fwd", "kda_fwd_cp", "kda_fwd_cp_plan", "kda_fwd_fused",
@@ -23,4 +24,5 @@ __all__ = ["KdaError", "kda_bwd", "kda_bwd_workspace_size", "kda_decode", "kda_d
            "kda_qk_norm", "kda_qk_norm_bwd", "kda_qk_norm_bwd_workspace_size",
            "kda_add_norm", "kda_add_norm_bwd", "kda_conv", "kda_conv_bwd", "kda_conv_bwd_workspace_size", "kda_conv_decode",
            "kda_gated_norm", "kda_gated_norm_bwd", "kda_norm_bwd_workspace_size",
+           "kda_ssm_bwd", "kda_ssm_bwd_workspace_size", "kda_ssm_decode", "kda_ssm_fwd", "kda_ssm_fwd_workspace_size",
            "library_path", "load_library"]

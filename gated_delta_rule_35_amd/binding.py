@@ -4,7 +4,8 @@ Names follow the C ABI in include/kda.h: kda_fwd, kda_fwd_ws, kda_fwd_noalloc,
 kda_fwd_intra, kda_fwd_scan, kda_fwd_trace, kda_fwd_cp, kda_decode, kda_bwd,
 kda_gdr_fwd, kda_gdr_bwd, kda_gdr_decode, kda_qk_norm, kda_qk_norm_bwd, kda_conv,
 kda_conv_bwd, kda_conv_decode, kda_gated_norm, kda_gated_norm_bwd, kda_add_norm,
-kda_add_norm_bwd (called through the extension _kda_py) and their size queries,
+kda_add_norm_bwd, kda_ssm_fwd, kda_ssm_bwd, kda_ssm_decode (called through the
+extension _kda_py) and their size queries,
 kda_status_string, kda_dv_slices.  Tensors are passed as
 kda_tensor_t descriptors built from torch tensors (data pointer, dtype, shape,
 strides); the stream is torch's current HIP stream unless one is given.  Where
@@ -34,7 +35,8 @@ EXPORTED = ["kda_fwd", "kda_fwd_fused", "kda_fwd_ws", "kda_fwd_qg", "kda_fwd_noa
             "kda_dv_slices", "kda_gdr_fwd", "kda_gdr_fwd_workspace_size", "kda_gdr_bwd", "kda_gdr_bwd_workspace_size",
             "kda_gdr_decode", "kda_qk_norm", "kda_qk_norm_bwd", "kda_qk_norm_bwd_workspace_size", "kda_conv", "kda_conv_bwd",
             "kda_conv_bwd_workspace_size", "kda_conv_decode", "kda_gated_norm", "kda_gated_norm_bwd",
-            "kda_norm_bwd_workspace_size", "kda_add_norm", "kda_add_norm_bwd"]
+            "kda_norm_bwd_workspace_size", "kda_add_norm", "kda_add_norm_bwd", "kda_ssm_fwd", "kda_ssm_fwd_workspace_size",
+            "kda_ssm_bwd", "kda_ssm_bwd_workspace_size", "kda_ssm_decode"]
 
 
 class KdaTensor(ctypes.Structure):
@@ -119,6 +121,11 @@ def load_library(path=None):
     lib.kda_gated_norm_bwd.argtypes = [vp] * 3 + [i32, i32, f32] + [vp] * 5 + [i64, vp]
     lib.kda_add_norm.argtypes = [vp] * 3 + [f32, f32] + [vp] * 3
     lib.kda_add_norm_bwd.argtypes = [vp] * 2 + [f32, f32] + [vp] * 6 + [i64, vp]
+    lib.kda_ssm_fwd.argtypes = [vp] * 7 + [i32] + [vp] * 5 + [i64, vp]
+    lib.kda_ssm_bwd.argtypes = [vp] * 7 + [i32] + [vp] * 13 + [i64, vp]
+    lib.kda_ssm_decode.argtypes = [vp] * 7 + [i32] + [vp] * 5
+    for name in ("kda_ssm_fwd_workspace_size", "kda_ssm_bwd_workspace_size"):
+        getattr(lib, name).argtypes, getattr(lib, name).restype = [i64] * 6, i64
     for name in _ENTRIES:
         getattr(lib, name).restype = ctypes.c_int
     lib.kda_conv_bwd_workspace_size.argtypes = [i64] * 3
@@ -481,9 +488,10 @@ def kda_bwd(q, k, v, g, beta, scale, d_out, initial_state=None, d_final_state=No
 # These entry points are called for every layer and token while serving, where the
 # host's share of a call counts: descriptors are made by the extension _kda_py (csrc/kda_py.c).
 _ENTRIES = ("kda_gdr_fwd", "kda_gdr_bwd", "kda_gdr_decode", "kda_qk_norm", "kda_qk_norm_bwd", "kda_conv", "kda_conv_bwd",
-            "kda_conv_decode", "kda_gated_norm", "kda_gated_norm_bwd", "kda_add_norm", "kda_add_norm_bwd")
+            "kda_conv_decode", "kda_gated_norm", "kda_gated_norm_bwd", "kda_add_norm", "kda_add_norm_bwd",
+            "kda_ssm_fwd", "kda_ssm_bwd", "kda_ssm_decode")
 (_GDR_FWD, _GDR_BWD, _GDR_DECODE, _QK_NORM, _QK_NORM_BWD, _CONV, _CONV_BWD, _CONV_DECODE, _GATED_NORM, _GATED_NORM_BWD,
- _ADD_NORM, _ADD_NORM_BWD) = range(len(_ENTRIES))
+ _ADD_NORM, _ADD_NORM_BWD, _SSM_FWD, _SSM_BWD, _SSM_DECODE) = range(len(_ENTRIES))
 _call_entry = None
 
 
@@ -829,3 +837,84 @@ def kda_add_norm_bwd(sum, d_out, weight=None, scale=1.0, eps=1e-6, d_sum=None, g
     _launch(_ADD_NORM_BWD, dev, (scale, eps),
             (sum, weight, d_out, d_sum, res["dx"], res["dresidual"], res["dweight"]), stream, workspace)
     return res
+
+
+def kda_ssm_fwd_workspace_size(total_tokens, num_sequences, num_heads, num_groups, head_dim, state_dim):
+    return int(load_library().kda_ssm_fwd_workspace_size(total_tokens, num_sequences, num_heads, num_groups, head_dim, state_dim))
+
+
+def kda_ssm_bwd_workspace_size(total_tokens, num_sequences, num_heads, num_groups, head_dim, state_dim):
+    return int(load_library().kda_ssm_bwd_workspace_size(total_tokens, num_sequences, num_heads, num_groups, head_dim, state_dim))
+
+
+def _ssm_scratch(size, x, B, cu_seqlens):
+    if x.dim() != 4 or B.dim() != 4:   # the C library rejects other ranks
+        return None
+    return _scratch(size(x.shape[0] * x.shape[1], _sequences(x, cu_seqlens), x.shape[2], B.shape[2], x.shape[3], B.shape[3]), x)
+
+
+def kda_ssm_fwd(x, dt, A, B, C, D=None, dt_bias=None, softplus=True, cu_seqlens=None, initial_state=None, out=None,
+                final_state=None, stream=None, workspace=None):
+    """Selective state space scan: x [B, T, H, P] bf16, dt [B, T, H] (bf16 or fp32), A, D, dt_bias [H] fp32, B and C
+    [B, T, G, S] bf16, states [N, H, S, P] fp32 (see include/kda.h).  x, dt, B and C may be views.  Returns (out,
+    final_state); out and final_state=True are allocated here when not given.  `workspace`: a uint8 device
+    tensor of kda_ssm_fwd_workspace_size() bytes, or None (taken here)."""
+    dev = _gpu_of(x, _SSM_FWD)
+    with _place(stream, dev):
+        if out is None:
+            out = _new(x, torch.bfloat16)
+        if final_state is True:
+            final_state = _new(x, torch.float32, (_sequences(x, cu_seqlens), x.shape[-2], B.shape[-1], x.shape[-1]))
+        if workspace is None:
+            workspace = _ssm_scratch(kda_ssm_fwd_workspace_size, x, B, cu_seqlens)
+    _launch(_SSM_FWD, dev, (bool(softplus),),
+            (x, dt, A, B, C, D, dt_bias, cu_seqlens, initial_state, out, final_state), stream, workspace)
+    return out, final_state
+
+
+def kda_ssm_bwd(x, dt, A, B, C, d_out, D=None, dt_bias=None, softplus=True, initial_state=None, d_final_state=None,
+                grads=None, d_initial_state=False, stream=None, workspace=None, cu_seqlens=None):
+    """Gradients of kda_ssm_fwd: a dict with dx, dB, dC (bf16), ddt, dA, dD, ddt_bias (fp32; the last two None
+    without D or dt_bias) and dh0 (fp32 [N, H, S, P] when d_initial_state is True or a tensor, else None).
+    `grads` may hold preallocated outputs under those names; `workspace` a uint8 device tensor of
+    kda_ssm_bwd_workspace_size() bytes (None: taken here)."""
+    dev = _gpu_of(x, _SSM_BWD)
+    res = dict(grads or {})
+    with _place(stream, dev):
+        for name, like, dtype in (("dx", x, torch.bfloat16), ("ddt", dt, torch.float32), ("dA", A, torch.float32),
+                                  ("dB", B, torch.bfloat16), ("dC", C, torch.bfloat16), ("dD", D, torch.float32),
+                                  ("ddt_bias", dt_bias, torch.float32)):
+            if like is None:
+                res[name] = None
+            elif res.get(name) is None:
+                res[name] = _new(like, dtype)
+        if isinstance(d_initial_state, torch.Tensor):
+            res["dh0"] = d_initial_state
+        elif d_initial_state:
+            res["dh0"] = _new(x, torch.float32, (_sequences(x, cu_seqlens), x.shape[-2], B.shape[-1], x.shape[-1]))
+        else:
+            res["dh0"] = None
+        if workspace is None:
+            workspace = _ssm_scratch(kda_ssm_bwd_workspace_size, x, B, cu_seqlens)
+    _launch(_SSM_BWD, dev, (bool(softplus),),
+            (x, dt, A, B, C, D, dt_bias, cu_seqlens, initial_state, d_out, d_final_state, res["dx"], res["ddt"], res["dA"],
+             res["dB"], res["dC"], res["dD"], res["ddt_bias"], res["dh0"]), stream, workspace)
+    return res
+
+
+def kda_ssm_decode(x, dt, A, B, C, state, D=None, dt_bias=None, softplus=True, state_indices=None, out=None, new_state=None,
+                   stream=None):
+    """One token per row of kda_ssm_fwd: x [N, H, P], dt [N, H], B and C [N, G, S].  `state` [N, H, S, P] fp32 (None:
+    zero), or with `state_indices` (int32 [N]) a pool [slots, H, S, P], under kda_gdr_decode's rules.  The new
+    states go to `new_state`, by default `state` itself.  Returns (out, new_state); rows of `out` that are skipped
+    are not written."""
+    if new_state is None and state is None and state_indices is not None:
+        raise ValueError("kda_ssm_decode needs a pool where state_indices name its slots")
+    dev = _gpu_of(x, _SSM_DECODE)
+    with _place(stream, dev):
+        if out is None:
+            out = _new(x, torch.bfloat16)
+        if new_state is None:
+            new_state = state if state is not None else _new(x, torch.float32, (x.shape[0], x.shape[1], B.shape[-1], x.shape[2]))
+    _launch(_SSM_DECODE, dev, (bool(softplus),), (x, dt, A, B, C, D, dt_bias, state, new_state, state_indices, out), stream)
+    return out, new_state

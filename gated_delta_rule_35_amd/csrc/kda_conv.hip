@@ -354,21 +354,21 @@ __global__ void __launch_bounds__(DT) kda_conv_decode_kernel(const ConvParams p)
 
 // Sums over rows: a work-group takes 32 columns, eight threads each every eighth row, then in order.
 __global__ void __launch_bounds__(256) kda_sum_rows_kernel(const SumParams p) {
-    __shared__ float sh[8][32];
+    __shared__ double sh[8][32];
     const int g = threadIdx.x >> 5, l = threadIdx.x & 31;
     const int64_t c = (int64_t)blockIdx.x * 32 + l;
-    float t = 0.f;
+    double t = 0.0;   // the sums of a long batch keep fp32's accuracy
     if (c < p.cols) {
 #pragma unroll 8
-        for (int64_t r = g; r < p.n; r += 8) t += p.part[r * p.cols + c];
+        for (int64_t r = g; r < p.n; r += 8) t += (double)p.part[r * p.cols + c];
     }
     sh[g][l] = t;
     __syncthreads();
     if (g == 0 && c < p.cols) {
 #pragma unroll
         for (int i = 1; i < 8; ++i) t += sh[i][l];
-        if (c < p.split) p.out[(c % p.inner) * p.outer + c / p.inner] = t;
-        else p.out2[c - p.split] = t;
+        if (c < p.split) p.out[(c % p.inner) * p.outer + c / p.inner] = (float)t;
+        else p.out2[c - p.split] = (float)t;
     }
 }
 

@@ -13,17 +13,18 @@
 
 enum {
     GDR_FWD, GDR_BWD, GDR_DECODE, QK_NORM, QK_NORM_BWD, CONV, CONV_BWD, CONV_DECODE, GATED_NORM, GATED_NORM_BWD,
-    ADD_NORM, ADD_NORM_BWD, ENTRIES
+    ADD_NORM, ADD_NORM_BWD, SSM_FWD, SSM_BWD, SSM_DECODE, ENTRIES
 };
-#define MOST_TENSORS 16
+#define MOST_TENSORS 20
 
 typedef const kda_tensor_t* T;
 static void* entry_point[ENTRIES];
 static const char* const entry_name[ENTRIES] = {"kda_gdr_fwd", "kda_gdr_bwd", "kda_gdr_decode", "kda_qk_norm",
                                                 "kda_qk_norm_bwd", "kda_conv", "kda_conv_bwd", "kda_conv_decode",
-                                                "kda_gated_norm", "kda_gated_norm_bwd", "kda_add_norm", "kda_add_norm_bwd"};
-static const int entry_tensors[ENTRIES] = {9, 15, 9, 9, 13, 7, 11, 7, 4, 7, 5, 7};
-static const int entry_scalars[ENTRIES] = {1, 1, 1, 3, 3, 1, 1, 1, 3, 3, 2, 2};
+                                                "kda_gated_norm", "kda_gated_norm_bwd", "kda_add_norm", "kda_add_norm_bwd",
+                                                "kda_ssm_fwd", "kda_ssm_bwd", "kda_ssm_decode"};
+static const int entry_tensors[ENTRIES] = {9, 15, 9, 9, 13, 7, 11, 7, 4, 7, 5, 7, 11, 19, 11};
+static const int entry_scalars[ENTRIES] = {1, 1, 1, 3, 3, 1, 1, 1, 3, 3, 2, 2, 1, 1, 1};
 static PyObject* dtypes[4];   /* by kda_dtype_t */
 static PyObject *s_get_device, *s_data_ptr, *s_dim, *s_shape, *s_stride, *s_dtype, *s_nbytes;
 
@@ -184,6 +185,20 @@ static PyObject* call(PyObject* self, PyObject* const* a, Py_ssize_t na) {
         case ADD_NORM_BWD:
             st = ((kda_status_t(*)(T, T, float, float, T, T, T, T, T, void*, int64_t, void*))entry_point[e])(
                 t[0], t[1], (float)s[0], (float)s[1], t[2], t[3], t[4], t[5], t[6], ws, ws_bytes, stream);
+            break;
+        case SSM_FWD:
+            st = ((kda_status_t(*)(T, T, T, T, T, T, T, int32_t, T, T, T, T, void*, int64_t, void*))entry_point[e])(
+                t[0], t[1], t[2], t[3], t[4], t[5], t[6], (int32_t)s[0], t[7], t[8], t[9], t[10], ws, ws_bytes, stream);
+            break;
+        case SSM_BWD:
+            st = ((kda_status_t(*)(T, T, T, T, T, T, T, int32_t, T, T, T, T, T, T, T, T, T, T, T, T, void*, int64_t,
+                                   void*))entry_point[e])(t[0], t[1], t[2], t[3], t[4], t[5], t[6], (int32_t)s[0], t[7],
+                                                          t[8], t[9], t[10], t[11], t[12], t[13], t[14], t[15], t[16],
+                                                          t[17], t[18], ws, ws_bytes, stream);
+            break;
+        case SSM_DECODE:
+            st = ((kda_status_t(*)(T, T, T, T, T, T, T, int32_t, T, T, T, T, void*))entry_point[e])(
+                t[0], t[1], t[2], t[3], t[4], t[5], t[6], (int32_t)s[0], t[7], t[8], t[9], t[10], stream);
             break;
     }
     Py_END_ALLOW_THREADS

@@ -1,0 +1,533 @@
+// The token gradients of the selective state space scan, all chunks at once, on gfx950
+// (MI355X).  For a chunk with S the state entering it, dS the gradient of the one leaving it, d the
+// steps, L_ij = e^{G_i - G_j} (j <= i) and R = dy x^T:
+//   V = x dS^T, W = dy S^T,  K_ij = L_ij R_ij d_j,  E_ij = L_ij (C B^T)_ij,  M = E R
+//   dC = e^G W + K B,  dB = e^{G_last - G} d V + K^T C   (sums over a group's heads)
+//   dx = d (e^{G_last - G} B dS + E^T dy) + D dy
+//   u_j = e^{G_last - G_j} B_j . V_j,  w_i = e^{G_i} C_i . W_i,  q = e^{G_last} <S, dS>
+//   da_t = sum_{j < t <= i} M_ij d_j + sum_{i >= t} w_i + sum_{j < t} u_j d_j + q
+//   dd_t = A da_t + u_t + sum_{i >= t} M_it,  ddt = dd times the step's slope
+// da_t adds only what passes token t, never differences of longer sums: it keeps fp32's accuracy
+// where strong decays make it small.
+//
+// A work-group of eight waves takes a chunk and a group's heads, or some of them where that
+// leaves compute units idle, one head after the other; C B^T, and dB and dC in accumulators, stay.
+// Of the products with S and dS a wave takes sixteen state channels (with 64 of them half the
+// tokens): the states come from memory as the operands that the walk left, and only dS goes
+// through LDS, for dx.  The 64 x 64 matrices are ten tiles, dealt to the waves; they leave as
+// operand fragments for the second half of a head's work.
+//
+// Precision.  What reaches ddt and the sums enters in three bf16 parts (S and dS in V and W, 24
+// bits), what only reaches bf16 results in two (K, E, and dS in dx).
+#include "kda_block.h"
+#include "kda_ssm_device.h"
+
+namespace kda {
+
+namespace {
+
+constexpr int NT = 512;
+
+template <int P>
+struct GL {
+    static constexpr int B = 0, C = 16384, X = 32768;            // [64][256 bytes] tiles, swizzled
+    static constexpr int DY = P == 64 ? X : X + 16384;           // P = 64: beside x in its rows
+    static constexpr int DS = DY + 16384;                        // [S][64 columns, two parts], swizzled
+    static constexpr int KC = DS + 32768, KB = KC + 2 * GDR_TRI, EX = KB + 2 * GDR_TRI;   // fragments, two parts each
+    static constexpr int REC = EX + 2 * GDR_TRI;
+    static constexpr int RS = REC + SSM_REC, CS = RS + 4 * 256, DR = CS + 4 * 256;   // sums of M's tiles by row, by column
+    static constexpr int UP = DR + 256, YP = UP + 8 * 256, SD = YP + 8 * 256, BYTES = SD + 256;
+};
+static_assert(GL<128>::BYTES <= 163840, "LDS");
+
+// Byte of piece q (16 bytes) of row r, and of 8-byte half h of it.
+__device__ __forceinline__ bf16x8 two8(const char* tile, int row, int at) {   // elements at .. + 3 and 16 more on
+    const int q = at >> 3, b = 2 * (at & 7);
+    return join(*reinterpret_cast<const u32x2*>(tile + tile_off(row, q) + b),
+                *reinterpret_cast<const u32x2*>(tile + tile_off(row, q + 2) + b));
+}
+// Transposing reads of rows r0 + 0 .. 3 and r1 + 0 .. 3: column `at` + jj.
+__device__ __forceinline__ bf16x8 two_tr(const char* tile, int r0, int r1, int at, int jj) {
+    const int e = at + 4 * (jj & 3), q = e >> 3, b = 2 * (e & 7), r = jj >> 2;
+    return join(lds_tr(tile + tile_off(r0 + r, q) + b), lds_tr(tile + tile_off(r1 + r, q) + b));
+}
+// Index of fragment (m, kk) in the lists whose rows are the pair matrices' columns.
+__device__ __forceinline__ constexpr int upper_frag(int m, int kk) { return m < 2 ? 2 * m + kk : m + 2; }
+
+// Inclusive sum over the lanes before this one, in its group of 16 or in the wave.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_f32(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, ROWS, 0xf, true));
+}
+__device__ __forceinline__ float prefix16(float x) {
+    x += dpp_f32<0x111, 0xf>(x);
+    x += dpp_f32<0x112, 0xf>(x);
+    x += dpp_f32<0x114, 0xf>(x);
+    x += dpp_f32<0x118, 0xf>(x);
+    return x;
+}
+__device__ __forceinline__ float prefix_wave(float x) {
+    x = prefix16(x);
+    x += dpp_f32<0x142, 0xa>(x);
+    x += dpp_f32<0x143, 0xc>(x);
+    return x;
+}
+__device__ __forceinline__ float suffix16(float x, int lane) { return __shfl(prefix16(__shfl(x, lane ^ 15)), lane ^ 15); }
+__device__ __forceinline__ float suffix_wave(float x, int lane) { return __shfl(prefix_wave(__shfl(x, lane ^ 63)), lane ^ 63); }
+// x of the lane before this one (0 for the first of each group of 16, or of the wave).
+__device__ __forceinline__ float before16(float x) { return dpp_f32<0x111, 0xf>(x); }
+__device__ __forceinline__ float before_wave(float x, int lane) {
+    const float y = __shfl(x, lane - 1);
+    return lane == 0 ? 0.f : y;
+}
+__device__ __forceinline__ float lane_f32(float x, int lane) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
+}
+
+}  // namespace
+
+template <int S, int P>
+__global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
+    typedef GL<P> L;
+    constexpr int KT = S / 32, KP = P / 32, MW = S == 128 ? 4 : 2;   // k steps; row tiles of a wave's state channels
+    constexpr int PX = P / 64;                                       // 16-byte pieces of x that a thread brings
+    __shared__ __attribute__((aligned(1024))) char smem[L::BYTES];
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, jj = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int R = p.H / p.G, hs = (R + p.sets - 1) / p.sets;
+    const int set = (int)(blockIdx.x % p.sets), group = (int)(blockIdx.x / p.sets % p.G);
+    const int64_t slot = blockIdx.x / p.sets / p.G;
+    const SsmChunk ch = ssm_chunk(p, slot);
+    if (ch.rows == 0) return;
+    const int h_from = group * R + set * hs, h_to = group * R + ((set + 1) * hs < R ? (set + 1) * hs : R);
+    const char *tb = smem + L::B, *tc = smem + L::C, *tx = smem + L::X, *ty = smem + L::DY;
+    constexpr int YO = P == 64 ? 64 : 0;   // dy's first element in its rows
+    const float* rec = reinterpret_cast<const float*>(smem + L::REC);
+    float *sRS = reinterpret_cast<float*>(smem + L::RS), *sCS = reinterpret_cast<float*>(smem + L::CS),
+          *sDR = reinterpret_cast<float*>(smem + L::DR), *sU = reinterpret_cast<float*>(smem + L::UP),
+          *sY = reinterpret_cast<float*>(smem + L::YP), *sS = reinterpret_cast<float*>(smem + L::SD);
+    const int t = S == 128 ? wave : wave & 3, m0 = S == 128 ? 0 : 2 * (wave >> 2);   // state tile, first row tile
+
+    {   // B and C
+        const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+        auto tile = [&](const Rows& w, uint32_t where) {
+            const __amdgpu_buffer_rsrc_t rs = chunk_rsrc(w.p + ch.row * w.sb + ch.tok * w.st + group * w.sh, w.st, ch.rows, S);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int r = 4 * (wave + 8 * u) + g, piece = jj ^ tsw(r);
+                const int off = (int)(r * w.st * 2) + 16 * piece;
+                dma_piece(rs, where + (wave + 8 * u) * 1024, S == 128 || piece < 8 ? off : 0x7ffffff0);
+            }
+        };
+        tile(p.B, lds + L::B);
+        tile(p.C, lds + L::C);
+    }
+    // what no tile of the pair matrices covers in the fragments
+    if (tid < 64) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            *reinterpret_cast<u32x2*>(smem + L::KC + n * GDR_TRI + tri_frag(0, 0) * GDR_FRAG + 16 * lane + 8) = u32x2{0, 0};
+            *reinterpret_cast<u32x2*>(smem + L::KC + n * GDR_TRI + tri_frag(2, 1) * GDR_FRAG + 16 * lane + 8) = u32x2{0, 0};
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                char* to = smem + (x ? L::EX : L::KB) + n * GDR_TRI + 16 * lane;
+                *reinterpret_cast<u32x2*>(to + upper_frag(1, 0) * GDR_FRAG) = u32x2{0, 0};
+                *reinterpret_cast<u32x2*>(to + upper_frag(3, 1) * GDR_FRAG) = u32x2{0, 0};
+            }
+        }
+    }
+    // A head's inputs, asked for ahead
+    u32x4 nx[PX], ny[PX], nrec;
+    f32x4 ns[KP][2], nds[KP][2];
+    const int lr = P == 64 ? tid >> 3 : tid >> 4, lp = P == 64 ? tid & 7 : tid & 15;   // row and piece of this thread
+    auto ask = [&](int h) {
+#pragma unroll
+        for (int u = 0; u < PX; ++u) {
+            const int r = lr + 32 * u;
+            nx[u] = ny[u] = u32x4{0, 0, 0, 0};
+            if (r < ch.rows) {
+                nx[u] = *reinterpret_cast<const u32x4*>(p.x.p + ch.row * p.x.sb + (ch.tok + r) * p.x.st + h * p.x.sh + 8 * lp);
+                ny[u] = *reinterpret_cast<const u32x4*>(p.dO.p + ch.row * p.dO.sb + (ch.tok + r) * p.dO.st + h * p.dO.sh + 8 * lp);
+            }
+        }
+        const int64_t unit = slot * p.H + h;
+        if (tid < SSM_REC / 16) nrec = *reinterpret_cast<const u32x4*>(p.rec + unit * SSM_REC + 16 * tid);
+#pragma unroll
+        for (int pp = 0; pp < KP; ++pp) {
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) {
+                const int64_t at = unit * S * P + pp * (S * 32) + t * 512 + 8 * lane + 4 * ct;
+                ns[pp][ct] = *reinterpret_cast<const f32x4*>(p.St + at);
+                nds[pp][ct] = *reinterpret_cast<const f32x4*>(p.dSt + at);
+            }
+        }
+    };
+    if (h_from < h_to) ask(h_from);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+
+    // tiles (I, J) of the pair matrices: waves 0 .. 5 one below the diagonal, 6 and 7 two on it
+    const int nt = wave < 6 ? 1 : 2;
+    const int tI = wave < 6 ? (wave < 1 ? 1 : wave < 3 ? 2 : 3) : 2 * (wave - 6);
+    const int tJ = wave < 6 ? (wave < 1 ? 0 : wave < 3 ? wave - 1 : wave - 3) : tI;
+    f32x4 cb[2];   // C B^T, rows 16 I + 4 g + r, column 16 J + jj
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        cb[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (x >= nt) continue;
+#pragma unroll
+        for (int kk = 0; kk < KT; ++kk)
+            cb[x] = mfma_bf(row_frag(tc, tI + x, kk, g, jj), row_frag(tb, tJ + x, kk, g, jj), cb[x]);
+    }
+    bf16x8 bcol[2], ccol[2];   // channel of tile t, tokens of k step kk
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+        bcol[kk] = col_frag(tb, t, kk, g, jj);
+        ccol[kk] = col_frag(tc, t, kk, g, jj);
+    }
+    f32x4 dB[MW], dC[MW];
+#pragma unroll
+    for (int m = 0; m < MW; ++m) dB[m] = dC[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto half_of = [](bf16x8 v, int h) {
+        const u32x4 w = __builtin_bit_cast(u32x4, v);
+        return widen(u32x2{w[2 * h], w[2 * h + 1]});
+    };
+
+    for (int h = h_from; h < h_to; ++h) {
+        // the head's inputs into LDS
+#pragma unroll
+        for (int u = 0; u < PX; ++u) {
+            *reinterpret_cast<u32x4*>(smem + L::X + tile_off(lr + 32 * u, lp)) = nx[u];
+            *reinterpret_cast<u32x4*>(smem + L::DY + tile_off(lr + 32 * u, lp + YO / 8)) = ny[u];
+        }
+        if (tid < SSM_REC / 16) *reinterpret_cast<u32x4*>(smem + L::REC + 16 * tid) = nrec;
+        f32x4 s[KP][2], ds[KP][2];
+#pragma unroll
+        for (int pp = 0; pp < KP; ++pp) {
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) {
+                s[pp][ct] = ns[pp][ct];
+                ds[pp][ct] = nds[pp][ct];
+            }
+        }
+        __syncthreads();
+        if (h + 1 < h_to) ask(h + 1);
+
+        // ---- the pair matrices' tiles
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (x >= nt) continue;
+            const int I = tI + x, J = tJ + x;
+            f32x4 r = {0.f, 0.f, 0.f, 0.f}, rt = r;   // dy x^T, and transposed
+#pragma unroll
+            for (int pp = 0; pp < KP; ++pp) {
+                const bf16x8 yf = two8(ty, 16 * I + jj, YO + 32 * pp + 4 * g), xf = two8(tx, 16 * J + jj, 32 * pp + 4 * g);
+                r = mfma_bf(yf, xf, r);
+                rt = mfma_bf(xf, yf, rt);
+            }
+            f32x4 l, lt;   // decays
+            const float dj = rec[SSM_DT + 16 * J + jj];
+            const f32x4 djt = num4(rec, SSM_DT, J, g);
+            if (I == J) {
+                const float hi = rec[SSM_GH + 16 * I + jj], lo = rec[SSM_GL + 16 * I + jj];
+                const f32x4 h4 = num4(rec, SSM_GH, I, g), l4 = num4(rec, SSM_GL, I, g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    l[e] = jj <= 4 * g + e ? fexp2((h4[e] - hi) + (l4[e] - lo)) : 0.f;
+                    lt[e] = 4 * g + e <= jj ? fexp2((hi - h4[e]) + (lo - l4[e])) : 0.f;
+                }
+            } else {
+                float mid = 1.f;
+                if (I > J + 1) mid = rec[SSM_RI + 16 * J + 31];
+                if (I > J + 2) mid *= rec[SSM_RI + 16 * J + 47];
+                l = num4(rec, SSM_RI, I, g) * (rec[SSM_KA + 16 * J + jj] * mid);
+                lt = num4(rec, SSM_KA, J, g) * (rec[SSM_RI + 16 * I + jj] * mid);
+            }
+            f32x4 e = cb[x], m;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // above the diagonal nothing counts, not even NaN
+                const bool on = I > J || jj <= 4 * g + i, ont = I > J || 4 * g + i <= jj;
+                e[i] = on ? e[i] * l[i] : 0.f;
+                m[i] = on ? e[i] * r[i] : 0.f;
+                lt[i] = ont ? lt[i] * rt[i] * djt[i] : 0.f;
+                l[i] = on ? l[i] * r[i] * dj : 0.f;
+            }
+            auto put = [&](int list, int frag, int half, const f32x4& a) {
+                char* to = smem + list + frag * GDR_FRAG + 16 * lane + 8 * half;
+                const uint32_t h0 = pack_bf2(a[0], a[1]), h1 = pack_bf2(a[2], a[3]);
+                *reinterpret_cast<u32x2*>(to) = u32x2{h0, h1};
+                *reinterpret_cast<u32x2*>(to + GDR_TRI) =
+                    u32x2{pack_bf2(a[0] - bf_lo(h0), a[1] - bf_hi(h0)), pack_bf2(a[2] - bf_lo(h1), a[3] - bf_hi(h1))};
+            };
+            put(L::KC, tri_frag(I, J >> 1), J & 1, lt);
+            put(L::KB, upper_frag(J, I >> 1), I & 1, l);
+            put(L::EX, upper_frag(J, I >> 1), I & 1, e);
+            // M's sums: of a column over the tile's rows, of a row with each column's step
+            const float cs = sum_groups((m[0] + m[1]) + (m[2] + m[3]));
+            if (g == 0) sCS[64 * I + 16 * J + jj] = cs;
+            f32x4 md = m * dj;
+            if (I > J) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) md[i] = sum16(md[i]);
+                if (jj == 0) *reinterpret_cast<f32x4*>(sRS + 64 * J + 16 * I + 4 * g) = md;
+            } else {   // sum over j < t <= i of the tile, and the diagonal of dy x^T
+                md[2] += md[3];
+                md[1] += md[2];
+                md[0] += md[1];
+                float above = 0.f;
+#pragma unroll
+                for (int o = 1; o < 4; ++o) {
+                    const float v = __shfl(md[0], lane + 16 * o);
+                    above += g + o < 4 ? v : 0.f;
+                }
+                float diag = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (jj == 4 * g + i) diag = r[i];
+                    md[i] = sum16(jj < 4 * g + i ? md[i] + above : 0.f);
+                }
+                if (jj == 0) *reinterpret_cast<f32x4*>(sDR + 16 * I + 4 * g) = md;
+                diag = sum64(diag);
+                if (lane == 0) sS[8 + I] = diag;
+            }
+        }
+        // ---- V and W of the wave's state channels, dS's parts into LDS
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        Split<3> sp[KP], dsp[KP];
+        float dot = 0.f;
+#pragma unroll
+        for (int pp = 0; pp < KP; ++pp) {
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dot = fmaf(s[pp][ct][i], ds[pp][ct][i], dot);
+            }
+            sp[pp] = split_acc<3>(s[pp][0], s[pp][1]);
+            dsp[pp] = split_acc<3>(ds[pp][0], ds[pp][1]);
+        }
+        dot = sum64(dot);
+        if (lane == 0) sS[wave] = S == 128 || wave < 4 ? dot : 0.f;
+        const int nrow = state_row(t, jj >> 2, jj & 3);
+        auto put_ds = [&](int half) {   // columns 64 half .. of dS in two parts
+            if (S == 64 && wave >= 4) return;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const u32x4 w = __builtin_bit_cast(u32x4, dsp[2 * half + q].s[n]);
+                    const int at = 64 * n + 32 * q + 4 * g;
+                    char* to = smem + L::DS + 2 * (at & 7);
+                    *reinterpret_cast<u32x2*>(to + tile_off(nrow, at >> 3)) = u32x2{w[0], w[1]};
+                    *reinterpret_cast<u32x2*>(to + tile_off(nrow, (at >> 3) + 2)) = u32x2{w[2], w[3]};
+                }
+            }
+        };
+        put_ds(0);
+#pragma unroll
+        for (int mi = 0; mi < MW; ++mi) {
+            const int m = m0 + mi;
+            f32x4 v = zero, w = zero;
+#pragma unroll
+            for (int pp = 0; pp < KP; ++pp) {
+                const bf16x8 xf = two8(tx, 16 * m + jj, 32 * pp + 4 * g), yf = two8(ty, 16 * m + jj, YO + 32 * pp + 4 * g);
+#pragma unroll
+                for (int n = 2; n >= 0; --n) {
+                    v = mfma_bf(xf, dsp[pp].s[n], v);
+                    w = mfma_bf(yf, sp[pp].s[n], w);
+                }
+            }
+            const f32x4 ga = num4(rec, SSM_GA, m, g), eg = num4(rec, SSM_EG, m, g);
+            f32x4 u = v * half_of(bcol[m >> 1], m & 1), y = w * half_of(ccol[m >> 1], m & 1);
+            dB[mi] += (ga * num4(rec, SSM_DT, m, g)) * v;
+            dC[mi] += eg * w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                u[i] = sum16(u[i]);
+                y[i] = sum16(y[i]);
+            }
+            if (jj == 0) {
+                *reinterpret_cast<f32x4*>(sU + 64 * t + 16 * m + 4 * g) = u;
+                *reinterpret_cast<f32x4*>(sY + 64 * t + 16 * m + 4 * g) = y;
+            }
+        }
+        __syncthreads();
+
+        // ---- dB and dC from the pair matrices
+#pragma unroll
+        for (int n = 1; n >= 0; --n) {
+#pragma unroll
+            for (int mi = 0; mi < MW; ++mi) {
+                const int m = m0 + mi;
+                const char *kc = smem + L::KC + n * GDR_TRI + 16 * lane, *kb = smem + L::KB + n * GDR_TRI + 16 * lane;
+                dC[mi] = mfma_bf(lds_bf8(kc + (m < 2 ? m : 2 * m - 2) * GDR_FRAG), bcol[0], dC[mi]);
+                if (m >= 2) dC[mi] = mfma_bf(lds_bf8(kc + (2 * m - 1) * GDR_FRAG), bcol[1], dC[mi]);
+                if (m < 2) dB[mi] = mfma_bf(lds_bf8(kb + 2 * m * GDR_FRAG), ccol[0], dB[mi]);
+                dB[mi] = mfma_bf(lds_bf8(kb + (m < 2 ? 2 * m + 1 : m + 2) * GDR_FRAG), ccol[1], dB[mi]);
+            }
+        }
+        // ---- dx, transposed: a lane holds four channels of one token
+        const float skip = p.D ? p.D[h] : 0.f;
+#pragma unroll
+        for (int half = 0; half < PX; ++half) {
+            if (half > 0) {
+                __syncthreads();
+                put_ds(half);
+                __syncthreads();
+            }
+            const int pt = wave & 3;
+#pragma unroll
+            for (int mi = 0; mi < 2; ++mi) {
+                const int m = 2 * (wave >> 2) + mi;
+                f32x4 a = zero, b = zero;
+#pragma unroll
+                for (int kk = 0; kk < KT; ++kk) {
+                    const bf16x8 bf = row_frag(tb, m, kk, g, jj);
+#pragma unroll
+                    for (int n = 1; n >= 0; --n)
+                        a = mfma_bf(two_tr(smem + L::DS, 32 * kk + 8 * g, 32 * kk + 8 * g + 4, 64 * n + 16 * pt, jj), bf, a);
+                }
+                const int col = 64 * half + 16 * pt;
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    if (kk == 0 && m >= 2) continue;
+                    const bf16x8 yf = two_tr(ty, 32 * kk + 4 * g, 32 * kk + 16 + 4 * g, YO + col, jj);
+                    const char* ex = smem + L::EX + 16 * lane + (m < 2 ? 2 * m + kk : m + 2) * GDR_FRAG;
+                    b = mfma_bf(yf, lds_bf8(ex + GDR_TRI), b);
+                    b = mfma_bf(yf, lds_bf8(ex), b);
+                }
+                const int tok = 16 * m + jj, at = YO + col + 4 * g;
+                const f32x4 dy = widen(*reinterpret_cast<const u32x2*>(ty + tile_off(tok, at >> 3) + 2 * (at & 7)));
+                a = rec[SSM_DT + tok] * (rec[SSM_GA + tok] * a + b) + skip * dy;
+                if (tok < ch.rows)
+                    *reinterpret_cast<u32x2*>(p.dx + ((ch.row * p.T + ch.tok + tok) * p.H + h) * P + col + 4 * g) =
+                        u32x2{pack_bf2(a[0], a[1]), pack_bf2(a[2], a[3])};
+            }
+        }
+        // ---- the numbers of each token, a wave for each head in turn
+        if (wave == (h & 7)) {
+            const int I = lane >> 4;
+            const float d = rec[SSM_DT + lane], A = p.A[h];
+            float rs = 0.f, cs = 0.f, u = 0.f, y = 0.f, q = 0.f;
+#pragma unroll
+            for (int j = 0; j < 3; ++j) rs += j < I ? sRS[64 * j + lane] : 0.f;
+#pragma unroll
+            for (int i = 1; i < 4; ++i) cs += i > I ? sCS[64 * i + lane] : 0.f;
+#pragma unroll
+            for (int w = 0; w < S / 16; ++w) {
+                u += sU[64 * w + lane];
+                y += sY[64 * w + lane];
+            }
+#pragma unroll
+            for (int w = 0; w < 8; ++w) q += sS[w];
+            const float t0 = sum16(I > 0 ? sRS[lane] : 0.f), t1 = sum16(I > 1 ? sRS[64 + lane] : 0.f);
+            const float t20 = lane_f32(t0, 32), t30 = lane_f32(t0, 48), t31 = lane_f32(t1, 48);
+            u *= rec[SSM_GA + lane];
+            y *= rec[SSM_EG + lane];
+            float da = suffix16(rs, lane) + before16(prefix16(cs * d)) + sDR[lane] + (I == 1 ? t20 + t30 : I == 2 ? t30 + t31 : 0.f);
+            da += suffix_wave(y, lane) + before_wave(prefix_wave(u * d), lane) + rec[SSM_EG + 63] * q;
+            const float dd = A * da + (u + cs + sCS[64 * I + lane]);
+            float slope = 1.f, own = 0.f, sa = 0.f;
+            const int64_t at = ch.row * p.T + ch.tok + lane;
+            if (lane < ch.rows) {
+                if (p.softplus)
+                    slope = sigmoid(ssm_raw(p.dt, p.dt_f32, ch.row * p.dtb + (ch.tok + lane) * p.dtt + h, p.bias, h));
+                own = dd * slope;
+                sa = d * da;
+                p.ddt[at * p.H + h] = own;
+            }
+            own = sum64(own);
+            sa = sum64(sa);
+            if (lane < 3)
+                p.part[(slot * 3 + lane) * p.H + h] =
+                    lane == 0 ? sa : lane == 1 ? (sS[8] + sS[9]) + (sS[10] + sS[11]) : own;
+        }
+        __syncthreads();   // everything in LDS but B and C is read
+    }
+
+    // ---- dB and dC
+    if (p.sets > 1) {
+        const int64_t base = ((int64_t)set * p.nslots + slot) * 64;
+#pragma unroll
+        for (int mi = 0; mi < MW; ++mi) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int tok = 16 * (m0 + mi) + 4 * g + i;
+                const int64_t at = ((base + tok) * p.G + group) * S + state_row(t, jj >> 2, jj & 3);
+                p.dBp[at] = dB[mi][i];
+                p.dCp[at] = dC[mi][i];
+            }
+        }
+        return;
+    }
+    __syncthreads();
+    const int n = state_row(t, jj >> 2, jj & 3);
+#pragma unroll
+    for (int mi = 0; mi < MW; ++mi) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = tile_off(16 * (m0 + mi) + 4 * g + i, n >> 3) + 2 * (n & 7);
+            *reinterpret_cast<uint16_t*>(smem + L::B + at) = (uint16_t)pack_bf2(dB[mi][i], 0.f);
+            *reinterpret_cast<uint16_t*>(smem + L::C + at) = (uint16_t)pack_bf2(dC[mi][i], 0.f);
+        }
+    }
+    __syncthreads();
+    for (int e = tid; e < 64 * S / 8; e += NT) {
+        const int r = e / (S / 8), q = e % (S / 8);
+        if (r >= ch.rows) continue;
+        const int64_t at = ((ch.row * p.T + ch.tok + r) * p.G + group) * S + 8 * q;
+        *reinterpret_cast<u32x4*>(p.dB + at) = *reinterpret_cast<const u32x4*>(tb + tile_off(r, q));
+        *reinterpret_cast<u32x4*>(p.dC + at) = *reinterpret_cast<const u32x4*>(tc + tile_off(r, q));
+    }
+}
+
+// dB and dC of a chunk as sums over its sets of heads, in order; a thread takes eight channels.
+__global__ void __launch_bounds__(256) kda_ssm_join_kernel(const SsmParams p) {
+    const SsmChunk ch = ssm_chunk(p, blockIdx.x);
+    const int row = p.G * p.S;   // elements of a token
+    for (int e = threadIdx.x * 8; e < ch.rows * row; e += 256 * 8) {
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            const float* from = (which ? p.dCp : p.dBp) + (int64_t)blockIdx.x * 64 * row + e;
+            f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
+            for (int s = 0; s < p.sets; ++s, from += p.nslots * 64 * row) {
+                a += *reinterpret_cast<const f32x4*>(from);
+                b += *reinterpret_cast<const f32x4*>(from + 4);
+            }
+            *reinterpret_cast<u32x4*>((which ? p.dC : p.dB) + (ch.row * p.T + ch.tok) * row + e) =
+                u32x4{pack_bf2(a[0], a[1]), pack_bf2(a[2], a[3]), pack_bf2(b[0], b[1]), pack_bf2(b[2], b[3])};
+        }
+    }
+}
+
+// The heads' sums over the chunks: dA, dD, dbias.  A work-group takes one of them and 32 heads, eight
+// threads each every eighth chunk, then in order.
+__global__ void __launch_bounds__(256) kda_ssm_sums_kernel(const SsmParams p) {
+    __shared__ double sh[8][32];
+    const int g = threadIdx.x >> 5, l = threadIdx.x & 31, which = blockIdx.x % 3, h = (int)(blockIdx.x / 3) * 32 + l;
+    float* out = which == 0 ? p.dA : which == 1 ? p.dD : p.dbias;
+    double x = 0.0;
+    if (out && h < p.H)
+        for (int64_t s = g; s < p.nslots; s += 8)
+            if (ssm_chunk(p, s).rows > 0) x += (double)p.part[(s * 3 + which) * p.H + h];
+    sh[g][l] = x;
+    __syncthreads();
+    if (g > 0 || !out || h >= p.H) return;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) x += sh[i][l];
+    out[h] = (float)x;
+}
+
+hipError_t launch_ssm_grads(const SsmParams& p, hipStream_t stream) {
+    const int64_t blocks = p.nslots * p.G * p.sets;
+    if (blocks > 0) {
+        auto* f = p.S == 128 ? (p.P == 128 ? kda_ssm_grads_kernel<128, 128> : kda_ssm_grads_kernel<128, 64>)
+                             : (p.P == 128 ? kda_ssm_grads_kernel<64, 128> : kda_ssm_grads_kernel<64, 64>);
+        hipLaunchKernelGGL(f, dim3((unsigned)blocks), dim3(NT), 0, stream, p);
+        if (p.sets > 1) hipLaunchKernelGGL(kda_ssm_join_kernel, dim3((unsigned)p.nslots), dim3(256), 0, stream, p);
+    }
+    hipLaunchKernelGGL(kda_ssm_sums_kernel, dim3((unsigned)(3 * ((p.H + 31) / 32))), dim3(256), 0, stream, p);
+    return hipGetLastError();
+}
+
+}  // namespace kda

@@ -677,6 +677,73 @@ kda_status_t kda_add_norm_bwd(const kda_tensor_t* sum, const kda_tensor_t* weigh
                               const kda_tensor_t* dresidual, const kda_tensor_t* dweight, void* workspace,
                               int64_t workspace_size, void* stream);
 
+/*
+ * kda_ssm_fwd -- the selective state space scan, the sibling of the delta rule without its
+ * correction: for every sequence and head, with the step d_t,
+ *
+ *     d_t = log(1 + e^{dt_t + dt_bias})   (softplus 1; 0: dt_t + dt_bias)
+ *     S_t = e^{d_t A} S_{t-1} + d_t B_t x_t^T,   y_t = S_t^T C_t + D x_t
+ *
+ *   x            [B, T, H, P]  bf16, P 64 or 128
+ *   dt           [B, T, H]     bf16 or fp32, heads contiguous, other strides any that are not negative
+ *   A            [H]           fp32 (negative; d A below -200 counts as -200)
+ *   B, C         [B, T, G, S]  bf16, S 64 or 128; G divides H, head h reads group h / (H / G)
+ *   D, dt_bias   [H]           fp32, or NULL (zeros)
+ *   cu_seqlens   as for kda_fwd
+ *   states       [N, H, S, P]  fp32, or NULL (zeros; not written); final_state may be initial_state
+ *   out          [B, T, H, P]  bf16
+ * x, B and C (and d_out) may be views under kda_gdr_fwd's rules: channels contiguous, 16-byte
+ * aligned data, strides non-negative multiples of 8 elements, tokens at least a row and at most
+ * 2^23 elements apart.  Every other tensor is contiguous.  Other head and state dimensions, more
+ * than 2^31 - 1 tokens, or grids above 2^22 work-groups ((chunk slot, head) pairs among them)
+ * return KDA_ERR_UNSUPPORTED.
+ * Precision: sums are fp32; what enters the state is formed from operands at fp32's 24 bits, what
+ * only adds to y at 16; y is rounded to bf16 once.  A token that holds NaN or infinity may
+ * reach every token of its 64-token chunk and later ones of its sequence, and through x only its own head.
+ * workspace: kda_ssm_fwd_workspace_size(B * T, N, H, G, P, S) bytes, 256-byte aligned, as for
+ * kda_gdr_fwd; NULL allocates it in stream order.
+ */
+int64_t kda_ssm_fwd_workspace_size(int64_t total_tokens, int64_t num_sequences, int64_t num_heads, int64_t num_groups,
+                                   int64_t head_dim, int64_t state_dim);
+kda_status_t kda_ssm_fwd(const kda_tensor_t* x, const kda_tensor_t* dt, const kda_tensor_t* A, const kda_tensor_t* B,
+                         const kda_tensor_t* C, const kda_tensor_t* D, const kda_tensor_t* dt_bias, int32_t softplus,
+                         const kda_tensor_t* cu_seqlens, const kda_tensor_t* initial_state, const kda_tensor_t* out,
+                         const kda_tensor_t* final_state, void* workspace, int64_t workspace_size, void* stream);
+
+/*
+ * kda_ssm_bwd -- gradients of kda_ssm_fwd, given those of the output (d_out, may be a view) and
+ * of the final state (d_final_state, NULL for zero).
+ *   dx                [B, T, H, P]  bf16
+ *   ddt               [B, T, H]     fp32
+ *   dB, dC            [B, T, G, S]  bf16 (summed over the heads of a group)
+ *   dA, dD, ddt_bias  [H]           fp32, summed over all tokens in a fixed order; dD and ddt_bias
+ *                                   may be NULL, and without D or dt_bias have to be
+ *   d_initial_state   [N, H, S, P]  fp32, or NULL (not computed)
+ * An empty sequence passes d_final_state through to its d_initial_state; ddt rows of tokens in no
+ * sequence are not written.  workspace: kda_ssm_bwd_workspace_size() bytes, as above: the states
+ * entering and the gradients leaving every chunk, 4 S P bytes each for every (chunk slot, head).
+ */
+int64_t kda_ssm_bwd_workspace_size(int64_t total_tokens, int64_t num_sequences, int64_t num_heads, int64_t num_groups,
+                                   int64_t head_dim, int64_t state_dim);
+kda_status_t kda_ssm_bwd(const kda_tensor_t* x, const kda_tensor_t* dt, const kda_tensor_t* A, const kda_tensor_t* B,
+                         const kda_tensor_t* C, const kda_tensor_t* D, const kda_tensor_t* dt_bias, int32_t softplus,
+                         const kda_tensor_t* cu_seqlens, const kda_tensor_t* initial_state, const kda_tensor_t* d_out,
+                         const kda_tensor_t* d_final_state, const kda_tensor_t* dx, const kda_tensor_t* ddt,
+                         const kda_tensor_t* dA, const kda_tensor_t* dB, const kda_tensor_t* dC, const kda_tensor_t* dD,
+                         const kda_tensor_t* ddt_bias, const kda_tensor_t* d_initial_state, void* workspace,
+                         int64_t workspace_size, void* stream);
+
+/*
+ * kda_ssm_decode -- one token for each of N rows: x [N, H, P], dt [N, H], B and C [N, G, S] (views,
+ * any row stride), out [N, H, P].  States and state_indices as for kda_gdr_decode: [N, H, S, P],
+ * or pools [slots, H, S, P] that state_indices [N] int32 name slots of.  All arithmetic is fp32;
+ * y is rounded to bf16 once.  N * H above 2^20 returns KDA_ERR_UNSUPPORTED.
+ */
+kda_status_t kda_ssm_decode(const kda_tensor_t* x, const kda_tensor_t* dt, const kda_tensor_t* A, const kda_tensor_t* B,
+                            const kda_tensor_t* C, const kda_tensor_t* D, const kda_tensor_t* dt_bias, int32_t softplus,
+                            const kda_tensor_t* state_in, const kda_tensor_t* state_out, const kda_tensor_t* state_indices,
+                            const kda_tensor_t* out, void* stream);
+
 /* Human-readable name of a status code (static storage; never NULL). */
 const char* kda_status_string(kda_status_t status);
 

@@ -150,10 +150,12 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
                 ny[u] = *reinterpret_cast<const u32x4*>(p.dO.p + ch.row * p.dO.sb + (ch.tok + r) * p.dO.st + h * p.dO.sh + 8 * lp);
             }
         }
+        if (tid < SSM_REC / 16) nrec = *reinterpret_cast<const u32x4*>(p.rec + (slot * p.H + h) * SSM_REC + 16 * tid);
+    };
+    auto ask_states = [&](int h, int from, int to) {   // columns 32 from .. 32 to - 1
         const int64_t unit = slot * p.H + h;
-        if (tid < SSM_REC / 16) nrec = *reinterpret_cast<const u32x4*>(p.rec + unit * SSM_REC + 16 * tid);
 #pragma unroll
-        for (int pp = 0; pp < KP; ++pp) {
+        for (int pp = from; pp < to; ++pp) {
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) {
                 const int64_t at = unit * S * P + pp * (S * 32) + t * 512 + 8 * lane + 4 * ct;
@@ -162,7 +164,10 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
             }
         }
     };
-    if (h_from < h_to) ask(h_from);
+    if (h_from < h_to) {
+        ask(h_from);
+        ask_states(h_from, 0, 2);
+    }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
 
@@ -179,18 +184,12 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
         for (int kk = 0; kk < KT; ++kk)
             cb[x] = mfma_bf(row_frag(tc, tI + x, kk, g, jj), row_frag(tb, tJ + x, kk, g, jj), cb[x]);
     }
-    bf16x8 bcol[2], ccol[2];   // channel of tile t, tokens of k step kk
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-        bcol[kk] = col_frag(tb, t, kk, g, jj);
-        ccol[kk] = col_frag(tc, t, kk, g, jj);
-    }
     f32x4 dB[MW], dC[MW];
 #pragma unroll
     for (int m = 0; m < MW; ++m) dB[m] = dC[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto half_of = [](bf16x8 v, int h) {
-        const u32x4 w = __builtin_bit_cast(u32x4, v);
-        return widen(u32x2{w[2 * h], w[2 * h + 1]});
+    // the lane's channel of the wave's state tile, tokens 16 m + 4 g + r
+    auto column = [&](const char* tile, int m, int g, int jj) {
+        return widen(lds_tr(tile + tile_off(16 * m + 4 * g + (jj >> 2), 4 * (t >> 1) + (jj & 3)) + 8 * (t & 1)));
     };
 
     for (int h = h_from; h < h_to; ++h) {
@@ -201,19 +200,12 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
             *reinterpret_cast<u32x4*>(smem + L::DY + tile_off(lr + 32 * u, lp + YO / 8)) = ny[u];
         }
         if (tid < SSM_REC / 16) *reinterpret_cast<u32x4*>(smem + L::REC + 16 * tid) = nrec;
-        f32x4 s[KP][2], ds[KP][2];
-#pragma unroll
-        for (int pp = 0; pp < KP; ++pp) {
-#pragma unroll
-            for (int ct = 0; ct < 2; ++ct) {
-                s[pp][ct] = ns[pp][ct];
-                ds[pp][ct] = nds[pp][ct];
-            }
-        }
         __syncthreads();
-        if (h + 1 < h_to) ask(h + 1);
+        ask_states(h, 2, KP);
 
         // ---- the pair matrices' tiles
+        {
+        const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;   // addresses formed anew: kept through the loop they would spill
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             if (x >= nt) continue;
@@ -292,92 +284,131 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
                 if (lane == 0) sS[8 + I] = diag;
             }
         }
-        // ---- V and W of the wave's state channels, dS's parts into LDS
-        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-        Split<3> sp[KP], dsp[KP];
-        float dot = 0.f;
-#pragma unroll
-        for (int pp = 0; pp < KP; ++pp) {
-#pragma unroll
-            for (int ct = 0; ct < 2; ++ct) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dot = fmaf(s[pp][ct][i], ds[pp][ct][i], dot);
-            }
-            sp[pp] = split_acc<3>(s[pp][0], s[pp][1]);
-            dsp[pp] = split_acc<3>(ds[pp][0], ds[pp][1]);
         }
-        dot = sum64(dot);
-        if (lane == 0) sS[wave] = S == 128 || wave < 4 ? dot : 0.f;
-        const int nrow = state_row(t, jj >> 2, jj & 3);
-        auto put_ds = [&](int half) {   // columns 64 half .. of dS in two parts
-            if (S == 64 && wave >= 4) return;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const u32x4 w = __builtin_bit_cast(u32x4, dsp[2 * half + q].s[n]);
-                    const int at = 64 * n + 32 * q + 4 * g;
-                    char* to = smem + L::DS + 2 * (at & 7);
-                    *reinterpret_cast<u32x2*>(to + tile_off(nrow, at >> 3)) = u32x2{w[0], w[1]};
-                    *reinterpret_cast<u32x2*>(to + tile_off(nrow, (at >> 3) + 2)) = u32x2{w[2], w[3]};
-                }
-            }
+        __builtin_amdgcn_sched_barrier(0);
+        // ---- V and W of the wave's state channels, 32 columns at a time, and dS's parts into LDS
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        u32x4 later[PX > 1 ? 2 : 1][2];   // two parts of dS's columns 64 ..
+        auto put_ds = [&](int q, int n, u32x4 w, int row, int g) {   // part n of 32 columns
+            const int at = 64 * n + 32 * q + 4 * g;
+            char* to = smem + L::DS + 2 * (at & 7);
+            *reinterpret_cast<u32x2*>(to + tile_off(row, at >> 3)) = u32x2{w[0], w[1]};
+            *reinterpret_cast<u32x2*>(to + tile_off(row, (at >> 3) + 2)) = u32x2{w[2], w[3]};
         };
-        put_ds(0);
+        {
+            const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
+            const int nrow = state_row(t, jj >> 2, jj & 3);
+            f32x4 v[MW], w[MW];
 #pragma unroll
-        for (int mi = 0; mi < MW; ++mi) {
-            const int m = m0 + mi;
-            f32x4 v = zero, w = zero;
+            for (int mi = 0; mi < MW; ++mi) v[mi] = w[mi] = zero;
+            float dot = 0.f;
 #pragma unroll
             for (int pp = 0; pp < KP; ++pp) {
-                const bf16x8 xf = two8(tx, 16 * m + jj, 32 * pp + 4 * g), yf = two8(ty, 16 * m + jj, YO + 32 * pp + 4 * g);
 #pragma unroll
-                for (int n = 2; n >= 0; --n) {
-                    v = mfma_bf(xf, dsp[pp].s[n], v);
-                    w = mfma_bf(yf, sp[pp].s[n], w);
+                for (int ct = 0; ct < 2; ++ct) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dot = fmaf(ns[pp][ct][i], nds[pp][ct][i], dot);
+                }
+                {
+                    const Split<3> dsp = split_acc<3>(nds[pp][0], nds[pp][1]);
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const u32x4 part = __builtin_bit_cast(u32x4, dsp.s[n]);
+                        if (pp >= 2) later[pp - 2][n] = part;
+                        else if (S == 128 || wave < 4) put_ds(pp, n, part, nrow, g);
+                    }
+                    bf16x8 f[MW];
+#pragma unroll
+                    for (int mi = 0; mi < MW; ++mi) f[mi] = two8(tx, 16 * (m0 + mi) + jj, 32 * pp + 4 * g);
+#pragma unroll
+                    for (int n = 2; n >= 0; --n) {
+#pragma unroll
+                        for (int mi = 0; mi < MW; ++mi) v[mi] = mfma_bf(f[mi], dsp.s[n], v[mi]);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                {
+                    const Split<3> sp = split_acc<3>(ns[pp][0], ns[pp][1]);
+                    bf16x8 f[MW];
+#pragma unroll
+                    for (int mi = 0; mi < MW; ++mi) f[mi] = two8(ty, 16 * (m0 + mi) + jj, YO + 32 * pp + 4 * g);
+#pragma unroll
+                    for (int n = 2; n >= 0; --n) {
+#pragma unroll
+                        for (int mi = 0; mi < MW; ++mi) w[mi] = mfma_bf(f[mi], sp.s[n], w[mi]);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            dot = sum64(dot);
+            if (ln == 0) sS[wave] = S == 128 || wave < 4 ? dot : 0.f;
+#pragma unroll
+            for (int mi = 0; mi < MW; ++mi) {
+                const int m = m0 + mi;
+                const f32x4 ga = num4(rec, SSM_GA, m, g), eg = num4(rec, SSM_EG, m, g);
+                f32x4 u = v[mi] * column(tb, m, g, jj), y = w[mi] * column(tc, m, g, jj);
+                dB[mi] += (ga * num4(rec, SSM_DT, m, g)) * v[mi];
+                dC[mi] += eg * w[mi];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    u[i] = sum16(u[i]);
+                    y[i] = sum16(y[i]);
+                }
+                if (jj == 0) {
+                    *reinterpret_cast<f32x4*>(sU + 64 * t + 16 * m + 4 * g) = u;
+                    *reinterpret_cast<f32x4*>(sY + 64 * t + 16 * m + 4 * g) = y;
                 }
             }
-            const f32x4 ga = num4(rec, SSM_GA, m, g), eg = num4(rec, SSM_EG, m, g);
-            f32x4 u = v * half_of(bcol[m >> 1], m & 1), y = w * half_of(ccol[m >> 1], m & 1);
-            dB[mi] += (ga * num4(rec, SSM_DT, m, g)) * v;
-            dC[mi] += eg * w;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                u[i] = sum16(u[i]);
-                y[i] = sum16(y[i]);
-            }
-            if (jj == 0) {
-                *reinterpret_cast<f32x4*>(sU + 64 * t + 16 * m + 4 * g) = u;
-                *reinterpret_cast<f32x4*>(sY + 64 * t + 16 * m + 4 * g) = y;
-            }
+        }
+        if (h + 1 < h_to) {
+            ask(h + 1);
+            ask_states(h + 1, 0, 2);
         }
         __syncthreads();
 
         // ---- dB and dC from the pair matrices
+        {
+            const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
+            bf16x8 bcol[2], ccol[2];   // channels of tile t, tokens of k step kk
 #pragma unroll
-        for (int n = 1; n >= 0; --n) {
+            for (int kk = 0; kk < 2; ++kk) {
+                bcol[kk] = col_frag(tb, t, kk, g, jj);
+                ccol[kk] = col_frag(tc, t, kk, g, jj);
+            }
 #pragma unroll
-            for (int mi = 0; mi < MW; ++mi) {
-                const int m = m0 + mi;
-                const char *kc = smem + L::KC + n * GDR_TRI + 16 * lane, *kb = smem + L::KB + n * GDR_TRI + 16 * lane;
-                dC[mi] = mfma_bf(lds_bf8(kc + (m < 2 ? m : 2 * m - 2) * GDR_FRAG), bcol[0], dC[mi]);
-                if (m >= 2) dC[mi] = mfma_bf(lds_bf8(kc + (2 * m - 1) * GDR_FRAG), bcol[1], dC[mi]);
-                if (m < 2) dB[mi] = mfma_bf(lds_bf8(kb + 2 * m * GDR_FRAG), ccol[0], dB[mi]);
-                dB[mi] = mfma_bf(lds_bf8(kb + (m < 2 ? 2 * m + 1 : m + 2) * GDR_FRAG), ccol[1], dB[mi]);
+            for (int n = 1; n >= 0; --n) {
+#pragma unroll
+                for (int mi = 0; mi < MW; ++mi) {
+                    const int m = m0 + mi;
+                    const char *kc = smem + L::KC + n * GDR_TRI + 16 * ln, *kb = smem + L::KB + n * GDR_TRI + 16 * ln;
+                    dC[mi] = mfma_bf(lds_bf8(kc + (m < 2 ? m : 2 * m - 2) * GDR_FRAG), bcol[0], dC[mi]);
+                    if (m >= 2) dC[mi] = mfma_bf(lds_bf8(kc + (2 * m - 1) * GDR_FRAG), bcol[1], dC[mi]);
+                    if (m < 2) dB[mi] = mfma_bf(lds_bf8(kb + 2 * m * GDR_FRAG), ccol[0], dB[mi]);
+                    dB[mi] = mfma_bf(lds_bf8(kb + (m < 2 ? 2 * m + 1 : m + 2) * GDR_FRAG), ccol[1], dB[mi]);
+                }
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
         // ---- dx, transposed: a lane holds four channels of one token
         const float skip = p.D ? p.D[h] : 0.f;
 #pragma unroll
         for (int half = 0; half < PX; ++half) {
+            const int lane = opaque(tid & 63), g = lane >> 4, jj = lane & 15;
             if (half > 0) {
                 __syncthreads();
-                put_ds(half);
+                if (S == 128 || wave < 4) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) put_ds(q, n, later[PX > 1 ? q : 0][n], state_row(t, jj >> 2, jj & 3), g);
+                    }
+                }
                 __syncthreads();
             }
             const int pt = wave & 3;
 #pragma unroll
             for (int mi = 0; mi < 2; ++mi) {
+                __builtin_amdgcn_sched_barrier(0);
                 const int m = 2 * (wave >> 2) + mi;
                 f32x4 a = zero, b = zero;
 #pragma unroll
@@ -404,6 +435,7 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
                         u32x2{pack_bf2(a[0], a[1]), pack_bf2(a[2], a[3])};
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
         // ---- the numbers of each token, a wave for each head in turn
         if (wave == (h & 7)) {
             const int I = lane >> 4;

@@ -171,10 +171,11 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
 
-    // tiles (I, J) of the pair matrices: waves 0 .. 5 one below the diagonal, 6 and 7 two on it
-    const int nt = wave < 6 ? 1 : 2;
-    const int tI = wave < 6 ? (wave < 1 ? 1 : wave < 3 ? 2 : 3) : 2 * (wave - 6);
-    const int tJ = wave < 6 ? (wave < 1 ? 0 : wave < 3 ? wave - 1 : wave - 3) : tI;
+    // tiles (I, J) of the pair matrices: waves 0 .. 3 take those below the diagonal, (1,0) (2,0) | (2,1) (3,0) | (3,1) |
+    // (3,2), and 4 .. 7 one on it
+    const int nt = wave < 2 ? 2 : 1;
+    const int tI[2] = {wave < 4 ? (wave < 2 ? wave + 1 : 3) : wave - 4, wave + 2};
+    const int tJ[2] = {wave < 4 ? (wave < 1 ? 0 : wave < 3 ? 1 : 2) : wave - 4, 0};
     f32x4 cb[2];   // C B^T, rows 16 I + 4 g + r, column 16 J + jj
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -182,14 +183,14 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
         if (x >= nt) continue;
 #pragma unroll
         for (int kk = 0; kk < KT; ++kk)
-            cb[x] = mfma_bf(row_frag(tc, tI + x, kk, g, jj), row_frag(tb, tJ + x, kk, g, jj), cb[x]);
+            cb[x] = mfma_bf(row_frag(tc, tI[x], kk, g, jj), row_frag(tb, tJ[x], kk, g, jj), cb[x]);
     }
     f32x4 dB[MW], dC[MW];
 #pragma unroll
     for (int m = 0; m < MW; ++m) dB[m] = dC[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // the lane's channel of the wave's state tile, tokens 16 m + 4 g + r
+    // token 16 m + jj's four channels of lane group g in the wave's state tile
     auto column = [&](const char* tile, int m, int g, int jj) {
-        return widen(lds_tr(tile + tile_off(16 * m + 4 * g + (jj >> 2), 4 * (t >> 1) + (jj & 3)) + 8 * (t & 1)));
+        return widen(*reinterpret_cast<const u32x2*>(tile + tile_off(16 * m + jj, 4 * (t >> 1) + g) + 8 * (t & 1)));
     };
 
     for (int h = h_from; h < h_to; ++h) {
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             if (x >= nt) continue;
-            const int I = tI + x, J = tJ + x;
+            const int I = tI[x], J = tJ[x];
             f32x4 r = {0.f, 0.f, 0.f, 0.f}, rt = r;   // dy x^T, and transposed
 #pragma unroll
             for (int pp = 0; pp < KP; ++pp) {
@@ -263,6 +264,10 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) md[i] = sum16(md[i]);
                 if (jj == 0) *reinterpret_cast<f32x4*>(sRS + 64 * J + 16 * I + 4 * g) = md;
+                if (I > J + 1) {   // (2, 0), (3, 0), (3, 1) whole
+                    const float all = sum_groups((md[0] + md[1]) + (md[2] + md[3]));
+                    if (ln == 0) sS[10 + I + J] = all;
+                }
             } else {   // sum over j < t <= i of the tile, and the diagonal of dy x^T
                 md[2] += md[3];
                 md[1] += md[2];
@@ -323,7 +328,7 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
 #pragma unroll
                     for (int n = 2; n >= 0; --n) {
 #pragma unroll
-                        for (int mi = 0; mi < MW; ++mi) v[mi] = mfma_bf(f[mi], dsp.s[n], v[mi]);
+                        for (int mi = 0; mi < MW; ++mi) v[mi] = mfma_bf(dsp.s[n], f[mi], v[mi]);
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);
@@ -335,7 +340,7 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
 #pragma unroll
                     for (int n = 2; n >= 0; --n) {
 #pragma unroll
-                        for (int mi = 0; mi < MW; ++mi) w[mi] = mfma_bf(f[mi], sp.s[n], w[mi]);
+                        for (int mi = 0; mi < MW; ++mi) w[mi] = mfma_bf(sp.s[n], f[mi], w[mi]);
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);
@@ -345,19 +350,13 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
 #pragma unroll
             for (int mi = 0; mi < MW; ++mi) {
                 const int m = m0 + mi;
-                const f32x4 ga = num4(rec, SSM_GA, m, g), eg = num4(rec, SSM_EG, m, g);
-                f32x4 u = v[mi] * column(tb, m, g, jj), y = w[mi] * column(tc, m, g, jj);
-                dB[mi] += (ga * num4(rec, SSM_DT, m, g)) * v[mi];
-                dC[mi] += eg * w[mi];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    u[i] = sum16(u[i]);
-                    y[i] = sum16(y[i]);
-                }
-                if (jj == 0) {
-                    *reinterpret_cast<f32x4*>(sU + 64 * t + 16 * m + 4 * g) = u;
-                    *reinterpret_cast<f32x4*>(sY + 64 * t + 16 * m + 4 * g) = y;
-                }
+                const int tok = 16 * m + jj;
+                const f32x4 u = v[mi] * column(tb, m, g, jj), y = w[mi] * column(tc, m, g, jj);
+                dB[mi] += (rec[SSM_GA + tok] * rec[SSM_DT + tok]) * v[mi];
+                dC[mi] += rec[SSM_EG + tok] * w[mi];
+                const float su = sum_groups((u[0] + u[1]) + (u[2] + u[3])), sy = sum_groups((y[0] + y[1]) + (y[2] + y[3]));
+                if (g == 0) sU[64 * t + tok] = su;
+                if (g == 1) sY[64 * t + tok] = sy;
             }
         }
         if (h + 1 < h_to) {
@@ -381,10 +380,10 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
                 for (int mi = 0; mi < MW; ++mi) {
                     const int m = m0 + mi;
                     const char *kc = smem + L::KC + n * GDR_TRI + 16 * ln, *kb = smem + L::KB + n * GDR_TRI + 16 * ln;
-                    dC[mi] = mfma_bf(lds_bf8(kc + (m < 2 ? m : 2 * m - 2) * GDR_FRAG), bcol[0], dC[mi]);
-                    if (m >= 2) dC[mi] = mfma_bf(lds_bf8(kc + (2 * m - 1) * GDR_FRAG), bcol[1], dC[mi]);
-                    if (m < 2) dB[mi] = mfma_bf(lds_bf8(kb + 2 * m * GDR_FRAG), ccol[0], dB[mi]);
-                    dB[mi] = mfma_bf(lds_bf8(kb + (m < 2 ? 2 * m + 1 : m + 2) * GDR_FRAG), ccol[1], dB[mi]);
+                    dC[mi] = mfma_bf(bcol[0], lds_bf8(kc + (m < 2 ? m : 2 * m - 2) * GDR_FRAG), dC[mi]);
+                    if (m >= 2) dC[mi] = mfma_bf(bcol[1], lds_bf8(kc + (2 * m - 1) * GDR_FRAG), dC[mi]);
+                    if (m < 2) dB[mi] = mfma_bf(ccol[0], lds_bf8(kb + 2 * m * GDR_FRAG), dB[mi]);
+                    dB[mi] = mfma_bf(ccol[1], lds_bf8(kb + (m < 2 ? 2 * m + 1 : m + 2) * GDR_FRAG), dB[mi]);
                 }
             }
         }
@@ -405,112 +404,121 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
                 }
                 __syncthreads();
             }
-            const int pt = wave & 3;
+            const int pt = wave & 3, ma = 2 * (wave >> 2), col = 64 * half + 16 * pt;   // columns; tokens of two tiles
+            f32x4 a[2] = {zero, zero}, b[2] = {zero, zero};
+#pragma unroll
+            for (int kk = 0; kk < KT; ++kk) {
+                const bf16x8 b0 = row_frag(tb, ma, kk, g, jj), b1 = row_frag(tb, ma + 1, kk, g, jj);
+#pragma unroll
+                for (int n = 1; n >= 0; --n) {
+                    const bf16x8 d = two_tr(smem + L::DS, 32 * kk + 8 * g, 32 * kk + 8 * g + 4, 64 * n + 16 * pt, jj);
+                    a[0] = mfma_bf(d, b0, a[0]);
+                    a[1] = mfma_bf(d, b1, a[1]);
+                }
+            }
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                if (kk == 0 && ma >= 2) continue;
+                const bf16x8 yf = two_tr(ty, 32 * kk + 4 * g, 32 * kk + 16 + 4 * g, YO + col, jj);
+                const char* ex = smem + L::EX + 16 * lane;
+#pragma unroll
+                for (int mi = 0; mi < 2; ++mi) {
+                    const int f = ma < 2 ? 2 * mi + kk : 4 + mi;   // fragment (ma + mi, kk)
+                    b[mi] = mfma_bf(yf, lds_bf8(ex + f * GDR_FRAG + GDR_TRI), b[mi]);
+                    b[mi] = mfma_bf(yf, lds_bf8(ex + f * GDR_FRAG), b[mi]);
+                }
+            }
 #pragma unroll
             for (int mi = 0; mi < 2; ++mi) {
-                __builtin_amdgcn_sched_barrier(0);
-                const int m = 2 * (wave >> 2) + mi;
-                f32x4 a = zero, b = zero;
-#pragma unroll
-                for (int kk = 0; kk < KT; ++kk) {
-                    const bf16x8 bf = row_frag(tb, m, kk, g, jj);
-#pragma unroll
-                    for (int n = 1; n >= 0; --n)
-                        a = mfma_bf(two_tr(smem + L::DS, 32 * kk + 8 * g, 32 * kk + 8 * g + 4, 64 * n + 16 * pt, jj), bf, a);
-                }
-                const int col = 64 * half + 16 * pt;
-#pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                    if (kk == 0 && m >= 2) continue;
-                    const bf16x8 yf = two_tr(ty, 32 * kk + 4 * g, 32 * kk + 16 + 4 * g, YO + col, jj);
-                    const char* ex = smem + L::EX + 16 * lane + (m < 2 ? 2 * m + kk : m + 2) * GDR_FRAG;
-                    b = mfma_bf(yf, lds_bf8(ex + GDR_TRI), b);
-                    b = mfma_bf(yf, lds_bf8(ex), b);
-                }
-                const int tok = 16 * m + jj, at = YO + col + 4 * g;
+                const int tok = 16 * (ma + mi) + jj, at = YO + col + 4 * g;
                 const f32x4 dy = widen(*reinterpret_cast<const u32x2*>(ty + tile_off(tok, at >> 3) + 2 * (at & 7)));
-                a = rec[SSM_DT + tok] * (rec[SSM_GA + tok] * a + b) + skip * dy;
+                const f32x4 d = rec[SSM_DT + tok] * (rec[SSM_GA + tok] * a[mi] + b[mi]) + skip * dy;
                 if (tok < ch.rows)
                     *reinterpret_cast<u32x2*>(p.dx + ((ch.row * p.T + ch.tok + tok) * p.H + h) * P + col + 4 * g) =
-                        u32x2{pack_bf2(a[0], a[1]), pack_bf2(a[2], a[3])};
+                        u32x2{pack_bf2(d[0], d[1]), pack_bf2(d[2], d[3])};
             }
         }
         __builtin_amdgcn_sched_barrier(0);
-        // ---- the numbers of each token, a wave for each head in turn
-        if (wave == (h & 7)) {
+        // ---- what the tokens' numbers are made of, into the head's record behind the steps: a wave a row
+        {
             const int I = lane >> 4;
-            const float d = rec[SSM_DT + lane], A = p.A[h];
-            float rs = 0.f, cs = 0.f, u = 0.f, y = 0.f, q = 0.f;
+            float x = 0.f;
+            if (wave == 0) {
 #pragma unroll
-            for (int j = 0; j < 3; ++j) rs += j < I ? sRS[64 * j + lane] : 0.f;
+                for (int j = 0; j < 3; ++j) x += j < I ? sRS[64 * j + lane] : 0.f;
+            } else if (wave == 1) {
 #pragma unroll
-            for (int i = 1; i < 4; ++i) cs += i > I ? sCS[64 * i + lane] : 0.f;
+                for (int i = 1; i < 4; ++i) x += i > I ? sCS[64 * i + lane] : 0.f;
+            } else if (wave == 2) {
+                x = sCS[64 * I + lane];
+            } else if (wave == 3) {
+                x = sDR[lane];
+            } else if (wave == 4 || wave == 5) {
+                const float* s = wave == 4 ? sU : sY;
 #pragma unroll
-            for (int w = 0; w < S / 16; ++w) {
-                u += sU[64 * w + lane];
-                y += sY[64 * w + lane];
+                for (int w = 0; w < S / 16; ++w) x += s[64 * w + lane];
+                x *= rec[(wave == 4 ? SSM_GA : SSM_EG) + lane];
+            } else if (wave == 6) {
+                x = lane < 8 ? sS[lane] * rec[SSM_EG + 63] : lane < 15 ? sS[lane] : 0.f;
+                const float q = sum16(lane < 8 ? x : 0.f), d = sum16(lane >= 8 && lane < 12 ? x : 0.f);
+                x = lane == 0 ? q : lane == 1 ? d : x;
             }
-#pragma unroll
-            for (int w = 0; w < 8; ++w) q += sS[w];
-            const float t0 = sum16(I > 0 ? sRS[lane] : 0.f), t1 = sum16(I > 1 ? sRS[64 + lane] : 0.f);
-            const float t20 = lane_f32(t0, 32), t30 = lane_f32(t0, 48), t31 = lane_f32(t1, 48);
-            u *= rec[SSM_GA + lane];
-            y *= rec[SSM_EG + lane];
-            float da = suffix16(rs, lane) + before16(prefix16(cs * d)) + sDR[lane] + (I == 1 ? t20 + t30 : I == 2 ? t30 + t31 : 0.f);
-            da += suffix_wave(y, lane) + before_wave(prefix_wave(u * d), lane) + rec[SSM_EG + 63] * q;
-            const float dd = A * da + (u + cs + sCS[64 * I + lane]);
-            float slope = 1.f, own = 0.f, sa = 0.f;
-            const int64_t at = ch.row * p.T + ch.tok + lane;
-            if (lane < ch.rows) {
-                if (p.softplus)
-                    slope = sigmoid(ssm_raw(p.dt, p.dt_f32, ch.row * p.dtb + (ch.tok + lane) * p.dtt + h, p.bias, h));
-                own = dd * slope;
-                sa = d * da;
-                p.ddt[at * p.H + h] = own;
-            }
-            own = sum64(own);
-            sa = sum64(sa);
-            if (lane < 3)
-                p.part[(slot * 3 + lane) * p.H + h] =
-                    lane == 0 ? sa : lane == 1 ? (sS[8] + sS[9]) + (sS[10] + sS[11]) : own;
+            if (wave < 7) reinterpret_cast<float*>(p.rec + (slot * p.H + h) * SSM_REC)[64 * (wave + 1) + lane] = x;
         }
         __syncthreads();   // everything in LDS but B and C is read
     }
 
-    // ---- dB and dC
-    if (p.sets > 1) {
-        const int64_t base = ((int64_t)set * p.nslots + slot) * 64;
-#pragma unroll
-        for (int mi = 0; mi < MW; ++mi) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int tok = 16 * (m0 + mi) + 4 * g + i;
-                const int64_t at = ((base + tok) * p.G + group) * S + state_row(t, jj >> 2, jj & 3);
-                p.dBp[at] = dB[mi][i];
-                p.dCp[at] = dC[mi][i];
-            }
-        }
-        return;
-    }
-    __syncthreads();
-    const int n = state_row(t, jj >> 2, jj & 3);
+    // ---- dB and dC: a lane holds four channels of token 16 m + jj
+    const int n = 32 * (t >> 1) + 8 * g + 4 * (t & 1);
+    const int64_t base = ((int64_t)set * p.nslots + slot) * 64;
 #pragma unroll
     for (int mi = 0; mi < MW; ++mi) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int at = tile_off(16 * (m0 + mi) + 4 * g + i, n >> 3) + 2 * (n & 7);
-            *reinterpret_cast<uint16_t*>(smem + L::B + at) = (uint16_t)pack_bf2(dB[mi][i], 0.f);
-            *reinterpret_cast<uint16_t*>(smem + L::C + at) = (uint16_t)pack_bf2(dC[mi][i], 0.f);
+        const int tok = 16 * (m0 + mi) + jj;
+        if (tok >= ch.rows) continue;
+        if (p.sets > 1) {
+            const int64_t at = ((base + tok) * p.G + group) * S + n;
+            *reinterpret_cast<f32x4*>(p.dBp + at) = dB[mi];
+            *reinterpret_cast<f32x4*>(p.dCp + at) = dC[mi];
+        } else {
+            const int64_t at = ((ch.row * p.T + ch.tok + tok) * p.G + group) * S + n;
+            *reinterpret_cast<u32x2*>(p.dB + at) = u32x2{pack_bf2(dB[mi][0], dB[mi][1]), pack_bf2(dB[mi][2], dB[mi][3])};
+            *reinterpret_cast<u32x2*>(p.dC + at) = u32x2{pack_bf2(dC[mi][0], dC[mi][1]), pack_bf2(dC[mi][2], dC[mi][3])};
         }
     }
-    __syncthreads();
-    for (int e = tid; e < 64 * S / 8; e += NT) {
-        const int r = e / (S / 8), q = e % (S / 8);
-        if (r >= ch.rows) continue;
-        const int64_t at = ((ch.row * p.T + ch.tok + r) * p.G + group) * S + 8 * q;
-        *reinterpret_cast<u32x4*>(p.dB + at) = *reinterpret_cast<const u32x4*>(tb + tile_off(r, q));
-        *reinterpret_cast<u32x4*>(p.dC + at) = *reinterpret_cast<const u32x4*>(tc + tile_off(r, q));
+}
+
+// The tokens' numbers of a chunk: ddt, and the chunk's part of the heads' sums.  A wave for each head,
+// lane = token, sixteen heads a work-group; ddt goes through LDS, so that the heads of a token are
+// stored side by side.
+__global__ void __launch_bounds__(1024) kda_ssm_numbers_kernel(const SsmParams p) {
+    __shared__ float sh[64][17];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), I = lane >> 4;
+    const int sixteens = (p.H + 15) / 16, h0 = (int)(blockIdx.x % sixteens) * 16, h = h0 + w;
+    const int64_t slot = blockIdx.x / sixteens;
+    const SsmChunk ch = ssm_chunk(p, slot);
+    float sa = 0.f, sd = 0.f, own = 0.f;
+    if (h < p.H && ch.rows > 0) {
+        const float* r = reinterpret_cast<const float*>(p.rec + (slot * p.H + h) * SSM_REC) + lane;
+        const float d = r[0], rs = r[64], cs = r[128], csd = r[192], dr = r[256], u = r[320], y = r[384], x = r[448];
+        const float q = lane_f32(x, 0), t20 = lane_f32(x, 12), t30 = lane_f32(x, 13), t31 = lane_f32(x, 14);
+        float slope = 1.f;
+        if (p.softplus && lane < ch.rows)
+            slope = sigmoid(ssm_raw(p.dt, p.dt_f32, ch.row * p.dtb + (ch.tok + lane) * p.dtt + h, p.bias, h));
+        float da = suffix16(rs, lane) + before16(prefix16(cs * d)) + dr + (I == 1 ? t20 + t30 : I == 2 ? t30 + t31 : 0.f);
+        da += suffix_wave(y, lane) + before_wave(prefix_wave(u * d), lane) + q;
+        if (lane < ch.rows) {
+            own = (p.A[h] * da + (u + cs + csd)) * slope;
+            sa = d * da;
+        }
+        sd = lane_f32(x, 1);
     }
+    sh[lane][w] = own;
+    own = sum64(own);
+    sa = sum64(sa);
+    if (lane < 3 && h < p.H) p.part[(slot * 3 + lane) * p.H + h] = lane == 0 ? sa : lane == 1 ? sd : own;
+    __syncthreads();
+    const int tok = threadIdx.x >> 4, i = threadIdx.x & 15;
+    if (tok < ch.rows && h0 + i < p.H) p.ddt[(ch.row * p.T + ch.tok + tok) * p.H + h0 + i] = sh[tok][i];
 }
 
 // dB and dC of a chunk as sums over its sets of heads, in order; a thread takes eight channels.
@@ -532,21 +540,19 @@ __global__ void __launch_bounds__(256) kda_ssm_join_kernel(const SsmParams p) {
     }
 }
 
-// The heads' sums over the chunks: dA, dD, dbias.  A work-group takes one of them and 32 heads, eight
-// threads each every eighth chunk, then in order.
-__global__ void __launch_bounds__(256) kda_ssm_sums_kernel(const SsmParams p) {
-    __shared__ double sh[8][32];
-    const int g = threadIdx.x >> 5, l = threadIdx.x & 31, which = blockIdx.x % 3, h = (int)(blockIdx.x / 3) * 32 + l;
+// The heads' sums over the chunks: dA, dD, dbias.  A work-group takes one of them and 16 heads, 64
+// threads each every 64th chunk, then in order.
+__global__ void __launch_bounds__(1024) kda_ssm_sums_kernel(const SsmParams p) {
+    __shared__ double sh[64][16];
+    const int g = threadIdx.x >> 4, l = threadIdx.x & 15, which = blockIdx.x % 3, h = (int)(blockIdx.x / 3) * 16 + l;
     float* out = which == 0 ? p.dA : which == 1 ? p.dD : p.dbias;
     double x = 0.0;
     if (out && h < p.H)
-        for (int64_t s = g; s < p.nslots; s += 8)
-            if (ssm_chunk(p, s).rows > 0) x += (double)p.part[(s * 3 + which) * p.H + h];
+        for (int64_t s = g; s < p.nslots; s += 64) x += (double)p.part[(s * 3 + which) * p.H + h];
     sh[g][l] = x;
     __syncthreads();
     if (g > 0 || !out || h >= p.H) return;
-#pragma unroll
-    for (int i = 1; i < 8; ++i) x += sh[i][l];
+    for (int i = 1; i < 64; ++i) x += sh[i][l];
     out[h] = (float)x;
 }
 
@@ -557,8 +563,9 @@ hipError_t launch_ssm_grads(const SsmParams& p, hipStream_t stream) {
                              : (p.P == 128 ? kda_ssm_grads_kernel<64, 128> : kda_ssm_grads_kernel<64, 64>);
         hipLaunchKernelGGL(f, dim3((unsigned)blocks), dim3(NT), 0, stream, p);
         if (p.sets > 1) hipLaunchKernelGGL(kda_ssm_join_kernel, dim3((unsigned)p.nslots), dim3(256), 0, stream, p);
+        hipLaunchKernelGGL(kda_ssm_numbers_kernel, dim3((unsigned)(p.nslots * ((p.H + 15) / 16))), dim3(1024), 0, stream, p);
     }
-    hipLaunchKernelGGL(kda_ssm_sums_kernel, dim3((unsigned)(3 * ((p.H + 31) / 32))), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL(kda_ssm_sums_kernel, dim3((unsigned)(3 * ((p.H + 15) / 16))), dim3(1024), 0, stream, p);
     return hipGetLastError();
 }
 

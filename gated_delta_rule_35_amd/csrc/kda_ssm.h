@@ -47,8 +47,11 @@ constexpr int SSM_REC = 2048;
 hipError_t launch_ssm_fwd(const SsmParams& p, hipStream_t stream);
 hipError_t launch_ssm_bwd(const SsmParams& p, hipStream_t stream);
 hipError_t launch_ssm_grads(const SsmParams& p, hipStream_t stream);
+void launch_ssm_scan(const SsmParams& p, hipStream_t stream);
+// What segments add to the state; `both`: and to its gradients.
+void launch_ssm_adds(const SsmParams& p, bool both, hipStream_t stream);
 
-// Value columns that a walking work-group takes, 32 a wave.
+// Value columns that a walking work-group takes.
 constexpr int SSM_COLS = 256;
 
 struct SsmDecodeParams {

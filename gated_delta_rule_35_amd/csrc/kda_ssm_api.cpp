@@ -119,10 +119,7 @@ Segments segments(int64_t tokens_per_row, int64_t N, bool packed, int64_t units)
     return s;
 }
 // Work-groups that share a group's heads in a walk.
-int64_t walk_units(int64_t H, int64_t G, int64_t P) {
-    const int64_t cols = H / G * P, width = cols > 128 ? kda::SSM_COLS : kda::SSM_COLS / 2;
-    return G * ((cols + width - 1) / width);
-}
+int64_t walk_units(int64_t H, int64_t G, int64_t P) { return G * ((H / G * P + kda::SSM_COLS - 1) / kda::SSM_COLS); }
 
 // A workspace's parts, in bytes from its start.
 struct Layout {

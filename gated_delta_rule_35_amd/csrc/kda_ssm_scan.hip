@@ -1,22 +1,12 @@
-// The selective state space scan's walks over chunks of 64 tokens, on gfx950 (MI355X).  With
-// d_t the steps, a_t = d_t A and G the running sum of a within a chunk:
-//   y = e^G C S + (C B^T e^{G_i - G_j} d_j, j <= i) x + D x,   S <- e^{G_last} S + B^T (e^{G_last - G} d x)
-// The state's transition is a number, so a sequence is cut into segments that are walked side by
-// side: a first walk forms what each segment adds to the state, a small kernel chains them, and a second
-// walk starts every segment from the state that enters it.  Where sequences and heads alone fill
-// the compute units there is one segment and one walk.
+// What the selective state space scan's walks share and the backward's own, on gfx950 (MI355X):
+// the numbers of every token, the chaining of segments, and the walks that leave the states.
 //
-// A wave owns 32 of a head's value columns: its state is S / 16 by 2 accumulator tiles, which as
-// B operands need no exchange (kda_gdr_fwd.hip has the order of their rows).  Eight waves (or
-// four, where a group of heads has 128 columns or fewer) share the chunk's B and C in LDS, and
-// each brings its own columns of x there; the next chunk's come by DMA during this one's products.
-// C B^T is formed transposed by every wave, so that what a lane holds of it, times the decays, is the A
-// operand of its product with x: no exchange either, at 40 of 224 matrix instructions.
-// The decay between tokens of different blocks of sixteen is a product of a number of each token and one
-// or two of the blocks, all at most 1 for A <= 0; within a block it is formed from the difference.
-//
-// Precision.  x, B and C are bf16.  What enters the state is formed in three bf16 parts, fp32's 24
-// bits; what only adds to y (S in C S, the pair matrix) in two, 16 bits for y's eight.
+// Backward: the state that enters each chunk, S <- e^{G_last} S + B^T (e^{G_last - G} d x), and the gradient of the one
+// that leaves it, last chunk first, dS <- e^{G_last} dS + C^T (e^G dy), both into memory as the operands
+// that the token gradients take.  A wave owns 32 of a head's value columns: its state is S / 16 by 2 accumulator
+// tiles, transposed (a lane holds four columns of a channel).  Eight waves (or four, where a group of
+// heads has 128 columns or fewer) share the chunk's B or C in LDS, and each brings its own columns
+// of x or dy there; the next chunk's come by DMA during this one's products.
 #include <algorithm>
 
 #include "kda_ssm_device.h"
@@ -62,12 +52,10 @@ __global__ void __launch_bounds__(256) kda_ssm_gates_kernel(const SsmParams p) {
 
 namespace {
 
-enum { FULL, LOCAL, KEEP };   // the forward's walk; what a segment adds; the states entering every chunk
-
-template <int NW, int MODE>
+template <int NW>
 struct SL {
     static constexpr int HEADS = NW / 2;   // at most, of 64 columns
-    static constexpr int B = 0, C = 16384, X = MODE == FULL ? 32768 : 16384, REC = X + NW * 4096;
+    static constexpr int B = 0, X = 16384, REC = X + NW * 4096;
     static constexpr int SLOT = REC + HEADS * SSM_REC, BYTES = 2 * SLOT;
 };
 
@@ -89,9 +77,9 @@ __device__ __forceinline__ bool walk_place(int b, int units, int64_t segs, int64
 }  // namespace
 
 // REV: the gradients' walk, with C, dy and e^G in the place of B, x and e^{G_last - G} d, last chunk first.
-template <int S, int NW, int MODE, bool REV>
+template <int S, int NW, bool REV>
 __device__ __forceinline__ void ssm_walk(const SsmParams& p, char* smem, int block) {
-    typedef SL<NW, MODE> L;
+    typedef SL<NW> L;
     constexpr int KT = S / 32, NT = S / 16;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, jj = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -101,7 +89,6 @@ __device__ __forceinline__ void ssm_walk(const SsmParams& p, char* smem, int blo
     if (!walk_place(block, per * p.G, p.segslots, sslot, unit)) return;
     const SsmSegment sg = ssm_segment(p, sslot);
     if (sg.index >= sg.count) return;
-    if (MODE == LOCAL && sg.index == (REV ? 0 : sg.count - 1)) return;   // nothing starts from what it adds
     const int group = unit / per, h0 = (unit % per) * 32 * NW / p.P;      // first head (in the group) of the unit
     const int col = (unit % per) * 32 * NW + 32 * wave;                   // the wave's first column in the group
     const bool on = col < R * p.P;
@@ -132,7 +119,6 @@ __device__ __forceinline__ void ssm_walk(const SsmParams& p, char* smem, int blo
             }
         };
         tile(REV ? p.C : p.B, to + L::B);
-        if (MODE == FULL) tile(p.C, to + L::C);
         if (on) {
             const Rows& t = REV ? p.dO : p.x;
             const __amdgpu_buffer_rsrc_t rs = chunk_rsrc(t.p + row * t.sb + tok * t.st + head * t.sh + pc, t.st, rows, 32);
@@ -147,59 +133,30 @@ __device__ __forceinline__ void ssm_walk(const SsmParams& p, char* smem, int blo
         }
     };
 
-    // The state that enters: natural order [S][P], or transposed for LOCAL and KEEP (a lane holds four
-    // columns of channel n of each tile).
+    // The state that enters, transposed: a lane holds four columns of channel state_row(t, jj / 4, jj % 4) of tile t
     f32x4 st[NT][2];
     const int64_t state = (int64_t)p.S * p.P;
-    const float* from = nullptr;
-    if (MODE != LOCAL) {
-        const float* outer = REV ? p.dhT : p.h0;
-        if (sg.count > 1) from = (REV ? p.dseg : p.seg) + (sslot * p.H + head) * state;
-        else if (outer) from = outer + ((int64_t)sg.n * p.H + head) * state;
-    }
+    const float *from = nullptr, *outer = REV ? p.dhT : p.h0;
+    if (sg.count > 1) from = (REV ? p.dseg : p.seg) + (sslot * p.H + head) * state;
+    else if (outer) from = outer + ((int64_t)sg.n * p.H + head) * state;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
         for (int ct = 0; ct < 2; ++ct) {
             st[t][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (!from || !on) continue;
-            if (MODE == FULL) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) st[t][ct][r] = from[(int64_t)state_row(t, g, r) * p.P + pc + 16 * ct + jj];
-            } else {
+            if (from && on)
                 st[t][ct] = *reinterpret_cast<const f32x4*>(from + (int64_t)state_row(t, jj >> 2, jj & 3) * p.P + pc + 16 * ct + 4 * g);
-            }
         }
     }
-    float total = 1.f;   // the segment's decay
-    const float skip = MODE == FULL && on && p.D ? p.D[head] : 0.f;
-
-    auto store_y = [&](int i) {   // the wave's columns, where x was
-        const int c = at(i), rows = rows_of(c);
-        const char* s = smem + (i & 1) * L::SLOT + L::X + wave * 4096;
-        u32x4 y[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) y[u] = *reinterpret_cast<const u32x4*>(s + u * 1024 + 16 * lane);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int r = 16 * u + (lane >> 2);
-            if (r < rows)
-                *reinterpret_cast<u32x4*>(p.y + ((row * p.T + tok0 + (int64_t)c * CH + r) * p.H + head) * p.P + pc +
-                                          8 * (lane & 3)) = y[u];
-        }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read before the DMA of what comes there
-    };
 
     if (nch > 0) dma(0);
     for (int i = 0; i < nch; ++i) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's pieces of the chunk
         lds_barrier();   // everyone's, and the other slot's reads are done
-        if (MODE == FULL && i > 0 && on) store_y(i - 1);
         if (i + 1 < nch) dma(i + 1);
         if (!on) continue;
         char* slot = smem + (i & 1) * L::SLOT;
-        const char *tb = slot + L::B, *tc = slot + L::C;
-        char* tx = slot + L::X + wave * 4096;
+        const char *tb = slot + L::B, *tx = slot + L::X + wave * 4096;
         const float* rec = reinterpret_cast<const float*>(slot + L::REC + myrec);
         const float el = rec[SSM_EG + 63];
         bf16x8 xf[2][2];
@@ -208,108 +165,11 @@ __device__ __forceinline__ void ssm_walk(const SsmParams& p, char* smem, int blo
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) xf[kk][ct] = x_frag(tx, kk, ct, g, jj);
         }
-        if (MODE == KEEP) {
-            float* to = (REV ? p.dSt : p.St) + ((sg.slot0 + c0 + at(i)) * p.H + head) * state + (pc >> 5) * (S * 32) + lane * 8;
+        float* to = (REV ? p.dSt : p.St) + ((sg.slot0 + c0 + at(i)) * p.H + head) * state + (pc >> 5) * (S * 32) + lane * 8;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
+        for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                for (int ct = 0; ct < 2; ++ct) *reinterpret_cast<f32x4*>(to + t * 512 + 4 * ct) = st[t][ct];
-            }
-        }
-        if (MODE == FULL) {
-            // the pair matrix in two parts, fragments (m, kk) of its lower triangle
-            u32x4 pm[2][6];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                pm[n][0][2] = pm[n][0][3] = 0;   // above the diagonal
-                pm[n][3][2] = pm[n][3][3] = 0;
-            }
-            {
-                bf16x8 cf[4][KT];
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-#pragma unroll
-                    for (int kk = 0; kk < KT; ++kk) cf[m][kk] = row_frag(tc, m, kk, g, jj);
-                }
-#pragma unroll
-                for (int J = 0; J < 4; ++J) {
-                    bf16x8 bf[KT];
-#pragma unroll
-                    for (int kk = 0; kk < KT; ++kk) bf[kk] = row_frag(tb, J, kk, g, jj);
-                    const f32x4 d = num4(rec, SSM_DT, J, g), ka = num4(rec, SSM_KA, J, g) * d;
-                    const f32x4 hj = num4(rec, SSM_GH, J, g), lj = num4(rec, SSM_GL, J, g);
-#pragma unroll
-                    for (int I = J; I < 4; ++I) {
-                        f32x4 a = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int kk = 0; kk < KT; ++kk) a = mfma_bf(bf[kk], cf[I][kk], a);
-                        if (I == J) {
-                            const float hi = rec[SSM_GH + 16 * I + jj], lo = rec[SSM_GL + 16 * I + jj];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                a[e] = 4 * g + e <= jj ? a[e] * fexp2((hi - hj[e]) + (lo - lj[e])) * d[e] : 0.f;
-                        } else {
-                            float ri = rec[SSM_RI + 16 * I + jj];
-                            if (I > J + 1) ri *= rec[SSM_RI + 16 * J + 31];
-                            if (I > J + 2) ri *= rec[SSM_RI + 16 * J + 47];
-                            a *= ka * ri;
-                        }
-                        const int f = I < 2 ? I : 2 * I - 2 + (J >> 1), w = 2 * (J & 1);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t q = pack_bf2(a[2 * e], a[2 * e + 1]);
-                            pm[0][f][w + e] = q;
-                            pm[1][f][w + e] = pack_bf2(a[2 * e] - bf_lo(q), a[2 * e + 1] - bf_hi(q));
-                        }
-                    }
-                }
-            }
-            f32x4 y[4][2];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) y[m][0] = y[m][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int kk = 0; kk < KT; ++kk) {
-                const Split<2> s0 = split_acc<2>(st[2 * kk][0], st[2 * kk + 1][0]), s1 = split_acc<2>(st[2 * kk][1], st[2 * kk + 1][1]);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const bf16x8 c = row_frag(tc, m, kk, g, jj);
-                    y[m][0] = mfma_bf(c, s0.s[1], y[m][0]);
-                    y[m][1] = mfma_bf(c, s1.s[1], y[m][1]);
-                    y[m][0] = mfma_bf(c, s0.s[0], y[m][0]);
-                    y[m][1] = mfma_bf(c, s1.s[0], y[m][1]);
-                }
-            }
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const f32x4 eg = num4(rec, SSM_EG, m, g);
-#pragma unroll
-                for (int ct = 0; ct < 2; ++ct) {
-                    const u32x4 xx = __builtin_bit_cast(u32x4, xf[m >> 1][ct]);
-                    y[m][ct] = y[m][ct] * eg + skip * widen(u32x2{xx[2 * (m & 1)], xx[2 * (m & 1) + 1]});
-                }
-            }
-            constexpr int FM[6] = {0, 1, 2, 2, 3, 3}, FK[6] = {0, 0, 0, 1, 0, 1};
-#pragma unroll
-            for (int n = 1; n >= 0; --n) {
-#pragma unroll
-                for (int f = 0; f < 6; ++f) {
-#pragma unroll
-                    for (int ct = 0; ct < 2; ++ct)
-                        y[FM[f]][ct] = mfma_bf(__builtin_bit_cast(bf16x8, pm[n][f]), xf[FK[f]][ct], y[FM[f]][ct]);
-                }
-            }
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-#pragma unroll
-                for (int ct = 0; ct < 2; ++ct) {
-                    const uint32_t p0 = pack_bf2(y[m][ct][0], y[m][ct][1]), p1 = pack_bf2(y[m][ct][2], y[m][ct][3]);
-                    char* dst = tx + (16 * m + 4 * g) * 64 + 32 * ct + 2 * jj;
-                    *reinterpret_cast<uint16_t*>(dst) = (uint16_t)p0;
-                    *reinterpret_cast<uint16_t*>(dst + 64) = (uint16_t)(p0 >> 16);
-                    *reinterpret_cast<uint16_t*>(dst + 128) = (uint16_t)p1;
-                    *reinterpret_cast<uint16_t*>(dst + 192) = (uint16_t)(p1 >> 16);
-                }
-            }
+            for (int ct = 0; ct < 2; ++ct) *reinterpret_cast<f32x4*>(to + t * 512 + 4 * ct) = st[t][ct];
         }
         // S <- e^{G_last} S + B^T (w x)
 #pragma unroll
@@ -317,7 +177,6 @@ __device__ __forceinline__ void ssm_walk(const SsmParams& p, char* smem, int blo
             st[t][0] *= el;
             st[t][1] *= el;
         }
-        total *= el;
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             f32x4 w0, w1;
@@ -341,48 +200,27 @@ __device__ __forceinline__ void ssm_walk(const SsmParams& p, char* smem, int blo
                 for (int n = 2; n >= 0; --n) {
 #pragma unroll
                     for (int ct = 0; ct < 2; ++ct)
-                        st[t][ct] = MODE == FULL ? mfma_bf(b, wx[ct].s[n], st[t][ct]) : mfma_bf(wx[ct].s[n], b, st[t][ct]);
+                        st[t][ct] = mfma_bf(wx[ct].s[n], b, st[t][ct]);
                 }
             }
         }
     }
-    if (!on) return;
-    if (MODE == FULL && nch > 0) store_y(nch - 1);
-    // what the walk leaves: y's wave's own columns only, so nothing has to be waited for
-    float* to = nullptr;
-    if (MODE == LOCAL) {
-        to = (REV ? p.dseg : p.seg) + (sslot * p.H + head) * state;
-        if (pc == 0 && lane == 0) (REV ? p.ddecay : p.decay)[sslot * p.H + head] = total;
-    } else if (sg.index == (REV ? 0 : sg.count - 1)) {
-        float* outer = MODE == FULL ? p.hT : REV ? p.dh0 : nullptr;
-        if (outer) to = outer + ((int64_t)sg.n * p.H + head) * state;
-    }
-    if (!to) return;
+    if (!REV || !on || !p.dh0 || sg.index != 0) return;
+    float* dh0 = p.dh0 + ((int64_t)sg.n * p.H + head) * state;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
-        for (int ct = 0; ct < 2; ++ct) {
-            if (MODE == FULL) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) to[(int64_t)state_row(t, g, r) * p.P + pc + 16 * ct + jj] = st[t][ct][r];
-            } else {
-                *reinterpret_cast<f32x4*>(to + (int64_t)state_row(t, jj >> 2, jj & 3) * p.P + pc + 16 * ct + 4 * g) = st[t][ct];
-            }
-        }
+        for (int ct = 0; ct < 2; ++ct)
+            *reinterpret_cast<f32x4*>(dh0 + (int64_t)state_row(t, jj >> 2, jj & 3) * p.P + pc + 16 * ct + 4 * g) = st[t][ct];
     }
 }
 
+// The second half of the work-groups walks the gradients.
 template <int S, int NW>
-__global__ void __launch_bounds__(64 * NW) kda_ssm_scan_kernel(const SsmParams p) {
-    __shared__ __attribute__((aligned(1024))) char smem[SL<NW, FULL>::BYTES];
-    ssm_walk<S, NW, FULL, false>(p, smem, (int)blockIdx.x);
-}
-// The backward's second half of the work-groups walks the gradients.
-template <int S, int NW, int MODE>
 __global__ void __launch_bounds__(64 * NW) kda_ssm_states_kernel(const SsmParams p, const int half) {
-    __shared__ __attribute__((aligned(1024))) char smem[SL<NW, MODE>::BYTES];
-    if ((int)blockIdx.x < half) ssm_walk<S, NW, MODE, false>(p, smem, (int)blockIdx.x);
-    else ssm_walk<S, NW, MODE, true>(p, smem, (int)blockIdx.x - half);
+    __shared__ __attribute__((aligned(1024))) char smem[SL<NW>::BYTES];
+    if ((int)blockIdx.x < half) ssm_walk<S, NW, false>(p, smem, (int)blockIdx.x);
+    else ssm_walk<S, NW, true>(p, smem, (int)blockIdx.x - half);
 }
 
 // Chains a sequence's segments: what enters each from what the ones before it add (REV: after it).
@@ -419,21 +257,23 @@ __global__ void __launch_bounds__(256) kda_ssm_chain_kernel(const SsmParams p, c
 
 namespace {
 
-template <int MODE>
-void states(const SsmParams& p, bool both, hipStream_t stream) {
+void states(const SsmParams& p, hipStream_t stream) {
     const bool wide = p.H / p.G * p.P > 128;
     const int nw = wide ? 8 : 4, per = (p.H / p.G * p.P + 32 * nw - 1) / (32 * nw);
-    const unsigned half = (unsigned)((p.segslots + 7) / 8 * 8 * per * p.G), blocks = both ? 2 * half : half;
-    auto* f = p.S == 128 ? (wide ? kda_ssm_states_kernel<128, 8, MODE> : kda_ssm_states_kernel<128, 4, MODE>)
-                         : (wide ? kda_ssm_states_kernel<64, 8, MODE> : kda_ssm_states_kernel<64, 4, MODE>);
-    hipLaunchKernelGGL(f, dim3(blocks), dim3(64 * nw), 0, stream, p, (int)half);
+    const unsigned half = (unsigned)((p.segslots + 7) / 8 * 8 * per * p.G);
+    auto* f = p.S == 128 ? (wide ? kda_ssm_states_kernel<128, 8> : kda_ssm_states_kernel<128, 4>)
+                         : (wide ? kda_ssm_states_kernel<64, 8> : kda_ssm_states_kernel<64, 4>);
+    hipLaunchKernelGGL(f, dim3(2 * half), dim3(64 * nw), 0, stream, p, (int)half);
 }
 bool segmented(const SsmParams& p) { return p.cu ? p.nc > p.segc : p.nseg > 1; }
 void gates(const SsmParams& p, hipStream_t stream) {
     if (p.nslots > 0)
         hipLaunchKernelGGL(kda_ssm_gates_kernel, dim3((unsigned)(p.nslots * ((p.H + 3) / 4))), dim3(256), 0, stream, p);
 }
-void chain(const SsmParams& p, bool both, hipStream_t stream) {
+// The states that enter the segments, and the gradients of those that leave them.
+void enter(const SsmParams& p, bool both, hipStream_t stream) {
+    if (!segmented(p)) return;
+    launch_ssm_adds(p, both, stream);
     const int64_t half = (int64_t)p.N * p.H * (p.S * p.P / 1024);
     hipLaunchKernelGGL(kda_ssm_chain_kernel, dim3((unsigned)(both ? 2 * half : half)), dim3(256), 0, stream, p, half);
 }
@@ -442,27 +282,16 @@ void chain(const SsmParams& p, bool both, hipStream_t stream) {
 
 hipError_t launch_ssm_fwd(const SsmParams& p, hipStream_t stream) {
     gates(p, stream);
-    if (segmented(p)) {
-        states<LOCAL>(p, false, stream);
-        chain(p, false, stream);
-    }
-    const bool wide = p.H / p.G * p.P > 128;
-    const int nw = wide ? 8 : 4, per = (p.H / p.G * p.P + 32 * nw - 1) / (32 * nw);
-    const unsigned blocks = (unsigned)((p.segslots + 7) / 8 * 8 * per * p.G);
-    auto* f = p.S == 128 ? (wide ? kda_ssm_scan_kernel<128, 8> : kda_ssm_scan_kernel<128, 4>)
-                         : (wide ? kda_ssm_scan_kernel<64, 8> : kda_ssm_scan_kernel<64, 4>);
-    hipLaunchKernelGGL(f, dim3(blocks), dim3(64 * nw), 0, stream, p);
+    enter(p, false, stream);
+    launch_ssm_scan(p, stream);
     return hipGetLastError();
 }
 
 hipError_t launch_ssm_bwd(const SsmParams& p, hipStream_t stream) {
     if (p.N > 0) {
         gates(p, stream);
-        if (segmented(p)) {
-            states<LOCAL>(p, true, stream);
-            chain(p, true, stream);
-        }
-        states<KEEP>(p, true, stream);
+        enter(p, true, stream);
+        states(p, stream);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

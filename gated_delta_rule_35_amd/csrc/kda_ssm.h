@@ -40,8 +40,8 @@ struct SsmParams {
 
 // A record's rows of 64 numbers (fp32), by token of the chunk: the step, e^G, e^{G_last - G}, G in
 // units of log 2 as a value and its remainder, e^{G - G_s} with G_s of the token before its block of
-// sixteen, e^{G_e - G} with G_e of its block's last token.
-enum { SSM_DT = 0, SSM_EG = 64, SSM_GA = 128, SSM_GH = 192, SSM_GL = 256, SSM_RI = 320, SSM_KA = 384 };
+// sixteen, e^{G_e - G} with G_e of its block's last token, the step times e^{G_last - G}.
+enum { SSM_DT = 0, SSM_EG = 64, SSM_GA = 128, SSM_GH = 192, SSM_GL = 256, SSM_RI = 320, SSM_KA = 384, SSM_W = 448 };
 constexpr int SSM_REC = 2048;
 
 hipError_t launch_ssm_fwd(const SsmParams& p, hipStream_t stream);

@@ -5,6 +5,19 @@
 
 namespace kda {
 
+// x, which is the same in every lane, in scalar registers (what a division leaves in vector ones).
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)x), hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32));
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+// x, formed where this stands: the compiler would put what a select drops behind a branch, which
+// parts matrix instructions from what could run beside them.
+__device__ __forceinline__ float formed(float x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // A token's step: dt + bias, or log(1 + e^{dt + bias}) of it.
 __device__ __forceinline__ float ssm_raw(const void* dt, int f32, int64_t i, const float* bias, int h) {
     const float v = gdr_beta(dt, f32, i);
@@ -40,7 +53,7 @@ __device__ __forceinline__ int ssm_find(const SsmParams& p, int64_t s, int64_t u
     }
     return lo;
 }
-// The chunk in slot s: its sequence's row, first token and real rows (0: the slot is empty).
+// The chunk in slot s (the same in every lane): its sequence's row, first token and real rows (0: the slot is empty).
 struct SsmChunk {
     int64_t tok, row;
     int rows;
@@ -49,7 +62,7 @@ __device__ __forceinline__ SsmChunk ssm_chunk(const SsmParams& p, int64_t s) {
     const int n = p.cu ? ssm_find(p, s, CH) : (int)(s / p.nc);
     const SsmSeq q = ssm_seq(p, n);
     const int64_t c = s - (p.cu ? q.bos / CH + n : (int64_t)n * p.nc), r = q.len - c * CH;
-    return {q.bos + c * CH, q.row, c < 0 || r <= 0 ? 0 : (r >= CH ? CH : (int)r)};
+    return {uniform(q.bos + c * CH), uniform(q.row), uniform(c < 0 || r <= 0 ? 0 : (r >= CH ? CH : (int)r))};
 }
 // The segment in slot s: sequence, its segments (at least one), which of them it is (beyond them:
 // the slot is empty), and the slot of the sequence's first segment and first chunk.
@@ -68,7 +81,8 @@ __device__ __forceinline__ SsmSegment ssm_segment(const SsmParams& p, int64_t s)
     g.index = (int)(s - g.seg0);
     const int64_t c = (g.q.len + unit - 1) / unit;
     g.count = c < 1 ? 1 : (int)c;
-    return g;
+    return {{uniform(g.q.bos), uniform(g.q.len), uniform(g.q.row)}, uniform(g.n), uniform(g.index), uniform(g.count),
+            uniform(g.seg0), uniform(g.slot0)};
 }
 
 // Row `row` of a record: the numbers of tokens 16 m + 4 g + r, r < 4.

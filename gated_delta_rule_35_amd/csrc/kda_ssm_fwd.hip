@@ -1,6 +1,6 @@
 // The selective state space scan's walks over chunks of 64 tokens, on gfx950 (MI355X).  With
 // d_t the steps, a_t = d_t A and G the running sum of a within a chunk:
-//   y = e^G C S + (C B^T e^{G_i - G_j} d_j, j <= i) x + D x,   S <- e^{G_last} S + B^T (e^{G_last - G} d x)
+//   y = e^G C S + (C B^T e^{G_i - G_j} d_j, j <= i, and D where i = j) x,   S <- e^{G_last} S + B^T (e^{G_last - G} d x)
 // The state's transition is a number, so a sequence is cut into segments that are walked side by
 // side: a first walk forms what each segment adds to the state, a small kernel chains them, and a second
 // walk starts every segment from the state that enters it.  Where sequences and heads alone fill
@@ -12,7 +12,7 @@
 // wave that waits for the memory's queue would keep its products waiting.  Three meetings a chunk:
 //   1  C S                                                    | y of the last chunk out of LDS, x in its place
 //   2  the pairs' products                                    | the next chunk's B, C and numbers into LDS
-//   3  the state grows, and the pair matrix (C B^T with its   | y stored, inputs asked for two chunks ahead
+//   3  the state grows, and the pair matrix (C B^T with its   | y stored, x asked for a chunk ahead, B and C two
 //      decays) of the next chunk, two waves half of it each
 // y is formed transposed, so that a lane holds four channels of one token.  The decay between tokens of
 // different blocks of sixteen is a product of a number of each token and one or two of the blocks,
@@ -63,21 +63,21 @@ struct SsmWalk {
 };
 // Work-groups are dealt to the 8 XCDs round robin: a segment's go to one of them, since they share B and C.
 __device__ __forceinline__ bool walk_place(const SsmParams& p, int block, int w, SsmWalk& k) {
-    const int R = p.H / p.G, per = (R * p.P + SSM_COLS - 1) / SSM_COLS, units = per * p.G;
-    const int r = block >> 3, unit = r % units;
-    k.sslot = (int64_t)(r / units) * 8 + (block & 7);
+    const int R = uniform(p.H / p.G), per = (R * p.P + SSM_COLS - 1) / SSM_COLS, units = per * p.G;
+    const int r = block >> 3, unit = uniform(r % units);
+    k.sslot = uniform((int64_t)(r / units) * 8 + (block & 7));
     if (k.sslot >= p.segslots) return false;
     k.sg = ssm_segment(p, k.sslot);
     if (k.sg.index >= k.sg.count) return false;
-    k.group = unit / per;
-    const int col = (unit % per) * SSM_COLS + 64 * w;
+    k.group = uniform(unit / per);
+    const int col = uniform((unit % per) * SSM_COLS + 64 * w);
     k.on = col < R * p.P;
-    k.head = k.group * R + (k.on ? col / p.P : 0);
-    k.pc = col % p.P;
+    k.head = uniform(k.group * R + (k.on ? col / p.P : 0));
+    k.pc = uniform(col % p.P);
     k.c0 = k.sg.index * p.segc;
     k.left = k.sg.q.len - (int64_t)k.c0 * CH;
     const int64_t n = (k.left + CH - 1) / CH;
-    k.nch = n <= 0 ? 0 : (n < p.segc ? (int)n : p.segc);
+    k.nch = uniform(n <= 0 ? 0 : (n < p.segc ? (int)n : p.segc));
     k.row = k.sg.q.row;
     k.tok0 = k.sg.q.bos + (int64_t)k.c0 * CH;
     return true;
@@ -124,14 +124,15 @@ struct Columns {
 #pragma unroll
         for (int u = 0; u < 8; ++u) v[u] = *reinterpret_cast<const u32x4*>(from + x_off(8 * u + (ln >> 3), 8 * (ln & 7)));
     }
+    // y's rows; those past the chunk's end lie past the buffer's and are dropped
     __device__ __forceinline__ void store(const SsmParams& p, const SsmWalk& k, int c, int ln) const {
-        const int rows = k.rows(c);
-        uint16_t* y = p.y + ((k.row * p.T + k.tok0 + (int64_t)c * CH) * p.H + k.head) * p.P + k.pc + 8 * (ln & 7);
+        const int st = p.H * p.P;
+        const __amdgpu_buffer_rsrc_t rs =
+            chunk_rsrc(p.y + ((k.row * p.T + k.tok0 + (int64_t)c * CH) * p.H + k.head) * p.P + k.pc, st, k.rows(c), 64);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int r = 8 * u + (ln >> 3);
-            if (r < rows) *reinterpret_cast<u32x4*>(y + (int64_t)r * p.H * p.P) = v[u];
-        }
+        for (int u = 0; u < 8; ++u)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(__attribute__((ext_vector_type(4))) unsigned int, v[u]), rs,
+                                                   (8 * u + (ln >> 3)) * st * 2 + 16 * (ln & 7), 0, 0);
     }
 };
 struct Record {
@@ -148,9 +149,9 @@ struct Record {
 };
 
 // Row I of tiles of a chunk's pair matrix, in two parts, into the fragments (m, kk) of its lower triangle in
-// LDS.  C B^T is formed transposed: tile (J, I) holds in a lane rows j = 16 J + 4 g + r of column i = 16 I + jj.
+// LDS; D is added to its diagonal.  C B^T is formed transposed: tile (J, I) holds in a lane rows j = 16 J + 4 g + r of column i = 16 I + jj.
 template <int S, int I>
-__device__ __forceinline__ void pair_row(const char* tb, const char* tc, const float* rec, char* pm, int lane) {
+__device__ __forceinline__ void pair_row(const char* tb, const char* tc, const float* rec, float skip, char* pm, int lane) {
     constexpr int KT = S / 32;
     const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
     f32x4 a[I + 1];
@@ -169,8 +170,10 @@ __device__ __forceinline__ void pair_row(const char* tb, const char* tc, const f
             const float hi = rec[SSM_GH + 16 * I + jj], lo = rec[SSM_GL + 16 * I + jj];
             const f32x4 hj = num4(rec, SSM_GH, J, g), lj = num4(rec, SSM_GL, J, g);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                a[J][e] = 4 * g + e <= jj ? a[J][e] * fexp2((hi - hj[e]) + (lo - lj[e])) * d[e] : 0.f;
+            for (int e = 0; e < 4; ++e) {
+                const float v = formed(a[J][e] * fexp2((hi - hj[e]) + (lo - lj[e])));
+                a[J][e] = 4 * g + e <= jj ? fmaf(v, d[e], 4 * g + e == jj ? skip : 0.f) : 0.f;
+            }
         } else {
             float ri = rec[SSM_RI + 16 * I + jj];
             if (I > J + 1) ri *= rec[SSM_RI + 16 * J + 31];
@@ -187,14 +190,14 @@ __device__ __forceinline__ void pair_row(const char* tb, const char* tc, const f
 }
 // Half of it: five tiles each.
 template <int S>
-__device__ __forceinline__ void pair_half(int half, const char* tb, const float* rec, char* pm, int lane) {
+__device__ __forceinline__ void pair_half(int half, const char* tb, const float* rec, float skip, char* pm, int lane) {
     const char* tc = tb + FL::C;
     if (half == 0) {
-        pair_row<S, 3>(tb, tc, rec, pm, lane);
-        pair_row<S, 0>(tb, tc, rec, pm, lane);
+        pair_row<S, 3>(tb, tc, rec, skip, pm, lane);
+        pair_row<S, 0>(tb, tc, rec, skip, pm, lane);
     } else {
-        pair_row<S, 2>(tb, tc, rec, pm, lane);
-        pair_row<S, 1>(tb, tc, rec, pm, lane);
+        pair_row<S, 2>(tb, tc, rec, skip, pm, lane);
+        pair_row<S, 1>(tb, tc, rec, skip, pm, lane);
     }
 }
 
@@ -233,17 +236,11 @@ struct State {
         const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
         const float el = rec[SSM_EG + 63];
         Split<3> wx[2][2];
+        constexpr int W = REV ? SSM_EG : SSM_W;
         auto weigh = [&](int kk, int c) {
-            f32x4 w0, w1;
-            if (REV) {
-                w0 = num4(rec, SSM_EG, 2 * kk, g);
-                w1 = num4(rec, SSM_EG, 2 * kk + 1, g);
-            } else {
-                w0 = num4(rec, SSM_GA, 2 * kk, g) * num4(rec, SSM_DT, 2 * kk, g);
-                w1 = num4(rec, SSM_GA, 2 * kk + 1, g) * num4(rec, SSM_DT, 2 * kk + 1, g);
-            }
             const u32x4 xx = __builtin_bit_cast(u32x4, x_frag(tx, kk, c0 + 16 * c, ln));
-            wx[kk][c] = split_acc<3>(w0 * widen(u32x2{xx[0], xx[1]}), w1 * widen(u32x2{xx[2], xx[3]}));
+            wx[kk][c] = split_acc<3>(num4(rec, W, 2 * kk, g) * widen(u32x2{xx[0], xx[1]}),
+                                     num4(rec, W, 2 * kk + 1, g) * widen(u32x2{xx[2], xx[3]}));
         };
         bf16x8 bq[2][2];
         auto columns = [&](int q) {   // of step q: k step q / QS, tiles 2 (q % QS) ..
@@ -308,7 +305,7 @@ __global__ void __launch_bounds__(WT) kda_ssm_scan_kernel(const SsmParams p) {
         const int hl = tid - 512;
         const Rows bc[2] = {p.B, p.C};
         Tiles<S, 2> t;
-        Columns x, next, y;   // x of this chunk and of the next one
+        Columns x, y;
         Record r;
         if (k.on) {   // above the diagonal
 #pragma unroll
@@ -326,10 +323,7 @@ __global__ void __launch_bounds__(WT) kda_ssm_scan_kernel(const SsmParams p) {
         if (k.on) r.put(record(0), lane);
         if (nch > 1) {
             t.ask(bc, k, 1, hl);
-            if (k.on) {
-                r.ask(p, k, 1, lane);
-                next.ask(p.x, k, 1, lane);
-            }
+            if (k.on) r.ask(p, k, 1, lane);
         }
         lds_barrier();   // B, C and the records of the first chunk
         for (int i = 0; i < nch; ++i) {
@@ -341,7 +335,6 @@ __global__ void __launch_bounds__(WT) kda_ssm_scan_kernel(const SsmParams p) {
                     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 }
                 x.put(tx, ln);
-                x = next;
             }
             lds_barrier();   // 2
             if (i + 1 < nch) {
@@ -351,14 +344,12 @@ __global__ void __launch_bounds__(WT) kda_ssm_scan_kernel(const SsmParams p) {
             lds_barrier();   // 3
             {
                 const int ln = opaque(lane), hn = opaque(hl);
-                if (i + 2 < nch) {
-                    if (k.on) {
-                        next.ask(p.x, k, i + 2, ln);
-                        r.ask(p, k, i + 2, ln);
-                    }
-                    t.ask(bc, k, i + 2, hn);
-                }
+                if (k.on && i + 1 < nch) x.ask(p.x, k, i + 1, ln);
                 if (k.on && i > 0) y.store(p, k, i - 1, ln);
+                if (i + 2 < nch) {
+                    t.ask(bc, k, i + 2, hn);
+                    if (k.on) r.ask(p, k, i + 2, ln);
+                }
             }
         }
         lds_barrier();
@@ -381,7 +372,7 @@ __global__ void __launch_bounds__(WT) kda_ssm_scan_kernel(const SsmParams p) {
     const float skip = k.on && p.D ? p.D[k.head] : 0.f;
     if (nch > 0) {
         lds_barrier();
-        if (k.on) pair_half<S>(wave & 1, slot(0), numbers(0), pm, lane);
+        if (k.on) pair_half<S>(wave & 1, slot(0), numbers(0), skip, pm, lane);
     }
     for (int i = 0; i < nch; ++i) {
         lds_barrier();   // 1: B, C and the records, and the pair matrix at 2
@@ -423,7 +414,7 @@ __global__ void __launch_bounds__(WT) kda_ssm_scan_kernel(const SsmParams p) {
         }
         lds_barrier();   // 2: x
         u32x2 out[4][2];   // y as bf16
-        {   // y = e^G C S + D x, then the pairs' products
+        {   // y = e^G C S, then the pairs' products
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
             bf16x8 xf[2][2], pf[6];
             constexpr int FM[6] = {0, 1, 2, 3, 2, 3}, FK[6] = {0, 0, 0, 0, 1, 1};
@@ -438,8 +429,7 @@ __global__ void __launch_bounds__(WT) kda_ssm_scan_kernel(const SsmParams p) {
             for (int m = 0; m < 4; ++m) {
                 const float eg = rec[SSM_EG + 16 * m + jj];
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    y[m][c] = y[m][c] * eg + skip * widen(*reinterpret_cast<const u32x2*>(tx + x_off(16 * m + jj, x0 + 16 * c + 4 * g)));
+                for (int c = 0; c < 2; ++c) y[m][c] *= eg;
             }
 #pragma unroll
             for (int n = 1; n >= 0; --n) {
@@ -458,9 +448,9 @@ __global__ void __launch_bounds__(WT) kda_ssm_scan_kernel(const SsmParams p) {
             __builtin_amdgcn_sched_barrier(0);
         }
         lds_barrier();   // 3: the pair matrix is read
-        // one wave of two grows first, the other forms its pairs first
+        // of a SIMD's two waves one grows first, the other forms its pairs first
         const bool pairs = i + 1 < nch;
-        if (pairs && (wave & 1)) pair_half<S>(1, slot(i + 1), numbers(i + 1), pm, lane);
+        if (pairs && wave >= 4) pair_half<S>(wave & 1, slot(i + 1), numbers(i + 1), skip, pm, lane);
         z.template grow<false>(slot(i), tx, x0, rec, lane, [&]() {   // y in the place of x
             const int ln = opaque(lane);
 #pragma unroll
@@ -470,7 +460,7 @@ __global__ void __launch_bounds__(WT) kda_ssm_scan_kernel(const SsmParams p) {
                     *reinterpret_cast<u32x2*>(tx + x_off(16 * m + (ln & 15), x0 + 16 * c + 4 * (ln >> 4))) = out[m][c];
             }
         });
-        if (pairs && !(wave & 1)) pair_half<S>(0, slot(i + 1), numbers(i + 1), pm, lane);
+        if (pairs && wave < 4) pair_half<S>(wave & 1, slot(i + 1), numbers(i + 1), skip, pm, lane);
     }
     if (nch > 0) lds_barrier();   // the last chunk's y
     if (k.on && p.hT && k.sg.index == k.sg.count - 1)

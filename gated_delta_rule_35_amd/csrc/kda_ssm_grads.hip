@@ -94,9 +94,9 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
     __shared__ __attribute__((aligned(1024))) char smem[L::BYTES];
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, jj = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int R = p.H / p.G, hs = (R + p.sets - 1) / p.sets;
-    const int set = (int)(blockIdx.x % p.sets), group = (int)(blockIdx.x / p.sets % p.G);
-    const int64_t slot = blockIdx.x / p.sets / p.G;
+    const int R = uniform(p.H / p.G), hs = uniform((R + p.sets - 1) / p.sets);
+    const int set = uniform((int)(blockIdx.x % p.sets)), group = uniform((int)(blockIdx.x / p.sets % p.G));
+    const int64_t slot = uniform((int)(blockIdx.x / p.sets / p.G));
     const SsmChunk ch = ssm_chunk(p, slot);
     if (ch.rows == 0) return;
     const int h_from = group * R + set * hs, h_to = group * R + ((set + 1) * hs < R ? (set + 1) * hs : R);
@@ -226,8 +226,8 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
                 const f32x4 h4 = num4(rec, SSM_GH, I, g), l4 = num4(rec, SSM_GL, I, g);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    l[e] = jj <= 4 * g + e ? fexp2((h4[e] - hi) + (l4[e] - lo)) : 0.f;
-                    lt[e] = 4 * g + e <= jj ? fexp2((hi - h4[e]) + (lo - l4[e])) : 0.f;
+                    l[e] = formed(fexp2((h4[e] - hi) + (l4[e] - lo)));
+                    lt[e] = formed(fexp2((hi - h4[e]) + (lo - l4[e])));
                 }
             } else {
                 float mid = 1.f;

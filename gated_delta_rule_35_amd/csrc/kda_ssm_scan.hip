@@ -43,7 +43,9 @@ __global__ void __launch_bounds__(256) kda_ssm_gates_kernel(const SsmParams p) {
     float* r = reinterpret_cast<float*>(p.rec + (slot * p.H + h) * SSM_REC) + lane;
     r[SSM_DT] = d;
     r[SSM_EG] = gate_exp(G);
-    r[SSM_GA] = gate_ratio(last, G);
+    const float ga = gate_ratio(last, G);
+    r[SSM_GA] = ga;
+    r[SSM_W] = ga * d;
     r[SSM_GH] = G.hi;
     r[SSM_GL] = G.lo;
     r[SSM_RI] = gate_ratio(G, s);
@@ -184,8 +186,8 @@ __device__ __forceinline__ void ssm_walk(const SsmParams& p, char* smem, int blo
                 w0 = num4(rec, SSM_EG, 2 * kk, g);
                 w1 = num4(rec, SSM_EG, 2 * kk + 1, g);
             } else {
-                w0 = num4(rec, SSM_GA, 2 * kk, g) * num4(rec, SSM_DT, 2 * kk, g);
-                w1 = num4(rec, SSM_GA, 2 * kk + 1, g) * num4(rec, SSM_DT, 2 * kk + 1, g);
+                w0 = num4(rec, SSM_W, 2 * kk, g);
+                w1 = num4(rec, SSM_W, 2 * kk + 1, g);
             }
             Split<3> wx[2];
 #pragma unroll

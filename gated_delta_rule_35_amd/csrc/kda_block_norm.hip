@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(NT) kda_block_norm_kernel(const BlockNormParam
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             if (GATED) {
-                g[k][e] = activation(p.act, g[k][e]);
+                g[k][e] = activation(p.act, g[k][e], sigmoid<XT == 2>(g[k][e]));
                 if (p.first) v[k][e] *= g[k][e];
             } else {
                 v[k][e] = fmaf(p.scale, v[k][e], g[k][e]);
@@ -165,23 +165,26 @@ __global__ void __launch_bounds__(NT) kda_block_norm_bwd_kernel(const BlockNormP
     for (int64_t base = first, i = walk.first; base < walk.end; base += walk.step, i += walk.step, ++turn) {
         const Inputs in = next;
         if (base + walk.step < walk.end) load(i + walk.step, next);
-        float v[K][8], a[K][8], b[K][8], sv = 0.f, sd = 0.f;   // a: the gate's activation, b: dn, then what is stored
+        float v[K][8], s[K][8], sv = 0.f, sd = 0.f;   // s: sigmoid of the gate
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const bool on = 8 * (l + k * L) < p.D;
-            float dy[8];
+            float dy[8], z[8];
             Elems<VT>::widen(in.v[k], v[k]);
             Elems<XT>::widen(in.dy[k], dy);
-            if (GATED) Elems<VT>::widen(in.z[k], a[k]);
+            if (GATED) Elems<VT>::widen(in.z[k], z);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                if (GATED) a[k][e] = activation(p.act, a[k][e]);
-                const float x = GATED && p.first ? v[k][e] * a[k][e] : v[k][e];
-                const float d = GATED && !p.first ? dy[e] * a[k][e] : dy[e];
-                if (on) {
-                    sv = fmaf(x, x, sv);
-                    sd = fmaf(x, d * w[k][e], sd);
+                float x = v[k][e], d = dy[e];
+                if (GATED) {
+                    s[k][e] = sigmoid<XT == 2>(z[e]);
+                    const float a = activation(p.act, z[e], s[k][e]);
+                    x = p.first ? x * a : x;
+                    d = p.first ? d : d * a;
                 }
+                if (!on) x = d = 0.f;
+                sv = fmaf(x, x, sv);
+                sd = fmaf(x, d * w[k][e], sd);
             }
         }
         const float rr = 1.f / sqrtf(row_sum<L>(sv, sh, 2 * turn) / (float)p.D + p.eps);
@@ -191,45 +194,44 @@ __global__ void __launch_bounds__(NT) kda_block_norm_bwd_kernel(const BlockNormP
         for (int k = 0; k < K; ++k) {
             const int c = 8 * (l + k * L);
             if (c >= p.D) continue;
-            float dy[8], z[8];
+            float dy[8], z[8], b[8];
             Elems<XT>::widen(in.dy[k], dy);
             if (GATED || p.dh) Elems<VT>::widen(in.z[k], z);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 if (GATED) {
-                    float g, slope;
-                    activation(p.act, z[e], g, slope);
+                    const float g = activation(p.act, z[e], s[k][e]);
                     const float x = p.first ? v[k][e] * g : v[k][e];
                     const float d = p.first ? dy[e] : dy[e] * g;
                     dw[k][e] = fmaf(d * rr, x, dw[k][e]);
                     const float dv = rr * (d * w[k][e] - x * m);
-                    b[k][e] = p.first ? dv * g : dv;
-                    z[e] = slope * (p.first ? dv * v[k][e] : dy[e] * (x * rr * w[k][e]));
+                    b[e] = p.first ? dv * g : dv;
+                    z[e] = slope(p.act, z[e], s[k][e]) * (p.first ? dv * v[k][e] : dy[e] * (x * rr * w[k][e]));
                 } else {
                     dw[k][e] = fmaf(dy[e] * rr, v[k][e], dw[k][e]);
                     const float dv = rr * (dy[e] * w[k][e] - v[k][e] * m);
                     z[e] = p.dh ? z[e] + dv : dv;
-                    b[k][e] = p.scale * z[e];
+                    b[e] = p.scale * z[e];
                 }
             }
-            Elems<XT>::store(p.dx, i * p.D + c, b[k]);
+            Elems<XT>::store(p.dx, i * p.D + c, b);
             Elems<VT>::store(p.dz, i * p.D + c, z);
         }
     }
     if (!p.dw) return;
     // the work-group's rows, in the order of their lanes; work-group g of head h leaves row g of [..][H][D]
     float* part = p.part + (int64_t)blockIdx.x * p.D;
-    float* s = sh + 8;
+    float* sums = sh + 8;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[8 * threadIdx.x + e] = dw[k][e];
+        for (int e = 0; e < 8; ++e) sums[8 * threadIdx.x + e] = dw[k][e];
         __syncthreads();
         for (int c = threadIdx.x; c < 8 * L; c += NT) {
             float t = 0.f;
 #pragma unroll
-            for (int r = 0; r < R; ++r) t += s[8 * L * r + c];
+            for (int r = 0; r < R; ++r) t += sums[8 * L * r + c];
             if (c + 8 * k * L < p.D) part[c + 8 * k * L] = t;
         }
     }
@@ -264,8 +266,10 @@ hipError_t forward(const BlockNormParams& p, hipStream_t stream) {
         by_width(p.D, [&](auto l, auto k) {
             constexpr int XT = decltype(xt)::value, L = decltype(l)::value, K = decltype(k)::value, R = NT / L;
             const dim3 grid((unsigned)((p.rows + R - 1) / R));
-            if (!GATED && p.wide) hipLaunchKernelGGL((kda_block_norm_kernel<GATED, XT, 2, L, K>), grid, dim3(NT), 0, stream, p);
-            else hipLaunchKernelGGL((kda_block_norm_kernel<GATED, XT, XT, L, K>), grid, dim3(NT), 0, stream, p);
+            auto kernel = kda_block_norm_kernel<GATED, XT, XT, L, K>;
+            if constexpr (!GATED)
+                if (p.wide) kernel = kda_block_norm_kernel<GATED, XT, 2, L, K>;
+            hipLaunchKernelGGL(kernel, grid, dim3(NT), 0, stream, p);
         });
     });
     return hipGetLastError();
@@ -282,10 +286,10 @@ hipError_t backward(const BlockNormParams& p, hipStream_t stream) {
                 groups = (per + R - 1) / R;
                 if (p.dw) groups = std::min<int64_t>(groups, std::max<int64_t>(BLOCK_DW_GROUPS / heads, 1));
                 const dim3 grid((unsigned)(groups * heads));
-                if (!GATED && p.wide)
-                    hipLaunchKernelGGL((kda_block_norm_bwd_kernel<GATED, XT, 2, L, K>), grid, dim3(NT), 0, stream, p);
-                else
-                    hipLaunchKernelGGL((kda_block_norm_bwd_kernel<GATED, XT, XT, L, K>), grid, dim3(NT), 0, stream, p);
+                auto kernel = kda_block_norm_bwd_kernel<GATED, XT, XT, L, K>;
+                if constexpr (!GATED)
+                    if (p.wide) kernel = kda_block_norm_bwd_kernel<GATED, XT, 2, L, K>;
+                hipLaunchKernelGGL(kernel, grid, dim3(NT), 0, stream, p);
             });
         });
         const hipError_t e = hipGetLastError();

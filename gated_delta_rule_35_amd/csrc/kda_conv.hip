@@ -106,6 +106,16 @@ __device__ __forceinline__ void shift(float (&x)[W][8]) {
     }
 }
 
+// act(z) and its derivative, of results of type XT.
+template <int XT, int ACT>
+__device__ __forceinline__ float act_of(float z) {
+    return ACT == ACT_NONE ? z : activation(ACT, z, sigmoid<XT == 2>(z));
+}
+template <int XT, int ACT>
+__device__ __forceinline__ float slope_of(float z) {
+    return ACT == ACT_NONE ? 1.f : slope(ACT, z, sigmoid<XT == 2>(z));
+}
+
 // The thread's channels and the first token of its run.
 struct Place {
     int c, run;
@@ -163,7 +173,7 @@ __global__ void __launch_bounds__(NT) kda_conv_kernel(const ConvParams p, const 
                 Elems<XT>::widen(raw[u], x[W - 1]);
                 float y[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = activation(ACT, f.at(x, e));
+                for (int e = 0; e < 8; ++e) y[e] = act_of<XT, ACT>(f.at(x, e));
                 if (i + u < m) Elems<XT>::store(p.y, (t + i + u) * p.C + q.c, y);
             }
         }
@@ -202,9 +212,7 @@ __global__ void __launch_bounds__(NT) kda_conv_bwd_kernel(const ConvParams p, co
             Elems<XT>::widen(Elems<XT>::load(p.dy, (s.a + t) * p.C + c), dy);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float y, slope;
-                activation(ACT, f.at(x, e), y, slope);
-                const float dz = dy[e] * slope;
+                const float dz = dy[e] * slope_of<XT, ACT>(f.at(x, e));
 #pragma unroll
                 for (int r = t; r < W - 1; ++r) g[r][e] = fmaf(f.w[r - t][e], dz, g[r][e]);
             }
@@ -254,9 +262,7 @@ __global__ void __launch_bounds__(NT) kda_conv_bwd_kernel(const ConvParams p, co
                     Elems<XT>::widen(rd[u], dy);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        float y, slope;
-                        activation(ACT, f.at(x, e), y, slope);
-                        const float d = j < real ? dy[e] * slope : 0.f;
+                        const float d = j < real ? dy[e] * slope_of<XT, ACT>(f.at(x, e)) : 0.f;
                         dz[W - 1][e] = d;
                         if (j < m) {
 #pragma unroll
@@ -309,7 +315,7 @@ __global__ void __launch_bounds__(NT) kda_conv_bwd_kernel(const ConvParams p, co
 namespace {
 constexpr int DT = 128;
 }
-template <int XT, int W>
+template <int XT, int W, int ACT>
 __global__ void __launch_bounds__(DT) kda_conv_decode_kernel(const ConvParams p) {
     const int pieces = p.C / 8, cols = (pieces + DT - 1) / DT;
     const int n0 = blockIdx.x / cols, piece = (int)(blockIdx.x % cols) * DT + threadIdx.x;
@@ -336,18 +342,18 @@ __global__ void __launch_bounds__(DT) kda_conv_decode_kernel(const ConvParams p)
             for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
         }
     }
-    for (int n = n0; n < p.N; ++n) {
-        if (n != n0 && (!more || p.idx[n] != slot)) {
-            if (!more) break;
-            continue;
-        }
+    int n = n0;
+    do {
         shift(x);
         Elems<XT>::widen(Elems<XT>::load(p.x, n * p.sb + c), x[W - 1]);
         float y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = activation(p.silu, f.at(x, e));
+        for (int e = 0; e < 8; ++e) y[e] = act_of<XT, ACT>(f.at(x, e));
         Elems<XT>::store(p.y, (int64_t)n * p.C + c, y);
-    }
+        if (!more) break;
+        do ++n;
+        while (n < p.N && p.idx[n] != slot);
+    } while (n < p.N);
 #pragma unroll
     for (int i = 1; i < W; ++i) Elems<XT>::store(p.s_out, ((int64_t)slot * (W - 1) + i - 1) * p.C + c, x[i]);
 }
@@ -420,7 +426,7 @@ struct Backward {
 template <int XT, int W, int ACT>
 struct Decode {
     static void run(const ConvParams& p, unsigned blocks, hipStream_t s) {
-        hipLaunchKernelGGL((kda_conv_decode_kernel<XT, W>), dim3(blocks), dim3(DT), 0, s, p);
+        hipLaunchKernelGGL((kda_conv_decode_kernel<XT, W, ACT>), dim3(blocks), dim3(DT), 0, s, p);
     }
 };
 }  // namespace

@@ -73,26 +73,20 @@ __device__ __forceinline__ float exp_of(float x) {
     const float h = x * LOG2E, l = fmaf(x, LOG2E, -h) + x * 1.92596299e-8f;
     return fexp2(h) * fmaf(l, LN2, 1.f);
 }
-// 1 / (1 + e^-z), and z times it.
-__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + exp_of(-z)); }
+// 1 / (1 + e^-z).  FULL: to fp32's accuracy; else e^-z as 2^{-z log2 e}, off by up to |z| 2^-24 of
+// itself, far below the half step of a 16-bit result.
+template <bool FULL>
+__device__ __forceinline__ float sigmoid(float z) {
+    return __builtin_amdgcn_rcpf(1.f + (FULL ? exp_of(-z) : fexp2(-LOG2E * z)));
+}
 
 enum { ACT_NONE = 0, ACT_SILU = 1, ACT_SIGMOID = 2 };
-// act(z), and its derivative where `slope` is wanted.
-__device__ __forceinline__ float activation(int act, float z) {
-    if (act == ACT_NONE) return z;
-    const float s = sigmoid(z);
-    return act == ACT_SILU ? z * s : s;
+// act(z) and its derivative from s = sigmoid(z): z s and s (1 + z (1 - s)), or s and s (1 - s).
+__device__ __forceinline__ float activation(int act, float z, float s) {
+    return act == ACT_NONE ? z : (act == ACT_SILU ? z : 1.f) * s;
 }
-__device__ __forceinline__ void activation(int act, float z, float& y, float& slope) {
-    if (act == ACT_NONE) {
-        y = z;
-        slope = 1.f;
-        return;
-    }
-    const float e = exp_of(-z), s = __builtin_amdgcn_rcpf(1.f + e);
-    const float r = e >= 0x1p100f ? 1.f : e * s;   // 1 - s without its cancellation
-    y = act == ACT_SILU ? z * s : s;
-    slope = act == ACT_SILU ? s * fmaf(z, r, 1.f) : s * r;
+__device__ __forceinline__ float slope(int act, float z, float s) {
+    return act == ACT_NONE ? 1.f : s * fmaf(act == ACT_SILU ? z : 1.f, 1.f - s, act == ACT_SILU ? 1.f : 0.f);
 }
 
 }  // namespace kda

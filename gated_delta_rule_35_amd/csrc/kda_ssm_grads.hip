@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(1024) kda_ssm_numbers_kernel(const SsmParams p
         const float q = lane_f32(x, 0), t20 = lane_f32(x, 12), t30 = lane_f32(x, 13), t31 = lane_f32(x, 14);
         float slope = 1.f;
         if (p.softplus && lane < ch.rows)
-            slope = sigmoid(ssm_raw(p.dt, p.dt_f32, ch.row * p.dtb + (ch.tok + lane) * p.dtt + h, p.bias, h));
+            slope = sigmoid<true>(ssm_raw(p.dt, p.dt_f32, ch.row * p.dtb + (ch.tok + lane) * p.dtt + h, p.bias, h));
         float da = suffix16(rs, lane) + before16(prefix16(cs * d)) + dr + (I == 1 ? t20 + t30 : I == 2 ? t30 + t31 : 0.f);
         da += suffix_wave(y, lane) + before_wave(prefix_wave(u * d), lane) + q;
         if (lane < ch.rows) {

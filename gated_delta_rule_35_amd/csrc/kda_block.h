@@ -38,7 +38,7 @@ struct ConvSplit {
     int32_t run, lanes;
     int64_t tiles, cols;   // work-groups along the tokens and along the channels
 };
-ConvSplit conv_split(int64_t total, int64_t C);
+ConvSplit conv_split(int64_t total, int64_t C, bool bwd);
 
 hipError_t launch_conv(const ConvParams& p, hipStream_t stream);
 hipError_t launch_conv_bwd(const ConvParams& p, hipStream_t stream);

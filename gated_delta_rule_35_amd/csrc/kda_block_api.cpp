@@ -98,8 +98,10 @@ kda_status_t conv_batch(const kda_tensor_t* x, const kda_tensor_t* cu, kda::Conv
     p.N = static_cast<int32_t>(N);
     p.T = T;
     p.total = B * T;
-    const kda::ConvSplit k = kda::conv_split(p.total, p.C);
-    if (k.tiles * k.cols + (N * (p.W - 1) * (p.C / 8)) / 256 + 1 > kMaxGrid) return KDA_ERR_UNSUPPORTED;
+    for (const bool bwd : {false, true}) {
+        const kda::ConvSplit k = kda::conv_split(p.total, p.C, bwd);
+        if (k.tiles * k.cols + (N * (p.W - 1) * (p.C / 8)) / 256 + 1 > kMaxGrid) return KDA_ERR_UNSUPPORTED;
+    }
     return KDA_OK;
 }
 kda_status_t check_conv_state(const kda_tensor_t* t, const kda::ConvParams& p, kda_dtype_t type, int64_t n) {
@@ -138,7 +140,7 @@ int64_t kda_conv_bwd_workspace_size(int64_t total_tokens, int64_t channels, int6
     if (total_tokens < 0 || total_tokens > kMaxTokens || channels < 0 || channels > kMaxConvChannels || width < 0 || width > 4)
         return -1;
     if (channels == 0) return 0;
-    return kda::conv_split(total_tokens, channels).tiles * (width + 1) * channels * 4;
+    return kda::conv_split(total_tokens, channels, true).tiles * (width + 1) * channels * 4;
 }
 
 kda_status_t kda_conv_bwd(const kda_tensor_t* x, const kda_tensor_t* weight, const kda_tensor_t* bias, int32_t activation,

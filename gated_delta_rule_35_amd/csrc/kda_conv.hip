@@ -11,6 +11,7 @@
 // and runs of up to 1 KB.  Eight rows are asked for at a time.  States are formed by
 // work-groups of their own from the rows that make them up.  Sums are fp32, rounded once; the weights'
 // gradients are summed over a run, then a work-group's runs, then the work-groups, each in order.
+#include <algorithm>
 #include <type_traits>
 
 #include "kda_block.h"
@@ -183,8 +184,8 @@ __global__ void __launch_bounds__(NT) kda_conv_kernel(const ConvParams p, const 
 // Gradients.  The walk goes W - 1 tokens past the run, within the sequence: dx of a token is whole
 // once dz of the W - 1 tokens after it is known.
 template <int XT, int W, int ACT>
-__global__ void __launch_bounds__(NT) kda_conv_bwd_kernel(const ConvParams p, const ConvSplit k) {
-    constexpr int U = 4;
+__global__ void __launch_bounds__(NT, 2) kda_conv_bwd_kernel(const ConvParams p, const ConvSplit k) {
+    constexpr int U = XT == 2 ? 2 : 4;   // rows that are asked for ahead, within the registers
     __shared__ __attribute__((aligned(16))) float sh[NT][8];
     const int64_t tiles = k.tiles * k.cols;
     if (blockIdx.x >= tiles) {   // gradients of the initial states, a thread eight channels of a sequence
@@ -244,14 +245,15 @@ __global__ void __launch_bounds__(NT) kda_conv_bwd_kernel(const ConvParams p, co
             }
             const int64_t base = x_at(p, s, t) + q.c, left = s.e - t;
             const int m = (int)(e1 - t), real = left < m + W - 1 ? (int)left : m + W - 1;   // tokens whose dz counts
-            for (int i = 0; i < m + W - 1; i += U) {
-                typename Elems<XT>::Raw rx[U], rd[U];
+            typename Elems<XT>::Raw rx[U], rd[U];
+            auto ask = [&](int u, int j) {
+                const int at = j < real ? j : real - 1;
+                rx[u] = Elems<XT>::load(p.x, base + at * p.st);
+                rd[u] = Elems<XT>::load(p.dy, (t + at) * p.C + q.c);
+            };
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int at = i + u < real ? i + u : real - 1;
-                    rx[u] = Elems<XT>::load(p.x, base + at * p.st);
-                    rd[u] = Elems<XT>::load(p.dy, (t + at) * p.C + q.c);
-                }
+            for (int u = 0; u < U; ++u) ask(u, u);
+            for (int i = 0; i < m + W - 1; i += U) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int j = i + u;
@@ -260,18 +262,22 @@ __global__ void __launch_bounds__(NT) kda_conv_bwd_kernel(const ConvParams p, co
                     shift(dz);
                     Elems<XT>::widen(rx[u], x[W - 1]);
                     Elems<XT>::widen(rd[u], dy);
+                    ask(u, j + U);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float d = j < real ? dy[e] * slope_of<XT, ACT>(f.at(x, e)) : 0.f;
-                        dz[W - 1][e] = d;
-                        if (j < m) {
-#pragma unroll
-                            for (int o = 0; o < W; ++o) dw[o][e] = fmaf(d, x[o][e], dw[o][e]);
-                            dw[W][e] += d;
-                        }
+                        const float d = formed(dy[e] * slope_of<XT, ACT>(f.at(x, e)));
+                        dz[W - 1][e] = j < real ? d : 0.f;
                         g[e] = 0.f;
 #pragma unroll
                         for (int o = 0; o < W; ++o) g[e] = fmaf(f.w[W - 1 - o][e], dz[o][e], g[e]);
+                    }
+                    if (j < m) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+#pragma unroll
+                            for (int o = 0; o < W; ++o) dw[o][e] = fmaf(dz[W - 1][e], x[o][e], dw[o][e]);
+                            dw[W][e] += dz[W - 1][e];
+                        }
                     }
                     const int64_t back = t + j - (W - 1);   // the token whose dx is whole
                     if (j >= W - 1 && j < m + W - 1) {
@@ -384,13 +390,19 @@ hipError_t launch_sum_rows(const SumParams& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-ConvSplit conv_split(int64_t total, int64_t C) {
+ConvSplit conv_split(int64_t total, int64_t C, bool bwd) {
+    const int64_t pieces = C / 8;
     ConvSplit k{};
     k.lanes = 64;
-    while (k.lanes > 1 && k.lanes / 2 * 8 >= C) k.lanes /= 2;
-    k.cols = (C + 8 * k.lanes - 1) / (8 * k.lanes);
-    // Long runs read fewer rows twice, short ones fill the device.
-    k.run = total * (C / 8) >= (int64_t(1) << 22) ? 32 : 8;
+    while (k.lanes > 1 && k.lanes / 2 >= pieces) k.lanes /= 2;
+    while (k.lanes > 16 && (pieces + k.lanes - 1) / k.lanes * k.lanes - pieces > pieces / 32) k.lanes /= 2;
+    k.cols = (pieces + k.lanes - 1) / k.lanes;
+    if (bwd) {
+        const int64_t once = (total * pieces + 64 * 2048 - 1) / (64 * 2048);
+        k.run = (int)std::min<int64_t>(std::max<int64_t>((once + 1) / 2 * 2, 8), 64);
+    } else {
+        k.run = total * pieces >= (int64_t(1) << 22) ? 32 : 8;
+    }
     k.tiles = (total + (int64_t)k.run * (NT / k.lanes) - 1) / ((int64_t)k.run * (NT / k.lanes));
     return k;
 }
@@ -432,7 +444,7 @@ struct Decode {
 }  // namespace
 
 hipError_t launch_conv(const ConvParams& p, hipStream_t stream) {
-    const ConvSplit k = conv_split(p.total, p.C);
+    const ConvSplit k = conv_split(p.total, p.C, false);
     const int64_t states = p.s_out ? ((int64_t)p.N * (p.W - 1) * (p.C / 8) + NT - 1) / NT : 0;
     const int64_t blocks = k.tiles * k.cols + states;
     if (blocks == 0) return hipSuccess;
@@ -441,7 +453,7 @@ hipError_t launch_conv(const ConvParams& p, hipStream_t stream) {
 }
 
 hipError_t launch_conv_bwd(const ConvParams& p, hipStream_t stream) {
-    const ConvSplit k = conv_split(p.total, p.C);
+    const ConvSplit k = conv_split(p.total, p.C, true);
     const int64_t states = p.ds_in ? ((int64_t)p.N * (p.C / 8) + NT - 1) / NT : 0;
     const int64_t blocks = k.tiles * k.cols + states;
     if (blocks > 0) {

@@ -73,6 +73,13 @@ __device__ __forceinline__ float exp_of(float x) {
     const float h = x * LOG2E, l = fmaf(x, LOG2E, -h) + x * 1.92596299e-8f;
     return fexp2(h) * fmaf(l, LN2, 1.f);
 }
+// x, formed where this stands: the compiler would put what a select drops behind a branch, which
+// parts matrix instructions (and a row's elements) from what could run beside them.
+__device__ __forceinline__ float formed(float x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // 1 / (1 + e^-z).  FULL: to fp32's accuracy; else e^-z as 2^{-z log2 e}, off by up to |z| 2^-24 of
 // itself, far below the half step of a 16-bit result.
 template <bool FULL>

@@ -11,13 +11,6 @@ __device__ __forceinline__ int64_t uniform(int64_t x) {
     const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)x), hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32));
     return (int64_t)(((uint64_t)hi << 32) | lo);
 }
-// x, formed where this stands: the compiler would put what a select drops behind a branch, which
-// parts matrix instructions from what could run beside them.
-__device__ __forceinline__ float formed(float x) {
-    asm volatile("" : "+v"(x));
-    return x;
-}
-
 // A token's step: dt + bias, or log(1 + e^{dt + bias}) of it.
 __device__ __forceinline__ float ssm_raw(const void* dt, int f32, int64_t i, const float* bias, int h) {
     const float v = gdr_beta(dt, f32, i);

@@ -17,8 +17,9 @@
 // through LDS, for dx.  The 64 x 64 matrices are ten tiles, dealt to the waves; they leave as
 // operand fragments for the second half of a head's work.
 //
-// Precision.  What reaches ddt and the sums enters in three bf16 parts (S and dS in V and W, 24
-// bits), what only reaches bf16 results in two (K, E, and dS in dx).
+// Precision.  S, dS, K and E enter in two bf16 parts each, off by 2^-18 of themselves at most, beside
+// operands that are bf16 as they come: the results in bf16 round at 2^-9, and ddt and the sums, which
+// add up thousands of such products, take part in steps of a dt that is mostly bf16 itself.
 #include "kda_block.h"
 #include "kda_ssm_device.h"
 
@@ -40,7 +41,11 @@ struct GL {
 };
 static_assert(GL<128>::BYTES <= 163840, "LDS");
 
-// Byte of piece q (16 bytes) of row r, and of 8-byte half h of it.
+// Byte of a 16-byte piece of a row of dS's tile: written from rows 8 a + b and read from four rows each of
+// 8 g, its pieces are permuted by the rows' bits 0, 1, 3 and 4.
+__device__ __forceinline__ int ds_off(int row, int piece) {
+    return row * 256 + ((piece ^ (((row & 3) << 2) | ((row >> 3) & 3))) << 4);
+}
 __device__ __forceinline__ bf16x8 two8(const char* tile, int row, int at) {   // elements at .. + 3 and 16 more on
     const int q = at >> 3, b = 2 * (at & 7);
     return join(*reinterpret_cast<const u32x2*>(tile + tile_off(row, q) + b),
@@ -138,17 +143,16 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
     }
     // A head's inputs, asked for ahead
     u32x4 nx[PX], ny[PX], nrec;
-    f32x4 ns[KP][2], nds[KP][2];
+    u32x4 ns[KP][2], nds[KP][2];   // two parts of S and of dS, 32 columns each
     const int lr = P == 64 ? tid >> 3 : tid >> 4, lp = P == 64 ? tid & 7 : tid & 15;   // row and piece of this thread
     auto ask = [&](int h) {
+        const auto rx = chunk_rsrc(p.x.p + ch.row * p.x.sb + ch.tok * p.x.st + h * p.x.sh, p.x.st, ch.rows, P);
+        const auto ry = chunk_rsrc(p.dO.p + ch.row * p.dO.sb + ch.tok * p.dO.st + h * p.dO.sh, p.dO.st, ch.rows, P);
 #pragma unroll
-        for (int u = 0; u < PX; ++u) {
+        for (int u = 0; u < PX; ++u) {   // rows past the chunk's end come as zeros
             const int r = lr + 32 * u;
-            nx[u] = ny[u] = u32x4{0, 0, 0, 0};
-            if (r < ch.rows) {
-                nx[u] = *reinterpret_cast<const u32x4*>(p.x.p + ch.row * p.x.sb + (ch.tok + r) * p.x.st + h * p.x.sh + 8 * lp);
-                ny[u] = *reinterpret_cast<const u32x4*>(p.dO.p + ch.row * p.dO.sb + (ch.tok + r) * p.dO.st + h * p.dO.sh + 8 * lp);
-            }
+            nx[u] = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(r * p.x.st * 2) + 16 * lp, 0, 0);
+            ny[u] = __builtin_amdgcn_raw_buffer_load_b128(ry, (int)(r * p.dO.st * 2) + 16 * lp, 0, 0);
         }
         if (tid < SSM_REC / 16) nrec = *reinterpret_cast<const u32x4*>(p.rec + (slot * p.H + h) * SSM_REC + 16 * tid);
     };
@@ -157,10 +161,10 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
 #pragma unroll
         for (int pp = from; pp < to; ++pp) {
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct) {
-                const int64_t at = unit * S * P + pp * (S * 32) + t * 512 + 8 * lane + 4 * ct;
-                ns[pp][ct] = *reinterpret_cast<const f32x4*>(p.St + at);
-                nds[pp][ct] = *reinterpret_cast<const f32x4*>(p.dSt + at);
+            for (int n = 0; n < 2; ++n) {
+                const int64_t at = unit * S * P + pp * (S * 32) + t * 512;
+                ns[pp][n] = *reinterpret_cast<const u32x4*>(p.St + at + (8 * lane + 4 * n));
+                nds[pp][n] = *reinterpret_cast<const u32x4*>(p.dSt + at + (8 * lane + 4 * n));
             }
         }
     };
@@ -297,8 +301,8 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
         auto put_ds = [&](int q, int n, u32x4 w, int row, int g) {   // part n of 32 columns
             const int at = 64 * n + 32 * q + 4 * g;
             char* to = smem + L::DS + 2 * (at & 7);
-            *reinterpret_cast<u32x2*>(to + tile_off(row, at >> 3)) = u32x2{w[0], w[1]};
-            *reinterpret_cast<u32x2*>(to + tile_off(row, (at >> 3) + 2)) = u32x2{w[2], w[3]};
+            *reinterpret_cast<u32x2*>(to + ds_off(row, at >> 3)) = u32x2{w[0], w[1]};
+            *reinterpret_cast<u32x2*>(to + ds_off(row, (at >> 3) + 2)) = u32x2{w[2], w[3]};
         };
         {
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
@@ -306,47 +310,40 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
             f32x4 v[MW], w[MW];
 #pragma unroll
             for (int mi = 0; mi < MW; ++mi) v[mi] = w[mi] = zero;
-            float dot = 0.f;
+            f32x4 dot = zero;   // S dS^T of the wave's channels: its diagonal sums to <S, dS>
 #pragma unroll
             for (int pp = 0; pp < KP; ++pp) {
+                bf16x8 fs[2], fd[2], fx[MW], fy[MW];
 #pragma unroll
-                for (int ct = 0; ct < 2; ++ct) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) dot = fmaf(ns[pp][ct][i], nds[pp][ct][i], dot);
+                for (int n = 0; n < 2; ++n) {
+                    fs[n] = __builtin_bit_cast(bf16x8, ns[pp][n]);
+                    fd[n] = __builtin_bit_cast(bf16x8, nds[pp][n]);
+                    if (pp >= 2) later[pp - 2][n] = nds[pp][n];
+                    else if (S == 128 || wave < 4) put_ds(pp, n, nds[pp][n], nrow, g);
                 }
-                {
-                    const Split<3> dsp = split_acc<3>(nds[pp][0], nds[pp][1]);
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const u32x4 part = __builtin_bit_cast(u32x4, dsp.s[n]);
-                        if (pp >= 2) later[pp - 2][n] = part;
-                        else if (S == 128 || wave < 4) put_ds(pp, n, part, nrow, g);
-                    }
-                    bf16x8 f[MW];
-#pragma unroll
-                    for (int mi = 0; mi < MW; ++mi) f[mi] = two8(tx, 16 * (m0 + mi) + jj, 32 * pp + 4 * g);
-#pragma unroll
-                    for (int n = 2; n >= 0; --n) {
-#pragma unroll
-                        for (int mi = 0; mi < MW; ++mi) v[mi] = mfma_bf(dsp.s[n], f[mi], v[mi]);
-                    }
+                for (int mi = 0; mi < MW; ++mi) {
+                    fx[mi] = two8(tx, 16 * (m0 + mi) + jj, 32 * pp + 4 * g);
+                    fy[mi] = two8(ty, 16 * (m0 + mi) + jj, YO + 32 * pp + 4 * g);
                 }
-                __builtin_amdgcn_sched_barrier(0);
-                {
-                    const Split<3> sp = split_acc<3>(ns[pp][0], ns[pp][1]);
-                    bf16x8 f[MW];
 #pragma unroll
-                    for (int mi = 0; mi < MW; ++mi) f[mi] = two8(ty, 16 * (m0 + mi) + jj, YO + 32 * pp + 4 * g);
+                for (int n = 1; n >= 0; --n) {
 #pragma unroll
-                    for (int n = 2; n >= 0; --n) {
-#pragma unroll
-                        for (int mi = 0; mi < MW; ++mi) w[mi] = mfma_bf(sp.s[n], f[mi], w[mi]);
+                    for (int mi = 0; mi < MW; ++mi) {
+                        v[mi] = mfma_bf(fd[n], fx[mi], v[mi]);
+                        w[mi] = mfma_bf(fs[n], fy[mi], w[mi]);
                     }
                 }
+                dot = mfma_bf(fs[1], fd[0], dot);
+                dot = mfma_bf(fs[0], fd[1], dot);
+                dot = mfma_bf(fs[0], fd[0], dot);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            dot = sum64(dot);
-            if (ln == 0) sS[wave] = S == 128 || wave < 4 ? dot : 0.f;
+            float q = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q += 4 * g + i == jj ? dot[i] : 0.f;
+            q = sum64(q);
+            if (ln == 0) sS[wave] = S == 128 || wave < 4 ? q : 0.f;
 #pragma unroll
             for (int mi = 0; mi < MW; ++mi) {
                 const int m = m0 + mi;
@@ -411,7 +408,9 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
                 const bf16x8 b0 = row_frag(tb, ma, kk, g, jj), b1 = row_frag(tb, ma + 1, kk, g, jj);
 #pragma unroll
                 for (int n = 1; n >= 0; --n) {
-                    const bf16x8 d = two_tr(smem + L::DS, 32 * kk + 8 * g, 32 * kk + 8 * g + 4, 64 * n + 16 * pt, jj);
+                    const int q = 8 * n + 2 * pt + ((jj & 3) >> 1), r = 32 * kk + 8 * g + (jj >> 2);
+                    const char* ds = smem + L::DS + 8 * (jj & 1);
+                    const bf16x8 d = join(lds_tr(ds + ds_off(r, q)), lds_tr(ds + ds_off(r + 4, q)));
                     a[0] = mfma_bf(d, b0, a[0]);
                     a[1] = mfma_bf(d, b1, a[1]);
                 }

@@ -153,7 +153,9 @@ __device__ __forceinline__ void ssm_walk(const SsmParams& p, char* smem, int blo
 
     if (nch > 0) dma(0);
     for (int i = 0; i < nch; ++i) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's pieces of the chunk
+        // this wave's pieces of the chunk; the 2 NT stores after them may still be under way
+        if (i > 0 && on) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * NT) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         lds_barrier();   // everyone's, and the other slot's reads are done
         if (i + 1 < nch) dma(i + 1);
         if (!on) continue;
@@ -167,11 +169,12 @@ __device__ __forceinline__ void ssm_walk(const SsmParams& p, char* smem, int blo
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) xf[kk][ct] = x_frag(tx, kk, ct, g, jj);
         }
-        float* to = (REV ? p.dSt : p.St) + ((sg.slot0 + c0 + at(i)) * p.H + head) * state + (pc >> 5) * (S * 32) + lane * 8;
+        uint32_t* to = (REV ? p.dSt : p.St) + ((sg.slot0 + c0 + at(i)) * p.H + head) * state + (pc >> 5) * (S * 32) + lane * 8;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
+            const Split<2> two = split_acc<2>(st[t][0], st[t][1]);
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct) *reinterpret_cast<f32x4*>(to + t * 512 + 4 * ct) = st[t][ct];
+            for (int n = 0; n < 2; ++n) *reinterpret_cast<bf16x8*>(to + t * 512 + 4 * n) = two.s[n];
         }
         // S <- e^{G_last} S + B^T (w x)
 #pragma unroll

@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
     }
     // A head's inputs, asked for ahead
     u32x4 nx[PX], ny[PX], nrec;
+    float nskip = 0.f;
     u32x4 ns[KP][2], nds[KP][2];   // two parts of S and of dS, 32 columns each
     const int lr = P == 64 ? tid >> 3 : tid >> 4, lp = P == 64 ? tid & 7 : tid & 15;   // row and piece of this thread
     auto ask = [&](int h) {
@@ -155,6 +156,7 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
             ny[u] = __builtin_amdgcn_raw_buffer_load_b128(ry, (int)(r * p.dO.st * 2) + 16 * lp, 0, 0);
         }
         if (tid < SSM_REC / 16) nrec = *reinterpret_cast<const u32x4*>(p.rec + (slot * p.H + h) * SSM_REC + 16 * tid);
+        nskip = p.D ? p.D[h] : 0.f;
     };
     auto ask_states = [&](int h, int from, int to) {   // columns 32 from .. 32 to - 1
         const int64_t unit = slot * p.H + h;
@@ -205,6 +207,7 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
             *reinterpret_cast<u32x4*>(smem + L::DY + tile_off(lr + 32 * u, lp + YO / 8)) = ny[u];
         }
         if (tid < SSM_REC / 16) *reinterpret_cast<u32x4*>(smem + L::REC + 16 * tid) = nrec;
+        const float skip = __int_as_float(uniform(__float_as_int(nskip)));
         __syncthreads();
         ask_states(h, 2, KP);
 
@@ -386,7 +389,6 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
         }
         __builtin_amdgcn_sched_barrier(0);
         // ---- dx, transposed: a lane holds four channels of one token
-        const float skip = p.D ? p.D[h] : 0.f;
 #pragma unroll
         for (int half = 0; half < PX; ++half) {
             const int lane = opaque(tid & 63), g = lane >> 4, jj = lane & 15;

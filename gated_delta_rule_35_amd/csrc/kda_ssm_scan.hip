@@ -192,17 +192,17 @@ __device__ __forceinline__ void ssm_walk(const SsmParams& p, char* smem, int blo
                 w0 = num4(rec, SSM_W, 2 * kk, g);
                 w1 = num4(rec, SSM_W, 2 * kk + 1, g);
             }
-            Split<3> wx[2];
+            Split<2> wx[2];
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) {
                 const u32x4 xx = __builtin_bit_cast(u32x4, xf[kk][ct]);
-                wx[ct] = split_acc<3>(w0 * widen(u32x2{xx[0], xx[1]}), w1 * widen(u32x2{xx[2], xx[3]}));
+                wx[ct] = split_acc<2>(w0 * widen(u32x2{xx[0], xx[1]}), w1 * widen(u32x2{xx[2], xx[3]}));
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const bf16x8 b = col_frag(tb, t, kk, g, jj);
 #pragma unroll
-                for (int n = 2; n >= 0; --n) {
+                for (int n = 1; n >= 0; --n) {
 #pragma unroll
                     for (int ct = 0; ct < 2; ++ct)
                         st[t][ct] = mfma_bf(wx[ct].s[n], b, st[t][ct]);

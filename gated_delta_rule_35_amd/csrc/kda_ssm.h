@@ -24,6 +24,7 @@ struct SsmParams {
     int64_t segslots;      // segment slots: N * nseg, or with cu T / (64 segc) + N
     int32_t N, H, G, P, S, nc;   // nc = ceil(T / 64)
     int32_t segc, nseg;    // chunks of a segment; segments of a row (without cu)
+    int32_t cols;          // value columns of a walking work-group: 256, or 128
     int32_t dt_f32, softplus;
     // backward
     const float* dhT;      // [N, H, S, P] or nullptr
@@ -52,7 +53,7 @@ void launch_ssm_scan(const SsmParams& p, hipStream_t stream);
 // What segments add to the state; `both`: and to its gradients.
 void launch_ssm_adds(const SsmParams& p, bool both, hipStream_t stream);
 
-// Value columns that a walking work-group takes.
+// Value columns that a walking work-group takes at most.
 constexpr int SSM_COLS = 256;
 
 struct SsmDecodeParams {

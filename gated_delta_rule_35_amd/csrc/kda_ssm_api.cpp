@@ -205,6 +205,8 @@ kda_status_t prepare(const kda_tensor_t* x, const kda_tensor_t* dt, const kda_te
     p.nc = static_cast<int32_t>((z.T + 63) / 64);
     p.segc = static_cast<int32_t>(L.s.segc);
     p.nseg = static_cast<int32_t>(L.s.nseg);
+    // half as many columns a work-group where a compute unit has no second one to take either way
+    p.cols = z.H / z.G * z.P <= 128 || 2 * p.segslots * walk_units(z.H, z.G, z.P) <= kUnits ? kda::SSM_COLS / 2 : kda::SSM_COLS;
     p.softplus = softplus;
     p.sets = static_cast<int32_t>(L.sets);
     return KDA_OK;

@@ -6,7 +6,8 @@
 // walk starts every segment from the state that enters it.  Where sequences and heads alone fill
 // the compute units there is one segment and one walk.
 //
-// A work-group takes 256 of a group's value columns.  Eight waves walk, 32 columns each: their state is S / 16
+// A work-group takes 256 of a group's value columns, or half of them where that leaves no compute unit with two (T = 195 on
+// 8 heads @@ us and not @@, a SIMD's walk then has it for itself).  Eight waves walk, 32 columns each: their state is S / 16
 // by 2 accumulator tiles, which as operands need no exchange (kda_gdr_fwd.hip has the order of their
 // rows); two walks a SIMD fill each other's gaps.  Four more waves bring what the walks need into LDS and store y: a
 // wave that waits for the memory's queue would keep its products waiting.  Three meetings a chunk:
@@ -50,7 +51,7 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, int off) {
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
-// Where a work-group is: a segment, 256 columns of a group's heads, and of those the 64 of two walking
+// Where a work-group is: a segment, 256 (or 128) columns of a group's heads, and of those the 64 of two walking
 // waves and a loading one.
 struct SsmWalk {
     SsmSegment sg;
@@ -64,15 +65,15 @@ struct SsmWalk {
 };
 // Work-groups are dealt to the 8 XCDs round robin: a segment's go to one of them, since they share B and C.
 __device__ __forceinline__ bool walk_place(const SsmParams& p, int block, int w, SsmWalk& k) {
-    const int R = uniform(p.H / p.G), per = (R * p.P + SSM_COLS - 1) / SSM_COLS, units = per * p.G;
+    const int R = uniform(p.H / p.G), per = uniform((R * p.P + p.cols - 1) / p.cols), units = per * p.G;
     const int r = block >> 3, unit = uniform(r % units);
     k.sslot = uniform((int64_t)(r / units) * 8 + (block & 7));
     if (k.sslot >= p.segslots) return false;
     k.sg = ssm_segment(p, k.sslot);
     if (k.sg.index >= k.sg.count) return false;
     k.group = uniform(unit / per);
-    const int col = uniform((unit % per) * SSM_COLS + 64 * w);
-    k.on = col < R * p.P;
+    const int col = uniform((unit % per) * p.cols + 64 * w);
+    k.on = 64 * w < p.cols && col < R * p.P;
     k.head = uniform(k.group * R + (k.on ? col / p.P : 0));
     k.pc = uniform(col % p.P);
     k.c0 = k.sg.index * p.segc;
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(WT) kda_ssm_adds_kernel(const SsmParams p, con
 
 namespace {
 unsigned walk_blocks(const SsmParams& p) {
-    return (unsigned)((p.segslots + 7) / 8 * 8 * p.G * ((p.H / p.G * p.P + SSM_COLS - 1) / SSM_COLS));
+    return (unsigned)((p.segslots + 7) / 8 * 8 * p.G * ((p.H / p.G * p.P + p.cols - 1) / p.cols));
 }
 }  // namespace
 

@@ -522,23 +522,21 @@ __global__ void __launch_bounds__(1024) kda_ssm_numbers_kernel(const SsmParams p
     if (tok < ch.rows && h0 + i < p.H) p.ddt[(ch.row * p.T + ch.tok + tok) * p.H + h0 + i] = sh[tok][i];
 }
 
-// dB and dC of a chunk as sums over its sets of heads, in order; a thread takes eight channels.
+// dB and dC of a chunk as sums over its sets of heads, in order; a thread takes four channels of one of them.
 __global__ void __launch_bounds__(256) kda_ssm_join_kernel(const SsmParams p) {
-    const SsmChunk ch = ssm_chunk(p, blockIdx.x);
-    const int row = p.G * p.S;   // elements of a token
-    for (int e = threadIdx.x * 8; e < ch.rows * row; e += 256 * 8) {
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            const float* from = (which ? p.dCp : p.dBp) + (int64_t)blockIdx.x * 64 * row + e;
-            f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
-            for (int s = 0; s < p.sets; ++s, from += p.nslots * 64 * row) {
-                a += *reinterpret_cast<const f32x4*>(from);
-                b += *reinterpret_cast<const f32x4*>(from + 4);
-            }
-            *reinterpret_cast<u32x4*>((which ? p.dC : p.dB) + (ch.row * p.T + ch.tok) * row + e) =
-                u32x4{pack_bf2(a[0], a[1]), pack_bf2(a[2], a[3]), pack_bf2(b[0], b[1]), pack_bf2(b[2], b[3])};
-        }
-    }
+    const int row = p.G * p.S, groups = row / 8;   // elements of a token; work-groups of a chunk
+    const int64_t slot = blockIdx.x / groups;
+    const int i = (int)(blockIdx.x % groups) * 256 + threadIdx.x;
+    const bool c = i >= 16 * row;
+    const int e = 4 * (c ? i - 16 * row : i);
+    const SsmChunk ch = ssm_chunk(p, slot);
+    if (e >= ch.rows * row) return;
+    const float* from = (c ? p.dCp : p.dBp) + slot * 64 * row + e;
+    const int64_t step = p.nslots * 64 * row;
+    f32x4 a = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int s = 0; s < p.sets; ++s) a += *reinterpret_cast<const f32x4*>(from + s * step);
+    *reinterpret_cast<u32x2*>((c ? p.dC : p.dB) + (ch.row * p.T + ch.tok) * row + e) = u32x2{pack_bf2(a[0], a[1]), pack_bf2(a[2], a[3])};
 }
 
 // The heads' sums over the chunks: dA, dD, dbias.  A work-group takes one of them and 16 heads, 64
@@ -563,7 +561,7 @@ hipError_t launch_ssm_grads(const SsmParams& p, hipStream_t stream) {
         auto* f = p.S == 128 ? (p.P == 128 ? kda_ssm_grads_kernel<128, 128> : kda_ssm_grads_kernel<128, 64>)
                              : (p.P == 128 ? kda_ssm_grads_kernel<64, 128> : kda_ssm_grads_kernel<64, 64>);
         hipLaunchKernelGGL(f, dim3((unsigned)blocks), dim3(NT), 0, stream, p);
-        if (p.sets > 1) hipLaunchKernelGGL(kda_ssm_join_kernel, dim3((unsigned)p.nslots), dim3(256), 0, stream, p);
+        if (p.sets > 1) hipLaunchKernelGGL(kda_ssm_join_kernel, dim3((unsigned)(p.nslots * (p.G * p.S / 8))), dim3(256), 0, stream, p);
         hipLaunchKernelGGL(kda_ssm_numbers_kernel, dim3((unsigned)(p.nslots * ((p.H + 15) / 16))), dim3(1024), 0, stream, p);
     }
     hipLaunchKernelGGL(kda_ssm_sums_kernel, dim3((unsigned)(3 * ((p.H + 15) / 16))), dim3(1024), 0, stream, p);

@@ -263,8 +263,8 @@ __global__ void __launch_bounds__(256) kda_ssm_chain_kernel(const SsmParams p, c
 namespace {
 
 void states(const SsmParams& p, hipStream_t stream) {
-    const bool wide = p.H / p.G * p.P > 128;
-    const int nw = wide ? 8 : 4, per = (p.H / p.G * p.P + 32 * nw - 1) / (32 * nw);
+    const bool wide = p.cols > 128;
+    const int nw = p.cols / 32, per = (p.H / p.G * p.P + 32 * nw - 1) / (32 * nw);
     const unsigned half = (unsigned)((p.segslots + 7) / 8 * 8 * per * p.G);
     auto* f = p.S == 128 ? (wide ? kda_ssm_states_kernel<128, 8> : kda_ssm_states_kernel<128, 4>)
                          : (wide ? kda_ssm_states_kernel<64, 8> : kda_ssm_states_kernel<64, 4>);

@@ -158,21 +158,18 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
         if (tid < SSM_REC / 16) nrec = *reinterpret_cast<const u32x4*>(p.rec + (slot * p.H + h) * SSM_REC + 16 * tid);
         nskip = p.D ? p.D[h] : 0.f;
     };
-    auto ask_states = [&](int h, int from, int to) {   // columns 32 from .. 32 to - 1
-        const int64_t unit = slot * p.H + h;
+    auto ask_state = [&](const uint32_t* from, u32x4 (&to)[KP][2], int h, int first, int end) {   // columns 32 first .. 32 end - 1
 #pragma unroll
-        for (int pp = from; pp < to; ++pp) {
+        for (int pp = first; pp < end; ++pp) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int64_t at = unit * S * P + pp * (S * 32) + t * 512;
-                ns[pp][n] = *reinterpret_cast<const u32x4*>(p.St + at + (8 * lane + 4 * n));
-                nds[pp][n] = *reinterpret_cast<const u32x4*>(p.dSt + at + (8 * lane + 4 * n));
-            }
+            for (int n = 0; n < 2; ++n)
+                to[pp][n] = *reinterpret_cast<const u32x4*>(from + (slot * p.H + h) * S * P + pp * (S * 32) + t * 512 + (8 * lane + 4 * n));
         }
     };
     if (h_from < h_to) {
         ask(h_from);
-        ask_states(h_from, 0, 2);
+        ask_state(p.St, ns, h_from, 0, 2);
+        ask_state(p.dSt, nds, h_from, 0, 2);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
@@ -209,7 +206,8 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
         if (tid < SSM_REC / 16) *reinterpret_cast<u32x4*>(smem + L::REC + 16 * tid) = nrec;
         const float skip = __int_as_float(uniform(__float_as_int(nskip)));
         __syncthreads();
-        ask_states(h, 2, KP);
+        ask_state(p.St, ns, h, 2, KP);
+        ask_state(p.dSt, nds, h, 2, KP);
 
         // ---- the pair matrices' tiles
         {
@@ -359,13 +357,11 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
                 if (g == 1) sY[64 * t + tok] = sy;
             }
         }
-        if (h + 1 < h_to) {
-            ask(h + 1);
-            ask_states(h + 1, 0, 2);
-        }
+        if (h + 1 < h_to) ask(h + 1);   // S and dS later: all at once would wait for the memory's queue
         __syncthreads();
 
         // ---- dB and dC from the pair matrices
+        if (h + 1 < h_to) ask_state(p.St, ns, h + 1, 0, 2);
         {
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
             bf16x8 bcol[2], ccol[2];   // channels of tile t, tokens of k step kk
@@ -389,6 +385,7 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
         }
         __builtin_amdgcn_sched_barrier(0);
         // ---- dx, transposed: a lane holds four channels of one token
+        if (h + 1 < h_to) ask_state(p.dSt, nds, h + 1, 0, 2);
 #pragma unroll
         for (int half = 0; half < PX; ++half) {
             const int lane = opaque(tid & 63), g = lane >> 4, jj = lane & 15;

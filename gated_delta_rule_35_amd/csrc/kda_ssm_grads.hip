@@ -143,27 +143,29 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
     }
     // A head's inputs, asked for ahead
     u32x4 nx[PX], ny[PX], nrec;
-    float nskip = 0.f;
+    uint32_t nskip = 0;
     u32x4 ns[KP][2], nds[KP][2];   // two parts of S and of dS, 32 columns each
     const int lr = P == 64 ? tid >> 3 : tid >> 4, lp = P == 64 ? tid & 7 : tid & 15;   // row and piece of this thread
+    // behind the last head the buffers are empty: loads that always stand there can be counted, and wait for less
     auto ask = [&](int h) {
-        const auto rx = chunk_rsrc(p.x.p + ch.row * p.x.sb + ch.tok * p.x.st + h * p.x.sh, p.x.st, ch.rows, P);
-        const auto ry = chunk_rsrc(p.dO.p + ch.row * p.dO.sb + ch.tok * p.dO.st + h * p.dO.sh, p.dO.st, ch.rows, P);
+        const bool real = h < h_to;
+        const auto rx = chunk_rsrc(p.x.p + ch.row * p.x.sb + ch.tok * p.x.st + h * p.x.sh, p.x.st, real ? ch.rows : 0, P);
+        const auto ry = chunk_rsrc(p.dO.p + ch.row * p.dO.sb + ch.tok * p.dO.st + h * p.dO.sh, p.dO.st, real ? ch.rows : 0, P);
 #pragma unroll
         for (int u = 0; u < PX; ++u) {   // rows past the chunk's end come as zeros
             const int r = lr + 32 * u;
             nx[u] = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(r * p.x.st * 2) + 16 * lp, 0, 0);
             ny[u] = __builtin_amdgcn_raw_buffer_load_b128(ry, (int)(r * p.dO.st * 2) + 16 * lp, 0, 0);
         }
-        if (tid < SSM_REC / 16) nrec = *reinterpret_cast<const u32x4*>(p.rec + (slot * p.H + h) * SSM_REC + 16 * tid);
-        nskip = p.D ? p.D[h] : 0.f;
+        nrec = __builtin_amdgcn_raw_buffer_load_b128(make_rsrc(p.rec + (slot * p.H + h) * SSM_REC, real ? SSM_REC : 0), 16 * tid, 0, 0);
+        nskip = __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(p.D + h, real && p.D ? 4 : 0), 0, 0, 0);
     };
     auto ask_state = [&](const uint32_t* from, u32x4 (&to)[KP][2], int h, int first, int end) {   // columns 32 first .. 32 end - 1
+        const auto rs = make_rsrc(from + (slot * p.H + h) * S * P, h < h_to ? S * P * 4 : 0);
 #pragma unroll
         for (int pp = first; pp < end; ++pp) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-                to[pp][n] = *reinterpret_cast<const u32x4*>(from + (slot * p.H + h) * S * P + pp * (S * 32) + t * 512 + (8 * lane + 4 * n));
+            for (int n = 0; n < 2; ++n) to[pp][n] = __builtin_amdgcn_raw_buffer_load_b128(rs, 2048 * t + 32 * lane + 16 * n, pp * (S * 128), 0);
         }
     };
     if (h_from < h_to) {
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
             *reinterpret_cast<u32x4*>(smem + L::DY + tile_off(lr + 32 * u, lp + YO / 8)) = ny[u];
         }
         if (tid < SSM_REC / 16) *reinterpret_cast<u32x4*>(smem + L::REC + 16 * tid) = nrec;
-        const float skip = __int_as_float(uniform(__float_as_int(nskip)));
+        const float skip = __int_as_float(uniform((int)nskip));
         __syncthreads();
         ask_state(p.St, ns, h, 2, KP);
         ask_state(p.dSt, nds, h, 2, KP);
@@ -357,11 +359,11 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
                 if (g == 1) sY[64 * t + tok] = sy;
             }
         }
-        if (h + 1 < h_to) ask(h + 1);   // S and dS later: all at once would wait for the memory's queue
+        ask(h + 1);   // S and dS later: all at once would wait for the memory's queue
         __syncthreads();
 
         // ---- dB and dC from the pair matrices
-        if (h + 1 < h_to) ask_state(p.St, ns, h + 1, 0, 2);
+        ask_state(p.St, ns, h + 1, 0, 2);
         {
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
             bf16x8 bcol[2], ccol[2];   // channels of tile t, tokens of k step kk
@@ -385,7 +387,7 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
         }
         __builtin_amdgcn_sched_barrier(0);
         // ---- dx, transposed: a lane holds four channels of one token
-        if (h + 1 < h_to) ask_state(p.dSt, nds, h + 1, 0, 2);
+        ask_state(p.dSt, nds, h + 1, 0, 2);
 #pragma unroll
         for (int half = 0; half < PX; ++half) {
             const int lane = opaque(tid & 63), g = lane >> 4, jj = lane & 15;

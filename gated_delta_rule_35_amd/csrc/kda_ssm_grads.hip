@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
 #pragma unroll
         for (int pp = first; pp < end; ++pp) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n) to[pp][n] = __builtin_amdgcn_raw_buffer_load_b128(rs, 2048 * t + 32 * lane + 16 * n, pp * (S * 128), 0);
+            for (int n = 0; n < 2; ++n) to[pp][n] = __builtin_amdgcn_raw_buffer_load_b128(rs, 2048 * t + 1024 * n + 16 * lane, pp * (S * 128), 0);
         }
     };
     if (h_from < h_to) {

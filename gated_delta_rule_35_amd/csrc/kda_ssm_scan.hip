@@ -4,9 +4,10 @@
 // Backward: the state that enters each chunk, S <- e^{G_last} S + B^T (e^{G_last - G} d x), and the gradient of the one
 // that leaves it, last chunk first, dS <- e^{G_last} dS + C^T (e^G dy), both into memory as the operands
 // that the token gradients take.  A wave owns 32 of a head's value columns: its state is S / 16 by 2 accumulator
-// tiles, transposed (a lane holds four columns of a channel).  Eight waves (or four, where a group of
-// heads has 128 columns or fewer) share the chunk's B or C in LDS, and each brings its own columns
-// of x or dy there; the next chunk's come by DMA during this one's products.
+// tiles, transposed (a lane holds four columns of a channel).  Four waves
+// share the chunk's B or C in LDS, and each brings its own columns of x or dy there; the next chunk's come by DMA
+// during this one's products, and two work-groups share a compute unit (one of eight waves: 112 us, not 107, packed
+// 4096 tokens of 32 heads of 128).
 #include <algorithm>
 
 #include "kda_ssm_device.h"
@@ -54,7 +55,8 @@ __global__ void __launch_bounds__(256) kda_ssm_gates_kernel(const SsmParams p) {
 
 namespace {
 
-template <int NW>
+constexpr int NW = 4;   // waves of a walk
+
 struct SL {
     static constexpr int HEADS = NW / 2;   // at most, of 64 columns
     static constexpr int B = 0, X = 16384, REC = X + NW * 4096;
@@ -79,9 +81,9 @@ __device__ __forceinline__ bool walk_place(int b, int units, int64_t segs, int64
 }  // namespace
 
 // REV: the gradients' walk, with C, dy and e^G in the place of B, x and e^{G_last - G} d, last chunk first.
-template <int S, int NW, bool REV>
+template <int S, bool REV>
 __device__ __forceinline__ void ssm_walk(const SsmParams& p, char* smem, int block) {
-    typedef SL<NW> L;
+    typedef SL L;
     constexpr int KT = S / 32, NT = S / 16;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, jj = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -169,12 +171,12 @@ __device__ __forceinline__ void ssm_walk(const SsmParams& p, char* smem, int blo
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) xf[kk][ct] = x_frag(tx, kk, ct, g, jj);
         }
-        uint32_t* to = (REV ? p.dSt : p.St) + ((sg.slot0 + c0 + at(i)) * p.H + head) * state + (pc >> 5) * (S * 32) + lane * 8;
+        uint32_t* to = (REV ? p.dSt : p.St) + ((sg.slot0 + c0 + at(i)) * p.H + head) * state + (pc >> 5) * (S * 32) + lane * 4;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const Split<2> two = split_acc<2>(st[t][0], st[t][1]);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) *reinterpret_cast<bf16x8*>(to + t * 512 + 4 * n) = two.s[n];
+            for (int n = 0; n < 2; ++n) *reinterpret_cast<bf16x8*>(to + t * 512 + 256 * n) = two.s[n];
         }
         // S <- e^{G_last} S + B^T (w x)
 #pragma unroll
@@ -221,11 +223,11 @@ __device__ __forceinline__ void ssm_walk(const SsmParams& p, char* smem, int blo
 }
 
 // The second half of the work-groups walks the gradients.
-template <int S, int NW>
+template <int S>
 __global__ void __launch_bounds__(64 * NW) kda_ssm_states_kernel(const SsmParams p, const int half) {
-    __shared__ __attribute__((aligned(1024))) char smem[SL<NW>::BYTES];
-    if ((int)blockIdx.x < half) ssm_walk<S, NW, false>(p, smem, (int)blockIdx.x);
-    else ssm_walk<S, NW, true>(p, smem, (int)blockIdx.x - half);
+    __shared__ __attribute__((aligned(1024))) char smem[SL::BYTES];
+    if ((int)blockIdx.x < half) ssm_walk<S, false>(p, smem, (int)blockIdx.x);
+    else ssm_walk<S, true>(p, smem, (int)blockIdx.x - half);
 }
 
 // Chains a sequence's segments: what enters each from what the ones before it add (REV: after it).
@@ -263,12 +265,10 @@ __global__ void __launch_bounds__(256) kda_ssm_chain_kernel(const SsmParams p, c
 namespace {
 
 void states(const SsmParams& p, hipStream_t stream) {
-    const bool wide = p.cols > 128;
-    const int nw = p.cols / 32, per = (p.H / p.G * p.P + 32 * nw - 1) / (32 * nw);
+    const int per = (p.H / p.G * p.P + 32 * NW - 1) / (32 * NW);
     const unsigned half = (unsigned)((p.segslots + 7) / 8 * 8 * per * p.G);
-    auto* f = p.S == 128 ? (wide ? kda_ssm_states_kernel<128, 8> : kda_ssm_states_kernel<128, 4>)
-                         : (wide ? kda_ssm_states_kernel<64, 8> : kda_ssm_states_kernel<64, 4>);
-    hipLaunchKernelGGL(f, dim3(2 * half), dim3(64 * nw), 0, stream, p, (int)half);
+    auto* f = p.S == 128 ? kda_ssm_states_kernel<128> : kda_ssm_states_kernel<64>;
+    hipLaunchKernelGGL(f, dim3(2 * half), dim3(64 * NW), 0, stream, p, (int)half);
 }
 bool segmented(const SsmParams& p) { return p.cu ? p.nc > p.segc : p.nseg > 1; }
 void gates(const SsmParams& p, hipStream_t stream) {

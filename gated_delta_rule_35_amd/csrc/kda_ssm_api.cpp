@@ -100,9 +100,12 @@ kda_status_t check_state(const kda_tensor_t* t, int64_t n, const Sizes& z) {
     return check_f32(t, 4, s, 16);
 }
 
-// Chunks of a segment and segments of a row.  Walks of whole sequences where they fill the
-// compute units (one work-group each, at least two thirds of them); otherwise segments for
-// that, of at least four chunks, since the walk that forms what they add reads their inputs again.
+// Chunks of a segment and segments of a row.  Walks of whole sequences where they fill the compute units (one
+// work-group each), else segments for that: of four chunks at least, since the walk that forms what they add reads
+// their inputs again, or of two where half the units suffice (then a work-group takes half the columns).  They are
+// chained one after the other: at most 4 sqrt(chunks).  S = 128, heads of 64: T = 1024 on 8 heads in 8 segments
+// 38 us, in 4 46, in one 76; T = 16384 in 64 76 us, in 128 96; T = 2048 on 64 heads in 8 58 us, in 16 64.  Below 8
+// chunks one walk is as fast.  The backward walks both ways at once: half as many segments each.
 // Packed sequences are cut the same way from their own starts, as if they were one.
 constexpr int64_t kUnits = 256;   // compute units: the workspace's size follows from the shapes alone
 struct Segments {
@@ -110,8 +113,12 @@ struct Segments {
 };
 Segments segments(int64_t tokens_per_row, int64_t N, bool packed, int64_t units) {
     const int64_t nc = (tokens_per_row + 63) / 64, walks = (packed ? 1 : N) * units;
-    int64_t nseg = walks > 0 ? std::max<int64_t>(1, kUnits / walks) : 1;
-    nseg = std::max<int64_t>(1, std::min(nseg, nc / 4));
+    int64_t nseg = 1, most = 1;
+    if (walks > 0 && nc >= 8) {
+        while (most * most < 16 * nc) ++most;
+        nseg = std::max<int64_t>({1, std::min(kUnits / walks, nc / 4), std::min(kUnits / 2 / walks, nc / 2)});
+        nseg = std::min(nseg, most);
+    }
     Segments s;
     s.segc = std::max<int64_t>(1, (nc + nseg - 1) / nseg);
     s.nseg = std::max<int64_t>(1, (nc + s.segc - 1) / s.segc);
@@ -129,7 +136,7 @@ struct Layout {
 Layout layout(int64_t B, int64_t T, int64_t N, bool packed, int64_t H, int64_t G, int64_t P, int64_t S, bool bwd) {
     Layout L{};
     const int64_t state = S * P * 4;
-    L.s = segments(T, N, packed, walk_units(H, G, P));
+    L.s = segments(T, N, packed, (bwd ? 2 : 1) * walk_units(H, G, P));
     L.slots = T == 0 ? 0 : packed ? (T + 63) / 64 + N : B * ((T + 63) / 64);
     const bool cut = packed ? (T + 63) / 64 > L.s.segc : L.s.nseg > 1;
     const int64_t segs = cut ? L.s.slots * H : 0;
@@ -167,7 +174,7 @@ int64_t any_layout(int64_t tokens, int64_t N, int64_t H, int64_t G, int64_t P, i
 // The checks and parameters that the forward and the backward share.
 kda_status_t prepare(const kda_tensor_t* x, const kda_tensor_t* dt, const kda_tensor_t* A, const kda_tensor_t* Bm,
                      const kda_tensor_t* Cm, const kda_tensor_t* D, const kda_tensor_t* bias, int32_t softplus,
-                     const kda_tensor_t* cu, kda::SsmParams& p, Sizes& z) {
+                     const kda_tensor_t* cu, bool bwd, kda::SsmParams& p, Sizes& z, Layout& L) {
     kda_status_t st;
     p = kda::SsmParams{};
     if ((st = check_rows(x, 4, &p.x)) != KDA_OK) return st;
@@ -183,9 +190,9 @@ kda_status_t prepare(const kda_tensor_t* x, const kda_tensor_t* dt, const kda_te
     }
     if (softplus != 0 && softplus != 1) return KDA_ERR_VALUE;
     if (z.N > (int64_t(1) << 24) || z.B * z.T > kMaxTokens) return KDA_ERR_UNSUPPORTED;
-    const Layout L = layout(z.B, z.T, z.N, cu != nullptr, z.H, z.G, z.P, z.S, true);
+    L = layout(z.B, z.T, z.N, cu != nullptr, z.H, z.G, z.P, z.S, bwd);
     // grids of at most 2^22 work-groups, segments rounded up to a multiple of 8
-    if (L.slots * z.H > kMaxBlocks || 2 * (L.s.slots + 8) * walk_units(z.H, z.G, z.P) > kMaxBlocks ||
+    if (L.slots * z.H > kMaxBlocks || 2 * (L.s.slots + 8) * walk_units(z.H, z.G, 2 * z.P) > kMaxBlocks ||
         2 * z.N * z.H * (z.S * z.P / 1024) > kMaxBlocks || L.slots * z.G * L.sets > kMaxBlocks)
         return KDA_ERR_UNSUPPORTED;
     p.dt = dt->data;
@@ -206,7 +213,7 @@ kda_status_t prepare(const kda_tensor_t* x, const kda_tensor_t* dt, const kda_te
     p.segc = static_cast<int32_t>(L.s.segc);
     p.nseg = static_cast<int32_t>(L.s.nseg);
     // half as many columns a work-group where a compute unit has no second one to take either way
-    p.cols = z.H / z.G * z.P <= 128 || 2 * p.segslots * walk_units(z.H, z.G, z.P) <= kUnits ? kda::SSM_COLS / 2 : kda::SSM_COLS;
+    p.cols = z.H / z.G * z.P <= 128 || (bwd ? 4 : 2) * p.segslots * walk_units(z.H, z.G, z.P) <= kUnits ? kda::SSM_COLS / 2 : kda::SSM_COLS;
     p.softplus = softplus;
     p.sets = static_cast<int32_t>(L.sets);
     return KDA_OK;
@@ -232,7 +239,8 @@ kda_status_t kda_ssm_fwd(const kda_tensor_t* x, const kda_tensor_t* dt, const kd
                          const kda_tensor_t* final_state, void* workspace, int64_t workspace_size, void* stream) {
     kda::SsmParams p;
     Sizes z;
-    kda_status_t st = prepare(x, dt, A, B, C, D, dt_bias, softplus, cu_seqlens, p, z);
+    Layout L;
+    kda_status_t st = prepare(x, dt, A, B, C, D, dt_bias, softplus, cu_seqlens, false, p, z, L);
     if (st != KDA_OK) return st;
     if ((st = check_bf16(out, x)) != KDA_OK) return st;
     if (initial_state && (st = check_state(initial_state, z.N, z)) != KDA_OK) return st;
@@ -242,7 +250,6 @@ kda_status_t kda_ssm_fwd(const kda_tensor_t* x, const kda_tensor_t* dt, const kd
     if (any_overlap(outs, 2, ins, 8) || overlaps(out, initial_state)) return KDA_ERR_LAYOUT;
     if (initial_state && final_state && partly_overlap(initial_state->data, final_state->data, span_of(final_state).bytes))
         return KDA_ERR_LAYOUT;
-    const Layout L = layout(z.B, z.T, z.N, cu_seqlens != nullptr, z.H, z.G, z.P, z.S, false);
     if (workspace && (workspace_size < L.total || reinterpret_cast<uintptr_t>(workspace) % 256 != 0)) return KDA_ERR_WORKSPACE;
     p.h0 = floats(initial_state);
     p.y = static_cast<uint16_t*>(out->data);
@@ -270,7 +277,8 @@ kda_status_t kda_ssm_bwd(const kda_tensor_t* x, const kda_tensor_t* dt, const kd
                          int64_t workspace_size, void* stream) {
     kda::SsmParams p;
     Sizes z;
-    kda_status_t st = prepare(x, dt, A, B, C, D, dt_bias, softplus, cu_seqlens, p, z);
+    Layout L;
+    kda_status_t st = prepare(x, dt, A, B, C, D, dt_bias, softplus, cu_seqlens, true, p, z, L);
     if (st != KDA_OK) return st;
     if ((st = check_rows(d_out, 4, &p.dO)) != KDA_OK) return st;
     if (!same_shape(d_out, x->shape, 4)) return KDA_ERR_SHAPE;
@@ -287,7 +295,6 @@ kda_status_t kda_ssm_bwd(const kda_tensor_t* x, const kda_tensor_t* dt, const kd
     const kda_tensor_t* ins[] = {x, dt, A, B, C, D, dt_bias, cu_seqlens, initial_state, d_out, d_final_state};
     const kda_tensor_t* outs[] = {dx, ddt, dA, dB, dC, dD, ddt_bias, d_initial_state};
     if (any_overlap(outs, 8, ins, 11)) return KDA_ERR_LAYOUT;
-    const Layout L = layout(z.B, z.T, z.N, cu_seqlens != nullptr, z.H, z.G, z.P, z.S, true);
     if (workspace && (workspace_size < L.total || reinterpret_cast<uintptr_t>(workspace) % 256 != 0)) return KDA_ERR_WORKSPACE;
     p.h0 = floats(initial_state);
     p.dhT = floats(d_final_state);

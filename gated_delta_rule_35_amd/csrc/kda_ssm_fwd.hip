@@ -7,7 +7,7 @@
 // the compute units there is one segment and one walk.
 //
 // A work-group takes 256 of a group's value columns, or half of them where that leaves no compute unit with two (T = 195 on
-// 8 heads @@ us and not @@, a SIMD's walk then has it for itself).  Eight waves walk, 32 columns each: their state is S / 16
+// 8 heads 25 us and not 33: a SIMD then has one walk).  Eight waves walk, 32 columns each: their state is S / 16
 // by 2 accumulator tiles, which as operands need no exchange (kda_gdr_fwd.hip has the order of their
 // rows); two walks a SIMD fill each other's gaps.  Four more waves bring what the walks need into LDS and store y: a
 // wave that waits for the memory's queue would keep its products waiting.  Three meetings a chunk:

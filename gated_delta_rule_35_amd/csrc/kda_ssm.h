@@ -33,8 +33,7 @@ struct SsmParams {
     float *ddt;            // [B, T, H]
     float *dA, *dD, *dbias;// [H]; dD and dbias may be nullptr
     float *dseg, *ddecay;  // seg and decay of the gradients' walk
-    uint32_t *St, *dSt;    // [nslots][H][P S] states entering each chunk and gradients of those leaving it, as operands: a
-                           // lane's eight values in two bf16 parts
+    float *St, *dSt;       // [nslots][H][P S] states entering each chunk and gradients of those leaving it, as fragments
     float *dBp, *dCp;      // [sets][nslots 64][G][S] sums of dB and dC over each set of heads, or nullptr (one set)
     float* part;           // [nslots][3][H] sums over a chunk: dA, dD, dbias
     int32_t sets;          // sets of heads that a group's gradients are formed in

@@ -316,8 +316,8 @@ kda_status_t kda_ssm_bwd(const kda_tensor_t* x, const kda_tensor_t* dt, const kd
         p.decay = part(L.decay);
         p.dseg = part(L.dseg);
         p.ddecay = part(L.ddecay);
-        p.St = reinterpret_cast<uint32_t*>(base + L.St);
-        p.dSt = reinterpret_cast<uint32_t*>(base + L.dSt);
+        p.St = part(L.St);
+        p.dSt = part(L.dSt);
         p.part = part(L.part);
         if (L.sets > 1) {
             p.dBp = part(L.dB);

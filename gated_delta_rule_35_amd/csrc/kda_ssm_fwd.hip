@@ -19,9 +19,9 @@
 // different blocks of sixteen is a product of a number of each token and one or two of the blocks,
 // all at most 1 for A <= 0; within a block it is formed from the difference.
 //
-// Precision.  x, B and C are bf16, the state and all sums fp32.  The products' other operands (w x, S in C S,
-// the pair matrix) enter in two bf16 parts, off by 2^-18 of themselves at most: x, and with it w x, is
-// known to 2^-9 only.  A third part of w x cost 30 us of 240 at B = 2, H = 64, T = 8192.
+// Precision.  x, B and C are bf16, the state and all sums fp32.  What enters the state is formed in three bf16
+// parts, fp32's 24 bits (the third is 14 us of 200 at B = 2, H = 64, T = 8192; without it the final state is off by
+// 2^-19 of itself); what only adds to y (S in C S, the pair matrix) in two, 16 bits for y's eight.
 #include "kda_ssm_device.h"
 
 namespace kda {
@@ -237,11 +237,11 @@ struct State {
         constexpr int QS = NT / 2;
         const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
         const float el = rec[SSM_EG + 63];
-        Split<2> wx[2][2];
+        Split<3> wx[2][2];
         constexpr int W = REV ? SSM_EG : SSM_W;
         auto weigh = [&](int kk, int c) {
             const u32x4 xx = __builtin_bit_cast(u32x4, x_frag(tx, kk, c0 + 16 * c, ln));
-            wx[kk][c] = split_acc<2>(num4(rec, W, 2 * kk, g) * widen(u32x2{xx[0], xx[1]}),
+            wx[kk][c] = split_acc<3>(num4(rec, W, 2 * kk, g) * widen(u32x2{xx[0], xx[1]}),
                                      num4(rec, W, 2 * kk + 1, g) * widen(u32x2{xx[2], xx[3]}));
         };
         bf16x8 bq[2][2];
@@ -267,15 +267,15 @@ struct State {
             if (q == QS - 2) weigh(1, 0);
             if (q == QS - 1) weigh(1, 1);
 #pragma unroll
-            for (int n = 1; n >= 0; --n) {
+            for (int n = 2; n >= 0; --n) {
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) st[t0 + t][c] = mfma_bf(bq[q & 1][t], wx[kk][c].s[n], st[t0 + t][c]);
                 }
             }
-            if (q == QS - 2 || q == QS - 1) interleave<8, 7, 1, 0>();
-            else interleave<8, 3, 1, 0>();
+            if (q == QS - 2 || q == QS - 1) interleave<12, 7, 1, 0>();
+            else interleave<12, 2, 1, 0>();
             if (q == QS - 1) {
                 read();
                 __builtin_amdgcn_sched_barrier(0);

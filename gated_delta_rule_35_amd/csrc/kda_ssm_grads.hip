@@ -17,9 +17,9 @@
 // through LDS, for dx.  The 64 x 64 matrices are ten tiles, dealt to the waves; they leave as
 // operand fragments for the second half of a head's work.
 //
-// Precision.  S, dS, K and E enter in two bf16 parts each, off by 2^-18 of themselves at most, beside
-// operands that are bf16 as they come: the results in bf16 round at 2^-9, and ddt and the sums, which
-// add up thousands of such products, take part in steps of a dt that is mostly bf16 itself.
+// Precision.  What reaches ddt and the sums enters in three bf16 parts (S and dS in V and W, 24
+// bits; in two, dA was off by 2 10^-6 at B = 2, H = 64, T = 8192, fp32's plain form by 4 10^-7), what only reaches
+// bf16 results in two (K, E, and dS in dx).
 #include "kda_block.h"
 #include "kda_ssm_device.h"
 
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
     // A head's inputs, asked for ahead
     u32x4 nx[PX], ny[PX], nrec;
     uint32_t nskip = 0;
-    u32x4 ns[KP][2], nds[KP][2];   // two parts of S and of dS, 32 columns each
+    f32x4 ns[KP][2], nds[KP][2];   // S and dS, 32 columns each
     const int lr = P == 64 ? tid >> 3 : tid >> 4, lp = P == 64 ? tid & 7 : tid & 15;   // row and piece of this thread
     // behind the last head the buffers are empty: loads that always stand there can be counted, and wait for less
     auto ask = [&](int h) {
@@ -160,12 +160,13 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
         nrec = __builtin_amdgcn_raw_buffer_load_b128(make_rsrc(p.rec + (slot * p.H + h) * SSM_REC, real ? SSM_REC : 0), 16 * tid, 0, 0);
         nskip = __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(p.D + h, real && p.D ? 4 : 0), 0, 0, 0);
     };
-    auto ask_state = [&](const uint32_t* from, u32x4 (&to)[KP][2], int h, int first, int end) {   // columns 32 first .. 32 end - 1
+    auto ask_state = [&](const float* from, f32x4 (&to)[KP][2], int h, int first, int end) {   // columns 32 first .. 32 end - 1
         const auto rs = make_rsrc(from + (slot * p.H + h) * S * P, h < h_to ? S * P * 4 : 0);
 #pragma unroll
         for (int pp = first; pp < end; ++pp) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n) to[pp][n] = __builtin_amdgcn_raw_buffer_load_b128(rs, 2048 * t + 1024 * n + 16 * lane, pp * (S * 128), 0);
+            for (int ct = 0; ct < 2; ++ct)
+                to[pp][ct] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, 2048 * t + 1024 * ct + 16 * lane, pp * (S * 128), 0));
         }
     };
     if (h_from < h_to) {
@@ -313,38 +314,45 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
             f32x4 v[MW], w[MW];
 #pragma unroll
             for (int mi = 0; mi < MW; ++mi) v[mi] = w[mi] = zero;
-            f32x4 dot = zero;   // S dS^T of the wave's channels: its diagonal sums to <S, dS>
-#pragma unroll
-            for (int pp = 0; pp < KP; ++pp) {
-                bf16x8 fs[2], fd[2], fx[MW], fy[MW];
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    fs[n] = __builtin_bit_cast(bf16x8, ns[pp][n]);
-                    fd[n] = __builtin_bit_cast(bf16x8, nds[pp][n]);
-                    if (pp >= 2) later[pp - 2][n] = nds[pp][n];
-                    else if (S == 128 || wave < 4) put_ds(pp, n, nds[pp][n], nrow, g);
-                }
-#pragma unroll
-                for (int mi = 0; mi < MW; ++mi) {
-                    fx[mi] = two8(tx, 16 * (m0 + mi) + jj, 32 * pp + 4 * g);
-                    fy[mi] = two8(ty, 16 * (m0 + mi) + jj, YO + 32 * pp + 4 * g);
-                }
-#pragma unroll
-                for (int n = 1; n >= 0; --n) {
-#pragma unroll
-                    for (int mi = 0; mi < MW; ++mi) {
-                        v[mi] = mfma_bf(fd[n], fx[mi], v[mi]);
-                        w[mi] = mfma_bf(fs[n], fy[mi], w[mi]);
-                    }
-                }
-                dot = mfma_bf(fs[1], fd[0], dot);
-                dot = mfma_bf(fs[0], fd[1], dot);
-                dot = mfma_bf(fs[0], fd[0], dot);
-                __builtin_amdgcn_sched_barrier(0);
-            }
             float q = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) q += 4 * g + i == jj ? dot[i] : 0.f;
+            for (int pp = 0; pp < KP; ++pp) {
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) q = fmaf(ns[pp][ct][i], nds[pp][ct][i], q);
+                }
+                {
+                    const Split<3> dsp = split_acc<3>(nds[pp][0], nds[pp][1]);
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const u32x4 part = __builtin_bit_cast(u32x4, dsp.s[n]);
+                        if (pp >= 2) later[pp - 2][n] = part;
+                        else if (S == 128 || wave < 4) put_ds(pp, n, part, nrow, g);
+                    }
+                    bf16x8 f[MW];
+#pragma unroll
+                    for (int mi = 0; mi < MW; ++mi) f[mi] = two8(tx, 16 * (m0 + mi) + jj, 32 * pp + 4 * g);
+#pragma unroll
+                    for (int n = 2; n >= 0; --n) {
+#pragma unroll
+                        for (int mi = 0; mi < MW; ++mi) v[mi] = mfma_bf(dsp.s[n], f[mi], v[mi]);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                {
+                    const Split<3> sp = split_acc<3>(ns[pp][0], ns[pp][1]);
+                    bf16x8 f[MW];
+#pragma unroll
+                    for (int mi = 0; mi < MW; ++mi) f[mi] = two8(ty, 16 * (m0 + mi) + jj, YO + 32 * pp + 4 * g);
+#pragma unroll
+                    for (int n = 2; n >= 0; --n) {
+#pragma unroll
+                        for (int mi = 0; mi < MW; ++mi) w[mi] = mfma_bf(sp.s[n], f[mi], w[mi]);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
             q = sum64(q);
             if (ln == 0) sS[wave] = S == 128 || wave < 4 ? q : 0.f;
 #pragma unroll

@@ -2,8 +2,8 @@
 // the numbers of every token, the chaining of segments, and the walks that leave the states.
 //
 // Backward: the state that enters each chunk, S <- e^{G_last} S + B^T (e^{G_last - G} d x), and the gradient of the one
-// that leaves it, last chunk first, dS <- e^{G_last} dS + C^T (e^G dy), both into memory as the operands
-// that the token gradients take.  A wave owns 32 of a head's value columns: its state is S / 16 by 2 accumulator
+// that leaves it, last chunk first, dS <- e^{G_last} dS + C^T (e^G dy), both into memory in the order
+// that the token gradients take as operands.  A wave owns 32 of a head's value columns: its state is S / 16 by 2 accumulator
 // tiles, transposed (a lane holds four columns of a channel).  Four waves
 // share the chunk's B or C in LDS, and each brings its own columns of x or dy there; the next chunk's come by DMA
 // during this one's products, and two work-groups share a compute unit (one of eight waves: 112 us, not 107, packed
@@ -171,12 +171,11 @@ __device__ __forceinline__ void ssm_walk(const SsmParams& p, char* smem, int blo
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) xf[kk][ct] = x_frag(tx, kk, ct, g, jj);
         }
-        uint32_t* to = (REV ? p.dSt : p.St) + ((sg.slot0 + c0 + at(i)) * p.H + head) * state + (pc >> 5) * (S * 32) + lane * 4;
+        float* to = (REV ? p.dSt : p.St) + ((sg.slot0 + c0 + at(i)) * p.H + head) * state + (pc >> 5) * (S * 32) + lane * 4;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const Split<2> two = split_acc<2>(st[t][0], st[t][1]);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) *reinterpret_cast<bf16x8*>(to + t * 512 + 256 * n) = two.s[n];
+            for (int ct = 0; ct < 2; ++ct) *reinterpret_cast<f32x4*>(to + t * 512 + 256 * ct) = st[t][ct];
         }
         // S <- e^{G_last} S + B^T (w x)
 #pragma unroll
@@ -194,17 +193,17 @@ __device__ __forceinline__ void ssm_walk(const SsmParams& p, char* smem, int blo
                 w0 = num4(rec, SSM_W, 2 * kk, g);
                 w1 = num4(rec, SSM_W, 2 * kk + 1, g);
             }
-            Split<2> wx[2];
+            Split<3> wx[2];
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) {
                 const u32x4 xx = __builtin_bit_cast(u32x4, xf[kk][ct]);
-                wx[ct] = split_acc<2>(w0 * widen(u32x2{xx[0], xx[1]}), w1 * widen(u32x2{xx[2], xx[3]}));
+                wx[ct] = split_acc<3>(w0 * widen(u32x2{xx[0], xx[1]}), w1 * widen(u32x2{xx[2], xx[3]}));
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const bf16x8 b = col_frag(tb, t, kk, g, jj);
 #pragma unroll
-                for (int n = 1; n >= 0; --n) {
+                for (int n = 2; n >= 0; --n) {
 #pragma unroll
                     for (int ct = 0; ct < 2; ++ct)
                         st[t][ct] = mfma_bf(wx[ct].s[n], b, st[t][ct]);

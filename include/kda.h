@@ -697,9 +697,8 @@ kda_status_t kda_add_norm_bwd(const kda_tensor_t* sum, const kda_tensor_t* weigh
  * 2^23 elements apart.  Every other tensor is contiguous.  Other head and state dimensions, more
  * than 2^31 - 1 tokens, or grids above 2^22 work-groups ((chunk slot, head) pairs among them)
  * return KDA_ERR_UNSUPPORTED.
- * Precision: states and sums are fp32; the products' operands that are not bf16 as they come (d e^{..} x, the
- * states in S^T C, the decayed C B^T) enter in two bf16 parts, off by 2^-18 of themselves at most; y is
- * rounded to bf16 once.  A token that holds NaN or infinity may
+ * Precision: states and sums are fp32; what enters the state is formed from operands at fp32's 24
+ * bits, what only adds to y at 16; y is rounded to bf16 once.  A token that holds NaN or infinity may
  * reach every token of its 64-token chunk and later ones of its sequence, and through x only its own head.
  * workspace: kda_ssm_fwd_workspace_size(B * T, N, H, G, P, S) bytes, 256-byte aligned, as for
  * kda_gdr_fwd; NULL allocates it in stream order.
@@ -721,8 +720,8 @@ kda_status_t kda_ssm_fwd(const kda_tensor_t* x, const kda_tensor_t* dt, const kd
  *                                   may be NULL, and without D or dt_bias have to be
  *   d_initial_state   [N, H, S, P]  fp32, or NULL (not computed)
  * An empty sequence passes d_final_state through to its d_initial_state; rows of tokens in no
- * sequence are not written.  Precision as above; ddt and the sums take the kept states in two bf16
- * parts each.  workspace: kda_ssm_bwd_workspace_size() bytes, as above: the states
+ * sequence are not written.  ddt, dA, ddt_bias and dD are formed from operands at 24 bits, dx, dB and dC
+ * at 16.  workspace: kda_ssm_bwd_workspace_size() bytes, as above: the states
  * entering and the gradients leaving every chunk, 4 S P bytes each for every (chunk slot, head).
  */
 int64_t kda_ssm_bwd_workspace_size(int64_t total_tokens, int64_t num_sequences, int64_t num_heads, int64_t num_groups,

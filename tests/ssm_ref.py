@@ -4,14 +4,14 @@ its tests.
 Tolerances.  Each result is compared with the magnitude of the terms that make it up: with Sabs the recurrence
 of |d B x| (Sabs_t = e^{d A} Sabs_{t-1} + d |B| |x|) and Dabs that of the gradients backwards,
   y      2^-8 of itself (its one rounding to bf16), and 2^-15 of |C| Sabs + |D x|: the states and the pair
-         matrix enter in two bf16 parts, off by 2^-18 of themselves at most; a chunk's sums are 128 fp32 terms,
-         2^-17, the states themselves (below) 2^-16.8, the decays' exponentials a few units of 2^-24
-  states 2^-16 of Sabs: what enters is formed in two bf16 parts, 2^-18; 64 fp32 terms a chunk, 2^-18, and one more
-         for each of at most 18 chunks here, 2^-19.8, 2^-16.8 in all; as much for the gradient of the initial state
+         matrix enter in two bf16 parts, off by 2^-17 of themselves at most; a chunk's sums are 128 fp32 terms,
+         2^-17, the decays' exponentials a few units of 2^-24
+  states 2^-17 of Sabs: 24-bit operands, 64 fp32 terms a chunk and one more a chunk, and as much for the
+         gradient of the initial state
   dC, dB, dx  2^-8 of themselves and 2^-15 of Sabs |dy|, Dabs d |x| (over a group's heads), d |B| Dabs + |D dy|
-  ddt    the step's slope times |A| da + |B| Dabs |x|, da = e^{dA} <Sabs, Dabs>, 2^-14: both states 2^-16.8 and their two
-         parts 2^-18 each make 2^-15.3, and the sums over pairs, 64 products of two 128-term sums, 2^-16
-  dA, ddt_bias, dD  2^-14, 2^-14 and 2^-15 of the sum of their terms' magnitudes
+  ddt    the step's slope times |A| da + |B| Dabs |x|, da = e^{dA} <Sabs, Dabs>: the sums over pairs take 64 products
+         of two 128-term sums, 2^-16 with their rows and columns added over 64 tokens, 2^-15 in all
+  dA, dD, ddt_bias  2^-15 of the sum of their terms' magnitudes
 """
 import torch
 
@@ -176,5 +176,5 @@ def close(got, want, off, what):
         assert float(over.max()) <= 2.0 ** -140, (what, "times the tolerance", float(worst.max()))
 
 
-BITS = dict(y=2.0 ** -15, state=2.0 ** -16, dx=2.0 ** -15, ddt=2.0 ** -14, dB=2.0 ** -15, dC=2.0 ** -15, dA=2.0 ** -14, dD=2.0 ** -15,
-            ddt_bias=2.0 ** -14, dh0=2.0 ** -16)
+BITS = dict(y=2.0 ** -15, state=2.0 ** -17, dx=2.0 ** -15, ddt=2.0 ** -15, dB=2.0 ** -15, dC=2.0 ** -15, dA=2.0 ** -15, dD=2.0 ** -15,
+            ddt_bias=2.0 ** -15, dh0=2.0 ** -17)

@@ -70,8 +70,8 @@ hipError_t launch_gated_norm_bwd(const BlockNormParams& p, hipStream_t stream);
 hipError_t launch_add_norm(const BlockNormParams& p, hipStream_t stream);
 hipError_t launch_add_norm_bwd(const BlockNormParams& p, hipStream_t stream);
 // Most work-groups whose sums of the weights' gradients are left to add (of every head, for a
-// weight per head, at least one).
-constexpr int BLOCK_DW_GROUPS = 1024;
+// weight per head, at least one).  1024 were 38 us and not 31 at 3001 x 4096: most of their time went into the sums' rows.
+constexpr int BLOCK_DW_GROUPS = 512;
 
 // Sums over the rows of part [n][cols], in a fixed order.  Column c < split goes to
 // out[(c % inner) * outer + c / inner], a later one to out2[c - split].

@@ -4,7 +4,9 @@
 // with the W - 1 inputs before a sequence's first token in an initial state.  Backward:
 //   dz = dy act'(z),  dx_t = sum_d w_{W-1-d} dz_{t+d},  dw_i = sum_t dz_t x_{t-W+1+i}
 //
-// Bound by HBM: x is read and y written once (backward: x and dy, dx).  A thread takes eight
+// Bound by HBM: x is read and y written once (backward: x and dy, dx; there a token's 40 instructions a channel
+// take as long).  16384 x 12288 in bf16: 158 us, 5.1 TB/s; gradients of 2 x 8192 x 12288 4.6 TB/s, of 2 x 4096 x 4352,
+// where a SIMD's two waves have one run each, 72 us, 3.0 TB/s.  A thread takes eight
 // channels of a run of tokens and walks it, the window of its last W inputs in registers, so
 // that a run reads W - 1 rows that others read too (backward 2 (W - 1) of x, W - 1 of dy), from
 // L2 as a rule.  Lanes lie along the channels: a wave's loads and stores are 16 bytes a lane
@@ -395,13 +397,16 @@ ConvSplit conv_split(int64_t total, int64_t C, bool bwd) {
     ConvSplit k{};
     k.lanes = 64;
     while (k.lanes > 1 && k.lanes / 2 >= pieces) k.lanes /= 2;
+    // fewer lanes side by side where the last column of them would be mostly empty
     while (k.lanes > 16 && (pieces + k.lanes - 1) / k.lanes * k.lanes - pieces > pieces / 32) k.lanes /= 2;
     k.cols = (pieces + k.lanes - 1) / k.lanes;
-    if (bwd) {
+    if (bwd) {   // one round of two waves a SIMD, in runs of up to 32: 4096 x 4352 in runs of 18 tokens 32 us, of 16 40, of 32 39; 16384 x
+                 // 4352 in runs of 32 108 us, of 16 112, of 64 125
         const int64_t once = (total * pieces + 64 * 2048 - 1) / (64 * 2048);
-        k.run = (int)std::min<int64_t>(std::max<int64_t>((once + 1) / 2 * 2, 8), 64);
-    } else {
-        k.run = total * pieces >= (int64_t(1) << 22) ? 32 : 8;
+        k.run = (int)std::min<int64_t>(std::max<int64_t>((once + 1) / 2 * 2, 8), 32);
+    } else {     // long runs read fewer rows twice, short ones fill the device: 8 and 32 tokens are 5.9 and 11.1 us at 512 x 4352,
+                 // 29 and 31 at 8192 x 4352, 62 and 56 at 16384 x 4352, 161 and 154 at 16384 x 12288
+        k.run = total * pieces >= (int64_t(3) << 21) ? 32 : 8;
     }
     k.tiles = (total + (int64_t)k.run * (NT / k.lanes) - 1) / ((int64_t)k.run * (NT / k.lanes));
     return k;

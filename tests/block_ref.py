@@ -7,7 +7,7 @@ Tolerances.  Every result is rounded once, by at most half a step of its type re
     |bias| + sum |w x|; the activation's exponential, reciprocal and product are off by at most
     a unit each and its slope is at most 1.1: together 2^-20 mag.  dz = dy act'(z) is off by 2^-20 |dy| (1 + mag)
     (act' is at most 1.1, its own slope at most 0.5), dx by as much of sum |w| |dy| (1 + mag).  The weights'
-    gradients are summed over a run of at most 64 tokens, at most 256 runs and an eighth of the tiles, far fewer
+    gradients are summed over a run of at most 32 tokens, at most 256 runs and an eighth of the tiles, far fewer
     than 512 additions one after the other in these tests: 2^-24 512 = 2^-15 of the sum of the magnitudes.
   norms: the sum of squares takes at most 32 additions in a lane and 12 between lanes, 2^-18 of itself with the
     rounding of each square, its inverse root half of that, the gate's activation 2^-21: together 2^-17 of

@@ -285,12 +285,9 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
                 md[2] += md[3];
                 md[1] += md[2];
                 md[0] += md[1];
-                float above = 0.f;
-#pragma unroll
-                for (int o = 1; o < 4; ++o) {
-                    const float v = __shfl(md[0], lane + 16 * o);
-                    above += g + o < 4 ? v : 0.f;
-                }
+                // over the lane groups behind this one: pairs of groups come as the even and the odd, then the lower and the upper one
+                const Pair two = across<16>(md[0]), halves = across<32>(two.a + two.b);
+                const float above = (g & 1 ? 0.f : two.b) + (g < 2 ? halves.b : 0.f);
                 float diag = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {

@@ -101,6 +101,18 @@ def test_packed(cu, P, S):
     check_gradients(c, cu)
 
 
+@pytest.mark.parametrize("P,S", [(64, 128), (128, 64)])
+def test_many_sequences(P, S):
+    """More walks than half the compute units: work-groups of 256 columns, of which 320 (or 640) leave the last one part."""
+    say(f"ssm 130 sequences P={P} S={S}")
+    cu = [0]
+    for n in [100, 130] + [1 + i % 3 for i in range(128)]:
+        cu.append(cu[-1] + n)
+    c = ref.make(1, cu[-1], 5, P, S, 1, N=130, h0=True, seed=P)
+    check_forward(c, cu)
+    check_gradients(c, cu)
+
+
 @pytest.mark.parametrize("cu", [None, [0, 700, 701, 1100], [0, 64, 1024, 1024, 1088]])
 def test_segments(cu):
     """Long sequences on few heads: segments side by side, chained; their states from outside and to outside."""

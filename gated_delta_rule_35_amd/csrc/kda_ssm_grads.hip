@@ -151,22 +151,29 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
     uint32_t nskip = 0;
     f32x4 ns[KP][2], nds[KP][2];   // S and dS, 32 columns each
     const int lr = P == 64 ? tid >> 3 : tid >> 4, lp = P == 64 ? tid & 7 : tid & 15;   // row and piece of this thread
-    // behind the last head the buffers are empty: loads that always stand there can be counted, and wait for less
-    auto ask = [&](int h) {
-        const bool real = h < h_to;
-        const auto rx = chunk_rsrc(p.x.p + ch.row * p.x.sb + ch.tok * p.x.st + h * p.x.sh, p.x.st, real ? ch.rows : 0, P);
-        const auto ry = chunk_rsrc(p.dO.p + ch.row * p.dO.sb + ch.tok * p.dO.st + h * p.dO.sh, p.dO.st, real ? ch.rows : 0, P);
+    // What a head reads and writes, from its first element: one head on at the end of each turn.  Behind the last
+    // head the buffers are empty: loads that always stand there can be counted, and wait for less.
+    const uint16_t *px = p.x.p + ch.row * p.x.sb + ch.tok * p.x.st + h_from * p.x.sh,
+                   *py = p.dO.p + ch.row * p.dO.sb + ch.tok * p.dO.st + h_from * p.dO.sh;
+    uint16_t* pdx = p.dx + ((ch.row * p.T + ch.tok) * p.H + h_from) * P;
+    const float *ps = p.St + (slot * p.H + h_from) * S * P, *pds = p.dSt + (slot * p.H + h_from) * S * P;
+    char* prec = p.rec + (slot * p.H + h_from) * SSM_REC;
+    const float* pd = p.D ? p.D + h_from : nullptr;
+    const int nx_bytes = (int)((ch.rows - 1) * p.x.st + P) * 2, ny_bytes = (int)((ch.rows - 1) * p.dO.st + P) * 2;
+    const int skips = p.D ? 4 : 0;
+    auto ask = [&](bool real, int on) {   // inputs `on` heads further
+        const auto rx = make_rsrc(px + on * p.x.sh, real ? nx_bytes : 0), ry = make_rsrc(py + on * p.dO.sh, real ? ny_bytes : 0);
 #pragma unroll
         for (int u = 0; u < PX; ++u) {   // rows past the chunk's end come as zeros
             const int r = lr + 32 * u;
-            nx[u] = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(r * p.x.st * 2) + 16 * lp, 0, 0);
-            ny[u] = __builtin_amdgcn_raw_buffer_load_b128(ry, (int)(r * p.dO.st * 2) + 16 * lp, 0, 0);
+            nx[u] = __builtin_amdgcn_raw_buffer_load_b128(rx, r * (int)p.x.st * 2 + 16 * lp, 0, 0);
+            ny[u] = __builtin_amdgcn_raw_buffer_load_b128(ry, r * (int)p.dO.st * 2 + 16 * lp, 0, 0);
         }
-        nrec = __builtin_amdgcn_raw_buffer_load_b128(make_rsrc(p.rec + (slot * p.H + h) * SSM_REC, real ? SSM_REC : 0), 16 * tid, 0, 0);
-        nskip = __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(p.D + h, real && p.D ? 4 : 0), 0, 0, 0);
+        nrec = __builtin_amdgcn_raw_buffer_load_b128(make_rsrc(prec + on * SSM_REC, real ? SSM_REC : 0), 16 * tid, 0, 0);
+        nskip = __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(pd + on, real ? skips : 0), 0, 0, 0);
     };
-    auto ask_state = [&](const float* from, f32x4 (&to)[KP][2], int h, int first, int end) {   // columns 32 first .. 32 end - 1
-        const auto rs = make_rsrc(from + (slot * p.H + h) * S * P, h < h_to ? S * P * 4 : 0);
+    auto ask_state = [&](const float* from, f32x4 (&to)[KP][2], bool real, int first, int end) {   // columns 32 first .. 32 end - 1
+        const auto rs = make_rsrc(from, real ? S * P * 4 : 0);
 #pragma unroll
         for (int pp = first; pp < end; ++pp) {
 #pragma unroll
@@ -174,11 +181,9 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
                 to[pp][ct] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, 2048 * t + 1024 * ct + 16 * lane, pp * (S * 128), 0));
         }
     };
-    if (h_from < h_to) {
-        ask(h_from);
-        ask_state(p.St, ns, h_from, 0, 2);
-        ask_state(p.dSt, nds, h_from, 0, 2);
-    }
+    ask(h_from < h_to, 0);
+    ask_state(ps, ns, h_from < h_to, 0, 2);
+    ask_state(pds, nds, h_from < h_to, 0, 2);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
 
@@ -214,8 +219,9 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
         if (tid < SSM_REC / 16) *reinterpret_cast<u32x4*>(smem + L::REC + 16 * tid) = nrec;
         const float skip = __int_as_float(uniform((int)nskip));
         __syncthreads();
-        ask_state(p.St, ns, h, 2, KP);
-        ask_state(p.dSt, nds, h, 2, KP);
+        const bool more = h + 1 < h_to;
+        ask_state(ps, ns, true, 2, KP);
+        ask_state(pds, nds, true, 2, KP);
 
         // ---- the pair matrices' tiles
         {
@@ -311,7 +317,6 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
             *reinterpret_cast<u32x2*>(to + ds_off(row, (at >> 3) + 2)) = u32x2{w[2], w[3]};
         };
         {
-            const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
             const int nrow = state_row(t, jj >> 2, jj & 3);
             f32x4 v[MW], w[MW];
 #pragma unroll
@@ -356,7 +361,7 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
                 __builtin_amdgcn_sched_barrier(0);
             }
             q = sum64(q);
-            if (ln == 0) sS[wave] = S == 128 || wave < 4 ? q : 0.f;
+            if (lane == 0) sS[wave] = S == 128 || wave < 4 ? q : 0.f;
 #pragma unroll
             for (int mi = 0; mi < MW; ++mi) {
                 const int m = m0 + mi;
@@ -369,13 +374,13 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
                 if (g == 1) sY[64 * t + tok] = sy;
             }
         }
-        ask(h + 1);   // S and dS later: all at once would wait for the memory's queue
+        ask(more, 1);   // S and dS later: all at once would wait for the memory's queue
         __syncthreads();
 
         // ---- dB and dC from the pair matrices
-        ask_state(p.St, ns, h + 1, 0, 2);
+        ask_state(ps + S * P, ns, more, 0, 2);
         {
-            const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
+            const int ln = P == 128 ? opaque(lane) : lane, g = ln >> 4, jj = ln & 15;
             bf16x8 bcol[2], ccol[2];   // channels of tile t, tokens of k step kk
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
@@ -397,10 +402,11 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
         }
         __builtin_amdgcn_sched_barrier(0);
         // ---- dx, transposed: a lane holds four channels of one token
-        ask_state(p.dSt, nds, h + 1, 0, 2);
+        ask_state(pds + S * P, nds, more, 0, 2);
+        const int dst = p.H * P;
+        const auto rdx = chunk_rsrc(pdx, dst, ch.rows, P);
 #pragma unroll
         for (int half = 0; half < PX; ++half) {
-            const int lane = opaque(tid & 63), g = lane >> 4, jj = lane & 15;
             if (half > 0) {
                 __syncthreads();
                 if (S == 128 || wave < 4) {
@@ -443,9 +449,10 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
                 const int tok = 16 * (ma + mi) + jj, at = YO + col + 4 * g;
                 const f32x4 dy = widen(*reinterpret_cast<const u32x2*>(ty + tile_off(tok, at >> 3) + 2 * (at & 7)));
                 const f32x4 d = rec[SSM_DT + tok] * (rec[SSM_GA + tok] * a[mi] + b[mi]) + skip * dy;
-                if (tok < ch.rows)
-                    *reinterpret_cast<u32x2*>(p.dx + ((ch.row * p.T + ch.tok + tok) * p.H + h) * P + col + 4 * g) =
-                        u32x2{pack_bf2(d[0], d[1]), pack_bf2(d[2], d[3])};
+                // rows past the chunk's end lie past the buffer's and are dropped
+                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(__attribute__((ext_vector_type(2))) unsigned int,
+                                                                         u32x2{pack_bf2(d[0], d[1]), pack_bf2(d[2], d[3])}),
+                                                      rdx, tok * dst * 2 + 2 * (col + 4 * g), 0, 0);
             }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -473,8 +480,15 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
                 const float q = sum16(lane < 8 ? x : 0.f), d = sum16(lane >= 8 && lane < 12 ? x : 0.f);
                 x = lane == 0 ? q : lane == 1 ? d : x;
             }
-            if (wave < 7) reinterpret_cast<float*>(p.rec + (slot * p.H + h) * SSM_REC)[64 * (wave + 1) + lane] = x;
+            if (wave < 7) reinterpret_cast<float*>(prec)[64 * (wave + 1) + lane] = x;
         }
+        px += p.x.sh;
+        py += p.dO.sh;
+        pdx += P;
+        ps += S * P;
+        pds += S * P;
+        prec += SSM_REC;
+        if (p.D) ++pd;
         __syncthreads();   // everything in LDS but B and C is read
     }
 

@@ -17,9 +17,9 @@
 // through LDS, for dx.  The 64 x 64 matrices are ten tiles, dealt to the waves; they leave as
 // operand fragments for the second half of a head's work.
 //
-// B = 2, H = 64, P = 64, S = 128, T = 8192: 490 us, 15,400 clocks a chunk and head, nearly all of them issue (7,500
-// vector, 800 matrix and 1,200 LDS instructions on four SIMDs): tiles 3,600, V and W 4,200, dB and dC 1,900, dx 2,500, the
-// meetings 1,200.  The inputs of a head are asked for during the head before, S and dS apart from each
+// B = 2, H = 64, P = 64, S = 128, T = 8192: 452 us, 14,000 clocks a chunk and head, most of them issue (6,200 vector, 800
+// matrix and 1,150 LDS instructions on four SIMDs); of 15,400 before the last steps the tiles took 3,600, V and W 4,200,
+// dB and dC 1,900, dx 2,500, the meetings 1,200.  The inputs of a head are asked for during the head before, S and dS apart from each
 // other: all at once they waited for the memory's queue.
 //
 // Precision.  What reaches ddt and the sums enters in three bf16 parts (S and dS in V and W, 24
@@ -46,10 +46,10 @@ struct GL {
 };
 static_assert(GL<128>::BYTES <= 163840, "LDS");
 
-// Byte of a 16-byte piece of a row of dS's tile: written from rows 8 a + b and read from four rows each of
-// 8 g, its pieces are permuted by the rows' bits 0, 1, 3 and 4.
+// Byte of a 16-byte piece of a row of dS's tile: written from rows 8 a + b and read, two pieces of each, from four rows
+// of 8 g, its pieces are permuted by the rows' bits 0, 1, 4 and 3, the last one so that neighbouring g do not meet.
 __device__ __forceinline__ int ds_off(int row, int piece) {
-    return row * 256 + ((piece ^ (((row & 3) << 2) | ((row >> 3) & 3))) << 4);
+    return row * 256 + ((piece ^ (((row & 3) << 2) | ((row >> 2) & 2) | ((row >> 4) & 1))) << 4);
 }
 __device__ __forceinline__ bf16x8 two8(const char* tile, int row, int at) {   // elements at .. + 3 and 16 more on
     const int q = at >> 3, b = 2 * (at & 7);

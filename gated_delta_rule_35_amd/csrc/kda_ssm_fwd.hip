@@ -236,9 +236,9 @@ struct State {
     // S <- e^{G_last} S + B^T (w x), w = e^{G_last - G} d (REV: e^G): 32 tokens at a time, the next ones' w x formed
     // beside the products.  c0: the wave's first column in x's rows; read() is called once x has been read.
     template <bool REV, typename F>
-    __device__ __forceinline__ void grow(const char* tb, const char* tx, int c0, const float* rec, int lane, F read) {
+    __device__ __forceinline__ void grow(const char* tb, const char* tx, int c0, const float* rec, int ln, F read) {
         constexpr int QS = NT / 2;
-        const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
+        const int g = ln >> 4, jj = ln & 15;
         const float el = rec[SSM_EG + 63];
         Split<3> wx[2][2];
         constexpr int W = REV ? SSM_EG : SSM_W;
@@ -348,11 +348,11 @@ __global__ void __launch_bounds__(WT) kda_ssm_scan_kernel(const SsmParams p) {
             }
             lds_barrier();   // 3
             {
-                const int ln = opaque(lane), hn = opaque(hl);
+                const int ln = opaque(lane);
                 if (k.on && i + 1 < nch) x.ask(p.x, k, i + 1, ln);
                 if (k.on && i > 0) y.store(p, k, i - 1, ln);
                 if (i + 2 < nch) {
-                    t.ask(bc, k, i + 2, hn);
+                    t.ask(bc, k, i + 2, hl);
                     if (k.on) r.ask(p, k, i + 2, ln);
                 }
             }

@@ -637,7 +637,8 @@ kda_status_t kda_conv_decode(const kda_tensor_t* x, const kda_tensor_t* weight, 
  *   x, gate   [B, T, H, D], views; D a multiple of 8 up to 8192
  *   weight    [D], or [H, D] (one per head), fp32, 16-byte aligned; or NULL (ones)
  *   out       [B, T, H, D] of x's type; may be x itself where x is contiguous
- * More than 2^31 - 1 rows or 2^16 heads return KDA_ERR_UNSUPPORTED.
+ * More than 2^16 heads, or 2^27 rows of up to 128 channels, 2^25 of up to 2048, 2^23 of more, return
+ * KDA_ERR_UNSUPPORTED.
  */
 kda_status_t kda_gated_norm(const kda_tensor_t* x, const kda_tensor_t* gate, const kda_tensor_t* weight,
                             int32_t activation, int32_t gate_first, float eps, const kda_tensor_t* out, void* stream);

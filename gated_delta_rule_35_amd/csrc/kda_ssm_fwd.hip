@@ -15,7 +15,7 @@
 //   2  the pairs' products                                    | the next chunk's B, C and numbers into LDS
 //   3  the state grows, and the pair matrix (C B^T with its   | y stored, x asked for a chunk ahead, B and C two
 //      decays) of the next chunk, two waves half of it each
-// B = 2, H = 64, P = 64, S = 128, T = 8192: 200 us, the two walks 61 and 136 of it, the numbers 14, the chain 12 (HBM alone
+// B = 2, H = 64, P = 64, S = 128, T = 8192: 200 us, the two walks 58 and 133 of it, the numbers 14, the chain 12 (HBM alone
 // 55); bound by what two walks a SIMD issue between the meetings: 840 vector and 204 matrix instructions a
 // wave and chunk, 20,000 clocks a chunk.  T = 195 on 8 heads: 25 us, 5.6 a chunk.
 // y is formed transposed, so that a lane holds four channels of one token.  The decay between tokens of

@@ -12,19 +12,21 @@
 // rows); two walks a SIMD fill each other's gaps.  Four more waves bring what the walks need into LDS and store y: a
 // wave that waits for the memory's queue would keep its products waiting.  Three meetings a chunk:
 //   1  C S                                                    | y of the last chunk out of LDS, x in its place
-//   2  the pairs' products                                    | the next chunk's B, C and numbers into LDS
-//   3  the state grows, and the pair matrix (C B^T with its   | y stored, x asked for a chunk ahead, B and C two
-//      decays) of the next chunk, two waves half of it each
-// B = 2, H = 64, P = 64, S = 128, T = 8192: 200 us, the two walks 58 and 133 of it, the numbers 14, the chain 12 (HBM alone
+//   2  the pairs' products                                    | the next chunk's B, C and numbers (but e^G) into LDS
+//   3  the state grows, and the pair matrix (C B^T with its   | e^G into LDS, y stored, x asked for a chunk ahead,
+//      decays) of the next chunk, two waves half of it each   | B and C two
+// B = 2, H = 64, P = 64, S = 128, T = 8192: 221 us, the two walks 58 and 154 of it, the numbers 14, the chain 12 (HBM alone
 // 55); bound by what two walks a SIMD issue between the meetings: 840 vector and 204 matrix instructions a
 // wave and chunk, 20,000 clocks a chunk.  T = 195 on 8 heads: 25 us, 5.6 a chunk.
 // y is formed transposed, so that a lane holds four channels of one token.  The decay between tokens of
 // different blocks of sixteen is a product of a number of each token and one or two of the blocks,
 // all at most 1 for A <= 0; within a block it is formed from the difference.
 //
-// Precision.  x, B and C are bf16, the state and all sums fp32.  What enters the state is formed in three bf16
-// parts, fp32's 24 bits (the third is 14 us of 200 at B = 2, H = 64, T = 8192; without it the final state is off by
-// 2^-19 of itself); what only adds to y (S in C S, the pair matrix) in two, 16 bits for y's eight.
+// Precision.  x, B and C are bf16, the state and all sums fp32, and what multiplies them enters in three bf16
+// parts, fp32's 24 bits: the state in C S, the pair matrix with D, what enters the state.  y's terms may cancel: with
+// two parts of the first two (200 us, not 221, at B = 2, H = 64, T = 8192) y was off by up to 2^-18 of its terms, and by
+// 1.0 10^-4 of its norm from a 32-bit form that is now 2 10^-5 away.  Two parts of what enters the state would leave the
+// final state 2^-19 of itself off.
 #include "kda_ssm_device.h"
 
 namespace kda {
@@ -33,8 +35,8 @@ namespace {
 
 constexpr int WT = 768;   // eight walking and four loading waves
 
-struct FL {   // LDS of the full walk; slots of B, C and of the records by chunk's parity
-    static constexpr int C = 16384, SLOT = 32768, X = 65536, PM = X + 32768, REC = PM + 4 * 2 * GDR_TRI, BYTES = REC + 4 * 2 * SSM_REC;
+struct FL {   // LDS of the full walk; slots of B by chunk's parity
+    static constexpr int C = 32768, X = C + 16384, PM = X + 32768, PARTS = 3 * GDR_TRI, REC = PM + 4 * PARTS, BYTES = REC + 4 * SSM_REC;
 };
 static_assert(FL::BYTES == 163840, "LDS");
 struct AL {   // of the walk that forms what segments add: B, x and the records, all by chunk's parity
@@ -105,11 +107,11 @@ struct Tiles {
             v[u] = load16(rs, (int)(r * m.st * 2) + 16 * (e % PIECES));
         }
     }
-    __device__ __forceinline__ void put(char* to, int hl) const {
+    __device__ __forceinline__ void put(char* to, char* to2, int hl) const {   // to2: the second tile
 #pragma unroll
         for (int u = 0; u < N; ++u) {
             const int e = (u % (N / T)) * 256 + hl;
-            *reinterpret_cast<u32x4*>(to + (u * T / N) * 16384 + tile_off(e / PIECES, e % PIECES)) = v[u];
+            *reinterpret_cast<u32x4*>((u * T / N ? to2 : to) + tile_off(e / PIECES, e % PIECES)) = v[u];
         }
     }
 };
@@ -151,9 +153,18 @@ struct Record {
         *reinterpret_cast<u32x4*>(to + 16 * ln) = v[0];
         *reinterpret_cast<u32x4*>(to + 1024 + 16 * ln) = v[1];
     }
+    // The full walk's: one record for all chunks, since of the chunk at hand only e^G and SSM_W's row are read while the next
+    // one's come in.  That row goes by the chunk's parity to its own place or to SSM_GA's, which is not used; e^G comes last.
+    __device__ __forceinline__ void put_but_eg(char* to, int odd, int ln) const {
+        if (ln < 16 || ln >= 48) *reinterpret_cast<u32x4*>(to + 16 * ln) = v[0];
+        *reinterpret_cast<u32x4*>(to + (odd && ln >= 48 ? 4 * SSM_GA - 768 : 1024) + 16 * ln) = v[1];
+    }
+    __device__ __forceinline__ void put_eg(char* to, int ln) const {
+        if (ln >= 16 && ln < 32) *reinterpret_cast<u32x4*>(to + 16 * ln) = v[0];
+    }
 };
 
-// Row I of tiles of a chunk's pair matrix, in two parts, into the fragments (m, kk) of its lower triangle in
+// Row I of tiles of a chunk's pair matrix, in three parts, into the fragments (m, kk) of its lower triangle in
 // LDS; D is added to its diagonal.  C B^T is formed transposed: tile (J, I) holds in a lane rows j = 16 J + 4 g + r of column i = 16 I + jj.
 template <int S, int I>
 __device__ __forceinline__ void pair_row(const char* tb, const char* tc, const float* rec, float skip, char* pm, int lane) {
@@ -186,17 +197,17 @@ __device__ __forceinline__ void pair_row(const char* tb, const char* tc, const f
             a[J] *= (num4(rec, SSM_KA, J, g) * d) * ri;
         }
         char* to = pm + tri_frag(I, J >> 1) * GDR_FRAG + 16 * ln + 8 * (J & 1);
-        const uint32_t h0 = pack_bf2(a[J][0], a[J][1]), h1 = pack_bf2(a[J][2], a[J][3]);
-        *reinterpret_cast<u32x2*>(to) = u32x2{h0, h1};
-        *reinterpret_cast<u32x2*>(to + GDR_TRI) =
-            u32x2{pack_bf2(a[J][0] - bf_lo(h0), a[J][1] - bf_hi(h0)), pack_bf2(a[J][2] - bf_lo(h1), a[J][3] - bf_hi(h1))};
+        u32x4 part[3];
+        split_pair<3>(part, 0, a[J][0], a[J][1]);
+        split_pair<3>(part, 1, a[J][2], a[J][3]);
+#pragma unroll
+        for (int n = 0; n < 3; ++n) *reinterpret_cast<u32x2*>(to + n * GDR_TRI) = u32x2{part[n][0], part[n][1]};
     }
     __builtin_amdgcn_sched_barrier(0);
 }
 // Half of it: five tiles each.
 template <int S>
-__device__ __forceinline__ void pair_half(int half, const char* tb, const float* rec, float skip, char* pm, int lane) {
-    const char* tc = tb + FL::C;
+__device__ __forceinline__ void pair_half(int half, const char* tb, const char* tc, const float* rec, float skip, char* pm, int lane) {
     if (half == 0) {
         pair_row<S, 3>(tb, tc, rec, skip, pm, lane);
         pair_row<S, 0>(tb, tc, rec, skip, pm, lane);
@@ -233,19 +244,17 @@ struct State {
             }
         }
     }
-    // S <- e^{G_last} S + B^T (w x), w = e^{G_last - G} d (REV: e^G): 32 tokens at a time, the next ones' w x formed
-    // beside the products.  c0: the wave's first column in x's rows; read() is called once x has been read.
-    template <bool REV, typename F>
-    __device__ __forceinline__ void grow(const char* tb, const char* tx, int c0, const float* rec, int ln, F read) {
+    // S <- el S + B^T (w x), el = e^{G_last}, w = e^{G_last - G} d (backwards e^G): 32 tokens at a time, the next ones' w x
+    // formed beside the products.  c0: the wave's first column in x's rows; read() is called once x has been read.
+    template <typename F>
+    __device__ __forceinline__ void grow(const char* tb, const char* tx, int c0, float el, const float* w, int ln, F read) {
         constexpr int QS = NT / 2;
         const int g = ln >> 4, jj = ln & 15;
-        const float el = rec[SSM_EG + 63];
         Split<3> wx[2][2];
-        constexpr int W = REV ? SSM_EG : SSM_W;
         auto weigh = [&](int kk, int c) {
             const u32x4 xx = __builtin_bit_cast(u32x4, x_frag(tx, kk, c0 + 16 * c, ln));
-            wx[kk][c] = split_acc<3>(num4(rec, W, 2 * kk, g) * widen(u32x2{xx[0], xx[1]}),
-                                     num4(rec, W, 2 * kk + 1, g) * widen(u32x2{xx[2], xx[3]}));
+            wx[kk][c] = split_acc<3>(num4(w, 0, 2 * kk, g) * widen(u32x2{xx[0], xx[1]}),
+                                     num4(w, 0, 2 * kk + 1, g) * widen(u32x2{xx[2], xx[3]}));
         };
         bf16x8 bq[2][2];
         auto columns = [&](int q) {   // of step q: k step q / QS, tiles 2 (q % QS) ..
@@ -299,10 +308,8 @@ __global__ void __launch_bounds__(WT) kda_ssm_scan_kernel(const SsmParams p) {
     if (!walk_place(p, (int)blockIdx.x, w, k)) return;
     const int nch = k.nch;
     const int64_t state = (int64_t)S * p.P;
-    char *tx = smem + FL::X + w * 8192, *pm = smem + FL::PM + w * 2 * GDR_TRI;
-    auto slot = [&](int i) { return smem + (i & 1) * FL::SLOT; };
-    auto record = [&](int i) { return smem + FL::REC + ((i & 1) * 4 + w) * SSM_REC; };
-    auto numbers = [&](int i) { return reinterpret_cast<const float*>(record(i)); };
+    char *tc = smem + FL::C, *tx = smem + FL::X + w * 8192, *pm = smem + FL::PM + w * FL::PARTS, *record = smem + FL::REC + w * SSM_REC;
+    auto tile = [&](int i) { return smem + (i & 1) * 16384; };   // B
 
     if (wave >= 8) {
         // ================= the waves that load and store =================
@@ -314,7 +321,7 @@ __global__ void __launch_bounds__(WT) kda_ssm_scan_kernel(const SsmParams p) {
         Record r;
         if (k.on) {   // above the diagonal
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
+            for (int n = 0; n < 3; ++n) {
                 *reinterpret_cast<u32x2*>(pm + n * GDR_TRI + tri_frag(0, 0) * GDR_FRAG + 16 * lane + 8) = u32x2{0, 0};
                 *reinterpret_cast<u32x2*>(pm + n * GDR_TRI + tri_frag(2, 1) * GDR_FRAG + 16 * lane + 8) = u32x2{0, 0};
             }
@@ -324,8 +331,11 @@ __global__ void __launch_bounds__(WT) kda_ssm_scan_kernel(const SsmParams p) {
             r.ask(p, k, 0, lane);
             x.ask(p.x, k, 0, lane);
         }
-        t.put(slot(0), hl);
-        if (k.on) r.put(record(0), lane);
+        t.put(tile(0), tc, hl);
+        if (k.on) {
+            r.put_but_eg(record, 0, lane);
+            r.put_eg(record, lane);
+        }
         if (nch > 1) {
             t.ask(bc, k, 1, hl);
             if (k.on) r.ask(p, k, 1, lane);
@@ -343,13 +353,16 @@ __global__ void __launch_bounds__(WT) kda_ssm_scan_kernel(const SsmParams p) {
             }
             lds_barrier();   // 2
             if (i + 1 < nch) {
-                t.put(slot(i + 1), opaque(hl));
-                if (k.on) r.put(record(i + 1), opaque(lane));
+                t.put(tile(i + 1), tc, opaque(hl));
+                if (k.on) r.put_but_eg(record, (i + 1) & 1, opaque(lane));
             }
             lds_barrier();   // 3
             {
                 const int ln = opaque(lane);
-                if (k.on && i + 1 < nch) x.ask(p.x, k, i + 1, ln);
+                if (k.on && i + 1 < nch) {
+                    r.put_eg(record, ln);
+                    x.ask(p.x, k, i + 1, ln);
+                }
                 if (k.on && i > 0) y.store(p, k, i - 1, ln);
                 if (i + 2 < nch) {
                     t.ask(bc, k, i + 2, hl);
@@ -375,56 +388,59 @@ __global__ void __launch_bounds__(WT) kda_ssm_scan_kernel(const SsmParams p) {
         z.load(k.on ? from : nullptr, p, pc, lane);
     }
     const float skip = k.on && p.D ? p.D[k.head] : 0.f;
+    const float* rec = reinterpret_cast<const float*>(record);
     if (nch > 0) {
         lds_barrier();
-        if (k.on) pair_half<S>(wave & 1, slot(0), numbers(0), skip, pm, lane);
+        if (k.on) pair_half<S>(wave & 1, tile(0), tc, rec, skip, pm, lane);
     }
     for (int i = 0; i < nch; ++i) {
         lds_barrier();   // 1: B, C and the records, and the pair matrix at 2
-        const char* tc = slot(i) + FL::C;
-        const float* rec = numbers(i);
         if (!k.on) {
             lds_barrier();
             lds_barrier();
             continue;
         }
         f32x4 y[4][2];   // channels 16 c + 4 g + r of token 16 m + jj
-        {   // C S, the state's parts of a k step formed beside the products of the one before it
+        {   // C S, 32 tokens at a time; the state's parts of a k step formed beside the products of the one before it
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
-            Split<2> sp[2][2];
-            bf16x8 cf[2][4];
-            auto prepare = [&](int kk) {
+            Split<3> sp[2][2];
+            bf16x8 cf[2][2];
+            auto parts = [&](int kk, int c) { sp[kk & 1][c] = split_acc<3>(z.st[2 * kk][c], z.st[2 * kk + 1][c]); };
+            auto rows = [&](int q) {   // of step q: k step q / 2, tokens 32 (q % 2) ..
 #pragma unroll
-                for (int c = 0; c < 2; ++c) sp[kk & 1][c] = split_acc<2>(z.st[2 * kk][c], z.st[2 * kk + 1][c]);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) cf[kk & 1][m] = row_frag(tc, m, kk, g, jj);
+                for (int m = 0; m < 2; ++m) cf[q & 1][m] = row_frag(tc, 2 * (q & 1) + m, q >> 1, g, jj);
             };
-            prepare(0);
+            parts(0, 0);
+            parts(0, 1);
+            rows(0);
 #pragma unroll
             for (int m = 0; m < 4; ++m) y[m][0] = y[m][1] = f32x4{0.f, 0.f, 0.f, 0.f};
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int kk = 0; kk < KT; ++kk) {
-                if (kk + 1 < KT) prepare(kk + 1);
+            for (int q = 0; q < 2 * KT; ++q) {
+                const int kk = q >> 1, m0 = 2 * (q & 1);
+                if (q + 1 < 2 * KT) rows(q + 1);
+                if (kk + 1 < KT) parts(kk + 1, q & 1);
 #pragma unroll
-                for (int n = 1; n >= 0; --n) {
+                for (int n = 2; n >= 0; --n) {
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        y[m][0] = mfma_bf(sp[kk & 1][0].s[n], cf[kk & 1][m], y[m][0]);
-                        y[m][1] = mfma_bf(sp[kk & 1][1].s[n], cf[kk & 1][m], y[m][1]);
+                    for (int m = 0; m < 2; ++m) {
+                        y[m0 + m][0] = mfma_bf(sp[kk & 1][0].s[n], cf[q & 1][m], y[m0 + m][0]);
+                        y[m0 + m][1] = mfma_bf(sp[kk & 1][1].s[n], cf[q & 1][m], y[m0 + m][1]);
                     }
                 }
-                interleave<16, 4, 1, 0>();
+                interleave<12, 4, 1, 0>();
             }
         }
         lds_barrier();   // 2: x
         u32x2 out[4][2];   // y as bf16
+        const float el = __int_as_float(uniform(__float_as_int(rec[SSM_EG + 63])));
         {   // y = e^G C S, then the pairs' products
             const int ln = opaque(lane), g = ln >> 4, jj = ln & 15;
             bf16x8 xf[2][2], pf[6];
             constexpr int FM[6] = {0, 1, 2, 3, 2, 3}, FK[6] = {0, 0, 0, 0, 1, 1};
 #pragma unroll
-            for (int f = 0; f < 6; ++f) pf[f] = lds_bf8(pm + GDR_TRI + tri_frag(FM[f], FK[f]) * GDR_FRAG + 16 * ln);
+            for (int f = 0; f < 6; ++f) pf[f] = lds_bf8(pm + 2 * GDR_TRI + tri_frag(FM[f], FK[f]) * GDR_FRAG + 16 * ln);
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
@@ -437,10 +453,10 @@ __global__ void __launch_bounds__(WT) kda_ssm_scan_kernel(const SsmParams p) {
                 for (int c = 0; c < 2; ++c) y[m][c] *= eg;
             }
 #pragma unroll
-            for (int n = 1; n >= 0; --n) {
+            for (int n = 2; n >= 0; --n) {
 #pragma unroll
                 for (int f = 0; f < 6; ++f) {
-                    if (n == 0) pf[f] = lds_bf8(pm + tri_frag(FM[f], FK[f]) * GDR_FRAG + 16 * ln);
+                    if (n < 2) pf[f] = lds_bf8(pm + n * GDR_TRI + tri_frag(FM[f], FK[f]) * GDR_FRAG + 16 * ln);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) y[FM[f]][c] = mfma_bf(xf[FK[f]][c], pf[f], y[FM[f]][c]);
                 }
@@ -455,8 +471,8 @@ __global__ void __launch_bounds__(WT) kda_ssm_scan_kernel(const SsmParams p) {
         lds_barrier();   // 3: the pair matrix is read
         // of a SIMD's two waves one grows first, the other forms its pairs first
         const bool pairs = i + 1 < nch;
-        if (pairs && wave >= 4) pair_half<S>(wave & 1, slot(i + 1), numbers(i + 1), skip, pm, lane);
-        z.template grow<false>(slot(i), tx, x0, rec, lane, [&]() {   // y in the place of x
+        if (pairs && wave >= 4) pair_half<S>(wave & 1, tile(i + 1), tc, rec, skip, pm, lane);
+        z.grow(tile(i), tx, x0, el, rec + (i & 1 ? SSM_GA : SSM_W), opaque(lane), [&]() {   // y in the place of x
             const int ln = opaque(lane);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
@@ -465,7 +481,7 @@ __global__ void __launch_bounds__(WT) kda_ssm_scan_kernel(const SsmParams p) {
                     *reinterpret_cast<u32x2*>(tx + x_off(16 * m + (ln & 15), x0 + 16 * c + 4 * (ln >> 4))) = out[m][c];
             }
         });
-        if (pairs && wave < 4) pair_half<S>(wave & 1, slot(i + 1), numbers(i + 1), skip, pm, lane);
+        if (pairs && wave < 4) pair_half<S>(wave & 1, tile(i + 1), tc, rec, skip, pm, lane);
     }
     if (nch > 0) lds_barrier();   // the last chunk's y
     if (k.on && p.hT && k.sg.index == k.sg.count - 1)
@@ -498,7 +514,7 @@ __device__ __forceinline__ void ssm_adds(const SsmParams& p, char* smem, int blo
             r.ask(p, k, at(i), lane);
         };
         auto put = [&](int i) {
-            t.put(tile(i), hl);
+            t.put(tile(i), nullptr, hl);
             if (!k.on) return;
             x.put(columns(i), lane);
             r.put(record(i), lane);
@@ -522,7 +538,7 @@ __device__ __forceinline__ void ssm_adds(const SsmParams& p, char* smem, int blo
         if (!k.on) continue;
         const float* rec = reinterpret_cast<const float*>(record(i));
         total *= rec[SSM_EG + 63];
-        z.template grow<REV>(tile(i), columns(i), x0, rec, lane, []() {});
+        z.grow(tile(i), columns(i), x0, rec[SSM_EG + 63], rec + (REV ? SSM_EG : SSM_W), lane, []() {});
     }
     if (!k.on) return;
     z.store((REV ? p.dseg : p.seg) + (k.sslot * p.H + k.head) * S * p.P, p, pc, lane);

@@ -698,8 +698,8 @@ kda_status_t kda_add_norm_bwd(const kda_tensor_t* sum, const kda_tensor_t* weigh
  * 2^23 elements apart.  Every other tensor is contiguous.  Other head and state dimensions, more
  * than 2^31 - 1 tokens, or grids above 2^22 work-groups ((chunk slot, head) pairs among them)
  * return KDA_ERR_UNSUPPORTED.
- * Precision: states and sums are fp32; what enters the state is formed from operands at fp32's 24
- * bits, what only adds to y at 16; y is rounded to bf16 once.  A token that holds NaN or infinity may
+ * Precision: states and sums are fp32, products are formed from operands at fp32's 24 bits; y is
+ * rounded to bf16 once.  A token that holds NaN or infinity may
  * reach every token of its 64-token chunk and later ones of its sequence, and through x only its own head.
  * workspace: kda_ssm_fwd_workspace_size(B * T, N, H, G, P, S) bytes, 256-byte aligned, as for
  * kda_gdr_fwd; NULL allocates it in stream order.

@@ -22,9 +22,10 @@
 // dB and dC 1,900, dx 2,500, the meetings 1,200.  The inputs of a head are asked for during the head before, S and dS apart from each
 // other: all at once they waited for the memory's queue.
 //
-// Precision.  What reaches ddt and the sums enters in three bf16 parts (S and dS in V and W, 24
-// bits; in two, dA was off by 2 10^-6 at B = 2, H = 64, T = 8192, fp32's plain form by 4 10^-7), what only reaches
-// bf16 results in two (K, E, and dS in dx).
+// Precision.  What multiplies x, dy, B and C enters in three bf16 parts, fp32's 24 bits: S and dS in V and W (in two parts,
+// dA was off by 2 10^-6 at B = 2, H = 64, T = 8192, fp32's plain form by 4 10^-7), K, E and dS in dx.  The terms of dx, dB
+// and dC may cancel: with two parts of the last three (the call 820 us there, not 855) they were off by up to 2^-18 of
+// their terms, and by 9 10^-5 of their norm from a 32-bit form that is now 2 to 3 10^-5 away.
 #include "kda_block.h"
 #include "kda_ssm_device.h"
 
@@ -39,12 +40,13 @@ struct GL {
     static constexpr int B = 0, C = 16384, X = 32768;            // [64][256 bytes] tiles, swizzled
     static constexpr int DY = P == 64 ? X : X + 16384;           // P = 64: beside x in its rows
     static constexpr int DS = DY + 16384;                        // [S][64 columns, two parts], swizzled
-    static constexpr int KC = DS + 32768, KB = KC + 2 * GDR_TRI, EX = KB + 2 * GDR_TRI;   // fragments, two parts each
-    static constexpr int REC = EX + 2 * GDR_TRI;
+    static constexpr int DT = P == 64 ? DS + 32768 : DS;         // [64][64 columns of rows r and r + 64, the third part]
+    static constexpr int KC = DS + (P == 64 ? 49152 : 32768), KB = KC + 3 * GDR_TRI, EX = KB + 3 * GDR_TRI;   // fragments, three parts each
+    static constexpr int REC = EX + 3 * GDR_TRI;
     static constexpr int RS = REC + SSM_REC, CS = RS + 4 * 256, DR = CS + 4 * 256;   // sums of M's tiles by row, by column
     static constexpr int UP = DR + 256, YP = UP + 8 * 256, SD = YP + 8 * 256, BYTES = SD + 256;
 };
-static_assert(GL<128>::BYTES <= 163840, "LDS");
+static_assert(GL<64>::BYTES <= 163840 && GL<128>::BYTES <= 163840, "LDS");
 
 // Byte of a 16-byte piece of a row of dS's tile: written from rows 8 a + b and read, two pieces of each, from four rows
 // of 8 g, its pieces are permuted by the rows' bits 0, 1, 4 and 3, the last one so that neighbouring g do not meet.
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
     // what no tile of the pair matrices covers in the fragments
     if (tid < 64) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < 3; ++n) {
             *reinterpret_cast<u32x2*>(smem + L::KC + n * GDR_TRI + tri_frag(0, 0) * GDR_FRAG + 16 * lane + 8) = u32x2{0, 0};
             *reinterpret_cast<u32x2*>(smem + L::KC + n * GDR_TRI + tri_frag(2, 1) * GDR_FRAG + 16 * lane + 8) = u32x2{0, 0};
 #pragma unroll
@@ -267,10 +269,11 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
             }
             auto put = [&](int list, int frag, int half, const f32x4& a) {
                 char* to = smem + list + frag * GDR_FRAG + 16 * lane + 8 * half;
-                const uint32_t h0 = pack_bf2(a[0], a[1]), h1 = pack_bf2(a[2], a[3]);
-                *reinterpret_cast<u32x2*>(to) = u32x2{h0, h1};
-                *reinterpret_cast<u32x2*>(to + GDR_TRI) =
-                    u32x2{pack_bf2(a[0] - bf_lo(h0), a[1] - bf_hi(h0)), pack_bf2(a[2] - bf_lo(h1), a[3] - bf_hi(h1))};
+                u32x4 part[3];
+                split_pair<3>(part, 0, a[0], a[1]);
+                split_pair<3>(part, 1, a[2], a[3]);
+#pragma unroll
+                for (int n = 0; n < 3; ++n) *reinterpret_cast<u32x2*>(to + n * GDR_TRI) = u32x2{part[n][0], part[n][1]};
             };
             put(L::KC, tri_frag(I, J >> 1), J & 1, lt);
             put(L::KB, upper_frag(J, I >> 1), I & 1, l);
@@ -309,10 +312,12 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
         __builtin_amdgcn_sched_barrier(0);
         // ---- V and W of the wave's state channels, 32 columns at a time, and dS's parts into LDS
         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-        u32x4 later[PX > 1 ? 2 : 1][2];   // two parts of dS's columns 64 ..
-        auto put_ds = [&](int q, int n, u32x4 w, int row, int g) {   // part n of 32 columns
-            const int at = 64 * n + 32 * q + 4 * g;
-            char* to = smem + L::DS + 2 * (at & 7);
+        // For P = 128 dS's tile holds by turns two parts of columns 0 .. 63, the third part of all, two parts of the others
+        u32x4 later[PX > 1 ? 2 : 1][2], third[PX > 1 ? KP : 1];   // two parts of columns 64 ..; third parts
+        auto put_ds = [&](int q, int n, u32x4 w, int row, int g, int base) {   // part n of 32 columns
+            const int at = n == 2 ? 64 * (row >> 6) + 32 * q + 4 * g : 64 * n + 32 * q + 4 * g;
+            char* to = smem + base + 2 * (at & 7);
+            if (n == 2) row &= 63;
             *reinterpret_cast<u32x2*>(to + ds_off(row, at >> 3)) = u32x2{w[0], w[1]};
             *reinterpret_cast<u32x2*>(to + ds_off(row, (at >> 3) + 2)) = u32x2{w[2], w[3]};
         };
@@ -332,10 +337,11 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
                 {
                     const Split<3> dsp = split_acc<3>(nds[pp][0], nds[pp][1]);
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
+                    for (int n = 0; n < 3; ++n) {
                         const u32x4 part = __builtin_bit_cast(u32x4, dsp.s[n]);
-                        if (pp >= 2) later[pp - 2][n] = part;
-                        else if (S == 128 || wave < 4) put_ds(pp, n, part, nrow, g);
+                        if (P == 128 && n == 2) third[pp] = part;
+                        else if (pp >= 2) later[pp - 2][n] = part;
+                        else if (S == 128 || wave < 4) put_ds(pp, n, part, nrow, g, n == 2 ? L::DT : L::DS);
                     }
                     bf16x8 f[MW];
 #pragma unroll
@@ -388,7 +394,7 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
                 ccol[kk] = col_frag(tc, t, kk, g, jj);
             }
 #pragma unroll
-            for (int n = 1; n >= 0; --n) {
+            for (int n = 2; n >= 0; --n) {
 #pragma unroll
                 for (int mi = 0; mi < MW; ++mi) {
                     const int m = m0 + mi;
@@ -405,33 +411,54 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
         ask_state(pds + S * P, nds, more, 0, 2);
         const int dst = p.H * P;
         const auto rdx = chunk_rsrc(pdx, dst, ch.rows, P);
+        const int pt = wave & 3, ma = 2 * (wave >> 2);   // columns 16 pt .. of 64; tokens of two tiles
+        f32x4 ds[PX][2];   // B dS
 #pragma unroll
-        for (int half = 0; half < PX; ++half) {
-            if (half > 0) {
-                __syncthreads();
-                if (S == 128 || wave < 4) {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) put_ds(q, n, later[PX > 1 ? q : 0][n], state_row(t, jj >> 2, jj & 3), g);
-                    }
-                }
-                __syncthreads();
-            }
-            const int pt = wave & 3, ma = 2 * (wave >> 2), col = 64 * half + 16 * pt;   // columns; tokens of two tiles
-            f32x4 a[2] = {zero, zero}, b[2] = {zero, zero};
+        for (int half = 0; half < PX; ++half) ds[half][0] = ds[half][1] = zero;
+        // a + B times parts `from` .. `to` - 1 of dS's columns 64 half .. in LDS
+        auto times_ds = [&](f32x4 (&a)[2], int from, int to, int third_at) {
 #pragma unroll
             for (int kk = 0; kk < KT; ++kk) {
                 const bf16x8 b0 = row_frag(tb, ma, kk, g, jj), b1 = row_frag(tb, ma + 1, kk, g, jj);
 #pragma unroll
-                for (int n = 1; n >= 0; --n) {
-                    const int q = 8 * n + 2 * pt + ((jj & 3) >> 1), r = 32 * kk + 8 * g + (jj >> 2);
-                    const char* ds = smem + L::DS + 8 * (jj & 1);
-                    const bf16x8 d = join(lds_tr(ds + ds_off(r, q)), lds_tr(ds + ds_off(r + 4, q)));
+                for (int n = to - 1; n >= from; --n) {
+                    const int q = (n == 2 ? 8 * (kk >> 1) : 8 * n) + 2 * pt + ((jj & 3) >> 1), r = (n == 2 ? 32 * (kk & 1) : 32 * kk) + 8 * g + (jj >> 2);
+                    const char* at = smem + (n == 2 ? third_at : L::DS) + 8 * (jj & 1);
+                    const bf16x8 d = join(lds_tr(at + ds_off(r, q)), lds_tr(at + ds_off(r + 4, q)));
                     a[0] = mfma_bf(d, b0, a[0]);
                     a[1] = mfma_bf(d, b1, a[1]);
                 }
             }
+        };
+        if (P == 64) {
+            times_ds(ds[0], 0, 3, L::DT);
+        } else {
+            const int nrow = state_row(t, jj >> 2, jj & 3);
+            const bool puts = S == 128 || wave < 4;
+            times_ds(ds[0], 0, 2, 0);
+            __syncthreads();
+            if (puts) {
+#pragma unroll
+                for (int q = 0; q < KP; ++q) put_ds(q & 1, 2, third[PX > 1 ? q : 0], nrow, g, L::DT + 16384 * (q >> 1));
+            }
+            __syncthreads();
+            times_ds(ds[0], 2, 3, L::DT);
+            times_ds(ds[PX - 1], 2, 3, L::DT + 16384);
+            __syncthreads();
+            if (puts) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) put_ds(q, n, later[PX > 1 ? q : 0][n], nrow, g, L::DS);
+                }
+            }
+            __syncthreads();
+            times_ds(ds[PX - 1], 0, 2, 0);
+        }
+#pragma unroll
+        for (int half = 0; half < PX; ++half) {
+            const int col = 64 * half + 16 * pt;
+            f32x4 b[2] = {zero, zero};
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
                 if (kk == 0 && ma >= 2) continue;
@@ -440,15 +467,15 @@ __global__ void __launch_bounds__(NT) kda_ssm_grads_kernel(const SsmParams p) {
 #pragma unroll
                 for (int mi = 0; mi < 2; ++mi) {
                     const int f = ma < 2 ? 2 * mi + kk : 4 + mi;   // fragment (ma + mi, kk)
-                    b[mi] = mfma_bf(yf, lds_bf8(ex + f * GDR_FRAG + GDR_TRI), b[mi]);
-                    b[mi] = mfma_bf(yf, lds_bf8(ex + f * GDR_FRAG), b[mi]);
+#pragma unroll
+                    for (int n = 2; n >= 0; --n) b[mi] = mfma_bf(yf, lds_bf8(ex + f * GDR_FRAG + n * GDR_TRI), b[mi]);
                 }
             }
 #pragma unroll
             for (int mi = 0; mi < 2; ++mi) {
                 const int tok = 16 * (ma + mi) + jj, at = YO + col + 4 * g;
                 const f32x4 dy = widen(*reinterpret_cast<const u32x2*>(ty + tile_off(tok, at >> 3) + 2 * (at & 7)));
-                const f32x4 d = rec[SSM_DT + tok] * (rec[SSM_GA + tok] * a[mi] + b[mi]) + skip * dy;
+                const f32x4 d = rec[SSM_DT + tok] * (rec[SSM_GA + tok] * ds[half][mi] + b[mi]) + skip * dy;
                 // rows past the chunk's end lie past the buffer's and are dropped
                 __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(__attribute__((ext_vector_type(2))) unsigned int,
                                                                          u32x2{pack_bf2(d[0], d[1]), pack_bf2(d[2], d[3])}),

@@ -721,9 +721,9 @@ kda_status_t kda_ssm_fwd(const kda_tensor_t* x, const kda_tensor_t* dt, const kd
  *                                   may be NULL, and without D or dt_bias have to be
  *   d_initial_state   [N, H, S, P]  fp32, or NULL (not computed)
  * An empty sequence passes d_final_state through to its d_initial_state; rows of tokens in no
- * sequence are not written.  ddt, dA, ddt_bias and dD are formed from operands at 24 bits, dx, dB and dC
- * at 16.  workspace: kda_ssm_bwd_workspace_size() bytes, as above: the states
- * entering and the gradients leaving every chunk, 4 S P bytes each for every (chunk slot, head).
+ * sequence are not written.  All are formed from operands at fp32's 24 bits.  workspace:
+ * kda_ssm_bwd_workspace_size() bytes, as above: the states entering and the gradients leaving every
+ * chunk, 4 S P bytes each for every (chunk slot, head).
  */
 int64_t kda_ssm_bwd_workspace_size(int64_t total_tokens, int64_t num_sequences, int64_t num_heads, int64_t num_groups,
                                    int64_t head_dim, int64_t state_dim);

@@ -110,3 +110,86 @@ def test_a_state_against_the_token_itself(P, S):
     c["C"][..., 3] = -1
     c["x"] = c["x"] + 1
     check_y(c, 70 * H * P)
+
+
+def fine(gen, n):
+    """n triples of bf16 numbers whose sum has 24 bits, all but its last seven or eight the same."""
+    r = (1 + torch.rand(1, generator=gen)).bfloat16().float() * 2.0 ** -8
+    s = (1 + torch.rand(n, generator=gen)).bfloat16().float() * 2.0 ** -16
+    return torch.stack([torch.ones(n), r.expand(n), s], dim=1)
+
+
+@pytest.mark.parametrize("P,S", SHAPES)
+def test_dC_of_tokens_against_each_other(P, S):
+    """dC_i = d_j B_j - d_k B_k."""
+    say(f"ssm cancel dC P={P} S={S}")
+    gen = torch.Generator().manual_seed(P + S + 3)
+    B, T = 24, 100
+    c = zeros(B, T, 1, P, S)
+    c["dy"][..., 7] = 1
+    for b, (i, j) in enumerate(zip(*pairs(gen, B, T))):
+        v = rand(gen, S).bfloat16()
+        c["B"][b, i, 0], c["B"][b, j, 0] = v, -v
+        c["x"][b, [i, j], 0, 7] = 1
+        c["dt"][b, i] = rand(gen, 1)
+        c["dt"][b, j] = near(c["dt"][b, i], gen)
+    check(c, "dC", B * S)
+
+
+@pytest.mark.parametrize("P,S", SHAPES)
+def test_dB_of_tokens_against_each_other(P, S):
+    """dB_k = <dy_i, x_k> C_i - <dy_j, x_k> C_j."""
+    say(f"ssm cancel dB P={P} S={S}")
+    gen = torch.Generator().manual_seed(P + S + 4)
+    B, T = 24, 100
+    c = zeros(B, T, 1, P, S)
+    c["x"][..., 0, [3, 20, P - 1]] = 1
+    for b, (i, j) in enumerate(zip(*pairs(gen, B, T))):
+        v = rand(gen, S).bfloat16()
+        c["C"][b, i, 0], c["C"][b, j, 0] = v, -v
+        for t, f in zip((i, j), fine(gen, 2)):
+            c["dy"][b, t, 0, [3, 20, P - 1]] = f.bfloat16()
+    check(c, "dB", B * S)
+
+
+@pytest.mark.parametrize("P,S", SHAPES)
+def test_dx_of_tokens_against_each_other(P, S):
+    """dx_k = <C_i, B_k> dy_i - <C_j, B_k> dy_j."""
+    say(f"ssm cancel dx P={P} S={S}")
+    gen = torch.Generator().manual_seed(P + S + 5)
+    B, T, H = 24, 100, 2
+    c = zeros(B, T, H, P, S)
+    c["B"][..., 0, [3, 20, S - 1]] = 1
+    for b, (i, j) in enumerate(zip(*pairs(gen, B, T))):
+        v = rand(gen, H, P).bfloat16()
+        c["dy"][b, i], c["dy"][b, j] = v, -v
+        for t, f in zip((i, j), fine(gen, 2)):
+            c["C"][b, t, 0, [3, 20, S - 1]] = f.bfloat16()
+    check(c, "dx", B * H * P)
+
+
+@pytest.mark.parametrize("P,S", SHAPES)
+def test_dx_of_channels_of_a_state_against_each_other(P, S):
+    """dx = dS_a - dS_b for the gradient of a final state."""
+    say(f"ssm cancel dS P={P} S={S}")
+    gen = torch.Generator().manual_seed(P + S + 6)
+    c = zeros(2, 70, 3, P, S)
+    c["dlast"] = torch.zeros(2, 3, S, P)
+    c["dlast"][:, :, 3] = rand(gen, 2, 3, P)
+    c["dlast"][:, :, S - 6] = near(c["dlast"][:, :, 3], gen)
+    c["B"][..., 3], c["B"][..., S - 6] = 1, -1
+    check(c, "dx", 2 * 70 * 3 * P)
+
+
+@pytest.mark.parametrize("P,S", SHAPES)
+def test_dx_of_a_state_against_the_token_itself(P, S):
+    """dx = dS_a + D dy with D dy near -dS_a."""
+    say(f"ssm cancel dS D P={P} S={S}")
+    gen = torch.Generator().manual_seed(P + S + 7)
+    H = 16
+    c = zeros(1, 70, H, P, S)
+    c["D"] = rand(gen, H)
+    c["dlast"] = near(c["D"], gen)[None, :, None, None] * torch.ones(1, H, S, P)
+    c["B"][..., 3] = -1
+    c["dy"] = c["dy"] + 1
+    check(c, "dx", 70 * H * P)

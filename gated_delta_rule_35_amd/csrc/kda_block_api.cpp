@@ -272,6 +272,8 @@ kda_status_t check_dweight(const kda_tensor_t* dweight, const kda_tensor_t* weig
     if (!weight) return KDA_ERR_NULL;
     const kda_status_t st = check_dense(dweight, KDA_F32, weight->ndim, weight->shape, 4);
     if (st != KDA_OK) return st;
+    // their sums' launch takes 256 threads for 32 of them, and fewer than 2^32 in all
+    if ((numel(weight) + 31) / 32 >= int64_t(1) << 24) return KDA_ERR_UNSUPPORTED;
     p.dw = static_cast<float*>(dweight->data);
     return KDA_OK;
 }

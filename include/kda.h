@@ -638,7 +638,7 @@ kda_status_t kda_conv_decode(const kda_tensor_t* x, const kda_tensor_t* weight, 
  *   weight    [D], or [H, D] (one per head), fp32, 16-byte aligned; or NULL (ones)
  *   out       [B, T, H, D] of x's type; may be x itself where x is contiguous
  * More than 2^16 heads, or 2^27 rows of up to 128 channels, 2^25 of up to 2048, 2^23 of more, return
- * KDA_ERR_UNSUPPORTED.
+ * KDA_ERR_UNSUPPORTED, and so do the gradients of 2^29 weights.
  */
 kda_status_t kda_gated_norm(const kda_tensor_t* x, const kda_tensor_t* gate, const kda_tensor_t* weight,
                             int32_t activation, int32_t gate_first, float eps, const kda_tensor_t* out, void* stream);

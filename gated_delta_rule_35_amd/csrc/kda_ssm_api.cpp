@@ -191,9 +191,11 @@ kda_status_t prepare(const kda_tensor_t* x, const kda_tensor_t* dt, const kda_te
     if (softplus != 0 && softplus != 1) return KDA_ERR_VALUE;
     if (z.N > (int64_t(1) << 24) || z.B * z.T > kMaxTokens) return KDA_ERR_UNSUPPORTED;
     L = layout(z.B, z.T, z.N, cu != nullptr, z.H, z.G, z.P, z.S, bwd);
-    // grids of at most 2^22 work-groups, segments rounded up to a multiple of 8
+    // grids of at most 2^22 work-groups (of 768 threads at most: fewer than 2^32), segments rounded up to a multiple of 8;
+    // the gradients' numbers take 1024 threads for 16 heads of a chunk
     if (L.slots * z.H > kMaxBlocks || 2 * (L.s.slots + 8) * walk_units(z.H, z.G, 2 * z.P) > kMaxBlocks ||
-        2 * z.N * z.H * (z.S * z.P / 1024) > kMaxBlocks || L.slots * z.G * L.sets > kMaxBlocks)
+        2 * z.N * z.H * (z.S * z.P / 1024) > kMaxBlocks || L.slots * z.G * L.sets > kMaxBlocks ||
+        (bwd && L.slots * ((z.H + 15) / 16) >= kMaxBlocks))
         return KDA_ERR_UNSUPPORTED;
     p.dt = dt->data;
     p.dt_f32 = dt->dtype == KDA_F32 ? 1 : 0;

@@ -696,8 +696,8 @@ kda_status_t kda_add_norm_bwd(const kda_tensor_t* sum, const kda_tensor_t* weigh
  * x, B and C (and d_out) may be views under kda_gdr_fwd's rules: channels contiguous, 16-byte
  * aligned data, strides non-negative multiples of 8 elements, tokens at least a row and at most
  * 2^23 elements apart.  Every other tensor is contiguous.  Other head and state dimensions, more
- * than 2^31 - 1 tokens, or grids above 2^22 work-groups ((chunk slot, head) pairs among them)
- * return KDA_ERR_UNSUPPORTED.
+ * than 2^31 - 1 tokens, or grids above 2^22 work-groups ((chunk slot, head) pairs among them; for
+ * gradients fewer (chunk slot, 16 heads) than that) return KDA_ERR_UNSUPPORTED.
  * Precision: states and sums are fp32, products are formed from operands at fp32's 24 bits; y is
  * rounded to bf16 once.  A token that holds NaN or infinity may
  * reach every token of its 64-token chunk and later ones of its sequence, and through x only its own head.

@@ -1,13 +1,14 @@
-"""GPU checks of the convolution against 64 bits at sizes that take runs of several batches of tokens."""
+"""GPU checks against 64 bits of the convolution and the scan at sizes that take their longer loops: runs of several
+batches of tokens, segments of wide heads, sets of several heads."""
 import ctypes
 
 import pytest
 import torch
 
 from gated_delta_rule_35_amd import kda_conv, load_library
-from tests import block_ref
+from tests import block_ref, ssm_ref as ref
 from tests.block_ref import TYPES
-from tests.test_gpu_ssm import say
+from tests.test_gpu_ssm import check_forward, check_gradients, say
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +52,26 @@ def test_forward_in_runs_of_four_batches(B, T, C, W, kind, act, cu):
         got, real = y[..., some].cpu(), ~torch.isnan(want)
         block_ref.close(got[real], want[real], 2.0 ** -20 * mag[real], "y")
         assert (got[~real] == 7).all() and torch.equal(last[..., some].cpu().double(), wl)
+
+
+@pytest.mark.parametrize("H,P,S,G,cu", [(4, 128, 128, 2, [0, 650, 651, 700]), (4, 128, 128, 2, None), (2, 64, 128, 1, [0, 30, 700]),
+                                        (3, 128, 64, 1, None), (6, 64, 128, 1, None)])
+def test_segments(H, P, S, G, cu):
+    """Segments side by side, chained, of heads and states of 128."""
+    say(f"ssm segments H={H} P={P} S={S} G={G} {cu}")
+    c = ref.make(1, 700, H, P, S, G, N=1 if cu is None else len(cu) - 1, h0=True, seed=H + P, fast=2.0)
+    c["bias"] = c["bias"] - 2   # slow decays, so that states of far segments count
+    check_forward(c, cu)
+    check_gradients(c, cu)
+
+
+@pytest.mark.parametrize("H,P,S,G", [(5, 64, 128, 1), (3, 128, 128, 1), (4, 128, 64, 1), (6, 64, 64, 2)])
+def test_one_set_of_several_heads(H, P, S, G):
+    """So many chunks that a group's heads are taken one after the other, dB and dC kept in registers over them."""
+    say(f"ssm one set H={H} P={P} S={S} G={G}")
+    cu = [0]
+    for n in [70, 130] + [1 + i % 2 for i in range(510 // G)]:
+        cu.append(cu[-1] + n)
+    c = ref.make(1, cu[-1], H, P, S, G, N=len(cu) - 1, h0=True, seed=P + S)
+    assert (cu[-1] // 64 + len(cu)) * G >= 512   # chunk slots and groups, two for each compute unit
+    check_gradients(c, cu)

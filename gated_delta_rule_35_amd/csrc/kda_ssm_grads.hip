@@ -26,7 +26,6 @@
 // dA was off by 2 10^-6 at B = 2, H = 64, T = 8192, fp32's plain form by 4 10^-7), K, E and dS in dx.  The terms of dx, dB
 // and dC may cancel: with two parts of the last three (the call 820 us there, not 855) they were off by up to 2^-18 of
 // their terms, and by 9 10^-5 of their norm from a 32-bit form that is now 2 to 3 10^-5 away.
-#include "kda_block.h"
 #include "kda_ssm_device.h"
 
 namespace kda {

@@ -85,7 +85,7 @@ __device__ __forceinline__ bool walk_place(int b, int units, int64_t segs, int64
 template <int S, bool REV>
 __device__ __forceinline__ void ssm_walk(const SsmParams& p, char* smem, int block) {
     typedef SL L;
-    constexpr int KT = S / 32, NT = S / 16;
+    constexpr int NT = S / 16;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, jj = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int R = p.H / p.G, per = (R * p.P + 32 * NW - 1) / (32 * NW);
@@ -131,7 +131,7 @@ __device__ __forceinline__ void ssm_walk(const SsmParams& p, char* smem, int blo
             for (int u = 0; u < 4; ++u)
                 dma_piece(rs, to + L::X + wave * 4096 + u * 1024, (int)((16 * u + (lane >> 2)) * t.st * 2) + 16 * (lane & 3));
         }
-        if (wave < 2 * L::HEADS && h0 + wave / 2 < R) {   // half of a head's record
+        if (h0 + wave / 2 < R) {   // half of a head's record
             const __amdgpu_buffer_rsrc_t rs = make_rsrc(
                 p.rec + ((sg.slot0 + c0 + c) * p.H + group * R + h0 + wave / 2) * SSM_REC, SSM_REC);
             dma_piece(rs, to + L::REC + wave * 1024, (wave & 1) * 1024 + 16 * lane);

@@ -400,15 +400,24 @@ ConvSplit conv_split(int64_t total, int64_t C, bool bwd) {
     // fewer lanes side by side where the last column of them would be mostly empty
     while (k.lanes > 16 && (pieces + k.lanes - 1) / k.lanes * k.lanes - pieces > pieces / 32) k.lanes /= 2;
     k.cols = (pieces + k.lanes - 1) / k.lanes;
-    if (bwd) {   // one round of two waves a SIMD, in runs of up to 32: 4096 x 4352 in runs of 18 tokens 32 us, of 16 40, of 32 39; 16384 x
-                 // 4352 in runs of 32 108 us, of 16 112, of 64 125
-        const int64_t once = (total * pieces + 64 * 2048 - 1) / (64 * 2048);
-        k.run = (int)std::min<int64_t>(std::max<int64_t>((once + 1) / 2 * 2, 8), 32);
+    auto tiles = [&](int run) { return (total + (int64_t)run * (NT / k.lanes) - 1) / ((int64_t)run * (NT / k.lanes)); };
+    if (bwd) {   // Whole rounds of the 512 work-groups that the device holds at once, each as long as a run and the W - 1 tokens behind
+                 // it: 8192 tokens x 4352 channels in runs of 36 (493 work-groups, one round) 47 us, of 32 (544) 61; 4096 x 4352 of 18
+                 // (510) 32 us, of 16 (544) 40, of 32 (272) 39; 32768 x 1096 of 40 (468) 60 us, of 32 (576) 71; 16384 x 4352 of 36
+                 // (986, two rounds) 101 us, of 32 (1088) 109, of 64 125; 8192 x 4096 of 32 (512) 44 us, of 36 (456) 47
+        int64_t least = 0;
+        for (int run = 8; run <= 40; run += 2) {
+            const int64_t cost = (tiles(run) * k.cols + 511) / 512 * (run + 3);
+            if (run == 8 || cost < least) {
+                least = cost;
+                k.run = run;
+            }
+        }
     } else {     // long runs read fewer rows twice, short ones fill the device: 8 and 32 tokens are 5.9 and 11.1 us at 512 x 4352,
                  // 29 and 31 at 8192 x 4352, 62 and 56 at 16384 x 4352, 161 and 154 at 16384 x 12288
         k.run = total * pieces >= (int64_t(3) << 21) ? 32 : 8;
     }
-    k.tiles = (total + (int64_t)k.run * (NT / k.lanes) - 1) / ((int64_t)k.run * (NT / k.lanes));
+    k.tiles = tiles(k.run);
     return k;
 }
 

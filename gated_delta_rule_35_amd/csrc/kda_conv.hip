@@ -5,8 +5,8 @@
 //   dz = dy act'(z),  dx_t = sum_d w_{W-1-d} dz_{t+d},  dw_i = sum_t dz_t x_{t-W+1+i}
 //
 // Bound by HBM: x is read and y written once (backward: x and dy, dx; there a token's 40 instructions a channel
-// take as long).  16384 x 12288 in bf16: 158 us, 5.1 TB/s; gradients of 2 x 8192 x 12288 4.6 TB/s, of 2 x 4096 x 4352,
-// where a SIMD's two waves have one run each, 72 us, 3.0 TB/s.  A thread takes eight
+// take as long).  16384 x 12288 in bf16: 158 us, 5.1 TB/s; gradients of 2 x 8192 x 12288 4.8 TB/s, of 2 x 4096 x 4352,
+// where a SIMD's two waves have one run each, 47 us, 4.5 TB/s.  A thread takes eight
 // channels of a run of tokens and walks it, the window of its last W inputs in registers, so
 // that a run reads W - 1 rows that others read too (backward 2 (W - 1) of x, W - 1 of dy), from
 // L2 as a rule.  Lanes lie along the channels: a wave's loads and stores are 16 bytes a lane
@@ -413,8 +413,9 @@ ConvSplit conv_split(int64_t total, int64_t C, bool bwd) {
                 k.run = run;
             }
         }
-    } else {     // long runs read fewer rows twice, short ones fill the device: 8 and 32 tokens are 5.9 and 11.1 us at 512 x 4352,
-                 // 29 and 31 at 8192 x 4352, 62 and 56 at 16384 x 4352, 161 and 154 at 16384 x 12288
+    } else {     // long runs read fewer rows twice, short ones fill the device: 8 and 32 tokens are 5.9 and 11.1 us at 512 x 4352, 29 and 31
+                 // at 8192 x 4352, 62 and 56 at 16384 x 4352, 192 and 161 at 16384 x 12288.  fp16's four taps hold 169 registers, two waves a SIMD
+                 // and not three: 33 and 32 us at 8192 x 4352, 237 and 161 at 16384 x 12288
         k.run = total * pieces >= (int64_t(3) << 21) ? 32 : 8;
     }
     k.tiles = tiles(k.run);

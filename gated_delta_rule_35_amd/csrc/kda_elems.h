@@ -80,8 +80,10 @@ __device__ __forceinline__ float formed(float x) {
     return x;
 }
 
-// 1 / (1 + e^-z).  FULL: to fp32's accuracy; else e^-z as 2^{-z log2 e}, off by up to |z| 2^-24 of
-// itself, far below the half step of a 16-bit result.
+// 1 / (1 + e^-z).  FULL: to fp32's accuracy; else, for values of 16 bits, e^-z as 2^{-z log2 e}, off by up to |z| 2^-24 of
+// itself: what a convolution's sum z is rounded by, and far below the half step of a 16-bit result.  Weights'
+// gradients in fp32 are as near to 64 bits either way (2.0 10^-7 of their norm, convolution 2 x 4096 x 4352 in bf16, gated
+// 3001 x 4096 1.4 10^-7); the full one took 66 us there and not 61, 33 and not 31.
 template <bool FULL>
 __device__ __forceinline__ float sigmoid(float z) {
     return __builtin_amdgcn_rcpf(1.f + (FULL ? exp_of(-z) : fexp2(-LOG2E * z)));

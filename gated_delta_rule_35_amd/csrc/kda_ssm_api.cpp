@@ -104,7 +104,7 @@ kda_status_t check_state(const kda_tensor_t* t, int64_t n, const Sizes& z) {
 // work-group each), else segments for that: of four chunks at least, since the walk that forms what they add reads
 // their inputs again, or of two where half the units suffice (then a work-group takes half the columns).  They are
 // chained one after the other: at most 4 sqrt(chunks).  S = 128, heads of 64: T = 1024 on 8 heads in 8 segments
-// 38 us, in 4 46, in one 76; T = 16384 in 64 76 us, in 128 96; T = 2048 on 64 heads in 8 58 us, in 16 64.  Below 8
+// 33 us, in 4 45, in one 88; T = 16384 in 64 72 us, in 128 92; T = 2048 on 64 heads in 8 59 us, in 4 83, in 16 63.  Below 8
 // chunks one walk is as fast.  The backward walks both ways at once: half as many segments each.
 // Packed sequences are cut the same way from their own starts, as if they were one.
 constexpr int64_t kUnits = 256;   // compute units: the workspace's size follows from the shapes alone

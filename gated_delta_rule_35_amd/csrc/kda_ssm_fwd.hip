@@ -7,7 +7,7 @@
 // the compute units there is one segment and one walk.
 //
 // A work-group takes 256 of a group's value columns, or half of them where that leaves no compute unit with two (T = 195 on
-// 8 heads 25 us and not 33: a SIMD then has one walk).  Eight waves walk, 32 columns each: their state is S / 16
+// 8 heads 29 us and not 40, T = 2048 on 64 heads 59 and not 70: a SIMD then has one walk).  Eight waves walk, 32 columns each: their state is S / 16
 // by 2 accumulator tiles, which as operands need no exchange (kda_gdr_fwd.hip has the order of their
 // rows); two walks a SIMD fill each other's gaps.  Four more waves bring what the walks need into LDS and store y: a
 // wave that waits for the memory's queue would keep its products waiting.  Three meetings a chunk:
@@ -15,9 +15,11 @@
 //   2  the pairs' products                                    | the next chunk's B, C and numbers (but e^G) into LDS
 //   3  the state grows, and the pair matrix (C B^T with its   | e^G into LDS, y stored, x asked for a chunk ahead,
 //      decays) of the next chunk, two waves half of it each   | B and C two
-// B = 2, H = 64, P = 64, S = 128, T = 8192: 221 us, the two walks 58 and 154 of it, the numbers 14, the chain 12 (HBM alone
-// 55); bound by what two walks a SIMD issue between the meetings: 840 vector and 204 matrix instructions a
-// wave and chunk, 20,000 clocks a chunk.  T = 195 on 8 heads: 25 us, 5.6 a chunk.
+// B = 2, H = 64, P = 64, S = 128, T = 8192: 221 to 228 us a call (HBM alone 55).  In a trace, which parts the launches and where the
+// clock is lower, a call takes 247: the numbers 14, the first walk 60, the chain 12, the second walk 161.  Of the second
+// walk's 345,000 clocks, 21,600 a chunk, a SIMD spends 154,000 on vector and 127,000 on matrix instructions, a compute unit's LDS
+// 153,000 and 51,000 on conflicts, and waves wait for 46% of theirs: no pipe is full, the meetings keep all walks
+// in one phase.  T = 195 on 8 heads: 29 us, 25 of them the walk, 6.2 a chunk.
 // y is formed transposed, so that a lane holds four channels of one token.  The decay between tokens of
 // different blocks of sixteen is a product of a number of each token and one or two of the blocks,
 // all at most 1 for A <= 0; within a block it is formed from the difference.

@@ -17,14 +17,14 @@
 // through LDS, for dx.  The 64 x 64 matrices are ten tiles, dealt to the waves; they leave as
 // operand fragments for the second half of a head's work.
 //
-// B = 2, H = 64, P = 64, S = 128, T = 8192: 452 us, 14,000 clocks a chunk and head, most of them issue (6,200 vector, 800
-// matrix and 1,150 LDS instructions on four SIMDs); of 15,400 before the last steps the tiles took 3,600, V and W 4,200,
-// dB and dC 1,900, dx 2,500, the meetings 1,200.  The inputs of a head are asked for during the head before, S and dS apart from each
-// other: all at once they waited for the memory's queue.
+// B = 2, H = 64, P = 64, S = 128, T = 8192: 499 us in a trace, 16,800 clocks a chunk and head.  Of those a SIMD spends 6,400 on
+// vector and 3,900 on matrix instructions, the compute unit's LDS 8,400 and 2,500 on conflicts, and waves wait for 45% of
+// theirs: LDS is the busiest pipe, the meetings keep the others from filling beside it.  The inputs of a head are asked for
+// during the head before, S and dS apart from each other: all at once they waited for the memory's queue.
 //
 // Precision.  What multiplies x, dy, B and C enters in three bf16 parts, fp32's 24 bits: S and dS in V and W (in two parts,
 // dA was off by 2 10^-6 at B = 2, H = 64, T = 8192, fp32's plain form by 4 10^-7), K, E and dS in dx.  The terms of dx, dB
-// and dC may cancel: with two parts of the last three (the call 820 us there, not 855) they were off by up to 2^-18 of
+// and dC may cancel: with two parts of the last three (the kernel 452 us in a trace there, not 499) they were off by up to 2^-18 of
 // their terms, and by 9 10^-5 of their norm from a 32-bit form that is now 2 to 3 10^-5 away.
 #include "kda_ssm_device.h"
 
